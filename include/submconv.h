@@ -42,6 +42,7 @@
 #ifndef SUBMCONV_H
 #define SUBMCONV_H
 
+#include <stddef.h>
 #include <stdint.h>
 
 #ifdef __cplusplus
@@ -283,6 +284,76 @@ int submconv_classify_5d(const int64_t *shape, int32_t hint, int32_t *layout);
  */
 int submconv_weight_convert(const void *src, int32_t layout, int32_t cout, int32_t cin, int32_t dtype, int32_t flip,
                             void *dst, void *stream);
+
+/*
+ * Layer normalisation of feature rows:
+ *
+ *     y[i] = (x[i] - mean_i) * rstd_i * weight + bias,
+ *     mean_i = sum_c x[i,c] / c,  rstd_i = 1 / sqrt(sum_c (x[i,c] - mean_i)^2 / c + eps)
+ *
+ *   x, y   : device [n, c] of dtype, rows x_row / y_row elements apart (x_row >= 0,
+ *            y_row >= c), the elements of a row next to each other; any alignment of the
+ *            element type.
+ *            y may be x itself (same pointer and row distance), else E_ALIAS if they overlap.
+ *   c      : 1..8192.
+ *   weight : device [c] of param_dtype, or NULL for 1.  bias likewise, or NULL for 0.
+ *   param_dtype : SUBMCONV_F32 or SUBMCONV_BF16, independent of dtype.
+ *   stats  : device fp32 [n, 2], receives (mean, rstd) for the backward pass, or NULL.
+ *
+ * Statistics are fp32; one rounding to dtype at the end.  Asynchronous, one launch.
+ */
+#define SUBMCONV_NORM_MAX_C 8192
+int submconv_layer_norm(const void *x, int64_t x_row, int64_t n, int32_t c, int32_t dtype, const void *weight,
+                        const void *bias, int32_t param_dtype, float eps, void *y, int64_t y_row, float *stats,
+                        void *stream);
+
+/* Bytes of device workspace submconv_layer_norm_backward needs (0 for bad sizes). */
+size_t submconv_layer_norm_backward_workspace(int64_t n, int32_t c, int32_t dtype);
+
+/*
+ * Backward pass of submconv_layer_norm: with h = (x - mean) rstd and gw = grad * weight,
+ *     dx = rstd (gw - sum(gw)/c - h sum(gw h)/c),  dweight = sum_i grad h,  dbias = sum_i grad.
+ *   grad, x, dx : [n, c] of dtype, rows grad_row, x_row, dx_row elements apart.  dx may be
+ *            grad itself (same pointer and row distance), else E_ALIAS on overlap.
+ *   stats  : what the forward stored for x.  weight: as in the forward (NULL for 1).
+ *   dweight, dbias : device [c] of param_dtype, each may be NULL.  Summed over the rows in
+ *            fp32 in a fixed order (the same bits for the same call), rounded once.
+ *   workspace : device memory of submconv_layer_norm_backward_workspace bytes, 16-byte
+ *            aligned, its contents undefined before and after (may be NULL when dweight
+ *            and dbias are).
+ * Asynchronous, one launch, and a second where dweight or dbias is wanted.
+ */
+int submconv_layer_norm_backward(const void *grad, int64_t grad_row, const void *x, int64_t x_row, int64_t n,
+                                 int32_t c, int32_t dtype, const float *stats, const void *weight,
+                                 int32_t param_dtype, void *dx, int64_t dx_row, void *dweight, void *dbias,
+                                 void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Rotary positions on several axes (trellis_sparse_mrp_mlx commits, the RoPE commit: phases
+ * from a voxel's coordinates, 3 x 21 = 63 frequencies, the 64th pair of a 128-wide head left
+ * unrotated).  Head vector (i, h) is dim/2 pairs; pair p of axis a turns by
+ * t = positions[i, a] * freqs[p]:
+ *
+ *     (u, v) -> (u cos t - v sin t, u sin t + v cos t);   inverse = 1 turns by -t,
+ *
+ * which undoes it and is also its gradient.  Pairs past the last section are copied.
+ *
+ *   x, out : device [n, heads, dim] of dtype; element (i, h, d) at i * row + h * head + d
+ *            elements.  out may be x itself (same pointer and distances), else E_ALIAS if the
+ *            two ranges overlap.  Any alignment of the element type.
+ *   positions : device int32, row i at i * pos_row, one value an axis next to each other (the
+ *            z, y, x columns of a coordinate set: coords + 1, pos_row = 4).
+ *   freqs  : device fp32 [sum of sections], radians for one step of the pair's axis.
+ *   sections : HOST int32 [axes]: pairs of each axis, in order; their sum is at most dim/2.
+ *   axes   : 1..SUBMCONV_ROTARY_MAX_AXES.   dim : even, 2..512.   heads : 1..1024.
+ *   split  : 0 = pair p is elements (2p, 2p + 1); 1 = elements (p, p + dim/2).
+ * Phases are formed in fp64, so large positions lose nothing.  Asynchronous, one launch.
+ */
+#define SUBMCONV_ROTARY_MAX_AXES 4
+int submconv_rotary(const void *x, int64_t x_row, int64_t x_head, const int32_t *positions, int64_t pos_row,
+                    const float *freqs, const int32_t *sections, int32_t axes, int64_t n, int32_t heads, int32_t dim,
+                    int32_t dtype, int32_t split, int32_t inverse, void *out, int64_t out_row, int64_t out_head,
+                    void *stream);
 
 /*
  * The library keeps device blocks it has freed (rulebooks, scratch) for reuse on the

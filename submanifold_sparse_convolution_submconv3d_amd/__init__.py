@@ -20,6 +20,10 @@ Functions carry the C names:
     classify_5d(shape, hint=None)                   -> "krsc" | "oidhw"
     weight_to_krsc(weight, layout=None, hint=None, flip=False) -> KRSC weight
     flip_ab(feats, weight, bias, rb)                -> {"corr": out, "conv": out} for an A/B
+    submconv_layer_norm(x, weight, bias, eps)       -> y (and its row statistics)
+    submconv_layer_norm_backward(grad, x, stats, weight) -> (dx, dweight, dbias)
+    submconv_rotary(x, positions, freqs, sections)  -> rotated heads
+    rotary_freqs(sections, theta, device)           -> one frequency ladder per axis
 
 `RulebookCache` keeps one rulebook per coordinate set, keyed like the
 upstream library's indice_key, so every convolution on a set reuses its map
@@ -39,6 +43,7 @@ __all__ = [
     "submconv_build_map", "submconv_forward", "submconv_subdivide",
     "submconv_space_to_depth", "submconv_depth_to_space", "submconv_upsample_masked", "submconv_downsample",
     "POOL_MAX", "POOL_MEAN", "classify_5d", "weight_to_krsc", "flip_ab", "release_cache", "set_cache_limit",
+    "submconv_layer_norm", "submconv_layer_norm_backward", "submconv_rotary", "rotary_freqs",
     "KERNEL_AUTO", "KERNEL_GENERIC", "KERNEL_LOWC", "KERNEL_MFMA", "KERNEL_WINDOW", "KERNEL_PERSISTENT",
 ]
 
@@ -72,7 +77,7 @@ def load_library():
         raise RuntimeError("libsubmconv.so is not built (%s); run "
                            "`python -m submanifold_sparse_convolution_submconv3d_amd._build`" % _LIB_PATH)
     lib = ctypes.CDLL(_LIB_PATH)
-    vp, i32, i64 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64
+    vp, i32, i64, f32 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_float
     i64p, i32p = ctypes.POINTER(ctypes.c_int64), ctypes.POINTER(ctypes.c_int32)
     sig = {
         "submconv_build_map": [vp, i64, i32, i32, vp, ctypes.POINTER(vp)],
@@ -92,11 +97,17 @@ def load_library():
         "submconv_release_cache": [i32],
         "submconv_set_cache_limit": [i64],
         "submconv_weight_convert": [vp, i32, i32, i32, i32, i32, vp, vp],
+        "submconv_layer_norm": [vp, i64, i64, i32, i32, vp, vp, i32, f32, vp, i64, vp, vp],
+        "submconv_layer_norm_backward": [vp, i64, vp, i64, i64, i32, i32, vp, vp, i32, vp, i64, vp, vp, vp,
+                                         ctypes.c_size_t, vp],
+        "submconv_rotary": [vp, i64, i64, vp, i64, vp, i32p, i32, i64, i32, i32, i32, i32, i32, vp, i64, i64, vp],
     }
     for name, args in sig.items():
         fn = getattr(lib, name)
         fn.argtypes = args
         fn.restype = ctypes.c_int
+    lib.submconv_layer_norm_backward_workspace.argtypes = [i64, i32, i32]
+    lib.submconv_layer_norm_backward_workspace.restype = ctypes.c_size_t
     for name in ("submconv_status_string",):
         getattr(lib, name).argtypes = [ctypes.c_int]
         getattr(lib, name).restype = ctypes.c_char_p
@@ -456,6 +467,149 @@ def flip_ab(feats: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tens
     (flip 1, the mirrored kernel)."""
     return {"corr": submconv_forward(feats, weight, bias, rb, flip=False),
             "conv": submconv_forward(feats, weight, bias, rb, flip=True)}
+
+
+def _strided(t: torch.Tensor, name: str, dims: int, device=None, dtype=None) -> torch.Tensor:
+    """A GPU tensor of `dims` dimensions whose innermost elements are next to each other."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError("%s must be a GPU tensor" % name)
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    if device is not None and t.device != device:
+        raise ValueError("%s is on %s, not on %s" % (name, t.device, device))
+    if t.dim() != dims:
+        raise ValueError("%s must have %d dimensions, got %d" % (name, dims, t.dim()))
+    if t.stride(dims - 1) != 1 and t.shape[dims - 1] > 1:
+        raise ValueError("the last dimension of %s must be contiguous" % name)
+    return t
+
+
+def _row_stride(t: torch.Tensor) -> int:
+    """Distance between rows; torch may report any for a single row."""
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def _norm_params(x: torch.Tensor, weight: Optional[torch.Tensor], bias: Optional[torch.Tensor]) -> int:
+    """Type code of the parameter vectors (both fp32 or both of x's type)."""
+    code = None
+    for name, p in (("weight", weight), ("bias", bias)):
+        if p is None:
+            continue
+        if _dev(p, name).device != x.device:
+            raise ValueError("%s is on %s, not on %s" % (name, p.device, x.device))
+        if p.shape != (x.shape[1],):
+            raise ValueError("%s must be [%d]" % (name, x.shape[1]))
+        if code is not None and code != _dtype_code(p):
+            raise TypeError("weight and bias must have one type")
+        code = _dtype_code(p)
+    return F32 if code is None else code
+
+
+def submconv_layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Optional[torch.Tensor] = None,
+                        eps: float = 1e-5, out: Optional[torch.Tensor] = None, return_stats: bool = False):
+    """Layer normalisation of the rows of x [N,C] (C <= 8192; rows may be strided) -> y, or (y, stats)
+    with stats fp32 [N,2] = (mean, 1/std) for the backward pass.
+
+    weight and bias [C] are fp32 or bf16 (None: 1 and 0); statistics are fp32.  `out` may be x."""
+    dev = _strided(x, "x", 2).device
+    n, c = x.shape
+    code = _norm_params(x, weight, bias)
+    if out is None:
+        out = torch.empty((n, c), dtype=x.dtype, device=dev)
+    elif tuple(_strided(out, "out", 2, dev, x.dtype).shape) != (n, c):
+        raise ValueError("out must be [N,C]")
+    stats = torch.empty((n, 2), dtype=torch.float32, device=dev) if return_stats else None
+    lib = _lib if _lib is not None else load_library()
+    with _on_device(dev):
+        _check(lib.submconv_layer_norm(
+            x.data_ptr(), _row_stride(x), n, c, _dtype_code(x), None if weight is None else weight.data_ptr(),
+            None if bias is None else bias.data_ptr(), code, eps, out.data_ptr(), _row_stride(out),
+            None if stats is None else stats.data_ptr(), _raw_stream(dev.index)), "submconv_layer_norm")
+    return (out, stats) if return_stats else out
+
+
+def submconv_layer_norm_backward(grad: torch.Tensor, x: torch.Tensor, stats: torch.Tensor,
+                                 weight: Optional[torch.Tensor] = None, param_dtype: Optional[torch.dtype] = None,
+                                 need_params: bool = True):
+    """Gradients of submconv_layer_norm -> (dx, dweight, dbias).
+
+    `stats` is what the forward returned for x.  dweight and dbias have weight's type (param_dtype,
+    or fp32, without a weight) and are None with need_params=False; they are summed in a fixed
+    order, so equal calls give equal bits."""
+    dev = _strided(x, "x", 2).device
+    n, c = x.shape
+    if tuple(_strided(grad, "grad", 2, dev, x.dtype).shape) != (n, c):
+        raise ValueError("grad must be [N,C]")
+    _dev(stats, "stats", torch.float32)
+    if tuple(stats.shape) != (n, 2) or stats.device != dev:
+        raise ValueError("stats must be fp32 [N,2] on x's device")
+    kind = weight.dtype if weight is not None else (param_dtype or torch.float32)
+    code = _norm_params(x, weight, None)
+    if weight is None and kind not in (torch.float32, torch.bfloat16):
+        raise TypeError("param_dtype must be float32 or bfloat16, got %s" % kind)
+    code = code if weight is not None else (F32 if kind == torch.float32 else BF16)
+    dx = torch.empty((n, c), dtype=x.dtype, device=dev)
+    lib = _lib if _lib is not None else load_library()
+    dw = db = ws = None
+    nbytes = 0
+    if need_params:
+        dw, db = torch.empty((2, c), dtype=kind, device=dev).unbind(0)
+        nbytes = lib.submconv_layer_norm_backward_workspace(n, c, _dtype_code(x))
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    with _on_device(dev):
+        _check(lib.submconv_layer_norm_backward(
+            grad.data_ptr(), _row_stride(grad), x.data_ptr(), _row_stride(x), n, c, _dtype_code(x), stats.data_ptr(),
+            None if weight is None else weight.data_ptr(), code, dx.data_ptr(), c,
+            None if dw is None else dw.data_ptr(), None if db is None else db.data_ptr(),
+            None if ws is None else ws.data_ptr(), nbytes, _raw_stream(dev.index)), "submconv_layer_norm_backward")
+    return dx, dw, db
+
+
+def rotary_freqs(sections, theta: float = 10000.0, device="cuda") -> torch.Tensor:
+    """One ladder per axis, theta^(-i/n) for i < n = its pairs: fp32 [sum(sections)], formed in fp64.
+    sections (21, 21, 21) are the 63 frequencies of a 128-wide head on three axes."""
+    parts = [torch.pow(float(theta), -torch.arange(int(n), dtype=torch.float64) / max(1, int(n))) for n in sections]
+    return torch.cat(parts).float().to(device)
+
+
+def _head_strides(t: torch.Tensor):
+    """(row, head) distances of [N,H,D]; torch may report any for a dimension of one."""
+    n, h, d = t.shape
+    head = t.stride(1) if h > 1 else d
+    return (t.stride(0) if n > 1 else max(h * head, d) if head else d), head
+
+
+def submconv_rotary(x: torch.Tensor, positions: torch.Tensor, freqs: torch.Tensor, sections, inverse: bool = False,
+                    split: bool = False, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Rotate the head vectors x [N,H,D] by integer positions on several axes.
+
+    positions int32 [N,A] (the coords[:, 1:] columns of a voxel set), freqs fp32 [sum(sections)] in
+    radians a step, sections = pairs of each axis (their sum <= D/2; the pairs left over are
+    copied).  Pair p is elements (2p, 2p+1), or (p, p + D/2) with split.  inverse turns back,
+    which is the gradient.  x may be strided (the query and key part of a packed projection);
+    `out` may be x itself."""
+    dev = _strided(x, "x", 3).device
+    _strided(positions, "positions", 2, dev, torch.int32)
+    if _dev(freqs, "freqs", torch.float32).device != dev:
+        raise ValueError("freqs is on %s, not on %s" % (freqs.device, dev))
+    n, h, d = x.shape
+    axes = len(sections)
+    if tuple(positions.shape) != (n, axes):
+        raise ValueError("positions must be [N,%d]" % axes)
+    if freqs.dim() != 1 or freqs.shape[0] != sum(sections):
+        raise ValueError("freqs must be [%d], one for each pair of the sections" % sum(sections))
+    if out is None:
+        out = torch.empty((n, h, d), dtype=x.dtype, device=dev)
+    elif tuple(_strided(out, "out", 3, dev, x.dtype).shape) != (n, h, d):
+        raise ValueError("out must be [N,H,D]")
+    xs, os_ = _head_strides(x), _head_strides(out)
+    lib = _lib if _lib is not None else load_library()
+    with _on_device(dev):
+        _check(lib.submconv_rotary(
+            x.data_ptr(), xs[0], xs[1], positions.data_ptr(), _row_stride(positions), freqs.data_ptr(),
+            (ctypes.c_int32 * max(1, axes))(*sections), axes, n, h, d, _dtype_code(x), int(bool(split)),
+            int(bool(inverse)), out.data_ptr(), os_[0], os_[1], _raw_stream(dev.index)), "submconv_rotary")
+    return out
 
 
 def release_cache(device: int = -1) -> None:

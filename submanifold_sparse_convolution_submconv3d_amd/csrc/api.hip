@@ -35,6 +35,15 @@ int downsample(const int32_t *coords, const void *feats, int64_t n, int c, int d
                int mean, int32_t *out_coords, void *out_feats, int64_t *out_m, hipStream_t s);
 int classify_5d(const int64_t *shape, int hint, int *layout);
 int weight_convert(const void *src, int layout, int cout, int cin, int dtype, int flip, void *dst, hipStream_t s);
+int layer_norm(const void *x, int64_t ldx, int64_t n, int c, int dtype, const void *w, const void *b, int pdtype,
+               float eps, void *y, int64_t ldy, float *stats, hipStream_t s);
+size_t norm_bwd_workspace(int64_t n, int c, int dtype);
+int layer_norm_backward(const void *gy, int64_t ldg, const void *x, int64_t ldx, int64_t n, int c, int dtype,
+                        const float *stats, const void *w, int pdtype, void *dx, int64_t lddx, void *dw, void *db,
+                        void *workspace, hipStream_t s);
+int rotary(const void *x, int64_t x_row, int64_t x_head, const int32_t *pos, int64_t pos_row, const float *freqs,
+           const int32_t *sections, int axes, int64_t n, int heads, int dim, int dtype, int split, int inverse,
+           void *out, int64_t out_row, int64_t out_head, hipStream_t s);
 
 static thread_local char g_err[512];
 
@@ -333,6 +342,16 @@ static bool overlaps(const void *a, size_t na, const void *b, size_t nb)
 }
 
 static size_t elem_size(int dtype) { return dtype == SUBMCONV_F32 ? 4 : 2; }
+
+static bool known_dtype(int dtype) { return dtype == SUBMCONV_F32 || dtype == SUBMCONV_BF16; }
+static bool aligned_to(const void *p, size_t bytes) { return ((uintptr_t)p & (bytes - 1)) == 0; }
+
+// Rows of the strided tensors: their number, and the largest distance in elements, such
+// that every byte offset below fits 63 bits.
+constexpr int64_t MAX_ROWS = int64_t(1) << 31, MAX_STRIDE = int64_t(1) << 24;
+
+// Bytes from the first to past the last element of [n, c] with rows ld apart.
+static size_t span2(int64_t n, int64_t c, int64_t ld, size_t es) { return n ? (size_t)((n - 1) * ld + c) * es : 0; }
 
 }  // namespace sc
 
@@ -646,6 +665,141 @@ int submconv_weight_convert(const void *src, int32_t layout, int32_t cout, int32
     const size_t bytes = (size_t)cout * 27 * cin * elem_size(dtype);
     if (overlaps(dst, bytes, src, bytes)) return fail(SUBMCONV_E_ALIAS, "dst overlaps src");
     return weight_convert(src, layout, cout, cin, dtype, flip, dst, (hipStream_t)stream);
+}
+
+static int norm_check(int64_t n, int32_t c, int32_t dtype, int32_t pdtype)
+{
+    if (n < 0 || n >= MAX_ROWS) return fail(SUBMCONV_E_INVALID_ARG, "n = %lld outside [0, 2^31)", (long long)n);
+    if (!known_dtype(dtype) || !known_dtype(pdtype)) return fail(SUBMCONV_E_UNSUPPORTED, "dtype %d, param_dtype %d", dtype, pdtype);
+    if (c < 1 || c > SUBMCONV_NORM_MAX_C)
+        return fail(SUBMCONV_E_UNSUPPORTED, "c = %d outside 1..%d", c, SUBMCONV_NORM_MAX_C);
+    return SUBMCONV_OK;
+}
+
+// Rows of an input may overlap or be one row (distance 0), those of an output may not.
+static int row_check(const char *what, int64_t ld, int32_t least)
+{
+    if (ld < least || ld > MAX_STRIDE)
+        return fail(SUBMCONV_E_INVALID_ARG, "%s rows are %lld elements apart, outside [%d, 2^24]", what, (long long)ld, least);
+    return SUBMCONV_OK;
+}
+
+int submconv_layer_norm(const void *x, int64_t x_row, int64_t n, int32_t c, int32_t dtype, const void *weight,
+                        const void *bias, int32_t param_dtype, float eps, void *y, int64_t y_row, float *stats,
+                        void *stream)
+{
+    SC_CHECK(norm_check(n, c, dtype, param_dtype));
+    SC_CHECK(row_check("x", x_row, 0));
+    SC_CHECK(row_check("y", y_row, c));
+    if (!(eps >= 0.0f)) return fail(SUBMCONV_E_INVALID_ARG, "eps = %g", (double)eps);
+    if (n == 0) return SUBMCONV_OK;
+    if (!x || !y) return fail(SUBMCONV_E_INVALID_ARG, "NULL tensor pointer");
+    const size_t es = elem_size(dtype), ps = elem_size(param_dtype);
+    if (!aligned_to(x, es) || !aligned_to(y, es) || !aligned_to(weight, ps) || !aligned_to(bias, ps) || !aligned_to(stats, 8))
+        return fail(SUBMCONV_E_INVALID_ARG, "misaligned pointer");
+    const size_t xb = span2(n, c, x_row, es), yb = span2(n, c, y_row, es), pb = (size_t)c * ps, sb = (size_t)n * 8;
+    if ((overlaps(y, yb, x, xb) && !(x == y && x_row == y_row)) || (weight && overlaps(y, yb, weight, pb)) ||
+        (bias && overlaps(y, yb, bias, pb)) ||
+        (stats && (overlaps(stats, sb, x, xb) || overlaps(stats, sb, y, yb) || (weight && overlaps(stats, sb, weight, pb)) ||
+                   (bias && overlaps(stats, sb, bias, pb)))))
+        return fail(SUBMCONV_E_ALIAS, "an output overlaps an input or the other output");
+    return layer_norm(x, x_row, n, c, dtype, weight, bias, param_dtype, eps, y, y_row, stats, (hipStream_t)stream);
+}
+
+size_t submconv_layer_norm_backward_workspace(int64_t n, int32_t c, int32_t dtype)
+{
+    return norm_check(n, c, dtype, SUBMCONV_F32) == SUBMCONV_OK ? norm_bwd_workspace(n, c, dtype) : 0;
+}
+
+int submconv_layer_norm_backward(const void *grad, int64_t grad_row, const void *x, int64_t x_row, int64_t n,
+                                 int32_t c, int32_t dtype, const float *stats, const void *weight,
+                                 int32_t param_dtype, void *dx, int64_t dx_row, void *dweight, void *dbias,
+                                 void *workspace, size_t workspace_bytes, void *stream)
+{
+    SC_CHECK(norm_check(n, c, dtype, param_dtype));
+    SC_CHECK(row_check("grad", grad_row, 0));
+    SC_CHECK(row_check("x", x_row, 0));
+    SC_CHECK(row_check("dx", dx_row, c));
+    if (n && (!grad || !x || !stats || !dx)) return fail(SUBMCONV_E_INVALID_ARG, "NULL tensor pointer");
+    const size_t es = elem_size(dtype), ps = elem_size(param_dtype);
+    if (!aligned_to(grad, es) || !aligned_to(x, es) || !aligned_to(dx, es) || !aligned_to(stats, 8) ||
+        !aligned_to(weight, ps) || !aligned_to(dweight, ps) || !aligned_to(dbias, ps) || !aligned16(workspace))
+        return fail(SUBMCONV_E_INVALID_ARG, "misaligned pointer");
+    const size_t need = dweight || dbias ? norm_bwd_workspace(n, c, dtype) : 0;
+    if (need && (!workspace || workspace_bytes < need))
+        return fail(SUBMCONV_E_INVALID_ARG, "workspace of %zu bytes, %zu needed", workspace ? workspace_bytes : 0, need);
+    const size_t gb = span2(n, c, grad_row, es), xb = span2(n, c, x_row, es), db = span2(n, c, dx_row, es),
+                 pb = (size_t)c * ps, sb = (size_t)n * 8;
+    struct { const void *p; size_t b; } in[] = {{x, xb}, {stats, sb}, {weight, pb}, {grad, gb}},
+                                        out[] = {{dweight, pb}, {dbias, pb}, {workspace, need}, {dx, db}};
+    for (int i = 0; i < 4; ++i) {
+        if (!out[i].p || !out[i].b) continue;
+        for (int j = 0; j < 4; ++j)
+            if (in[j].p && overlaps(out[i].p, out[i].b, in[j].p, in[j].b) &&
+                !(i == 3 && j == 3 && dx == grad && dx_row == grad_row))
+                return fail(SUBMCONV_E_ALIAS, "an output or the workspace overlaps an input");
+        for (int j = 0; j < i; ++j)
+            if (out[j].p && overlaps(out[i].p, out[i].b, out[j].p, out[j].b))
+                return fail(SUBMCONV_E_ALIAS, "two outputs or the workspace overlap");
+    }
+    return layer_norm_backward(grad, grad_row, x, x_row, n, c, dtype, stats, weight, param_dtype, dx, dx_row, dweight,
+                               dbias, workspace, (hipStream_t)stream);
+}
+
+// Bytes spanned by [n, heads, dim] with the given element distances; 0 if empty.
+static size_t span3(int64_t n, int64_t heads, int64_t dim, int64_t row, int64_t head, size_t es)
+{
+    return n && heads ? (size_t)((n - 1) * row + (heads - 1) * head + dim) * es : 0;
+}
+
+// The distances of an [n, heads, dim] tensor; one that is written has each element once.
+static int heads_check(const char *what, int64_t n, int64_t heads, int64_t dim, int64_t row, int64_t head, bool written)
+{
+    if (row < 0 || head < 0 || row > MAX_STRIDE || head > int64_t(1) << 40)
+        return fail(SUBMCONV_E_INVALID_ARG, "%s: row distance %lld outside [0, 2^24] or head distance %lld outside [0, 2^40]",
+                    what, (long long)row, (long long)head);
+    const bool by_row = (heads <= 1 || head >= dim) && (n <= 1 || row >= (heads - 1) * head + dim);
+    const bool by_head = (n <= 1 || row >= dim) && (heads <= 1 || head >= (n - 1) * row + dim);
+    if (written && !by_row && !by_head)
+        return fail(SUBMCONV_E_INVALID_ARG, "%s: heads or rows overlap (distances %lld, %lld)", what, (long long)row,
+                    (long long)head);
+    return SUBMCONV_OK;
+}
+
+int submconv_rotary(const void *x, int64_t x_row, int64_t x_head, const int32_t *positions, int64_t pos_row,
+                    const float *freqs, const int32_t *sections, int32_t axes, int64_t n, int32_t heads, int32_t dim,
+                    int32_t dtype, int32_t split, int32_t inverse, void *out, int64_t out_row, int64_t out_head,
+                    void *stream)
+{
+    if (n < 0 || n >= MAX_ROWS) return fail(SUBMCONV_E_INVALID_ARG, "n = %lld outside [0, 2^31)", (long long)n);
+    if (!known_dtype(dtype)) return fail(SUBMCONV_E_UNSUPPORTED, "dtype %d", dtype);
+    if (dim < 2 || dim > 512 || dim % 2) return fail(SUBMCONV_E_UNSUPPORTED, "dim = %d is not an even number in 2..512", dim);
+    if (heads < 1 || heads > 1024) return fail(SUBMCONV_E_UNSUPPORTED, "heads = %d outside 1..1024", heads);
+    if (axes < 1 || axes > SUBMCONV_ROTARY_MAX_AXES)
+        return fail(SUBMCONV_E_UNSUPPORTED, "axes = %d outside 1..%d", axes, SUBMCONV_ROTARY_MAX_AXES);
+    if ((split | inverse) & ~1) return fail(SUBMCONV_E_INVALID_ARG, "split and inverse must be 0 or 1");
+    if (!sections) return fail(SUBMCONV_E_INVALID_ARG, "sections is NULL");
+    int64_t pairs = 0;
+    for (int a = 0; a < axes; ++a) {
+        if (sections[a] < 0) return fail(SUBMCONV_E_INVALID_ARG, "sections[%d] = %d", a, sections[a]);
+        pairs += sections[a];
+    }
+    if (pairs > dim / 2) return fail(SUBMCONV_E_INVALID_ARG, "sections hold %lld pairs, a head has %d", (long long)pairs, dim / 2);
+    SC_CHECK(heads_check("x", n, heads, dim, x_row, x_head, false));
+    SC_CHECK(heads_check("out", n, heads, dim, out_row, out_head, true));
+    if (pos_row < 0 || pos_row > MAX_STRIDE) return fail(SUBMCONV_E_INVALID_ARG, "pos_row = %lld", (long long)pos_row);
+    if (n == 0) return SUBMCONV_OK;
+    if (!x || !out || !positions || (pairs && !freqs)) return fail(SUBMCONV_E_INVALID_ARG, "NULL tensor pointer");
+    const size_t es = elem_size(dtype);
+    if (!aligned_to(x, es) || !aligned_to(out, es) || !aligned_to(positions, 4) || !aligned_to(freqs, 4))
+        return fail(SUBMCONV_E_INVALID_ARG, "misaligned pointer");
+    const size_t xb = span3(n, heads, dim, x_row, x_head, es), ob = span3(n, heads, dim, out_row, out_head, es);
+    const bool same = x == out && x_row == out_row && (heads == 1 || x_head == out_head);
+    if ((overlaps(out, ob, x, xb) && !same) || overlaps(out, ob, positions, span2(n, axes, pos_row, 4)) ||
+        (pairs && overlaps(out, ob, freqs, (size_t)pairs * 4)))
+        return fail(SUBMCONV_E_ALIAS, "out overlaps an input");
+    return rotary(x, x_row, x_head, positions, pos_row, freqs, sections, axes, n, heads, dim, dtype, split, inverse,
+                  out, out_row, out_head, (hipStream_t)stream);
 }
 
 int submconv_release_cache(int32_t device)
