@@ -356,6 +356,63 @@ int submconv_rotary(const void *x, int64_t x_row, int64_t x_head, const int32_t 
                     void *stream);
 
 /*
+ * Softmax attention inside each entry of a ragged batch.  For query row i of entry e and
+ * query head h (key head h / (heads / kv_heads)), over the keys j of the same entry:
+ *
+ *     s_j = scale * q[i,h] . k[j,hk],  p = softmax(s),  out[i,h] = sum_j p_j v[j,hk],
+ *     lse[i,h] = log sum_j exp(s_j)
+ *
+ * A query whose entry has no keys gets zeros and lse = -inf; so does one whose scores are
+ * all -inf.  Not causal: voxels have no order.
+ *
+ *   q, out : device [nq, heads, dim];  k, v : device [nk, kv_heads, dim], all of dtype;
+ *            elements of a head next to each other, any alignment of the element type.
+ *   strides : HOST int64 [8]: row and head distance in elements of q, k, v, out.
+ *   q_offsets, k_offsets : device int32 [entries + 1], ascending: entry e has the rows
+ *            [off[e], off[e + 1]).  Rows before the first or from the last offset on belong
+ *            to no entry: queries there get zeros.  They are read on the device only;
+ *            values outside [0, n] are clamped, so bad offsets give wrong rows, never
+ *            accesses outside the tensors.
+ *   entries: 1..2^20.  nq, nk >= 0, nq * heads and nk * kv_heads < 2^31.
+ *   heads  : a multiple of kv_heads, up to 1024.   dim : a multiple of 8, 8..128.
+ *   scale  : finite, > 0.
+ *   lse    : device fp32 [nq, heads] for the backward pass, or NULL.
+ *   workspace : device memory of submconv_attention_workspace bytes, 16-byte aligned
+ *            (may be NULL when that is 0); contents undefined before and after.
+ * Scores, softmax and sums are fp32.  In bf16 the weights exp(s - max) are rounded to bf16
+ * for the product with v (the matrix cores take bf16); the sum of the weights is not.
+ * Outputs may not overlap inputs (E_ALIAS).  Asynchronous; one launch, or two when few
+ * queries meet many keys and the keys are split between blocks.  The same call gives the
+ * same bits.
+ */
+#define SUBMCONV_ATTENTION_MAX_DIM 128
+size_t submconv_attention_workspace(int32_t entries, int64_t nq, int64_t nk, int32_t heads, int32_t kv_heads,
+                                    int32_t dim, int32_t dtype);
+int submconv_attention(const void *q, const void *k, const void *v, const int64_t *strides, const int32_t *q_offsets,
+                       const int32_t *k_offsets, int32_t entries, int64_t nq, int64_t nk, int32_t heads,
+                       int32_t kv_heads, int32_t dim, int32_t dtype, float scale, void *out, float *lse,
+                       void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Backward pass of submconv_attention: dq [nq, heads, dim], dk and dv [nk, kv_heads, dim]
+ * (a key head's gradient is summed over the query heads that share it).  out and lse are
+ * the forward's.
+ *   strides : HOST int64 [16]: row and head distance of grad, q, k, v, out, dq, dk, dv.
+ *   workspace : submconv_attention_backward_workspace bytes, 16-byte aligned, never 0 for
+ *            nq > 0.
+ * Sums are fp32 in a fixed order; in bf16 the weights and their gradients are rounded to
+ * bf16 for the products.  Asynchronous; two launches, up to five when a short side is
+ * split.  Rows outside every entry get zeros.
+ */
+size_t submconv_attention_backward_workspace(int32_t entries, int64_t nq, int64_t nk, int32_t heads, int32_t kv_heads,
+                                             int32_t dim, int32_t dtype);
+int submconv_attention_backward(const void *grad, const void *q, const void *k, const void *v, const void *out,
+                                const float *lse, const int64_t *strides, const int32_t *q_offsets,
+                                const int32_t *k_offsets, int32_t entries, int64_t nq, int64_t nk, int32_t heads,
+                                int32_t kv_heads, int32_t dim, int32_t dtype, float scale, void *dq, void *dk,
+                                void *dv, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
  * The library keeps device blocks it has freed (rulebooks, scratch) for reuse on the
  * same device, up to a limit per device (2 GiB unless set below), so that repeated
  * builds make no driver allocation calls.  A block freed while work queued on its

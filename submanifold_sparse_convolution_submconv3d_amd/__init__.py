@@ -24,6 +24,9 @@ Functions carry the C names:
     submconv_layer_norm_backward(grad, x, stats, weight) -> (dx, dweight, dbias)
     submconv_rotary(x, positions, freqs, sections)  -> rotated heads
     rotary_freqs(sections, theta, device)           -> one frequency ladder per axis
+    submconv_attention(q, k, v, q_offsets, k_offsets) -> out (and its log-sum-exp)
+    submconv_attention_backward(grad, q, k, v, out, lse, q_offsets, k_offsets) -> (dq, dk, dv)
+    batch_offsets(coords, batch)                    -> offsets of a coordinate set's batch entries
 
 `RulebookCache` keeps one rulebook per coordinate set, keyed like the
 upstream library's indice_key, so every convolution on a set reuses its map
@@ -44,6 +47,7 @@ __all__ = [
     "submconv_space_to_depth", "submconv_depth_to_space", "submconv_upsample_masked", "submconv_downsample",
     "POOL_MAX", "POOL_MEAN", "classify_5d", "weight_to_krsc", "flip_ab", "release_cache", "set_cache_limit",
     "submconv_layer_norm", "submconv_layer_norm_backward", "submconv_rotary", "rotary_freqs",
+    "submconv_attention", "submconv_attention_backward", "batch_offsets",
     "KERNEL_AUTO", "KERNEL_GENERIC", "KERNEL_LOWC", "KERNEL_MFMA", "KERNEL_WINDOW", "KERNEL_PERSISTENT",
 ]
 
@@ -101,11 +105,18 @@ def load_library():
         "submconv_layer_norm_backward": [vp, i64, vp, i64, i64, i32, i32, vp, vp, i32, vp, i64, vp, vp, vp,
                                          ctypes.c_size_t, vp],
         "submconv_rotary": [vp, i64, i64, vp, i64, vp, i32p, i32, i64, i32, i32, i32, i32, i32, vp, i64, i64, vp],
+        "submconv_attention": [vp, vp, vp, i64p, vp, vp, i32, i64, i64, i32, i32, i32, i32, f32, vp, vp, vp,
+                               ctypes.c_size_t, vp],
+        "submconv_attention_backward": [vp, vp, vp, vp, vp, vp, i64p, vp, vp, i32, i64, i64, i32, i32, i32, i32, f32,
+                                        vp, vp, vp, vp, ctypes.c_size_t, vp],
     }
     for name, args in sig.items():
         fn = getattr(lib, name)
         fn.argtypes = args
         fn.restype = ctypes.c_int
+    for name in ("submconv_attention_workspace", "submconv_attention_backward_workspace"):
+        getattr(lib, name).argtypes = [i32, i64, i64, i32, i32, i32, i32]
+        getattr(lib, name).restype = ctypes.c_size_t
     lib.submconv_layer_norm_backward_workspace.argtypes = [i64, i32, i32]
     lib.submconv_layer_norm_backward_workspace.restype = ctypes.c_size_t
     for name in ("submconv_status_string",):
@@ -479,7 +490,7 @@ def _strided(t: torch.Tensor, name: str, dims: int, device=None, dtype=None) -> 
         raise ValueError("%s is on %s, not on %s" % (name, t.device, device))
     if t.dim() != dims:
         raise ValueError("%s must have %d dimensions, got %d" % (name, dims, t.dim()))
-    if t.stride(dims - 1) != 1 and t.shape[dims - 1] > 1:
+    if t.stride(dims - 1) != 1 and t.shape[dims - 1] > 1 and t.numel():
         raise ValueError("the last dimension of %s must be contiguous" % name)
     return t
 
@@ -575,8 +586,10 @@ def rotary_freqs(sections, theta: float = 10000.0, device="cuda") -> torch.Tenso
 def _head_strides(t: torch.Tensor):
     """(row, head) distances of [N,H,D]; torch may report any for a dimension of one."""
     n, h, d = t.shape
+    if not n:
+        return h * d, d
     head = t.stride(1) if h > 1 else d
-    return (t.stride(0) if n > 1 else max(h * head, d) if head else d), head
+    return (t.stride(0) if n > 1 else (h - 1) * head + d), head
 
 
 def submconv_rotary(x: torch.Tensor, positions: torch.Tensor, freqs: torch.Tensor, sections, inverse: bool = False,
@@ -610,6 +623,98 @@ def submconv_rotary(x: torch.Tensor, positions: torch.Tensor, freqs: torch.Tenso
             (ctypes.c_int32 * max(1, axes))(*sections), axes, n, h, d, _dtype_code(x), int(bool(split)),
             int(bool(inverse)), out.data_ptr(), os_[0], os_[1], _raw_stream(dev.index)), "submconv_rotary")
     return out
+
+
+def batch_offsets(coords: torch.Tensor, batch: int) -> torch.Tensor:
+    """Offsets int32 [batch+1] of the batch entries of coords [N,4] whose rows are grouped by
+    ascending b (as argwhere order and every call here that makes coordinates leave them)."""
+    _dev(coords, "coords", torch.int32)
+    edges = torch.arange(int(batch) + 1, dtype=torch.int32, device=coords.device)
+    return torch.searchsorted(coords[:, 0].contiguous(), edges, out_int32=True)
+
+
+def _attention_sizes(q, k, v, q_offsets, k_offsets):
+    """Checks shared by both directions -> (device, nq, heads, dim, nk, kv_heads, entries)."""
+    dev = _strided(q, "q", 3).device
+    _strided(k, "k", 3, dev, q.dtype)
+    _strided(v, "v", 3, dev, q.dtype)
+    if k.shape != v.shape or k.shape[2] != q.shape[2]:
+        raise ValueError("q [Nq,H,D], k and v [Nk,Hk,D] must agree")
+    for name, o in (("q_offsets", q_offsets), ("k_offsets", k_offsets)):
+        if _dev(o, name, torch.int32).device != dev:
+            raise ValueError("%s is on %s, not on %s" % (name, o.device, dev))
+    entries = q_offsets.numel() - 1
+    if q_offsets.dim() != 1 or k_offsets.shape != q_offsets.shape or entries < 1:
+        raise ValueError("q_offsets and k_offsets must be [entries+1]")
+    return (dev,) + tuple(q.shape) + (k.shape[0], k.shape[1], entries)
+
+
+def submconv_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_offsets: torch.Tensor,
+                       k_offsets: Optional[torch.Tensor] = None, scale: Optional[float] = None,
+                       out: Optional[torch.Tensor] = None, return_lse: bool = False):
+    """Softmax attention inside each entry of a ragged batch -> out [Nq,H,D], or (out, lse) with
+    lse fp32 [Nq,H] for the backward pass.
+
+    q [Nq,H,D], k and v [Nk,Hk,D] with H a multiple of Hk, D a multiple of 8 up to 128; strided
+    views (parts of a packed projection) are taken as they are.  Offsets int32 [entries+1] on the
+    device (batch_offsets); k_offsets None: those of the queries.  scale None: 1/sqrt(D).  Queries
+    of an entry without keys, and rows outside every entry, give zeros (lse -inf)."""
+    k_offsets = q_offsets if k_offsets is None else k_offsets
+    dev, nq, h, d, nk, hk, entries = _attention_sizes(q, k, v, q_offsets, k_offsets)
+    if out is None:
+        out = torch.empty((nq, h, d), dtype=q.dtype, device=dev)
+    elif tuple(_strided(out, "out", 3, dev, q.dtype).shape) != (nq, h, d):
+        raise ValueError("out must be [Nq,H,D]")
+    lse = torch.empty((nq, h), dtype=torch.float32, device=dev) if return_lse else None
+    lib = _lib if _lib is not None else load_library()
+    code = _dtype_code(q)
+    nbytes = lib.submconv_attention_workspace(entries, nq, nk, h, hk, d, code)
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
+    strides = (ctypes.c_int64 * 8)(*_head_strides(q), *_head_strides(k), *_head_strides(v), *_head_strides(out))
+    with _on_device(dev):
+        _check(lib.submconv_attention(
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), strides, q_offsets.data_ptr(), k_offsets.data_ptr(), entries, nq,
+            nk, h, hk, d, code, d ** -0.5 if scale is None else scale, out.data_ptr(),
+            None if lse is None else lse.data_ptr(), None if ws is None else ws.data_ptr(), nbytes,
+            _raw_stream(dev.index)), "submconv_attention")
+    return (out, lse) if return_lse else out
+
+
+def submconv_attention_backward(grad: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                                out: torch.Tensor, lse: torch.Tensor, q_offsets: torch.Tensor,
+                                k_offsets: Optional[torch.Tensor] = None, scale: Optional[float] = None,
+                                dq: Optional[torch.Tensor] = None, dk: Optional[torch.Tensor] = None,
+                                dv: Optional[torch.Tensor] = None):
+    """Gradients of submconv_attention -> (dq, dk, dv), from its out and lse.  A shared key head's
+    gradient is summed over its query heads.  dq, dk, dv may be given (parts of a packed gradient).
+    Sums run in a fixed order: equal calls give equal bits."""
+    k_offsets = q_offsets if k_offsets is None else k_offsets
+    dev, nq, h, d, nk, hk, entries = _attention_sizes(q, k, v, q_offsets, k_offsets)
+    for name, t in (("grad", grad), ("out", out)):
+        if tuple(_strided(t, name, 3, dev, q.dtype).shape) != (nq, h, d):
+            raise ValueError("%s must be [Nq,H,D]" % name)
+    if tuple(_dev(lse, "lse", torch.float32).shape) != (nq, h) or lse.device != dev:
+        raise ValueError("lse must be fp32 [Nq,H] on q's device")
+    made = []
+    for name, t, shape in (("dq", dq, (nq, h, d)), ("dk", dk, (nk, hk, d)), ("dv", dv, (nk, hk, d))):
+        if t is None:
+            t = torch.empty(shape, dtype=q.dtype, device=dev)
+        elif tuple(_strided(t, name, 3, dev, q.dtype).shape) != shape:
+            raise ValueError("%s must be %s" % (name, list(shape)))
+        made.append(t)
+    dq, dk, dv = made
+    lib = _lib if _lib is not None else load_library()
+    code = _dtype_code(q)
+    nbytes = lib.submconv_attention_backward_workspace(entries, nq, nk, h, hk, d, code)
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    strides = (ctypes.c_int64 * 16)(*[s for t in (grad, q, k, v, out, dq, dk, dv) for s in _head_strides(t)])
+    with _on_device(dev):
+        _check(lib.submconv_attention_backward(
+            grad.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(), strides,
+            q_offsets.data_ptr(), k_offsets.data_ptr(), entries, nq, nk, h, hk, d, code,
+            d ** -0.5 if scale is None else scale, dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), ws.data_ptr(), nbytes,
+            _raw_stream(dev.index)), "submconv_attention_backward")
+    return dq, dk, dv
 
 
 def release_cache(device: int = -1) -> None:

@@ -10,6 +10,7 @@
 #include <unordered_map>
 #include <vector>
 
+#include "attention.h"
 #include "common.h"
 
 namespace sc {
@@ -44,6 +45,10 @@ int layer_norm_backward(const void *gy, int64_t ldg, const void *x, int64_t ldx,
 int rotary(const void *x, int64_t x_row, int64_t x_head, const int32_t *pos, int64_t pos_row, const float *freqs,
            const int32_t *sections, int axes, int64_t n, int heads, int dim, int dtype, int split, int inverse,
            void *out, int64_t out_row, int64_t out_head, hipStream_t s);
+size_t attention_workspace(const AttnArgs &A, int dtype);
+int attention(const AttnArgs &A, int dtype, void *workspace, hipStream_t s);
+size_t attention_backward_workspace(const AttnArgs &A, int dtype);
+int attention_backward(AttnArgs A, int dtype, void *workspace, hipStream_t s);
 
 static thread_local char g_err[512];
 
@@ -352,6 +357,46 @@ constexpr int64_t MAX_ROWS = int64_t(1) << 31, MAX_STRIDE = int64_t(1) << 24;
 
 // Bytes from the first to past the last element of [n, c] with rows ld apart.
 static size_t span2(int64_t n, int64_t c, int64_t ld, size_t es) { return n ? (size_t)((n - 1) * ld + c) * es : 0; }
+
+// Memory a call reads or writes: rows of `foot` bytes, `row` bytes apart (0: one piece),
+// `bytes` from the first byte to past the last.
+struct Range {
+    const char *what;
+    const void *p;
+    size_t bytes;
+    bool written;
+    size_t row, foot;
+};
+
+static Range range1(const char *what, const void *p, size_t bytes, bool written) { return Range{what, p, bytes, written, 0, 0}; }
+
+static Range range2(const char *what, const void *p, int64_t n, int64_t c, int64_t ld, size_t es, bool written)
+{
+    return Range{what, p, span2(n, c, ld, es), written, (size_t)ld * es, (size_t)c * es};
+}
+
+// Whether two ranges share bytes.  Rows equally far apart may interleave (columns of one
+// wider tensor).
+static bool collide(const Range &a, const Range &b)
+{
+    if (!a.p || !b.p || !a.bytes || !b.bytes || !overlaps(a.p, a.bytes, b.p, b.bytes)) return false;
+    if (a.row && a.row == b.row && a.foot <= a.row && b.foot <= b.row) {
+        const uintptr_t x = (uintptr_t)a.p, y = (uintptr_t)b.p;
+        const size_t d = x <= y ? (y - x) % a.row : (a.row - (x - y) % a.row) % a.row;
+        return !(d >= a.foot && d + b.foot <= a.row);
+    }
+    return true;
+}
+
+// A written range may share bytes with no other.
+static int ranges_check(const Range *r, int n)
+{
+    for (int i = 0; i < n; ++i)
+        for (int j = 0; j < n; ++j)
+            if (i != j && r[i].written && collide(r[i], r[j]))
+                return fail(SUBMCONV_E_ALIAS, "%s overlaps %s", r[i].what, r[j].what);
+    return SUBMCONV_OK;
+}
 
 }  // namespace sc
 
@@ -697,12 +742,11 @@ int submconv_layer_norm(const void *x, int64_t x_row, int64_t n, int32_t c, int3
     const size_t es = elem_size(dtype), ps = elem_size(param_dtype);
     if (!aligned_to(x, es) || !aligned_to(y, es) || !aligned_to(weight, ps) || !aligned_to(bias, ps) || !aligned_to(stats, 8))
         return fail(SUBMCONV_E_INVALID_ARG, "misaligned pointer");
-    const size_t xb = span2(n, c, x_row, es), yb = span2(n, c, y_row, es), pb = (size_t)c * ps, sb = (size_t)n * 8;
-    if ((overlaps(y, yb, x, xb) && !(x == y && x_row == y_row)) || (weight && overlaps(y, yb, weight, pb)) ||
-        (bias && overlaps(y, yb, bias, pb)) ||
-        (stats && (overlaps(stats, sb, x, xb) || overlaps(stats, sb, y, yb) || (weight && overlaps(stats, sb, weight, pb)) ||
-                   (bias && overlaps(stats, sb, bias, pb)))))
-        return fail(SUBMCONV_E_ALIAS, "an output overlaps an input or the other output");
+    // y in the place of x is fine
+    const Range r[] = {range2("x", x == y && x_row == y_row ? nullptr : x, n, c, x_row, es, false),
+                       range2("y", y, n, c, y_row, es, true), range1("weight", weight, (size_t)c * ps, false),
+                       range1("bias", bias, (size_t)c * ps, false), range1("stats", stats, (size_t)n * 8, true)};
+    SC_CHECK(ranges_check(r, 5));
     return layer_norm(x, x_row, n, c, dtype, weight, bias, param_dtype, eps, y, y_row, stats, (hipStream_t)stream);
 }
 
@@ -728,28 +772,24 @@ int submconv_layer_norm_backward(const void *grad, int64_t grad_row, const void 
     const size_t need = dweight || dbias ? norm_bwd_workspace(n, c, dtype) : 0;
     if (need && (!workspace || workspace_bytes < need))
         return fail(SUBMCONV_E_INVALID_ARG, "workspace of %zu bytes, %zu needed", workspace ? workspace_bytes : 0, need);
-    const size_t gb = span2(n, c, grad_row, es), xb = span2(n, c, x_row, es), db = span2(n, c, dx_row, es),
-                 pb = (size_t)c * ps, sb = (size_t)n * 8;
-    struct { const void *p; size_t b; } in[] = {{x, xb}, {stats, sb}, {weight, pb}, {grad, gb}},
-                                        out[] = {{dweight, pb}, {dbias, pb}, {workspace, need}, {dx, db}};
-    for (int i = 0; i < 4; ++i) {
-        if (!out[i].p || !out[i].b) continue;
-        for (int j = 0; j < 4; ++j)
-            if (in[j].p && overlaps(out[i].p, out[i].b, in[j].p, in[j].b) &&
-                !(i == 3 && j == 3 && dx == grad && dx_row == grad_row))
-                return fail(SUBMCONV_E_ALIAS, "an output or the workspace overlaps an input");
-        for (int j = 0; j < i; ++j)
-            if (out[j].p && overlaps(out[i].p, out[i].b, out[j].p, out[j].b))
-                return fail(SUBMCONV_E_ALIAS, "two outputs or the workspace overlap");
-    }
+    const size_t pb = (size_t)c * ps;
+    // dx in the place of grad is fine
+    const Range r[] = {range2("grad", grad == dx && grad_row == dx_row ? nullptr : grad, n, c, grad_row, es, false),
+                       range2("x", x, n, c, x_row, es, false), range2("dx", dx, n, c, dx_row, es, true),
+                       range1("stats", stats, (size_t)n * 8, false), range1("weight", weight, pb, false),
+                       range1("dweight", dweight, pb, true), range1("dbias", dbias, pb, true),
+                       range1("workspace", workspace, need, true)};
+    SC_CHECK(ranges_check(r, 8));
     return layer_norm_backward(grad, grad_row, x, x_row, n, c, dtype, stats, weight, param_dtype, dx, dx_row, dweight,
                                dbias, workspace, (hipStream_t)stream);
 }
 
-// Bytes spanned by [n, heads, dim] with the given element distances; 0 if empty.
-static size_t span3(int64_t n, int64_t heads, int64_t dim, int64_t row, int64_t head, size_t es)
+// [n, heads, dim] with the given element distances.
+static Range range3(const char *what, const void *p, int64_t n, int64_t heads, int64_t dim, int64_t row, int64_t head,
+                    size_t es, bool written)
 {
-    return n && heads ? (size_t)((n - 1) * row + (heads - 1) * head + dim) * es : 0;
+    const size_t foot = (size_t)((heads - 1) * head + dim) * es;
+    return Range{what, p, n ? (size_t)((n - 1) * row) * es + foot : 0, written, (size_t)row * es, foot};
 }
 
 // The distances of an [n, heads, dim] tensor; one that is written has each element once.
@@ -793,13 +833,134 @@ int submconv_rotary(const void *x, int64_t x_row, int64_t x_head, const int32_t 
     const size_t es = elem_size(dtype);
     if (!aligned_to(x, es) || !aligned_to(out, es) || !aligned_to(positions, 4) || !aligned_to(freqs, 4))
         return fail(SUBMCONV_E_INVALID_ARG, "misaligned pointer");
-    const size_t xb = span3(n, heads, dim, x_row, x_head, es), ob = span3(n, heads, dim, out_row, out_head, es);
-    const bool same = x == out && x_row == out_row && (heads == 1 || x_head == out_head);
-    if ((overlaps(out, ob, x, xb) && !same) || overlaps(out, ob, positions, span2(n, axes, pos_row, 4)) ||
-        (pairs && overlaps(out, ob, freqs, (size_t)pairs * 4)))
-        return fail(SUBMCONV_E_ALIAS, "out overlaps an input");
+    const bool same = x == out && x_row == out_row && (heads == 1 || x_head == out_head);  // in place
+    const Range r[] = {range3("x", same ? nullptr : x, n, heads, dim, x_row, x_head, es, false),
+                       range3("out", out, n, heads, dim, out_row, out_head, es, true),
+                       range2("positions", positions, n, axes, pos_row, 4, false),
+                       range1("freqs", freqs, (size_t)pairs * 4, false)};
+    SC_CHECK(ranges_check(r, 4));
     return rotary(x, x_row, x_head, positions, pos_row, freqs, sections, axes, n, heads, dim, dtype, split, inverse,
                   out, out_row, out_head, (hipStream_t)stream);
+}
+
+// Sizes of an attention call, checked, into A (pointers stay zero).
+static int attn_sizes(AttnArgs *A, int32_t entries, int64_t nq, int64_t nk, int32_t heads, int32_t kv_heads,
+                      int32_t dim, int32_t dtype)
+{
+    *A = AttnArgs{};
+    if (!known_dtype(dtype)) return fail(SUBMCONV_E_UNSUPPORTED, "dtype %d", dtype);
+    if (entries < 1 || entries > 1 << 20) return fail(SUBMCONV_E_INVALID_ARG, "entries = %d outside 1..2^20", entries);
+    if (kv_heads < 1 || heads < kv_heads || heads > 1024 || heads % kv_heads)
+        return fail(SUBMCONV_E_UNSUPPORTED, "heads = %d, kv_heads = %d: heads must be a multiple of kv_heads, up to 1024", heads, kv_heads);
+    if (dim < 8 || dim > SUBMCONV_ATTENTION_MAX_DIM || dim % 8)
+        return fail(SUBMCONV_E_UNSUPPORTED, "dim = %d is not a multiple of 8 in 8..%d", dim, SUBMCONV_ATTENTION_MAX_DIM);
+    if (nq < 0 || nk < 0 || nq >= MAX_ROWS / heads || nk >= MAX_ROWS / kv_heads)
+        return fail(SUBMCONV_E_INVALID_ARG, "nq = %lld, nk = %lld: rows times heads must stay below 2^31", (long long)nq, (long long)nk);
+    A->entries = entries;
+    A->nq = nq;
+    A->nk = nk;
+    A->heads = heads;
+    A->kv_heads = kv_heads;
+    A->group = heads / kv_heads;
+    A->dim = dim;
+    return SUBMCONV_OK;
+}
+
+size_t submconv_attention_workspace(int32_t entries, int64_t nq, int64_t nk, int32_t heads, int32_t kv_heads,
+                                    int32_t dim, int32_t dtype)
+{
+    AttnArgs A;
+    return attn_sizes(&A, entries, nq, nk, heads, kv_heads, dim, dtype) == SUBMCONV_OK ? attention_workspace(A, dtype) : 0;
+}
+
+size_t submconv_attention_backward_workspace(int32_t entries, int64_t nq, int64_t nk, int32_t heads, int32_t kv_heads,
+                                             int32_t dim, int32_t dtype)
+{
+    AttnArgs A;
+    return attn_sizes(&A, entries, nq, nk, heads, kv_heads, dim, dtype) == SUBMCONV_OK ? attention_backward_workspace(A, dtype) : 0;
+}
+
+// One [n, heads, dim] tensor of a call: its pointer, distances and range.
+static int attn_tensor(const char *what, const void *p, const int64_t *st, int64_t n, int64_t heads, int64_t dim,
+                       size_t es, bool written, Heads *h, Range *r)
+{
+    if (n && !p) return fail(SUBMCONV_E_INVALID_ARG, "%s is NULL", what);
+    if (!aligned_to(p, es)) return fail(SUBMCONV_E_INVALID_ARG, "%s is misaligned", what);
+    SC_CHECK(heads_check(what, n, heads, dim, st[0], st[1], written));
+    *h = Heads{p, st[0], st[1]};
+    *r = range3(what, p, n, heads, dim, st[0], st[1], es, written);
+    return SUBMCONV_OK;
+}
+
+int submconv_attention(const void *q, const void *k, const void *v, const int64_t *strides, const int32_t *q_offsets,
+                       const int32_t *k_offsets, int32_t entries, int64_t nq, int64_t nk, int32_t heads,
+                       int32_t kv_heads, int32_t dim, int32_t dtype, float scale, void *out, float *lse,
+                       void *workspace, size_t workspace_bytes, void *stream)
+{
+    AttnArgs A;
+    SC_CHECK(attn_sizes(&A, entries, nq, nk, heads, kv_heads, dim, dtype));
+    if (!(scale > 0.0f) || scale > 3.4e38f) return fail(SUBMCONV_E_INVALID_ARG, "scale = %g is not finite and positive", (double)scale);
+    if (!strides) return fail(SUBMCONV_E_INVALID_ARG, "strides is NULL");
+    if (nq == 0) return SUBMCONV_OK;
+    if (!q_offsets || !k_offsets) return fail(SUBMCONV_E_INVALID_ARG, "offsets are NULL");
+    if (!aligned_to(q_offsets, 4) || !aligned_to(k_offsets, 4) || !aligned_to(lse, 4) || !aligned16(workspace))
+        return fail(SUBMCONV_E_INVALID_ARG, "misaligned pointer");
+    const size_t es = elem_size(dtype), need = attention_workspace(A, dtype), ob = ((size_t)entries + 1) * 4;
+    if (need && (!workspace || workspace_bytes < need))
+        return fail(SUBMCONV_E_INVALID_ARG, "workspace of %zu bytes, %zu needed", workspace ? workspace_bytes : 0, need);
+    Range r[8];
+    SC_CHECK(attn_tensor("q", q, strides, nq, heads, dim, es, false, &A.q, &r[0]));
+    SC_CHECK(attn_tensor("k", k, strides + 2, nk, kv_heads, dim, es, false, &A.k, &r[1]));
+    SC_CHECK(attn_tensor("v", v, strides + 4, nk, kv_heads, dim, es, false, &A.v, &r[2]));
+    SC_CHECK(attn_tensor("out", out, strides + 6, nq, heads, dim, es, true, &A.out, &r[3]));
+    r[4] = range1("lse", lse, (size_t)nq * heads * 4, true);
+    r[5] = range1("workspace", workspace, need, true);
+    r[6] = range1("q_offsets", q_offsets, ob, false);
+    r[7] = range1("k_offsets", k_offsets, ob, false);
+    SC_CHECK(ranges_check(r, 8));
+    A.q_off = q_offsets;
+    A.k_off = k_offsets;
+    A.scale = scale;
+    A.lse = lse;
+    return attention(A, dtype, workspace, (hipStream_t)stream);
+}
+
+int submconv_attention_backward(const void *grad, const void *q, const void *k, const void *v, const void *out,
+                                const float *lse, const int64_t *strides, const int32_t *q_offsets,
+                                const int32_t *k_offsets, int32_t entries, int64_t nq, int64_t nk, int32_t heads,
+                                int32_t kv_heads, int32_t dim, int32_t dtype, float scale, void *dq, void *dk,
+                                void *dv, void *workspace, size_t workspace_bytes, void *stream)
+{
+    AttnArgs A;
+    SC_CHECK(attn_sizes(&A, entries, nq, nk, heads, kv_heads, dim, dtype));
+    if (!(scale > 0.0f) || scale > 3.4e38f) return fail(SUBMCONV_E_INVALID_ARG, "scale = %g is not finite and positive", (double)scale);
+    if (!strides) return fail(SUBMCONV_E_INVALID_ARG, "strides is NULL");
+    if (nq == 0 && nk == 0) return SUBMCONV_OK;
+    if (!q_offsets || !k_offsets || (nq && !lse)) return fail(SUBMCONV_E_INVALID_ARG, "offsets or lse are NULL");
+    if (!aligned_to(q_offsets, 4) || !aligned_to(k_offsets, 4) || !aligned_to(lse, 4) || !aligned16(workspace))
+        return fail(SUBMCONV_E_INVALID_ARG, "misaligned pointer");
+    const size_t es = elem_size(dtype), need = attention_backward_workspace(A, dtype), ob = ((size_t)entries + 1) * 4;
+    if (need && (!workspace || workspace_bytes < need))
+        return fail(SUBMCONV_E_INVALID_ARG, "workspace of %zu bytes, %zu needed", workspace ? workspace_bytes : 0, need);
+    Range r[12];
+    SC_CHECK(attn_tensor("grad", grad, strides, nq, heads, dim, es, false, &A.grad, &r[0]));
+    SC_CHECK(attn_tensor("q", q, strides + 2, nq, heads, dim, es, false, &A.q, &r[1]));
+    SC_CHECK(attn_tensor("k", k, strides + 4, nk, kv_heads, dim, es, false, &A.k, &r[2]));
+    SC_CHECK(attn_tensor("v", v, strides + 6, nk, kv_heads, dim, es, false, &A.v, &r[3]));
+    SC_CHECK(attn_tensor("out", out, strides + 8, nq, heads, dim, es, false, &A.out, &r[4]));
+    SC_CHECK(attn_tensor("dq", dq, strides + 10, nq, heads, dim, es, true, &A.dq, &r[5]));
+    SC_CHECK(attn_tensor("dk", dk, strides + 12, nk, kv_heads, dim, es, true, &A.dk, &r[6]));
+    SC_CHECK(attn_tensor("dv", dv, strides + 14, nk, kv_heads, dim, es, true, &A.dv, &r[7]));
+    r[8] = range1("lse", lse, (size_t)nq * heads * 4, false);
+    r[9] = range1("workspace", workspace, need, true);
+    r[10] = range1("q_offsets", q_offsets, ob, false);
+    r[11] = range1("k_offsets", k_offsets, ob, false);
+    SC_CHECK(ranges_check(r, 12));
+    A.q_off = q_offsets;
+    A.k_off = k_offsets;
+    A.scale = scale;
+    A.lse = const_cast<float *>(lse);
+    return attention_backward(A, dtype, workspace, (hipStream_t)stream);
 }
 
 int submconv_release_cache(int32_t device)

@@ -1,0 +1,361 @@
+// Shared by the attention kernels (attention.hip, attention_bwd.hip): the ragged tile
+// lookup, tiles in LDS, and the matrix products on them.
+//
+// All products are 32x32 blocks on the matrix cores.  With l = lane, a = l / 32, an
+// operand of a product over the head dimension is row l % 32 of a tile, 16 bytes at a time: half a
+// holds pieces 2j + a.  (For fp32 that orders the dimension differently from the
+// instruction's own order, the same way on both sides, so the sum is the same.)  The
+// result block has column l % 32 and rows 8 (i / 4) + 4 a + i % 4 in its 16 registers i.
+//
+// The kernels always put the rows they own (queries, or keys) in the columns.  A lane
+// then owns one query (or key), softmax statistics need one exchange between halves,
+// and the result registers, rounded to the operand type, are the second operand of the
+// next product, over the other side's rows: its first operand, the transposed tile, is
+// read from LDS in the row order those registers have.
+#pragma once
+
+#include "rowvec.h"
+
+namespace sc {
+
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+
+#define SC_LDS __attribute__((address_space(3)))
+
+constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
+
+// --------------------------------------------------------------------------
+// ragged batches
+// --------------------------------------------------------------------------
+
+// The rows of a packed ragged batch: entry e has rows [off[e], off[e + 1]).  Seen as
+// entries + 2 parts: what lies before the first and after the last offset are parts
+// without a counterpart on the other side.  Bounds are clamped to [0, n], so offsets
+// that do not ascend cannot lead outside the tensors.
+struct Ragged {
+    const int32_t *off;
+    int entries;
+    int64_t n;
+    int mult;  // query rows of a token (heads that share a key head), 1 for keys
+
+    __device__ __forceinline__ int64_t bound(int part) const
+    {
+        if (part <= 0) return 0;
+        if (part > entries + 1) return n;
+        const int64_t o = off[part - 1];
+        return o < 0 ? 0 : (o > n ? n : o);
+    }
+    // First tile number of a part: tiles of `rows` rows, numbered with gaps so that the
+    // number needs the part's own bound alone.
+    __device__ __forceinline__ int64_t first_tile(int part, int rows) const { return bound(part) * mult / rows + part; }
+};
+
+static inline int64_t ragged_tiles(int64_t n, int entries, int mult, int rows) { return n * mult / rows + entries + 2; }
+
+// Part and tile within it of tile number `slot`: 64 bounds are compared at a time.  The
+// same in all lanes.
+__device__ __forceinline__ void find_tile(const Ragged &r, int rows, int64_t slot, int *part, int64_t *tile)
+{
+    int lo = 0, hi = r.entries + 2;
+    while (hi - lo > 1) {
+        const int step = (hi - lo + 63) / 64;
+        const int p = lo + (int)lane_id() * step;
+        const uint64_t le = __ballot(p < hi && r.first_tile(p, rows) <= slot);
+        const int count = ~le ? __builtin_ctzll(~le) : 64;
+        const int next = lo + (count > 1 ? count - 1 : 0) * step;
+        hi = next + step < hi ? next + step : hi;
+        lo = next;
+    }
+    *part = __builtin_amdgcn_readfirstlane(lo);
+    *tile = slot - r.first_tile(*part, rows);
+}
+
+// The part that holds a row (mult = 1).
+__device__ __forceinline__ int find_part(const Ragged &r, int64_t row)
+{
+    int lo = 0, hi = r.entries + 2;
+    while (hi - lo > 1) {
+        const int step = (hi - lo + 63) / 64;
+        const int p = lo + (int)lane_id() * step;
+        const uint64_t le = __ballot(p < hi && r.bound(p) <= row);
+        const int count = ~le ? __builtin_ctzll(~le) : 64;
+        const int next = lo + (count > 1 ? count - 1 : 0) * step;
+        hi = next + step < hi ? next + step : hi;
+        lo = next;
+    }
+    return __builtin_amdgcn_readfirstlane(lo);
+}
+
+// Work number of a block: runs of 16 go to one XCD (blocks are dealt to the 8 XCDs in
+// turn), so that neighbours, which read the same keys, share an L2.  Grids are whole
+// multiples of 128; numbers past the work are idle.
+constexpr int XCD_RUN = 16;
+static inline unsigned xcd_grid(int64_t total) { return (unsigned)((total + 8 * XCD_RUN - 1) / (8 * XCD_RUN) * (8 * XCD_RUN)); }
+__device__ __forceinline__ unsigned xcd_work()
+{
+    const unsigned b = blockIdx.x, g = b / (8 * XCD_RUN), in = b % (8 * XCD_RUN);
+    return g * (8 * XCD_RUN) + (in % 8) * XCD_RUN + in / 8;
+}
+
+// --------------------------------------------------------------------------
+// tiles in LDS
+// --------------------------------------------------------------------------
+
+// A tile is rows of RB bytes (the padded head).  16-byte pieces of row r are permuted by
+// an exclusive or with swizzle(r): 16 rows read at one piece (the operand over the head
+// dimension), and 4 rows read at four neighbouring pieces (the transposed operand), then fall on
+// different banks for every RB.
+template <int RB>
+__device__ __forceinline__ uint32_t swizzle(uint32_t row)
+{
+    uint32_t s = (row >> 2) & 3;
+    if (RB % 256 == 0) s |= (row & 3) << 2;
+    else if (RB % 128 == 0) s |= ((row >> 1) & 1) << 2;
+    return s;
+}
+
+template <int RB>
+__device__ __forceinline__ uint32_t piece_at(uint32_t row, uint32_t piece)
+{
+    return row * RB + ((piece ^ swizzle<RB>(row)) << 4);
+}
+
+__device__ __forceinline__ Raw16 lds_read16(uint32_t at) { return *(const SC_LDS Raw16 *)(uintptr_t)at; }
+__device__ __forceinline__ void lds_write16(uint32_t at, Raw16 v) { *(SC_LDS Raw16 *)(uintptr_t)at = v; }
+
+// Rows [row0, row0 + ROWS) of [*, heads, dim], a block's threads holding PER pieces
+// each.  Rows from `rows` on and pieces past dim are zero.
+template <typename T, int RB, int ROWS, int THREADS>
+struct TileLoad {
+    static constexpr int CPR = RB / 16, PER = ROWS * CPR / THREADS;
+    static_assert(ROWS * CPR % THREADS == 0, "whole pieces a thread");
+    Raw16 r[PER];
+
+    __device__ __forceinline__ void load(const T *base, int64_t row_stride, int rows, int dim)
+    {
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const int x = threadIdx.x + i * THREADS, row = x / CPR, c = x % CPR;
+            r[i] = Raw16{0, 0, 0, 0};
+            if (row < rows && c * VEC<T> < dim) r[i] = *(const Raw16Any *)(base + row * row_stride + c * VEC<T>);
+        }
+    }
+    // Rows of a group of query heads: row r is token r / group, head r % group of the group.
+    __device__ __forceinline__ void load_grouped(const T *base, int64_t row_stride, int64_t head_stride, uint32_t row0,
+                                                 uint32_t group, int rows, int dim)
+    {
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const int x = threadIdx.x + i * THREADS, row = x / CPR, c = x % CPR;
+            r[i] = Raw16{0, 0, 0, 0};
+            if (row < rows && c * VEC<T> < dim) {
+                const uint32_t at = row0 + row, token = group == 1 ? at : at / group;
+                r[i] = *(const Raw16Any *)(base + token * row_stride + (at - token * group) * head_stride + c * VEC<T>);
+            }
+        }
+    }
+    __device__ __forceinline__ void store(uint32_t lds) const
+    {
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const int x = threadIdx.x + i * THREADS;
+            lds_write16(lds + piece_at<RB>(x / CPR, x % CPR), r[i]);
+        }
+    }
+};
+
+// --------------------------------------------------------------------------
+// products
+// --------------------------------------------------------------------------
+
+// c += a b over one pair of pieces (8 bf16 or 4 fp32 of each half).
+template <typename T>
+__device__ __forceinline__ f32x16 mma_pieces(Raw16 a, Raw16 b, f32x16 c)
+{
+    if constexpr (sizeof(T) == 2) {
+        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            c = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(a[i]), __uint_as_float(b[i]), c, 0, 0, 0);
+        return c;
+    }
+}
+
+// Addresses of a lane's operand over the head dimension: row l % 32, piece 2j + a.
+template <int RB>
+struct HeadAddr {
+    uint32_t at[RB / 32];
+    __device__ __forceinline__ explicit HeadAddr(uint32_t lds)
+    {
+        const uint32_t l = lane_id();
+#pragma unroll
+        for (int j = 0; j < RB / 32; ++j) at[j] = lds + piece_at<RB>(l & 31, 2 * j + (l >> 5));
+    }
+};
+
+// Addresses of a lane's transposed operand: row l % 32 of it is element 32 db + l % 32
+// of the head; its columns are tile rows in the order of a result block's registers.
+//   bf16: two 8-byte transposing reads give rows 4a .. 4a + 3 and 8 + 4a .. of 16.
+//   fp32: one element of row 8 (i / 4) + 4 a + i % 4 at a time.
+template <typename T, int RB>
+struct RowsAddr;
+template <int RB>
+struct RowsAddr<uint16_t, RB> {
+    static constexpr int DB = RB / 64;
+    uint32_t at[2][DB];
+    __device__ __forceinline__ explicit RowsAddr(uint32_t lds)
+    {
+        const uint32_t l = lane_id(), a = l >> 5, g = (l >> 4) & 1, t = l & 15;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int db = 0; db < DB; ++db)
+                at[h][db] = lds + piece_at<RB>(8 * h + 4 * a + t / 4, db * 4 + g * 2 + (t & 3) / 2) + (t & 1) * 8;
+    }
+};
+template <int RB>
+struct RowsAddr<float, RB> {
+    static constexpr int DB = RB / 128;
+    uint32_t at[8][DB];  // by i % 4 and bit 3 of the row; rows 16 apart share a swizzle
+    __device__ __forceinline__ explicit RowsAddr(uint32_t lds)
+    {
+        const uint32_t l = lane_id(), a = l >> 5, d = l & 31;
+#pragma unroll
+        for (int h = 0; h < 8; ++h)
+#pragma unroll
+            for (int db = 0; db < DB; ++db)
+                at[h][db] = lds + piece_at<RB>(8 * (h >> 2) + 4 * a + (h & 3), db * 8 + d / 4) + (d & 3) * 4;
+    }
+};
+
+__device__ __forceinline__ u32x2 lds_read_tr(uint32_t at)
+{
+    return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((SC_LDS s16x4 *)(uintptr_t)at));
+}
+
+// The result registers of a block of 32 rows as an operand over those rows.
+template <typename T>
+struct RowsOperand;
+template <>
+struct RowsOperand<uint16_t> {
+    Raw16 v[2];  // rows 0..15, 16..31, each rounded to bf16 (nearest even)
+    __device__ __forceinline__ void set(const f32x16 &s)
+    {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[h][i] = pack_bf16(s[8 * h + 2 * i], s[8 * h + 2 * i + 1]);
+    }
+};
+template <>
+struct RowsOperand<float> {
+    f32x16 v;
+    __device__ __forceinline__ void set(const f32x16 &s) { v = s; }
+};
+
+// acc[db] += transpose(tile rows `at_row` .. + 31) p, for every 32 elements db of the head.
+template <int RB>
+__device__ __forceinline__ void mma_rows(const RowsAddr<uint16_t, RB> &ad, uint32_t lds, const RowsOperand<uint16_t> &p,
+                                         f32x16 (&acc)[RB / 64])
+{
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int db = 0; db < RB / 64; ++db) {
+            const u32x2 lo = lds_read_tr(ad.at[0][db] + lds + 16 * h * RB), hi = lds_read_tr(ad.at[1][db] + lds + 16 * h * RB);
+            acc[db] = mma_pieces<uint16_t>(Raw16{lo[0], lo[1], hi[0], hi[1]}, p.v[h], acc[db]);
+        }
+}
+template <int RB>
+__device__ __forceinline__ void mma_rows(const RowsAddr<float, RB> &ad, uint32_t lds, const RowsOperand<float> &p,
+                                         f32x16 (&acc)[RB / 128])
+{
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+#pragma unroll
+        for (int db = 0; db < RB / 128; ++db) {
+            const float v = *(const SC_LDS float *)(uintptr_t)(ad.at[i & 7][db] + lds + 16 * (i >> 3) * RB);
+            acc[db] = __builtin_amdgcn_mfma_f32_32x32x2f32(v, p.v[i], acc[db], 0, 0, 0);
+        }
+}
+
+// The other half's value (lanes l and l ^ 32).
+__device__ __forceinline__ float other_half(float v)
+{
+    auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return __uint_as_float(lane_id() < 32 ? r[1] : r[0]);
+}
+
+// Store row l % 32 of the transposed accumulators (elements of the head in registers),
+// each value times `f`: the halves trade registers so that a lane holds 8 elements in a
+// row, and write 16 bytes (bf16) or 32 bytes (fp32) at a time.
+template <typename T, int DB>
+__device__ __forceinline__ void store_rows(const f32x16 (&acc)[DB], float f, T *row, int dim, bool valid)
+{
+    const int a = lane_id() >> 5;
+#pragma unroll
+    for (int db = 0; db < DB; ++db)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {  // registers 8h .. 8h + 3 and 8h + 4 .. 8h + 7
+            float v[8];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(acc[db][8 * h + i] * f),
+                                                          __float_as_uint(acc[db][8 * h + 4 + i] * f), false, false);
+                v[i] = __uint_as_float(r[0]);
+                v[4 + i] = __uint_as_float(r[1]);
+            }
+            const int e = 32 * db + 16 * h + 8 * a;
+            if (!valid || e >= dim) continue;
+            if constexpr (sizeof(T) == 2) {
+                *(Raw16Any *)(row + e) = Raw16{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7])};
+            } else {
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    *(Raw16Any *)(row + e + 4 * i) = Raw16{__float_as_uint(v[4 * i]), __float_as_uint(v[4 * i + 1]),
+                                                           __float_as_uint(v[4 * i + 2]), __float_as_uint(v[4 * i + 3])};
+            }
+        }
+}
+
+// --------------------------------------------------------------------------
+// arguments
+// --------------------------------------------------------------------------
+
+// [n, heads, dim] in device memory: element (i, h, d) at i * row + h * head + d.
+struct Heads {
+    const void *p;
+    int64_t row, head;
+};
+
+struct AttnArgs {
+    Heads q, k, v, out, grad, dq, dk, dv;
+    const int32_t *q_off, *k_off;
+    int entries;
+    int64_t nq, nk;
+    int heads, kv_heads, group, dim;
+    float scale;
+    float *lse;    // [nq, heads]
+    float *delta;  // [nq, heads] (backward)
+    float *part;   // partial results of a split pass
+    float *part2;
+    int chunk;     // rows of the long side in one split
+    int64_t splits;
+    int tiles;     // tiles of the short side taken by different blocks
+};
+
+// How a pass is cut along its long side: runs of `chunk` rows (0: not cut), at most
+// `splits` of them in an entry, `tiles` tiles of the own side taken by different blocks.
+struct SplitPlan {
+    int chunk;
+    int64_t splits;
+    int tiles;
+};
+SplitPlan split_plan(int64_t own_rows, int own_tile, int64_t other_rows, int other_tile, int entries, int kv_heads);
+
+}  // namespace sc
