@@ -367,7 +367,8 @@ int submconv_rotary(const void *x, int64_t x_row, int64_t x_head, const int32_t 
  *
  *   q, out : device [nq, heads, dim];  k, v : device [nk, kv_heads, dim], all of dtype;
  *            elements of a head next to each other, any alignment of the element type.
- *   strides : HOST int64 [8]: row and head distance in elements of q, k, v, out.
+ *   strides : HOST int64 [8]: row and head distance in elements of q, k, v, out; a row
+ *            distance is at most SUBMCONV_ATTENTION_MAX_ROW (else E_UNSUPPORTED).
  *   q_offsets, k_offsets : device int32 [entries + 1], ascending: entry e has the rows
  *            [off[e], off[e + 1]).  Rows before the first or from the last offset on belong
  *            to no entry: queries there get zeros.  They are read on the device only;
@@ -386,6 +387,7 @@ int submconv_rotary(const void *x, int64_t x_row, int64_t x_head, const int32_t 
  * same bits.
  */
 #define SUBMCONV_ATTENTION_MAX_DIM 128
+#define SUBMCONV_ATTENTION_MAX_ROW (1 << 22)
 size_t submconv_attention_workspace(int32_t entries, int64_t nq, int64_t nk, int32_t heads, int32_t kv_heads,
                                     int32_t dim, int32_t dtype);
 int submconv_attention(const void *q, const void *k, const void *v, const int64_t *strides, const int32_t *q_offsets,

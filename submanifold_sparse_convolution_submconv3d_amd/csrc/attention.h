@@ -101,6 +101,12 @@ __device__ __forceinline__ unsigned xcd_work()
     return g * (8 * XCD_RUN) + (in % 8) * XCD_RUN + in / 8;
 }
 
+// [n, heads, dim] in device memory: element (i, h, d) at i * row + h * head + d.
+struct Heads {
+    const void *p;
+    int64_t row, head;
+};
+
 // --------------------------------------------------------------------------
 // tiles in LDS
 // --------------------------------------------------------------------------
@@ -127,43 +133,88 @@ __device__ __forceinline__ uint32_t piece_at(uint32_t row, uint32_t piece)
 __device__ __forceinline__ Raw16 lds_read16(uint32_t at) { return *(const SC_LDS Raw16 *)(uintptr_t)at; }
 __device__ __forceinline__ void lds_write16(uint32_t at, Raw16 v) { *(SC_LDS Raw16 *)(uintptr_t)at = v; }
 
-// Rows [row0, row0 + ROWS) of [*, heads, dim], a block's threads holding PER pieces
-// each.  Rows from `rows` on and pieces past dim are zero.
-template <typename T, int RB, int ROWS, int THREADS>
-struct TileLoad {
-    static constexpr int CPR = RB / 16, PER = ROWS * CPR / THREADS;
-    static_assert(ROWS * CPR % THREADS == 0, "whole pieces a thread");
-    Raw16 r[PER];
+// Waits until at most N of this wave's vector-memory loads are in flight, and all its LDS
+// accesses are done; then a barrier.  Copies into LDS count as loads and the compiler
+// does not wait for them by itself.
+template <int N>
+__device__ __forceinline__ void wait_copies_and_barrier()
+{
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
+}
 
-    __device__ __forceinline__ void load(const T *base, int64_t row_stride, int rows, int dim)
+// Copies of 32 rows of two tensors (a tile of each, TILE = 32 RB bytes) into LDS, shared
+// evenly by the waves of a block: each copy moves 64 pieces of 16 bytes, and there are
+// RB / 16 in all.  Rows from `left` on and pieces past dim become zeros.
+//   DIRECT: straight into LDS through bounds-checked buffer copies; the data must be 16-byte
+//   aligned and 32 rows apart by less than 2^31 bytes.  The wave's copies stay in flight.
+//   Otherwise: loads and LDS writes, any alignment, done when the function returns (after
+//   a barrier).
+constexpr uint32_t OUT_OF_RANGE = 0x80000000u;
+
+template <typename T, int RB, int WAVES, bool DIRECT>
+struct Fill {
+    static constexpr int TILE = 32 * RB, PER = RB / 16 / WAVES;
+    static_assert(RB / 16 % WAVES == 0, "the same number of copies in every wave");
+    uint32_t off[PER];
+    int row[PER];
+    bool second[PER];  // which tensor a copy is of (the same in all lanes)
+    uint32_t at[PER];
+
+    // row_a, row_b: distances between rows in elements (0 for copy_grouped).
+    __device__ __forceinline__ void init(int64_t row_a, int64_t row_b, int dim)
     {
+        const uint32_t wave = threadIdx.x >> 6, lane = lane_id();
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
-            const int x = threadIdx.x + i * THREADS, row = x / CPR, c = x % CPR;
-            r[i] = Raw16{0, 0, 0, 0};
-            if (row < rows && c * VEC<T> < dim) r[i] = *(const Raw16Any *)(base + row * row_stride + c * VEC<T>);
+            const uint32_t x = wave * PER + i, sec = x >= RB / 32, in = (x - (sec ? RB / 32 : 0)) * 1024 + lane * 16;
+            const uint32_t r = in / RB, piece = (in % RB / 16) ^ swizzle<RB>(r);
+            second[i] = __builtin_amdgcn_readfirstlane(sec);
+            at[i] = __builtin_amdgcn_readfirstlane(in);  // of lane 0
+            row[i] = (int)r;
+            off[i] = piece * VEC<T> < (uint32_t)dim ? r * (uint32_t)((second[i] ? row_b : row_a) * sizeof(T)) + piece * 16
+                                                    : OUT_OF_RANGE;
         }
     }
-    // Rows of a group of query heads: row r is token r / group, head r % group of the group.
-    __device__ __forceinline__ void load_grouped(const T *base, int64_t row_stride, int64_t head_stride, uint32_t row0,
-                                                 uint32_t group, int rows, int dim)
+    // a, b: row 0 of the tiles; left_a, left_b: rows that exist; lds_a, lds_b: where to.
+    __device__ __forceinline__ void copy(const T *a, int left_a, uint32_t lds_a, const T *b, int left_b, uint32_t lds_b) const
     {
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
-            const int x = threadIdx.x + i * THREADS, row = x / CPR, c = x % CPR;
-            r[i] = Raw16{0, 0, 0, 0};
-            if (row < rows && c * VEC<T> < dim) {
-                const uint32_t at = row0 + row, token = group == 1 ? at : at / group;
-                r[i] = *(const Raw16Any *)(base + token * row_stride + (at - token * group) * head_stride + c * VEC<T>);
-            }
+            const T *base = second[i] ? b : a;
+            const int left = second[i] ? left_b : left_a;
+            const uint32_t to = (second[i] ? lds_b : lds_a) + at[i], o = row[i] < left ? off[i] : OUT_OF_RANGE;
+            put(base, o, to);
         }
     }
-    __device__ __forceinline__ void store(uint32_t lds) const
+    // The same for the rows of an entry's grouped query heads: row r is token token0 +
+    // r / group, head head0 + r % group; row0 is the tiles' first.
+    __device__ __forceinline__ void copy_grouped(const Heads &a, const Heads &b, int64_t token0, int head0, uint32_t row0,
+                                                 uint32_t group, int left, uint32_t lds_a, uint32_t lds_b) const
     {
+        const uint32_t t0 = row0 / group;
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
-            const int x = threadIdx.x + i * THREADS;
-            lds_write16(lds + piece_at<RB>(x / CPR, x % CPR), r[i]);
+            const Heads &h = second[i] ? b : a;
+            const T *base = (const T *)h.p + (token0 + t0) * h.row + head0 * h.head;
+            const uint32_t r = row0 + row[i], t = r / group, g = r - t * group;
+            const uint32_t piece = off[i];  // init with distances 0
+            const uint32_t o = row[i] < left && piece != OUT_OF_RANGE
+                                   ? (t - t0) * (uint32_t)(h.row * sizeof(T)) + g * (uint32_t)(h.head * sizeof(T)) + piece
+                                   : OUT_OF_RANGE;
+            put(base, o, (second[i] ? lds_b : lds_a) + at[i]);
+        }
+    }
+
+  private:
+    static __device__ __forceinline__ void put(const T *base, uint32_t o, uint32_t to)
+    {
+        if constexpr (DIRECT) {
+            const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc((void *)base, (short)0, 0x7fffffff, 0x00020000);
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (SC_LDS void *)(uintptr_t)to, 16, o, 0, 0, 0);
+        } else {
+            Raw16 v = {0, 0, 0, 0};
+            if (o != OUT_OF_RANGE) v = *(const Raw16Any *)((const char *)base + o);
+            lds_write16(to + lane_id() * 16, v);
         }
     }
 };
@@ -196,6 +247,11 @@ struct HeadAddr {
 #pragma unroll
         for (int j = 0; j < RB / 32; ++j) at[j] = lds + piece_at<RB>(l & 31, 2 * j + (l >> 5));
     }
+    __device__ __forceinline__ void move(uint32_t by)
+    {
+#pragma unroll
+        for (int j = 0; j < RB / 32; ++j) at[j] += by;
+    }
 };
 
 // Addresses of a lane's transposed operand: row l % 32 of it is element 32 db + l % 32
@@ -217,6 +273,13 @@ struct RowsAddr<uint16_t, RB> {
             for (int db = 0; db < DB; ++db)
                 at[h][db] = lds + piece_at<RB>(8 * h + 4 * a + t / 4, db * 4 + g * 2 + (t & 3) / 2) + (t & 1) * 8;
     }
+    __device__ __forceinline__ void move(uint32_t by)
+    {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int db = 0; db < DB; ++db) at[h][db] += by;
+    }
 };
 template <int RB>
 struct RowsAddr<float, RB> {
@@ -230,6 +293,13 @@ struct RowsAddr<float, RB> {
 #pragma unroll
             for (int db = 0; db < DB; ++db)
                 at[h][db] = lds + piece_at<RB>(8 * (h >> 2) + 4 * a + (h & 3), db * 8 + d / 4) + (d & 3) * 4;
+    }
+    __device__ __forceinline__ void move(uint32_t by)
+    {
+#pragma unroll
+        for (int h = 0; h < 8; ++h)
+#pragma unroll
+            for (int db = 0; db < DB; ++db) at[h][db] += by;
     }
 };
 
@@ -258,31 +328,37 @@ struct RowsOperand<float> {
     __device__ __forceinline__ void set(const f32x16 &s) { v = s; }
 };
 
-// acc[db] += transpose(tile rows `at_row` .. + 31) p, for every 32 elements db of the head.
-template <int RB>
-__device__ __forceinline__ void mma_rows(const RowsAddr<uint16_t, RB> &ad, uint32_t lds, const RowsOperand<uint16_t> &p,
-                                         f32x16 (&acc)[RB / 64])
+// acc[x][db] += transpose(32 tile rows) p[x], for every 32 elements db of the head; `at` is
+// added to the addresses.
+template <int RB, int N>
+__device__ __forceinline__ void mma_rows(const RowsAddr<uint16_t, RB> &ad, uint32_t at, const RowsOperand<uint16_t> (&p)[N],
+                                         f32x16 (&acc)[N][RB / 64])
 {
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
         for (int db = 0; db < RB / 64; ++db) {
-            const u32x2 lo = lds_read_tr(ad.at[0][db] + lds + 16 * h * RB), hi = lds_read_tr(ad.at[1][db] + lds + 16 * h * RB);
-            acc[db] = mma_pieces<uint16_t>(Raw16{lo[0], lo[1], hi[0], hi[1]}, p.v[h], acc[db]);
+            const u32x2 lo = lds_read_tr(ad.at[0][db] + at + 16 * h * RB), hi = lds_read_tr(ad.at[1][db] + at + 16 * h * RB);
+#pragma unroll
+            for (int x = 0; x < N; ++x)
+                acc[x][db] = mma_pieces<uint16_t>(Raw16{lo[0], lo[1], hi[0], hi[1]}, p[x].v[h], acc[x][db]);
         }
 }
-template <int RB>
-__device__ __forceinline__ void mma_rows(const RowsAddr<float, RB> &ad, uint32_t lds, const RowsOperand<float> &p,
-                                         f32x16 (&acc)[RB / 128])
+template <int RB, int N>
+__device__ __forceinline__ void mma_rows(const RowsAddr<float, RB> &ad, uint32_t at, const RowsOperand<float> (&p)[N],
+                                         f32x16 (&acc)[N][RB / 128])
 {
 #pragma unroll
     for (int i = 0; i < 16; ++i)
 #pragma unroll
         for (int db = 0; db < RB / 128; ++db) {
-            const float v = *(const SC_LDS float *)(uintptr_t)(ad.at[i & 7][db] + lds + 16 * (i >> 3) * RB);
-            acc[db] = __builtin_amdgcn_mfma_f32_32x32x2f32(v, p.v[i], acc[db], 0, 0, 0);
+            const float v = *(const SC_LDS float *)(uintptr_t)(ad.at[i & 7][db] + at + 16 * (i >> 3) * RB);
+#pragma unroll
+            for (int x = 0; x < N; ++x) acc[x][db] = __builtin_amdgcn_mfma_f32_32x32x2f32(v, p[x].v[i], acc[x][db], 0, 0, 0);
         }
 }
+
+__device__ __forceinline__ int rows_left(int64_t left) { return left < 0 ? 0 : (left > 32 ? 32 : (int)left); }
 
 // The other half's value (lanes l and l ^ 32).
 __device__ __forceinline__ float other_half(float v)
@@ -327,12 +403,6 @@ __device__ __forceinline__ void store_rows(const f32x16 (&acc)[DB], float f, T *
 // arguments
 // --------------------------------------------------------------------------
 
-// [n, heads, dim] in device memory: element (i, h, d) at i * row + h * head + d.
-struct Heads {
-    const void *p;
-    int64_t row, head;
-};
-
 struct AttnArgs {
     Heads q, k, v, out, grad, dq, dk, dv;
     const int32_t *q_off, *k_off;
@@ -341,7 +411,7 @@ struct AttnArgs {
     int heads, kv_heads, group, dim;
     float scale;
     float *lse;    // [nq, heads]
-    float *delta;  // [nq, heads] (backward)
+    float *stat;   // [nq, heads, 2]: (base, delta) of a query row (backward)
     float *part;   // partial results of a split pass
     float *part2;
     int chunk;     // rows of the long side in one split

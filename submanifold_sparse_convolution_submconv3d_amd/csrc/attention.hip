@@ -40,18 +40,23 @@ __device__ __forceinline__ float log_sum(float m, float l, float scale)
     return huge(m, c) ? m * scale + e * LN2 : (m * c + e) * LN2;
 }
 
-constexpr int FWD_WAVES = 4, FWD_ROWS = 32 * FWD_WAVES;
-template <typename T> constexpr int FWD_KEYS = sizeof(T) == 2 ? 64 : 32;
+constexpr int FWD_WAVES = 4, RING = 4;
 
-// SPLIT: a block takes one run of `chunk` keys of an entry and leaves (sum, m, l) of it
-// in part / part2 for k_attn_join; otherwise a block takes one tile of query rows over
-// all keys.
-template <typename T, int DP, bool SPLIT>
-__global__ __launch_bounds__(64 * FWD_WAVES, 2) void k_attn(AttnArgs A)
+// A step handles 32 keys.  Its wave has the scores of its own keys in registers already,
+// and, while it turns them into weights, the matrix cores form the scores of the next
+// 32 keys; then they take the weights' product with the values, and the next scores'
+// maximum is found meanwhile.  Keys are copied four steps ahead and values three, into
+// rings of four tiles in LDS.
+//
+// QB: blocks of 32 query rows a wave owns.  SPLIT: a block takes one run of `chunk` keys of
+// an entry and leaves (sum, m, l) of it in part / part2 for k_attn_join; otherwise a block
+// takes one tile of query rows over all keys.
+template <typename T, int DP, int QB, bool SPLIT, bool DIRECT>
+__global__ __launch_bounds__(64 * FWD_WAVES, DP * sizeof(T) * QB > 256 ? 1 : 2) void k_attn(AttnArgs A)
 {
-    constexpr int RB = DP * (int)sizeof(T), NJ = RB / 32, DB = DP / 32, KT = FWD_KEYS<T>, KB = KT / 32;
-    constexpr int TILE = KT * RB, BUF = 2 * TILE;
-    __shared__ __attribute__((aligned(16))) char smem[2 * BUF];
+    constexpr int RB = DP * (int)sizeof(T), NJ = RB / 32, DB = DP / 32, TILE = 32 * RB, ROWS = 32 * QB * FWD_WAVES;
+    constexpr uint32_t V0 = RING * TILE;  // the values' ring
+    __shared__ __attribute__((aligned(1024))) char smem[2 * RING * TILE];
     const uint32_t lds = (uint32_t)(uintptr_t)(SC_LDS char *)smem;
 
     const Ragged rq = {A.q_off, A.entries, A.nq, A.group}, rk = {A.k_off, A.entries, A.nk, 1};
@@ -65,131 +70,193 @@ __global__ __launch_bounds__(64 * FWD_WAVES, 2) void k_attn(AttnArgs A)
         find_tile(rk, A.chunk, w % slots, &part, &split);
         key0 = split * A.chunk;
     } else {
-        const int64_t slots = A.nq * A.group / FWD_ROWS + A.entries + 2, w = xcd_work();
+        const int64_t slots = A.nq * A.group / ROWS + A.entries + 2, w = xcd_work();
         if (w >= slots * A.kv_heads) return;
         hk = (int)(w / slots);
-        find_tile(rq, FWD_ROWS, w % slots, &part, &qtile);
+        find_tile(rq, ROWS, w % slots, &part, &qtile);
     }
     const int64_t q_beg = rq.bound(part), k_beg = rk.bound(part);
     const bool real = part >= 1 && part <= A.entries;
     const int64_t rows = (rq.bound(part + 1) - q_beg) * A.group;
-    int64_t keys = real ? rk.bound(part + 1) - k_beg - key0 : 0;
-    if (SPLIT && (keys <= 0 || !real)) return;
-    if (SPLIT && keys > A.chunk) keys = A.chunk;
-    if (keys < 0) keys = 0;
+    int64_t keys64 = real ? rk.bound(part + 1) - k_beg - key0 : 0;
+    if (SPLIT && (keys64 <= 0 || !real)) return;
+    if (SPLIT && keys64 > A.chunk) keys64 = A.chunk;
+    const int keys = keys64 < 0 ? 0 : (int)keys64, steps = (keys + 31) / 32;
 
     const int lane = lane_id(), half = lane >> 5;
     const float c = A.scale * LOG2E;
     const T *kp = (const T *)A.k.p + (k_beg + key0) * A.k.row + hk * A.k.head;
     const T *vp = (const T *)A.v.p + (k_beg + key0) * A.v.row + hk * A.v.head;
+    Fill<T, RB, FWD_WAVES, DIRECT> fill;
+    constexpr int PER = Fill<T, RB, FWD_WAVES, DIRECT>::PER;
+    fill.init(A.k.row, A.v.row, A.dim);
+    HeadAddr<RB> ka(lds);
+    RowsAddr<T, RB> va(lds + V0);
+    // keys of step u + RING and values of step u + RING - 1: their places were last read in step u - 1
+    auto copy = [&](int u) {
+        const int a = u + RING, b = u + RING - 1;
+        fill.copy(kp + a * 32 * A.k.row, rows_left((int64_t)keys - a * 32ll), lds + (a & (RING - 1)) * TILE,
+                  vp + b * 32 * A.v.row, rows_left(b < 0 ? 0 : (int64_t)keys - b * 32ll), lds + V0 + (b & (RING - 1)) * TILE);
+    };
 
-    for (; qtile * FWD_ROWS < rows; qtile += SPLIT ? A.tiles : rows) {
-        const int64_t wave_row = qtile * FWD_ROWS + (threadIdx.x >> 6) * 32;
-        const bool busy = wave_row < rows;  // a wave past the entry's rows only helps with the tiles
-        const uint32_t row = (uint32_t)(wave_row + (lane & 31));
-        const bool valid = row < rows;
-        const uint32_t token = A.group == 1 ? row : row / A.group, head = hk * A.group + (row - token * A.group);
-        Raw16 q[NJ];
-        {
-            const T *qp = (const T *)A.q.p + (q_beg + (valid ? token : 0)) * A.q.row + (valid ? head : 0) * A.q.head;
+    for (; qtile * ROWS < rows; qtile += SPLIT ? A.tiles : rows) {
+        const int64_t wave_row = qtile * ROWS + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) * (32 * QB);
+        if (SPLIT) __syncthreads();  // the rings' last readers are done
+        if (steps)
+            for (int u = -RING; u < 0; ++u) copy(u);
+        if (wave_row >= rows) {  // a wave past the entry's rows only helps with the copies
+            if (steps) {
+                wait_copies_and_barrier<3 * PER>();
+                for (int u = -1; u < steps - 1; ++u) {
+                    if (u >= 0) copy(u);
+                    wait_copies_and_barrier<2 * PER>();
+                }
+                wait_copies_and_barrier<0>();
+            }
+            continue;
+        }
+
+        Raw16 q[QB][NJ];
+#pragma unroll
+        for (int qb = 0; qb < QB; ++qb) {
+            const uint32_t row = (uint32_t)(wave_row + 32 * qb + (lane & 31)), token = A.group == 1 ? row : row / A.group;
+            const bool valid = row < rows;
+            const T *qp = (const T *)A.q.p + (q_beg + token) * A.q.row + (hk * A.group + (row - token * A.group)) * A.q.head;
 #pragma unroll
             for (int j = 0; j < NJ; ++j) {
                 const int e = (2 * j + half) * VEC<T>;
-                q[j] = Raw16{0, 0, 0, 0};
-                if (valid && e < A.dim) q[j] = *(const Raw16Any *)(qp + e);
+                q[qb][j] = Raw16{0, 0, 0, 0};
+                if (valid && e < A.dim) q[qb][j] = *(const Raw16Any *)(qp + e);
             }
         }
-        f32x16 o[DB];
+        f32x16 o[QB][DB], s[2][QB];
+        float m[QB], l[QB], base[QB];
 #pragma unroll
-        for (int db = 0; db < DB; ++db) o[db] = f32x16{};
-        float m = -INFINITY, l = 0.0f;
+        for (int qb = 0; qb < QB; ++qb) {
+            m[qb] = -INFINITY;
+            l[qb] = base[qb] = 0.0f;
+#pragma unroll
+            for (int db = 0; db < DB; ++db) o[qb][db] = f32x16{};
+        }
 
-        TileLoad<T, RB, KT, 64 * FWD_WAVES> tk, tv;
-        HeadAddr<RB> ka(lds);
-        RowsAddr<T, RB> va(lds + TILE);
-        if (SPLIT) __syncthreads();  // the last tile's readers are done before it is written again
-        if (keys > 0) {
-            tk.load(kp, A.k.row, (int)(keys < KT ? keys : KT), A.dim);
-            tv.load(vp, A.v.row, (int)(keys < KT ? keys : KT), A.dim);
-            tk.store(lds);
-            tv.store(lds + TILE);
+        // scores of the keys in ring place `at`
+        auto scores = [&](f32x16(&t)[QB], uint32_t at) {
+#pragma unroll
+            for (int qb = 0; qb < QB; ++qb) t[qb] = f32x16{};
+#pragma unroll
+            for (int j = 0; j < NJ; ++j) {
+                const Raw16 k = lds_read16(ka.at[j] + at);
+#pragma unroll
+                for (int qb = 0; qb < QB; ++qb) t[qb] = mma_pieces<T>(k, q[qb][j], t[qb]);
+            }
+        };
+        // after a step's products: what the next scores (of step u) need before they become weights
+        auto settle = [&](f32x16(&t)[QB], int u) {
+            if (keys - u * 32 < 32) {
+#pragma unroll
+                for (int qb = 0; qb < QB; ++qb)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        if (8 * (i / 4) + 4 * half + i % 4 >= keys - u * 32) t[qb][i] = -INFINITY;
+            }
+            float top[QB];
+            bool moved = false, big = false;
+#pragma unroll
+            for (int qb = 0; qb < QB; ++qb) {
+                top[qb] = t[qb][0];
+#pragma unroll
+                for (int i = 1; i < 16; ++i) top[qb] = fmaxf(top[qb], t[qb][i]);
+                top[qb] = fmaxf(top[qb], other_half(top[qb]));
+                moved |= (top[qb] - m[qb]) * c > SLACK;
+            }
+            if (__ballot(moved)) {
+#pragma unroll
+                for (int qb = 0; qb < QB; ++qb) {
+                    const float next = fmaxf(m[qb], top[qb]), f = rescale(m[qb], next, c);
+                    m[qb] = next;
+                    l[qb] *= f;
+                    base[qb] = next == -INFINITY ? 0.0f : next * c;  // no finite score yet: weights are exp(-inf)
+#pragma unroll
+                    for (int db = 0; db < DB; ++db) o[qb][db] *= f;
+                }
+            }
+#pragma unroll
+            for (int qb = 0; qb < QB; ++qb) big |= huge(m[qb], c);
+            if (__ballot(big)) {  // scores replaced by exponents over c, so that the step below still holds
+#pragma unroll
+                for (int qb = 0; qb < QB; ++qb) {
+                    const bool mine = huge(m[qb], c);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) t[qb][i] = mine ? t[qb][i] - m[qb] : t[qb][i];
+                    base[qb] = mine ? 0.0f : base[qb];
+                }
+            }
+        };
+        auto weights = [&](f32x16(&t)[QB], RowsOperand<T>(&p)[QB]) {
+#pragma unroll
+            for (int qb = 0; qb < QB; ++qb) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    t[qb][i] = __builtin_amdgcn_exp2f(fmaf(t[qb][i], c, -base[qb]));
+                    l[qb] += t[qb][i];
+                }
+                p[qb].set(t[qb]);
+            }
+        };
+        // step u from scores t, leaving the next step's in n; kat, vat: the tiles' places past ka and va
+        auto step = [&](f32x16(&t)[QB], f32x16(&n)[QB], int u, uint32_t kat, uint32_t vat) {
+            copy(u);
+            RowsOperand<T> p[QB];
+            scores(n, kat);
+            weights(t, p);
+            mma_rows<RB>(va, vat, p, o);
+            settle(n, u + 1);
+            wait_copies_and_barrier<2 * PER>();
+        };
+
+        if (steps) {
+            wait_copies_and_barrier<3 * PER>();
+            scores(s[0], 0);
+            settle(s[0], 0);
+            wait_copies_and_barrier<2 * PER>();
+            int u = 0;
+            for (; u + 2 < steps; u += 2) {  // ring places u mod 4 = 0 or 2: the addresses move to the other half
+                const uint32_t other = u & 2 ? -2 * TILE : 2 * TILE;
+                step(s[0], s[1], u, TILE, 0);
+                ka.move(other);
+                step(s[1], s[0], u + 1, 0, TILE);
+                va.move(other);
+            }
+            RowsOperand<T> p[QB];
+            if (u + 1 < steps) {
+                step(s[0], s[1], u, TILE, 0);
+                weights(s[1], p);
+                mma_rows<RB>(va, TILE, p, o);
+            } else {
+                weights(s[0], p);
+                mma_rows<RB>(va, 0, p, o);
+            }
+            if (u & 2) {
+                ka.move(-2 * TILE);
+                va.move(-2 * TILE);
+            }
+            wait_copies_and_barrier<0>();  // nothing may still arrive when the next tile's copies start, or the block ends
         }
-        __syncthreads();
-        uint32_t buf = 0;
-        for (int64_t k0 = 0; k0 < keys; k0 += KT, buf ^= BUF) {
-            const int64_t left = keys - k0;
-            if (left > KT) {
-                const int n = (int)(left - KT < KT ? left - KT : KT);
-                tk.load(kp + (k0 + KT) * A.k.row, A.k.row, n, A.dim);
-                tv.load(vp + (k0 + KT) * A.v.row, A.v.row, n, A.dim);
+#pragma unroll
+        for (int qb = 0; qb < QB; ++qb) {
+            const uint32_t row = (uint32_t)(wave_row + 32 * qb + (lane & 31)), token = A.group == 1 ? row : row / A.group;
+            const int head = hk * A.group + (int)(row - token * A.group);
+            const bool valid = row < rows;
+            const float sum = l[qb] + other_half(l[qb]);
+            if constexpr (SPLIT) {
+                const int64_t at = split * A.nq * A.heads + (q_beg + token) * A.heads + head;
+                store_rows<float>(o[qb], 1.0f, A.part + at * A.dim, A.dim, valid);
+                if (valid && half == 0) *(float2 *)(A.part2 + 2 * at) = make_float2(m[qb], sum);
+            } else {
+                T *op = (T *)A.out.p + (q_beg + token) * A.out.row + head * A.out.head;
+                store_rows<T>(o[qb], sum > 0.0f ? 1.0f / sum : (sum == 0.0f ? 0.0f : sum), op, A.dim, valid);
+                if (A.lse && valid && half == 0) A.lse[(q_beg + token) * A.heads + head] = log_sum(m[qb], sum, A.scale);
             }
-            if (busy) {
-                f32x16 s[KB];
-#pragma unroll
-                for (int kb = 0; kb < KB; ++kb) {
-                    s[kb] = f32x16{};
-#pragma unroll
-                    for (int j = 0; j < NJ; ++j) s[kb] = mma_pieces<T>(lds_read16(ka.at[j] + buf + kb * 32 * RB), q[j], s[kb]);
-                }
-                if (left < KT) {
-#pragma unroll
-                    for (int kb = 0; kb < KB; ++kb)
-#pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            if (kb * 32 + 8 * (i / 4) + 4 * half + i % 4 >= left) s[kb][i] = -INFINITY;
-                }
-                float top = s[0][0];
-#pragma unroll
-                for (int kb = 0; kb < KB; ++kb)
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) top = fmaxf(top, s[kb][i]);
-                top = fmaxf(top, other_half(top));
-                if (__ballot((top - m) * c > SLACK)) {
-                    const float next = fmaxf(m, top), f = rescale(m, next, c);
-                    m = next;
-                    l *= f;
-#pragma unroll
-                    for (int db = 0; db < DB; ++db) o[db] *= f;
-                }
-                float base = m == -INFINITY ? 0.0f : m * c, cs = c;  // no finite score yet: weights are exp(-inf)
-                if (__ballot(huge(m, c))) {
-                    const bool mine = huge(m, c);
-                    cs = 1.0f;
-#pragma unroll
-                    for (int kb = 0; kb < KB; ++kb)
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) s[kb][i] = mine ? (s[kb][i] - m) * c : fmaf(s[kb][i], c, -base);
-                    base = 0.0f;
-                }
-#pragma unroll
-                for (int kb = 0; kb < KB; ++kb) {
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        s[kb][i] = __builtin_amdgcn_exp2f(fmaf(s[kb][i], cs, -base));
-                        l += s[kb][i];
-                    }
-                    RowsOperand<T> p;
-                    p.set(s[kb]);
-                    mma_rows<RB>(va, buf + kb * 32 * RB, p, o);
-                }
-            }
-            if (left > KT) {
-                tk.store(lds + (buf ^ BUF));
-                tv.store(lds + (buf ^ BUF) + TILE);
-            }
-            __syncthreads();
-        }
-        if (!busy) continue;
-        l += other_half(l);
-        if constexpr (SPLIT) {
-            const int64_t at = split * A.nq * A.heads + (q_beg + token) * A.heads + head;
-            store_rows<float>(o, 1.0f, A.part + at * A.dim, A.dim, valid);
-            if (valid && half == 0) *(float2 *)(A.part2 + 2 * at) = make_float2(m, l);
-        } else {
-            T *op = (T *)A.out.p + (q_beg + token) * A.out.row + head * A.out.head;
-            store_rows<T>(o, l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l), op, A.dim, valid);
-            if (A.lse && valid && half == 0)
-                A.lse[(q_beg + token) * A.heads + head] = log_sum(m, l, A.scale);
         }
     }
 }
@@ -279,21 +346,36 @@ SplitPlan split_plan(int64_t own_rows, int own_tile, int64_t other_rows, int oth
     return p;
 }
 
-static SplitPlan fwd_plan(const AttnArgs &A, int dtype)
+// Query rows a block takes without a split: 64 a wave where that still gives every
+// compute unit a block.
+static int fwd_blocks_of_rows(const AttnArgs &A, int dtype)
 {
-    return split_plan(A.nq * A.group, FWD_ROWS, A.nk, dtype == SUBMCONV_F32 ? FWD_KEYS<float> : FWD_KEYS<uint16_t>,
-                      A.entries, A.kv_heads);
+    if (dtype == SUBMCONV_F32) return 1;
+    const int64_t rows = A.nq * A.group;
+    return 1;
 }
 
-size_t attention_workspace(const AttnArgs &A, int dtype)
+static SplitPlan fwd_plan(const AttnArgs &A)
 {
-    const SplitPlan p = fwd_plan(A, dtype);
+    return split_plan(A.nq * A.group, 32 * FWD_WAVES, A.nk, 32, A.entries, A.kv_heads);
+}
+
+size_t attention_workspace(const AttnArgs &A)
+{
+    const SplitPlan p = fwd_plan(A);
     return p.chunk ? (size_t)p.splits * A.nq * A.heads * (A.dim + 2) * sizeof(float) : 0;
 }
 
-template <typename T, int DP>
-static int run_fwd(AttnArgs A, const SplitPlan &p, void *workspace, hipStream_t st)
+// Whether keys and values can be copied straight into LDS.
+static bool direct(const AttnArgs &A, int es)
 {
+    return !(((uintptr_t)A.k.p | (uintptr_t)A.v.p | (uintptr_t)((A.k.row | A.v.row | A.k.head | A.v.head) * es)) & 15);
+}
+
+template <typename T, int DP, bool DIRECT>
+static int run_fwd(AttnArgs A, const SplitPlan &p, int qb, void *workspace, hipStream_t st)
+{
+    const dim3 block(64 * FWD_WAVES);
     if (p.chunk) {
         A.chunk = p.chunk;
         A.splits = p.splits;
@@ -301,28 +383,37 @@ static int run_fwd(AttnArgs A, const SplitPlan &p, void *workspace, hipStream_t 
         A.part = (float *)workspace;
         A.part2 = A.part + p.splits * A.nq * A.heads * A.dim;
         const int64_t work = ragged_tiles(A.nk, A.entries, 1, p.chunk) * A.kv_heads * p.tiles;
-        hipLaunchKernelGGL((k_attn<T, DP, true>), dim3(xcd_grid(work)), dim3(64 * FWD_WAVES), 0, st, A);
+        hipLaunchKernelGGL((k_attn<T, DP, 1, true, DIRECT>), dim3(xcd_grid(work)), block, 0, st, A);
         SC_LAUNCHED("attention (split)");
         hipLaunchKernelGGL((k_attn_join<T>), dim3((unsigned)(A.nq * A.heads)), dim3(256), 0, st, A);
         SC_LAUNCHED("attention join");
         return SUBMCONV_OK;
     }
-    const int64_t work = ragged_tiles(A.nq, A.entries, A.group, FWD_ROWS) * A.kv_heads;
-    hipLaunchKernelGGL((k_attn<T, DP, false>), dim3(xcd_grid(work)), dim3(64 * FWD_WAVES), 0, st, A);
+    const dim3 grid(xcd_grid(ragged_tiles(A.nq, A.entries, A.group, 32 * FWD_WAVES * qb) * A.kv_heads));
+    if constexpr (sizeof(T) == 2 && DIRECT) {
+        if (qb == 2) {
+            hipLaunchKernelGGL((k_attn<T, DP, 2, false, true>), grid, block, 0, st, A);
+            SC_LAUNCHED("attention");
+            return SUBMCONV_OK;
+        }
+    }
+    hipLaunchKernelGGL((k_attn<T, DP, 1, false, DIRECT>), grid, block, 0, st, A);
     SC_LAUNCHED("attention");
     return SUBMCONV_OK;
 }
 
 int attention(const AttnArgs &A, int dtype, void *workspace, hipStream_t st)
 {
-    const SplitPlan p = fwd_plan(A, dtype);
+    const SplitPlan p = fwd_plan(A);
     const int dp = (A.dim + 31) / 32;
-#define GO(T)                                                \
-    switch (dp) {                                            \
-    case 1: return run_fwd<T, 32>(A, p, workspace, st);      \
-    case 2: return run_fwd<T, 64>(A, p, workspace, st);      \
-    case 3: return run_fwd<T, 96>(A, p, workspace, st);      \
-    default: return run_fwd<T, 128>(A, p, workspace, st);    \
+#define GO(T)                                                                                       \
+    if (!direct(A, sizeof(T))) return run_fwd<T, 128, false>(A, p, 1, workspace, st);               \
+    const int qb = fwd_blocks_of_rows(A, dtype);                                                    \
+    switch (dp) {                                                                                   \
+    case 1: return run_fwd<T, 32, true>(A, p, qb, workspace, st);                                   \
+    case 2: return run_fwd<T, 64, true>(A, p, qb, workspace, st);                                   \
+    case 3: return run_fwd<T, 96, true>(A, p, qb, workspace, st);                                   \
+    default: return run_fwd<T, 128, true>(A, p, qb, workspace, st);                                 \
     }
     if (dtype == SUBMCONV_F32) {
         GO(float)

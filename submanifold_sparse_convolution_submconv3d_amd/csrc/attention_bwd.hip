@@ -13,19 +13,22 @@
 
 namespace sc {
 
-constexpr int BWD_WAVES = 4, BWD_ROWS = 32 * BWD_WAVES;
-template <typename T> constexpr int BWD_TILE = sizeof(T) == 2 ? 64 : 32;
+constexpr int BWD_WAVES = 4, BWD_ROWS = 32 * BWD_WAVES, BWD_RING = 4;
 
 // A score's exponent is s c - base; a query whose scores are all -inf has lse = -inf and
 // weights exp(-inf), so its base must be finite.
 __device__ __forceinline__ float lse_base(float lse) { return lse == -INFINITY ? 0.0f : lse * LOG2E; }
 
-template <typename T, int DP, bool SPLIT>
-__global__ __launch_bounds__(64 * BWD_WAVES, DP <= 64 ? 2 : 1) void k_attn_dq(AttnArgs A)
+// A step handles 32 keys: the matrix cores form s^T = k q^T and dp^T = v g^T of the next
+// keys while ds of its own is computed, then add k^T ds.  Keys and values are copied three
+// steps ahead into rings of four tiles in LDS.  Leaves (base, delta) of every query
+// row for k_attn_dkv.
+template <typename T, int DP, bool SPLIT, bool DIRECT>
+__global__ __launch_bounds__(64 * BWD_WAVES, DP * sizeof(T) > 256 ? 1 : 2) void k_attn_dq(AttnArgs A)
 {
-    constexpr int RB = DP * (int)sizeof(T), NJ = RB / 32, DB = DP / 32, KT = BWD_TILE<T>, KB = KT / 32;
-    constexpr int TILE = KT * RB, BUF = 2 * TILE;
-    __shared__ __attribute__((aligned(16))) char smem[2 * BUF];
+    constexpr int RB = DP * (int)sizeof(T), NJ = RB / 32, DB = DP / 32, TILE = 32 * RB;
+    constexpr uint32_t V0 = BWD_RING * TILE;
+    __shared__ __attribute__((aligned(1024))) char smem[2 * BWD_RING * TILE];
     const uint32_t lds = (uint32_t)(uintptr_t)(SC_LDS char *)smem;
 
     const Ragged rq = {A.q_off, A.entries, A.nq, A.group}, rk = {A.k_off, A.entries, A.nk, 1};
@@ -47,22 +50,45 @@ __global__ __launch_bounds__(64 * BWD_WAVES, DP <= 64 ? 2 : 1) void k_attn_dq(At
     const int64_t q_beg = rq.bound(part), k_beg = rk.bound(part);
     const bool real = part >= 1 && part <= A.entries;
     const int64_t rows = (rq.bound(part + 1) - q_beg) * A.group;
-    int64_t keys = real ? rk.bound(part + 1) - k_beg - key0 : 0;
-    if (SPLIT && (keys <= 0 || !real)) return;
-    if (SPLIT && keys > A.chunk) keys = A.chunk;
-    if (keys < 0) keys = 0;
+    int64_t keys64 = real ? rk.bound(part + 1) - k_beg - key0 : 0;
+    if (SPLIT && (keys64 <= 0 || !real)) return;
+    if (SPLIT && keys64 > A.chunk) keys64 = A.chunk;
+    const int keys = keys64 < 0 ? 0 : (int)keys64, steps = (keys + 31) / 32;
 
     const int lane = lane_id(), half = lane >> 5;
     const float c = A.scale * LOG2E;
     const T *kp = (const T *)A.k.p + (k_beg + key0) * A.k.row + hk * A.k.head;
     const T *vp = (const T *)A.v.p + (k_beg + key0) * A.v.row + hk * A.v.head;
+    Fill<T, RB, BWD_WAVES, DIRECT> fill;
+    constexpr int PER = Fill<T, RB, BWD_WAVES, DIRECT>::PER;
+    fill.init(A.k.row, A.v.row, A.dim);
+    HeadAddr<RB> ka(lds);
+    RowsAddr<T, RB> kt(lds);
+    // keys and values of step u + 3: their places were last read in step u - 1
+    auto copy = [&](int u) {
+        const int a = u + BWD_RING - 1, at = (a & (BWD_RING - 1)) * TILE, left = rows_left((int64_t)keys - a * 32ll);
+        fill.copy(kp + a * 32 * A.k.row, left, lds + at, vp + a * 32 * A.v.row, left, lds + V0 + at);
+    };
 
     for (; qtile * BWD_ROWS < rows; qtile += SPLIT ? A.tiles : rows) {
-        const int64_t wave_row = qtile * BWD_ROWS + (threadIdx.x >> 6) * 32;
-        const bool busy = wave_row < rows;
-        const uint32_t row = (uint32_t)(wave_row + (lane & 31));
+        const int64_t wave_row = qtile * BWD_ROWS + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) * 32;
+        if (SPLIT) __syncthreads();
+        if (steps)
+            for (int u = 1 - BWD_RING; u < 0; ++u) copy(u);
+        if (wave_row >= rows) {  // a wave past the entry's rows only helps with the copies
+            if (steps) {
+                wait_copies_and_barrier<2 * PER>();
+                for (int u = -1; u < steps - 1; ++u) {
+                    if (u >= 0) copy(u);
+                    wait_copies_and_barrier<PER>();
+                }
+                wait_copies_and_barrier<0>();
+            }
+            continue;
+        }
+        const uint32_t row = (uint32_t)(wave_row + (lane & 31)), token = A.group == 1 ? row : row / A.group;
+        const int head = hk * A.group + (int)(row - token * A.group);
         const bool valid = row < rows;
-        const uint32_t token = A.group == 1 ? row : row / A.group, head = hk * A.group + (row - token * A.group);
         const int64_t at = (q_beg + token) * A.heads + head;
         Raw16 q[NJ], g[NJ];
         float base = 0.0f, delta = 0.0f;
@@ -87,70 +113,81 @@ __global__ __launch_bounds__(64 * BWD_WAVES, DP <= 64 ? 2 : 1) void k_attn_dq(At
             }
         }
         delta += other_half(delta);
-        if (valid && half == 0 && split == 0) A.delta[at] = delta;
+        if (valid && half == 0 && split == 0) *(float2 *)(A.stat + 2 * at) = make_float2(base, delta);
 
-        f32x16 dq[DB];
+        f32x16 dq[1][DB], s[2], dp[2];
 #pragma unroll
-        for (int db = 0; db < DB; ++db) dq[db] = f32x16{};
-        TileLoad<T, RB, KT, 64 * BWD_WAVES> tk, tv;
-        HeadAddr<RB> ka(lds);
-        RowsAddr<T, RB> kt(lds);
-        if (SPLIT) __syncthreads();
-        if (keys > 0) {
-            tk.load(kp, A.k.row, (int)(keys < KT ? keys : KT), A.dim);
-            tv.load(vp, A.v.row, (int)(keys < KT ? keys : KT), A.dim);
-            tk.store(lds);
-            tv.store(lds + TILE);
+        for (int db = 0; db < DB; ++db) dq[0][db] = f32x16{};
+        auto products = [&](f32x16 &t, f32x16 &e, uint32_t place) {
+            t = e = f32x16{};
+#pragma unroll
+            for (int j = 0; j < NJ; ++j) {
+                t = mma_pieces<T>(lds_read16(ka.at[j] + place), q[j], t);
+                e = mma_pieces<T>(lds_read16(ka.at[j] + place + V0), g[j], e);
+            }
+        };
+        auto mask = [&](f32x16 &t, int u) {
+            if (keys - u * 32 < 32) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    if (8 * (i / 4) + 4 * half + i % 4 >= keys - u * 32) t[i] = -INFINITY;
+            }
+        };
+        auto gradient = [&](f32x16 &t, const f32x16 &e, uint32_t place) {
+            RowsOperand<T> ds[1];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) t[i] = __builtin_amdgcn_exp2f(fmaf(t[i], c, -base)) * (e[i] - delta);
+            ds[0].set(t);
+            mma_rows<RB>(kt, place, ds, dq);
+        };
+        auto step = [&](int from, int to, int u, uint32_t next_at, uint32_t own_at) {
+            copy(u);
+            products(s[to], dp[to], next_at);
+            gradient(s[from], dp[from], own_at);
+            mask(s[to], u + 1);
+            wait_copies_and_barrier<PER>();
+        };
+        if (steps) {
+            wait_copies_and_barrier<2 * PER>();
+            products(s[0], dp[0], 0);
+            mask(s[0], 0);
+            wait_copies_and_barrier<PER>();
+            int u = 0;
+            for (; u + 2 < steps; u += 2) {  // ring places u mod 4 = 0 or 2: the addresses move to the other half
+                const uint32_t other = u & 2 ? -2 * TILE : 2 * TILE;
+                step(0, 1, u, TILE, 0);
+                ka.move(other);
+                step(1, 0, u + 1, 0, TILE);
+                kt.move(other);
+            }
+            if (u + 1 < steps) {
+                step(0, 1, u, TILE, 0);
+                gradient(s[1], dp[1], TILE);
+            } else {
+                gradient(s[0], dp[0], 0);
+            }
+            if (u & 2) {
+                ka.move(-2 * TILE);
+                kt.move(-2 * TILE);
+            }
+            wait_copies_and_barrier<0>();
         }
-        __syncthreads();
-        uint32_t buf = 0;
-        for (int64_t k0 = 0; k0 < keys; k0 += KT, buf ^= BUF) {
-            const int64_t left = keys - k0;
-            if (left > KT) {
-                const int n = (int)(left - KT < KT ? left - KT : KT);
-                tk.load(kp + (k0 + KT) * A.k.row, A.k.row, n, A.dim);
-                tv.load(vp + (k0 + KT) * A.v.row, A.v.row, n, A.dim);
-            }
-            if (busy) {
-#pragma unroll
-                for (int kb = 0; kb < KB; ++kb) {
-                    f32x16 s = {}, dp = {};
-#pragma unroll
-                    for (int j = 0; j < NJ; ++j) {
-                        s = mma_pieces<T>(lds_read16(ka.at[j] + buf + kb * 32 * RB), q[j], s);
-                        dp = mma_pieces<T>(lds_read16(ka.at[j] + buf + TILE + kb * 32 * RB), g[j], dp);
-                    }
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        if (left < KT && kb * 32 + 8 * (i / 4) + 4 * half + i % 4 >= left) s[i] = -INFINITY;
-                        s[i] = __builtin_amdgcn_exp2f(fmaf(s[i], c, -base)) * (dp[i] - delta);
-                    }
-                    RowsOperand<T> ds;
-                    ds.set(s);
-                    mma_rows<RB>(kt, buf + kb * 32 * RB, ds, dq);
-                }
-            }
-            if (left > KT) {
-                tk.store(lds + (buf ^ BUF));
-                tv.store(lds + (buf ^ BUF) + TILE);
-            }
-            __syncthreads();
-        }
-        if (!busy) continue;
         if constexpr (SPLIT)
-            store_rows<float>(dq, 1.0f, A.part + (split * A.nq * A.heads + at) * A.dim, A.dim, valid);
+            store_rows<float>(dq[0], 1.0f, A.part + (split * A.nq * A.heads + at) * A.dim, A.dim, valid);
         else
-            store_rows<T>(dq, A.scale, (T *)A.dq.p + (q_beg + token) * A.dq.row + head * A.dq.head, A.dim, valid);
+            store_rows<T>(dq[0], A.scale, (T *)A.dq.p + (q_beg + token) * A.dq.row + head * A.dq.head, A.dim, valid);
     }
 }
 
-template <typename T, int DP, bool SPLIT>
-__global__ __launch_bounds__(64 * BWD_WAVES, DP <= 64 ? 2 : 1) void k_attn_dkv(AttnArgs A)
+// A step handles 32 query rows of the group: s = q k^T and dp = g v^T of the next rows
+// are formed while p and ds of its own are computed, then dv^T += g^T p and dk^T += q^T ds.
+// Rows past the end are copied as zeros and so add nothing.
+template <typename T, int DP, bool SPLIT, bool DIRECT>
+__global__ __launch_bounds__(64 * BWD_WAVES, DP * sizeof(T) > 128 ? 1 : 2) void k_attn_dkv(AttnArgs A)
 {
-    constexpr int RB = DP * (int)sizeof(T), NJ = RB / 32, DB = DP / 32, QT = BWD_TILE<T>, QB = QT / 32;
-    constexpr int TILE = QT * RB, BUF = 2 * TILE;
-    __shared__ __attribute__((aligned(16))) char smem[2 * BUF];
-    __shared__ __attribute__((aligned(16))) float stat[2][2][QT];  // base and delta of a tile's queries
+    constexpr int RB = DP * (int)sizeof(T), NJ = RB / 32, DB = DP / 32, TILE = 32 * RB;
+    constexpr uint32_t G0 = BWD_RING * TILE, STAT0 = 2 * BWD_RING * TILE;
+    __shared__ __attribute__((aligned(1024))) char smem[2 * BWD_RING * TILE + BWD_RING * BWD_WAVES * 256];
     const uint32_t lds = (uint32_t)(uintptr_t)(SC_LDS char *)smem;
 
     const Ragged rq = {A.q_off, A.entries, A.nq, A.group}, rk = {A.k_off, A.entries, A.nk, 1};
@@ -172,19 +209,57 @@ __global__ __launch_bounds__(64 * BWD_WAVES, DP <= 64 ? 2 : 1) void k_attn_dkv(A
     const int64_t q_beg = rq.bound(part), k_beg = rk.bound(part);
     const bool real = part >= 1 && part <= A.entries;
     const int64_t keys = rk.bound(part + 1) - k_beg;
-    int64_t rows = real ? (rq.bound(part + 1) - q_beg) * A.group - row0 : 0;
-    if (SPLIT && (rows <= 0 || !real)) return;
-    if (SPLIT && rows > A.chunk) rows = A.chunk;
-    if (rows < 0) rows = 0;
+    int64_t rows64 = real ? (rq.bound(part + 1) - q_beg) * A.group - row0 : 0;
+    if (SPLIT && (rows64 <= 0 || !real)) return;
+    if (SPLIT && rows64 > A.chunk) rows64 = A.chunk;
+    const int rows = rows64 < 0 ? 0 : (int)rows64, steps = (rows + 31) / 32;
 
-    const int lane = lane_id(), half = lane >> 5;
+    const int lane = lane_id(), half = lane >> 5, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const float c = A.scale * LOG2E;
-    const T *qp = (const T *)A.q.p + q_beg * A.q.row + (int64_t)hk * A.group * A.q.head;
-    const T *gp = (const T *)A.grad.p + q_beg * A.grad.row + (int64_t)hk * A.group * A.grad.head;
+    const uint32_t group = A.group;
+    Fill<T, RB, BWD_WAVES, DIRECT> fill;
+    constexpr int PER = Fill<T, RB, BWD_WAVES, DIRECT>::PER + 1;  // and the rows' statistics
+    fill.init(group == 1 ? A.q.row : 0, group == 1 ? A.grad.row : 0, A.dim);
+    HeadAddr<RB> qa(lds);
+    RowsAddr<T, RB> qt(lds);
+    const uint32_t my_stat = lds + STAT0 + wave * 256;  // each wave keeps its own copy
+    auto copy = [&](int u) {
+        const int a = u + BWD_RING - 1, place = a & (BWD_RING - 1), left = rows_left((int64_t)rows - a * 32ll);
+        const uint32_t first = (uint32_t)row0 + a * 32;
+        if (group == 1)
+            fill.copy((const T *)A.q.p + (q_beg + first) * A.q.row + hk * A.q.head, left, lds + place * TILE,
+                      (const T *)A.grad.p + (q_beg + first) * A.grad.row + hk * A.grad.head, left, lds + G0 + place * TILE);
+        else
+            fill.copy_grouped(A.q, A.grad, q_beg, hk * group, first, group, left, lds + place * TILE, lds + G0 + place * TILE);
+        // (base, delta) of 32 rows: one word a lane
+        const uint32_t t0 = group == 1 ? first : first / group, r = first + lane / 2, t = group == 1 ? r : r / group;
+        const float *sp = A.stat + ((q_beg + t0) * A.heads + hk * group) * 2;
+        const uint32_t o = lane / 2 < left ? ((t - t0) * A.heads + (r - t * group)) * 8 + (lane & 1) * 4 : OUT_OF_RANGE;
+        const uint32_t to = my_stat + place * (BWD_WAVES * 256);
+        if constexpr (DIRECT) {
+            const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc((void *)sp, (short)0, 0x7fffffff, 0x00020000);
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (SC_LDS void *)(uintptr_t)to, 4, o, 0, 0, 0);
+        } else {
+            *(SC_LDS float *)(uintptr_t)(to + lane * 4) = o != OUT_OF_RANGE ? *(const float *)((const char *)sp + o) : 0.0f;
+        }
+    };
 
     for (; ktile * BWD_ROWS < keys; ktile += SPLIT ? A.tiles : keys) {
-        const int64_t wave_key = ktile * BWD_ROWS + (threadIdx.x >> 6) * 32;
-        const bool busy = wave_key < keys;
+        const int64_t wave_key = ktile * BWD_ROWS + wave * 32;
+        if (SPLIT) __syncthreads();
+        if (steps)
+            for (int u = 1 - BWD_RING; u < 0; ++u) copy(u);
+        if (wave_key >= keys) {
+            if (steps) {
+                wait_copies_and_barrier<2 * PER>();
+                for (int u = -1; u < steps - 1; ++u) {
+                    if (u >= 0) copy(u);
+                    wait_copies_and_barrier<PER>();
+                }
+                wait_copies_and_barrier<0>();
+            }
+            continue;
+        }
         const int64_t key = wave_key + (lane & 31);
         const bool valid = key < keys;
         Raw16 k[NJ], v[NJ];
@@ -197,84 +272,71 @@ __global__ __launch_bounds__(64 * BWD_WAVES, DP <= 64 ? 2 : 1) void k_attn_dkv(A
                 v[j] = *(const Raw16Any *)((const T *)A.v.p + (k_beg + key) * A.v.row + hk * A.v.head + e);
             }
         }
-        f32x16 dk[DB], dv[DB];
+        f32x16 dk[1][DB], dv[1][DB], s[2], dp[2];
 #pragma unroll
-        for (int db = 0; db < DB; ++db) dk[db] = dv[db] = f32x16{};
-        TileLoad<T, RB, QT, 64 * BWD_WAVES> tq, tg;
-        HeadAddr<RB> qa(lds);
-        RowsAddr<T, RB> qt(lds);
-        float nb = 0.0f, nd = 0.0f;
-        auto fetch = [&](int64_t r0) {  // rows past the run weigh exp(-inf)
-            const int n = (int)(rows - r0 < QT ? rows - r0 : QT);
-            tq.load_grouped(qp, A.q.row, A.q.head, (uint32_t)(row0 + r0), A.group, n, A.dim);
-            tg.load_grouped(gp, A.grad.row, A.grad.head, (uint32_t)(row0 + r0), A.group, n, A.dim);
-            if (threadIdx.x < QT) {
-                nb = INFINITY;
-                nd = 0.0f;
-                if ((int)threadIdx.x < n) {
-                    const uint32_t r = (uint32_t)(row0 + r0) + threadIdx.x, token = A.group == 1 ? r : r / A.group;
-                    const int64_t at = (q_beg + token) * A.heads + hk * A.group + (r - token * A.group);
-                    nb = lse_base(A.lse[at]);
-                    nd = A.delta[at];
-                }
+        for (int db = 0; db < DB; ++db) dk[0][db] = dv[0][db] = f32x16{};
+        auto products = [&](f32x16 &t, f32x16 &e, uint32_t place) {
+            t = e = f32x16{};
+#pragma unroll
+            for (int j = 0; j < NJ; ++j) {
+                t = mma_pieces<T>(lds_read16(qa.at[j] + place), k[j], t);
+                e = mma_pieces<T>(lds_read16(qa.at[j] + place + G0), v[j], e);
             }
         };
-        auto put = [&](uint32_t to, int b) {
-            tq.store(lds + to);
-            tg.store(lds + to + TILE);
-            if (threadIdx.x < QT) {
-                stat[b][0][threadIdx.x] = nb;
-                stat[b][1][threadIdx.x] = nd;
-            }
-        };
-        if (SPLIT) __syncthreads();
-        if (rows > 0) {
-            fetch(0);
-            put(0, 0);
-        }
-        __syncthreads();
-        uint32_t buf = 0;
-        for (int64_t r0 = 0; r0 < rows; r0 += QT, buf ^= BUF) {
-            const bool more = rows - r0 > QT;
-            if (more) fetch(r0 + QT);
-            if (busy) {
-                const float *st = &stat[buf ? 1 : 0][0][0];
+        auto gradient = [&](f32x16 &t, f32x16 &e, int u, uint32_t place) {
+            const uint32_t st = my_stat + (u & (BWD_RING - 1)) * (BWD_WAVES * 256) + 32 * half;
+            RowsOperand<T> p[1], ds[1];
 #pragma unroll
-                for (int qb = 0; qb < QB; ++qb) {
-                    f32x16 s = {}, dp = {};
+            for (int i = 0; i < 16; i += 2) {  // rows 8 (i / 4) + 4 half + i % 4: two (base, delta) pairs
+                const f32x4 bd = __builtin_bit_cast(f32x4, lds_read16(st + 64 * (i / 4) + 8 * (i % 4)));
 #pragma unroll
-                    for (int j = 0; j < NJ; ++j) {
-                        s = mma_pieces<T>(lds_read16(qa.at[j] + buf + qb * 32 * RB), k[j], s);
-                        dp = mma_pieces<T>(lds_read16(qa.at[j] + buf + TILE + qb * 32 * RB), v[j], dp);
-                    }
-#pragma unroll
-                    for (int i = 0; i < 16; i += 4) {
-                        const f32x4 b = *(const f32x4 *)(st + qb * 32 + 2 * i + 4 * half);
-                        const f32x4 d = *(const f32x4 *)(st + QT + qb * 32 + 2 * i + 4 * half);
-#pragma unroll
-                        for (int x = 0; x < 4; ++x) {
-                            s[i + x] = __builtin_amdgcn_exp2f(fmaf(s[i + x], c, -b[x]));
-                            dp[i + x] = s[i + x] * (dp[i + x] - d[x]);
-                        }
-                    }
-                    RowsOperand<T> p, ds;
-                    p.set(s);
-                    mma_rows<RB>(qt, buf + TILE + qb * 32 * RB, p, dv);
-                    ds.set(dp);
-                    mma_rows<RB>(qt, buf + qb * 32 * RB, ds, dk);
+                for (int x = 0; x < 2; ++x) {
+                    t[i + x] = __builtin_amdgcn_exp2f(fmaf(t[i + x], c, -bd[2 * x]));
+                    e[i + x] = t[i + x] * (e[i + x] - bd[2 * x + 1]);
                 }
             }
-            if (more) put(buf ^ BUF, buf ? 0 : 1);
-            __syncthreads();
+            p[0].set(t);
+            mma_rows<RB>(qt, place + G0, p, dv);
+            ds[0].set(e);
+            mma_rows<RB>(qt, place, ds, dk);
+        };
+        auto step = [&](int from, int to, int u, uint32_t next_at, uint32_t own_at) {
+            copy(u);
+            products(s[to], dp[to], next_at);
+            gradient(s[from], dp[from], u, own_at);
+            wait_copies_and_barrier<PER>();
+        };
+        if (steps) {
+            wait_copies_and_barrier<2 * PER>();
+            products(s[0], dp[0], 0);
+            wait_copies_and_barrier<PER>();
+            int u = 0;
+            for (; u + 2 < steps; u += 2) {
+                const uint32_t other = u & 2 ? -2 * TILE : 2 * TILE;
+                step(0, 1, u, TILE, 0);
+                qa.move(other);
+                step(1, 0, u + 1, 0, TILE);
+                qt.move(other);
+            }
+            if (u + 1 < steps) {
+                step(0, 1, u, TILE, 0);
+                gradient(s[1], dp[1], u + 1, TILE);
+            } else {
+                gradient(s[0], dp[0], u, 0);
+            }
+            if (u & 2) {
+                qa.move(-2 * TILE);
+                qt.move(-2 * TILE);
+            }
+            wait_copies_and_barrier<0>();
         }
-        if (!busy) continue;
         if constexpr (SPLIT) {
             const int64_t at = ((split * A.nk + k_beg + key) * A.kv_heads + hk) * A.dim;
-            store_rows<float>(dk, 1.0f, A.part + at, A.dim, valid);
-            store_rows<float>(dv, 1.0f, A.part2 + at, A.dim, valid);
+            store_rows<float>(dk[0], 1.0f, A.part + at, A.dim, valid);
+            store_rows<float>(dv[0], 1.0f, A.part2 + at, A.dim, valid);
         } else {
-            store_rows<T>(dk, A.scale, (T *)A.dk.p + (k_beg + key) * A.dk.row + hk * A.dk.head, A.dim, valid);
-            store_rows<T>(dv, 1.0f, (T *)A.dv.p + (k_beg + key) * A.dv.row + hk * A.dv.head, A.dim, valid);
+            store_rows<T>(dk[0], A.scale, (T *)A.dk.p + (k_beg + key) * A.dk.row + hk * A.dk.head, A.dim, valid);
+            store_rows<T>(dv[0], 1.0f, (T *)A.dv.p + (k_beg + key) * A.dv.row + hk * A.dv.head, A.dim, valid);
         }
     }
 }
@@ -315,26 +377,25 @@ __global__ __launch_bounds__(256) void k_attn_sum(Ragged own, Ragged other, int 
 
 struct BwdPlan {
     SplitPlan q, k;
-    size_t delta, part;  // bytes of the workspace's two areas
+    size_t stat, part;  // bytes of the workspace's two areas
 };
 
-static BwdPlan bwd_plan(const AttnArgs &A, int dtype)
+static BwdPlan bwd_plan(const AttnArgs &A)
 {
-    const int tile = dtype == SUBMCONV_F32 ? BWD_TILE<float> : BWD_TILE<uint16_t>;
     BwdPlan p;
-    p.q = split_plan(A.nq * A.group, BWD_ROWS, A.nk, tile, A.entries, A.kv_heads);
-    p.k = split_plan(A.nk, BWD_ROWS, A.nq * A.group, tile, A.entries, A.kv_heads);
-    p.delta = ((size_t)A.nq * A.heads * sizeof(float) + 15) / 16 * 16;
+    p.q = split_plan(A.nq * A.group, BWD_ROWS, A.nk, 32, A.entries, A.kv_heads);
+    p.k = split_plan(A.nk, BWD_ROWS, A.nq * A.group, 32, A.entries, A.kv_heads);
+    p.stat = ((size_t)A.nq * A.heads * 2 * sizeof(float) + 15) / 16 * 16;
     const size_t a = p.q.chunk ? (size_t)p.q.splits * A.nq * A.heads * A.dim * sizeof(float) : 0;
     const size_t b = p.k.chunk ? (size_t)p.k.splits * A.nk * A.kv_heads * A.dim * 2 * sizeof(float) : 0;
     p.part = a > b ? a : b;  // the two passes use it one after the other
     return p;
 }
 
-size_t attention_backward_workspace(const AttnArgs &A, int dtype)
+size_t attention_backward_workspace(const AttnArgs &A)
 {
-    const BwdPlan p = bwd_plan(A, dtype);
-    return p.delta + p.part;
+    const BwdPlan p = bwd_plan(A);
+    return p.stat + p.part;
 }
 
 static void set_split(AttnArgs &A, const SplitPlan &p)
@@ -344,7 +405,7 @@ static void set_split(AttnArgs &A, const SplitPlan &p)
     A.tiles = p.tiles;
 }
 
-template <typename T, int DP>
+template <typename T, int DP, bool DIRECT>
 static int run_bwd(AttnArgs A, const BwdPlan &p, hipStream_t st)
 {
     const dim3 block(64 * BWD_WAVES);
@@ -353,13 +414,13 @@ static int run_bwd(AttnArgs A, const BwdPlan &p, hipStream_t st)
         if (p.q.chunk) {
             set_split(A, p.q);
             const int64_t work = ragged_tiles(A.nk, A.entries, 1, A.chunk) * A.kv_heads * A.tiles;
-            hipLaunchKernelGGL((k_attn_dq<T, DP, true>), dim3(xcd_grid(work)), block, 0, st, A);
+            hipLaunchKernelGGL((k_attn_dq<T, DP, true, DIRECT>), dim3(xcd_grid(work)), block, 0, st, A);
             SC_LAUNCHED("attention_backward queries (split)");
             hipLaunchKernelGGL(k_attn_sum<T>, dim3((unsigned)(A.nq * A.heads)), dim3(256), 0, st, rq, rk, A.heads, A.dim,
                                A.chunk, A.part, A.scale, A.dq);
         } else {
             const int64_t work = ragged_tiles(A.nq, A.entries, A.group, BWD_ROWS) * A.kv_heads;
-            hipLaunchKernelGGL((k_attn_dq<T, DP, false>), dim3(xcd_grid(work)), block, 0, st, A);
+            hipLaunchKernelGGL((k_attn_dq<T, DP, false, DIRECT>), dim3(xcd_grid(work)), block, 0, st, A);
         }
         SC_LAUNCHED("attention_backward queries");
     }
@@ -368,7 +429,7 @@ static int run_bwd(AttnArgs A, const BwdPlan &p, hipStream_t st)
             set_split(A, p.k);
             A.part2 = A.part + p.k.splits * A.nk * A.kv_heads * A.dim;
             const int64_t work = ragged_tiles(A.nq, A.entries, A.group, A.chunk) * A.kv_heads * A.tiles;
-            hipLaunchKernelGGL((k_attn_dkv<T, DP, true>), dim3(xcd_grid(work)), block, 0, st, A);
+            hipLaunchKernelGGL((k_attn_dkv<T, DP, true, DIRECT>), dim3(xcd_grid(work)), block, 0, st, A);
             SC_LAUNCHED("attention_backward keys (split)");
             const Ragged rows = {A.q_off, A.entries, A.nq, A.group};
             const dim3 grid((unsigned)(A.nk * A.kv_heads));
@@ -378,25 +439,35 @@ static int run_bwd(AttnArgs A, const BwdPlan &p, hipStream_t st)
                                1.0f, A.dv);
         } else {
             const int64_t work = ragged_tiles(A.nk, A.entries, 1, BWD_ROWS) * A.kv_heads;
-            hipLaunchKernelGGL((k_attn_dkv<T, DP, false>), dim3(xcd_grid(work)), block, 0, st, A);
+            hipLaunchKernelGGL((k_attn_dkv<T, DP, false, DIRECT>), dim3(xcd_grid(work)), block, 0, st, A);
         }
         SC_LAUNCHED("attention_backward keys");
     }
     return SUBMCONV_OK;
 }
 
+// Whether all tiles can be copied straight into LDS (see Fill).
+static bool direct(const AttnArgs &A, int es)
+{
+    uintptr_t bits = 0;
+    for (const Heads *h : {&A.q, &A.k, &A.v, &A.grad}) bits |= (uintptr_t)h->p | (uintptr_t)(h->row * es) | (uintptr_t)(h->head * es);
+    const int64_t far = (A.q.head > A.grad.head ? A.q.head : A.grad.head) * A.group * es;  // heads of a group
+    return !(bits & 15) && (A.group == 1 || far < int64_t(1) << 30);
+}
+
 int attention_backward(AttnArgs A, int dtype, void *workspace, hipStream_t st)
 {
-    const BwdPlan p = bwd_plan(A, dtype);
-    A.delta = (float *)workspace;
-    A.part = (float *)((char *)workspace + p.delta);
+    const BwdPlan p = bwd_plan(A);
+    A.stat = (float *)workspace;
+    A.part = (float *)((char *)workspace + p.stat);
     const int dp = (A.dim + 31) / 32;
-#define GO(T)                                   \
-    switch (dp) {                               \
-    case 1: return run_bwd<T, 32>(A, p, st);    \
-    case 2: return run_bwd<T, 64>(A, p, st);    \
-    case 3: return run_bwd<T, 96>(A, p, st);    \
-    default: return run_bwd<T, 128>(A, p, st);  \
+#define GO(T)                                                                  \
+    if (!direct(A, sizeof(T))) return run_bwd<T, 128, false>(A, p, st);        \
+    switch (dp) {                                                              \
+    case 1: return run_bwd<T, 32, true>(A, p, st);                             \
+    case 2: return run_bwd<T, 64, true>(A, p, st);                             \
+    case 3: return run_bwd<T, 96, true>(A, p, st);                             \
+    default: return run_bwd<T, 128, true>(A, p, st);                           \
     }
     if (dtype == SUBMCONV_F32) {
         GO(float)
