@@ -308,18 +308,23 @@ __device__ __forceinline__ u32x2 lds_read_tr(uint32_t at)
     return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((SC_LDS s16x4 *)(uintptr_t)at));
 }
 
+// Result registers 8h .. 8h + 7, rounded to bf16 (nearest even): the operand over 16 rows.
+__device__ __forceinline__ Raw16 pack8(const f32x16 &s, int h)
+{
+    return Raw16{pack_bf16(s[8 * h], s[8 * h + 1]), pack_bf16(s[8 * h + 2], s[8 * h + 3]),
+                 pack_bf16(s[8 * h + 4], s[8 * h + 5]), pack_bf16(s[8 * h + 6], s[8 * h + 7])};
+}
+
 // The result registers of a block of 32 rows as an operand over those rows.
 template <typename T>
 struct RowsOperand;
 template <>
 struct RowsOperand<uint16_t> {
-    Raw16 v[2];  // rows 0..15, 16..31, each rounded to bf16 (nearest even)
+    Raw16 v[2];
     __device__ __forceinline__ void set(const f32x16 &s)
     {
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) v[h][i] = pack_bf16(s[8 * h + 2 * i], s[8 * h + 2 * i + 1]);
+        v[0] = pack8(s, 0);
+        v[1] = pack8(s, 1);
     }
 };
 template <>
@@ -327,6 +332,15 @@ struct RowsOperand<float> {
     f32x16 v;
     __device__ __forceinline__ void set(const f32x16 &s) { v = s; }
 };
+
+// The transposed operand of rows 16 (x / DB) .. + 15 and elements 32 (x % DB) .. + 31.
+template <int RB>
+__device__ __forceinline__ Raw16 rows_piece(const RowsAddr<uint16_t, RB> &ad, uint32_t at, int x)
+{
+    const int h = x / (RB / 64), db = x % (RB / 64);
+    const u32x2 lo = lds_read_tr(ad.at[0][db] + at + 16 * h * RB), hi = lds_read_tr(ad.at[1][db] + at + 16 * h * RB);
+    return Raw16{lo[0], lo[1], hi[0], hi[1]};
+}
 
 // acc[x][db] += transpose(32 tile rows) p[x], for every 32 elements db of the head; `at` is
 // added to the addresses.
@@ -338,10 +352,9 @@ __device__ __forceinline__ void mma_rows(const RowsAddr<uint16_t, RB> &ad, uint3
     for (int h = 0; h < 2; ++h)
 #pragma unroll
         for (int db = 0; db < RB / 64; ++db) {
-            const u32x2 lo = lds_read_tr(ad.at[0][db] + at + 16 * h * RB), hi = lds_read_tr(ad.at[1][db] + at + 16 * h * RB);
+            const Raw16 v = rows_piece<RB>(ad, at, h * (RB / 64) + db);
 #pragma unroll
-            for (int x = 0; x < N; ++x)
-                acc[x][db] = mma_pieces<uint16_t>(Raw16{lo[0], lo[1], hi[0], hi[1]}, p[x].v[h], acc[x][db]);
+            for (int x = 0; x < N; ++x) acc[x][db] = mma_pieces<uint16_t>(v, p[x].v[h], acc[x][db]);
         }
 }
 template <int RB, int N>

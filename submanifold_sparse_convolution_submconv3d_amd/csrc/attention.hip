@@ -40,6 +40,28 @@ __device__ __forceinline__ float log_sum(float m, float l, float scale)
     return huge(m, c) ? m * scale + e * LN2 : (m * c + e) * LN2;
 }
 
+// acc *= f where `on`, in place.  One straight piece of code for the compiler: a branch
+// around the products makes it keep every accumulator twice and copy them where the
+// branch is not taken, which is nearly always.  The waits cover a matrix product that is
+// still writing acc, and one that reads it next.
+__device__ __forceinline__ void scale_if(f32x16 &acc, float f, uint64_t on)
+{
+    asm volatile("s_cmp_eq_u64 %17, 0\n\t"
+                 "s_cbranch_scc1 .Lkeep%=\n\t"
+                 "s_nop 15\n\ts_nop 15\n\t"
+                 "v_mul_f32 %0, %16, %0\n\tv_mul_f32 %1, %16, %1\n\tv_mul_f32 %2, %16, %2\n\tv_mul_f32 %3, %16, %3\n\t"
+                 "v_mul_f32 %4, %16, %4\n\tv_mul_f32 %5, %16, %5\n\tv_mul_f32 %6, %16, %6\n\tv_mul_f32 %7, %16, %7\n\t"
+                 "v_mul_f32 %8, %16, %8\n\tv_mul_f32 %9, %16, %9\n\tv_mul_f32 %10, %16, %10\n\tv_mul_f32 %11, %16, %11\n\t"
+                 "v_mul_f32 %12, %16, %12\n\tv_mul_f32 %13, %16, %13\n\tv_mul_f32 %14, %16, %14\n\tv_mul_f32 %15, %16, %15\n\t"
+                 "s_nop 7\n"
+                 ".Lkeep%=:"
+                 : "+v"(acc[0]), "+v"(acc[1]), "+v"(acc[2]), "+v"(acc[3]), "+v"(acc[4]), "+v"(acc[5]), "+v"(acc[6]),
+                   "+v"(acc[7]), "+v"(acc[8]), "+v"(acc[9]), "+v"(acc[10]), "+v"(acc[11]), "+v"(acc[12]), "+v"(acc[13]),
+                   "+v"(acc[14]), "+v"(acc[15])
+                 : "v"(f), "s"(on)
+                 : "scc");
+}
+
 constexpr int FWD_WAVES = 4, RING = 4;
 
 // A step handles 32 keys.  Its wave has the scores of its own keys in registers already,
@@ -52,7 +74,7 @@ constexpr int FWD_WAVES = 4, RING = 4;
 // an entry and leaves (sum, m, l) of it in part / part2 for k_attn_join; otherwise a block
 // takes one tile of query rows over all keys.
 template <typename T, int DP, int QB, bool SPLIT, bool DIRECT>
-__global__ __launch_bounds__(64 * FWD_WAVES, DP * sizeof(T) * QB > 256 ? 1 : 2) void k_attn(AttnArgs A)
+__global__ __launch_bounds__(64 * FWD_WAVES, DP * sizeof(T) * QB > 256 ? 1 : DP * sizeof(T) * QB > 128 ? 2 : 3) void k_attn(AttnArgs A)
 {
     constexpr int RB = DP * (int)sizeof(T), NJ = RB / 32, DB = DP / 32, TILE = 32 * RB, ROWS = 32 * QB * FWD_WAVES;
     constexpr uint32_t V0 = RING * TILE;  // the values' ring
@@ -131,6 +153,7 @@ __global__ __launch_bounds__(64 * FWD_WAVES, DP * sizeof(T) * QB > 256 ? 1 : 2) 
         }
         f32x16 o[QB][DB], s[2][QB];
         float m[QB], l[QB], base[QB];
+        uint64_t big = 0;  // some row's maximum is huge
 #pragma unroll
         for (int qb = 0; qb < QB; ++qb) {
             m[qb] = -INFINITY;
@@ -150,74 +173,131 @@ __global__ __launch_bounds__(64 * FWD_WAVES, DP * sizeof(T) * QB > 256 ? 1 : 2) 
                 for (int qb = 0; qb < QB; ++qb) t[qb] = mma_pieces<T>(k, q[qb][j], t[qb]);
             }
         };
-        // after a step's products: what the next scores (of step u) need before they become weights
-        auto settle = [&](f32x16(&t)[QB], int u) {
-            if (keys - u * 32 < 32) {
+        // scores of step u past the last key are none
+        auto mask = [&](f32x16(&t)[QB], int u) {
+            if (__builtin_expect(keys - u * 32 < 32, 0)) {
 #pragma unroll
                 for (int qb = 0; qb < QB; ++qb)
 #pragma unroll
                     for (int i = 0; i < 16; ++i)
                         if (8 * (i / 4) + 4 * half + i % 4 >= keys - u * 32) t[qb][i] = -INFINITY;
             }
-            float top[QB];
-            bool moved = false, big = false;
+        };
+        // with the scores' maximum of this half's keys, everything their weights need
+        auto settle = [&](f32x16(&t)[QB], float(&top)[QB]) {
+            bool moved = false;
+            float f[QB];
 #pragma unroll
             for (int qb = 0; qb < QB; ++qb) {
-                top[qb] = t[qb][0];
-#pragma unroll
-                for (int i = 1; i < 16; ++i) top[qb] = fmaxf(top[qb], t[qb][i]);
                 top[qb] = fmaxf(top[qb], other_half(top[qb]));
                 moved |= (top[qb] - m[qb]) * c > SLACK;
+                f[qb] = 1.0f;
             }
-            if (__ballot(moved)) {
+            const uint64_t any = __ballot(moved);
+            if (__builtin_expect(any != 0, 0)) {
+                bool b = false;
 #pragma unroll
                 for (int qb = 0; qb < QB; ++qb) {
-                    const float next = fmaxf(m[qb], top[qb]), f = rescale(m[qb], next, c);
+                    const float next = fmaxf(m[qb], top[qb]);
+                    f[qb] = rescale(m[qb], next, c);
                     m[qb] = next;
-                    l[qb] *= f;
-                    base[qb] = next == -INFINITY ? 0.0f : next * c;  // no finite score yet: weights are exp(-inf)
-#pragma unroll
-                    for (int db = 0; db < DB; ++db) o[qb][db] *= f;
+                    l[qb] *= f[qb];
+                    base[qb] = next == -INFINITY || huge(next, c) ? 0.0f : next * c;  // -inf: weights are exp(-inf)
+                    b |= huge(next, c);
                 }
+                big = __ballot(b);
             }
 #pragma unroll
-            for (int qb = 0; qb < QB; ++qb) big |= huge(m[qb], c);
-            if (__ballot(big)) {  // scores replaced by exponents over c, so that the step below still holds
+            for (int qb = 0; qb < QB; ++qb)
+#pragma unroll
+                for (int db = 0; db < DB; ++db) scale_if(o[qb][db], f[qb], any);
+            if (__builtin_expect(big != 0, 0)) {  // differences of scores in the scores' place
 #pragma unroll
                 for (int qb = 0; qb < QB; ++qb) {
                     const bool mine = huge(m[qb], c);
 #pragma unroll
                     for (int i = 0; i < 16; ++i) t[qb][i] = mine ? t[qb][i] - m[qb] : t[qb][i];
-                    base[qb] = mine ? 0.0f : base[qb];
                 }
             }
         };
-        auto weights = [&](f32x16(&t)[QB], RowsOperand<T>(&p)[QB]) {
+        auto maximum = [&](const f32x16(&t)[QB], float(&top)[QB], int from, int to) {
 #pragma unroll
-            for (int qb = 0; qb < QB; ++qb) {
+            for (int qb = 0; qb < QB; ++qb)
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
+                for (int i = from; i < to; ++i) top[qb] = i ? fmaxf(top[qb], t[qb][i]) : t[qb][i];
+        };
+        auto weights = [&](f32x16(&t)[QB], int from, int to) {
+#pragma unroll
+            for (int qb = 0; qb < QB; ++qb)
+#pragma unroll
+                for (int i = from; i < to; ++i) {
                     t[qb][i] = __builtin_amdgcn_exp2f(fmaf(t[qb][i], c, -base[qb]));
                     l[qb] += t[qb][i];
                 }
-                p[qb].set(t[qb]);
-            }
+        };
+        auto product = [&](f32x16(&t)[QB], uint32_t vat) {
+            RowsOperand<T> p[QB];
+#pragma unroll
+            for (int qb = 0; qb < QB; ++qb) p[qb].set(t[qb]);
+            mma_rows<RB>(va, vat, p, o);
         };
         // step u from scores t, leaving the next step's in n; kat, vat: the tiles' places past ka and va
         auto step = [&](f32x16(&t)[QB], f32x16(&n)[QB], int u, uint32_t kat, uint32_t vat) {
+            float top[QB];
             copy(u);
-            RowsOperand<T> p[QB];
-            scores(n, kat);
-            weights(t, p);
-            mma_rows<RB>(va, vat, p, o);
-            settle(n, u + 1);
+            if constexpr (sizeof(T) == 2) {
+                // in the order it is to run: LDS reads AHEAD of their use, and between the matrix
+                // products a piece of the arithmetic; first the scores with half the weights, then
+                // their product with the values, with the other half and the maximum
+                constexpr int AHEAD = NJ < 4 ? NJ : 4;
+                Raw16 k[NJ], v[2 * DB], p[QB][2];
+#pragma unroll
+                for (int j = 0; j < AHEAD; ++j) k[j] = lds_read16(ka.at[j] + kat);
+                __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                for (int j = 0; j < NJ; ++j) {
+                    if (j + AHEAD < NJ) k[j + AHEAD] = lds_read16(ka.at[j + AHEAD] + kat);
+                    else if (j + AHEAD - NJ < 2 && j + AHEAD - NJ < 2 * DB) v[j + AHEAD - NJ] = rows_piece<RB>(va, vat, j + AHEAD - NJ);
+#pragma unroll
+                    for (int qb = 0; qb < QB; ++qb) n[qb] = mma_pieces<T>(k[j], q[qb][j], j ? n[qb] : f32x16{});
+                    weights(t, 8 * j / NJ, 8 * (j + 1) / NJ);
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+#pragma unroll
+                for (int qb = 0; qb < QB; ++qb) p[qb][0] = pack8(t[qb], 0);
+                mask(n, u + 1);
+#pragma unroll
+                for (int x = 0; x < 2 * DB; ++x) {
+                    const int h = x / DB, db = x % DB;
+                    if (x + 2 < 2 * DB) v[x + 2] = rows_piece<RB>(va, vat, x + 2);
+#pragma unroll
+                    for (int qb = 0; qb < QB; ++qb) o[qb][db] = mma_pieces<T>(v[x], p[qb][h], o[qb][db]);
+                    if (h == 0) weights(t, 8 + 8 * db / DB, 8 + 8 * (db + 1) / DB);
+                    else maximum(n, top, 16 * db / DB, 16 * (db + 1) / DB);
+                    if (x == DB - 1) {
+#pragma unroll
+                        for (int qb = 0; qb < QB; ++qb) p[qb][1] = pack8(t[qb], 1);
+                    }
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+            } else {
+                scores(n, kat);
+                weights(t, 0, 16);
+                product(t, vat);
+                mask(n, u + 1);
+                maximum(n, top, 0, 16);
+            }
+            settle(n, top);
             wait_copies_and_barrier<2 * PER>();
         };
 
         if (steps) {
             wait_copies_and_barrier<3 * PER>();
+            float top[QB];
             scores(s[0], 0);
-            settle(s[0], 0);
+            mask(s[0], 0);
+            maximum(s[0], top, 0, 16);
+            settle(s[0], top);
             wait_copies_and_barrier<2 * PER>();
             int u = 0;
             for (; u + 2 < steps; u += 2) {  // ring places u mod 4 = 0 or 2: the addresses move to the other half
@@ -227,14 +307,13 @@ __global__ __launch_bounds__(64 * FWD_WAVES, DP * sizeof(T) * QB > 256 ? 1 : 2) 
                 step(s[1], s[0], u + 1, 0, TILE);
                 va.move(other);
             }
-            RowsOperand<T> p[QB];
             if (u + 1 < steps) {
                 step(s[0], s[1], u, TILE, 0);
-                weights(s[1], p);
-                mma_rows<RB>(va, TILE, p, o);
+                weights(s[1], 0, 16);
+                product(s[1], TILE);
             } else {
-                weights(s[0], p);
-                mma_rows<RB>(va, 0, p, o);
+                weights(s[0], 0, 16);
+                product(s[0], 0);
             }
             if (u & 2) {
                 ka.move(-2 * TILE);

@@ -127,7 +127,7 @@ __global__ __launch_bounds__(64 * BWD_WAVES, DP * sizeof(T) > 256 ? 1 : 2) void 
             }
         };
         auto mask = [&](f32x16 &t, int u) {
-            if (keys - u * 32 < 32) {
+            if (__builtin_expect(keys - u * 32 < 32, 0)) {
 #pragma unroll
                 for (int i = 0; i < 16; ++i)
                     if (8 * (i / 4) + 4 * half + i % 4 >= keys - u * 32) t[i] = -INFINITY;
