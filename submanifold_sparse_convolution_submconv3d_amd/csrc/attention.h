@@ -142,80 +142,102 @@ __device__ __forceinline__ void wait_copies_and_barrier()
     asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
 }
 
-// Copies of 32 rows of two tensors (a tile of each, TILE = 32 RB bytes) into LDS, shared
-// evenly by the waves of a block: each copy moves 64 pieces of 16 bytes, and there are
-// RB / 16 in all.  Rows from `left` on and pieces past dim become zeros.
-//   DIRECT: straight into LDS through bounds-checked buffer copies; the data must be 16-byte
-//   aligned and 32 rows apart by less than 2^31 bytes.  The wave's copies stay in flight.
-//   Otherwise: loads and LDS writes, any alignment, done when the function returns (after
-//   a barrier).
+// Tiles of 32 rows of two tensors, copied one after the other into rings of RING places in
+// LDS, 64 pieces of 16 bytes (1 KB) a copy.  The first half of a block's waves copies the
+// one tensor, the second half the other, so a wave has one pointer to move.  Rows past the
+// tensor's part and pieces past dim become zeros.
+//   DIRECT: straight into LDS through bounds-checked buffer copies, which stay in flight.
+//   Needs 16-byte alignment, and rows that do not overlap (the check is on the offset).
+//   Otherwise: loads and LDS writes, any alignment and row distance.
 constexpr uint32_t OUT_OF_RANGE = 0x80000000u;
+constexpr int RING = 4;
 
 template <typename T, int RB, int WAVES, bool DIRECT>
 struct Fill {
-    static constexpr int TILE = 32 * RB, PER = RB / 16 / WAVES;
-    static_assert(RB / 16 % WAVES == 0, "the same number of copies in every wave");
-    uint32_t off[PER];
-    int row[PER];
-    bool second[PER];  // which tensor a copy is of (the same in all lanes)
-    uint32_t at[PER];
+    static constexpr int TILE = 32 * RB, PER = RB / 16 / WAVES;  // copies of a wave for a tile
+    static_assert(RB / 16 % WAVES == 0 && WAVES % 2 == 0, "whole copies, waves of one tensor");
+    uint32_t off[PER];      // byte offset of the lane's piece from row 0 of a tile
+    uint32_t to;            // LDS address of the wave's first copy in place 0
+    int64_t row_bytes;      // of the wave's tensor
+    bool second;            // which one it is
+    const char *ptr;        // row 0 of the next tile
+    int left;               // its rows that exist (more than 32: all do)
+    uint32_t place;         // its place's offset in the ring
 
-    // row_a, row_b: distances between rows in elements (0 for copy_grouped).
-    __device__ __forceinline__ void init(int64_t row_a, int64_t row_b, int dim)
+    // lds_a, lds_b: the rings; row_a, row_b: distances between rows in elements (both 0 for
+    // next_grouped).
+    __device__ __forceinline__ void init(uint32_t lds_a, uint32_t lds_b, int64_t row_a, int64_t row_b, int dim)
     {
-        const uint32_t wave = threadIdx.x >> 6, lane = lane_id();
+        const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = lane_id();
+        second = wave >= WAVES / 2;
+        const uint32_t first = (wave - (second ? WAVES / 2 : 0)) * PER * 1024;
+        to = (second ? lds_b : lds_a) + first;
+        row_bytes = (second ? row_b : row_a) * (int64_t)sizeof(T);
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
-            const uint32_t x = wave * PER + i, sec = x >= RB / 32, in = (x - (sec ? RB / 32 : 0)) * 1024 + lane * 16;
-            const uint32_t r = in / RB, piece = (in % RB / 16) ^ swizzle<RB>(r);
-            second[i] = __builtin_amdgcn_readfirstlane(sec);
-            at[i] = __builtin_amdgcn_readfirstlane(in);  // of lane 0
-            row[i] = (int)r;
-            off[i] = piece * VEC<T> < (uint32_t)dim ? r * (uint32_t)((second[i] ? row_b : row_a) * sizeof(T)) + piece * 16
-                                                    : OUT_OF_RANGE;
+            const uint32_t in = first + i * 1024 + lane * 16, r = in / RB, piece = (in % RB / 16) ^ swizzle<RB>(r);
+            off[i] = piece * VEC<T> < (uint32_t)dim ? r * (uint32_t)row_bytes + piece * 16 : OUT_OF_RANGE;
         }
     }
-    // a, b: row 0 of the tiles; left_a, left_b: rows that exist; lds_a, lds_b: where to.
-    __device__ __forceinline__ void copy(const T *a, int left_a, uint32_t lds_a, const T *b, int left_b, uint32_t lds_b) const
+    // The next tile is the first: `rows` rows from a and b on.
+    __device__ __forceinline__ void start(const T *a, const T *b, int rows)
     {
+        ptr = (const char *)(second ? b : a);
+        left = rows;
+        place = 0;
+    }
+    __device__ __forceinline__ void next()
+    {
+        const int n = left < 0 ? 0 : (left > 32 ? 32 : left);
+        if constexpr (DIRECT) {
+            const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc((void *)ptr, (short)0, n * (int)row_bytes, 0x00020000);
 #pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            const T *base = second[i] ? b : a;
-            const int left = second[i] ? left_b : left_a;
-            const uint32_t to = (second[i] ? lds_b : lds_a) + at[i], o = row[i] < left ? off[i] : OUT_OF_RANGE;
-            put(base, o, to);
+            for (int i = 0; i < PER; ++i)
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (SC_LDS void *)(uintptr_t)(to + place + i * 1024), 16, off[i], 0, 0, 0);
+        } else {
+#pragma unroll
+            for (int i = 0; i < PER; ++i) put(ptr, row(i) < n ? off[i] : OUT_OF_RANGE, i);
         }
+        ptr += 32 * row_bytes;
+        advance();
     }
-    // The same for the rows of an entry's grouped query heads: row r is token token0 +
-    // r / group, head head0 + r % group; row0 is the tiles' first.
-    __device__ __forceinline__ void copy_grouped(const Heads &a, const Heads &b, int64_t token0, int head0, uint32_t row0,
-                                                 uint32_t group, int left, uint32_t lds_a, uint32_t lds_b) const
+    // The next 32 rows of grouped query heads (row r is token token0 + r / group, head head0 +
+    // r % group): row0 is the first.
+    __device__ __forceinline__ void next_grouped(const Heads &a, const Heads &b, int64_t token0, int head0, uint32_t row0, uint32_t group)
     {
+        const Heads &h = second ? b : a;
         const uint32_t t0 = row0 / group;
+        const char *base = (const char *)h.p + ((token0 + t0) * h.row + head0 * h.head) * (int64_t)sizeof(T);
+        const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc((void *)base, (short)0, 0x7fffffff, 0x00020000);
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
-            const Heads &h = second[i] ? b : a;
-            const T *base = (const T *)h.p + (token0 + t0) * h.row + head0 * h.head;
-            const uint32_t r = row0 + row[i], t = r / group, g = r - t * group;
-            const uint32_t piece = off[i];  // init with distances 0
-            const uint32_t o = row[i] < left && piece != OUT_OF_RANGE
-                                   ? (t - t0) * (uint32_t)(h.row * sizeof(T)) + g * (uint32_t)(h.head * sizeof(T)) + piece
+            const uint32_t r = row0 + row(i), t = r / group;
+            const uint32_t o = row(i) < left && off[i] != OUT_OF_RANGE
+                                   ? (t - t0) * (uint32_t)(h.row * sizeof(T)) + (r - t * group) * (uint32_t)(h.head * sizeof(T)) + off[i]
                                    : OUT_OF_RANGE;
-            put(base, o, (second[i] ? lds_b : lds_a) + at[i]);
+            if constexpr (DIRECT)
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (SC_LDS void *)(uintptr_t)(to + place + i * 1024), 16, o, 0, 0, 0);
+            else
+                put(base, o, i);
         }
+        advance();
     }
 
   private:
-    static __device__ __forceinline__ void put(const T *base, uint32_t o, uint32_t to)
+    __device__ __forceinline__ int row(int i) const
     {
-        if constexpr (DIRECT) {
-            const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc((void *)base, (short)0, 0x7fffffff, 0x00020000);
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (SC_LDS void *)(uintptr_t)to, 16, o, 0, 0, 0);
-        } else {
-            Raw16 v = {0, 0, 0, 0};
-            if (o != OUT_OF_RANGE) v = *(const Raw16Any *)((const char *)base + o);
-            lds_write16(to + lane_id() * 16, v);
-        }
+        return (int)(((__builtin_amdgcn_readfirstlane(threadIdx.x >> 6) % (WAVES / 2)) * PER * 1024 + i * 1024 + lane_id() * 16) / RB);
+    }
+    __device__ __forceinline__ void advance()
+    {
+        left -= 32;
+        place = place == (RING - 1) * TILE ? 0 : place + TILE;
+    }
+    __device__ __forceinline__ void put(const char *base, uint32_t o, int i) const
+    {
+        Raw16 v = {0, 0, 0, 0};
+        if (o != OUT_OF_RANGE) v = *(const Raw16Any *)(base + o);
+        lds_write16(to + place + i * 1024 + lane_id() * 16, v);
     }
 };
 
@@ -370,8 +392,6 @@ __device__ __forceinline__ void mma_rows(const RowsAddr<float, RB> &ad, uint32_t
             for (int x = 0; x < N; ++x) acc[x][db] = __builtin_amdgcn_mfma_f32_32x32x2f32(v, p[x].v[i], acc[x][db], 0, 0, 0);
         }
 }
-
-__device__ __forceinline__ int rows_left(int64_t left) { return left < 0 ? 0 : (left > 32 ? 32 : (int)left); }
 
 // The other half's value (lanes l and l ^ 32).
 __device__ __forceinline__ float other_half(float v)

@@ -62,21 +62,22 @@ __device__ __forceinline__ void scale_if(f32x16 &acc, float f, uint64_t on)
                  : "scc");
 }
 
-constexpr int FWD_WAVES = 4, RING = 4;
+constexpr int FWD_WAVES = 4;
 
 // A step handles 32 keys.  Its wave has the scores of its own keys in registers already,
 // and, while it turns them into weights, the matrix cores form the scores of the next
 // 32 keys; then they take the weights' product with the values, and the next scores'
-// maximum is found meanwhile.  Keys are copied four steps ahead and values three, into
-// rings of four tiles in LDS.
+// maximum is found meanwhile.  Keys and values are copied three steps ahead, into rings of
+// four tiles in LDS.
 //
 // QB: blocks of 32 query rows a wave owns.  SPLIT: a block takes one run of `chunk` keys of
 // an entry and leaves (sum, m, l) of it in part / part2 for k_attn_join; otherwise a block
 // takes one tile of query rows over all keys.
-template <typename T, int DP, int QB, bool SPLIT, bool DIRECT>
-__global__ __launch_bounds__(64 * FWD_WAVES, DP * sizeof(T) * QB > 256 ? 1 : DP * sizeof(T) * QB > 128 ? 2 : 3) void k_attn(AttnArgs A)
+template <typename T, int DP, bool SPLIT, bool DIRECT>
+__global__ __launch_bounds__(64 * FWD_WAVES, DP * sizeof(T) > 256 ? 1 : DP * sizeof(T) > 128 ? 2 : 3) void k_attn(AttnArgs A)
 {
-    constexpr int RB = DP * (int)sizeof(T), NJ = RB / 32, DB = DP / 32, TILE = 32 * RB, ROWS = 32 * QB * FWD_WAVES;
+    constexpr int RB = DP * (int)sizeof(T), NJ = RB / 32, DB = DP / 32, TILE = 32 * RB, ROWS = 32 * FWD_WAVES;
+    constexpr int QB = 1;
     constexpr uint32_t V0 = RING * TILE;  // the values' ring
     __shared__ __attribute__((aligned(1024))) char smem[2 * RING * TILE];
     const uint32_t lds = (uint32_t)(uintptr_t)(SC_LDS char *)smem;
@@ -111,27 +112,22 @@ __global__ __launch_bounds__(64 * FWD_WAVES, DP * sizeof(T) * QB > 256 ? 1 : DP 
     const T *vp = (const T *)A.v.p + (k_beg + key0) * A.v.row + hk * A.v.head;
     Fill<T, RB, FWD_WAVES, DIRECT> fill;
     constexpr int PER = Fill<T, RB, FWD_WAVES, DIRECT>::PER;
-    fill.init(A.k.row, A.v.row, A.dim);
+    fill.init(lds, lds + V0, A.k.row, A.v.row, A.dim);
     HeadAddr<RB> ka(lds);
     RowsAddr<T, RB> va(lds + V0);
-    // keys of step u + RING and values of step u + RING - 1: their places were last read in step u - 1
-    auto copy = [&](int u) {
-        const int a = u + RING, b = u + RING - 1;
-        fill.copy(kp + a * 32 * A.k.row, rows_left((int64_t)keys - a * 32ll), lds + (a & (RING - 1)) * TILE,
-                  vp + b * 32 * A.v.row, rows_left(b < 0 ? 0 : (int64_t)keys - b * 32ll), lds + V0 + (b & (RING - 1)) * TILE);
-    };
 
     for (; qtile * ROWS < rows; qtile += SPLIT ? A.tiles : rows) {
         const int64_t wave_row = qtile * ROWS + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) * (32 * QB);
         if (SPLIT) __syncthreads();  // the rings' last readers are done
+        fill.start(kp, vp, keys);
         if (steps)
-            for (int u = -RING; u < 0; ++u) copy(u);
+            for (int u = 1; u < RING; ++u) fill.next();
         if (wave_row >= rows) {  // a wave past the entry's rows only helps with the copies
             if (steps) {
-                wait_copies_and_barrier<3 * PER>();
-                for (int u = -1; u < steps - 1; ++u) {
-                    if (u >= 0) copy(u);
-                    wait_copies_and_barrier<2 * PER>();
+                wait_copies_and_barrier<2 * PER>();
+                for (int u = 0; u < steps; ++u) {
+                    if (u) fill.next();
+                    wait_copies_and_barrier<PER>();
                 }
                 wait_copies_and_barrier<0>();
             }
@@ -244,7 +240,7 @@ __global__ __launch_bounds__(64 * FWD_WAVES, DP * sizeof(T) * QB > 256 ? 1 : DP 
         // step u from scores t, leaving the next step's in n; kat, vat: the tiles' places past ka and va
         auto step = [&](f32x16(&t)[QB], f32x16(&n)[QB], int u, uint32_t kat, uint32_t vat) {
             float top[QB];
-            copy(u);
+            fill.next();  // tiles u + 3: their places were last read in step u - 1
             if constexpr (sizeof(T) == 2) {
                 // in the order it is to run: LDS reads AHEAD of their use, and between the matrix
                 // products a piece of the arithmetic; first the scores with half the weights, then
@@ -288,17 +284,17 @@ __global__ __launch_bounds__(64 * FWD_WAVES, DP * sizeof(T) * QB > 256 ? 1 : DP 
                 maximum(n, top, 0, 16);
             }
             settle(n, top);
-            wait_copies_and_barrier<2 * PER>();
+            wait_copies_and_barrier<PER>();
         };
 
         if (steps) {
-            wait_copies_and_barrier<3 * PER>();
+            wait_copies_and_barrier<2 * PER>();
             float top[QB];
             scores(s[0], 0);
             mask(s[0], 0);
             maximum(s[0], top, 0, 16);
             settle(s[0], top);
-            wait_copies_and_barrier<2 * PER>();
+            wait_copies_and_barrier<PER>();
             int u = 0;
             for (; u + 2 < steps; u += 2) {  // ring places u mod 4 = 0 or 2: the addresses move to the other half
                 const uint32_t other = u & 2 ? -2 * TILE : 2 * TILE;
@@ -339,6 +335,23 @@ __global__ __launch_bounds__(64 * FWD_WAVES, DP * sizeof(T) * QB > 256 ? 1 : DP 
         }
     }
 }
+
+// Every variant that is launched, spelled out: the host pass leaves some of them out when they
+// are only named in a launch.
+#define VARIANTS(T, DP, DIRECT) \
+    template __global__ void k_attn<T, DP, false, DIRECT>(AttnArgs); \
+    template __global__ void k_attn<T, DP, true, DIRECT>(AttnArgs);
+VARIANTS(float, 32, true)
+VARIANTS(float, 64, true)
+VARIANTS(float, 96, true)
+VARIANTS(float, 128, true)
+VARIANTS(float, 128, false)
+VARIANTS(uint16_t, 32, true)
+VARIANTS(uint16_t, 64, true)
+VARIANTS(uint16_t, 96, true)
+VARIANTS(uint16_t, 128, true)
+VARIANTS(uint16_t, 128, false)
+#undef VARIANTS
 
 // One block to a query row: the splits' sums joined in order of their number.
 constexpr int JOIN_MAX_SPLITS = 2048;
@@ -425,15 +438,6 @@ SplitPlan split_plan(int64_t own_rows, int own_tile, int64_t other_rows, int oth
     return p;
 }
 
-// Query rows a block takes without a split: 64 a wave where that still gives every
-// compute unit a block.
-static int fwd_blocks_of_rows(const AttnArgs &A, int dtype)
-{
-    if (dtype == SUBMCONV_F32) return 1;
-    const int64_t rows = A.nq * A.group;
-    return 1;
-}
-
 static SplitPlan fwd_plan(const AttnArgs &A)
 {
     return split_plan(A.nq * A.group, 32 * FWD_WAVES, A.nk, 32, A.entries, A.kv_heads);
@@ -445,14 +449,15 @@ size_t attention_workspace(const AttnArgs &A)
     return p.chunk ? (size_t)p.splits * A.nq * A.heads * (A.dim + 2) * sizeof(float) : 0;
 }
 
-// Whether keys and values can be copied straight into LDS.
+// Whether keys and values can be copied straight into LDS (see Fill).
 static bool direct(const AttnArgs &A, int es)
 {
-    return !(((uintptr_t)A.k.p | (uintptr_t)A.v.p | (uintptr_t)((A.k.row | A.v.row | A.k.head | A.v.head) * es)) & 15);
+    return !(((uintptr_t)A.k.p | (uintptr_t)A.v.p | (uintptr_t)((A.k.row | A.v.row | A.k.head | A.v.head) * es)) & 15) &&
+           A.k.row >= A.dim && A.v.row >= A.dim;
 }
 
 template <typename T, int DP, bool DIRECT>
-static int run_fwd(AttnArgs A, const SplitPlan &p, int qb, void *workspace, hipStream_t st)
+static int run_fwd(AttnArgs A, const SplitPlan &p, void *workspace, hipStream_t st)
 {
     const dim3 block(64 * FWD_WAVES);
     if (p.chunk) {
@@ -462,21 +467,14 @@ static int run_fwd(AttnArgs A, const SplitPlan &p, int qb, void *workspace, hipS
         A.part = (float *)workspace;
         A.part2 = A.part + p.splits * A.nq * A.heads * A.dim;
         const int64_t work = ragged_tiles(A.nk, A.entries, 1, p.chunk) * A.kv_heads * p.tiles;
-        hipLaunchKernelGGL((k_attn<T, DP, 1, true, DIRECT>), dim3(xcd_grid(work)), block, 0, st, A);
+        hipLaunchKernelGGL((k_attn<T, DP, true, DIRECT>), dim3(xcd_grid(work)), block, 0, st, A);
         SC_LAUNCHED("attention (split)");
         hipLaunchKernelGGL((k_attn_join<T>), dim3((unsigned)(A.nq * A.heads)), dim3(256), 0, st, A);
         SC_LAUNCHED("attention join");
         return SUBMCONV_OK;
     }
-    const dim3 grid(xcd_grid(ragged_tiles(A.nq, A.entries, A.group, 32 * FWD_WAVES * qb) * A.kv_heads));
-    if constexpr (sizeof(T) == 2 && DIRECT) {
-        if (qb == 2) {
-            hipLaunchKernelGGL((k_attn<T, DP, 2, false, true>), grid, block, 0, st, A);
-            SC_LAUNCHED("attention");
-            return SUBMCONV_OK;
-        }
-    }
-    hipLaunchKernelGGL((k_attn<T, DP, 1, false, DIRECT>), grid, block, 0, st, A);
+    const dim3 grid(xcd_grid(ragged_tiles(A.nq, A.entries, A.group, 32 * FWD_WAVES) * A.kv_heads));
+    hipLaunchKernelGGL((k_attn<T, DP, false, DIRECT>), grid, block, 0, st, A);
     SC_LAUNCHED("attention");
     return SUBMCONV_OK;
 }
@@ -486,13 +484,12 @@ int attention(const AttnArgs &A, int dtype, void *workspace, hipStream_t st)
     const SplitPlan p = fwd_plan(A);
     const int dp = (A.dim + 31) / 32;
 #define GO(T)                                                                                       \
-    if (!direct(A, sizeof(T))) return run_fwd<T, 128, false>(A, p, 1, workspace, st);               \
-    const int qb = fwd_blocks_of_rows(A, dtype);                                                    \
+    if (!direct(A, sizeof(T))) return run_fwd<T, 128, false>(A, p, workspace, st); \
     switch (dp) {                                                                                   \
-    case 1: return run_fwd<T, 32, true>(A, p, qb, workspace, st);                                   \
-    case 2: return run_fwd<T, 64, true>(A, p, qb, workspace, st);                                   \
-    case 3: return run_fwd<T, 96, true>(A, p, qb, workspace, st);                                   \
-    default: return run_fwd<T, 128, true>(A, p, qb, workspace, st);                                 \
+    case 1: return run_fwd<T, 32, true>(A, p, workspace, st); \
+    case 2: return run_fwd<T, 64, true>(A, p, workspace, st); \
+    case 3: return run_fwd<T, 96, true>(A, p, workspace, st); \
+    default: return run_fwd<T, 128, true>(A, p, workspace, st); \
     }
     if (dtype == SUBMCONV_F32) {
         GO(float)

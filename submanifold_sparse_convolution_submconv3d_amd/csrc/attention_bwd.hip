@@ -13,7 +13,7 @@
 
 namespace sc {
 
-constexpr int BWD_WAVES = 4, BWD_ROWS = 32 * BWD_WAVES, BWD_RING = 4;
+constexpr int BWD_WAVES = 4, BWD_ROWS = 32 * BWD_WAVES;
 
 // A score's exponent is s c - base; a query whose scores are all -inf has lse = -inf and
 // weights exp(-inf), so its base must be finite.
@@ -27,8 +27,8 @@ template <typename T, int DP, bool SPLIT, bool DIRECT>
 __global__ __launch_bounds__(64 * BWD_WAVES, DP * sizeof(T) > 256 ? 1 : 2) void k_attn_dq(AttnArgs A)
 {
     constexpr int RB = DP * (int)sizeof(T), NJ = RB / 32, DB = DP / 32, TILE = 32 * RB;
-    constexpr uint32_t V0 = BWD_RING * TILE;
-    __shared__ __attribute__((aligned(1024))) char smem[2 * BWD_RING * TILE];
+    constexpr uint32_t V0 = RING * TILE;
+    __shared__ __attribute__((aligned(1024))) char smem[2 * RING * TILE];
     const uint32_t lds = (uint32_t)(uintptr_t)(SC_LDS char *)smem;
 
     const Ragged rq = {A.q_off, A.entries, A.nq, A.group}, rk = {A.k_off, A.entries, A.nk, 1};
@@ -61,25 +61,21 @@ __global__ __launch_bounds__(64 * BWD_WAVES, DP * sizeof(T) > 256 ? 1 : 2) void 
     const T *vp = (const T *)A.v.p + (k_beg + key0) * A.v.row + hk * A.v.head;
     Fill<T, RB, BWD_WAVES, DIRECT> fill;
     constexpr int PER = Fill<T, RB, BWD_WAVES, DIRECT>::PER;
-    fill.init(A.k.row, A.v.row, A.dim);
+    fill.init(lds, lds + V0, A.k.row, A.v.row, A.dim);
     HeadAddr<RB> ka(lds);
     RowsAddr<T, RB> kt(lds);
-    // keys and values of step u + 3: their places were last read in step u - 1
-    auto copy = [&](int u) {
-        const int a = u + BWD_RING - 1, at = (a & (BWD_RING - 1)) * TILE, left = rows_left((int64_t)keys - a * 32ll);
-        fill.copy(kp + a * 32 * A.k.row, left, lds + at, vp + a * 32 * A.v.row, left, lds + V0 + at);
-    };
 
     for (; qtile * BWD_ROWS < rows; qtile += SPLIT ? A.tiles : rows) {
         const int64_t wave_row = qtile * BWD_ROWS + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) * 32;
         if (SPLIT) __syncthreads();
+        fill.start(kp, vp, keys);
         if (steps)
-            for (int u = 1 - BWD_RING; u < 0; ++u) copy(u);
+            for (int u = 1; u < RING; ++u) fill.next();
         if (wave_row >= rows) {  // a wave past the entry's rows only helps with the copies
             if (steps) {
                 wait_copies_and_barrier<2 * PER>();
-                for (int u = -1; u < steps - 1; ++u) {
-                    if (u >= 0) copy(u);
+                for (int u = 0; u < steps; ++u) {
+                    if (u) fill.next();
                     wait_copies_and_barrier<PER>();
                 }
                 wait_copies_and_barrier<0>();
@@ -133,18 +129,56 @@ __global__ __launch_bounds__(64 * BWD_WAVES, DP * sizeof(T) > 256 ? 1 : 2) void 
                     if (8 * (i / 4) + 4 * half + i % 4 >= keys - u * 32) t[i] = -INFINITY;
             }
         };
+        auto weigh = [&](f32x16 &t, const f32x16 &e, int from, int to) {
+#pragma unroll
+            for (int i = from; i < to; ++i) t[i] = __builtin_amdgcn_exp2f(fmaf(t[i], c, -base)) * (e[i] - delta);
+        };
         auto gradient = [&](f32x16 &t, const f32x16 &e, uint32_t place) {
             RowsOperand<T> ds[1];
-#pragma unroll
-            for (int i = 0; i < 16; ++i) t[i] = __builtin_amdgcn_exp2f(fmaf(t[i], c, -base)) * (e[i] - delta);
+            weigh(t, e, 0, 16);
             ds[0].set(t);
             mma_rows<RB>(kt, place, ds, dq);
         };
-        auto step = [&](int from, int to, int u, uint32_t next_at, uint32_t own_at) {
-            copy(u);
-            products(s[to], dp[to], next_at);
-            gradient(s[from], dp[from], own_at);
-            mask(s[to], u + 1);
+        auto step = [&](f32x16 &t, f32x16 &e, f32x16 &nt, f32x16 &ne, int u, uint32_t next_at, uint32_t own_at) {
+            fill.next();  // tiles u + 3: their places were last read in step u - 1
+            if constexpr (sizeof(T) == 2) {
+                // in the order it is to run: LDS reads ahead of their use, the arithmetic between the products
+                constexpr int AHEAD = NJ < 2 ? NJ : 2;
+                Raw16 k[NJ], v[NJ], r[2 * DB], ds[2];
+#pragma unroll
+                for (int j = 0; j < AHEAD; ++j) {
+                    k[j] = lds_read16(ka.at[j] + next_at);
+                    v[j] = lds_read16(ka.at[j] + next_at + V0);
+                }
+                __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                for (int j = 0; j < NJ; ++j) {
+                    if (j + AHEAD < NJ) {
+                        k[j + AHEAD] = lds_read16(ka.at[j + AHEAD] + next_at);
+                        v[j + AHEAD] = lds_read16(ka.at[j + AHEAD] + next_at + V0);
+                    } else if (j + AHEAD - NJ < 2 * DB) {
+                        r[j + AHEAD - NJ] = rows_piece<RB>(kt, own_at, j + AHEAD - NJ);
+                    }
+                    nt = mma_pieces<T>(k[j], q[j], j ? nt : f32x16{});
+                    weigh(t, e, 16 * j / NJ, 16 * j / NJ + 8 / NJ);
+                    __builtin_amdgcn_sched_barrier(0);
+                    ne = mma_pieces<T>(v[j], g[j], j ? ne : f32x16{});
+                    weigh(t, e, 16 * j / NJ + 8 / NJ, 16 * (j + 1) / NJ);
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+                ds[0] = pack8(t, 0);
+                ds[1] = pack8(t, 1);
+#pragma unroll
+                for (int x = 0; x < 2 * DB; ++x) {
+                    if (x + AHEAD < 2 * DB) r[x + AHEAD] = rows_piece<RB>(kt, own_at, x + AHEAD);
+                    dq[0][x % DB] = mma_pieces<T>(r[x], ds[x / DB], dq[0][x % DB]);
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+            } else {
+                products(nt, ne, next_at);
+                gradient(t, e, own_at);
+            }
+            mask(nt, u + 1);
             wait_copies_and_barrier<PER>();
         };
         if (steps) {
@@ -155,13 +189,13 @@ __global__ __launch_bounds__(64 * BWD_WAVES, DP * sizeof(T) > 256 ? 1 : 2) void 
             int u = 0;
             for (; u + 2 < steps; u += 2) {  // ring places u mod 4 = 0 or 2: the addresses move to the other half
                 const uint32_t other = u & 2 ? -2 * TILE : 2 * TILE;
-                step(0, 1, u, TILE, 0);
+                step(s[0], dp[0], s[1], dp[1], u, TILE, 0);
                 ka.move(other);
-                step(1, 0, u + 1, 0, TILE);
+                step(s[1], dp[1], s[0], dp[0], u + 1, 0, TILE);
                 kt.move(other);
             }
             if (u + 1 < steps) {
-                step(0, 1, u, TILE, 0);
+                step(s[0], dp[0], s[1], dp[1], u, TILE, 0);
                 gradient(s[1], dp[1], TILE);
             } else {
                 gradient(s[0], dp[0], 0);
@@ -186,8 +220,8 @@ template <typename T, int DP, bool SPLIT, bool DIRECT>
 __global__ __launch_bounds__(64 * BWD_WAVES, DP * sizeof(T) > 128 ? 1 : 2) void k_attn_dkv(AttnArgs A)
 {
     constexpr int RB = DP * (int)sizeof(T), NJ = RB / 32, DB = DP / 32, TILE = 32 * RB;
-    constexpr uint32_t G0 = BWD_RING * TILE, STAT0 = 2 * BWD_RING * TILE;
-    __shared__ __attribute__((aligned(1024))) char smem[2 * BWD_RING * TILE + BWD_RING * BWD_WAVES * 256];
+    constexpr uint32_t G0 = RING * TILE, STAT0 = 2 * RING * TILE;
+    __shared__ __attribute__((aligned(1024))) char smem[2 * RING * TILE + RING * BWD_WAVES * 256];
     const uint32_t lds = (uint32_t)(uintptr_t)(SC_LDS char *)smem;
 
     const Ragged rq = {A.q_off, A.entries, A.nq, A.group}, rk = {A.k_off, A.entries, A.nk, 1};
@@ -219,41 +253,40 @@ __global__ __launch_bounds__(64 * BWD_WAVES, DP * sizeof(T) > 128 ? 1 : 2) void 
     const uint32_t group = A.group;
     Fill<T, RB, BWD_WAVES, DIRECT> fill;
     constexpr int PER = Fill<T, RB, BWD_WAVES, DIRECT>::PER + 1;  // and the rows' statistics
-    fill.init(group == 1 ? A.q.row : 0, group == 1 ? A.grad.row : 0, A.dim);
+    fill.init(lds, lds + G0, group == 1 ? A.q.row : 0, group == 1 ? A.grad.row : 0, A.dim);
     HeadAddr<RB> qa(lds);
     RowsAddr<T, RB> qt(lds);
     const uint32_t my_stat = lds + STAT0 + wave * 256;  // each wave keeps its own copy
-    auto copy = [&](int u) {
-        const int a = u + BWD_RING - 1, place = a & (BWD_RING - 1), left = rows_left((int64_t)rows - a * 32ll);
+    auto copy = [&](int a) {                            // the rows of step a: their places were last read in step a - 4
         const uint32_t first = (uint32_t)row0 + a * 32;
-        if (group == 1)
-            fill.copy((const T *)A.q.p + (q_beg + first) * A.q.row + hk * A.q.head, left, lds + place * TILE,
-                      (const T *)A.grad.p + (q_beg + first) * A.grad.row + hk * A.grad.head, left, lds + G0 + place * TILE);
-        else
-            fill.copy_grouped(A.q, A.grad, q_beg, hk * group, first, group, left, lds + place * TILE, lds + G0 + place * TILE);
+        const int left = rows - a * 32;
         // (base, delta) of 32 rows: one word a lane
         const uint32_t t0 = group == 1 ? first : first / group, r = first + lane / 2, t = group == 1 ? r : r / group;
         const float *sp = A.stat + ((q_beg + t0) * A.heads + hk * group) * 2;
         const uint32_t o = lane / 2 < left ? ((t - t0) * A.heads + (r - t * group)) * 8 + (lane & 1) * 4 : OUT_OF_RANGE;
-        const uint32_t to = my_stat + place * (BWD_WAVES * 256);
+        const uint32_t to = my_stat + (a & (RING - 1)) * (BWD_WAVES * 256);
         if constexpr (DIRECT) {
             const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc((void *)sp, (short)0, 0x7fffffff, 0x00020000);
             __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (SC_LDS void *)(uintptr_t)to, 4, o, 0, 0, 0);
         } else {
             *(SC_LDS float *)(uintptr_t)(to + lane * 4) = o != OUT_OF_RANGE ? *(const float *)((const char *)sp + o) : 0.0f;
         }
+        if (group == 1) fill.next();
+        else fill.next_grouped(A.q, A.grad, q_beg, hk * group, first, group);
     };
 
     for (; ktile * BWD_ROWS < keys; ktile += SPLIT ? A.tiles : keys) {
         const int64_t wave_key = ktile * BWD_ROWS + wave * 32;
         if (SPLIT) __syncthreads();
+        fill.start((const T *)A.q.p + (q_beg + row0) * A.q.row + hk * A.q.head,
+                   (const T *)A.grad.p + (q_beg + row0) * A.grad.row + hk * A.grad.head, rows);  // (group = 1)
         if (steps)
-            for (int u = 1 - BWD_RING; u < 0; ++u) copy(u);
+            for (int u = 0; u < RING - 1; ++u) copy(u);
         if (wave_key >= keys) {
             if (steps) {
                 wait_copies_and_barrier<2 * PER>();
-                for (int u = -1; u < steps - 1; ++u) {
-                    if (u >= 0) copy(u);
+                for (int u = 0; u < steps; ++u) {
+                    if (u) copy(u + RING - 2);
                     wait_copies_and_barrier<PER>();
                 }
                 wait_copies_and_barrier<0>();
@@ -283,27 +316,73 @@ __global__ __launch_bounds__(64 * BWD_WAVES, DP * sizeof(T) > 128 ? 1 : 2) void 
                 e = mma_pieces<T>(lds_read16(qa.at[j] + place + G0), v[j], e);
             }
         };
+        // registers i, i + 1: rows 8 (i / 4) + 4 half + i % 4 and the next, two (base, delta) pairs
+        auto stats = [&](int u, int i) {
+            return __builtin_bit_cast(f32x4, lds_read16(my_stat + (u & (RING - 1)) * (BWD_WAVES * 256) + 32 * half + 64 * (i / 4) + 8 * (i % 4)));
+        };
+        auto weigh = [&](f32x16 &t, f32x16 &e, int i, f32x4 bd) {
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                t[i + x] = __builtin_amdgcn_exp2f(fmaf(t[i + x], c, -bd[2 * x]));
+                e[i + x] = t[i + x] * (e[i + x] - bd[2 * x + 1]);
+            }
+        };
         auto gradient = [&](f32x16 &t, f32x16 &e, int u, uint32_t place) {
-            const uint32_t st = my_stat + (u & (BWD_RING - 1)) * (BWD_WAVES * 256) + 32 * half;
             RowsOperand<T> p[1], ds[1];
 #pragma unroll
-            for (int i = 0; i < 16; i += 2) {  // rows 8 (i / 4) + 4 half + i % 4: two (base, delta) pairs
-                const f32x4 bd = __builtin_bit_cast(f32x4, lds_read16(st + 64 * (i / 4) + 8 * (i % 4)));
-#pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    t[i + x] = __builtin_amdgcn_exp2f(fmaf(t[i + x], c, -bd[2 * x]));
-                    e[i + x] = t[i + x] * (e[i + x] - bd[2 * x + 1]);
-                }
-            }
+            for (int i = 0; i < 16; i += 2) weigh(t, e, i, stats(u, i));
             p[0].set(t);
             mma_rows<RB>(qt, place + G0, p, dv);
             ds[0].set(e);
             mma_rows<RB>(qt, place, ds, dk);
         };
-        auto step = [&](int from, int to, int u, uint32_t next_at, uint32_t own_at) {
-            copy(u);
-            products(s[to], dp[to], next_at);
-            gradient(s[from], dp[from], u, own_at);
+        auto step = [&](f32x16 &t, f32x16 &e, f32x16 &nt, f32x16 &ne, int u, uint32_t next_at, uint32_t own_at) {
+            copy(u + RING - 1);
+            if constexpr (sizeof(T) == 2) {
+                // in the order it is to run: LDS reads ahead of their use, the arithmetic between the products
+                constexpr int AHEAD = NJ < 2 ? NJ : 2;
+                Raw16 a[NJ], b[NJ], r[4 * DB], w[4];
+                f32x4 bd[8];
+                auto rows = [&](int x) { return rows_piece<RB>(qt, own_at + (x < 2 * DB ? G0 : 0), x % (2 * DB)); };
+#pragma unroll
+                for (int i = 0; i < 8; ++i) bd[i] = stats(u, 2 * i);
+#pragma unroll
+                for (int j = 0; j < AHEAD; ++j) {
+                    a[j] = lds_read16(qa.at[j] + next_at);
+                    b[j] = lds_read16(qa.at[j] + next_at + G0);
+                }
+                __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                for (int j = 0; j < NJ; ++j) {
+                    if (j + AHEAD < NJ) {
+                        a[j + AHEAD] = lds_read16(qa.at[j + AHEAD] + next_at);
+                        b[j + AHEAD] = lds_read16(qa.at[j + AHEAD] + next_at + G0);
+                    } else {
+                        r[2 * (j + AHEAD - NJ)] = rows(2 * (j + AHEAD - NJ));
+                        r[2 * (j + AHEAD - NJ) + 1] = rows(2 * (j + AHEAD - NJ) + 1);
+                    }
+                    nt = mma_pieces<T>(a[j], k[j], j ? nt : f32x16{});
+                    __builtin_amdgcn_sched_barrier(0);
+                    ne = mma_pieces<T>(b[j], v[j], j ? ne : f32x16{});
+#pragma unroll
+                    for (int i = 8 * j / NJ; i < 8 * (j + 1) / NJ; ++i) weigh(t, e, 2 * i, bd[i]);
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+                w[0] = pack8(t, 0);
+                w[1] = pack8(t, 1);
+                w[2] = pack8(e, 0);
+                w[3] = pack8(e, 1);
+#pragma unroll
+                for (int x = 0; x < 4 * DB; ++x) {
+                    if (x + 2 * AHEAD < 4 * DB) r[x + 2 * AHEAD] = rows(x + 2 * AHEAD);
+                    f32x16 &d = x < 2 * DB ? dv[0][x % DB] : dk[0][x % DB];
+                    d = mma_pieces<T>(r[x], w[x / DB], d);
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+            } else {
+                products(nt, ne, next_at);
+                gradient(t, e, u, own_at);
+            }
             wait_copies_and_barrier<PER>();
         };
         if (steps) {
@@ -313,13 +392,13 @@ __global__ __launch_bounds__(64 * BWD_WAVES, DP * sizeof(T) > 128 ? 1 : 2) void 
             int u = 0;
             for (; u + 2 < steps; u += 2) {
                 const uint32_t other = u & 2 ? -2 * TILE : 2 * TILE;
-                step(0, 1, u, TILE, 0);
+                step(s[0], dp[0], s[1], dp[1], u, TILE, 0);
                 qa.move(other);
-                step(1, 0, u + 1, 0, TILE);
+                step(s[1], dp[1], s[0], dp[0], u + 1, 0, TILE);
                 qt.move(other);
             }
             if (u + 1 < steps) {
-                step(0, 1, u, TILE, 0);
+                step(s[0], dp[0], s[1], dp[1], u, TILE, 0);
                 gradient(s[1], dp[1], u + 1, TILE);
             } else {
                 gradient(s[0], dp[0], u, 0);
@@ -340,6 +419,25 @@ __global__ __launch_bounds__(64 * BWD_WAVES, DP * sizeof(T) > 128 ? 1 : 2) void 
         }
     }
 }
+
+// Every variant that is launched, spelled out: the host pass leaves some of them out when they
+// are only named in a launch.
+#define VARIANTS(T, DP, DIRECT) \
+    template __global__ void k_attn_dq<T, DP, false, DIRECT>(AttnArgs); \
+    template __global__ void k_attn_dq<T, DP, true, DIRECT>(AttnArgs); \
+    template __global__ void k_attn_dkv<T, DP, false, DIRECT>(AttnArgs); \
+    template __global__ void k_attn_dkv<T, DP, true, DIRECT>(AttnArgs);
+VARIANTS(float, 32, true)
+VARIANTS(float, 64, true)
+VARIANTS(float, 96, true)
+VARIANTS(float, 128, true)
+VARIANTS(float, 128, false)
+VARIANTS(uint16_t, 32, true)
+VARIANTS(uint16_t, 64, true)
+VARIANTS(uint16_t, 96, true)
+VARIANTS(uint16_t, 128, true)
+VARIANTS(uint16_t, 128, false)
+#undef VARIANTS
 
 // One block to an output row: the splits' partial gradients of an [n, heads, dim] tensor
 // summed in order of their number and scaled.  `other` is the side that was split.
@@ -452,7 +550,8 @@ static bool direct(const AttnArgs &A, int es)
     uintptr_t bits = 0;
     for (const Heads *h : {&A.q, &A.k, &A.v, &A.grad}) bits |= (uintptr_t)h->p | (uintptr_t)(h->row * es) | (uintptr_t)(h->head * es);
     const int64_t far = (A.q.head > A.grad.head ? A.q.head : A.grad.head) * A.group * es;  // heads of a group
-    return !(bits & 15) && (A.group == 1 || far < int64_t(1) << 30);
+    return !(bits & 15) && A.k.row >= A.dim && A.v.row >= A.dim &&
+           (A.group == 1 ? A.q.row >= A.dim && A.grad.row >= A.dim : far < int64_t(1) << 30);
 }
 
 int attention_backward(AttnArgs A, int dtype, void *workspace, hipStream_t st)
