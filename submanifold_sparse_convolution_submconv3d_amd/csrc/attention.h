@@ -56,10 +56,38 @@ struct Ragged {
 
 static inline int64_t ragged_tiles(int64_t n, int entries, int mult, int rows) { return n * mult / rows + entries + 2; }
 
-// Part and tile within it of tile number `slot`: 64 bounds are compared at a time.  The
+// What work number w is: work is all tiles of all parts, once for each of `many` (heads,
+// and tiles of the other side), whose number comes in *which.  False past the end.  The
 // same in all lanes.
-__device__ __forceinline__ void find_tile(const Ragged &r, int rows, int64_t slot, int *part, int64_t *tile)
+//   Up to 62 entries a lane counts the tiles of a part and a sum over lanes numbers them
+//   without gaps, so that the blocks with work spread evenly over the card whatever the
+//   lengths; with more entries tiles are numbered as first_tile has it, and 64 bounds are
+//   compared at a time.
+__device__ __forceinline__ bool find_work(const Ragged &r, int rows, uint32_t w, uint32_t many, uint32_t *which, int *part, int64_t *tile)
 {
+    if (r.entries <= 62) {
+        const int p = (int)lane_id();
+        const int64_t len = p <= r.entries + 1 ? (r.bound(p + 1) - r.bound(p)) * r.mult : 0;
+        const uint32_t count = len > 0 ? (uint32_t)((len + rows - 1) / rows) : 0;
+        uint32_t sum = count;
+#pragma unroll
+        for (int o = 1; o < 64; o <<= 1) {
+            const uint32_t y = __shfl_up(sum, o, 64);
+            if (p >= o) sum += y;
+        }
+        const uint32_t total = __builtin_amdgcn_readlane(sum, 63);
+        if (total == 0 || w >= (uint64_t)total * many) return false;
+        *which = w / total;
+        const uint32_t slot = w - *which * total;
+        const int at = __builtin_ctzll(__ballot(sum > slot));
+        *part = at;
+        *tile = slot - (__builtin_amdgcn_readlane(sum, at) - __builtin_amdgcn_readlane(count, at));
+        return true;
+    }
+    const uint32_t slots = (uint32_t)(r.n * r.mult / rows + r.entries + 2);
+    *which = w / slots;
+    if (*which >= many) return false;
+    const uint32_t slot = w - *which * slots;
     int lo = 0, hi = r.entries + 2;
     while (hi - lo > 1) {
         const int step = (hi - lo + 63) / 64;
@@ -72,6 +100,7 @@ __device__ __forceinline__ void find_tile(const Ragged &r, int rows, int64_t slo
     }
     *part = __builtin_amdgcn_readfirstlane(lo);
     *tile = slot - r.first_tile(*part, rows);
+    return true;
 }
 
 // The part that holds a row (mult = 1).
@@ -90,10 +119,10 @@ __device__ __forceinline__ int find_part(const Ragged &r, int64_t row)
     return __builtin_amdgcn_readfirstlane(lo);
 }
 
-// Work number of a block: runs of 16 go to one XCD (blocks are dealt to the 8 XCDs in
+// Work number of a block: runs of 4 go to one XCD (blocks are dealt to the 8 XCDs in
 // turn), so that neighbours, which read the same keys, share an L2.  Grids are whole
-// multiples of 128; numbers past the work are idle.
-constexpr int XCD_RUN = 16;
+// multiples of 32; numbers past the work are idle.
+constexpr int XCD_RUN = 4;
 static inline unsigned xcd_grid(int64_t total) { return (unsigned)((total + 8 * XCD_RUN - 1) / (8 * XCD_RUN) * (8 * XCD_RUN)); }
 __device__ __forceinline__ unsigned xcd_work()
 {
@@ -364,6 +393,14 @@ __device__ __forceinline__ Raw16 rows_piece(const RowsAddr<uint16_t, RB> &ad, ui
     return Raw16{lo[0], lo[1], hi[0], hi[1]};
 }
 
+// The transposed operand of the rows of result register x / DB and elements 32 (x % DB) .. + 31.
+template <int RB>
+__device__ __forceinline__ float rows_piece(const RowsAddr<float, RB> &ad, uint32_t at, int x)
+{
+    const int i = x / (RB / 128), db = x % (RB / 128);
+    return *(const SC_LDS float *)(uintptr_t)(ad.at[i & 7][db] + at + 16 * (i >> 3) * RB);
+}
+
 // acc[x][db] += transpose(32 tile rows) p[x], for every 32 elements db of the head; `at` is
 // added to the addresses.
 template <int RB, int N>
@@ -387,7 +424,7 @@ __device__ __forceinline__ void mma_rows(const RowsAddr<float, RB> &ad, uint32_t
     for (int i = 0; i < 16; ++i)
 #pragma unroll
         for (int db = 0; db < RB / 128; ++db) {
-            const float v = *(const SC_LDS float *)(uintptr_t)(ad.at[i & 7][db] + at + 16 * (i >> 3) * RB);
+            const float v = rows_piece<RB>(ad, at, i * (RB / 128) + db);
 #pragma unroll
             for (int x = 0; x < N; ++x) acc[x][db] = __builtin_amdgcn_mfma_f32_32x32x2f32(v, p[x].v[i], acc[x][db], 0, 0, 0);
         }

@@ -83,21 +83,18 @@ __global__ __launch_bounds__(64 * FWD_WAVES, DP * sizeof(T) > 256 ? 1 : DP * siz
     const uint32_t lds = (uint32_t)(uintptr_t)(SC_LDS char *)smem;
 
     const Ragged rq = {A.q_off, A.entries, A.nq, A.group}, rk = {A.k_off, A.entries, A.nk, 1};
-    int part, hk;
+    int part;
+    uint32_t which;
     int64_t qtile, key0 = 0, split = 0;
     if constexpr (SPLIT) {
-        const int64_t slots = A.nk / A.chunk + A.entries + 2, w = xcd_work();
-        if (w >= slots * A.kv_heads * A.tiles) return;
-        hk = (int)(w / (slots * A.tiles));
-        qtile = w / slots % A.tiles;
-        find_tile(rk, A.chunk, w % slots, &part, &split);
+        if (!find_work(rk, A.chunk, xcd_work(), A.kv_heads * A.tiles, &which, &part, &split)) return;
         key0 = split * A.chunk;
+        qtile = which % A.tiles;
+        which /= A.tiles;
     } else {
-        const int64_t slots = A.nq * A.group / ROWS + A.entries + 2, w = xcd_work();
-        if (w >= slots * A.kv_heads) return;
-        hk = (int)(w / slots);
-        find_tile(rq, ROWS, w % slots, &part, &qtile);
+        if (!find_work(rq, ROWS, xcd_work(), A.kv_heads, &which, &part, &qtile)) return;
     }
+    const int hk = (int)which;
     const int64_t q_beg = rq.bound(part), k_beg = rk.bound(part);
     const bool real = part >= 1 && part <= A.entries;
     const int64_t rows = (rq.bound(part + 1) - q_beg) * A.group;
@@ -277,11 +274,39 @@ __global__ __launch_bounds__(64 * FWD_WAVES, DP * sizeof(T) > 256 ? 1 : DP * siz
                     __builtin_amdgcn_sched_barrier(0);
                 }
             } else {
-                scores(n, kat);
-                weights(t, 0, 16);
-                product(t, vat);
+                // the same; a weight is an operand as it is, so the second half is made as the product goes
+                constexpr int AHEAD = NJ < 2 ? NJ : 2, FAR = 8;
+                Raw16 k[NJ];
+                float v[16 * DB];
+#pragma unroll
+                for (int j = 0; j < AHEAD; ++j) k[j] = lds_read16(ka.at[j] + kat);
+                __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                for (int j = 0; j < NJ; ++j) {
+                    if (j + AHEAD < NJ) k[j + AHEAD] = lds_read16(ka.at[j + AHEAD] + kat);
+                    else {
+#pragma unroll
+                        for (int x = 0; x < FAR / AHEAD; ++x)
+                            v[(j + AHEAD - NJ) * (FAR / AHEAD) + x] = rows_piece<RB>(va, vat, (j + AHEAD - NJ) * (FAR / AHEAD) + x);
+                    }
+#pragma unroll
+                    for (int qb = 0; qb < QB; ++qb) n[qb] = mma_pieces<T>(k[j], q[qb][j], j ? n[qb] : f32x16{});
+                    weights(t, 8 * j / NJ, 8 * (j + 1) / NJ);
+                    __builtin_amdgcn_sched_barrier(0);
+                }
                 mask(n, u + 1);
-                maximum(n, top, 0, 16);
+#pragma unroll
+                for (int x = 0; x < 16 * DB; ++x) {
+                    const int i = x / DB, db = x % DB;
+                    if (x + FAR < 16 * DB) v[x + FAR] = rows_piece<RB>(va, vat, x + FAR);
+#pragma unroll
+                    for (int qb = 0; qb < QB; ++qb) o[qb][db] = __builtin_amdgcn_mfma_f32_32x32x2f32(v[x], t[qb][i], o[qb][db], 0, 0, 0);
+                    if (db == 0) {
+                        if (i < 8) weights(t, 8 + i, 9 + i);
+                        else maximum(n, top, 2 * (i - 8), 2 * (i - 8) + 2);
+                    }
+                    __builtin_amdgcn_sched_barrier(0);
+                }
             }
             settle(n, top);
             wait_copies_and_barrier<PER>();

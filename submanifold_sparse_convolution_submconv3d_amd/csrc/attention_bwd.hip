@@ -32,21 +32,18 @@ __global__ __launch_bounds__(64 * BWD_WAVES, DP * sizeof(T) > 256 ? 1 : 2) void 
     const uint32_t lds = (uint32_t)(uintptr_t)(SC_LDS char *)smem;
 
     const Ragged rq = {A.q_off, A.entries, A.nq, A.group}, rk = {A.k_off, A.entries, A.nk, 1};
-    int part, hk;
+    int part;
+    uint32_t which;
     int64_t qtile, key0 = 0, split = 0;
     if constexpr (SPLIT) {
-        const int64_t slots = A.nk / A.chunk + A.entries + 2, w = xcd_work();
-        if (w >= slots * A.kv_heads * A.tiles) return;
-        hk = (int)(w / (slots * A.tiles));
-        qtile = w / slots % A.tiles;
-        find_tile(rk, A.chunk, w % slots, &part, &split);
+        if (!find_work(rk, A.chunk, xcd_work(), A.kv_heads * A.tiles, &which, &part, &split)) return;
         key0 = split * A.chunk;
+        qtile = which % A.tiles;
+        which /= A.tiles;
     } else {
-        const int64_t slots = A.nq * A.group / BWD_ROWS + A.entries + 2, w = xcd_work();
-        if (w >= slots * A.kv_heads) return;
-        hk = (int)(w / slots);
-        find_tile(rq, BWD_ROWS, w % slots, &part, &qtile);
+        if (!find_work(rq, BWD_ROWS, xcd_work(), A.kv_heads, &which, &part, &qtile)) return;
     }
+    const int hk = (int)which;
     const int64_t q_beg = rq.bound(part), k_beg = rk.bound(part);
     const bool real = part >= 1 && part <= A.entries;
     const int64_t rows = (rq.bound(part + 1) - q_beg) * A.group;
@@ -175,8 +172,36 @@ __global__ __launch_bounds__(64 * BWD_WAVES, DP * sizeof(T) > 256 ? 1 : 2) void 
                     __builtin_amdgcn_sched_barrier(0);
                 }
             } else {
-                products(nt, ne, next_at);
-                gradient(t, e, own_at);
+                constexpr int AHEAD = NJ < 2 ? NJ : 2, FAR = 8;
+                Raw16 k[NJ], v[NJ];
+                float r[16 * DB];
+#pragma unroll
+                for (int j = 0; j < AHEAD; ++j) {
+                    k[j] = lds_read16(ka.at[j] + next_at);
+                    v[j] = lds_read16(ka.at[j] + next_at + V0);
+                }
+                __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                for (int j = 0; j < NJ; ++j) {
+                    if (j + AHEAD < NJ) {
+                        k[j + AHEAD] = lds_read16(ka.at[j + AHEAD] + next_at);
+                        v[j + AHEAD] = lds_read16(ka.at[j + AHEAD] + next_at + V0);
+                    } else {
+#pragma unroll
+                        for (int x = 0; x < FAR / AHEAD; ++x)
+                            r[(j + AHEAD - NJ) * (FAR / AHEAD) + x] = rows_piece<RB>(kt, own_at, (j + AHEAD - NJ) * (FAR / AHEAD) + x);
+                    }
+                    nt = mma_pieces<T>(k[j], q[j], j ? nt : f32x16{});
+                    ne = mma_pieces<T>(v[j], g[j], j ? ne : f32x16{});
+                    weigh(t, e, 16 * j / NJ, 16 * (j + 1) / NJ);
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+#pragma unroll
+                for (int x = 0; x < 16 * DB; ++x) {
+                    if (x + FAR < 16 * DB) r[x + FAR] = rows_piece<RB>(kt, own_at, x + FAR);
+                    dq[0][x % DB] = __builtin_amdgcn_mfma_f32_32x32x2f32(r[x], t[x / DB], dq[0][x % DB], 0, 0, 0);
+                    __builtin_amdgcn_sched_barrier(0);
+                }
             }
             mask(nt, u + 1);
             wait_copies_and_barrier<PER>();
@@ -225,21 +250,18 @@ __global__ __launch_bounds__(64 * BWD_WAVES, DP * sizeof(T) > 128 ? 1 : 2) void 
     const uint32_t lds = (uint32_t)(uintptr_t)(SC_LDS char *)smem;
 
     const Ragged rq = {A.q_off, A.entries, A.nq, A.group}, rk = {A.k_off, A.entries, A.nk, 1};
-    int part, hk;
+    int part;
+    uint32_t which;
     int64_t ktile, row0 = 0, split = 0;
     if constexpr (SPLIT) {
-        const int64_t slots = A.nq * A.group / A.chunk + A.entries + 2, w = xcd_work();
-        if (w >= slots * A.kv_heads * A.tiles) return;
-        hk = (int)(w / (slots * A.tiles));
-        ktile = w / slots % A.tiles;
-        find_tile(rq, A.chunk, w % slots, &part, &split);
+        if (!find_work(rq, A.chunk, xcd_work(), A.kv_heads * A.tiles, &which, &part, &split)) return;
         row0 = split * A.chunk;
+        ktile = which % A.tiles;
+        which /= A.tiles;
     } else {
-        const int64_t slots = A.nk / BWD_ROWS + A.entries + 2, w = xcd_work();
-        if (w >= slots * A.kv_heads) return;
-        hk = (int)(w / slots);
-        find_tile(rk, BWD_ROWS, w % slots, &part, &ktile);
+        if (!find_work(rk, BWD_ROWS, xcd_work(), A.kv_heads, &which, &part, &ktile)) return;
     }
+    const int hk = (int)which;
     const int64_t q_beg = rq.bound(part), k_beg = rk.bound(part);
     const bool real = part >= 1 && part <= A.entries;
     const int64_t keys = rk.bound(part + 1) - k_beg;
@@ -380,8 +402,43 @@ __global__ __launch_bounds__(64 * BWD_WAVES, DP * sizeof(T) > 128 ? 1 : 2) void 
                     __builtin_amdgcn_sched_barrier(0);
                 }
             } else {
-                products(nt, ne, next_at);
-                gradient(t, e, u, own_at);
+                constexpr int AHEAD = NJ < 2 ? NJ : 2, FAR = 8;
+                Raw16 a[NJ], b[NJ];
+                float r[32 * DB];
+                f32x4 bd[8];
+                auto rows = [&](int x) { return rows_piece<RB>(qt, own_at + (x < 16 * DB ? G0 : 0), x % (16 * DB)); };
+#pragma unroll
+                for (int i = 0; i < 8; ++i) bd[i] = stats(u, 2 * i);
+#pragma unroll
+                for (int j = 0; j < AHEAD; ++j) {
+                    a[j] = lds_read16(qa.at[j] + next_at);
+                    b[j] = lds_read16(qa.at[j] + next_at + G0);
+                }
+                __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                for (int j = 0; j < NJ; ++j) {
+                    if (j + AHEAD < NJ) {
+                        a[j + AHEAD] = lds_read16(qa.at[j + AHEAD] + next_at);
+                        b[j + AHEAD] = lds_read16(qa.at[j + AHEAD] + next_at + G0);
+                    } else {
+#pragma unroll
+                        for (int x = 0; x < FAR / AHEAD; ++x)
+                            r[(j + AHEAD - NJ) * (FAR / AHEAD) + x] = rows((j + AHEAD - NJ) * (FAR / AHEAD) + x);
+                    }
+                    nt = mma_pieces<T>(a[j], k[j], j ? nt : f32x16{});
+                    ne = mma_pieces<T>(b[j], v[j], j ? ne : f32x16{});
+#pragma unroll
+                    for (int i = 8 * j / NJ; i < 8 * (j + 1) / NJ; ++i) weigh(t, e, 2 * i, bd[i]);
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+#pragma unroll
+                for (int x = 0; x < 32 * DB; ++x) {
+                    if (x + FAR < 32 * DB) r[x + FAR] = rows(x + FAR);
+                    const int y = x % (16 * DB);
+                    f32x16 &d = x < 16 * DB ? dv[0][y % DB] : dk[0][y % DB];
+                    d = __builtin_amdgcn_mfma_f32_32x32x2f32(r[x], x < 16 * DB ? t[y / DB] : e[y / DB], d, 0, 0, 0);
+                    __builtin_amdgcn_sched_barrier(0);
+                }
             }
             wait_copies_and_barrier<PER>();
         };
