@@ -56,50 +56,97 @@ struct Ragged {
 
 static inline int64_t ragged_tiles(int64_t n, int entries, int mult, int rows) { return n * mult / rows + entries + 2; }
 
-// What work number w is: work is all tiles of all parts, once for each of `many` (heads,
-// and tiles of the other side), whose number comes in *which.  False past the end.  The
-// same in all lanes.
-//   Up to 62 entries a lane counts the tiles of a part and a sum over lanes numbers them
-//   without gaps, so that the blocks with work spread evenly over the card whatever the
-//   lengths; with more entries tiles are numbered as first_tile has it, and 64 bounds are
-//   compared at a time.
-__device__ __forceinline__ bool find_work(const Ragged &r, int rows, uint32_t w, uint32_t many, uint32_t *which, int *part, int64_t *tile)
+// A block's share: tile `tile` of a part's rows on its own side, for `which` of the heads (and
+// tiles of the other side); where the part lies on both sides, in rows.  `real`: the part is
+// an entry.
+struct Work {
+    uint32_t which;
+    bool real;
+    int64_t tile, own_beg, own_len, other_beg, other_len;
+};
+
+// What work number w is: work is all tiles of all parts, `many` times over.  False past the
+// end.  The same in all lanes.
+//   Up to 254 entries each lane counts the tiles of its EACH parts and a sum over lanes numbers
+//   them without gaps, so that the blocks with work spread evenly over the card whatever
+//   the lengths, and the bounds come with one memory latency; with more entries tiles are
+//   numbered as first_tile has it, and 64 bounds are compared at a time.
+constexpr int EACH = 4;
+__device__ __forceinline__ bool find_work(const Ragged &own, const Ragged &other, int rows, uint32_t w, uint32_t many, Work *k)
 {
-    if (r.entries <= 62) {
-        const int p = (int)lane_id();
-        const int64_t len = p <= r.entries + 1 ? (r.bound(p + 1) - r.bound(p)) * r.mult : 0;
-        const uint32_t count = len > 0 ? (uint32_t)((len + rows - 1) / rows) : 0;
+    const int parts = own.entries + 2, lane = (int)lane_id();
+    int part;
+    if (parts <= 64 * EACH) {
+        const int each = (parts + 63) / 64, p0 = lane * each;
+        int64_t b[EACH + 1], ob[EACH + 1];
+#pragma unroll
+        for (int i = 0; i <= EACH; ++i) {
+            const int p = p0 + (i < each ? i : each);
+            b[i] = own.bound(p < parts ? p : parts);
+            ob[i] = other.bound(p < parts ? p : parts);
+        }
+        uint32_t tiles[EACH], count = 0;
+#pragma unroll
+        for (int i = 0; i < EACH; ++i) {
+            const int64_t len = (b[i + 1] - b[i]) * own.mult;  // 0 past the lane's parts
+            tiles[i] = len > 0 ? (uint32_t)((len + rows - 1) / rows) : 0;
+            count += tiles[i];
+        }
         uint32_t sum = count;
 #pragma unroll
         for (int o = 1; o < 64; o <<= 1) {
             const uint32_t y = __shfl_up(sum, o, 64);
-            if (p >= o) sum += y;
+            if (lane >= o) sum += y;
         }
         const uint32_t total = __builtin_amdgcn_readlane(sum, 63);
         if (total == 0 || w >= (uint64_t)total * many) return false;
-        *which = w / total;
-        const uint32_t slot = w - *which * total;
+        k->which = w / total;
+        const uint32_t slot = w - k->which * total;
         const int at = __builtin_ctzll(__ballot(sum > slot));
-        *part = at;
-        *tile = slot - (__builtin_amdgcn_readlane(sum, at) - __builtin_amdgcn_readlane(count, at));
-        return true;
+        uint32_t tile = slot - (sum - count);  // meant in lane `at`
+        int64_t beg = b[0], end = b[1], obeg = ob[0], oend = ob[1];
+        part = p0;
+#pragma unroll
+        for (int i = 1; i < EACH; ++i)  // which of the lane's parts
+            if (part == p0 + i - 1 && tile >= tiles[i - 1]) {
+                tile -= tiles[i - 1];
+                part = p0 + i;
+                beg = b[i];
+                end = b[i + 1];
+                obeg = ob[i];
+                oend = ob[i + 1];
+            }
+        part = __builtin_amdgcn_readlane(part, at);
+        k->tile = (uint32_t)__builtin_amdgcn_readlane(tile, at);
+        k->own_beg = __builtin_amdgcn_readlane((int)beg, at);
+        k->own_len = __builtin_amdgcn_readlane((int)end, at) - k->own_beg;
+        k->other_beg = __builtin_amdgcn_readlane((int)obeg, at);
+        k->other_len = __builtin_amdgcn_readlane((int)oend, at) - k->other_beg;
+    } else {
+        const uint32_t slots = (uint32_t)(own.n * own.mult / rows + own.entries + 2);
+        k->which = w / slots;
+        if (k->which >= many) return false;
+        const uint32_t slot = w - k->which * slots;
+        int lo = 0, hi = parts;
+        while (hi - lo > 1) {
+            const int step = (hi - lo + 63) / 64;
+            const int p = lo + lane * step;
+            const uint64_t le = __ballot(p < hi && own.first_tile(p, rows) <= slot);
+            const int count = ~le ? __builtin_ctzll(~le) : 64;
+            const int next = lo + (count > 1 ? count - 1 : 0) * step;
+            hi = next + step < hi ? next + step : hi;
+            lo = next;
+        }
+        part = __builtin_amdgcn_readfirstlane(lo);
+        k->tile = slot - own.first_tile(part, rows);
+        k->own_beg = own.bound(part);
+        k->own_len = own.bound(part + 1) - k->own_beg;
+        k->other_beg = other.bound(part);
+        k->other_len = other.bound(part + 1) - k->other_beg;
     }
-    const uint32_t slots = (uint32_t)(r.n * r.mult / rows + r.entries + 2);
-    *which = w / slots;
-    if (*which >= many) return false;
-    const uint32_t slot = w - *which * slots;
-    int lo = 0, hi = r.entries + 2;
-    while (hi - lo > 1) {
-        const int step = (hi - lo + 63) / 64;
-        const int p = lo + (int)lane_id() * step;
-        const uint64_t le = __ballot(p < hi && r.first_tile(p, rows) <= slot);
-        const int count = ~le ? __builtin_ctzll(~le) : 64;
-        const int next = lo + (count > 1 ? count - 1 : 0) * step;
-        hi = next + step < hi ? next + step : hi;
-        lo = next;
-    }
-    *part = __builtin_amdgcn_readfirstlane(lo);
-    *tile = slot - r.first_tile(*part, rows);
+    if (k->own_len < 0) k->own_len = 0;
+    k->real = part >= 1 && part <= own.entries;
+    if (!k->real || k->other_len < 0) k->other_len = 0;
     return true;
 }
 

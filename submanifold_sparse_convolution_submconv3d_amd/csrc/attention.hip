@@ -83,25 +83,24 @@ __global__ __launch_bounds__(64 * FWD_WAVES, DP * sizeof(T) > 256 ? 1 : DP * siz
     const uint32_t lds = (uint32_t)(uintptr_t)(SC_LDS char *)smem;
 
     const Ragged rq = {A.q_off, A.entries, A.nq, A.group}, rk = {A.k_off, A.entries, A.nk, 1};
-    int part;
-    uint32_t which;
+    Work w;
     int64_t qtile, key0 = 0, split = 0;
     if constexpr (SPLIT) {
-        if (!find_work(rk, A.chunk, xcd_work(), A.kv_heads * A.tiles, &which, &part, &split)) return;
+        if (!find_work(rk, rq, A.chunk, xcd_work(), A.kv_heads * A.tiles, &w) || !w.real) return;
+        split = w.tile;
         key0 = split * A.chunk;
-        qtile = which % A.tiles;
-        which /= A.tiles;
+        qtile = w.which % A.tiles;
+        w.which /= A.tiles;
     } else {
-        if (!find_work(rq, ROWS, xcd_work(), A.kv_heads, &which, &part, &qtile)) return;
+        if (!find_work(rq, rk, ROWS, xcd_work(), A.kv_heads, &w)) return;
+        qtile = w.tile;
     }
-    const int hk = (int)which;
-    const int64_t q_beg = rq.bound(part), k_beg = rk.bound(part);
-    const bool real = part >= 1 && part <= A.entries;
-    const int64_t rows = (rq.bound(part + 1) - q_beg) * A.group;
-    int64_t keys64 = real ? rk.bound(part + 1) - k_beg - key0 : 0;
-    if (SPLIT && (keys64 <= 0 || !real)) return;
+    const int hk = (int)w.which;
+    const int64_t q_beg = SPLIT ? w.other_beg : w.own_beg, k_beg = SPLIT ? w.own_beg : w.other_beg;
+    const int64_t rows = (SPLIT ? w.other_len : w.own_len) * A.group;
+    int64_t keys64 = (SPLIT ? w.own_len : w.other_len) - key0;
     if (SPLIT && keys64 > A.chunk) keys64 = A.chunk;
-    const int keys = keys64 < 0 ? 0 : (int)keys64, steps = (keys + 31) / 32;
+    const int keys = (int)keys64, steps = (keys + 31) / 32;
 
     const int lane = lane_id(), half = lane >> 5;
     const float c = A.scale * LOG2E;
@@ -378,70 +377,68 @@ VARIANTS(uint16_t, 128, true)
 VARIANTS(uint16_t, 128, false)
 #undef VARIANTS
 
-// One block to a query row: the splits' sums joined in order of their number.
-constexpr int JOIN_MAX_SPLITS = 2048;
+// The splits' sums of a query row joined, in a fixed order, by A.tiles of a block's four
+// waves (four rows a block, or one where there are many splits).
+constexpr int JOIN_MAX_SPLITS = 2048, JOIN_WAVES = 4, JOIN_WAVE_SPLITS = 64;
 template <typename T>
-__global__ __launch_bounds__(256) void k_attn_join(AttnArgs A)
+__global__ __launch_bounds__(64 * JOIN_WAVES) void k_attn_join(AttnArgs A)
 {
-    __shared__ float w[JOIN_MAX_SPLITS];
-    __shared__ float red[4];
-    __shared__ f32x4 acc[256];
-    const int64_t at = blockIdx.x, token = at / A.heads;
+    __shared__ f32x4 acc[JOIN_WAVES][64];
+    __shared__ float part_l[JOIN_WAVES], weights[JOIN_MAX_SPLITS];
+    const int lane = lane_id(), wave = threadIdx.x >> 6, mine = wave % A.tiles, first = wave - mine;
+    const int64_t rows = A.nq * A.heads, at = (int64_t)blockIdx.x * (JOIN_WAVES / A.tiles) + wave / A.tiles;
+    const bool on = at < rows;
+    const int64_t token = on ? at / A.heads : 0;
     const int head = (int)(at - token * A.heads);
     const Ragged rq = {A.q_off, A.entries, A.nq, 1}, rk = {A.k_off, A.entries, A.nk, 1};
     const int part = find_part(rq, token);
     const bool real = part >= 1 && part <= A.entries;
-    const int64_t keys = real ? rk.bound(part + 1) - rk.bound(part) : 0;
+    const int64_t keys = real && on ? rk.bound(part + 1) - rk.bound(part) : 0;
     const int n = keys > 0 ? (int)((keys + A.chunk - 1) / A.chunk) : 0;
-    const int64_t rows = A.nq * A.heads;
     const float c = A.scale * LOG2E;
 
     float top = -INFINITY;
-    for (int s = threadIdx.x; s < n; s += 256) top = fmaxf(top, A.part2[2 * (s * rows + at)]);
+    for (int s = lane; s < n; s += 64) top = fmaxf(top, A.part2[2 * (s * rows + at)]);
 #pragma unroll
     for (int o = 32; o; o >>= 1) top = fmaxf(top, __shfl_xor(top, o, 64));
-    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = top;
-    __syncthreads();
-    top = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
-    __syncthreads();
-    float l = 0.0f;
-    for (int s = threadIdx.x; s < n; s += 256) {
+    float l = 0.0f, *weight = weights + (A.tiles == 1 ? wave * JOIN_WAVE_SPLITS : 0);
+    for (int s = lane + 64 * mine; s < n; s += 64 * A.tiles) {
         const float2 ml = *(const float2 *)(A.part2 + 2 * (s * rows + at));
-        const float f = rescale(ml.x, top, c);
-        w[s] = f;
-        l += ml.y * f;
+        weight[s] = rescale(ml.x, top, c);
+        l += ml.y * weight[s];
+    }
+    __syncthreads();
+    const int pieces = A.dim / 4, groups = 64 / pieces, g = lane / pieces, e = lane % pieces;
+    f32x4 sum = {0, 0, 0, 0};
+    if (g < groups) {
+#pragma unroll 8
+        for (int s = g + groups * mine; s < n; s += groups * A.tiles)
+            sum += *(const f32x4 *)(A.part + (s * rows + at) * A.dim + 4 * e) * weight[s];
     }
     l = lanes_sum<64>(l);
-    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = l;
+    acc[wave][lane] = sum;
+    if (lane == 0) part_l[wave] = l;
     __syncthreads();
-    l = (red[0] + red[1]) + (red[2] + red[3]);
-
-    const int pieces = A.dim / 4, groups = 256 / pieces, g = threadIdx.x / pieces, e = threadIdx.x % pieces;
-    f32x4 sum = {0, 0, 0, 0};
-    if (g < groups)
-        for (int s = g; s < n; s += groups) sum += *(const f32x4 *)(A.part + (s * rows + at) * A.dim + 4 * e) * w[s];
-    acc[threadIdx.x] = sum;
-    __syncthreads();
-    if (g == 0) {
-        for (int i = 1; i < groups; ++i) sum += acc[i * pieces + e];
-        sum *= l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);
-        T *op = (T *)A.out.p + token * A.out.row + head * A.out.head + 4 * e;
-        if constexpr (sizeof(T) == 2) {
-            const uint32_t a = pack_bf16(sum[0], sum[1]), b = pack_bf16(sum[2], sum[3]);
-            op[0] = (uint16_t)a;
-            op[1] = (uint16_t)(a >> 16);
-            op[2] = (uint16_t)b;
-            op[3] = (uint16_t)(b >> 16);
-        } else {
-            *(Raw16Any *)op = __builtin_bit_cast(Raw16, sum);
-        }
-        if (A.lse && e == 0) A.lse[at] = log_sum(top, l, A.scale);
+    if (!on || mine || g) return;
+    for (int i = 1; i < groups * A.tiles; ++i) sum += acc[first + i / groups][i % groups * pieces + e];
+    for (int i = 1; i < A.tiles; ++i) l += part_l[first + i];
+    sum *= l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);
+    T *op = (T *)A.out.p + token * A.out.row + head * A.out.head + 4 * e;
+    if constexpr (sizeof(T) == 2) {
+        const uint32_t a = pack_bf16(sum[0], sum[1]), b = pack_bf16(sum[2], sum[3]);
+        op[0] = (uint16_t)a;
+        op[1] = (uint16_t)(a >> 16);
+        op[2] = (uint16_t)b;
+        op[3] = (uint16_t)(b >> 16);
+    } else {
+        *(Raw16Any *)op = __builtin_bit_cast(Raw16, sum);
     }
+    if (A.lse && e == 0) A.lse[at] = log_sum(top, l, A.scale);
 }
 
 // How a pass over a long side is split when its own side has few tiles: enough runs that
 // all blocks together fill the card, none shorter than MIN_CHUNK rows.  chunk = 0: not at all.
-constexpr int64_t WANT_BLOCKS = 768, MIN_CHUNK = 256;
+constexpr int64_t WANT_BLOCKS = 768, MIN_CHUNK = 64;
 
 SplitPlan split_plan(int64_t own_rows, int own_tile, int64_t other_rows, int other_tile, int entries, int kv_heads)
 {
@@ -494,7 +491,9 @@ static int run_fwd(AttnArgs A, const SplitPlan &p, void *workspace, hipStream_t 
         const int64_t work = ragged_tiles(A.nk, A.entries, 1, p.chunk) * A.kv_heads * p.tiles;
         hipLaunchKernelGGL((k_attn<T, DP, true, DIRECT>), dim3(xcd_grid(work)), block, 0, st, A);
         SC_LAUNCHED("attention (split)");
-        hipLaunchKernelGGL((k_attn_join<T>), dim3((unsigned)(A.nq * A.heads)), dim3(256), 0, st, A);
+        A.tiles = p.splits > JOIN_WAVE_SPLITS ? JOIN_WAVES : 1;
+        const int64_t per = JOIN_WAVES / A.tiles;
+        hipLaunchKernelGGL((k_attn_join<T>), dim3((unsigned)((A.nq * A.heads + per - 1) / per)), dim3(64 * JOIN_WAVES), 0, st, A);
         SC_LAUNCHED("attention join");
         return SUBMCONV_OK;
     }

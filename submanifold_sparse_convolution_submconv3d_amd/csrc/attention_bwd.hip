@@ -32,25 +32,24 @@ __global__ __launch_bounds__(64 * BWD_WAVES, DP * sizeof(T) > 256 ? 1 : 2) void 
     const uint32_t lds = (uint32_t)(uintptr_t)(SC_LDS char *)smem;
 
     const Ragged rq = {A.q_off, A.entries, A.nq, A.group}, rk = {A.k_off, A.entries, A.nk, 1};
-    int part;
-    uint32_t which;
+    Work w;
     int64_t qtile, key0 = 0, split = 0;
     if constexpr (SPLIT) {
-        if (!find_work(rk, A.chunk, xcd_work(), A.kv_heads * A.tiles, &which, &part, &split)) return;
+        if (!find_work(rk, rq, A.chunk, xcd_work(), A.kv_heads * A.tiles, &w) || !w.real) return;
+        split = w.tile;
         key0 = split * A.chunk;
-        qtile = which % A.tiles;
-        which /= A.tiles;
+        qtile = w.which % A.tiles;
+        w.which /= A.tiles;
     } else {
-        if (!find_work(rq, BWD_ROWS, xcd_work(), A.kv_heads, &which, &part, &qtile)) return;
+        if (!find_work(rq, rk, BWD_ROWS, xcd_work(), A.kv_heads, &w)) return;
+        qtile = w.tile;
     }
-    const int hk = (int)which;
-    const int64_t q_beg = rq.bound(part), k_beg = rk.bound(part);
-    const bool real = part >= 1 && part <= A.entries;
-    const int64_t rows = (rq.bound(part + 1) - q_beg) * A.group;
-    int64_t keys64 = real ? rk.bound(part + 1) - k_beg - key0 : 0;
-    if (SPLIT && (keys64 <= 0 || !real)) return;
+    const int hk = (int)w.which;
+    const int64_t q_beg = SPLIT ? w.other_beg : w.own_beg, k_beg = SPLIT ? w.own_beg : w.other_beg;
+    const int64_t rows = (SPLIT ? w.other_len : w.own_len) * A.group;
+    int64_t keys64 = (SPLIT ? w.own_len : w.other_len) - key0;
     if (SPLIT && keys64 > A.chunk) keys64 = A.chunk;
-    const int keys = keys64 < 0 ? 0 : (int)keys64, steps = (keys + 31) / 32;
+    const int keys = (int)keys64, steps = (keys + 31) / 32;
 
     const int lane = lane_id(), half = lane >> 5;
     const float c = A.scale * LOG2E;
@@ -250,25 +249,24 @@ __global__ __launch_bounds__(64 * BWD_WAVES, DP * sizeof(T) > 128 ? 1 : 2) void 
     const uint32_t lds = (uint32_t)(uintptr_t)(SC_LDS char *)smem;
 
     const Ragged rq = {A.q_off, A.entries, A.nq, A.group}, rk = {A.k_off, A.entries, A.nk, 1};
-    int part;
-    uint32_t which;
+    Work w;
     int64_t ktile, row0 = 0, split = 0;
     if constexpr (SPLIT) {
-        if (!find_work(rq, A.chunk, xcd_work(), A.kv_heads * A.tiles, &which, &part, &split)) return;
+        if (!find_work(rq, rk, A.chunk, xcd_work(), A.kv_heads * A.tiles, &w) || !w.real) return;
+        split = w.tile;
         row0 = split * A.chunk;
-        ktile = which % A.tiles;
-        which /= A.tiles;
+        ktile = w.which % A.tiles;
+        w.which /= A.tiles;
     } else {
-        if (!find_work(rk, BWD_ROWS, xcd_work(), A.kv_heads, &which, &part, &ktile)) return;
+        if (!find_work(rk, rq, BWD_ROWS, xcd_work(), A.kv_heads, &w)) return;
+        ktile = w.tile;
     }
-    const int hk = (int)which;
-    const int64_t q_beg = rq.bound(part), k_beg = rk.bound(part);
-    const bool real = part >= 1 && part <= A.entries;
-    const int64_t keys = rk.bound(part + 1) - k_beg;
-    int64_t rows64 = real ? (rq.bound(part + 1) - q_beg) * A.group - row0 : 0;
-    if (SPLIT && (rows64 <= 0 || !real)) return;
+    const int hk = (int)w.which;
+    const int64_t q_beg = SPLIT ? w.own_beg : w.other_beg, k_beg = SPLIT ? w.other_beg : w.own_beg;
+    const int64_t keys = SPLIT ? w.other_len : w.own_len;
+    int64_t rows64 = (SPLIT ? w.own_len : w.other_len) * A.group - row0;
     if (SPLIT && rows64 > A.chunk) rows64 = A.chunk;
-    const int rows = rows64 < 0 ? 0 : (int)rows64, steps = (rows + 31) / 32;
+    const int rows = (int)rows64, steps = (rows + 31) / 32;
 
     const int lane = lane_id(), half = lane >> 5, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const float c = A.scale * LOG2E;
@@ -497,11 +495,16 @@ VARIANTS(uint16_t, 128, false)
 #undef VARIANTS
 
 // One block to an output row: the splits' partial gradients of an [n, heads, dim] tensor
-// summed in order of their number and scaled.  `other` is the side that was split.
+// summed in order of their number and scaled, for one or two such tensors (blockIdx.y).
+// `other` is the side that was split.
 template <typename T>
 __global__ __launch_bounds__(256) void k_attn_sum(Ragged own, Ragged other, int heads, int dim, int chunk,
-                                                  const float *__restrict__ part, float scale, Heads out)
+                                                  const float *__restrict__ part_a, float scale_a, Heads out_a,
+                                                  const float *__restrict__ part_b, float scale_b, Heads out_b)
 {
+    const float *part = blockIdx.y ? part_b : part_a;
+    const float scale = blockIdx.y ? scale_b : scale_a;
+    const Heads out = blockIdx.y ? out_b : out_a;
     __shared__ f32x4 acc[256];
     const int64_t at = blockIdx.x, row = at / heads;
     const int head = (int)(at - row * heads), p = find_part(own, row);
@@ -572,7 +575,7 @@ static int run_bwd(AttnArgs A, const BwdPlan &p, hipStream_t st)
             hipLaunchKernelGGL((k_attn_dq<T, DP, true, DIRECT>), dim3(xcd_grid(work)), block, 0, st, A);
             SC_LAUNCHED("attention_backward queries (split)");
             hipLaunchKernelGGL(k_attn_sum<T>, dim3((unsigned)(A.nq * A.heads)), dim3(256), 0, st, rq, rk, A.heads, A.dim,
-                               A.chunk, A.part, A.scale, A.dq);
+                               A.chunk, A.part, A.scale, A.dq, nullptr, 0.0f, Heads{});
         } else {
             const int64_t work = ragged_tiles(A.nq, A.entries, A.group, BWD_ROWS) * A.kv_heads;
             hipLaunchKernelGGL((k_attn_dq<T, DP, false, DIRECT>), dim3(xcd_grid(work)), block, 0, st, A);
@@ -587,11 +590,8 @@ static int run_bwd(AttnArgs A, const BwdPlan &p, hipStream_t st)
             hipLaunchKernelGGL((k_attn_dkv<T, DP, true, DIRECT>), dim3(xcd_grid(work)), block, 0, st, A);
             SC_LAUNCHED("attention_backward keys (split)");
             const Ragged rows = {A.q_off, A.entries, A.nq, A.group};
-            const dim3 grid((unsigned)(A.nk * A.kv_heads));
-            hipLaunchKernelGGL(k_attn_sum<T>, grid, dim3(256), 0, st, rk, rows, A.kv_heads, A.dim, A.chunk, A.part,
-                               A.scale, A.dk);
-            hipLaunchKernelGGL(k_attn_sum<T>, grid, dim3(256), 0, st, rk, rows, A.kv_heads, A.dim, A.chunk, A.part2,
-                               1.0f, A.dv);
+            hipLaunchKernelGGL(k_attn_sum<T>, dim3((unsigned)(A.nk * A.kv_heads), 2), dim3(256), 0, st, rk, rows, A.kv_heads,
+                               A.dim, A.chunk, A.part, A.scale, A.dk, A.part2, 1.0f, A.dv);
         } else {
             const int64_t work = ragged_tiles(A.nk, A.entries, 1, BWD_ROWS) * A.kv_heads;
             hipLaunchKernelGGL((k_attn_dkv<T, DP, false, DIRECT>), dim3(xcd_grid(work)), block, 0, st, A);
