@@ -1,0 +1,159 @@
+"""Refusals of the transformer-block entry points: every bad size, type, pointer, distance or
+overlap comes back as a status before any HIP call.  CPU only; pointers are never read."""
+import ctypes
+
+import pytest
+import torch
+
+import submanifold_sparse_convolution_submconv3d_amd as sc
+
+E_INVALID_ARG, E_UNSUPPORTED, E_ALIAS = -1, -4, -5
+P = lambda i: ctypes.c_void_p(i << 32)  # noqa: E731  (addresses 4 GiB apart)
+
+
+@pytest.fixture(scope="module")
+def lib():
+    return sc.load_library()
+
+
+def norm(lib, x=P(1), x_row=64, n=10, c=64, dtype=0, w=P(2), b=P(3), pdtype=0, eps=1e-5, y=P(4), y_row=64, stats=P(5)):
+    return lib.submconv_layer_norm(x, x_row, n, c, dtype, w, b, pdtype, eps, y, y_row, stats, None)
+
+
+def test_layer_norm_refusals(lib):
+    assert norm(lib, n=0) == 0 and norm(lib, n=0, x=None, y=None) == 0
+    for bad in (dict(n=-1), dict(n=1 << 31), dict(x=None), dict(y=None), dict(y_row=63), dict(x_row=-1), dict(x_row=(1 << 24) + 1),
+                dict(eps=-1.0), dict(eps=float("nan")), dict(x=ctypes.c_void_p(0x1002)), dict(stats=ctypes.c_void_p(0x1004)),
+                dict(w=ctypes.c_void_p(0x1002))):
+        assert norm(lib, **bad) == E_INVALID_ARG, bad
+    for bad in (dict(c=0), dict(c=8193, x_row=8193, y_row=8193), dict(dtype=2), dict(pdtype=-1)):
+        assert norm(lib, **bad) == E_UNSUPPORTED, bad
+    for bad in (dict(y=ctypes.c_void_p((1 << 32) + 4)), dict(y=P(1), y_row=65), dict(y=P(2)), dict(y=P(3)), dict(stats=P(1)),
+                dict(stats=P(4)), dict(stats=P(2))):
+        assert norm(lib, **bad) == E_ALIAS, bad
+    # columns of one wider tensor interleave without overlap, next to and not into each other
+    assert norm(lib, n=0, y=ctypes.c_void_p((1 << 32) + 256), x_row=128, y_row=128) == 0
+    assert norm(lib, y=ctypes.c_void_p((1 << 32) + 252), x_row=128, y_row=128) == E_ALIAS
+
+
+def norm_bwd(lib, g=P(1), g_row=64, x=P(2), x_row=64, n=10, c=64, dtype=1, stats=P(3), w=P(4), pdtype=0, dx=P(5), dx_row=64,
+             dw=P(6), db=P(7), ws=P(8), nbytes=1 << 20):
+    return lib.submconv_layer_norm_backward(g, g_row, x, x_row, n, c, dtype, stats, w, pdtype, dx, dx_row, dw, db, ws, nbytes, None)
+
+
+def test_layer_norm_backward_refusals(lib):
+    need = lib.submconv_layer_norm_backward_workspace(10, 64, 1)
+    assert need > 0 and need % 4 == 0
+    assert lib.submconv_layer_norm_backward_workspace(-1, 64, 1) == 0
+    assert lib.submconv_layer_norm_backward_workspace(10, 9000, 1) == 0
+    assert norm_bwd(lib, n=0, dw=None, db=None, ws=None, nbytes=0) == 0
+    for bad in (dict(n=-1), dict(g=None), dict(x=None), dict(stats=None), dict(dx=None), dict(dx_row=63), dict(g_row=-1),
+                dict(ws=None), dict(nbytes=need - 1), dict(ws=ctypes.c_void_p(0x1008))):
+        assert norm_bwd(lib, **bad) == E_INVALID_ARG, bad
+    for bad in (dict(c=0), dict(dtype=3), dict(pdtype=7)):
+        assert norm_bwd(lib, **bad) == E_UNSUPPORTED, bad
+    for bad in (dict(dx=P(2)), dict(dx=P(1), dx_row=80), dict(dw=P(4)), dict(db=P(6)), dict(ws=P(5)), dict(ws=P(2))):
+        assert norm_bwd(lib, **bad) == E_ALIAS, bad
+
+
+def rotary(lib, x=P(1), x_row=256, x_head=64, pos=P(2), pos_row=4, freqs=P(3), sections=(10, 10, 10), axes=3, n=10, heads=4, dim=64,
+           dtype=0, split=0, inverse=0, out=P(4), out_row=256, out_head=64):
+    s = None if sections is None else (ctypes.c_int32 * len(sections))(*sections)
+    return lib.submconv_rotary(x, x_row, x_head, pos, pos_row, freqs, s, axes, n, heads, dim, dtype, split, inverse, out, out_row,
+                               out_head, None)
+
+
+def test_rotary_refusals(lib):
+    assert rotary(lib, n=0) == 0
+    for bad in (dict(n=-1), dict(x=None), dict(out=None), dict(pos=None), dict(freqs=None), dict(sections=None), dict(split=2),
+                dict(inverse=-1), dict(sections=(10, -1, 3)), dict(sections=(11, 11, 11)), dict(pos_row=-1), dict(x_row=-4),
+                dict(out_row=255), dict(out_head=63), dict(out_row=0), dict(x=ctypes.c_void_p(0x1002)), dict(pos=ctypes.c_void_p(0x1002))):
+        assert rotary(lib, **bad) == E_INVALID_ARG, bad
+    for bad in (dict(dim=63), dict(dim=0), dict(dim=514, x_head=514, out_head=514), dict(heads=0), dict(heads=1025), dict(axes=0),
+                dict(sections=(1,) * 5, axes=5), dict(dtype=2)):
+        assert rotary(lib, **bad) == E_UNSUPPORTED, bad
+    for bad in (dict(out=ctypes.c_void_p((1 << 32) + 16)), dict(out=P(1), out_row=512), dict(out=P(2)), dict(out=P(3))):
+        assert rotary(lib, **bad) == E_ALIAS, bad
+
+
+SIZES = dict(entries=2, nq=100, nk=100, heads=4, kv_heads=2, dim=64, dtype=1)
+
+
+def attention(lib, q=P(1), k=P(2), v=P(3), strides=(256, 64, 128, 64, 128, 64, 256, 64), qo=P(4), ko=P(5), scale=0.125, out=P(6), lse=P(7),
+              ws=P(8), nbytes=0, **sizes):
+    s = {**SIZES, **sizes}
+    st = None if strides is None else (ctypes.c_int64 * 8)(*strides)
+    return lib.submconv_attention(q, k, v, st, qo, ko, s["entries"], s["nq"], s["nk"], s["heads"], s["kv_heads"], s["dim"], s["dtype"],
+                                  scale, out, lse, ws, nbytes, None)
+
+
+def test_attention_refusals(lib):
+    assert attention(lib, nq=0) == 0
+    for bad in (dict(entries=0), dict(entries=(1 << 20) + 1), dict(nq=-1), dict(nk=-1), dict(nq=1 << 30), dict(scale=0.0), dict(scale=-1.0),
+                dict(scale=float("inf")), dict(scale=float("nan")), dict(strides=None), dict(q=None), dict(k=None), dict(v=None),
+                dict(out=None), dict(qo=None), dict(ko=None), dict(q=ctypes.c_void_p(0x1001)), dict(ws=ctypes.c_void_p(0x1004)),
+                dict(strides=(256, 64, -1, 64, 128, 64, 256, 64)), dict(strides=(256, 64, 128, 64, 128, 64, 255, 64)),
+                dict(strides=(256, 64, 128, 64, 128, 64, 256, 32))):
+        assert attention(lib, **bad) == E_INVALID_ARG, bad
+    for bad in (dict(dim=0), dict(dim=12), dict(dim=136), dict(heads=3), dict(kv_heads=0), dict(heads=2048), dict(dtype=2),
+                dict(strides=((1 << 22) + 8, 64, 128, 64, 128, 64, 256, 64))):
+        assert attention(lib, **bad) == E_UNSUPPORTED, bad
+    for bad in (dict(out=P(1)), dict(out=P(2)), dict(out=P(5)), dict(lse=P(6)), dict(lse=P(3))):
+        assert attention(lib, **bad) == E_ALIAS, bad
+    # few queries over many keys need a workspace
+    need = lib.submconv_attention_workspace(1, 1, 100000, 4, 2, 64, 1)
+    assert need > 0 and lib.submconv_attention_workspace(1, 100000, 100000, 4, 2, 64, 1) == 0
+    assert lib.submconv_attention_workspace(1, 1, 100, 4, 3, 64, 1) == 0
+    big = dict(entries=1, nq=1, nk=100000)
+    assert attention(lib, **big, nbytes=need - 1) == E_INVALID_ARG
+    assert attention(lib, **big, nbytes=need, ws=None) == E_INVALID_ARG
+    assert attention(lib, **big, nbytes=need, ws=P(2)) == E_ALIAS
+
+
+def attention_bwd(lib, g=P(1), q=P(2), k=P(3), v=P(4), out=P(5), lse=P(6), strides=(256, 64, 256, 64, 128, 64, 128, 64, 256, 64, 256, 64, 128, 64, 128, 64),
+                  qo=P(7), ko=P(8), scale=0.125, dq=P(9), dk=P(10), dv=P(11), ws=P(12), nbytes=1 << 31, **sizes):
+    s = {**SIZES, **sizes}
+    st = None if strides is None else (ctypes.c_int64 * 16)(*strides)
+    return lib.submconv_attention_backward(g, q, k, v, out, lse, st, qo, ko, s["entries"], s["nq"], s["nk"], s["heads"], s["kv_heads"],
+                                           s["dim"], s["dtype"], scale, dq, dk, dv, ws, nbytes, None)
+
+
+def test_attention_backward_refusals(lib):
+    assert attention_bwd(lib, nq=0, nk=0) == 0
+    need = lib.submconv_attention_backward_workspace(2, 100, 100, 4, 2, 64, 1)
+    assert need >= 100 * 4 * 8
+    for bad in (dict(g=None), dict(q=None), dict(k=None), dict(v=None), dict(out=None), dict(lse=None), dict(dq=None), dict(dk=None),
+                dict(dv=None), dict(qo=None), dict(ws=None), dict(nbytes=need - 1), dict(scale=0.0), dict(strides=None), dict(entries=0)):
+        assert attention_bwd(lib, **bad) == E_INVALID_ARG, bad
+    for bad in (dict(dim=20), dict(heads=5), dict(dtype=9)):
+        assert attention_bwd(lib, **bad) == E_UNSUPPORTED, bad
+    for bad in (dict(dq=P(1)), dict(dk=P(3)), dict(dv=P(10)), dict(dq=P(6)), dict(ws=P(2)), dict(dv=P(7))):
+        assert attention_bwd(lib, **bad) == E_ALIAS, bad
+
+
+def test_last_error_names_the_argument(lib):
+    assert norm(lib, c=9000, x_row=9000, y_row=9000) == E_UNSUPPORTED
+    assert b"c = 9000" in lib.submconv_last_error()
+    assert attention(lib, dim=12) == E_UNSUPPORTED
+    assert b"dim = 12" in lib.submconv_last_error()
+    assert rotary(lib, sections=(11, 11, 11)) == E_INVALID_ARG
+    assert b"33 pairs" in lib.submconv_last_error()
+
+
+def test_binding_refuses_host_tensors():
+    x, h, o = torch.zeros((4, 8)), torch.zeros((4, 2, 8)), torch.zeros(2, dtype=torch.int32)
+    with pytest.raises(TypeError):
+        sc.submconv_layer_norm(x)
+    with pytest.raises(TypeError):
+        sc.submconv_layer_norm_backward(x, x, x)
+    with pytest.raises(TypeError):
+        sc.submconv_rotary(h, torch.zeros((4, 3), dtype=torch.int32), torch.zeros(3), (1, 1, 1))
+    with pytest.raises(TypeError):
+        sc.submconv_attention(h, h, h, o)
+    with pytest.raises(TypeError):
+        sc.submconv_attention_backward(h, h, h, h, h, x, o)
+
+
+def test_rotary_freqs_on_the_host():
+    f = sc.rotary_freqs((2, 0, 4), theta=100.0, device="cpu")
+    assert f.dtype == torch.float32 and torch.equal(f, torch.tensor([1.0, 0.1, 1.0, 100.0 ** -0.25, 0.1, 100.0 ** -0.75]))
