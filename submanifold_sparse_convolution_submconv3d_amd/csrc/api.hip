@@ -45,9 +45,9 @@ int layer_norm_backward(const void *gy, int64_t ldg, const void *x, int64_t ldx,
 int rotary(const void *x, int64_t x_row, int64_t x_head, const int32_t *pos, int64_t pos_row, const float *freqs,
            const int32_t *sections, int axes, int64_t n, int heads, int dim, int dtype, int split, int inverse,
            void *out, int64_t out_row, int64_t out_head, hipStream_t s);
-size_t attention_workspace(const AttnArgs &A);
+size_t attention_workspace(const AttnArgs &A, int dtype);
 int attention(const AttnArgs &A, int dtype, void *workspace, hipStream_t s);
-size_t attention_backward_workspace(const AttnArgs &A);
+size_t attention_backward_workspace(const AttnArgs &A, int dtype);
 int attention_backward(AttnArgs A, int dtype, void *workspace, hipStream_t s);
 
 static thread_local char g_err[512];
@@ -870,14 +870,14 @@ size_t submconv_attention_workspace(int32_t entries, int64_t nq, int64_t nk, int
                                     int32_t dim, int32_t dtype)
 {
     AttnArgs A;
-    return attn_sizes(&A, entries, nq, nk, heads, kv_heads, dim, dtype) == SUBMCONV_OK ? attention_workspace(A) : 0;
+    return attn_sizes(&A, entries, nq, nk, heads, kv_heads, dim, dtype) == SUBMCONV_OK ? attention_workspace(A, dtype) : 0;
 }
 
 size_t submconv_attention_backward_workspace(int32_t entries, int64_t nq, int64_t nk, int32_t heads, int32_t kv_heads,
                                              int32_t dim, int32_t dtype)
 {
     AttnArgs A;
-    return attn_sizes(&A, entries, nq, nk, heads, kv_heads, dim, dtype) == SUBMCONV_OK ? attention_backward_workspace(A) : 0;
+    return attn_sizes(&A, entries, nq, nk, heads, kv_heads, dim, dtype) == SUBMCONV_OK ? attention_backward_workspace(A, dtype) : 0;
 }
 
 // One [n, heads, dim] tensor of a call: its pointer, distances and range.
@@ -907,7 +907,7 @@ int submconv_attention(const void *q, const void *k, const void *v, const int64_
     if (!q_offsets || !k_offsets) return fail(SUBMCONV_E_INVALID_ARG, "offsets are NULL");
     if (!aligned_to(q_offsets, 4) || !aligned_to(k_offsets, 4) || !aligned_to(lse, 4) || !aligned16(workspace))
         return fail(SUBMCONV_E_INVALID_ARG, "misaligned pointer");
-    const size_t es = elem_size(dtype), need = attention_workspace(A), ob = ((size_t)entries + 1) * 4;
+    const size_t es = elem_size(dtype), need = attention_workspace(A, dtype), ob = ((size_t)entries + 1) * 4;
     if (need && (!workspace || workspace_bytes < need))
         return fail(SUBMCONV_E_INVALID_ARG, "workspace of %zu bytes, %zu needed", workspace ? workspace_bytes : 0, need);
     Range r[8];
@@ -941,7 +941,7 @@ int submconv_attention_backward(const void *grad, const void *q, const void *k, 
     if (!q_offsets || !k_offsets || (nq && !lse)) return fail(SUBMCONV_E_INVALID_ARG, "offsets or lse are NULL");
     if (!aligned_to(q_offsets, 4) || !aligned_to(k_offsets, 4) || !aligned_to(lse, 4) || !aligned16(workspace))
         return fail(SUBMCONV_E_INVALID_ARG, "misaligned pointer");
-    const size_t es = elem_size(dtype), need = attention_backward_workspace(A), ob = ((size_t)entries + 1) * 4;
+    const size_t es = elem_size(dtype), need = attention_backward_workspace(A, dtype), ob = ((size_t)entries + 1) * 4;
     if (need && (!workspace || workspace_bytes < need))
         return fail(SUBMCONV_E_INVALID_ARG, "workspace of %zu bytes, %zu needed", workspace ? workspace_bytes : 0, need);
     Range r[12];

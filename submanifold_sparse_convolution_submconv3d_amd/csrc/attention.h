@@ -63,7 +63,29 @@ struct Work {
     uint32_t which;
     bool real;
     int64_t tile, own_beg, own_len, other_beg, other_len;
+    // Cut tiles: the block takes piece `piece` of `pieces` of the other side; its partial
+    // results have number `index`.
+    uint32_t piece, pieces, index;
 };
+
+// Tiles that do not fill the card's `slots` blocks another time are cut along the other side,
+// so that their pieces do: 1.6 rounds of tiles take the time of 1.6 to 1.7, not of 2.  The
+// number of pieces is the one that ends soonest; a larger one has to gain a fifth (partial
+// results cost memory traffic).
+// slots = 0: nothing is cut.
+constexpr uint32_t MAX_PIECES = 5;
+__device__ __forceinline__ uint32_t cut_pieces(uint32_t rest, uint32_t slots)
+{
+    uint32_t best = 1, rounds = 1;
+    for (uint32_t n = 2; n <= MAX_PIECES && rest * n <= 2 * slots; ++n) {
+        const uint32_t r = (rest * n + slots - 1) / slots;
+        if (r * best * 10 < rounds * n * 8) {
+            best = n;
+            rounds = r;
+        }
+    }
+    return best;
+}
 
 // What work number w is: work is all tiles of all parts, `many` times over.  False past the
 // end.  The same in all lanes.
@@ -72,10 +94,12 @@ struct Work {
 //   the lengths, and the bounds come with one memory latency; with more entries tiles are
 //   numbered as first_tile has it, and 64 bounds are compared at a time.
 constexpr int EACH = 4;
-__device__ __forceinline__ bool find_work(const Ragged &own, const Ragged &other, int rows, uint32_t w, uint32_t many, Work *k)
+__device__ __forceinline__ bool find_work(const Ragged &own, const Ragged &other, int rows, uint32_t w, uint32_t many, uint32_t slots, bool join, Work *k)
 {
     const int parts = own.entries + 2, lane = (int)lane_id();
     int part;
+    k->piece = k->index = 0;
+    k->pieces = 1;
     if (parts <= 64 * EACH) {
         const int each = (parts + 63) / 64, p0 = lane * each;
         int64_t b[EACH + 1], ob[EACH + 1];
@@ -99,7 +123,24 @@ __device__ __forceinline__ bool find_work(const Ragged &own, const Ragged &other
             if (lane >= o) sum += y;
         }
         const uint32_t total = __builtin_amdgcn_readlane(sum, 63);
-        if (total == 0 || w >= (uint64_t)total * many) return false;
+        if (total == 0) return false;
+        const uint32_t all = total * many;
+        if (slots) {
+            const uint32_t rest = all % slots, full = all - rest, n = cut_pieces(rest, slots);
+            if (join) {  // w counts cut tiles
+                if (n == 1 || w >= rest) return false;
+                k->pieces = n;
+                k->index = w * n;
+                w += full;
+            } else if (n > 1 && w >= full) {
+                k->index = w - full;
+                if (k->index >= rest * n) return false;
+                k->pieces = n;
+                k->piece = k->index % n;
+                w = full + k->index / n;
+            }
+        }
+        if (w >= all) return false;
         k->which = w / total;
         const uint32_t slot = w - k->which * total;
         const int at = __builtin_ctzll(__ballot(sum > slot));
@@ -123,10 +164,10 @@ __device__ __forceinline__ bool find_work(const Ragged &own, const Ragged &other
         k->other_beg = __builtin_amdgcn_readlane((int)obeg, at);
         k->other_len = __builtin_amdgcn_readlane((int)oend, at) - k->other_beg;
     } else {
-        const uint32_t slots = (uint32_t)(own.n * own.mult / rows + own.entries + 2);
-        k->which = w / slots;
-        if (k->which >= many) return false;
-        const uint32_t slot = w - k->which * slots;
+        const uint32_t numbers = (uint32_t)(own.n * own.mult / rows + own.entries + 2);
+        k->which = w / numbers;
+        if (join || k->which >= many) return false;
+        const uint32_t slot = w - k->which * numbers;
         int lo = 0, hi = parts;
         while (hi - lo > 1) {
             const int step = (hi - lo + 63) / 64;
@@ -516,6 +557,17 @@ __device__ __forceinline__ void store_rows(const f32x16 (&acc)[DB], float f, T *
         }
 }
 
+// Four elements of a row, each rounded once.
+__device__ __forceinline__ void store4(float *p, f32x4 v) { *(Raw16Any *)p = __builtin_bit_cast(Raw16, v); }
+__device__ __forceinline__ void store4(uint16_t *p, f32x4 v)
+{
+    const uint32_t a = pack_bf16(v[0], v[1]), b = pack_bf16(v[2], v[3]);
+    p[0] = (uint16_t)a;
+    p[1] = (uint16_t)(a >> 16);
+    p[2] = (uint16_t)b;
+    p[3] = (uint16_t)(b >> 16);
+}
+
 // --------------------------------------------------------------------------
 // arguments
 // --------------------------------------------------------------------------
@@ -534,9 +586,27 @@ struct AttnArgs {
     int chunk;     // rows of the long side in one split
     int64_t splits;
     int tiles;     // tiles of the short side taken by different blocks
+    uint32_t slots;  // blocks that run at once, for cutting tiles (0: none are cut)
 };
 
-// How a pass is cut along its long side: runs of `chunk` rows (0: not cut), at most
+// Rows [beg, end) of `len` that a piece takes, in whole steps of 32.
+__device__ __forceinline__ void piece_rows(const Work &w, int64_t len, int64_t *beg, int64_t *end)
+{
+    const int64_t steps = (len + 31) / 32;
+    *beg = steps * w.piece / w.pieces * 32;
+    *end = w.piece + 1 == w.pieces ? len : steps * (w.piece + 1) / w.pieces * 32;
+}
+
+// Compute units, and the blocks of 256 threads a unit holds at a time for tiles of `rb` bytes a
+// row when registers allow `waves` a SIMD (LDS: two rings of four tiles of 32 rows).
+constexpr int UNITS = 256;
+constexpr int blocks_at_once(int rb, int waves) { return UNITS * (waves < 163840 / (256 * rb + 4096) ? waves : 163840 / (256 * rb + 4096)); }
+
+// Whether tiles may be cut: a tile is long (64 steps and more of the other side on average), so
+// that a part of a round is worth the partial results and their join.
+static inline bool cut_pays(int64_t other_rows, int entries) { return entries + 2 <= 64 * EACH && other_rows / entries >= 2048; }
+
+// How a pass is split along its long side: runs of `chunk` rows (0: not cut), at most
 // `splits` of them in an entry, `tiles` tiles of the own side taken by different blocks.
 struct SplitPlan {
     int chunk;

@@ -86,13 +86,13 @@ __global__ __launch_bounds__(64 * FWD_WAVES, DP * sizeof(T) > 256 ? 1 : DP * siz
     Work w;
     int64_t qtile, key0 = 0, split = 0;
     if constexpr (SPLIT) {
-        if (!find_work(rk, rq, A.chunk, xcd_work(), A.kv_heads * A.tiles, &w) || !w.real) return;
+        if (!find_work(rk, rq, A.chunk, xcd_work(), A.kv_heads * A.tiles, 0, false, &w) || !w.real) return;
         split = w.tile;
         key0 = split * A.chunk;
         qtile = w.which % A.tiles;
         w.which /= A.tiles;
     } else {
-        if (!find_work(rq, rk, ROWS, xcd_work(), A.kv_heads, &w)) return;
+        if (!find_work(rq, rk, ROWS, xcd_work(), A.kv_heads, A.slots, false, &w)) return;
         qtile = w.tile;
     }
     const int hk = (int)w.which;
@@ -100,6 +100,10 @@ __global__ __launch_bounds__(64 * FWD_WAVES, DP * sizeof(T) > 256 ? 1 : DP * siz
     const int64_t rows = (SPLIT ? w.other_len : w.own_len) * A.group;
     int64_t keys64 = (SPLIT ? w.own_len : w.other_len) - key0;
     if (SPLIT && keys64 > A.chunk) keys64 = A.chunk;
+    if (!SPLIT && w.pieces > 1) {
+        piece_rows(w, w.other_len, &key0, &keys64);
+        keys64 -= key0;
+    }
     const int keys = (int)keys64, steps = (keys + 31) / 32;
 
     const int lane = lane_id(), half = lane >> 5;
@@ -351,6 +355,10 @@ __global__ __launch_bounds__(64 * FWD_WAVES, DP * sizeof(T) > 256 ? 1 : DP * siz
                 const int64_t at = split * A.nq * A.heads + (q_beg + token) * A.heads + head;
                 store_rows<float>(o[qb], 1.0f, A.part + at * A.dim, A.dim, valid);
                 if (valid && half == 0) *(float2 *)(A.part2 + 2 * at) = make_float2(m[qb], sum);
+            } else if (w.pieces > 1) {
+                const int64_t at = (int64_t)w.index * ROWS + (threadIdx.x >> 6) * (32 * QB) + 32 * qb + (lane & 31);
+                store_rows<float>(o[qb], 1.0f, A.part + at * A.dim, A.dim, valid);
+                if (valid && half == 0) *(float2 *)(A.part2 + 2 * at) = make_float2(m[qb], sum);
             } else {
                 T *op = (T *)A.out.p + (q_beg + token) * A.out.row + head * A.out.head;
                 store_rows<T>(o[qb], sum > 0.0f ? 1.0f / sum : (sum == 0.0f ? 0.0f : sum), op, A.dim, valid);
@@ -423,17 +431,51 @@ __global__ __launch_bounds__(64 * JOIN_WAVES) void k_attn_join(AttnArgs A)
     for (int i = 1; i < groups * A.tiles; ++i) sum += acc[first + i / groups][i % groups * pieces + e];
     for (int i = 1; i < A.tiles; ++i) l += part_l[first + i];
     sum *= l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);
-    T *op = (T *)A.out.p + token * A.out.row + head * A.out.head + 4 * e;
-    if constexpr (sizeof(T) == 2) {
-        const uint32_t a = pack_bf16(sum[0], sum[1]), b = pack_bf16(sum[2], sum[3]);
-        op[0] = (uint16_t)a;
-        op[1] = (uint16_t)(a >> 16);
-        op[2] = (uint16_t)b;
-        op[3] = (uint16_t)(b >> 16);
-    } else {
-        *(Raw16Any *)op = __builtin_bit_cast(Raw16, sum);
-    }
+    store4((T *)A.out.p + token * A.out.row + head * A.out.head + 4 * e, sum);
     if (A.lse && e == 0) A.lse[at] = log_sum(top, l, A.scale);
+}
+
+// The pieces of cut tiles joined: blockIdx.x counts the tiles, blockIdx.y their quarters.
+template <typename T>
+__global__ __launch_bounds__(256) void k_attn_join_cut(AttnArgs A)
+{
+    constexpr int ROWS = 32 * FWD_WAVES;
+    const Ragged rq = {A.q_off, A.entries, A.nq, A.group}, rk = {A.k_off, A.entries, A.nk, 1};
+    Work w;
+    if (!find_work(rq, rk, ROWS, blockIdx.x, A.kv_heads, A.slots, true, &w)) return;
+    const int pieces = A.dim / 4, groups = 256 / pieces, g = threadIdx.x / pieces, e = threadIdx.x % pieces;
+    const int64_t rows = w.own_len * A.group - w.tile * ROWS;  // of this tile on
+    if (g >= groups) return;
+    for (int r = blockIdx.y * (ROWS / 4) + g; r < (int)(blockIdx.y + 1) * (ROWS / 4) && r < rows; r += groups) {
+        const uint32_t row = (uint32_t)(w.tile * ROWS) + r, token = A.group == 1 ? row : row / A.group;
+        const int head = (int)(w.which * A.group + (row - token * A.group));
+        const int64_t first = (int64_t)w.index * ROWS + r;
+        float2 ml[MAX_PIECES];
+        f32x4 v[MAX_PIECES];
+        float top = -INFINITY, l = 0.0f;
+#pragma unroll
+        for (uint32_t i = 0; i < MAX_PIECES; ++i) {
+            ml[i] = make_float2(-INFINITY, 0.0f);
+            v[i] = f32x4{0, 0, 0, 0};
+            if (i < w.pieces) {
+                ml[i] = *(const float2 *)(A.part2 + 2 * (first + i * ROWS));
+                v[i] = *(const f32x4 *)(A.part + (first + i * ROWS) * A.dim + 4 * e);
+            }
+        }
+#pragma unroll
+        for (uint32_t i = 0; i < MAX_PIECES; ++i) top = fmaxf(top, ml[i].x);
+        f32x4 sum = {0, 0, 0, 0};
+#pragma unroll
+        for (uint32_t i = 0; i < MAX_PIECES; ++i)
+            if (i < w.pieces) {
+                const float f = rescale(ml[i].x, top, A.scale * LOG2E);
+                l += ml[i].y * f;
+                sum += v[i] * f;
+            }
+        sum *= l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);
+        store4((T *)A.out.p + (w.own_beg + token) * A.out.row + head * A.out.head + 4 * e, sum);
+        if (A.lse && e == 0) A.lse[(w.own_beg + token) * A.heads + head] = log_sum(top, l, A.scale);
+    }
 }
 
 // How a pass over a long side is split when its own side has few tiles: enough runs that
@@ -445,7 +487,7 @@ SplitPlan split_plan(int64_t own_rows, int own_tile, int64_t other_rows, int oth
     SplitPlan p = {0, 0, 1};
     if (own_rows == 0 || other_rows == 0) return p;
     const int64_t per_entry = (own_rows / entries + own_tile - 1) / own_tile;
-    const int64_t tiles = per_entry > 0 ? per_entry : 1;
+    int64_t tiles = per_entry > 0 ? per_entry : 1;
     const int64_t used = entries < own_rows ? entries : own_rows;
     if (tiles * used * kv_heads * 2 > WANT_BLOCKS) return p;
     int64_t runs = WANT_BLOCKS / (tiles * kv_heads);
@@ -456,6 +498,8 @@ SplitPlan split_plan(int64_t own_rows, int own_tile, int64_t other_rows, int oth
     if (chunk * 2 > other_rows / entries || chunk > (1 << 30)) return p;  // entries of one run or two: nothing to gain
     p.chunk = (int)chunk;
     p.splits = (other_rows + chunk - 1) / chunk;
+    // an entry longer than the average has more tiles, and a block that takes two takes twice as long
+    if (entries > 1 && tiles > 1) tiles *= 2;
     p.tiles = (int)tiles;
     return p;
 }
@@ -465,10 +509,19 @@ static SplitPlan fwd_plan(const AttnArgs &A)
     return split_plan(A.nq * A.group, 32 * FWD_WAVES, A.nk, 32, A.entries, A.kv_heads);
 }
 
-size_t attention_workspace(const AttnArgs &A)
+// Blocks that run at once (the launch bounds of k_attn).
+static uint32_t fwd_slots(const AttnArgs &A, int dtype)
+{
+    if (!cut_pays(A.nk, A.entries)) return 0;
+    const int rb = (A.dim + 31) / 32 * 32 * (dtype == SUBMCONV_F32 ? 4 : 2);
+    return (uint32_t)blocks_at_once(rb, rb > 256 ? 1 : rb > 128 ? 2 : 3);
+}
+
+size_t attention_workspace(const AttnArgs &A, int dtype)
 {
     const SplitPlan p = fwd_plan(A);
-    return p.chunk ? (size_t)p.splits * A.nq * A.heads * (A.dim + 2) * sizeof(float) : 0;
+    const size_t rows = p.chunk ? (size_t)p.splits * A.nq * A.heads : (size_t)2 * fwd_slots(A, dtype) * 32 * FWD_WAVES;
+    return rows * (A.dim + 2) * sizeof(float);
 }
 
 // Whether keys and values can be copied straight into LDS (see Fill).
@@ -497,9 +550,16 @@ static int run_fwd(AttnArgs A, const SplitPlan &p, void *workspace, hipStream_t 
         SC_LAUNCHED("attention join");
         return SUBMCONV_OK;
     }
-    const dim3 grid(xcd_grid(ragged_tiles(A.nq, A.entries, A.group, 32 * FWD_WAVES) * A.kv_heads));
-    hipLaunchKernelGGL((k_attn<T, DP, false, DIRECT>), grid, block, 0, st, A);
+    A.slots = DIRECT ? fwd_slots(A, sizeof(T) == 4 ? SUBMCONV_F32 : SUBMCONV_BF16) : 0;
+    A.part = (float *)workspace;
+    A.part2 = A.part + (size_t)2 * A.slots * 32 * FWD_WAVES * A.dim;
+    const int64_t work = ragged_tiles(A.nq, A.entries, A.group, 32 * FWD_WAVES) * A.kv_heads + 2 * A.slots;
+    hipLaunchKernelGGL((k_attn<T, DP, false, DIRECT>), dim3(xcd_grid(work)), block, 0, st, A);
     SC_LAUNCHED("attention");
+    if (A.slots) {
+        hipLaunchKernelGGL(k_attn_join_cut<T>, dim3(A.slots, 4), dim3(256), 0, st, A);
+        SC_LAUNCHED("attention join of cut tiles");
+    }
     return SUBMCONV_OK;
 }
 

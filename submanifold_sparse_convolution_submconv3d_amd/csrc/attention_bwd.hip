@@ -35,13 +35,13 @@ __global__ __launch_bounds__(64 * BWD_WAVES, DP * sizeof(T) > 256 ? 1 : 2) void 
     Work w;
     int64_t qtile, key0 = 0, split = 0;
     if constexpr (SPLIT) {
-        if (!find_work(rk, rq, A.chunk, xcd_work(), A.kv_heads * A.tiles, &w) || !w.real) return;
+        if (!find_work(rk, rq, A.chunk, xcd_work(), A.kv_heads * A.tiles, 0, false, &w) || !w.real) return;
         split = w.tile;
         key0 = split * A.chunk;
         qtile = w.which % A.tiles;
         w.which /= A.tiles;
     } else {
-        if (!find_work(rq, rk, BWD_ROWS, xcd_work(), A.kv_heads, &w)) return;
+        if (!find_work(rq, rk, BWD_ROWS, xcd_work(), A.kv_heads, A.slots, false, &w)) return;
         qtile = w.tile;
     }
     const int hk = (int)w.which;
@@ -49,6 +49,10 @@ __global__ __launch_bounds__(64 * BWD_WAVES, DP * sizeof(T) > 256 ? 1 : 2) void 
     const int64_t rows = (SPLIT ? w.other_len : w.own_len) * A.group;
     int64_t keys64 = (SPLIT ? w.own_len : w.other_len) - key0;
     if (SPLIT && keys64 > A.chunk) keys64 = A.chunk;
+    if (!SPLIT && w.pieces > 1) {
+        piece_rows(w, w.other_len, &key0, &keys64);
+        keys64 -= key0;
+    }
     const int keys = (int)keys64, steps = (keys + 31) / 32;
 
     const int lane = lane_id(), half = lane >> 5;
@@ -105,7 +109,7 @@ __global__ __launch_bounds__(64 * BWD_WAVES, DP * sizeof(T) > 256 ? 1 : 2) void 
             }
         }
         delta += other_half(delta);
-        if (valid && half == 0 && split == 0) *(float2 *)(A.stat + 2 * at) = make_float2(base, delta);
+        if (valid && half == 0 && split == 0 && w.piece == 0) *(float2 *)(A.stat + 2 * at) = make_float2(base, delta);
 
         f32x16 dq[1][DB], s[2], dp[2];
 #pragma unroll
@@ -232,6 +236,8 @@ __global__ __launch_bounds__(64 * BWD_WAVES, DP * sizeof(T) > 256 ? 1 : 2) void 
         }
         if constexpr (SPLIT)
             store_rows<float>(dq[0], 1.0f, A.part + (split * A.nq * A.heads + at) * A.dim, A.dim, valid);
+        else if (w.pieces > 1)
+            store_rows<float>(dq[0], 1.0f, A.part + ((int64_t)w.index * BWD_ROWS + (threadIdx.x >> 6) * 32 + (lane & 31)) * A.dim, A.dim, valid);
         else
             store_rows<T>(dq[0], A.scale, (T *)A.dq.p + (q_beg + token) * A.dq.row + head * A.dq.head, A.dim, valid);
     }
@@ -252,13 +258,13 @@ __global__ __launch_bounds__(64 * BWD_WAVES, DP * sizeof(T) > 128 ? 1 : 2) void 
     Work w;
     int64_t ktile, row0 = 0, split = 0;
     if constexpr (SPLIT) {
-        if (!find_work(rq, rk, A.chunk, xcd_work(), A.kv_heads * A.tiles, &w) || !w.real) return;
+        if (!find_work(rq, rk, A.chunk, xcd_work(), A.kv_heads * A.tiles, 0, false, &w) || !w.real) return;
         split = w.tile;
         row0 = split * A.chunk;
         ktile = w.which % A.tiles;
         w.which /= A.tiles;
     } else {
-        if (!find_work(rk, rq, BWD_ROWS, xcd_work(), A.kv_heads, &w)) return;
+        if (!find_work(rk, rq, BWD_ROWS, xcd_work(), A.kv_heads, A.slots, false, &w)) return;
         ktile = w.tile;
     }
     const int hk = (int)w.which;
@@ -266,6 +272,10 @@ __global__ __launch_bounds__(64 * BWD_WAVES, DP * sizeof(T) > 128 ? 1 : 2) void 
     const int64_t keys = SPLIT ? w.other_len : w.own_len;
     int64_t rows64 = (SPLIT ? w.own_len : w.other_len) * A.group - row0;
     if (SPLIT && rows64 > A.chunk) rows64 = A.chunk;
+    if (!SPLIT && w.pieces > 1) {
+        piece_rows(w, w.other_len * A.group, &row0, &rows64);
+        rows64 -= row0;
+    }
     const int rows = (int)rows64, steps = (rows + 31) / 32;
 
     const int lane = lane_id(), half = lane >> 5, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -468,6 +478,10 @@ __global__ __launch_bounds__(64 * BWD_WAVES, DP * sizeof(T) > 128 ? 1 : 2) void 
             const int64_t at = ((split * A.nk + k_beg + key) * A.kv_heads + hk) * A.dim;
             store_rows<float>(dk[0], 1.0f, A.part + at, A.dim, valid);
             store_rows<float>(dv[0], 1.0f, A.part2 + at, A.dim, valid);
+        } else if (w.pieces > 1) {
+            const int64_t at = ((int64_t)w.index * BWD_ROWS + wave * 32 + (lane & 31)) * A.dim;
+            store_rows<float>(dk[0], 1.0f, A.part + at, A.dim, valid);
+            store_rows<float>(dv[0], 1.0f, A.part2 + at, A.dim, valid);
         } else {
             store_rows<T>(dk[0], A.scale, (T *)A.dk.p + (k_beg + key) * A.dk.row + hk * A.dk.head, A.dim, valid);
             store_rows<T>(dv[0], 1.0f, (T *)A.dv.p + (k_beg + key) * A.dv.row + hk * A.dv.head, A.dim, valid);
@@ -520,39 +534,64 @@ __global__ __launch_bounds__(256) void k_attn_sum(Ragged own, Ragged other, int 
     if (g == 0) {
         for (int i = 1; i < groups; ++i) sum += acc[i * pieces + e];
         sum *= scale;
-        T *op = (T *)out.p + row * out.row + head * out.head + 4 * e;
-        if constexpr (sizeof(T) == 2) {
-            const uint32_t a = pack_bf16(sum[0], sum[1]), b = pack_bf16(sum[2], sum[3]);
-            op[0] = (uint16_t)a;
-            op[1] = (uint16_t)(a >> 16);
-            op[2] = (uint16_t)b;
-            op[3] = (uint16_t)(b >> 16);
-        } else {
-            *(Raw16Any *)op = __builtin_bit_cast(Raw16, sum);
-        }
+        store4((T *)out.p + row * out.row + head * out.head + 4 * e, sum);
+    }
+}
+
+// The pieces of cut tiles summed and scaled, for one or two tensors (blockIdx.z): blockIdx.x
+// counts the tiles, blockIdx.y their quarters.  own: the side whose rows the tiles are.
+template <typename T>
+__global__ __launch_bounds__(256) void k_attn_sum_cut(Ragged own, Ragged other, int kv_heads, int group, int dim, uint32_t slots,
+                                                      const float *__restrict__ part_a, float scale_a, Heads out_a,
+                                                      const float *__restrict__ part_b, float scale_b, Heads out_b)
+{
+    Work w;
+    if (!find_work(own, other, BWD_ROWS, blockIdx.x, kv_heads, slots, true, &w)) return;
+    const float *part = blockIdx.z ? part_b : part_a;
+    const float scale = blockIdx.z ? scale_b : scale_a;
+    const Heads out = blockIdx.z ? out_b : out_a;
+    const int pieces = dim / 4, groups = 256 / pieces, g = threadIdx.x / pieces, e = threadIdx.x % pieces;
+    const int64_t rows = w.own_len * group - w.tile * BWD_ROWS;
+    if (g >= groups) return;
+    for (int r = blockIdx.y * (BWD_ROWS / 4) + g; r < (int)(blockIdx.y + 1) * (BWD_ROWS / 4) && r < rows; r += groups) {
+        const uint32_t row = (uint32_t)(w.tile * BWD_ROWS) + r, token = group == 1 ? row : row / group;
+        const int head = (int)(w.which * group + (row - token * group));
+        f32x4 v[MAX_PIECES];
+#pragma unroll
+        for (uint32_t i = 0; i < MAX_PIECES; ++i)
+            v[i] = i < w.pieces ? *(const f32x4 *)(part + ((int64_t)(w.index + i) * BWD_ROWS + r) * dim + 4 * e) : f32x4{0, 0, 0, 0};
+        f32x4 sum = v[0];
+#pragma unroll
+        for (uint32_t i = 1; i < MAX_PIECES; ++i) sum += v[i];
+        store4((T *)out.p + (w.own_beg + token) * out.row + head * out.head + 4 * e, sum * scale);
     }
 }
 
 struct BwdPlan {
     SplitPlan q, k;
+    uint32_t q_slots, k_slots;  // blocks that run at once where tiles may be cut
     size_t stat, part;  // bytes of the workspace's two areas
 };
 
-static BwdPlan bwd_plan(const AttnArgs &A)
+static BwdPlan bwd_plan(const AttnArgs &A, int dtype)
 {
+    const int rb = (A.dim + 31) / 32 * 32 * (dtype == SUBMCONV_F32 ? 4 : 2);
     BwdPlan p;
     p.q = split_plan(A.nq * A.group, BWD_ROWS, A.nk, 32, A.entries, A.kv_heads);
     p.k = split_plan(A.nk, BWD_ROWS, A.nq * A.group, 32, A.entries, A.kv_heads);
+    p.q_slots = cut_pays(A.nk, A.entries) ? (uint32_t)blocks_at_once(rb, rb > 256 ? 1 : 2) : 0;
+    p.k_slots = cut_pays(A.nq * A.group, A.entries) ? (uint32_t)blocks_at_once(rb, rb > 128 ? 1 : 2) : 0;
     p.stat = ((size_t)A.nq * A.heads * 2 * sizeof(float) + 15) / 16 * 16;
-    const size_t a = p.q.chunk ? (size_t)p.q.splits * A.nq * A.heads * A.dim * sizeof(float) : 0;
-    const size_t b = p.k.chunk ? (size_t)p.k.splits * A.nk * A.kv_heads * A.dim * 2 * sizeof(float) : 0;
+    const size_t row = A.dim * sizeof(float), tile = BWD_ROWS * row;
+    const size_t a = p.q.chunk ? (size_t)p.q.splits * A.nq * A.heads * row : 2 * p.q_slots * tile;
+    const size_t b = p.k.chunk ? (size_t)p.k.splits * A.nk * A.kv_heads * 2 * row : 4 * p.k_slots * tile;
     p.part = a > b ? a : b;  // the two passes use it one after the other
     return p;
 }
 
-size_t attention_backward_workspace(const AttnArgs &A)
+size_t attention_backward_workspace(const AttnArgs &A, int dtype)
 {
-    const BwdPlan p = bwd_plan(A);
+    const BwdPlan p = bwd_plan(A, dtype);
     return p.stat + p.part;
 }
 
@@ -577,8 +616,15 @@ static int run_bwd(AttnArgs A, const BwdPlan &p, hipStream_t st)
             hipLaunchKernelGGL(k_attn_sum<T>, dim3((unsigned)(A.nq * A.heads)), dim3(256), 0, st, rq, rk, A.heads, A.dim,
                                A.chunk, A.part, A.scale, A.dq, nullptr, 0.0f, Heads{});
         } else {
-            const int64_t work = ragged_tiles(A.nq, A.entries, A.group, BWD_ROWS) * A.kv_heads;
+            A.slots = DIRECT ? p.q_slots : 0;
+            const int64_t work = ragged_tiles(A.nq, A.entries, A.group, BWD_ROWS) * A.kv_heads + 2 * A.slots;
             hipLaunchKernelGGL((k_attn_dq<T, DP, false, DIRECT>), dim3(xcd_grid(work)), block, 0, st, A);
+            if (A.slots) {
+                SC_LAUNCHED("attention_backward queries");
+                const Ragged own = {A.q_off, A.entries, A.nq, A.group};
+                hipLaunchKernelGGL(k_attn_sum_cut<T>, dim3(A.slots, 4), dim3(256), 0, st, own, rk, A.kv_heads, A.group, A.dim, A.slots,
+                                   A.part, A.scale, A.dq, nullptr, 0.0f, Heads{});
+            }
         }
         SC_LAUNCHED("attention_backward queries");
     }
@@ -593,8 +639,16 @@ static int run_bwd(AttnArgs A, const BwdPlan &p, hipStream_t st)
             hipLaunchKernelGGL(k_attn_sum<T>, dim3((unsigned)(A.nk * A.kv_heads), 2), dim3(256), 0, st, rk, rows, A.kv_heads,
                                A.dim, A.chunk, A.part, A.scale, A.dk, A.part2, 1.0f, A.dv);
         } else {
-            const int64_t work = ragged_tiles(A.nk, A.entries, 1, BWD_ROWS) * A.kv_heads;
+            A.slots = DIRECT ? p.k_slots : 0;
+            A.part2 = A.part + (size_t)2 * A.slots * BWD_ROWS * A.dim;
+            const int64_t work = ragged_tiles(A.nk, A.entries, 1, BWD_ROWS) * A.kv_heads + 2 * A.slots;
             hipLaunchKernelGGL((k_attn_dkv<T, DP, false, DIRECT>), dim3(xcd_grid(work)), block, 0, st, A);
+            if (A.slots) {
+                SC_LAUNCHED("attention_backward keys");
+                const Ragged other = {A.q_off, A.entries, A.nq, A.group};
+                hipLaunchKernelGGL(k_attn_sum_cut<T>, dim3(A.slots, 4, 2), dim3(256), 0, st, rk, other, A.kv_heads, 1, A.dim, A.slots,
+                                   A.part, A.scale, A.dk, A.part2, 1.0f, A.dv);
+            }
         }
         SC_LAUNCHED("attention_backward keys");
     }
@@ -613,7 +667,7 @@ static bool direct(const AttnArgs &A, int es)
 
 int attention_backward(AttnArgs A, int dtype, void *workspace, hipStream_t st)
 {
-    const BwdPlan p = bwd_plan(A);
+    const BwdPlan p = bwd_plan(A, dtype);
     A.stat = (float *)workspace;
     A.part = (float *)((char *)workspace + p.stat);
     const int dp = (A.dim + 31) / 32;

@@ -272,3 +272,39 @@ def test_attention_gradient_against_differences(h, hk, d, dtype):
             slope = (loss(hi) - loss(lo)) / (2 * step)
             # step^2 times a third derivative, and fp32 rounding of each gradient element
             assert abs(slope - float((grads[i] * dirn).sum())) <= 1e-4 * float(np.abs(grads[i] * dirn).sum()) + 1e-5
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("h,hk,d,lens", [(13, 13, 32, [3900]), (14, 7, 64, [5003, 2000]), (8, 8, 128, [4200, 0, 3001])])
+def test_attention_long_tiles(h, hk, d, lens, dtype):
+    """Long entries, whose last round of tiles is cut into pieces and joined, against the same rows
+    with hundreds of empty entries behind them (never cut), and 40 queries against 64 bits."""
+    rng = np.random.default_rng([12, h, d])
+    qo = offsets(lens)
+    n = int(qo[-1])
+    q, k, v, g = (heads(n, m, d, dtype, rng) for m in (h, hk, hk, h))
+    t = device_offsets(qo)
+    many = device_offsets(list(qo) + [n] * 300)
+    note("attention long tiles h=%d/%d d=%d %s %s" % (h, hk, d, lens, dtype))
+    out, lse = sc.submconv_attention(q, k, v, t, return_lse=True)
+    grads = sc.submconv_attention_backward(g, q, k, v, out, lse, t)
+    assert torch.equal(sc.submconv_attention(q, k, v, t), out)
+    assert all(torch.equal(a, b) for a, b in zip(grads, sc.submconv_attention_backward(g, q, k, v, out, lse, t)))
+    plain, plse = sc.submconv_attention(q, k, v, many, return_lse=True)
+    pgrads = sc.submconv_attention_backward(g, q, k, v, plain, plse, many)
+    # both sides are within max(lens) additions and a few roundings of the exact values
+    tol = 4 * ref.UNIT[dtype] + 4 * max(lens) * ref.U32
+    for name, a, b in (("out", out, plain), ("lse", lse, plse)) + tuple(zip(("dq", "dk", "dv"), grads, pgrads)):
+        gap = float((a.float() - b.float()).abs().max())
+        assert gap <= tol * float(b.float().abs().max()), "%s: %.3e apart" % (name, gap)
+    pick = np.sort(rng.choice(n, 40, replace=False))
+    for e in range(len(lens)):
+        rows = pick[(pick >= qo[e]) & (pick < qo[e + 1])]
+        if not len(rows):
+            continue
+        some, keys = [to_f64(x[rows]) for x in (q, g)], [to_f64(x[qo[e]:qo[e + 1]]) for x in (k, v)]
+        one, all_ = np.array([0, len(rows)]), np.array([0, lens[e]])
+        expect, _, bound, _ = ref.attention(some[0], *keys, one, all_, d ** -0.5, ref.UNIT[dtype])
+        within("out", out[rows], expect, bound)
+        expect, bounds = ref.attention_backward(some[1], some[0], *keys, one, all_, d ** -0.5, ref.UNIT[dtype])
+        within("dq", grads[0][rows], expect[0], bounds[0])
