@@ -111,7 +111,6 @@ __global__ __launch_bounds__(64 * FWD_WAVES, DP * sizeof(T) > 256 ? 1 : DP * siz
     const T *kp = (const T *)A.k.p + (k_beg + key0) * A.k.row + hk * A.k.head;
     const T *vp = (const T *)A.v.p + (k_beg + key0) * A.v.row + hk * A.v.head;
     Fill<T, RB, FWD_WAVES, DIRECT> fill;
-    constexpr int PER = Fill<T, RB, FWD_WAVES, DIRECT>::PER;
     fill.init(lds, lds + V0, A.k.row, A.v.row, A.dim);
     HeadAddr<RB> ka(lds);
     RowsAddr<T, RB> va(lds + V0);
@@ -120,16 +119,19 @@ __global__ __launch_bounds__(64 * FWD_WAVES, DP * sizeof(T) > 256 ? 1 : DP * siz
         const int64_t wave_row = qtile * ROWS + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) * (32 * QB);
         if (SPLIT) __syncthreads();  // the rings' last readers are done
         fill.start(kp, vp, keys);
+        // keys 0 .. 2 and values 0 .. 1; then, before every pair of steps u, u + 1, keys u + 3 and
+        // u + 4 and values u + 2 and u + 3, whose places were last read in the pair before
         if (steps)
-            for (int u = 1; u < RING; ++u) fill.next();
+            for (int u = fill.second; u < 3; ++u) fill.next();
         if (wave_row >= rows) {  // a wave past the entry's rows only helps with the copies
             if (steps) {
-                wait_copies_and_barrier<2 * PER>();
-                for (int u = 0; u < steps; ++u) {
-                    if (u) fill.next();
-                    wait_copies_and_barrier<PER>();
-                }
                 wait_copies_and_barrier<0>();
+                wait_copies_and_barrier<0>();
+                for (int u = 0; u + 2 < steps; u += 2) {
+                    fill.next();
+                    fill.next();
+                    wait_copies_and_barrier<0>();
+                }
             }
             continue;
         }
@@ -240,7 +242,6 @@ __global__ __launch_bounds__(64 * FWD_WAVES, DP * sizeof(T) > 256 ? 1 : DP * siz
         // step u from scores t, leaving the next step's in n; kat, vat: the tiles' places past ka and va
         auto step = [&](f32x16(&t)[QB], f32x16(&n)[QB], int u, uint32_t kat, uint32_t vat) {
             float top[QB];
-            fill.next();  // tiles u + 3: their places were last read in step u - 1
             if constexpr (sizeof(T) == 2) {
                 // in the order it is to run: LDS reads AHEAD of their use, and between the matrix
                 // products a piece of the arithmetic; first the scores with half the weights, then
@@ -312,24 +313,26 @@ __global__ __launch_bounds__(64 * FWD_WAVES, DP * sizeof(T) > 256 ? 1 : DP * siz
                 }
             }
             settle(n, top);
-            wait_copies_and_barrier<PER>();
         };
 
         if (steps) {
-            wait_copies_and_barrier<2 * PER>();
+            wait_copies_and_barrier<0>();
             float top[QB];
             scores(s[0], 0);
             mask(s[0], 0);
             maximum(s[0], top, 0, 16);
             settle(s[0], top);
-            wait_copies_and_barrier<PER>();
+            wait_copies_and_barrier<0>();
             int u = 0;
             for (; u + 2 < steps; u += 2) {  // ring places u mod 4 = 0 or 2: the addresses move to the other half
                 const uint32_t other = u & 2 ? -2 * TILE : 2 * TILE;
+                fill.next();
+                fill.next();
                 step(s[0], s[1], u, TILE, 0);
                 ka.move(other);
                 step(s[1], s[0], u + 1, 0, TILE);
                 va.move(other);
+                wait_copies_and_barrier<0>();
             }
             if (u + 1 < steps) {
                 step(s[0], s[1], u, TILE, 0);
@@ -343,7 +346,6 @@ __global__ __launch_bounds__(64 * FWD_WAVES, DP * sizeof(T) > 256 ? 1 : DP * siz
                 ka.move(-2 * TILE);
                 va.move(-2 * TILE);
             }
-            wait_copies_and_barrier<0>();  // nothing may still arrive when the next tile's copies start, or the block ends
         }
 #pragma unroll
         for (int qb = 0; qb < QB; ++qb) {
