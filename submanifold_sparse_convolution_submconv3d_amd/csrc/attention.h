@@ -267,9 +267,18 @@ __device__ __forceinline__ void wait_copies_and_barrier()
 //   Needs 16-byte alignment, and rows that do not overlap (the check is on the offset).
 //   Otherwise: loads and LDS writes, any alignment and row distance.
 constexpr uint32_t OUT_OF_RANGE = 0x80000000u;
-constexpr int RING = 4;
 
-template <typename T, int RB, int WAVES, bool DIRECT>
+// A buffer of `bytes` from p on.  Both are the same in all lanes; said so explicitly, since a
+// copy whose buffer the compiler holds in vector registers is put into a loop over lanes.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t scalar_rsrc(const void *p, int bytes)
+{
+    const uint64_t u = (uint64_t)p;
+    const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)u), hi = __builtin_amdgcn_readfirstlane((uint32_t)(u >> 32));
+    const uint64_t q = (uint64_t)hi << 32 | lo;  // (the builtin returns a signed int)
+    return __builtin_amdgcn_make_buffer_rsrc((void *)q, (short)0, __builtin_amdgcn_readfirstlane(bytes), 0x00020000);
+}
+
+template <typename T, int RB, int WAVES, int RING, bool DIRECT>
 struct Fill {
     static constexpr int TILE = 32 * RB, PER = RB / 16 / WAVES;  // copies of a wave for a tile
     static_assert(RB / 16 % WAVES == 0 && WAVES % 2 == 0, "whole copies, waves of one tensor");
@@ -307,10 +316,11 @@ struct Fill {
     {
         const int n = left < 0 ? 0 : (left > 32 ? 32 : left);
         if constexpr (DIRECT) {
-            const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc((void *)ptr, (short)0, n * (int)row_bytes, 0x00020000);
+            const __amdgpu_buffer_rsrc_t r = scalar_rsrc(ptr, n * (int)row_bytes);
+            const uint32_t at = __builtin_amdgcn_readfirstlane(to + place);
 #pragma unroll
             for (int i = 0; i < PER; ++i)
-                __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (SC_LDS void *)(uintptr_t)(to + place + i * 1024), 16, off[i], 0, 0, 0);
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (SC_LDS void *)(uintptr_t)(at + i * 1024), 16, off[i], 0, 0, 0);
         } else {
 #pragma unroll
             for (int i = 0; i < PER; ++i) put(ptr, row(i) < n ? off[i] : OUT_OF_RANGE, i);
@@ -325,7 +335,7 @@ struct Fill {
         const Heads &h = second ? b : a;
         const uint32_t t0 = row0 / group;
         const char *base = (const char *)h.p + ((token0 + t0) * h.row + head0 * h.head) * (int64_t)sizeof(T);
-        const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc((void *)base, (short)0, 0x7fffffff, 0x00020000);
+        const __amdgpu_buffer_rsrc_t rs = scalar_rsrc(base, 0x7fffffff);
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
             const uint32_t r = row0 + row(i), t = r / group;

@@ -62,7 +62,7 @@ __device__ __forceinline__ void scale_if(f32x16 &acc, float f, uint64_t on)
                  : "scc");
 }
 
-constexpr int FWD_WAVES = 4;
+constexpr int FWD_WAVES = 4, RING = 4;
 
 // A step handles 32 keys.  Its wave has the scores of its own keys in registers already,
 // and, while it turns them into weights, the matrix cores form the scores of the next
@@ -110,7 +110,7 @@ __global__ __launch_bounds__(64 * FWD_WAVES, DP * sizeof(T) > 256 ? 1 : DP * siz
     const float c = A.scale * LOG2E;
     const T *kp = (const T *)A.k.p + (k_beg + key0) * A.k.row + hk * A.k.head;
     const T *vp = (const T *)A.v.p + (k_beg + key0) * A.v.row + hk * A.v.head;
-    Fill<T, RB, FWD_WAVES, DIRECT> fill;
+    Fill<T, RB, FWD_WAVES, RING, DIRECT> fill;
     fill.init(lds, lds + V0, A.k.row, A.v.row, A.dim);
     HeadAddr<RB> ka(lds);
     RowsAddr<T, RB> va(lds + V0);

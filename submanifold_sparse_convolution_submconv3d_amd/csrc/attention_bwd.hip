@@ -13,7 +13,7 @@
 
 namespace sc {
 
-constexpr int BWD_WAVES = 4, BWD_ROWS = 32 * BWD_WAVES;
+constexpr int BWD_WAVES = 4, BWD_ROWS = 32 * BWD_WAVES, RING = 4;
 
 // A score's exponent is s c - base; a query whose scores are all -inf has lse = -inf and
 // weights exp(-inf), so its base must be finite.
@@ -59,8 +59,8 @@ __global__ __launch_bounds__(64 * BWD_WAVES, DP * sizeof(T) > 256 ? 1 : 2) void 
     const float c = A.scale * LOG2E;
     const T *kp = (const T *)A.k.p + (k_beg + key0) * A.k.row + hk * A.k.head;
     const T *vp = (const T *)A.v.p + (k_beg + key0) * A.v.row + hk * A.v.head;
-    Fill<T, RB, BWD_WAVES, DIRECT> fill;
-    constexpr int PER = Fill<T, RB, BWD_WAVES, DIRECT>::PER;
+    Fill<T, RB, BWD_WAVES, RING, DIRECT> fill;
+    constexpr int PER = Fill<T, RB, BWD_WAVES, RING, DIRECT>::PER;
     fill.init(lds, lds + V0, A.k.row, A.v.row, A.dim);
     HeadAddr<RB> ka(lds);
     RowsAddr<T, RB> kt(lds);
@@ -281,8 +281,8 @@ __global__ __launch_bounds__(64 * BWD_WAVES, DP * sizeof(T) > 128 ? 1 : 2) void 
     const int lane = lane_id(), half = lane >> 5, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const float c = A.scale * LOG2E;
     const uint32_t group = A.group;
-    Fill<T, RB, BWD_WAVES, DIRECT> fill;
-    constexpr int PER = Fill<T, RB, BWD_WAVES, DIRECT>::PER + 1;  // and the rows' statistics
+    Fill<T, RB, BWD_WAVES, RING, DIRECT> fill;
+    constexpr int PER = Fill<T, RB, BWD_WAVES, RING, DIRECT>::PER + 1;  // and the rows' statistics
     fill.init(lds, lds + G0, group == 1 ? A.q.row : 0, group == 1 ? A.grad.row : 0, A.dim);
     HeadAddr<RB> qa(lds);
     RowsAddr<T, RB> qt(lds);
@@ -296,8 +296,7 @@ __global__ __launch_bounds__(64 * BWD_WAVES, DP * sizeof(T) > 128 ? 1 : 2) void 
         const uint32_t o = lane / 2 < left ? ((t - t0) * A.heads + (r - t * group)) * 8 + (lane & 1) * 4 : OUT_OF_RANGE;
         const uint32_t to = my_stat + (a & (RING - 1)) * (BWD_WAVES * 256);
         if constexpr (DIRECT) {
-            const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc((void *)sp, (short)0, 0x7fffffff, 0x00020000);
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (SC_LDS void *)(uintptr_t)to, 4, o, 0, 0, 0);
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(scalar_rsrc(sp, 0x7fffffff), (SC_LDS void *)(uintptr_t)__builtin_amdgcn_readfirstlane(to), 4, o, 0, 0, 0);
         } else {
             *(SC_LDS float *)(uintptr_t)(to + lane * 4) = o != OUT_OF_RANGE ? *(const float *)((const char *)sp + o) : 0.0f;
         }
