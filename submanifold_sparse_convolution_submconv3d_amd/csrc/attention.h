@@ -612,9 +612,13 @@ __device__ __forceinline__ void piece_rows(const Work &w, int64_t len, int64_t *
 constexpr int UNITS = 256;
 constexpr int blocks_at_once(int rb, int waves) { return UNITS * (waves < 163840 / (256 * rb + 4096) ? waves : 163840 / (256 * rb + 4096)); }
 
-// Whether tiles may be cut: a tile is long (64 steps and more of the other side on average), so
-// that a part of a round is worth the partial results and their join.
-static inline bool cut_pays(int64_t other_rows, int entries) { return entries + 2 <= 64 * EACH && other_rows / entries >= 2048; }
+// Whether tiles may be cut: a tile is long enough that a part of a round is worth the partial
+// results and their join (some 20 us): on average 64 steps of the other side in bf16, 16
+// in fp32, whose matrix products take eight times as long.
+static inline bool cut_pays(int64_t other_rows, int entries, int dtype)
+{
+    return entries + 2 <= 64 * EACH && other_rows / entries >= (dtype == SUBMCONV_F32 ? 512 : 2048);
+}
 
 // How a pass is split along its long side: runs of `chunk` rows (0: not cut), at most
 // `splits` of them in an entry, `tiles` tiles of the own side taken by different blocks.
@@ -623,6 +627,6 @@ struct SplitPlan {
     int64_t splits;
     int tiles;
 };
-SplitPlan split_plan(int64_t own_rows, int own_tile, int64_t other_rows, int other_tile, int entries, int kv_heads);
+SplitPlan split_plan(int64_t own_rows, int own_tile, int64_t other_rows, int other_tile, int entries, int kv_heads, int64_t slots);
 
 }  // namespace sc

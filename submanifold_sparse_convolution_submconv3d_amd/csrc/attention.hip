@@ -480,18 +480,21 @@ __global__ __launch_bounds__(256) void k_attn_join_cut(AttnArgs A)
     }
 }
 
-// How a pass over a long side is split when its own side has few tiles: enough runs that
-// all blocks together fill the card, none shorter than MIN_CHUNK rows.  chunk = 0: not at all.
-constexpr int64_t WANT_BLOCKS = 768, MIN_CHUNK = 64;
+// How a pass over a long side is split when its own side has few tiles, so few that they and
+// half as many more would still run at once (`slots` blocks do): into runs of at least
+// MIN_CHUNK rows, WANT_BLOCKS blocks in all, several to each place, since the entries and
+// the last runs are not alike (measured on 20384 x 4111 rows, 4 heads of 64, fp32, for the keys'
+// gradients: 768 blocks 538 us, 1536 466, 3072 490).  chunk = 0: not at all.
+constexpr int64_t WANT_BLOCKS = 1536, MIN_CHUNK = 64;
 
-SplitPlan split_plan(int64_t own_rows, int own_tile, int64_t other_rows, int other_tile, int entries, int kv_heads)
+SplitPlan split_plan(int64_t own_rows, int own_tile, int64_t other_rows, int other_tile, int entries, int kv_heads, int64_t slots)
 {
     SplitPlan p = {0, 0, 1};
     if (own_rows == 0 || other_rows == 0) return p;
     const int64_t per_entry = (own_rows / entries + own_tile - 1) / own_tile;
     int64_t tiles = per_entry > 0 ? per_entry : 1;
     const int64_t used = entries < own_rows ? entries : own_rows;
-    if (tiles * used * kv_heads * 2 > WANT_BLOCKS) return p;
+    if (tiles * used * kv_heads * 3 > slots * 2) return p;
     int64_t runs = WANT_BLOCKS / (tiles * kv_heads);
     if (runs > JOIN_MAX_SPLITS - 1) runs = JOIN_MAX_SPLITS - 1;
     int64_t chunk = (other_rows + runs - 1) / runs;
@@ -506,23 +509,25 @@ SplitPlan split_plan(int64_t own_rows, int own_tile, int64_t other_rows, int oth
     return p;
 }
 
-static SplitPlan fwd_plan(const AttnArgs &A)
+// Blocks that run at once (the launch bounds of k_attn).
+static int fwd_slots(const AttnArgs &A, int dtype)
 {
-    return split_plan(A.nq * A.group, 32 * FWD_WAVES, A.nk, 32, A.entries, A.kv_heads);
+    const int rb = (A.dim + 31) / 32 * 32 * (dtype == SUBMCONV_F32 ? 4 : 2);
+    return blocks_at_once(rb, rb > 256 ? 1 : rb > 128 ? 2 : 3);
 }
 
-// Blocks that run at once (the launch bounds of k_attn).
-static uint32_t fwd_slots(const AttnArgs &A, int dtype)
+static SplitPlan fwd_plan(const AttnArgs &A, int dtype)
 {
-    if (!cut_pays(A.nk, A.entries)) return 0;
-    const int rb = (A.dim + 31) / 32 * 32 * (dtype == SUBMCONV_F32 ? 4 : 2);
-    return (uint32_t)blocks_at_once(rb, rb > 256 ? 1 : rb > 128 ? 2 : 3);
+    return split_plan(A.nq * A.group, 32 * FWD_WAVES, A.nk, 32, A.entries, A.kv_heads, fwd_slots(A, dtype));
 }
+
+// The same where tiles may be cut, else 0.
+static uint32_t fwd_cut(const AttnArgs &A, int dtype) { return cut_pays(A.nk, A.entries, dtype) ? (uint32_t)fwd_slots(A, dtype) : 0; }
 
 size_t attention_workspace(const AttnArgs &A, int dtype)
 {
-    const SplitPlan p = fwd_plan(A);
-    const size_t rows = p.chunk ? (size_t)p.splits * A.nq * A.heads : (size_t)2 * fwd_slots(A, dtype) * 32 * FWD_WAVES;
+    const SplitPlan p = fwd_plan(A, dtype);
+    const size_t rows = p.chunk ? (size_t)p.splits * A.nq * A.heads : (size_t)2 * fwd_cut(A, dtype) * 32 * FWD_WAVES;
     return rows * (A.dim + 2) * sizeof(float);
 }
 
@@ -552,7 +557,7 @@ static int run_fwd(AttnArgs A, const SplitPlan &p, void *workspace, hipStream_t 
         SC_LAUNCHED("attention join");
         return SUBMCONV_OK;
     }
-    A.slots = DIRECT ? fwd_slots(A, sizeof(T) == 4 ? SUBMCONV_F32 : SUBMCONV_BF16) : 0;
+    A.slots = DIRECT ? fwd_cut(A, sizeof(T) == 4 ? SUBMCONV_F32 : SUBMCONV_BF16) : 0;
     A.part = (float *)workspace;
     A.part2 = A.part + (size_t)2 * A.slots * 32 * FWD_WAVES * A.dim;
     const int64_t work = ragged_tiles(A.nq, A.entries, A.group, 32 * FWD_WAVES) * A.kv_heads + 2 * A.slots;
@@ -567,7 +572,7 @@ static int run_fwd(AttnArgs A, const SplitPlan &p, void *workspace, hipStream_t 
 
 int attention(const AttnArgs &A, int dtype, void *workspace, hipStream_t st)
 {
-    const SplitPlan p = fwd_plan(A);
+    const SplitPlan p = fwd_plan(A, dtype);
     const int dp = (A.dim + 31) / 32;
 #define GO(T)                                                                                       \
     if (!direct(A, sizeof(T))) return run_fwd<T, 128, false>(A, p, workspace, st); \

@@ -507,34 +507,38 @@ VARIANTS(uint16_t, 128, true)
 VARIANTS(uint16_t, 128, false)
 #undef VARIANTS
 
-// One block to an output row: the splits' partial gradients of an [n, heads, dim] tensor
+// One wave to an output row: the splits' partial gradients of an [n, heads, dim] tensor
 // summed in order of their number and scaled, for one or two such tensors (blockIdx.y).
 // `other` is the side that was split.
+constexpr int SUM_WAVES = 4;
 template <typename T>
-__global__ __launch_bounds__(256) void k_attn_sum(Ragged own, Ragged other, int heads, int dim, int chunk,
-                                                  const float *__restrict__ part_a, float scale_a, Heads out_a,
-                                                  const float *__restrict__ part_b, float scale_b, Heads out_b)
+__global__ __launch_bounds__(64 * SUM_WAVES) void k_attn_sum(Ragged own, Ragged other, int heads, int dim, int chunk,
+                                                             const float *__restrict__ part_a, float scale_a, Heads out_a,
+                                                             const float *__restrict__ part_b, float scale_b, Heads out_b)
 {
+    __shared__ f32x4 acc[SUM_WAVES][64];
     const float *part = blockIdx.y ? part_b : part_a;
     const float scale = blockIdx.y ? scale_b : scale_a;
     const Heads out = blockIdx.y ? out_b : out_a;
-    __shared__ f32x4 acc[256];
-    const int64_t at = blockIdx.x, row = at / heads;
+    const int lane = lane_id(), wave = threadIdx.x >> 6;
+    const int64_t at = (int64_t)blockIdx.x * SUM_WAVES + wave, rows = own.n * heads;
+    const bool on = at < rows;
+    const int64_t row = on ? at / heads : 0;
     const int head = (int)(at - row * heads), p = find_part(own, row);
-    const bool real = p >= 1 && p <= own.entries;
+    const bool real = on && p >= 1 && p <= own.entries;
     const int64_t len = real ? (other.bound(p + 1) - other.bound(p)) * other.mult : 0;
     const int n = len > 0 ? (int)((len + chunk - 1) / chunk) : 0;
-    const int pieces = dim / 4, groups = 256 / pieces, g = threadIdx.x / pieces, e = threadIdx.x % pieces;
+    const int pieces = dim / 4, groups = 64 / pieces, g = lane / pieces, e = lane % pieces;
     f32x4 sum = {0, 0, 0, 0};
-    if (g < groups)
-        for (int s = g; s < n; s += groups) sum += *(const f32x4 *)(part + (s * own.n * heads + at) * dim + 4 * e);
-    acc[threadIdx.x] = sum;
-    __syncthreads();
-    if (g == 0) {
-        for (int i = 1; i < groups; ++i) sum += acc[i * pieces + e];
-        sum *= scale;
-        store4((T *)out.p + row * out.row + head * out.head + 4 * e, sum);
+    if (g < groups) {
+#pragma unroll 8
+        for (int s = g; s < n; s += groups) sum += *(const f32x4 *)(part + (s * rows + at) * dim + 4 * e);
     }
+    acc[wave][lane] = sum;
+    __syncthreads();
+    if (!on || g) return;
+    for (int i = 1; i < groups; ++i) sum += acc[wave][i * pieces + e];
+    store4((T *)out.p + row * out.row + head * out.head + 4 * e, sum * scale);
 }
 
 // The pieces of cut tiles summed and scaled, for one or two tensors (blockIdx.z): blockIdx.x
@@ -576,10 +580,12 @@ static BwdPlan bwd_plan(const AttnArgs &A, int dtype)
 {
     const int rb = (A.dim + 31) / 32 * 32 * (dtype == SUBMCONV_F32 ? 4 : 2);
     BwdPlan p;
-    p.q = split_plan(A.nq * A.group, BWD_ROWS, A.nk, 32, A.entries, A.kv_heads);
-    p.k = split_plan(A.nk, BWD_ROWS, A.nq * A.group, 32, A.entries, A.kv_heads);
-    p.q_slots = cut_pays(A.nk, A.entries) ? (uint32_t)blocks_at_once(rb, rb > 256 ? 1 : 2) : 0;
-    p.k_slots = cut_pays(A.nq * A.group, A.entries) ? (uint32_t)blocks_at_once(rb, rb > 128 ? 1 : 2) : 0;
+    // the launch bounds of k_attn_dq and k_attn_dkv
+    const int q_slots = blocks_at_once(rb, rb > 256 ? 1 : 2), k_slots = blocks_at_once(rb, rb > 128 ? 1 : 2);
+    p.q = split_plan(A.nq * A.group, BWD_ROWS, A.nk, 32, A.entries, A.kv_heads, q_slots);
+    p.k = split_plan(A.nk, BWD_ROWS, A.nq * A.group, 32, A.entries, A.kv_heads, k_slots);
+    p.q_slots = cut_pays(A.nk, A.entries, dtype) ? (uint32_t)q_slots : 0;
+    p.k_slots = cut_pays(A.nq * A.group, A.entries, dtype) ? (uint32_t)k_slots : 0;
     p.stat = ((size_t)A.nq * A.heads * 2 * sizeof(float) + 15) / 16 * 16;
     const size_t row = A.dim * sizeof(float), tile = BWD_ROWS * row;
     const size_t a = p.q.chunk ? (size_t)p.q.splits * A.nq * A.heads * row : 2 * p.q_slots * tile;
@@ -612,7 +618,7 @@ static int run_bwd(AttnArgs A, const BwdPlan &p, hipStream_t st)
             const int64_t work = ragged_tiles(A.nk, A.entries, 1, A.chunk) * A.kv_heads * A.tiles;
             hipLaunchKernelGGL((k_attn_dq<T, DP, true, DIRECT>), dim3(xcd_grid(work)), block, 0, st, A);
             SC_LAUNCHED("attention_backward queries (split)");
-            hipLaunchKernelGGL(k_attn_sum<T>, dim3((unsigned)(A.nq * A.heads)), dim3(256), 0, st, rq, rk, A.heads, A.dim,
+            hipLaunchKernelGGL(k_attn_sum<T>, dim3((unsigned)((A.nq * A.heads + SUM_WAVES - 1) / SUM_WAVES)), dim3(64 * SUM_WAVES), 0, st, rq, rk, A.heads, A.dim,
                                A.chunk, A.part, A.scale, A.dq, nullptr, 0.0f, Heads{});
         } else {
             A.slots = DIRECT ? p.q_slots : 0;
@@ -635,7 +641,7 @@ static int run_bwd(AttnArgs A, const BwdPlan &p, hipStream_t st)
             hipLaunchKernelGGL((k_attn_dkv<T, DP, true, DIRECT>), dim3(xcd_grid(work)), block, 0, st, A);
             SC_LAUNCHED("attention_backward keys (split)");
             const Ragged rows = {A.q_off, A.entries, A.nq, A.group};
-            hipLaunchKernelGGL(k_attn_sum<T>, dim3((unsigned)(A.nk * A.kv_heads), 2), dim3(256), 0, st, rk, rows, A.kv_heads,
+            hipLaunchKernelGGL(k_attn_sum<T>, dim3((unsigned)((A.nk * A.kv_heads + SUM_WAVES - 1) / SUM_WAVES), 2), dim3(64 * SUM_WAVES), 0, st, rk, rows, A.kv_heads,
                                A.dim, A.chunk, A.part, A.scale, A.dk, A.part2, 1.0f, A.dv);
         } else {
             A.slots = DIRECT ? p.k_slots : 0;
