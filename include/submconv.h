@@ -307,7 +307,7 @@ int submconv_layer_norm(const void *x, int64_t x_row, int64_t n, int32_t c, int3
                         const void *bias, int32_t param_dtype, float eps, void *y, int64_t y_row, float *stats,
                         void *stream);
 
-/* Bytes of device workspace submconv_layer_norm_backward needs (0 for bad sizes). */
+/* Bytes of device workspace submconv_layer_norm_backward needs (may be 0; 0 for bad sizes). */
 size_t submconv_layer_norm_backward_workspace(int64_t n, int32_t c, int32_t dtype);
 
 /*
@@ -321,7 +321,8 @@ size_t submconv_layer_norm_backward_workspace(int64_t n, int32_t c, int32_t dtyp
  *   workspace : device memory of submconv_layer_norm_backward_workspace bytes, 16-byte
  *            aligned, its contents undefined before and after (may be NULL when dweight
  *            and dbias are).
- * Asynchronous, one launch, and a second where dweight or dbias is wanted.
+ * Asynchronous, one launch, and a second where dweight or dbias is wanted and the rows
+ * take more than one block.
  */
 int submconv_layer_norm_backward(const void *grad, int64_t grad_row, const void *x, int64_t x_row, int64_t n,
                                  int32_t c, int32_t dtype, const float *stats, const void *weight,

@@ -501,18 +501,20 @@ def _row_stride(t: torch.Tensor) -> int:
 
 
 def _norm_params(x: torch.Tensor, weight: Optional[torch.Tensor], bias: Optional[torch.Tensor]) -> int:
-    """Type code of the parameter vectors (both fp32 or both of x's type)."""
+    """Type code of the parameter vectors (both fp32 or both bf16)."""
     code = None
+    index, shape = x.get_device(), x.shape[1:]
     for name, p in (("weight", weight), ("bias", bias)):
         if p is None:
             continue
-        if _dev(p, name).device != x.device:
+        if _dev(p, name).get_device() != index:
             raise ValueError("%s is on %s, not on %s" % (name, p.device, x.device))
-        if p.shape != (x.shape[1],):
+        if p.shape != shape:
             raise ValueError("%s must be [%d]" % (name, x.shape[1]))
-        if code is not None and code != _dtype_code(p):
+        kind = _dtype_code(p)
+        if code is not None and code != kind:
             raise TypeError("weight and bias must have one type")
-        code = _dtype_code(p)
+        code = kind
     return F32 if code is None else code
 
 
@@ -566,7 +568,7 @@ def submconv_layer_norm_backward(grad: torch.Tensor, x: torch.Tensor, stats: tor
     if need_params:
         dw, db = torch.empty((2, c), dtype=kind, device=dev).unbind(0)
         nbytes = lib.submconv_layer_norm_backward_workspace(n, c, _dtype_code(x))
-        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
     with _on_device(dev):
         _check(lib.submconv_layer_norm_backward(
             grad.data_ptr(), _row_stride(grad), x.data_ptr(), _row_stride(x), n, c, _dtype_code(x), stats.data_ptr(),

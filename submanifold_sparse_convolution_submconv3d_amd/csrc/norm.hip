@@ -17,6 +17,15 @@ __device__ __forceinline__ float param(const void *p, int dtype, int i)
     return dtype == SUBMCONV_F32 ? ((const float *)p)[i] : bf16_to_f32(((const uint16_t *)p)[i]);
 }
 
+__device__ __forceinline__ void set_param(void *p, int dtype, int i, float v)
+{
+    if (!p) return;
+    if (dtype == SUBMCONV_F32)
+        ((float *)p)[i] = v;
+    else
+        ((uint16_t *)p)[i] = f32_to_bf16(v);
+}
+
 // Sum of v over the TPR threads of a row.  TPR = 256: the whole block, through LDS;
 // `slot` alternates between the two halves of `part`, so one barrier a sum is enough.
 template <int TPR>
@@ -95,12 +104,14 @@ __global__ __launch_bounds__(256) void k_norm(const T *__restrict__ x, int64_t l
 
 // dx, and each block's share of dw and db over its rows: kept in registers by the
 // thread that owns the channel, summed over the block's row groups through LDS in a
-// fixed order, written to partial [block][2][c] and summed over blocks by k_norm_wgrad.
+// fixed order, written to partial [block][2][c] and summed over blocks by k_norm_wgrad; a
+// single block writes dw and db itself (partial is NULL).
 template <typename T, int CH, int TPR>
 __global__ __launch_bounds__(256) void k_norm_bwd(const T *__restrict__ gy, int64_t ldg, const T *__restrict__ x,
                                                   int64_t ldx, int64_t n, int c, const float2 *__restrict__ stats,
                                                   const void *__restrict__ w, int pdtype, T *__restrict__ dx,
-                                                  int64_t lddx, float *__restrict__ partial)
+                                                  int64_t lddx, float *__restrict__ partial, void *__restrict__ dw_out,
+                                                  void *__restrict__ db_out)
 {
     constexpr int V = VEC<T>, RPB = 256 / TPR, CPAD = CH * TPR * V;
     __shared__ float part[16];
@@ -167,8 +178,12 @@ __global__ __launch_bounds__(256) void k_norm_bwd(const T *__restrict__ gy, int6
             }
         }
     }
-    if (!partial) return;
-    float *mine = partial + (int64_t)blockIdx.x * 2 * c;
+    if (!partial && !dw_out && !db_out) return;
+    float *mine = partial ? partial + (int64_t)blockIdx.x * 2 * c : nullptr;
+    auto put = [&](int p, int e, float v) {
+        if (mine) mine[p * c + e] = v;
+        else set_param(p ? db_out : dw_out, pdtype, e, v);
+    };
 #pragma unroll
     for (int p = 0; p < 2; ++p) {
         if constexpr (RPB > 1) {
@@ -182,14 +197,14 @@ __global__ __launch_bounds__(256) void k_norm_bwd(const T *__restrict__ gy, int6
                 float s = 0.0f;
 #pragma unroll 8
                 for (int r = 0; r < RPB; ++r) s += red[r * CPAD + e];
-                mine[p * c + e] = s;
+                put(p, e, s);
             }
         } else {
 #pragma unroll
             for (int i = 0; i < CH; ++i)
 #pragma unroll
                 for (int j = 0; j < V; ++j)
-                    if (j < nv[i]) mine[p * c + (i * TPR + t) * V + j] = p ? db[i][j] : dw[i][j];
+                    if (j < nv[i]) put(p, (i * TPR + t) * V + j, p ? db[i][j] : dw[i][j]);
         }
     }
 }
@@ -216,14 +231,7 @@ __global__ __launch_bounds__(256) void k_norm_wgrad(const float *__restrict__ pa
         for (int o = 8; o; o >>= 1)
 #pragma unroll
             for (int i = 0; i < o; ++i) v[i] += v[i + o];
-        void *d = col < c ? dw : db;
-        const int e = col < c ? col : col - c;
-        if (d) {
-            if (pdtype == SUBMCONV_F32)
-                ((float *)d)[e] = v[0];
-            else
-                ((uint16_t *)d)[e] = f32_to_bf16(v[0]);
-        }
+        set_param(col < c ? dw : db, pdtype, col < c ? col : col - c, v[0]);
     }
 }
 
@@ -258,10 +266,20 @@ static int64_t norm_blocks(int64_t n, int c, int dtype, int64_t most)
 
 constexpr int64_t NORM_FWD_BLOCKS = 2048;  // eight to a compute unit
 constexpr int64_t NORM_BWD_BLOCKS = 1024;
+// Row groups that one block walks in less time than a second launch takes (450 rows of 16
+// channels: 8 blocks and the sum over them 17.3 us a call, one block 13.9).
+constexpr int64_t NORM_BWD_ALONE = 8;
+
+static int64_t norm_bwd_blocks(int64_t n, int c, int dtype)
+{
+    const int64_t b = norm_blocks(n, c, dtype, NORM_BWD_BLOCKS);
+    return b > 0 && b <= NORM_BWD_ALONE ? 1 : b;
+}
 
 size_t norm_bwd_workspace(int64_t n, int c, int dtype)
 {
-    return (size_t)norm_blocks(n, c, dtype, NORM_BWD_BLOCKS) * 2 * c * sizeof(float);
+    const int64_t blocks = norm_bwd_blocks(n, c, dtype);
+    return blocks == 1 ? 0 : (size_t)blocks * 2 * c * sizeof(float);
 }
 
 #define NORM_SHAPES(T, GO)                                                         \
@@ -304,13 +322,15 @@ int layer_norm_backward(const void *gy, int64_t ldg, const void *x, int64_t ldx,
                         void *workspace, hipStream_t st)
 {
     const NormShape s = norm_shape(c, dtype);
-    const int64_t blocks = norm_blocks(n, c, dtype, NORM_BWD_BLOCKS);
-    float *partial = dw || db ? (float *)workspace : nullptr;
+    const int64_t blocks = norm_bwd_blocks(n, c, dtype);
+    const bool alone = blocks == 1;
+    float *partial = (dw || db) && !alone ? (float *)workspace : nullptr;
     if (n > 0) {
         const dim3 grid((unsigned)blocks);
 #define GO(T, CH, TPR)                                                                                          \
     hipLaunchKernelGGL((k_norm_bwd<T, CH, TPR>), grid, dim3(256), 0, st, (const T *)gy, ldg, (const T *)x, ldx, \
-                       n, c, (const float2 *)stats, w, pdtype, (T *)dx, lddx, partial)
+                       n, c, (const float2 *)stats, w, pdtype, (T *)dx, lddx, partial, alone ? dw : nullptr,       \
+                       alone ? db : nullptr)
         if (dtype == SUBMCONV_F32) {
             NORM_SHAPES(float, GO)
         } else {
@@ -319,7 +339,7 @@ int layer_norm_backward(const void *gy, int64_t ldg, const void *x, int64_t ldx,
 #undef GO
         SC_LAUNCHED("layer_norm_backward");
     }
-    if (dw || db) {
+    if ((dw || db) && !alone) {
         hipLaunchKernelGGL(k_norm_wgrad, dim3((unsigned)((2 * c + 15) / 16)), dim3(256), 0, st, partial, (int)blocks,
                            c, dw, db, pdtype);
         SC_LAUNCHED("layer_norm_backward sums");

@@ -36,13 +36,13 @@ def test_layer_norm_refusals(lib):
     assert norm(lib, y=ctypes.c_void_p((1 << 32) + 252), x_row=128, y_row=128) == E_ALIAS
 
 
-def norm_bwd(lib, g=P(1), g_row=64, x=P(2), x_row=64, n=10, c=64, dtype=1, stats=P(3), w=P(4), pdtype=0, dx=P(5), dx_row=64,
+def norm_bwd(lib, g=P(1), g_row=64, x=P(2), x_row=64, n=1000, c=64, dtype=1, stats=P(3), w=P(4), pdtype=0, dx=P(5), dx_row=64,
              dw=P(6), db=P(7), ws=P(8), nbytes=1 << 20):
     return lib.submconv_layer_norm_backward(g, g_row, x, x_row, n, c, dtype, stats, w, pdtype, dx, dx_row, dw, db, ws, nbytes, None)
 
 
 def test_layer_norm_backward_refusals(lib):
-    need = lib.submconv_layer_norm_backward_workspace(10, 64, 1)
+    need = lib.submconv_layer_norm_backward_workspace(1000, 64, 1)
     assert need > 0 and need % 4 == 0
     assert lib.submconv_layer_norm_backward_workspace(-1, 64, 1) == 0
     assert lib.submconv_layer_norm_backward_workspace(10, 9000, 1) == 0
