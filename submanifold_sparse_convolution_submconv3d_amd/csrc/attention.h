@@ -499,33 +499,23 @@ __device__ __forceinline__ float rows_piece(const RowsAddr<float, RB> &ad, uint3
     return *(const SC_LDS float *)(uintptr_t)(ad.at[i & 7][db] + at + 16 * (i >> 3) * RB);
 }
 
-// acc[x][db] += transpose(32 tile rows) p[x], for every 32 elements db of the head; `at` is
-// added to the addresses.
-template <int RB, int N>
-__device__ __forceinline__ void mma_rows(const RowsAddr<uint16_t, RB> &ad, uint32_t at, const RowsOperand<uint16_t> (&p)[N],
-                                         f32x16 (&acc)[N][RB / 64])
+// acc[db] += transpose(32 tile rows) p, for every 32 elements db of the head; `at` is added to the
+// addresses.
+template <int RB>
+__device__ __forceinline__ void mma_rows(const RowsAddr<uint16_t, RB> &ad, uint32_t at, const RowsOperand<uint16_t> &p,
+                                         f32x16 (&acc)[RB / 64])
 {
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int db = 0; db < RB / 64; ++db) {
-            const Raw16 v = rows_piece<RB>(ad, at, h * (RB / 64) + db);
-#pragma unroll
-            for (int x = 0; x < N; ++x) acc[x][db] = mma_pieces<uint16_t>(v, p[x].v[h], acc[x][db]);
-        }
+    for (int x = 0; x < 2 * (RB / 64); ++x)
+        acc[x % (RB / 64)] = mma_pieces<uint16_t>(rows_piece<RB>(ad, at, x), p.v[x / (RB / 64)], acc[x % (RB / 64)]);
 }
-template <int RB, int N>
-__device__ __forceinline__ void mma_rows(const RowsAddr<float, RB> &ad, uint32_t at, const RowsOperand<float> (&p)[N],
-                                         f32x16 (&acc)[N][RB / 128])
+template <int RB>
+__device__ __forceinline__ void mma_rows(const RowsAddr<float, RB> &ad, uint32_t at, const RowsOperand<float> &p,
+                                         f32x16 (&acc)[RB / 128])
 {
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
-#pragma unroll
-        for (int db = 0; db < RB / 128; ++db) {
-            const float v = rows_piece<RB>(ad, at, i * (RB / 128) + db);
-#pragma unroll
-            for (int x = 0; x < N; ++x) acc[x][db] = __builtin_amdgcn_mfma_f32_32x32x2f32(v, p[x].v[i], acc[x][db], 0, 0, 0);
-        }
+    for (int x = 0; x < 16 * (RB / 128); ++x)
+        acc[x % (RB / 128)] = __builtin_amdgcn_mfma_f32_32x32x2f32(rows_piece<RB>(ad, at, x), p.v[x / (RB / 128)], acc[x % (RB / 128)], 0, 0, 0);
 }
 
 // The other half's value (lanes l and l ^ 32).
@@ -594,7 +584,6 @@ struct AttnArgs {
     float *part;   // partial results of a split pass
     float *part2;
     int chunk;     // rows of the long side in one split
-    int64_t splits;
     int tiles;     // tiles of the short side taken by different blocks
     uint32_t slots;  // blocks that run at once, for cutting tiles (0: none are cut)
 };

@@ -77,14 +77,15 @@ constexpr int FWD_WAVES = 4, RING = 4;
 // maximum is found meanwhile.  Keys and values are copied three steps ahead, into rings of
 // four tiles in LDS.
 //
-// QB: blocks of 32 query rows a wave owns.  SPLIT: a block takes one run of `chunk` keys of
+// SPLIT: a block takes one run of `chunk` keys of
 // an entry and leaves (sum, m, l) of it in part / part2 for k_attn_join; otherwise a block
 // takes one tile of query rows over all keys.
+constexpr int fwd_residency(int rb) { return rb > 256 ? 1 : rb > 128 ? 2 : rb > 64 ? 3 : 4; }  // waves a SIMD
+
 template <typename T, int DP, bool SPLIT, bool DIRECT>
-__global__ __launch_bounds__(64 * FWD_WAVES, DP * sizeof(T) > 256 ? 1 : DP * sizeof(T) > 128 ? 2 : 3) void k_attn(AttnArgs A)
+__global__ __launch_bounds__(64 * FWD_WAVES, fwd_residency(DP * sizeof(T))) void k_attn(AttnArgs A)
 {
     constexpr int RB = DP * (int)sizeof(T), NJ = RB / 32, DB = DP / 32, TILE = 32 * RB, ROWS = 32 * FWD_WAVES;
-    constexpr int QB = 1;
     constexpr uint32_t V0 = RING * TILE;  // the values' ring
     __shared__ __attribute__((aligned(1024))) char smem[2 * RING * TILE];
     const uint32_t lds = (uint32_t)(uintptr_t)(SC_LDS char *)smem;
@@ -106,6 +107,7 @@ __global__ __launch_bounds__(64 * FWD_WAVES, DP * sizeof(T) > 256 ? 1 : DP * siz
     const int64_t q_beg = SPLIT ? w.other_beg : w.own_beg, k_beg = SPLIT ? w.own_beg : w.other_beg;
     const int64_t rows = (SPLIT ? w.other_len : w.own_len) * A.group;
     int64_t keys64 = (SPLIT ? w.own_len : w.other_len) - key0;
+    if (SPLIT && keys64 <= 0) return;  // a number without a run (see first_tile)
     if (SPLIT && keys64 > A.chunk) keys64 = A.chunk;
     if (!SPLIT && w.pieces > 1) {
         piece_rows(w, w.other_len, &key0, &keys64);
@@ -123,7 +125,7 @@ __global__ __launch_bounds__(64 * FWD_WAVES, DP * sizeof(T) > 256 ? 1 : DP * siz
     RowsAddr<T, RB> va(lds + V0);
 
     for (; qtile * ROWS < rows; qtile += SPLIT ? A.tiles : rows) {
-        const int64_t wave_row = qtile * ROWS + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) * (32 * QB);
+        const int64_t wave_row = qtile * ROWS + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) * 32;
         if (SPLIT) __syncthreads();  // the rings' last readers are done
         fill.start(kp, vp, keys);
         // keys 0 .. 2 and values 0 .. 1; then, before every pair of steps u, u + 1, keys u + 3 and
@@ -143,118 +145,86 @@ __global__ __launch_bounds__(64 * FWD_WAVES, DP * sizeof(T) > 256 ? 1 : DP * siz
             continue;
         }
 
-        Raw16 q[QB][NJ];
+        Raw16 q[NJ];
+        const uint32_t row = (uint32_t)(wave_row + (lane & 31)), token = A.group == 1 ? row : row / A.group;
+        const int head = hk * A.group + (int)(row - token * A.group);
+        const bool valid = row < rows;
+        const T *qp = (const T *)A.q.p + (q_beg + token) * A.q.row + head * A.q.head;
 #pragma unroll
-        for (int qb = 0; qb < QB; ++qb) {
-            const uint32_t row = (uint32_t)(wave_row + 32 * qb + (lane & 31)), token = A.group == 1 ? row : row / A.group;
-            const bool valid = row < rows;
-            const T *qp = (const T *)A.q.p + (q_beg + token) * A.q.row + (hk * A.group + (row - token * A.group)) * A.q.head;
-#pragma unroll
-            for (int j = 0; j < NJ; ++j) {
-                const int e = (2 * j + half) * VEC<T>;
-                q[qb][j] = Raw16{0, 0, 0, 0};
-                if (valid && e < A.dim) q[qb][j] = *(const Raw16Any *)(qp + e);
-            }
+        for (int j = 0; j < NJ; ++j) {
+            const int e = (2 * j + half) * VEC<T>;
+            q[j] = Raw16{0, 0, 0, 0};
+            if (valid && e < A.dim) q[j] = *(const Raw16Any *)(qp + e);
         }
-        f32x16 o[QB][DB], s[2][QB];
-        float m[QB], l[QB], base[QB];
+        f32x16 o[DB], s[2];
+        float m = -INFINITY, l = 0.0f, base = 0.0f;
         uint64_t big = 0;  // some row's maximum is huge
 #pragma unroll
-        for (int qb = 0; qb < QB; ++qb) {
-            m[qb] = -INFINITY;
-            l[qb] = base[qb] = 0.0f;
-#pragma unroll
-            for (int db = 0; db < DB; ++db) o[qb][db] = f32x16{};
-        }
+        for (int db = 0; db < DB; ++db) o[db] = f32x16{};
 
         // scores of the keys in ring place `at`
-        auto scores = [&](f32x16(&t)[QB], uint32_t at) {
-#pragma unroll
-            for (int qb = 0; qb < QB; ++qb) t[qb] = f32x16{};
+        auto scores = [&](f32x16 &t, uint32_t at) {
+            t = f32x16{};
 #pragma unroll
             for (int j = 0; j < NJ; ++j) {
                 const Raw16 k = lds_read16(ka.at[j] + at);
-#pragma unroll
-                for (int qb = 0; qb < QB; ++qb) t[qb] = mma_pieces<T>(k, q[qb][j], t[qb]);
+                t = mma_pieces<T>(k, q[j], t);
             }
         };
         // scores of step u past the last key are none
-        auto mask = [&](f32x16(&t)[QB], int u) {
+        auto mask = [&](f32x16 &t, int u) {
             if (__builtin_expect(keys - u * 32 < 32, 0)) {
 #pragma unroll
-                for (int qb = 0; qb < QB; ++qb)
-#pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        if (8 * (i / 4) + 4 * half + i % 4 >= keys - u * 32) t[qb][i] = -INFINITY;
+                for (int i = 0; i < 16; ++i)
+                    if (8 * (i / 4) + 4 * half + i % 4 >= keys - u * 32) t[i] = -INFINITY;
             }
         };
         // with the scores' maximum of this half's keys, everything their weights need
-        auto settle = [&](f32x16(&t)[QB], float(&top)[QB]) {
-            bool moved = false;
-            float f[QB];
-#pragma unroll
-            for (int qb = 0; qb < QB; ++qb) {
-                top[qb] = fmaxf(top[qb], other_half(top[qb]));
-                moved |= (top[qb] - m[qb]) * c > SLACK;
-                f[qb] = 1.0f;
-            }
-            const uint64_t any = __ballot(moved);
+        auto settle = [&](f32x16 &t, float &top) {
+            float f = 1.0f;
+            top = fmaxf(top, other_half(top));
+            const uint64_t any = __ballot((top - m) * c > SLACK);
             if (__builtin_expect(any != 0, 0)) {
-                bool b = false;
-#pragma unroll
-                for (int qb = 0; qb < QB; ++qb) {
-                    const float next = fmaxf(m[qb], top[qb]);
-                    f[qb] = rescale(m[qb], next, c);
-                    m[qb] = next;
-                    l[qb] *= f[qb];
-                    base[qb] = next == -INFINITY || huge(next, c) ? 0.0f : next * c;  // -inf: weights are exp(-inf)
-                    b |= huge(next, c);
-                }
-                big = __ballot(b);
+                const float next = fmaxf(m, top);
+                f = rescale(m, next, c);
+                m = next;
+                l *= f;
+                base = next == -INFINITY || huge(next, c) ? 0.0f : next * c;  // -inf: weights are exp(-inf)
+                big = __ballot(huge(next, c));
             }
 #pragma unroll
-            for (int qb = 0; qb < QB; ++qb)
-#pragma unroll
-                for (int db = 0; db < DB; ++db) scale_if(o[qb][db], f[qb], any);
+            for (int db = 0; db < DB; ++db) scale_if(o[db], f, any);
             if (__builtin_expect(big != 0, 0)) {  // differences of scores in the scores' place
+                const bool mine = huge(m, c);
 #pragma unroll
-                for (int qb = 0; qb < QB; ++qb) {
-                    const bool mine = huge(m[qb], c);
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) t[qb][i] = mine ? t[qb][i] - m[qb] : t[qb][i];
-                }
+                for (int i = 0; i < 16; ++i) t[i] = mine ? t[i] - m : t[i];
             }
         };
-        auto maximum = [&](const f32x16(&t)[QB], float(&top)[QB], int from, int to) {
+        auto maximum = [&](const f32x16 &t, float &top, int from, int to) {
 #pragma unroll
-            for (int qb = 0; qb < QB; ++qb)
-#pragma unroll
-                for (int i = from; i < to; ++i) top[qb] = i ? fmaxf(top[qb], t[qb][i]) : t[qb][i];
+            for (int i = from; i < to; ++i) top = i ? fmaxf(top, t[i]) : t[i];
         };
-        auto weights = [&](f32x16(&t)[QB], int from, int to) {
+        auto weights = [&](f32x16 &t, int from, int to) {
 #pragma unroll
-            for (int qb = 0; qb < QB; ++qb)
-#pragma unroll
-                for (int i = from; i < to; ++i) {
-                    t[qb][i] = __builtin_amdgcn_exp2f(fmaf(t[qb][i], c, -base[qb]));
-                    l[qb] += t[qb][i];
-                }
+            for (int i = from; i < to; ++i) {
+                t[i] = __builtin_amdgcn_exp2f(fmaf(t[i], c, -base));
+                l += t[i];
+            }
         };
-        auto product = [&](f32x16(&t)[QB], uint32_t vat) {
-            RowsOperand<T> p[QB];
-#pragma unroll
-            for (int qb = 0; qb < QB; ++qb) p[qb].set(t[qb]);
+        auto product = [&](f32x16 &t, uint32_t vat) {
+            RowsOperand<T> p;
+            p.set(t);
             mma_rows<RB>(va, vat, p, o);
         };
         // step u from scores t, leaving the next step's in n; kat, vat: the tiles' places past ka and va
-        auto step = [&](f32x16(&t)[QB], f32x16(&n)[QB], int u, uint32_t kat, uint32_t vat) {
-            float top[QB];
+        auto step = [&](f32x16 &t, f32x16 &n, int u, uint32_t kat, uint32_t vat) {
+            float top;
             if constexpr (sizeof(T) == 2) {
                 // in the order it is to run: LDS reads AHEAD of their use, and between the matrix
                 // products a piece of the arithmetic; first the scores with half the weights, then
                 // their product with the values, with the other half and the maximum
                 constexpr int AHEAD = NJ < 4 ? NJ : 4;
-                Raw16 k[NJ], v[2 * DB], p[QB][2];
+                Raw16 k[NJ], v[2 * DB], p[2];
 #pragma unroll
                 for (int j = 0; j < AHEAD; ++j) k[j] = lds_read16(ka.at[j] + kat);
                 __builtin_amdgcn_sched_barrier(0);
@@ -262,26 +232,20 @@ __global__ __launch_bounds__(64 * FWD_WAVES, DP * sizeof(T) > 256 ? 1 : DP * siz
                 for (int j = 0; j < NJ; ++j) {
                     if (j + AHEAD < NJ) k[j + AHEAD] = lds_read16(ka.at[j + AHEAD] + kat);
                     else if (j + AHEAD - NJ < 2 && j + AHEAD - NJ < 2 * DB) v[j + AHEAD - NJ] = rows_piece<RB>(va, vat, j + AHEAD - NJ);
-#pragma unroll
-                    for (int qb = 0; qb < QB; ++qb) n[qb] = mma_pieces<T>(k[j], q[qb][j], j ? n[qb] : f32x16{});
+                    n = mma_pieces<T>(k[j], q[j], j ? n : f32x16{});
                     weights(t, 8 * j / NJ, 8 * (j + 1) / NJ);
                     __builtin_amdgcn_sched_barrier(0);
                 }
-#pragma unroll
-                for (int qb = 0; qb < QB; ++qb) p[qb][0] = pack8(t[qb], 0);
+                p[0] = pack8(t, 0);
                 mask(n, u + 1);
 #pragma unroll
                 for (int x = 0; x < 2 * DB; ++x) {
                     const int h = x / DB, db = x % DB;
                     if (x + 2 < 2 * DB) v[x + 2] = rows_piece<RB>(va, vat, x + 2);
-#pragma unroll
-                    for (int qb = 0; qb < QB; ++qb) o[qb][db] = mma_pieces<T>(v[x], p[qb][h], o[qb][db]);
+                    o[db] = mma_pieces<T>(v[x], p[h], o[db]);
                     if (h == 0) weights(t, 8 + 8 * db / DB, 8 + 8 * (db + 1) / DB);
                     else maximum(n, top, 16 * db / DB, 16 * (db + 1) / DB);
-                    if (x == DB - 1) {
-#pragma unroll
-                        for (int qb = 0; qb < QB; ++qb) p[qb][1] = pack8(t[qb], 1);
-                    }
+                    if (x == DB - 1) p[1] = pack8(t, 1);
                     __builtin_amdgcn_sched_barrier(0);
                 }
             } else {
@@ -300,8 +264,7 @@ __global__ __launch_bounds__(64 * FWD_WAVES, DP * sizeof(T) > 256 ? 1 : DP * siz
                         for (int x = 0; x < FAR / AHEAD; ++x)
                             v[(j + AHEAD - NJ) * (FAR / AHEAD) + x] = rows_piece<RB>(va, vat, (j + AHEAD - NJ) * (FAR / AHEAD) + x);
                     }
-#pragma unroll
-                    for (int qb = 0; qb < QB; ++qb) n[qb] = mma_pieces<T>(k[j], q[qb][j], j ? n[qb] : f32x16{});
+                    n = mma_pieces<T>(k[j], q[j], j ? n : f32x16{});
                     weights(t, 8 * j / NJ, 8 * (j + 1) / NJ);
                     __builtin_amdgcn_sched_barrier(0);
                 }
@@ -310,8 +273,7 @@ __global__ __launch_bounds__(64 * FWD_WAVES, DP * sizeof(T) > 256 ? 1 : DP * siz
                 for (int x = 0; x < 16 * DB; ++x) {
                     const int i = x / DB, db = x % DB;
                     if (x + FAR < 16 * DB) v[x + FAR] = rows_piece<RB>(va, vat, x + FAR);
-#pragma unroll
-                    for (int qb = 0; qb < QB; ++qb) o[qb][db] = __builtin_amdgcn_mfma_f32_32x32x2f32(v[x], t[qb][i], o[qb][db], 0, 0, 0);
+                    o[db] = __builtin_amdgcn_mfma_f32_32x32x2f32(v[x], t[i], o[db], 0, 0, 0);
                     if (db == 0) {
                         if (i < 8) weights(t, 8 + i, 9 + i);
                         else maximum(n, top, 2 * (i - 8), 2 * (i - 8) + 2);
@@ -324,7 +286,7 @@ __global__ __launch_bounds__(64 * FWD_WAVES, DP * sizeof(T) > 256 ? 1 : DP * siz
 
         if (steps) {
             wait_copies_and_barrier<0>();
-            float top[QB];
+            float top;
             scores(s[0], 0);
             mask(s[0], 0);
             maximum(s[0], top, 0, 16);
@@ -354,25 +316,19 @@ __global__ __launch_bounds__(64 * FWD_WAVES, DP * sizeof(T) > 256 ? 1 : DP * siz
                 va.move(-2 * TILE);
             }
         }
-#pragma unroll
-        for (int qb = 0; qb < QB; ++qb) {
-            const uint32_t row = (uint32_t)(wave_row + 32 * qb + (lane & 31)), token = A.group == 1 ? row : row / A.group;
-            const int head = hk * A.group + (int)(row - token * A.group);
-            const bool valid = row < rows;
-            const float sum = l[qb] + other_half(l[qb]);
-            if constexpr (SPLIT) {
-                const int64_t at = split * A.nq * A.heads + (q_beg + token) * A.heads + head;
-                store_rows<float>(o[qb], 1.0f, A.part + at * A.dim, A.dim, valid);
-                if (valid && half == 0) *(float2 *)(A.part2 + 2 * at) = make_float2(m[qb], sum);
-            } else if (w.pieces > 1) {
-                const int64_t at = (int64_t)w.index * ROWS + (threadIdx.x >> 6) * (32 * QB) + 32 * qb + (lane & 31);
-                store_rows<float>(o[qb], 1.0f, A.part + at * A.dim, A.dim, valid);
-                if (valid && half == 0) *(float2 *)(A.part2 + 2 * at) = make_float2(m[qb], sum);
-            } else {
-                T *op = (T *)A.out.p + (q_beg + token) * A.out.row + head * A.out.head;
-                store_rows<T>(o[qb], sum > 0.0f ? 1.0f / sum : (sum == 0.0f ? 0.0f : sum), op, A.dim, valid);
-                if (A.lse && valid && half == 0) A.lse[(q_beg + token) * A.heads + head] = log_sum(m[qb], sum, A.scale);
-            }
+        const float sum = l + other_half(l);
+        if constexpr (SPLIT) {
+            const int64_t at = split * A.nq * A.heads + (q_beg + token) * A.heads + head;
+            store_rows<float>(o, 1.0f, A.part + at * A.dim, A.dim, valid);
+            if (valid && half == 0) *(float2 *)(A.part2 + 2 * at) = make_float2(m, sum);
+        } else if (w.pieces > 1) {
+            const int64_t at = (int64_t)w.index * ROWS + (threadIdx.x >> 6) * 32 + (lane & 31);
+            store_rows<float>(o, 1.0f, A.part + at * A.dim, A.dim, valid);
+            if (valid && half == 0) *(float2 *)(A.part2 + 2 * at) = make_float2(m, sum);
+        } else {
+            T *op = (T *)A.out.p + (q_beg + token) * A.out.row + head * A.out.head;
+            store_rows<T>(o, sum > 0.0f ? 1.0f / sum : (sum == 0.0f ? 0.0f : sum), op, A.dim, valid);
+            if (A.lse && valid && half == 0) A.lse[(q_beg + token) * A.heads + head] = log_sum(m, sum, A.scale);
         }
     }
 }
@@ -516,11 +472,11 @@ SplitPlan split_plan(int64_t own_rows, int own_tile, int64_t other_rows, int oth
     return p;
 }
 
-// Blocks that run at once (the launch bounds of k_attn).
+// Blocks that run at once.
 static int fwd_slots(const AttnArgs &A, int dtype)
 {
     const int rb = (A.dim + 31) / 32 * 32 * (dtype == SUBMCONV_F32 ? 4 : 2);
-    return blocks_at_once(rb, rb > 256 ? 1 : rb > 128 ? 2 : 3);
+    return blocks_at_once(rb, fwd_residency(rb));
 }
 
 static SplitPlan fwd_plan(const AttnArgs &A, int dtype)
@@ -551,7 +507,6 @@ static int run_fwd(AttnArgs A, const SplitPlan &p, void *workspace, hipStream_t 
     const dim3 block(64 * FWD_WAVES);
     if (p.chunk) {
         A.chunk = p.chunk;
-        A.splits = p.splits;
         A.tiles = p.tiles;
         A.part = (float *)workspace;
         A.part2 = A.part + p.splits * A.nq * A.heads * A.dim;

@@ -24,8 +24,10 @@ __device__ __forceinline__ float lse_base(float lse) { return lse == -INFINITY ?
 // steps ahead into rings of four tiles in LDS.  Leaves (base, delta) of every query
 // row for k_attn_dkv.  7042 + 5906 rows x 8 x 128 bf16: 472 us, 1.10 PFLOP/s of its three
 // products.
+constexpr int dq_residency(int rb) { return rb > 256 ? 1 : 2; }  // waves a SIMD
+
 template <typename T, int DP, bool SPLIT, bool DIRECT>
-__global__ __launch_bounds__(64 * BWD_WAVES, DP * sizeof(T) > 256 ? 1 : 2) void k_attn_dq(AttnArgs A)
+__global__ __launch_bounds__(64 * BWD_WAVES, dq_residency(DP * sizeof(T))) void k_attn_dq(AttnArgs A)
 {
     constexpr int RB = DP * (int)sizeof(T), NJ = RB / 32, DB = DP / 32, TILE = 32 * RB;
     constexpr uint32_t V0 = RING * TILE;
@@ -49,6 +51,7 @@ __global__ __launch_bounds__(64 * BWD_WAVES, DP * sizeof(T) > 256 ? 1 : 2) void 
     const int64_t q_beg = SPLIT ? w.other_beg : w.own_beg, k_beg = SPLIT ? w.own_beg : w.other_beg;
     const int64_t rows = (SPLIT ? w.other_len : w.own_len) * A.group;
     int64_t keys64 = (SPLIT ? w.own_len : w.other_len) - key0;
+    if (SPLIT && keys64 <= 0) return;  // a number without a run (see first_tile)
     if (SPLIT && keys64 > A.chunk) keys64 = A.chunk;
     if (!SPLIT && w.pieces > 1) {
         piece_rows(w, w.other_len, &key0, &keys64);
@@ -112,9 +115,9 @@ __global__ __launch_bounds__(64 * BWD_WAVES, DP * sizeof(T) > 256 ? 1 : 2) void 
         delta += other_half(delta);
         if (valid && half == 0 && split == 0 && w.piece == 0) *(float2 *)(A.stat + 2 * at) = make_float2(base, delta);
 
-        f32x16 dq[1][DB], s[2], dp[2];
+        f32x16 dq[DB], s[2], dp[2];
 #pragma unroll
-        for (int db = 0; db < DB; ++db) dq[0][db] = f32x16{};
+        for (int db = 0; db < DB; ++db) dq[db] = f32x16{};
         auto products = [&](f32x16 &t, f32x16 &e, uint32_t place) {
             t = e = f32x16{};
 #pragma unroll
@@ -135,9 +138,9 @@ __global__ __launch_bounds__(64 * BWD_WAVES, DP * sizeof(T) > 256 ? 1 : 2) void 
             for (int i = from; i < to; ++i) t[i] = __builtin_amdgcn_exp2f(fmaf(t[i], c, -base)) * (e[i] - delta);
         };
         auto gradient = [&](f32x16 &t, const f32x16 &e, uint32_t place) {
-            RowsOperand<T> ds[1];
+            RowsOperand<T> ds;
             weigh(t, e, 0, 16);
-            ds[0].set(t);
+            ds.set(t);
             mma_rows<RB>(kt, place, ds, dq);
         };
         auto step = [&](f32x16 &t, f32x16 &e, f32x16 &nt, f32x16 &ne, int u, uint32_t next_at, uint32_t own_at) {
@@ -172,7 +175,7 @@ __global__ __launch_bounds__(64 * BWD_WAVES, DP * sizeof(T) > 256 ? 1 : 2) void 
 #pragma unroll
                 for (int x = 0; x < 2 * DB; ++x) {
                     if (x + AHEAD < 2 * DB) r[x + AHEAD] = rows_piece<RB>(kt, own_at, x + AHEAD);
-                    dq[0][x % DB] = mma_pieces<T>(r[x], ds[x / DB], dq[0][x % DB]);
+                    dq[x % DB] = mma_pieces<T>(r[x], ds[x / DB], dq[x % DB]);
                     __builtin_amdgcn_sched_barrier(0);
                 }
             } else {
@@ -203,7 +206,7 @@ __global__ __launch_bounds__(64 * BWD_WAVES, DP * sizeof(T) > 256 ? 1 : 2) void 
 #pragma unroll
                 for (int x = 0; x < 16 * DB; ++x) {
                     if (x + FAR < 16 * DB) r[x + FAR] = rows_piece<RB>(kt, own_at, x + FAR);
-                    dq[0][x % DB] = __builtin_amdgcn_mfma_f32_32x32x2f32(r[x], t[x / DB], dq[0][x % DB], 0, 0, 0);
+                    dq[x % DB] = __builtin_amdgcn_mfma_f32_32x32x2f32(r[x], t[x / DB], dq[x % DB], 0, 0, 0);
                     __builtin_amdgcn_sched_barrier(0);
                 }
             }
@@ -236,11 +239,11 @@ __global__ __launch_bounds__(64 * BWD_WAVES, DP * sizeof(T) > 256 ? 1 : 2) void 
             wait_copies_and_barrier<0>();
         }
         if constexpr (SPLIT)
-            store_rows<float>(dq[0], 1.0f, A.part + (split * A.nq * A.heads + at) * A.dim, A.dim, valid);
+            store_rows<float>(dq, 1.0f, A.part + (split * A.nq * A.heads + at) * A.dim, A.dim, valid);
         else if (w.pieces > 1)
-            store_rows<float>(dq[0], 1.0f, A.part + ((int64_t)w.index * BWD_ROWS + (threadIdx.x >> 6) * 32 + (lane & 31)) * A.dim, A.dim, valid);
+            store_rows<float>(dq, 1.0f, A.part + ((int64_t)w.index * BWD_ROWS + (threadIdx.x >> 6) * 32 + (lane & 31)) * A.dim, A.dim, valid);
         else
-            store_rows<T>(dq[0], A.scale, (T *)A.dq.p + (q_beg + token) * A.dq.row + head * A.dq.head, A.dim, valid);
+            store_rows<T>(dq, A.scale, (T *)A.dq.p + (q_beg + token) * A.dq.row + head * A.dq.head, A.dim, valid);
     }
 }
 
@@ -251,8 +254,10 @@ __global__ __launch_bounds__(64 * BWD_WAVES, DP * sizeof(T) > 256 ? 1 : 2) void 
 // values and both gradients take 192 registers, so one wave runs on a SIMD and its LDS
 // reads and barriers are hidden only by its own products.  One barrier for two steps
 // (rings of five tiles) was no faster there (828 us).
+constexpr int dkv_residency(int rb) { return rb > 128 ? 1 : 2; }  // waves a SIMD
+
 template <typename T, int DP, bool SPLIT, bool DIRECT>
-__global__ __launch_bounds__(64 * BWD_WAVES, DP * sizeof(T) > 128 ? 1 : 2) void k_attn_dkv(AttnArgs A)
+__global__ __launch_bounds__(64 * BWD_WAVES, dkv_residency(DP * sizeof(T))) void k_attn_dkv(AttnArgs A)
 {
     constexpr int RB = DP * (int)sizeof(T), NJ = RB / 32, DB = DP / 32, TILE = 32 * RB;
     constexpr uint32_t G0 = RING * TILE, STAT0 = 2 * RING * TILE;
@@ -276,6 +281,7 @@ __global__ __launch_bounds__(64 * BWD_WAVES, DP * sizeof(T) > 128 ? 1 : 2) void 
     const int64_t q_beg = SPLIT ? w.own_beg : w.other_beg, k_beg = SPLIT ? w.other_beg : w.own_beg;
     const int64_t keys = SPLIT ? w.other_len : w.own_len;
     int64_t rows64 = (SPLIT ? w.own_len : w.other_len) * A.group - row0;
+    if (SPLIT && rows64 <= 0) return;  // a number without a run (see first_tile)
     if (SPLIT && rows64 > A.chunk) rows64 = A.chunk;
     if (!SPLIT && w.pieces > 1) {
         piece_rows(w, w.other_len * A.group, &row0, &rows64);
@@ -339,9 +345,9 @@ __global__ __launch_bounds__(64 * BWD_WAVES, DP * sizeof(T) > 128 ? 1 : 2) void 
                 v[j] = *(const Raw16Any *)((const T *)A.v.p + (k_beg + key) * A.v.row + hk * A.v.head + e);
             }
         }
-        f32x16 dk[1][DB], dv[1][DB], s[2], dp[2];
+        f32x16 dk[DB], dv[DB], s[2], dp[2];
 #pragma unroll
-        for (int db = 0; db < DB; ++db) dk[0][db] = dv[0][db] = f32x16{};
+        for (int db = 0; db < DB; ++db) dk[db] = dv[db] = f32x16{};
         auto products = [&](f32x16 &t, f32x16 &e, uint32_t place) {
             t = e = f32x16{};
 #pragma unroll
@@ -362,12 +368,12 @@ __global__ __launch_bounds__(64 * BWD_WAVES, DP * sizeof(T) > 128 ? 1 : 2) void 
             }
         };
         auto gradient = [&](f32x16 &t, f32x16 &e, int u, uint32_t place) {
-            RowsOperand<T> p[1], ds[1];
+            RowsOperand<T> p, ds;
 #pragma unroll
             for (int i = 0; i < 16; i += 2) weigh(t, e, i, stats(u, i));
-            p[0].set(t);
+            p.set(t);
             mma_rows<RB>(qt, place + G0, p, dv);
-            ds[0].set(e);
+            ds.set(e);
             mma_rows<RB>(qt, place, ds, dk);
         };
         auto step = [&](f32x16 &t, f32x16 &e, f32x16 &nt, f32x16 &ne, int u, uint32_t next_at, uint32_t own_at) {
@@ -409,7 +415,7 @@ __global__ __launch_bounds__(64 * BWD_WAVES, DP * sizeof(T) > 128 ? 1 : 2) void 
 #pragma unroll
                 for (int x = 0; x < 4 * DB; ++x) {
                     if (x + 2 * AHEAD < 4 * DB) r[x + 2 * AHEAD] = rows(x + 2 * AHEAD);
-                    f32x16 &d = x < 2 * DB ? dv[0][x % DB] : dk[0][x % DB];
+                    f32x16 &d = x < 2 * DB ? dv[x % DB] : dk[x % DB];
                     d = mma_pieces<T>(r[x], w[x / DB], d);
                     __builtin_amdgcn_sched_barrier(0);
                 }
@@ -447,7 +453,7 @@ __global__ __launch_bounds__(64 * BWD_WAVES, DP * sizeof(T) > 128 ? 1 : 2) void 
                 for (int x = 0; x < 32 * DB; ++x) {
                     if (x + FAR < 32 * DB) r[x + FAR] = rows(x + FAR);
                     const int y = x % (16 * DB);
-                    f32x16 &d = x < 16 * DB ? dv[0][y % DB] : dk[0][y % DB];
+                    f32x16 &d = x < 16 * DB ? dv[y % DB] : dk[y % DB];
                     d = __builtin_amdgcn_mfma_f32_32x32x2f32(r[x], x < 16 * DB ? t[y / DB] : e[y / DB], d, 0, 0, 0);
                     __builtin_amdgcn_sched_barrier(0);
                 }
@@ -480,15 +486,15 @@ __global__ __launch_bounds__(64 * BWD_WAVES, DP * sizeof(T) > 128 ? 1 : 2) void 
         }
         if constexpr (SPLIT) {
             const int64_t at = ((split * A.nk + k_beg + key) * A.kv_heads + hk) * A.dim;
-            store_rows<float>(dk[0], 1.0f, A.part + at, A.dim, valid);
-            store_rows<float>(dv[0], 1.0f, A.part2 + at, A.dim, valid);
+            store_rows<float>(dk, 1.0f, A.part + at, A.dim, valid);
+            store_rows<float>(dv, 1.0f, A.part2 + at, A.dim, valid);
         } else if (w.pieces > 1) {
             const int64_t at = ((int64_t)w.index * BWD_ROWS + wave * 32 + (lane & 31)) * A.dim;
-            store_rows<float>(dk[0], 1.0f, A.part + at, A.dim, valid);
-            store_rows<float>(dv[0], 1.0f, A.part2 + at, A.dim, valid);
+            store_rows<float>(dk, 1.0f, A.part + at, A.dim, valid);
+            store_rows<float>(dv, 1.0f, A.part2 + at, A.dim, valid);
         } else {
-            store_rows<T>(dk[0], A.scale, (T *)A.dk.p + (k_beg + key) * A.dk.row + hk * A.dk.head, A.dim, valid);
-            store_rows<T>(dv[0], 1.0f, (T *)A.dv.p + (k_beg + key) * A.dv.row + hk * A.dv.head, A.dim, valid);
+            store_rows<T>(dk, A.scale, (T *)A.dk.p + (k_beg + key) * A.dk.row + hk * A.dk.head, A.dim, valid);
+            store_rows<T>(dv, 1.0f, (T *)A.dv.p + (k_beg + key) * A.dv.row + hk * A.dv.head, A.dim, valid);
         }
     }
 }
@@ -585,8 +591,7 @@ static BwdPlan bwd_plan(const AttnArgs &A, int dtype)
 {
     const int rb = (A.dim + 31) / 32 * 32 * (dtype == SUBMCONV_F32 ? 4 : 2);
     BwdPlan p;
-    // the launch bounds of k_attn_dq and k_attn_dkv
-    const int q_slots = blocks_at_once(rb, rb > 256 ? 1 : 2), k_slots = blocks_at_once(rb, rb > 128 ? 1 : 2);
+    const int q_slots = blocks_at_once(rb, dq_residency(rb)), k_slots = blocks_at_once(rb, dkv_residency(rb));
     p.q = split_plan(A.nq * A.group, BWD_ROWS, A.nk, 32, A.entries, A.kv_heads, q_slots);
     p.k = split_plan(A.nk, BWD_ROWS, A.nq * A.group, 32, A.entries, A.kv_heads, k_slots);
     p.q_slots = cut_pays(A.nk, A.entries, dtype) ? (uint32_t)q_slots : 0;
@@ -608,7 +613,6 @@ size_t attention_backward_workspace(const AttnArgs &A, int dtype)
 static void set_split(AttnArgs &A, const SplitPlan &p)
 {
     A.chunk = p.chunk;
-    A.splits = p.splits;
     A.tiles = p.tiles;
 }
 

@@ -308,3 +308,14 @@ def test_attention_long_tiles(h, hk, d, lens, dtype):
         within("out", out[rows], expect, bound)
         expect, bounds = ref.attention_backward(some[1], some[0], *keys, one, all_, d ** -0.5, ref.UNIT[dtype])
         within("dq", grads[0][rows], expect[0], bounds[0])
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_attention_splits_among_many_entries(dtype):
+    """Few rows on one side and more entries than lanes can count (254): the long side is split into runs
+    numbered with gaps, also where one entry holds all of it."""
+    none = [0] * 298
+    check([2] + none + [1], [45011] + none + [0], 2, 1, 32, dtype)   # above 128 rows an entry on average
+    check([1] + none + [2], [300] + none + [45001], 1, 1, 64, dtype)
+    check([45011] + none + [0], [2] + none + [1], 2, 1, 32, dtype)
+    check([2] + none[:200] + [1], [30000] + none[:200] + [5001], 2, 2, 32, dtype)
