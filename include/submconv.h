@@ -375,7 +375,8 @@ int submconv_rotary(const void *x, int64_t x_row, int64_t x_head, const int32_t 
  *            to no entry: queries there get zeros.  They are read on the device only;
  *            values outside [0, n] are clamped, so bad offsets give wrong rows, never
  *            accesses outside the tensors.
- *   entries: 1..2^20.  nq, nk >= 0, nq * heads and nk * kv_heads < 2^31.
+ *   entries: 1..2^20.  nq, nk >= 0, nq * heads and nk * kv_heads < 2^31.  Tiles of 128 rows and
+ *            entries times key heads together stay below 2^24 - 2^16 (else E_UNSUPPORTED).
  *   heads  : a multiple of kv_heads, up to 1024.   dim : a multiple of 8, 8..128.
  *   scale  : finite, > 0.
  *   lse    : device fp32 [nq, heads] for the backward pass, or NULL.
@@ -404,7 +405,8 @@ int submconv_attention(const void *q, const void *k, const void *v, const int64_
  *   workspace : submconv_attention_backward_workspace bytes, 16-byte aligned, never 0 for
  *            nq > 0.
  * Sums are fp32 in a fixed order; in bf16 the weights and their gradients are rounded to
- * bf16 for the products.  Asynchronous; two launches, up to five when a short side is
+ * bf16 for the products.  The weights are formed again as exp(s - lse) in fp32, so scores
+ * of a size S lose S * 2^-24 of relative accuracy here; the forward has no such limit.  Asynchronous; two launches, up to five when a short side is
  * split.  Rows outside every entry get zeros.
  */
 size_t submconv_attention_backward_workspace(int32_t entries, int64_t nq, int64_t nk, int32_t heads, int32_t kv_heads,

@@ -856,6 +856,11 @@ static int attn_sizes(AttnArgs *A, int32_t entries, int64_t nq, int64_t nk, int3
         return fail(SUBMCONV_E_UNSUPPORTED, "dim = %d is not a multiple of 8 in 8..%d", dim, SUBMCONV_ATTENTION_MAX_DIM);
     if (nq < 0 || nk < 0 || nq >= MAX_ROWS / heads || nk >= MAX_ROWS / kv_heads)
         return fail(SUBMCONV_E_INVALID_ARG, "nq = %lld, nk = %lld: rows times heads must stay below 2^31", (long long)nq, (long long)nk);
+    // a launch holds 2^32 threads: 2^24 blocks, some left for cut tiles
+    const int64_t rows = nq * heads > nk * kv_heads ? nq * heads : nk * kv_heads;
+    if (rows / 128 + ((int64_t)entries + 2) * kv_heads > (1 << 24) - (1 << 16))
+        return fail(SUBMCONV_E_UNSUPPORTED, "%lld tiles and %d entries of %d key heads are more than one launch holds",
+                    (long long)(rows / 128), entries, kv_heads);
     A->entries = entries;
     A->nq = nq;
     A->nk = nk;

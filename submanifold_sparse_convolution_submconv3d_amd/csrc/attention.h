@@ -323,7 +323,7 @@ struct Fill {
                 __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (SC_LDS void *)(uintptr_t)(at + i * 1024), 16, off[i], 0, 0, 0);
         } else {
 #pragma unroll
-            for (int i = 0; i < PER; ++i) put(ptr, row(i) < n ? off[i] : OUT_OF_RANGE, i);
+            for (int i = 0; i < PER; ++i) put(row(i) < n && off[i] != OUT_OF_RANGE ? ptr + off[i] : nullptr, i);
         }
         ptr += 32 * row_bytes;
         advance();
@@ -339,13 +339,14 @@ struct Fill {
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
             const uint32_t r = row0 + row(i), t = r / group;
-            const uint32_t o = row(i) < left && off[i] != OUT_OF_RANGE
-                                   ? (t - t0) * (uint32_t)(h.row * sizeof(T)) + (r - t * group) * (uint32_t)(h.head * sizeof(T)) + off[i]
-                                   : OUT_OF_RANGE;
-            if constexpr (DIRECT)
+            const bool there = row(i) < left && off[i] != OUT_OF_RANGE;
+            if constexpr (DIRECT) {  // (the group's heads lie within 2^30 bytes)
+                const uint32_t o = there ? (t - t0) * (uint32_t)(h.row * sizeof(T)) + (r - t * group) * (uint32_t)(h.head * sizeof(T)) + off[i]
+                                         : OUT_OF_RANGE;
                 __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (SC_LDS void *)(uintptr_t)(to + place + i * 1024), 16, o, 0, 0, 0);
-            else
-                put(base, o, i);
+            } else {
+                put(there ? base + ((int64_t)(t - t0) * h.row + (int64_t)(r - t * group) * h.head) * (int64_t)sizeof(T) + off[i] : nullptr, i);
+            }
         }
         advance();
     }
@@ -360,10 +361,10 @@ struct Fill {
         left -= 32;
         place = place == (RING - 1) * TILE ? 0 : place + TILE;
     }
-    __device__ __forceinline__ void put(const char *base, uint32_t o, int i) const
+    __device__ __forceinline__ void put(const char *from, int i) const
     {
         Raw16 v = {0, 0, 0, 0};
-        if (o != OUT_OF_RANGE) v = *(const Raw16Any *)(base + o);
+        if (from) v = *(const Raw16Any *)from;
         lds_write16(to + place + i * 1024 + lane_id() * 16, v);
     }
 };

@@ -30,6 +30,7 @@ __device__ __forceinline__ void turn(int32_t position, float freq, bool inverse,
     if (inverse) *s = -*s;
 }
 
+constexpr int64_t ROTARY_BLOCKS = 1 << 22;  // along x (a launch's axis holds 2^32 threads); the rest along y
 constexpr int ROTARY_HEADS = 4;  // heads a thread works on at a time, their loads issued together
 
 template <typename T, bool SPLIT>
@@ -43,13 +44,14 @@ __global__ __launch_bounds__(256) void k_rotary(const T *x, int64_t x_row, int64
     const int per_row = pieces * hgroups;
     const int r = threadIdx.x / per_row, u = threadIdx.x - r * per_row;
     const int h0 = u / pieces, piece = u - h0 * pieces;
-    const int64_t row = (int64_t)blockIdx.x * rows_per_block + r;
+    const int64_t row = ((int64_t)blockIdx.y * ROTARY_BLOCKS + blockIdx.x) * rows_per_block + r;
     if (r >= rows_per_block || row >= n) return;
 
     const int half = dim / 2, used = ax.end[SUBMCONV_ROTARY_MAX_AXES - 1];
     const int e = piece * V;                      // first element (split: also first pair)
     const int left = (SPLIT ? half : dim) - e;
     const int nv = left < V ? left : V;
+    const int turning = used - (SPLIT ? e : e / 2);  // pairs of the piece that turn; the others are copied as they are
     float c[PAIRS], s[PAIRS];
 #pragma unroll
     for (int j = 0; j < PAIRS; ++j) {
@@ -86,6 +88,7 @@ __global__ __launch_bounds__(256) void k_rotary(const T *x, int64_t x_row, int64
 #pragma unroll
                 for (int j = 0; j < V; ++j) {
                     const float p = va[j], q = vb[j];
+                    if (j >= turning) continue;
                     va[j] = p * c[j] - q * s[j];
                     vb[j] = p * s[j] + q * c[j];
                 }
@@ -94,6 +97,7 @@ __global__ __launch_bounds__(256) void k_rotary(const T *x, int64_t x_row, int64
 #pragma unroll
                 for (int j = 0; j < PAIRS; ++j) {
                     const float p = va[2 * j], q = va[2 * j + 1];
+                    if (j >= turning) continue;
                     va[2 * j] = p * c[j] - q * s[j];
                     va[2 * j + 1] = p * s[j] + q * c[j];
                 }
@@ -114,7 +118,8 @@ int rotary(const void *x, int64_t x_row, int64_t x_head, const int32_t *pos, int
     int hgroups = (heads + ROTARY_HEADS - 1) / ROTARY_HEADS;
     if (hgroups * pieces > 256) hgroups = 256 / pieces;
     const int rows = 256 / (pieces * hgroups);
-    const dim3 grid((unsigned)((n + rows - 1) / rows));
+    const int64_t blocks = (n + rows - 1) / rows;
+    const dim3 grid((unsigned)(blocks < ROTARY_BLOCKS ? blocks : ROTARY_BLOCKS), (unsigned)((blocks + ROTARY_BLOCKS - 1) / ROTARY_BLOCKS));
 #define GO(T, SPLIT)                                                                                              \
     hipLaunchKernelGGL((k_rotary<T, SPLIT>), grid, dim3(256), 0, st, (const T *)x, x_row, x_head, pos, pos_row, freqs, \
                        ax, n, heads, dim, pieces, hgroups, rows, inverse, (T *)out, out_row, out_head)

@@ -319,3 +319,24 @@ def test_attention_splits_among_many_entries(dtype):
     check([1] + none + [2], [300] + none + [45001], 1, 1, 64, dtype)
     check([45011] + none + [0], [2] + none + [1], 2, 1, 32, dtype)
     check([2] + none[:200] + [1], [30000] + none[:200] + [5001], 2, 2, 32, dtype)
+
+
+def test_attention_heads_far_apart():
+    """Query heads of a group more than 2^30 bytes apart (head-major memory of a very large set): the
+    same bits as next to each other."""
+    n, d, far = 150, 32, (1 << 28) + 64
+    rng = np.random.default_rng(13)
+    note("attention heads far apart")
+    memory = torch.empty(2 * far, dtype=torch.bfloat16, device=DEV)
+    q = memory.as_strided((n, 2, d), (d, far, 1))
+    q.copy_(heads(n, 2, d, "bf16", rng))
+    k, v, g = heads(n, 1, d, "bf16", rng), heads(n, 1, d, "bf16", rng), heads(n, 2, d, "bf16", rng)
+    off = device_offsets([0, 60, n])
+    near = q.contiguous()
+    out, lse = sc.submconv_attention(q, k, v, off, return_lse=True)
+    expect, elos = sc.submconv_attention(near, k, v, off, return_lse=True)
+    assert torch.equal(out, expect) and torch.equal(lse, elos)
+    got, want = sc.submconv_attention_backward(g, q, k, v, out, lse, off), sc.submconv_attention_backward(g, near, k, v, out, lse, off)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    del memory, q
+    torch.cuda.empty_cache()

@@ -147,3 +147,20 @@ def test_rotary_empty_and_offsets_past_32_bits():
     assert torch.equal(sc.submconv_rotary(x, pos, freqs, sections), sc.submconv_rotary(x0, pos, freqs, sections))
     del wide, x
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("split", [False, True])
+def test_rotary_copies_what_does_not_turn(split):
+    """Infinities and NaN in the pairs past the sections stay where they are and reach nothing else."""
+    sections, n, h, d = (3, 2), 40, 2, 16                     # 5 of 8 pairs turn
+    freqs = sc.rotary_freqs(sections, device=DEV)
+    x, pos = make(n, h, d, "f32", 10, axes=2)
+    plain = sc.submconv_rotary(x, pos, freqs, sections, split=split)
+    at = 6 if split else 12                                   # the first element of pair 6
+    x[:, :, at] = float("inf")
+    x[3, 1, at] = float("nan")
+    note("rotary copies split=%s" % split)
+    out = sc.submconv_rotary(x, pos, freqs, sections, split=split)
+    rest = [i for i in range(d) if i != at]
+    assert torch.equal(out[..., rest], plain[..., rest])
+    assert bool(torch.isnan(out[3, 1, at])) and int(torch.isinf(out[..., at]).sum()) == n * h - 1
