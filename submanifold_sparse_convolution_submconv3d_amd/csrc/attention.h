@@ -617,6 +617,7 @@ struct SplitPlan {
     int64_t splits;
     int tiles;
 };
-SplitPlan split_plan(int64_t own_rows, int own_tile, int64_t other_rows, int other_tile, int entries, int kv_heads, int64_t slots);
+SplitPlan split_plan(int64_t own_rows, int own_tile, int64_t other_rows, int other_tile, int entries, int kv_heads, int64_t slots,
+                     int dtype);
 
 }  // namespace sc

@@ -447,13 +447,20 @@ __global__ __launch_bounds__(256) void k_attn_join_cut(AttnArgs A)
 // half as many more would still run at once (`slots` blocks do): into runs of at least
 // MIN_CHUNK rows, WANT_BLOCKS blocks in all, several to each place, since the entries and
 // the last runs are not alike (measured on 20384 x 4111 rows, 4 heads of 64, fp32, for the keys'
-// gradients: 768 blocks 538 us, 1536 466, 3072 490).  chunk = 0: not at all.
+// gradients: 768 blocks 538 us, 1536 466, 3072 490).  chunk = 0: not at all, as in bf16 where
+// the other side is so short that the join's launch costs more than the split saves (64
+// queries of 4 x 64: 512 keys 18.8 us split, 16.3 whole; 1024 keys 19.2 and 20.4).  The limit
+// lies between those two; among several entries the longest sets the time, some times the
+// average, so it is lower (7 entries, 611 keys on average, 1904 the longest: 20.4 and 31.3).
+// fp32 has no such limit: 64 queries over 256 keys take 21.8 us split and 24.3 whole.
 constexpr int64_t WANT_BLOCKS = 1536, MIN_CHUNK = 64;
 
-SplitPlan split_plan(int64_t own_rows, int own_tile, int64_t other_rows, int other_tile, int entries, int kv_heads, int64_t slots)
+SplitPlan split_plan(int64_t own_rows, int own_tile, int64_t other_rows, int other_tile, int entries, int kv_heads, int64_t slots,
+                     int dtype)
 {
     SplitPlan p = {0, 0, 1};
     if (own_rows == 0 || other_rows == 0) return p;
+    if (dtype == SUBMCONV_BF16 && other_rows / entries < (entries == 1 ? 768 : 512)) return p;
     const int64_t per_entry = (own_rows / entries + own_tile - 1) / own_tile;
     int64_t tiles = per_entry > 0 ? per_entry : 1;
     const int64_t used = entries < own_rows ? entries : own_rows;
@@ -481,7 +488,7 @@ static int fwd_slots(const AttnArgs &A, int dtype)
 
 static SplitPlan fwd_plan(const AttnArgs &A, int dtype)
 {
-    return split_plan(A.nq * A.group, 32 * FWD_WAVES, A.nk, 32, A.entries, A.kv_heads, fwd_slots(A, dtype));
+    return split_plan(A.nq * A.group, 32 * FWD_WAVES, A.nk, 32, A.entries, A.kv_heads, fwd_slots(A, dtype), dtype);
 }
 
 // The same where tiles may be cut, else 0.

@@ -592,8 +592,8 @@ static BwdPlan bwd_plan(const AttnArgs &A, int dtype)
     const int rb = (A.dim + 31) / 32 * 32 * (dtype == SUBMCONV_F32 ? 4 : 2);
     BwdPlan p;
     const int q_slots = blocks_at_once(rb, dq_residency(rb)), k_slots = blocks_at_once(rb, dkv_residency(rb));
-    p.q = split_plan(A.nq * A.group, BWD_ROWS, A.nk, 32, A.entries, A.kv_heads, q_slots);
-    p.k = split_plan(A.nk, BWD_ROWS, A.nq * A.group, 32, A.entries, A.kv_heads, k_slots);
+    p.q = split_plan(A.nq * A.group, BWD_ROWS, A.nk, 32, A.entries, A.kv_heads, q_slots, dtype);
+    p.k = split_plan(A.nk, BWD_ROWS, A.nq * A.group, 32, A.entries, A.kv_heads, k_slots, dtype);
     p.q_slots = cut_pays(A.nk, A.entries, dtype) ? (uint32_t)q_slots : 0;
     p.k_slots = cut_pays(A.nq * A.group, A.entries, dtype) ? (uint32_t)k_slots : 0;
     p.stat = ((size_t)A.nq * A.heads * 2 * sizeof(float) + 15) / 16 * 16;

@@ -321,6 +321,19 @@ def test_attention_splits_among_many_entries(dtype):
     check([2] + none[:200] + [1], [30000] + none[:200] + [5001], 2, 2, 32, dtype)
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_attention_splits_among_many_long_entries(dtype):
+    """The same with more than 512 rows an entry on average, from where on bf16 is split too; and one entry on
+    both sides of its limit of 768 rows."""
+    none = [0] * 298
+    check([2] + none + [1], [160011] + none + [0], 2, 1, 32, dtype)
+    check([1] + none + [2], [300] + none + [160001], 1, 1, 64, dtype)
+    check([160011] + none + [0], [2] + none + [1], 1, 1, 32, dtype)
+    check([2] + none[:260] + [1], [130000] + none[:260] + [9001], 2, 2, 32, dtype)
+    check([5], [767], 2, 1, 64, dtype)
+    check([5], [768], 2, 1, 64, dtype)
+
+
 def test_attention_heads_far_apart():
     """Query heads of a group more than 2^30 bytes apart (head-major memory of a very large set): the
     same bits as next to each other."""
