@@ -25,18 +25,32 @@ namespace sc {
 // rescaled: weights stay below 2^8, far from overflow, and most tiles skip the rescaling.
 constexpr float SLACK = 8.0f;
 
-// A weight is exp2(s c - m c) with c = scale log2(e) and m the row's running maximum: one
-// fused rounding of the difference, and the rounding of m c is a common factor of a row's
-// weights and their sum.  Past this size of m c that factor could overflow (and m c
-// itself); the weight is then exp2((s - m) c), where equal scores cancel exactly.
+// A weight is exp2(s c - base) with c = scale log2(e), m the row's running maximum and base = m c
+// rounded to fp32: one fused rounding of the difference.  What the rounding of m c leaves
+// is a common factor of the row's weights and their sum, so everything that follows has to
+// use that same rounded number: the product is kept out of any fused operation (contraction
+// would make base - next_base a fused m c - next_base, off by up to 2^5 in the exponent).
+// Past this size of m c that common factor could overflow (and m c itself); the weight is
+// then exp2((s - m) c), where equal scores cancel exactly.
 constexpr float HUGE_BASE = 1073741824.0f;
+__device__ __forceinline__ float rounded_product(float m, float c)
+{
+#pragma clang fp contract(off)
+    return m * c;
+}
 __device__ __forceinline__ bool huge(float m, float c) { return m != -INFINITY && !(fabsf(m * c) <= HUGE_BASE); }
+__device__ __forceinline__ float base_of(float m, float c) { return m == -INFINITY || huge(m, c) ? 0.0f : rounded_product(m, c); }
 
-// What sums relative to the maximum m are worth relative to next >= m.
+// What sums relative to the maximum m are worth relative to next >= m: exactly 1 where the
+// maximum is the same.  Where just one of the two is huge, its m c is meant exactly.
 __device__ __forceinline__ float rescale(float m, float next, float c)
 {
-    if (next == -INFINITY) return 1.0f;
-    return __builtin_amdgcn_exp2f(huge(next, c) ? (m - next) * c : m * c - next * c);
+    if (m == next) return 1.0f;
+    if (m == -INFINITY) return 0.0f;  // nothing is summed yet
+    float e = base_of(m, c) - base_of(next, c);
+    if (huge(m, c)) e = huge(next, c) ? (m - next) * c : fmaf(m, c, -base_of(next, c));
+    else if (huge(next, c)) e = -fmaf(next, c, -base_of(m, c));
+    return __builtin_amdgcn_exp2f(e);
 }
 
 // log sum exp from the maximum and the sum of the weights.
@@ -44,7 +58,7 @@ __device__ __forceinline__ float log_sum(float m, float l, float scale)
 {
     if (l == 0.0f) return -INFINITY;  // no key, or none with a finite score
     const float c = scale * LOG2E, e = __builtin_amdgcn_logf(l);
-    return huge(m, c) ? m * scale + e * LN2 : (m * c + e) * LN2;
+    return huge(m, c) ? m * scale + e * LN2 : (base_of(m, c) + e) * LN2;
 }
 
 // acc *= f where `on`, in place.  One straight piece of code for the compiler: a branch
@@ -189,7 +203,7 @@ __global__ __launch_bounds__(64 * FWD_WAVES, fwd_residency(DP * sizeof(T))) void
                 f = rescale(m, next, c);
                 m = next;
                 l *= f;
-                base = next == -INFINITY || huge(next, c) ? 0.0f : next * c;  // -inf: weights are exp(-inf)
+                base = base_of(next, c);  // (0 for -inf: weights are exp(-inf))
                 big = __ballot(huge(next, c));
             }
 #pragma unroll
