@@ -378,7 +378,7 @@ int submconv_rotary(const void *x, int64_t x_row, int64_t x_head, const int32_t 
  *   entries: 1..2^20.  nq, nk >= 0, nq * heads and nk * kv_heads < 2^31.  Tiles of 128 rows and
  *            entries times key heads together stay below 2^24 - 2^16 (else E_UNSUPPORTED).
  *   heads  : a multiple of kv_heads, up to 1024.   dim : a multiple of 8, 8..128.
- *   scale  : finite, > 0.
+ *   scale  : above 0, at most SUBMCONV_ATTENTION_MAX_SCALE.
  *   lse    : device fp32 [nq, heads] for the backward pass, or NULL.
  *   workspace : device memory of submconv_attention_workspace bytes, 16-byte aligned
  *            (may be NULL when that is 0); contents undefined before and after.
@@ -390,6 +390,7 @@ int submconv_rotary(const void *x, int64_t x_row, int64_t x_head, const int32_t 
  */
 #define SUBMCONV_ATTENTION_MAX_DIM 128
 #define SUBMCONV_ATTENTION_MAX_ROW (1 << 22)
+#define SUBMCONV_ATTENTION_MAX_SCALE 1e38f
 size_t submconv_attention_workspace(int32_t entries, int64_t nq, int64_t nk, int32_t heads, int32_t kv_heads,
                                     int32_t dim, int32_t dtype);
 int submconv_attention(const void *q, const void *k, const void *v, const int64_t *strides, const int32_t *q_offsets,

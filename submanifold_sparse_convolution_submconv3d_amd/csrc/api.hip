@@ -885,6 +885,14 @@ size_t submconv_attention_backward_workspace(int32_t entries, int64_t nq, int64_
     return attn_sizes(&A, entries, nq, nk, heads, kv_heads, dim, dtype) == SUBMCONV_OK ? attention_backward_workspace(A, dtype) : 0;
 }
 
+// Weights are powers of two, so scale log2(e) has to stay finite too.
+static int attn_scale_check(float scale)
+{
+    if (!(scale > 0.0f) || scale > SUBMCONV_ATTENTION_MAX_SCALE)
+        return fail(SUBMCONV_E_INVALID_ARG, "scale = %g outside (0, %g]", (double)scale, (double)SUBMCONV_ATTENTION_MAX_SCALE);
+    return SUBMCONV_OK;
+}
+
 // One [n, heads, dim] tensor of a call: its pointer, distances and range.
 static int attn_tensor(const char *what, const void *p, const int64_t *st, int64_t n, int64_t heads, int64_t dim,
                        size_t es, bool written, Heads *h, Range *r)
@@ -906,7 +914,7 @@ int submconv_attention(const void *q, const void *k, const void *v, const int64_
 {
     AttnArgs A;
     SC_CHECK(attn_sizes(&A, entries, nq, nk, heads, kv_heads, dim, dtype));
-    if (!(scale > 0.0f) || scale > 3.4e38f) return fail(SUBMCONV_E_INVALID_ARG, "scale = %g is not finite and positive", (double)scale);
+    SC_CHECK(attn_scale_check(scale));
     if (!strides) return fail(SUBMCONV_E_INVALID_ARG, "strides is NULL");
     if (nq == 0) return SUBMCONV_OK;
     if (!q_offsets || !k_offsets) return fail(SUBMCONV_E_INVALID_ARG, "offsets are NULL");
@@ -940,7 +948,7 @@ int submconv_attention_backward(const void *grad, const void *q, const void *k, 
 {
     AttnArgs A;
     SC_CHECK(attn_sizes(&A, entries, nq, nk, heads, kv_heads, dim, dtype));
-    if (!(scale > 0.0f) || scale > 3.4e38f) return fail(SUBMCONV_E_INVALID_ARG, "scale = %g is not finite and positive", (double)scale);
+    SC_CHECK(attn_scale_check(scale));
     if (!strides) return fail(SUBMCONV_E_INVALID_ARG, "strides is NULL");
     if (nq == 0 && nk == 0) return SUBMCONV_OK;
     if (!q_offsets || !k_offsets || (nq && !lse)) return fail(SUBMCONV_E_INVALID_ARG, "offsets or lse are NULL");

@@ -78,3 +78,17 @@ def test_attention_scores_around_the_change_of_form(sign):
     out = to_f64(sc.submconv_attention(q, k, v, off(33), off(n), scale=1.0))
     expect = to_f64(v)[64:].mean(axis=0)
     assert np.abs(out - expect).max() <= 4 * n * ref.U32 * np.abs(to_f64(v)).max()
+
+
+def test_attention_largest_scale():
+    """The largest scale that is taken, on products of its inverse's size."""
+    d, n, scale = 32, 100, 1e38
+    v = torch.from_numpy(np.random.default_rng(2).standard_normal((n, 1, d)).astype(np.float32)).to(DEV)
+    q, k = torch.zeros((5, 1, d), device=DEV), torch.zeros((n, 1, d), device=DEV)
+    q[..., 0] = 2.0 ** -63
+    k[:40, 0, 0], k[40:, 0, 0] = 2.0 ** -63, 2.0 ** -62
+    off = lambda m: torch.tensor([0, m], dtype=torch.int32, device=DEV)  # noqa: E731
+    note("attention largest scale")
+    out, _, bound, _ = ref.attention(to_f64(q), to_f64(k), to_f64(v), np.array([0, 5]), np.array([0, n]), float(np.float32(scale)), ref.U32)
+    got = to_f64(sc.submconv_attention(q, k, v, off(5), off(n), scale=scale))
+    assert (np.abs(got - out) <= bound).all()
