@@ -355,37 +355,53 @@ static bool aligned_to(const void *p, size_t bytes) { return ((uintptr_t)p & (by
 // that every byte offset below fits 63 bits.
 constexpr int64_t MAX_ROWS = int64_t(1) << 31, MAX_STRIDE = int64_t(1) << 24;
 
-// Bytes from the first to past the last element of [n, c] with rows ld apart.
-static size_t span2(int64_t n, int64_t c, int64_t ld, size_t es) { return n ? (size_t)((n - 1) * ld + c) * es : 0; }
-
-// Memory a call reads or writes: rows of `foot` bytes, `row` bytes apart (0: one piece),
-// `bytes` from the first byte to past the last.
+// Memory a call reads or writes: n x heads pieces of `dim` bytes, rows `row` bytes apart
+// and heads `head` bytes apart (one piece: n = heads = 1).
 struct Range {
     const char *what;
     const void *p;
-    size_t bytes;
     bool written;
-    size_t row, foot;
+    int64_t n, row, heads, head, dim;
+
+    int64_t bytes() const { return p && n > 0 && dim > 0 ? (n - 1) * row + (heads - 1) * head + dim : 0; }
 };
 
-static Range range1(const char *what, const void *p, size_t bytes, bool written) { return Range{what, p, bytes, written, 0, 0}; }
+static Range range1(const char *what, const void *p, size_t bytes, bool written) { return Range{what, p, written, 1, 0, 1, 0, (int64_t)bytes}; }
 
 static Range range2(const char *what, const void *p, int64_t n, int64_t c, int64_t ld, size_t es, bool written)
 {
-    return Range{what, p, span2(n, c, ld, es), written, (size_t)ld * es, (size_t)c * es};
+    return Range{what, p, written, n, ld * (int64_t)es, 1, 0, c * (int64_t)es};
 }
 
-// Whether two ranges share bytes.  Rows equally far apart may interleave (columns of one
-// wider tensor).
-static bool collide(const Range &a, const Range &b)
+// Whether two ranges share bytes; exact where their rows and heads are equally far apart, as
+// parts of one wider tensor are, else by whole rows, whole heads or the whole span.
+static bool collide(Range a, Range b)
 {
-    if (!a.p || !b.p || !a.bytes || !b.bytes || !overlaps(a.p, a.bytes, b.p, b.bytes)) return false;
-    if (a.row && a.row == b.row && a.foot <= a.row && b.foot <= b.row) {
-        const uintptr_t x = (uintptr_t)a.p, y = (uintptr_t)b.p;
-        const size_t d = x <= y ? (y - x) % a.row : (a.row - (x - y) % a.row) % a.row;
-        return !(d >= a.foot && d + b.foot <= a.row);
+    if (!a.bytes() || !b.bytes() || !overlaps(a.p, a.bytes(), b.p, b.bytes())) return false;
+    // a distance that is not used is as good as any
+    if (a.n == 1) a.row = b.row;
+    if (b.n == 1) b.row = a.row;
+    if (a.heads == 1) a.head = b.head;
+    if (b.heads == 1) b.head = a.head;
+    if (a.row != b.row && a.head != b.head) return true;
+    for (Range *r : {&a, &b}) {
+        if (a.head != b.head) r->dim += (r->heads - 1) * r->head, r->heads = 1;
+        else if (a.row != b.row) r->dim += (r->n - 1) * r->row, r->n = 1;
     }
-    return true;
+    // Two pieces i and h steps apart lie at d - i row - h head of each other, and share bytes
+    // where that is between -b.dim and a.dim.  For every h, the first i below the upper end:
+    const int64_t d = (int64_t)((intptr_t)b.p - (intptr_t)a.p);
+    const int64_t row = a.n > 1 ? a.row : b.row, head = a.heads > 1 ? a.head : b.head;
+    for (int64_t h = 1 - b.heads; h < a.heads; ++h) {
+        const int64_t e = d - h * head, over = e - a.dim;
+        int64_t i = 1 - b.n;
+        if (row > 0) {
+            const int64_t first = (over >= 0 ? over / row : -((-over + row - 1) / row)) + 1;
+            if (first > i) i = first;
+        }
+        if (i < a.n && e - i * row < a.dim && e - i * row > -b.dim) return true;
+    }
+    return false;
 }
 
 // A written range may share bytes with no other.
@@ -393,7 +409,7 @@ static int ranges_check(const Range *r, int n)
 {
     for (int i = 0; i < n; ++i)
         for (int j = 0; j < n; ++j)
-            if (i != j && r[i].written && collide(r[i], r[j]))
+            if (i != j && r[i].written && !(r[j].written && j < i) && collide(r[i], r[j]))
                 return fail(SUBMCONV_E_ALIAS, "%s overlaps %s", r[i].what, r[j].what);
     return SUBMCONV_OK;
 }
@@ -743,7 +759,7 @@ int submconv_layer_norm(const void *x, int64_t x_row, int64_t n, int32_t c, int3
     if (!aligned_to(x, es) || !aligned_to(y, es) || !aligned_to(weight, ps) || !aligned_to(bias, ps) || !aligned_to(stats, 8))
         return fail(SUBMCONV_E_INVALID_ARG, "misaligned pointer");
     // y in the place of x is fine
-    const Range r[] = {range2("x", x == y && x_row == y_row ? nullptr : x, n, c, x_row, es, false),
+    const Range r[] = {range2("x", x == y && (x_row == y_row || n == 1) ? nullptr : x, n, c, x_row, es, false),
                        range2("y", y, n, c, y_row, es, true), range1("weight", weight, (size_t)c * ps, false),
                        range1("bias", bias, (size_t)c * ps, false), range1("stats", stats, (size_t)n * 8, true)};
     SC_CHECK(ranges_check(r, 5));
@@ -774,7 +790,7 @@ int submconv_layer_norm_backward(const void *grad, int64_t grad_row, const void 
         return fail(SUBMCONV_E_INVALID_ARG, "workspace of %zu bytes, %zu needed", workspace ? workspace_bytes : 0, need);
     const size_t pb = (size_t)c * ps;
     // dx in the place of grad is fine
-    const Range r[] = {range2("grad", grad == dx && grad_row == dx_row ? nullptr : grad, n, c, grad_row, es, false),
+    const Range r[] = {range2("grad", grad == dx && (grad_row == dx_row || n == 1) ? nullptr : grad, n, c, grad_row, es, false),
                        range2("x", x, n, c, x_row, es, false), range2("dx", dx, n, c, dx_row, es, true),
                        range1("stats", stats, (size_t)n * 8, false), range1("weight", weight, pb, false),
                        range1("dweight", dweight, pb, true), range1("dbias", dbias, pb, true),
@@ -788,8 +804,8 @@ int submconv_layer_norm_backward(const void *grad, int64_t grad_row, const void 
 static Range range3(const char *what, const void *p, int64_t n, int64_t heads, int64_t dim, int64_t row, int64_t head,
                     size_t es, bool written)
 {
-    const size_t foot = (size_t)((heads - 1) * head + dim) * es;
-    return Range{what, p, n ? (size_t)((n - 1) * row) * es + foot : 0, written, (size_t)row * es, foot};
+    const int64_t b = (int64_t)es;
+    return Range{what, p, written, n, row * b, heads, head * b, dim * b};
 }
 
 // The distances of an [n, heads, dim] tensor; one that is written has each element once.
@@ -833,7 +849,7 @@ int submconv_rotary(const void *x, int64_t x_row, int64_t x_head, const int32_t 
     const size_t es = elem_size(dtype);
     if (!aligned_to(x, es) || !aligned_to(out, es) || !aligned_to(positions, 4) || !aligned_to(freqs, 4))
         return fail(SUBMCONV_E_INVALID_ARG, "misaligned pointer");
-    const bool same = x == out && x_row == out_row && (heads == 1 || x_head == out_head);  // in place
+    const bool same = x == out && (n == 1 || x_row == out_row) && (heads == 1 || x_head == out_head);  // in place
     const Range r[] = {range3("x", same ? nullptr : x, n, heads, dim, x_row, x_head, es, false),
                        range3("out", out, n, heads, dim, out_row, out_head, es, true),
                        range2("positions", positions, n, axes, pos_row, 4, false),

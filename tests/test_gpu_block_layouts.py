@@ -1,0 +1,70 @@
+"""Layouts of packed tensors that the transformer-block entry points take as they are."""
+import ctypes
+
+import pytest
+import torch
+
+import submanifold_sparse_convolution_submconv3d_amd as sc
+
+from gpu_common import note
+
+pytestmark = pytest.mark.gpu
+DEV = torch.device("cuda:0")
+F32, BF16 = torch.float32, torch.bfloat16
+
+
+def randn(*shape, dtype=F32, seed=0):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return torch.randn(shape, generator=g, device="cuda").to(dtype)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("order", ["heads, 3, rows", "rows, heads, 3", "3, heads, rows", "heads, rows, 3"])
+def test_packed_projections_and_gradients(order, dtype):
+    """Queries, keys and values, and their gradients, as parts of one tensor in any order of heads, parts and
+    rows: the same bits as in tensors of their own."""
+    n, h, d = 83, 3, 40
+    shape = {"heads": h, "3": 3, "rows": n}
+    names = order.split(", ")
+    perm = [names.index(x) for x in ("3", "rows", "heads")] + [3]
+    part = lambda t: t.permute(perm).unbind(0)  # noqa: E731
+    packed = randn(*(shape[x] for x in names), d, dtype=dtype, seed=1)
+    off = torch.tensor([0, 30, n], dtype=torch.int32, device=DEV)
+    grad = randn(n, h, d, dtype=dtype, seed=2)
+    note("packed %s %s" % (order, dtype))
+    own = [t.contiguous() for t in part(packed)]
+    expect, elos = sc.submconv_attention(*own, off, return_lse=True)
+    out, lse = sc.submconv_attention(*part(packed), off, return_lse=True)
+    assert torch.equal(out, expect) and torch.equal(lse, elos)
+    room = torch.full_like(packed, 7.0)
+    dq, dk, dv = part(room)
+    sc.submconv_attention_backward(grad, *part(packed), out, lse, off, dq=dq, dk=dk, dv=dv)
+    assert all(torch.equal(a, b) for a, b in zip((dq, dk, dv), sc.submconv_attention_backward(grad, *own, out, lse, off)))
+    # queries turned into the place between other heads, and a result written there
+    pos, freqs = torch.arange(3 * n, dtype=torch.int32, device=DEV).view(n, 3), sc.rotary_freqs((6, 6, 6), device=DEV)
+    q, k, v = part(packed)
+    room = packed.clone()
+    sc.submconv_rotary(part(room)[0], pos, freqs, (6, 6, 6), out=part(room)[2])
+    assert torch.equal(part(room)[2], sc.submconv_rotary(own[0], pos, freqs, (6, 6, 6)))
+    assert torch.equal(part(room)[0], own[0]) and torch.equal(part(room)[1], own[1])
+    room = packed.clone()
+    three = part(room)
+    sc.submconv_attention(three[0], three[1], three[1], off, out=three[2])
+    assert torch.equal(three[2], sc.submconv_attention(own[0], own[1], own[1], off))
+
+
+def test_one_row_in_place_at_any_distance():
+    """A single row is the same memory whatever its row distance."""
+    lib = sc.load_library()
+    x = randn(1, 64)
+    expect, stats = sc.submconv_layer_norm(x, return_stats=True)
+    stream = ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    p = lambda t: ctypes.c_void_p(t.data_ptr())  # noqa: E731
+    note("one row in place")
+    y = x.clone()
+    assert lib.submconv_layer_norm(p(y), 64, 1, 64, 0, None, None, 0, 1e-5, p(y), 80, None, stream) == 0
+    assert torch.equal(y, expect)
+    g = randn(1, 64, seed=3)
+    want = sc.submconv_layer_norm_backward(g, x, stats, need_params=False)[0]
+    assert lib.submconv_layer_norm_backward(p(g), 64, p(x), 64, 1, 64, 0, p(stats), None, 0, p(g), 80, None, None, None, 0, stream) == 0
+    assert torch.equal(g, want)
