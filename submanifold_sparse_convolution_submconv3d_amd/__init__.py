@@ -55,6 +55,7 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_HERE, "_lib", "libsubmconv.so")
 
 F32, BF16 = 0, 1
+OUT_F32 = 256  # added to the type code of an attention call whose out is fp32 (SUBMCONV_OUT_F32)
 KERNEL_AUTO, KERNEL_GENERIC, KERNEL_LOWC, KERNEL_MFMA, KERNEL_WINDOW, KERNEL_PERSISTENT = 0, 1, 2, 3, 4, 5
 
 _lib = None
@@ -651,25 +652,37 @@ def _attention_sizes(q, k, v, q_offsets, k_offsets):
     return (dev,) + tuple(q.shape) + (k.shape[0], k.shape[1], entries)
 
 
+def _attention_code(q: torch.Tensor, out: torch.Tensor) -> int:
+    """Type code of an attention call: out has q's type or is fp32."""
+    if out.dtype == q.dtype:
+        return _dtype_code(q)
+    if out.dtype != torch.float32:
+        raise TypeError("out must be %s or float32, got %s" % (q.dtype, out.dtype))
+    return _dtype_code(q) | OUT_F32
+
+
 def submconv_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_offsets: torch.Tensor,
                        k_offsets: Optional[torch.Tensor] = None, scale: Optional[float] = None,
-                       out: Optional[torch.Tensor] = None, return_lse: bool = False):
+                       out: Optional[torch.Tensor] = None, return_lse: bool = False,
+                       out_dtype: Optional[torch.dtype] = None):
     """Softmax attention inside each entry of a ragged batch -> out [Nq,H,D], or (out, lse) with
     lse fp32 [Nq,H] for the backward pass.
 
     q [Nq,H,D], k and v [Nk,Hk,D] with H a multiple of Hk, D a multiple of 8 up to 128; strided
     views (parts of a packed projection) are taken as they are.  Offsets int32 [entries+1] on the
     device (batch_offsets); k_offsets None: those of the queries.  scale None: 1/sqrt(D).  Queries
-    of an entry without keys, and rows outside every entry, give zeros (lse -inf)."""
+    of an entry without keys, and rows outside every entry, give zeros (lse -inf).  out_dtype (or
+    `out`) may be float32 beside bf16 tensors: the result without its last rounding, from which the
+    backward pass takes more accurate gradients."""
     k_offsets = q_offsets if k_offsets is None else k_offsets
     dev, nq, h, d, nk, hk, entries = _attention_sizes(q, k, v, q_offsets, k_offsets)
     if out is None:
-        out = torch.empty((nq, h, d), dtype=q.dtype, device=dev)
-    elif tuple(_strided(out, "out", 3, dev, q.dtype).shape) != (nq, h, d):
+        out = torch.empty((nq, h, d), dtype=out_dtype or q.dtype, device=dev)
+    elif tuple(_strided(out, "out", 3, dev, out_dtype).shape) != (nq, h, d):
         raise ValueError("out must be [Nq,H,D]")
     lse = torch.empty((nq, h), dtype=torch.float32, device=dev) if return_lse else None
     lib = _lib if _lib is not None else load_library()
-    code = _dtype_code(q)
+    code = _attention_code(q, out)
     nbytes = lib.submconv_attention_workspace(entries, nq, nk, h, hk, d, code)
     ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
     strides = (ctypes.c_int64 * 8)(*_head_strides(q), *_head_strides(k), *_head_strides(v), *_head_strides(out))
@@ -689,11 +702,13 @@ def submconv_attention_backward(grad: torch.Tensor, q: torch.Tensor, k: torch.Te
                                 dv: Optional[torch.Tensor] = None):
     """Gradients of submconv_attention -> (dq, dk, dv), from its out and lse.  A shared key head's
     gradient is summed over its query heads.  dq, dk, dv may be given (parts of a packed gradient).
-    Sums run in a fixed order: equal calls give equal bits."""
+    Sums run in a fixed order: equal calls give equal bits.  With bf16 tensors, `out` kept in float32
+    (the forward's out_dtype) spares dq and dk the rounding of out, which is the largest part of
+    their error where the softmax is peaked or v has a common offset."""
     k_offsets = q_offsets if k_offsets is None else k_offsets
     dev, nq, h, d, nk, hk, entries = _attention_sizes(q, k, v, q_offsets, k_offsets)
-    for name, t in (("grad", grad), ("out", out)):
-        if tuple(_strided(t, name, 3, dev, q.dtype).shape) != (nq, h, d):
+    for name, t, kind in (("grad", grad, q.dtype), ("out", out, None)):
+        if tuple(_strided(t, name, 3, dev, kind).shape) != (nq, h, d):
             raise ValueError("%s must be [Nq,H,D]" % name)
     if tuple(_dev(lse, "lse", torch.float32).shape) != (nq, h) or lse.device != dev:
         raise ValueError("lse must be fp32 [Nq,H] on q's device")
@@ -706,7 +721,7 @@ def submconv_attention_backward(grad: torch.Tensor, q: torch.Tensor, k: torch.Te
         made.append(t)
     dq, dk, dv = made
     lib = _lib if _lib is not None else load_library()
-    code = _dtype_code(q)
+    code = _attention_code(q, out)
     nbytes = lib.submconv_attention_backward_workspace(entries, nq, nk, h, hk, d, code)
     ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
     strides = (ctypes.c_int64 * 16)(*[s for t in (grad, q, k, v, out, dq, dk, dv) for s in _head_strides(t)])

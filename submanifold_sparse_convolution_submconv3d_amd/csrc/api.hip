@@ -859,11 +859,13 @@ int submconv_rotary(const void *x, int64_t x_row, int64_t x_head, const int32_t 
                   out, out_row, out_head, (hipStream_t)stream);
 }
 
-// Sizes of an attention call, checked, into A (pointers stay zero).
+// Sizes of an attention call, checked, into A (pointers stay zero).  Takes the flag out of dtype.
 static int attn_sizes(AttnArgs *A, int32_t entries, int64_t nq, int64_t nk, int32_t heads, int32_t kv_heads,
-                      int32_t dim, int32_t dtype)
+                      int32_t dim, int32_t &dtype)
 {
     *A = AttnArgs{};
+    A->out_f32 = dtype >= 0 && (dtype & SUBMCONV_OUT_F32);
+    if (A->out_f32) dtype &= ~SUBMCONV_OUT_F32;
     if (!known_dtype(dtype)) return fail(SUBMCONV_E_UNSUPPORTED, "dtype %d", dtype);
     if (entries < 1 || entries > 1 << 20) return fail(SUBMCONV_E_INVALID_ARG, "entries = %d outside 1..2^20", entries);
     if (kv_heads < 1 || heads < kv_heads || heads > 1024 || heads % kv_heads)
@@ -943,7 +945,7 @@ int submconv_attention(const void *q, const void *k, const void *v, const int64_
     SC_CHECK(attn_tensor("q", q, strides, nq, heads, dim, es, false, &A.q, &r[0]));
     SC_CHECK(attn_tensor("k", k, strides + 2, nk, kv_heads, dim, es, false, &A.k, &r[1]));
     SC_CHECK(attn_tensor("v", v, strides + 4, nk, kv_heads, dim, es, false, &A.v, &r[2]));
-    SC_CHECK(attn_tensor("out", out, strides + 6, nq, heads, dim, es, true, &A.out, &r[3]));
+    SC_CHECK(attn_tensor("out", out, strides + 6, nq, heads, dim, A.out_f32 ? 4 : es, true, &A.out, &r[3]));
     r[4] = range1("lse", lse, (size_t)nq * heads * 4, true);
     r[5] = range1("workspace", workspace, need, true);
     r[6] = range1("q_offsets", q_offsets, ob, false);
@@ -978,7 +980,7 @@ int submconv_attention_backward(const void *grad, const void *q, const void *k, 
     SC_CHECK(attn_tensor("q", q, strides + 2, nq, heads, dim, es, false, &A.q, &r[1]));
     SC_CHECK(attn_tensor("k", k, strides + 4, nk, kv_heads, dim, es, false, &A.k, &r[2]));
     SC_CHECK(attn_tensor("v", v, strides + 6, nk, kv_heads, dim, es, false, &A.v, &r[3]));
-    SC_CHECK(attn_tensor("out", out, strides + 8, nq, heads, dim, es, false, &A.out, &r[4]));
+    SC_CHECK(attn_tensor("out", out, strides + 8, nq, heads, dim, A.out_f32 ? 4 : es, false, &A.out, &r[4]));
     SC_CHECK(attn_tensor("dq", dq, strides + 10, nq, heads, dim, es, true, &A.dq, &r[5]));
     SC_CHECK(attn_tensor("dk", dk, strides + 12, nk, kv_heads, dim, es, true, &A.dk, &r[6]));
     SC_CHECK(attn_tensor("dv", dv, strides + 14, nk, kv_heads, dim, es, true, &A.dv, &r[7]));

@@ -569,6 +569,20 @@ __device__ __forceinline__ void store4(uint16_t *p, f32x4 v)
     p[3] = (uint16_t)(b >> 16);
 }
 
+// Store into the output, of type T or fp32: `at` is the row's first element.
+template <typename T, int DB>
+__device__ __forceinline__ void store_out(const f32x16 (&acc)[DB], float f, void *out, bool f32, int64_t at, int dim, bool valid)
+{
+    if (sizeof(T) == 4 || f32) store_rows<float>(acc, f, (float *)out + at, dim, valid);
+    else store_rows<T>(acc, f, (T *)out + at, dim, valid);
+}
+template <typename T>
+__device__ __forceinline__ void store4_out(f32x4 v, void *out, bool f32, int64_t at)
+{
+    if (sizeof(T) == 4 || f32) store4((float *)out + at, v);
+    else store4((T *)out + at, v);
+}
+
 // --------------------------------------------------------------------------
 // arguments
 // --------------------------------------------------------------------------
@@ -580,6 +594,7 @@ struct AttnArgs {
     int64_t nq, nk;
     int heads, kv_heads, group, dim;
     float scale;
+    bool out_f32;  // out is fp32 beside bf16 tensors
     float *lse;    // [nq, heads]
     float *stat;   // [nq, heads, 2]: (base, delta) of a query row (backward)
     float *part;   // partial results of a split pass

@@ -340,8 +340,8 @@ __global__ __launch_bounds__(64 * FWD_WAVES, fwd_residency(DP * sizeof(T))) void
             store_rows<float>(o, 1.0f, A.part + at * A.dim, A.dim, valid);
             if (valid && half == 0) *(float2 *)(A.part2 + 2 * at) = make_float2(m, sum);
         } else {
-            T *op = (T *)A.out.p + (q_beg + token) * A.out.row + head * A.out.head;
-            store_rows<T>(o, sum > 0.0f ? 1.0f / sum : (sum == 0.0f ? 0.0f : sum), op, A.dim, valid);
+            store_out<T>(o, sum > 0.0f ? 1.0f / sum : (sum == 0.0f ? 0.0f : sum), (void *)A.out.p, A.out_f32,
+                         (q_beg + token) * A.out.row + head * A.out.head, A.dim, valid);
             if (A.lse && valid && half == 0) A.lse[(q_beg + token) * A.heads + head] = log_sum(m, sum, A.scale);
         }
     }
@@ -410,7 +410,7 @@ __global__ __launch_bounds__(64 * JOIN_WAVES) void k_attn_join(AttnArgs A)
     for (int i = 1; i < groups * A.tiles; ++i) sum += acc[first + i / groups][i % groups * pieces + e];
     for (int i = 1; i < A.tiles; ++i) l += part_l[first + i];
     sum *= l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);
-    store4((T *)A.out.p + token * A.out.row + head * A.out.head + 4 * e, sum);
+    store4_out<T>(sum, (void *)A.out.p, A.out_f32, token * A.out.row + head * A.out.head + 4 * e);
     if (A.lse && e == 0) A.lse[at] = log_sum(top, l, A.scale);
 }
 
@@ -452,7 +452,7 @@ __global__ __launch_bounds__(256) void k_attn_join_cut(AttnArgs A)
                 sum += v[i] * f;
             }
         sum *= l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);
-        store4((T *)A.out.p + (w.own_beg + token) * A.out.row + head * A.out.head + 4 * e, sum);
+        store4_out<T>(sum, (void *)A.out.p, A.out_f32, (w.own_beg + token) * A.out.row + head * A.out.head + 4 * e);
         if (A.lse && e == 0) A.lse[(w.own_beg + token) * A.heads + head] = log_sum(top, l, A.scale);
     }
 }

@@ -22,7 +22,9 @@ __device__ __forceinline__ float lse_base(float lse) { return lse == -INFINITY ?
 // A step handles 32 keys: the matrix cores form s^T = k q^T and dp^T = v g^T of the next
 // keys while ds of its own is computed, then add k^T ds.  Keys and values are copied three
 // steps ahead into rings of four tiles in LDS.  Leaves (base, delta) of every query
-// row for k_attn_dkv.  7042 + 5906 rows x 8 x 128 bf16: 472 us, 1.10 PFLOP/s of its three
+// row for k_attn_dkv.  delta comes from out as it is stored: forming it as sum_k p dp instead would
+// take another product here (dq needs sum_k p k to be set right afterwards); a caller to whom
+// the rounding of a bf16 out matters keeps it in fp32.  7042 + 5906 rows x 8 x 128 bf16: 472 us, 1.10 PFLOP/s of its three
 // products.
 constexpr int dq_residency(int rb) { return rb > 256 ? 1 : 2; }  // waves a SIMD
 
@@ -97,7 +99,7 @@ __global__ __launch_bounds__(64 * BWD_WAVES, dq_residency(DP * sizeof(T))) void 
         if (valid) {
             const T *qp = (const T *)A.q.p + (q_beg + token) * A.q.row + head * A.q.head;
             const T *gp = (const T *)A.grad.p + (q_beg + token) * A.grad.row + head * A.grad.head;
-            const T *op = (const T *)A.out.p + (q_beg + token) * A.out.row + head * A.out.head;
+            const int64_t o = (q_beg + token) * A.out.row + head * A.out.head;
             base = lse_base(A.lse[at]);
 #pragma unroll
             for (int j = 0; j < NJ; ++j) {
@@ -107,7 +109,12 @@ __global__ __launch_bounds__(64 * BWD_WAVES, dq_residency(DP * sizeof(T))) void 
                 g[j] = *(const Raw16Any *)(gp + e);
                 float a[VEC<T>], b[VEC<T>];
                 unpack(g[j], a, gp);
-                unpack((Raw16) * (const Raw16Any *)(op + e), b, gp);
+                if (sizeof(T) == 2 && A.out_f32) {
+#pragma unroll
+                    for (int i = 0; i < VEC<T>; ++i) b[i] = ((const float *)A.out.p)[o + e + i];
+                } else {
+                    unpack((Raw16) * (const Raw16Any *)((const T *)A.out.p + o + e), b, gp);
+                }
 #pragma unroll
                 for (int i = 0; i < VEC<T>; ++i) delta += a[i] * b[i];
             }

@@ -6,7 +6,7 @@ import pytest
 
 import submanifold_sparse_convolution_submconv3d_amd as sc
 
-from test_block_abi_cpu import E_ALIAS, E_INVALID_ARG, attention, attention_bwd
+from test_block_abi_cpu import E_ALIAS, E_INVALID_ARG, E_UNSUPPORTED, attention, attention_bwd
 
 
 @pytest.fixture(scope="module")
@@ -41,3 +41,19 @@ def test_interleaved_outputs_that_overlap_are_refused(lib):
     # a written tensor between the heads of one that is read, the last of its rows one element too far
     strides = (d, 2 * n * d) + (h * d, d) * 2 + (d, 2 * n * d)
     assert attention(lib, strides=strides, out=at(1, n * d + 1), **sizes) == E_ALIAS
+
+
+def test_fp32_out_flag(lib):
+    """SUBMCONV_OUT_F32 beside a known type; an fp32 out has twice the bytes of a bf16 one."""
+    flag = sc.OUT_F32
+    sizes = (2, 100, 100, 4, 2, 64)
+    for dtype in (0, 1):
+        assert attention(lib, nq=0, dtype=dtype | flag) == 0
+        assert lib.submconv_attention_backward_workspace(*sizes, dtype | flag) == lib.submconv_attention_backward_workspace(*sizes, dtype) > 0
+    for dtype in (2 | flag, flag << 1, 1 | flag << 1, -1, -1 & ~flag):
+        assert attention(lib, nq=0, dtype=dtype) == E_UNSUPPORTED, dtype
+        assert lib.submconv_attention_backward_workspace(*sizes, dtype) == 0
+    # 100 rows of 256: past 51200 bytes only if they are fp32
+    near = ctypes.c_void_p((6 << 32) + 60000)
+    assert attention(lib, lse=near, dtype=1 | flag) == E_ALIAS
+    assert attention(lib, out=ctypes.c_void_p((6 << 32) + 2), dtype=1 | flag) == E_INVALID_ARG
