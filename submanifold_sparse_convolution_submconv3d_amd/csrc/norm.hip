@@ -270,14 +270,22 @@ static int64_t norm_blocks(int64_t n, int c, int dtype, int64_t most)
 
 constexpr int64_t NORM_FWD_BLOCKS = 2048;  // eight to a compute unit
 constexpr int64_t NORM_BWD_BLOCKS = 1024;
-// Row groups that one block walks in less time than a second launch takes (450 rows of 16
-// channels: 8 blocks and the sum over them 17.3 us a call, one block 13.9).
-constexpr int64_t NORM_BWD_ALONE = 8;
+// Row groups that one block walks alone, to spare the second launch; where a row takes the whole
+// block, only while the rows are few bytes too.  A call in us, two launches and one:
+//   fp32, 8 groups:  x 16 17.4 and 13.6,  x 128 17.3 and 13.5,  x 1024 17.4 and 13.7
+//   fp32, 32 groups: x 16 17.5 and 16.8,  x 128 17.3 and 17.0,  x 1024 17.4 and 44.4
+//   fp32 x 2560:  6 rows 17.4 and 13.7,  12 rows 17.6 and 21.5
+//   fp32 x 8192:  2 rows 17.4 and 14.9,  3 rows 17.5 and 19.2,  8 rows 17.6 and 41.0
+//   bf16 x 8192:  4 rows 18.3 and 18.8,  8 rows 18.3 and 25.9
+// Where the host does not set the pace (a replayed graph) the GPU's time counts, and the limit
+// is near four groups (fp32 x 16: 5.2 and 4.7; 8 groups 5.3 and 6.4).
+constexpr int64_t NORM_BWD_ALONE = 8, NORM_BWD_ALONE_BYTES = 64 << 10;
 
 static int64_t norm_bwd_blocks(int64_t n, int c, int dtype)
 {
     const int64_t b = norm_blocks(n, c, dtype, NORM_BWD_BLOCKS);
-    return b > 0 && b <= NORM_BWD_ALONE ? 1 : b;
+    const bool wide = norm_shape(c, dtype).tpr == 256;  // (then b rows in all)
+    return b > 0 && b <= NORM_BWD_ALONE && (!wide || b * c * (dtype == SUBMCONV_F32 ? 4 : 2) <= NORM_BWD_ALONE_BYTES) ? 1 : b;
 }
 
 size_t norm_bwd_workspace(int64_t n, int c, int dtype)
