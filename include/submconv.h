@@ -292,8 +292,8 @@ int submconv_weight_convert(const void *src, int32_t layout, int32_t cout, int32
  *     mean_i = sum_c x[i,c] / c,  rstd_i = 1 / sqrt(sum_c (x[i,c] - mean_i)^2 / c + eps)
  *
  *   x, y   : device [n, c] of dtype, rows x_row / y_row elements apart (x_row >= 0,
- *            y_row >= c), the elements of a row next to each other; any alignment of the
- *            element type.
+ *            y_row >= c, both at most 2^24), the elements of a row next to each other; any
+ *            alignment of the element type.
  *            y may be x itself (same pointer and row distance), else E_ALIAS if they overlap.
  *   c      : 1..8192.
  *   weight : device [c] of param_dtype, or NULL for 1.  bias likewise, or NULL for 0.
@@ -313,8 +313,8 @@ size_t submconv_layer_norm_backward_workspace(int64_t n, int32_t c, int32_t dtyp
 /*
  * Backward pass of submconv_layer_norm: with h = (x - mean) rstd and gw = grad * weight,
  *     dx = rstd (gw - sum(gw)/c - h sum(gw h)/c),  dweight = sum_i grad h,  dbias = sum_i grad.
- *   grad, x, dx : [n, c] of dtype, rows grad_row, x_row, dx_row elements apart.  dx may be
- *            grad itself (same pointer and row distance), else E_ALIAS on overlap.
+ *   grad, x, dx : [n, c] of dtype, rows grad_row, x_row, dx_row elements apart (limits as in
+ *            the forward).  dx may be grad itself (same pointer and row distance), else E_ALIAS on overlap.
  *   stats  : what the forward stored for x.  weight: as in the forward (NULL for 1).
  *   dweight, dbias : device [c] of param_dtype, each may be NULL.  Summed over the rows in
  *            fp32 in a fixed order (the same bits for the same call), rounded once.
@@ -340,7 +340,7 @@ int submconv_layer_norm_backward(const void *grad, int64_t grad_row, const void 
  * which undoes it and is also its gradient.  Pairs past the last section are copied.
  *
  *   x, out : device [n, heads, dim] of dtype; element (i, h, d) at i * row + h * head + d
- *            elements.  out may be x itself (same pointer and distances), else E_ALIAS if the
+ *            elements, row at most 2^24 and head at most 2^40.  out may be x itself (same pointer and distances), else E_ALIAS if the
  *            two ranges overlap.  Any alignment of the element type.
  *   positions : device int32, row i at i * pos_row, one value an axis next to each other (the
  *            z, y, x columns of a coordinate set: coords + 1, pos_row = 4).
@@ -387,9 +387,10 @@ int submconv_rotary(const void *x, int64_t x_row, int64_t x_head, const int32_t 
  * Scores, softmax and sums are fp32.  In bf16 the weights exp(s - max) are rounded to bf16
  * for the product with v (the matrix cores take bf16); the sum of the weights is not.  A
  * caller who wants 32-bit weights passes fp32 tensors (about eight times as long).
- * Outputs may not overlap inputs (E_ALIAS).  Asynchronous; one launch, or two when few
- * queries meet many keys and the keys are split between blocks.  The same call gives the
- * same bits.
+ * Outputs may not overlap inputs (E_ALIAS).  Asynchronous; one launch, and a second that
+ * joins partial results where few queries meet many keys (the keys are split between blocks)
+ * or entries are long (tiles that do not fill the card another time are cut along the keys).
+ * The same call gives the same bits.
  */
 #define SUBMCONV_OUT_F32 256
 #define SUBMCONV_ATTENTION_MAX_DIM 128
@@ -417,8 +418,9 @@ int submconv_attention(const void *q, const void *k, const void *v, const int64_
  * does: of 200 x 200 rows of 64, dq is off by 0.24 % (rms; its own rounding alone 0.17 %) for
  * flat softmaxes and values around 0, but by 0.6 % for peaked ones and by 2.5 % for values
  * around 8.  An fp32 out (SUBMCONV_OUT_F32) leaves 0.24 % and 0.6 % there.
- * Asynchronous; two launches, up to five when a short side is
- * split.  Rows outside every entry get zeros.
+ * Asynchronous; two launches, one for the queries' gradient and one for the keys', each with
+ * a second that joins partial results where it is split or cut (as in the forward): four at
+ * most.  Rows outside every entry get zeros.
  */
 size_t submconv_attention_backward_workspace(int32_t entries, int64_t nq, int64_t nk, int32_t heads, int32_t kv_heads,
                                              int32_t dim, int32_t dtype);

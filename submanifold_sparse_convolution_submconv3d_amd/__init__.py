@@ -8,6 +8,9 @@ library `_lib/libsubmconv.so`.  PyTorch provides device memory and streams.
 If the library has not been built, every call raises: there is no CPU or
 PyTorch fallback.
 
+No call records anything for torch's autograd: results are detached, also of tensors that
+require a gradient.  The backward passes are calls of their own.
+
 Functions carry the C names:
 
     submconv_build_map(coords, res, batch)        -> Rulebook
@@ -524,7 +527,8 @@ def submconv_layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, 
     """Layer normalisation of the rows of x [N,C] (C <= 8192; rows may be strided) -> y, or (y, stats)
     with stats fp32 [N,2] = (mean, 1/std) for the backward pass.
 
-    weight and bias [C] are fp32 or bf16 (None: 1 and 0); statistics are fp32.  `out` may be x."""
+    weight and bias [C] are fp32 or bf16 (None: 1 and 0); statistics are fp32.  `out` may be x.
+    Not recorded by autograd: submconv_layer_norm_backward gives the gradients."""
     dev = _strided(x, "x", 2).device
     n, c = x.shape
     code = _norm_params(x, weight, bias)
@@ -602,7 +606,7 @@ def submconv_rotary(x: torch.Tensor, positions: torch.Tensor, freqs: torch.Tenso
     positions int32 [N,A] (the coords[:, 1:] columns of a voxel set), freqs fp32 [sum(sections)] in
     radians a step, sections = pairs of each axis (their sum <= D/2; the pairs left over are
     copied).  Pair p is elements (2p, 2p+1), or (p, p + D/2) with split.  inverse turns back,
-    which is the gradient.  x may be strided (the query and key part of a packed projection);
+    which is the gradient (autograd does not record this call).  x may be strided (the query and key part of a packed projection);
     `out` may be x itself."""
     dev = _strided(x, "x", 3).device
     _strided(positions, "positions", 2, dev, torch.int32)
@@ -673,7 +677,8 @@ def submconv_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_offs
     device (batch_offsets); k_offsets None: those of the queries.  scale None: 1/sqrt(D).  Queries
     of an entry without keys, and rows outside every entry, give zeros (lse -inf).  out_dtype (or
     `out`) may be float32 beside bf16 tensors: the result without its last rounding, from which the
-    backward pass takes more accurate gradients."""
+    backward pass takes more accurate gradients.  Not recorded by autograd:
+    submconv_attention_backward gives the gradients."""
     k_offsets = q_offsets if k_offsets is None else k_offsets
     dev, nq, h, d, nk, hk, entries = _attention_sizes(q, k, v, q_offsets, k_offsets)
     if out is None:

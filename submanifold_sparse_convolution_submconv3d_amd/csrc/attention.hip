@@ -11,8 +11,8 @@
 // second operand of o^T += v^T p^T.  A block's four waves share tiles of keys and
 // values in LDS.
 //
-// 12,948 x 12 x 128 bf16: 1.03 ms, 992 TFLOP/s (a library product of 8192^3 reaches 1136 on
-// the same card); 32,768 x 12 x 128: 1055.  Bound by what two waves of a SIMD issue: the
+// 12,948 x 12 x 128 bf16: 1.04 ms, 990 TFLOP/s (a library product of 8192^3 reaches 1124 to
+// 1136); 32,768 x 12 x 128: 1051.  Bound by what two waves of a SIMD issue: the
 // matrix pipe is busy about half the time, the softmax's arithmetic takes most of the
 // rest, and one does not hide all of the other.  64 query rows a wave (half the LDS reads)
 // need more registers than there are for two waves and ran 2.7 times as long; eight

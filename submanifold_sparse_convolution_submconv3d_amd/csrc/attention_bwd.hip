@@ -24,8 +24,9 @@ __device__ __forceinline__ float lse_base(float lse) { return lse == -INFINITY ?
 // steps ahead into rings of four tiles in LDS.  Leaves (base, delta) of every query
 // row for k_attn_dkv.  delta comes from out as it is stored: forming it as sum_k p dp instead would
 // take another product here (dq needs sum_k p k to be set right afterwards); a caller to whom
-// the rounding of a bf16 out matters keeps it in fp32.  7042 + 5906 rows x 8 x 128 bf16: 472 us, 1.10 PFLOP/s of its three
-// products.
+// the rounding of a bf16 out matters keeps it in fp32.  7042 + 5906 rows x 8 x 128 bf16: 468 us,
+// 1.11 PFLOP/s of its three products, with 56 registers spilled (two waves a SIMD leave 256).
+// 8000 x 4 x 128 fp32: 1.51 ms, 130 TFLOP/s (a library product of 8192^3 reaches 151).
 constexpr int dq_residency(int rb) { return rb > 256 ? 1 : 2; }  // waves a SIMD
 
 template <typename T, int DP, bool SPLIT, bool DIRECT>
@@ -258,10 +259,10 @@ __global__ __launch_bounds__(64 * BWD_WAVES, dq_residency(DP * sizeof(T))) void 
 // are formed while p and ds of its own are computed, then dv^T += g^T p and dk^T += q^T ds.
 // Rows past the end are copied as zeros; their scores and dp are 0 times a key's elements,
 // which is not 0 where the key holds an infinity, so their weights are set to 0.
-// Same rows: 780 us, 0.89 PFLOP/s of its four products.  At 128 elements a head the keys,
+// Same rows: 755 us, 0.92 PFLOP/s of its four products.  At 128 elements a head the keys,
 // values and both gradients take 192 registers, so one wave runs on a SIMD and its LDS
-// reads and barriers are hidden only by its own products.  One barrier for two steps
-// (rings of five tiles) was no faster there (828 us).
+// reads and barriers are hidden only by its own products; in fp32 the next products'
+// operands do not fit and 141 to 143 registers are spilled (8000 x 4 x 128: 2.64 ms, 99 TFLOP/s).
 constexpr int dkv_residency(int rb) { return rb > 128 ? 1 : 2; }  // waves a SIMD
 
 template <typename T, int DP, bool SPLIT, bool DIRECT>

@@ -42,7 +42,7 @@ __device__ __forceinline__ float row_sum(float v, float *part, int slot)
 // TPR threads hold a row, CH pieces of 16 bytes each; a block of 256 walks rows in
 // grid-sized strides with the next rows' loads issued before the current rows' sums.
 // y may be x (so neither is restrict).
-// 1,187,403 x 64 bf16: 57 us, 5.3 TB/s (a plain device copy reaches 4.8).
+// 1,187,403 x 64 bf16: 56 us, 5.4 TB/s (a plain device copy reaches 4.8 to 4.9).
 template <typename T, int CH, int TPR>
 __global__ __launch_bounds__(256) void k_norm(const T *x, int64_t ldx, int64_t n, int c,
                                               const void *__restrict__ w, const void *__restrict__ b, int pdtype,
@@ -109,7 +109,7 @@ __global__ __launch_bounds__(256) void k_norm(const T *x, int64_t ldx, int64_t n
 // fixed order, written to partial [block][2][c] and summed over blocks by k_norm_wgrad; a
 // single block writes dw and db itself (partial is NULL).  No atomics: the order is fixed.
 // dx may be gy (so neither is restrict).
-// 97,001 x 1024 bf16: 130 us for three passes over the rows, 4.6 TB/s, and 6 us for the sum.
+// 97,001 x 1024 bf16: 135 us for three passes over the rows, 4.4 TB/s, and 6 us for the sum.
 template <typename T, int CH, int TPR>
 __global__ __launch_bounds__(256) void k_norm_bwd(const T *gy, int64_t ldg, const T *__restrict__ x,
                                                   int64_t ldx, int64_t n, int c, const float2 *__restrict__ stats,

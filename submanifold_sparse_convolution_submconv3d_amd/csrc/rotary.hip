@@ -11,8 +11,8 @@
 // The kernel is bound by memory (each element read and written once).  A thread owns
 // one 16-byte piece of the head (a piece of each half in the split layout), forms the
 // sines and cosines of its pairs once and applies them to several heads of the row, four
-// heads' loads in flight at a time.  400,311 x 24 x 128 bf16: 851 us, 5.8 TB/s (a plain
-// device copy reaches 4.8); 20,384 x 24 x 128 inside a packed projection: 45 us, 5.6 TB/s.
+// heads' loads in flight at a time.  400,311 x 24 x 128 bf16: 860 us, 5.7 TB/s (a plain
+// device copy reaches 4.8 to 4.9); 20,384 x 24 x 128 inside a packed projection: 46 us, 5.5 TB/s.
 #include "rowvec.h"
 
 namespace sc {
