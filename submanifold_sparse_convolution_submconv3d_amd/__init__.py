@@ -656,6 +656,10 @@ def _attention_sizes(q, k, v, q_offsets, k_offsets):
     return (dev,) + tuple(q.shape) + (k.shape[0], k.shape[1], entries)
 
 
+def _attention_scale(scale: Optional[float], d: int) -> float:
+    return scale if scale is not None else max(d, 1) ** -0.5
+
+
 def _attention_code(q: torch.Tensor, out: torch.Tensor) -> int:
     """Type code of an attention call: out has q's type or is fp32."""
     if out.dtype == q.dtype:
@@ -694,7 +698,7 @@ def submconv_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_offs
     with _on_device(dev):
         _check(lib.submconv_attention(
             q.data_ptr(), k.data_ptr(), v.data_ptr(), strides, q_offsets.data_ptr(), k_offsets.data_ptr(), entries, nq,
-            nk, h, hk, d, code, d ** -0.5 if scale is None else scale, out.data_ptr(),
+            nk, h, hk, d, code, _attention_scale(scale, d), out.data_ptr(),
             None if lse is None else lse.data_ptr(), None if ws is None else ws.data_ptr(), nbytes,
             _raw_stream(dev.index)), "submconv_attention")
     return (out, lse) if return_lse else out
@@ -734,7 +738,7 @@ def submconv_attention_backward(grad: torch.Tensor, q: torch.Tensor, k: torch.Te
         _check(lib.submconv_attention_backward(
             grad.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(), strides,
             q_offsets.data_ptr(), k_offsets.data_ptr(), entries, nq, nk, h, hk, d, code,
-            d ** -0.5 if scale is None else scale, dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), ws.data_ptr(), nbytes,
+            _attention_scale(scale, d), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), ws.data_ptr(), nbytes,
             _raw_stream(dev.index)), "submconv_attention_backward")
     return dq, dk, dv
 

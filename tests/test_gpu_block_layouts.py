@@ -68,3 +68,13 @@ def test_one_row_in_place_at_any_distance():
     want = sc.submconv_layer_norm_backward(g, x, stats, need_params=False)[0]
     assert lib.submconv_layer_norm_backward(p(g), 64, p(x), 64, 1, 64, 0, p(stats), None, 0, p(g), 80, None, None, None, 0, stream) == 0
     assert torch.equal(g, want)
+
+
+def test_heads_without_elements_are_refused():
+    """The library's own refusal, also where the scale is left to the call."""
+    h, off = randn(6, 2, 0), torch.tensor([0, 6], dtype=torch.int32, device=DEV)
+    note("heads without elements")
+    with pytest.raises(sc.SubmconvError):
+        sc.submconv_attention(h, h, h, off)
+    with pytest.raises(sc.SubmconvError):
+        sc.submconv_attention_backward(h, h, h, h, h, randn(6, 2), off)
