@@ -431,6 +431,171 @@ int submconv_attention_backward(const void *grad, const void *q, const void *k, 
                                 void *dv, void *workspace, size_t workspace_bytes, void *stream);
 
 /*
+ * The root-mean-square norm of each query or key head, with the rotation by the row's positions in
+ * the same pass.  For head vector x of row i and head h, R the rotation that submconv_rotary makes:
+ *
+ *     y[i,h] = R(x * rstd * w),   rstd[i,h] = 1 / sqrt(sum_d x_d^2 / dim + eps)
+ *
+ *   x, out : device [n, heads, dim] of dtype, distances in elements as in submconv_rotary; out may be
+ *            x itself (same pointer and distances), else E_ALIAS on overlap.
+ *   weight : device [weight_rows, dim] of param_dtype, or NULL for 1 (weight_rows is then 1).
+ *            weight_rows = heads: one for each head; 1: one for all; with q_heads > 0 it is 2:
+ *            heads below q_heads take row 0 (queries), the others row 1 (keys).
+ *   q_heads: 0, or 1..heads.
+ *   positions, freqs, sections, axes, split : as in submconv_rotary; axes = 0 leaves the rotation
+ *            out (the pointers may then be NULL).
+ *   dim    : even, 2..512.   heads : 1..1024.   eps >= 0.
+ *   rstd   : device fp32 [n, heads] for the backward pass, or NULL.
+ * The norm and the rotation are fp32, with one rounding to dtype at the end (the two calls
+ * submconv_rotary and a norm round twice).  Asynchronous, one launch.
+ */
+int submconv_head_norm_rotary(const void *x, int64_t x_row, int64_t x_head, const void *weight, int32_t weight_rows,
+                              int32_t q_heads, int32_t param_dtype, float eps, const int32_t *positions,
+                              int64_t pos_row, const float *freqs, const int32_t *sections, int32_t axes, int64_t n,
+                              int32_t heads, int32_t dim, int32_t dtype, int32_t split, void *out, int64_t out_row,
+                              int64_t out_head, float *rstd, void *stream);
+
+/* Bytes of device workspace submconv_head_norm_rotary_backward needs for dweight (0 for bad sizes). */
+size_t submconv_head_norm_rotary_backward_workspace(int64_t n, int32_t heads, int32_t dim, int32_t dtype,
+                                                    int32_t weight_rows, int32_t q_heads);
+
+/*
+ * Backward pass of submconv_head_norm_rotary: with u = R^-1 grad and h = x rstd,
+ *     dx = rstd (u w - h sum_d(u w h) / dim),   dweight = sum of u h over the rows, and over the heads
+ * that share a row of the weight.
+ *   strides : HOST int64 [6]: row and head distance of grad, x, dx.  dx may be grad itself (same
+ *            pointer and distances), else E_ALIAS on overlap.
+ *   rstd   : what the forward stored for x.
+ *   dweight: device [weight_rows, dim] of param_dtype, or NULL; summed in fp32 in a fixed order (the
+ *            same bits for the same call), rounded once.
+ *   workspace : submconv_head_norm_rotary_backward_workspace bytes, 16-byte aligned, contents
+ *            undefined before and after (may be NULL when dweight is).
+ * Asynchronous, one launch, and a second for dweight.
+ */
+int submconv_head_norm_rotary_backward(const void *grad, const void *x, const float *rstd, const void *weight,
+                                       int32_t weight_rows, int32_t q_heads, int32_t param_dtype,
+                                       const int32_t *positions, int64_t pos_row, const float *freqs,
+                                       const int32_t *sections, int32_t axes, const int64_t *strides, int64_t n,
+                                       int32_t heads, int32_t dim, int32_t dtype, int32_t split, void *dx,
+                                       void *dweight, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * The k best experts of each row of scores, their gates, and the plan that groups the (row,
+ * expert) pairs by expert for submconv_grouped_linear and submconv_combine.
+ *
+ *   logits : device [n, experts] of dtype, rows `row` elements apart (row >= 0), any alignment of the type.
+ *   chosen : device int32 [n, k]: experts in descending order of their scores, equal scores by
+ *            number.  A score of -inf closes an expert to the row: it is never chosen, and where
+ *            fewer than k are open the rest is -1.  A NaN comes before all other scores.
+ *   gates  : device fp32 [n, k]: normalize = 1: the softmax over the row's chosen experts;
+ *            0: their share of the softmax over all experts.  0 beside a -1.  A NaN or +inf among
+ *            the scores makes the row's gates NaN.
+ *   offsets: device int32 [experts + 1]: expert e has the positions [offsets[e], offsets[e + 1]), its
+ *            rows ascending.  From offsets[experts] on: the pairs without an expert, in order.
+ *   rows   : device int32 [n k]: the row of each position.
+ *   slots  : device int32 [n, k]: the position of each pair (a permutation of 0 .. n k - 1).
+ *   experts: 1..SUBMCONV_ROUTE_MAX_EXPERTS.  k : 1..min(experts, SUBMCONV_ROUTE_MAX_K).  n k < 2^31.
+ *   workspace : submconv_route_workspace bytes, 16-byte aligned (NULL when that is 0), contents
+ *            undefined before and after.
+ * Asynchronous; the plan is exact and the same call gives the same bits.  n = 0 writes offsets alone.
+ */
+#define SUBMCONV_ROUTE_MAX_EXPERTS 512
+#define SUBMCONV_ROUTE_MAX_K 16
+size_t submconv_route_workspace(int64_t n, int32_t experts, int32_t k);
+int submconv_route(const void *logits, int64_t row, int64_t n, int32_t experts, int32_t k, int32_t dtype,
+                   int32_t normalize, int32_t *chosen, float *gates, int32_t *offsets, int32_t *rows, int32_t *slots,
+                   void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Gradient of the gates of submconv_route: with d_j = grad[i,j] gates[i,j],
+ *     dlogits[i,e] = (sum of d_j with chosen[i,j] = e) - p_e sum_j d_j
+ * where p is the softmax over the chosen experts (normalize = 1) or over all (0; a row with no open
+ * expert gives zeros).  Numbers outside [0, experts) in chosen stand for no expert.
+ *   grad, gates : device fp32 [n, k];  chosen : device int32 [n, k];  logits : as in submconv_route
+ *   (not read, may be NULL, with normalize = 1);  dlogits : device [n, experts] of dtype, out_row >= experts.
+ * fp32, one rounding at the end.  Asynchronous, one launch.
+ */
+int submconv_route_backward(const float *grad, const void *logits, int64_t row, int64_t n, int32_t experts, int32_t k,
+                            int32_t dtype, int32_t normalize, const int32_t *chosen, const float *gates, void *dlogits,
+                            int64_t out_row, void *stream);
+
+/*
+ * Matrix products of ragged groups of rows, each group with its own weight (experts, or the entries of
+ * a batch).  For position i of group g:
+ *
+ *     out[i] = weight[g] x[rows[i]] + bias[g]
+ *
+ *   x      : device [nx, cin] of dtype, rows x_row elements apart (0..2^24), any alignment of the type.
+ *   rows   : device int32 [n], the row of x that each position takes, or NULL for the position
+ *            itself (nx is then n).  Any order, any number of times; a number outside [0, nx) reads zeros.
+ *   weight : device [groups, cout, cin] of dtype, contiguous.
+ *   bias   : device fp32 [groups, cout], or NULL.
+ *   offsets: device int32 [groups + 1], ascending: group g has the positions [offsets[g],
+ *            offsets[g + 1]).  Read on the device only.  Positions before the first and from the
+ *            last offset on belong to no group and get zeros.  Each offset counts as the largest
+ *            up to it, clamped to [0, n]: bad offsets give wrong rows, never stray accesses.
+ *   out    : device [n, cout] of dtype, rows out_row >= cout elements apart; must not overlap an input.
+ *   cin, cout : 1..65536.   groups : 1..65536.   groups cin cout < 2^40.   n, nx < 2^31 - 2^16.  Tiles of all
+ *            groups must fit a launch (E_UNSUPPORTED beyond 2^24 blocks).
+ * Products of the tensors' type on the matrix cores, sums and bias fp32, one rounding at the end.
+ * Asynchronous; the same call gives the same bits.
+ */
+int submconv_grouped_linear(const void *x, int64_t x_row, int64_t nx, const int32_t *rows, const void *weight,
+                            const float *bias, const int32_t *offsets, int32_t groups, int64_t n, int32_t cin,
+                            int32_t cout, int32_t dtype, void *out, int64_t out_row, void *stream);
+
+/* Bytes of device workspace submconv_grouped_linear_backward needs (may be 0; 0 for bad sizes). */
+size_t submconv_grouped_linear_backward_workspace(int32_t groups, int64_t n, int32_t cin, int32_t cout, int32_t dtype);
+
+/*
+ * Gradients of submconv_grouped_linear from grad [n, cout] (rows grad_row apart):
+ *   dx      : device [n, cin] of dtype, of the rows as they were taken: dx[i] = weight[g]^T grad[i]
+ *             (submconv_combine without gates sums them for each row of x).  Zeros for positions of no
+ *             group.  Or NULL.
+ *   dweight : device [groups, cout, cin] of dtype: sum over the group's positions of grad[i] x[rows[i]]^T,
+ *             zeros for an empty group.  Or NULL.
+ *   dbias   : device fp32 [groups, cout], sum of grad[i]; only together with dweight.  Or NULL.
+ *   x, rows may be NULL where dweight is, weight where dx is.
+ *   workspace : submconv_grouped_linear_backward_workspace bytes, 16-byte aligned (NULL when that is 0).
+ * Sums are fp32 in a fixed order, one rounding at the end.  Asynchronous.
+ */
+int submconv_grouped_linear_backward(const void *grad, int64_t grad_row, const void *x, int64_t x_row, int64_t nx,
+                                     const int32_t *rows, const void *weight, const int32_t *offsets, int32_t groups,
+                                     int64_t n, int32_t cin, int32_t cout, int32_t dtype, void *dx, int64_t dx_row,
+                                     void *dweight, float *dbias, void *workspace, size_t workspace_bytes,
+                                     void *stream);
+
+/*
+ * The sum of each row's expert results, weighted by its gates:
+ *
+ *     out[i] = sum_j gates[i,j] y[slots[i,j]]
+ *
+ *   y      : device [np, c] of dtype, rows y_row elements apart (0..2^24).
+ *   slots  : device int32 [n, k]; a number outside [0, np) adds nothing.
+ *   gates  : device fp32 [n, k], or NULL for 1 (the gradient of a gather of rows).
+ *   out    : device [n, c] of dtype, rows out_row >= c elements apart; must not overlap an input.
+ *   c      : 1..65536.   k : 1..SUBMCONV_ROUTE_MAX_K.
+ * fp32 sums in the order of j, one rounding.  Asynchronous, one launch.
+ */
+int submconv_combine(const void *y, int64_t y_row, int64_t np, const int32_t *slots, const float *gates, int64_t n,
+                     int32_t k, int32_t c, int32_t dtype, void *out, int64_t out_row, void *stream);
+
+/*
+ * Gradients of submconv_combine from grad [n, c]:
+ *     dy[slots[i,j]] = gates[i,j] grad[i],   dgates[i,j] = grad[i] . y[slots[i,j]]
+ *   rows   : device int32 [np], the row of each position (submconv_route's): position p of dy is the
+ *            gradient of row rows[p], with the sum of that row's gates whose slot is p.  A position
+ *            that its row does not name gets zeros.
+ *   dy     : device [np, c] of dtype, rows dy_row >= c apart, or NULL (rows may then be NULL).
+ *   dgates : device fp32 [n, k], or NULL (y may then be NULL); 0 for a slot outside [0, np).
+ *   gates may be NULL for 1.
+ * Sums are fp32 in a fixed order.  Asynchronous, one launch.
+ */
+int submconv_combine_backward(const void *grad, int64_t grad_row, const void *y, int64_t y_row, int64_t np,
+                              const int32_t *slots, const int32_t *rows, const float *gates, int64_t n, int32_t k,
+                              int32_t c, int32_t dtype, void *dy, int64_t dy_row, float *dgates, void *stream);
+
+/*
  * The library keeps device blocks it has freed (rulebooks, scratch) for reuse on the
  * same device, up to a limit per device (2 GiB unless set below), so that repeated
  * builds make no driver allocation calls.  A block freed while work queued on its

@@ -30,6 +30,14 @@ Functions carry the C names:
     submconv_attention(q, k, v, q_offsets, k_offsets) -> out (and its log-sum-exp)
     submconv_attention_backward(grad, q, k, v, out, lse, q_offsets, k_offsets) -> (dq, dk, dv)
     batch_offsets(coords, batch)                    -> offsets of a coordinate set's batch entries
+    submconv_head_norm_rotary(x, weight, positions, freqs, sections) -> normed and rotated heads (and their 1/rms)
+    submconv_head_norm_rotary_backward(grad, x, rstd, weight, positions, freqs, sections) -> (dx, dweight)
+    submconv_route(logits, k)                       -> Route(experts, gates, offsets, rows, slots)
+    submconv_route_backward(grad, logits, experts, gates) -> dlogits
+    submconv_grouped_linear(x, weight, offsets, bias, rows) -> out
+    submconv_grouped_linear_backward(grad, x, weight, offsets, rows) -> (dx, dweight, dbias)
+    submconv_combine(y, slots, gates)               -> out
+    submconv_combine_backward(grad, y, slots, rows, gates) -> (dy, dgates)
 
 `RulebookCache` keeps one rulebook per coordinate set, keyed like the
 upstream library's indice_key, so every convolution on a set reuses its map
@@ -40,7 +48,7 @@ from __future__ import annotations
 import ctypes
 import os
 import weakref
-from typing import Optional
+from typing import NamedTuple, Optional
 
 import torch
 
@@ -51,6 +59,8 @@ __all__ = [
     "POOL_MAX", "POOL_MEAN", "classify_5d", "weight_to_krsc", "flip_ab", "release_cache", "set_cache_limit",
     "submconv_layer_norm", "submconv_layer_norm_backward", "submconv_rotary", "rotary_freqs",
     "submconv_attention", "submconv_attention_backward", "batch_offsets",
+    "submconv_head_norm_rotary", "submconv_head_norm_rotary_backward", "Route", "submconv_route", "submconv_route_backward",
+    "submconv_grouped_linear", "submconv_grouped_linear_backward", "submconv_combine", "submconv_combine_backward",
     "KERNEL_AUTO", "KERNEL_GENERIC", "KERNEL_LOWC", "KERNEL_MFMA", "KERNEL_WINDOW", "KERNEL_PERSISTENT",
 ]
 
@@ -113,6 +123,17 @@ def load_library():
                                ctypes.c_size_t, vp],
         "submconv_attention_backward": [vp, vp, vp, vp, vp, vp, i64p, vp, vp, i32, i64, i64, i32, i32, i32, i32, f32,
                                         vp, vp, vp, vp, ctypes.c_size_t, vp],
+        "submconv_head_norm_rotary": [vp, i64, i64, vp, i32, i32, i32, f32, vp, i64, vp, i32p, i32, i64, i32, i32, i32, i32,
+                                      vp, i64, i64, vp, vp],
+        "submconv_head_norm_rotary_backward": [vp, vp, vp, vp, i32, i32, i32, vp, i64, vp, i32p, i32, i64p, i64, i32, i32,
+                                               i32, i32, vp, vp, vp, ctypes.c_size_t, vp],
+        "submconv_route": [vp, i64, i64, i32, i32, i32, i32, vp, vp, vp, vp, vp, vp, ctypes.c_size_t, vp],
+        "submconv_route_backward": [vp, vp, i64, i64, i32, i32, i32, i32, vp, vp, vp, i64, vp],
+        "submconv_grouped_linear": [vp, i64, i64, vp, vp, vp, vp, i32, i64, i32, i32, i32, vp, i64, vp],
+        "submconv_grouped_linear_backward": [vp, i64, vp, i64, i64, vp, vp, vp, i32, i64, i32, i32, i32, vp, i64, vp, vp,
+                                             vp, ctypes.c_size_t, vp],
+        "submconv_combine": [vp, i64, i64, vp, vp, i64, i32, i32, i32, vp, i64, vp],
+        "submconv_combine_backward": [vp, i64, vp, i64, i64, vp, vp, vp, i64, i32, i32, i32, vp, i64, vp, vp],
     }
     for name, args in sig.items():
         fn = getattr(lib, name)
@@ -120,6 +141,12 @@ def load_library():
         fn.restype = ctypes.c_int
     for name in ("submconv_attention_workspace", "submconv_attention_backward_workspace"):
         getattr(lib, name).argtypes = [i32, i64, i64, i32, i32, i32, i32]
+        getattr(lib, name).restype = ctypes.c_size_t
+    lib.submconv_head_norm_rotary_backward_workspace.argtypes = [i64, i32, i32, i32, i32, i32]
+    lib.submconv_route_workspace.argtypes = [i64, i32, i32]
+    lib.submconv_grouped_linear_backward_workspace.argtypes = [i32, i64, i32, i32, i32]
+    for name in ("submconv_head_norm_rotary_backward_workspace", "submconv_route_workspace",
+                 "submconv_grouped_linear_backward_workspace"):
         getattr(lib, name).restype = ctypes.c_size_t
     lib.submconv_layer_norm_backward_workspace.argtypes = [i64, i32, i32]
     lib.submconv_layer_norm_backward_workspace.restype = ctypes.c_size_t
@@ -741,6 +768,285 @@ def submconv_attention_backward(grad: torch.Tensor, q: torch.Tensor, k: torch.Te
             _attention_scale(scale, d), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), ws.data_ptr(), nbytes,
             _raw_stream(dev.index)), "submconv_attention_backward")
     return dq, dk, dv
+
+
+def _ptr(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
+def _same_device(t: Optional[torch.Tensor], name: str, dtype, device, shape) -> Optional[torch.Tensor]:
+    """A contiguous tensor of this type, device and shape (None passes)."""
+    if t is not None:
+        if _dev(t, name, dtype).device != device:
+            raise ValueError("%s is on %s, not on %s" % (name, t.device, device))
+        if tuple(t.shape) != tuple(shape):
+            raise ValueError("%s must be %s, got %s" % (name, list(shape), list(t.shape)))
+    return t
+
+
+def _workspace(nbytes: int, device) -> Optional[torch.Tensor]:
+    return torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
+
+
+def _head_norm_args(x, weight, positions, freqs, sections, q_heads):
+    """Checks shared by both directions -> (device, weight's rows, its type code, sections)."""
+    dev = _strided(x, "x", 3).device
+    n, h, d = x.shape
+    many, code = 1, F32
+    if weight is not None:
+        code = _dtype_code(weight)
+        many = weight.shape[0] if weight.dim() == 2 else 1
+        if (2 if q_heads else many) != many or many not in (1, 2 if q_heads else 1, h):
+            raise ValueError("weight must be [D], [H,D], or [2,D] with q_heads")
+        _same_device(weight, "weight", None, dev, (d,) if weight.dim() == 1 else (many, d))
+    elif q_heads:
+        raise ValueError("q_heads without a weight")
+    sections = tuple(sections) if positions is not None else ()
+    if positions is not None:
+        _strided(positions, "positions", 2, dev, torch.int32)
+        if tuple(positions.shape) != (n, len(sections)):
+            raise ValueError("positions must be [N,%d]" % len(sections))
+        if freqs is None:
+            raise ValueError("positions without freqs")
+        _same_device(freqs, "freqs", torch.float32, dev, (sum(sections),))
+    return dev, many, code, sections
+
+
+def submconv_head_norm_rotary(x: torch.Tensor, weight: Optional[torch.Tensor] = None, positions: Optional[torch.Tensor] = None,
+                              freqs: Optional[torch.Tensor] = None, sections=(), eps: float = 1e-6, q_heads: int = 0,
+                              split: bool = False, out: Optional[torch.Tensor] = None, return_rstd: bool = False):
+    """Root-mean-square norm of the head vectors x [N,H,D] and their rotation by integer positions, in one
+    pass -> y, or (y, rstd) with rstd fp32 [N,H] for the backward pass.
+
+    weight (fp32 or bf16; None: 1) is [H,D], one for each head, [D], one for all, or [2,D] with q_heads: heads
+    below q_heads are queries (row 0), the others keys (row 1).  positions, freqs, sections and split are
+    those of submconv_rotary; without positions nothing turns.  x may be strided (the query and key part
+    of a packed projection); `out` may be x itself.  fp32, one rounding at the end.  Not recorded by
+    autograd: submconv_head_norm_rotary_backward gives the gradients."""
+    dev, many, code, sections = _head_norm_args(x, weight, positions, freqs, sections, q_heads)
+    n, h, d = x.shape
+    if out is None:
+        out = torch.empty((n, h, d), dtype=x.dtype, device=dev)
+    elif tuple(_strided(out, "out", 3, dev, x.dtype).shape) != (n, h, d):
+        raise ValueError("out must be [N,H,D]")
+    rstd = torch.empty((n, h), dtype=torch.float32, device=dev) if return_rstd else None
+    xs, os_ = _head_strides(x), _head_strides(out)
+    lib = _lib if _lib is not None else load_library()
+    with _on_device(dev):
+        _check(lib.submconv_head_norm_rotary(
+            x.data_ptr(), xs[0], xs[1], _ptr(weight), many, q_heads, code, eps, _ptr(positions),
+            0 if positions is None else _row_stride(positions), None if positions is None else freqs.data_ptr(),
+            (ctypes.c_int32 * max(1, len(sections)))(*sections), len(sections), n, h, d, _dtype_code(x), int(bool(split)),
+            out.data_ptr(), os_[0], os_[1], _ptr(rstd), _raw_stream(dev.index)), "submconv_head_norm_rotary")
+    return (out, rstd) if return_rstd else out
+
+
+def submconv_head_norm_rotary_backward(grad: torch.Tensor, x: torch.Tensor, rstd: torch.Tensor, weight: Optional[torch.Tensor] = None,
+                                       positions: Optional[torch.Tensor] = None, freqs: Optional[torch.Tensor] = None, sections=(),
+                                       q_heads: int = 0, split: bool = False, dx: Optional[torch.Tensor] = None,
+                                       need_weight: bool = True):
+    """Gradients of submconv_head_norm_rotary -> (dx, dweight).
+
+    `rstd` is what the forward returned for x.  dweight has weight's shape and type (None without a weight
+    or with need_weight=False), summed in a fixed order, so equal calls give equal bits.  dx may be given
+    (part of a packed gradient, or grad itself)."""
+    dev, many, code, sections = _head_norm_args(x, weight, positions, freqs, sections, q_heads)
+    n, h, d = x.shape
+    if tuple(_strided(grad, "grad", 3, dev, x.dtype).shape) != (n, h, d):
+        raise ValueError("grad must be [N,H,D]")
+    _same_device(rstd, "rstd", torch.float32, dev, (n, h))
+    if dx is None:
+        dx = torch.empty((n, h, d), dtype=x.dtype, device=dev)
+    elif tuple(_strided(dx, "dx", 3, dev, x.dtype).shape) != (n, h, d):
+        raise ValueError("dx must be [N,H,D]")
+    lib = _lib if _lib is not None else load_library()
+    dw = ws = None
+    nbytes = 0
+    if weight is not None and need_weight:
+        dw = torch.empty_like(weight)
+        nbytes = lib.submconv_head_norm_rotary_backward_workspace(n, h, d, _dtype_code(x), many, q_heads)
+        ws = _workspace(nbytes, dev)
+    strides = (ctypes.c_int64 * 6)(*_head_strides(grad), *_head_strides(x), *_head_strides(dx))
+    with _on_device(dev):
+        _check(lib.submconv_head_norm_rotary_backward(
+            grad.data_ptr(), x.data_ptr(), rstd.data_ptr(), _ptr(weight), many, q_heads, code, _ptr(positions),
+            0 if positions is None else _row_stride(positions), None if positions is None else freqs.data_ptr(),
+            (ctypes.c_int32 * max(1, len(sections)))(*sections), len(sections), strides, n, h, d, _dtype_code(x),
+            int(bool(split)), dx.data_ptr(), _ptr(dw), _ptr(ws), nbytes, _raw_stream(dev.index)),
+            "submconv_head_norm_rotary_backward")
+    return dx, dw
+
+
+class Route(NamedTuple):
+    """The plan of submconv_route for [N,E] scores and k experts a row."""
+    experts: torch.Tensor  # int32 [N,k], best first; -1 where fewer than k are open
+    gates: torch.Tensor    # fp32 [N,k]; 0 beside a -1
+    offsets: torch.Tensor  # int32 [E+1]: the positions of each expert; from the last on, pairs without an expert
+    rows: torch.Tensor     # int32 [N*k]: the row of each position
+    slots: torch.Tensor    # int32 [N,k]: the position of each pair
+
+
+def submconv_route(logits: torch.Tensor, k: int, normalize: bool = True) -> Route:
+    """The k best experts of each row of scores [N,E], their gates, and the rows grouped by expert.
+
+    Equal scores go by number; -inf closes an expert to a row.  Gates are the softmax over the row's chosen
+    experts (normalize), or their share of the softmax over all.  The plan feeds submconv_grouped_linear
+    (offsets, rows) and submconv_combine (slots, gates); it is exact and formed on the device."""
+    dev = _strided(logits, "logits", 2).device
+    n, e = logits.shape
+    k = int(k)
+    m = max(k, 0)
+    experts = torch.empty((n, m), dtype=torch.int32, device=dev)
+    slots = torch.empty((n, m), dtype=torch.int32, device=dev)
+    rows = torch.empty(n * m, dtype=torch.int32, device=dev)
+    gates = torch.empty((n, m), dtype=torch.float32, device=dev)
+    offsets = torch.empty(e + 1, dtype=torch.int32, device=dev)
+    lib = _lib if _lib is not None else load_library()
+    nbytes = lib.submconv_route_workspace(n, e, k)
+    ws = _workspace(nbytes, dev)
+    with _on_device(dev):
+        _check(lib.submconv_route(
+            logits.data_ptr(), _row_stride(logits), n, e, k, _dtype_code(logits), int(bool(normalize)), experts.data_ptr(),
+            gates.data_ptr(), offsets.data_ptr(), rows.data_ptr(), slots.data_ptr(), _ptr(ws), nbytes, _raw_stream(dev.index)),
+            "submconv_route")
+    return Route(experts, gates, offsets, rows, slots)
+
+
+def submconv_route_backward(grad: torch.Tensor, logits: torch.Tensor, experts: torch.Tensor, gates: torch.Tensor,
+                            normalize: bool = True) -> torch.Tensor:
+    """Gradient of the scores [N,E] from the gradient of submconv_route's gates, fp32 [N,k] -> dlogits, of
+    logits' type.  experts and gates are the Route's, normalize as in its call."""
+    dev = _strided(logits, "logits", 2).device
+    n, e = logits.shape
+    k = gates.shape[1] if gates.dim() == 2 else 0
+    for name, t, kind in (("grad", grad, torch.float32), ("gates", gates, torch.float32), ("experts", experts, torch.int32)):
+        _same_device(t, name, kind, dev, (n, k))
+    out = torch.empty((n, e), dtype=logits.dtype, device=dev)
+    lib = _lib if _lib is not None else load_library()
+    with _on_device(dev):
+        _check(lib.submconv_route_backward(
+            grad.data_ptr(), logits.data_ptr(), _row_stride(logits), n, e, k, _dtype_code(logits), int(bool(normalize)),
+            experts.data_ptr(), gates.data_ptr(), out.data_ptr(), e, _raw_stream(dev.index)), "submconv_route_backward")
+    return out
+
+
+def _linear_args(x, weight, offsets, rows):
+    """Checks shared by both directions -> (device, positions, groups, cout)."""
+    dev = _strided(x, "x", 2).device
+    if weight.dim() != 3 or weight.shape[2] != x.shape[1]:
+        raise ValueError("weight must be [G,Cout,Cin] for x [N,Cin]")
+    _same_device(weight, "weight", x.dtype, dev, weight.shape)
+    groups, cout = weight.shape[:2]
+    _same_device(offsets, "offsets", torch.int32, dev, (groups + 1,))
+    if rows is not None:
+        if rows.dim() != 1:
+            raise ValueError("rows must be [P]")
+        _same_device(rows, "rows", torch.int32, dev, rows.shape)
+    return dev, x.shape[0] if rows is None else rows.shape[0], groups, cout
+
+
+def submconv_grouped_linear(x: torch.Tensor, weight: torch.Tensor, offsets: torch.Tensor, bias: Optional[torch.Tensor] = None,
+                            rows: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Matrix products of ragged groups of rows, each group with its own weight -> out [P,Cout]:
+    out[i] = weight[g] x[rows[i]] + bias[g] for the positions i of group g.
+
+    x [N,Cin] (rows may be strided), weight [G,Cout,Cin] of x's type, bias fp32 [G,Cout] or None, offsets int32
+    [G+1] on the device (submconv_route's, or batch_offsets), rows int32 [P]: the row of x of each position
+    (None: the position itself, P = N).  Positions outside every group get zeros.  Not recorded by
+    autograd: submconv_grouped_linear_backward gives the gradients."""
+    dev, many, groups, cout = _linear_args(x, weight, offsets, rows)
+    nx, cin = x.shape
+    _same_device(bias, "bias", torch.float32, dev, (groups, cout))
+    if out is None:
+        out = torch.empty((many, cout), dtype=x.dtype, device=dev)
+    elif tuple(_strided(out, "out", 2, dev, x.dtype).shape) != (many, cout):
+        raise ValueError("out must be [P,Cout]")
+    lib = _lib if _lib is not None else load_library()
+    with _on_device(dev):
+        _check(lib.submconv_grouped_linear(
+            x.data_ptr(), _row_stride(x), nx, _ptr(rows), weight.data_ptr(), _ptr(bias), offsets.data_ptr(), groups, many, cin,
+            cout, _dtype_code(x), out.data_ptr(), _row_stride(out), _raw_stream(dev.index)), "submconv_grouped_linear")
+    return out
+
+
+def submconv_grouped_linear_backward(grad: torch.Tensor, x: torch.Tensor, weight: torch.Tensor, offsets: torch.Tensor,
+                                     rows: Optional[torch.Tensor] = None, need_x: bool = True, need_weight: bool = True,
+                                     need_bias: bool = False):
+    """Gradients of submconv_grouped_linear from grad [P,Cout] -> (dx, dweight, dbias), None for what is not needed.
+
+    dx [P,Cin] is the gradient of the rows as they were taken: with `rows`, submconv_combine(dx, slots) sums it for
+    each row of x.  dweight has weight's type, dbias is fp32; need_bias takes need_weight.  Sums run in a
+    fixed order: equal calls give equal bits."""
+    dev, many, groups, cout = _linear_args(x, weight, offsets, rows)
+    nx, cin = x.shape
+    if tuple(_strided(grad, "grad", 2, dev, x.dtype).shape) != (many, cout):
+        raise ValueError("grad must be [P,Cout]")
+    if need_bias and not need_weight:
+        raise ValueError("need_bias takes need_weight")
+    dx = torch.empty((many, cin), dtype=x.dtype, device=dev) if need_x else None
+    dw = torch.empty_like(weight) if need_weight else None
+    db = torch.empty((groups, cout), dtype=torch.float32, device=dev) if need_bias else None
+    lib = _lib if _lib is not None else load_library()
+    nbytes = lib.submconv_grouped_linear_backward_workspace(groups, many, cin, cout, _dtype_code(x)) if need_weight else 0
+    ws = _workspace(nbytes, dev)
+    with _on_device(dev):
+        _check(lib.submconv_grouped_linear_backward(
+            grad.data_ptr(), _row_stride(grad), x.data_ptr(), _row_stride(x), nx, _ptr(rows), weight.data_ptr(), offsets.data_ptr(),
+            groups, many, cin, cout, _dtype_code(x), _ptr(dx), cin, _ptr(dw), _ptr(db), _ptr(ws), nbytes, _raw_stream(dev.index)),
+            "submconv_grouped_linear_backward")
+    return dx, dw, db
+
+
+def submconv_combine(y: torch.Tensor, slots: torch.Tensor, gates: Optional[torch.Tensor] = None,
+                     out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The sum of each row's expert results, out[i] = sum_j gates[i,j] y[slots[i,j]] -> out [N,C].
+
+    y [P,C] (rows may be strided), slots int32 [N,k] and gates fp32 [N,k] of a Route (gates None: 1, which makes it
+    the gradient of the gather by Route.rows).  Slots outside [0, P) add nothing.  Not recorded by
+    autograd: submconv_combine_backward gives the gradients."""
+    dev = _strided(y, "y", 2).device
+    np_, c = y.shape
+    if slots.dim() != 2:
+        raise ValueError("slots must be [N,k]")
+    n, k = slots.shape
+    _same_device(slots, "slots", torch.int32, dev, (n, k))
+    _same_device(gates, "gates", torch.float32, dev, (n, k))
+    if out is None:
+        out = torch.empty((n, c), dtype=y.dtype, device=dev)
+    elif tuple(_strided(out, "out", 2, dev, y.dtype).shape) != (n, c):
+        raise ValueError("out must be [N,C]")
+    lib = _lib if _lib is not None else load_library()
+    with _on_device(dev):
+        _check(lib.submconv_combine(y.data_ptr(), _row_stride(y), np_, slots.data_ptr(), _ptr(gates), n, k, c, _dtype_code(y),
+                                    out.data_ptr(), _row_stride(out), _raw_stream(dev.index)), "submconv_combine")
+    return out
+
+
+def submconv_combine_backward(grad: torch.Tensor, y: torch.Tensor, slots: torch.Tensor, rows: torch.Tensor,
+                              gates: Optional[torch.Tensor] = None, need_y: bool = True):
+    """Gradients of submconv_combine from grad [N,C] -> (dy, dgates): dy[slots[i,j]] = gates[i,j] grad[i],
+    dgates[i,j] = grad[i] . y[slots[i,j]] (None without gates).
+
+    rows int32 [P] is the Route's: position p of dy belongs to row rows[p], and gets zeros if that row does not
+    name it among its slots."""
+    dev = _strided(y, "y", 2).device
+    np_, c = y.shape
+    if slots.dim() != 2:
+        raise ValueError("slots must be [N,k]")
+    n, k = slots.shape
+    _same_device(slots, "slots", torch.int32, dev, (n, k))
+    _same_device(rows, "rows", torch.int32, dev, (np_,))
+    _same_device(gates, "gates", torch.float32, dev, (n, k))
+    if tuple(_strided(grad, "grad", 2, dev, y.dtype).shape) != (n, c):
+        raise ValueError("grad must be [N,C]")
+    dy = torch.empty((np_, c), dtype=y.dtype, device=dev) if need_y else None
+    dgates = torch.empty((n, k), dtype=torch.float32, device=dev) if gates is not None else None
+    lib = _lib if _lib is not None else load_library()
+    with _on_device(dev):
+        _check(lib.submconv_combine_backward(
+            grad.data_ptr(), _row_stride(grad), y.data_ptr(), _row_stride(y), np_, slots.data_ptr(), rows.data_ptr(), _ptr(gates), n,
+            k, c, _dtype_code(y), _ptr(dy), c, _ptr(dgates), _raw_stream(dev.index)), "submconv_combine_backward")
+    return dy, dgates
 
 
 def release_cache(device: int = -1) -> None:

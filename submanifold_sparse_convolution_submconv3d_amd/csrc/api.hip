@@ -12,6 +12,8 @@
 
 #include "attention.h"
 #include "common.h"
+#include "headnorm.h"
+#include "linear.h"
 
 namespace sc {
 int build_map(const int32_t *coords, submconv_rulebook *rb, hipStream_t stream);
@@ -49,6 +51,17 @@ size_t attention_workspace(const AttnArgs &A, int dtype);
 int attention(const AttnArgs &A, int dtype, void *workspace, hipStream_t s);
 size_t attention_backward_workspace(const AttnArgs &A, int dtype);
 int attention_backward(AttnArgs A, int dtype, void *workspace, hipStream_t s);
+size_t route_workspace(int64_t n, int experts, int k);
+int route(const void *logits, int64_t ld, int64_t n, int experts, int k, int dtype, int normalize, int32_t *chosen,
+          float *gates, int32_t *offsets, int32_t *rows, int32_t *slots, void *workspace, hipStream_t s);
+int route_none(int32_t *offsets, int experts, hipStream_t s);
+int route_backward(const float *grad, const void *logits, int64_t ld, int64_t n, int experts, int k, int dtype,
+                   int normalize, const int32_t *chosen, const float *gates, void *out, int64_t out_ld, hipStream_t s);
+int combine(const void *y, int64_t ldy, int64_t np, const int32_t *slots, const float *gates, int64_t n, int k, int c,
+            int dtype, void *out, int64_t ldo, hipStream_t s);
+int combine_backward(const void *g, int64_t ldg, const void *y, int64_t ldy, int64_t np, const int32_t *slots,
+                     const int32_t *rows, const float *gates, int64_t n, int k, int c, int dtype, void *dy,
+                     int64_t lddy, float *dgates, hipStream_t s);
 
 static thread_local char g_err[512];
 
@@ -994,6 +1007,356 @@ int submconv_attention_backward(const void *grad, const void *q, const void *k, 
     A.scale = scale;
     A.lse = const_cast<float *>(lse);
     return attention_backward(A, dtype, workspace, (hipStream_t)stream);
+}
+
+// Sizes, sections and positions of a call of the heads' norm (axes = 0: no rotation); *pairs is what turns.
+static int head_norm_check(int64_t n, int32_t heads, int32_t dim, int32_t dtype, int32_t param_dtype, const void *weight,
+                           int32_t weight_rows, int32_t q_heads, const int32_t *sections, int32_t axes, int32_t split,
+                           int64_t pos_row, int64_t *pairs)
+{
+    if (n < 0 || n >= MAX_ROWS) return fail(SUBMCONV_E_INVALID_ARG, "n = %lld outside [0, 2^31)", (long long)n);
+    if (!known_dtype(dtype) || !known_dtype(param_dtype)) return fail(SUBMCONV_E_UNSUPPORTED, "dtype %d, param_dtype %d", dtype, param_dtype);
+    if (dim < 2 || dim > 512 || dim % 2) return fail(SUBMCONV_E_UNSUPPORTED, "dim = %d is not an even number in 2..512", dim);
+    if (heads < 1 || heads > 1024) return fail(SUBMCONV_E_UNSUPPORTED, "heads = %d outside 1..1024", heads);
+    if (axes < 0 || axes > SUBMCONV_ROTARY_MAX_AXES)
+        return fail(SUBMCONV_E_UNSUPPORTED, "axes = %d outside 0..%d", axes, SUBMCONV_ROTARY_MAX_AXES);
+    if (split & ~1) return fail(SUBMCONV_E_INVALID_ARG, "split must be 0 or 1");
+    if (q_heads < 0 || q_heads > heads) return fail(SUBMCONV_E_INVALID_ARG, "q_heads = %d outside 0..%d", q_heads, heads);
+    if (q_heads ? weight_rows != 2 : (weight_rows != 1 && weight_rows != heads))
+        return fail(SUBMCONV_E_INVALID_ARG, "weight_rows = %d for %d heads, q_heads = %d", weight_rows, heads, q_heads);
+    if (!weight && (weight_rows != 1 || q_heads)) return fail(SUBMCONV_E_INVALID_ARG, "weight is NULL, weight_rows = %d, q_heads = %d", weight_rows, q_heads);
+    *pairs = 0;
+    if (axes && !sections) return fail(SUBMCONV_E_INVALID_ARG, "sections is NULL");
+    for (int a = 0; a < axes; ++a) {
+        if (sections[a] < 0) return fail(SUBMCONV_E_INVALID_ARG, "sections[%d] = %d", a, sections[a]);
+        *pairs += sections[a];
+    }
+    if (*pairs > dim / 2) return fail(SUBMCONV_E_INVALID_ARG, "sections hold %lld pairs, a head has %d", (long long)*pairs, dim / 2);
+    if (pos_row < 0 || pos_row > MAX_STRIDE) return fail(SUBMCONV_E_INVALID_ARG, "pos_row = %lld", (long long)pos_row);
+    return SUBMCONV_OK;
+}
+
+static HeadNormArgs head_norm_args(int64_t n, int32_t heads, int32_t dim, const void *weight, int32_t weight_rows, int32_t q_heads,
+                                   int32_t param_dtype, const int32_t *positions, int64_t pos_row, const float *freqs,
+                                   const int32_t *sections, int32_t axes)
+{
+    HeadNormArgs A = {};
+    A.n = n;
+    A.heads = heads;
+    A.dim = dim;
+    A.w = weight;
+    A.weight_rows = weight_rows;
+    A.q_heads = q_heads;
+    A.pdtype = param_dtype;
+    A.pos = positions;
+    A.pos_row = pos_row;
+    A.freqs = freqs;
+    A.ax = rotary_axes(sections, axes);
+    return A;
+}
+
+int submconv_head_norm_rotary(const void *x, int64_t x_row, int64_t x_head, const void *weight, int32_t weight_rows,
+                              int32_t q_heads, int32_t param_dtype, float eps, const int32_t *positions,
+                              int64_t pos_row, const float *freqs, const int32_t *sections, int32_t axes, int64_t n,
+                              int32_t heads, int32_t dim, int32_t dtype, int32_t split, void *out, int64_t out_row,
+                              int64_t out_head, float *rstd, void *stream)
+{
+    int64_t pairs;
+    SC_CHECK(head_norm_check(n, heads, dim, dtype, param_dtype, weight, weight_rows, q_heads, sections, axes, split, pos_row, &pairs));
+    if (!(eps >= 0.0f)) return fail(SUBMCONV_E_INVALID_ARG, "eps = %g", (double)eps);
+    SC_CHECK(heads_check("x", n, heads, dim, x_row, x_head, false));
+    SC_CHECK(heads_check("out", n, heads, dim, out_row, out_head, true));
+    if (n == 0) return SUBMCONV_OK;
+    if (!x || !out || (pairs && (!positions || !freqs))) return fail(SUBMCONV_E_INVALID_ARG, "NULL tensor pointer");
+    const size_t es = elem_size(dtype), ps = elem_size(param_dtype);
+    if (!aligned_to(x, es) || !aligned_to(out, es) || !aligned_to(weight, ps) || !aligned_to(positions, 4) || !aligned_to(freqs, 4) ||
+        !aligned_to(rstd, 4))
+        return fail(SUBMCONV_E_INVALID_ARG, "misaligned pointer");
+    const bool same = x == out && (n == 1 || x_row == out_row) && (heads == 1 || x_head == out_head);  // in place
+    const Range r[] = {range3("x", same ? nullptr : x, n, heads, dim, x_row, x_head, es, false),
+                       range3("out", out, n, heads, dim, out_row, out_head, es, true),
+                       range2("positions", pairs ? positions : nullptr, n, axes, pos_row, 4, false),
+                       range1("freqs", freqs, (size_t)pairs * 4, false),
+                       range1("weight", weight, (size_t)weight_rows * dim * ps, false),
+                       range1("rstd", rstd, (size_t)n * heads * 4, true)};
+    SC_CHECK(ranges_check(r, 6));
+    HeadNormArgs A = head_norm_args(n, heads, dim, weight, weight_rows, q_heads, param_dtype, positions, pos_row, freqs, sections, axes);
+    A.x = x;
+    A.x_row = x_row;
+    A.x_head = x_head;
+    A.out = out;
+    A.out_row = out_row;
+    A.out_head = out_head;
+    A.rstd = rstd;
+    A.eps = eps;
+    return head_norm(A, dtype, split, (hipStream_t)stream);
+}
+
+size_t submconv_head_norm_rotary_backward_workspace(int64_t n, int32_t heads, int32_t dim, int32_t dtype,
+                                                    int32_t weight_rows, int32_t q_heads)
+{
+    int64_t pairs;
+    const int some = 0;
+    if (head_norm_check(n, heads, dim, dtype, SUBMCONV_F32, &some, weight_rows, q_heads, nullptr, 0, 0, 0, &pairs) != SUBMCONV_OK) return 0;
+    return head_norm_bwd_workspace(n, heads, dim, dtype, weight_rows, q_heads);
+}
+
+int submconv_head_norm_rotary_backward(const void *grad, const void *x, const float *rstd, const void *weight,
+                                       int32_t weight_rows, int32_t q_heads, int32_t param_dtype,
+                                       const int32_t *positions, int64_t pos_row, const float *freqs,
+                                       const int32_t *sections, int32_t axes, const int64_t *strides, int64_t n,
+                                       int32_t heads, int32_t dim, int32_t dtype, int32_t split, void *dx,
+                                       void *dweight, void *workspace, size_t workspace_bytes, void *stream)
+{
+    int64_t pairs;
+    SC_CHECK(head_norm_check(n, heads, dim, dtype, param_dtype, weight, weight_rows, q_heads, sections, axes, split, pos_row, &pairs));
+    if (!strides) return fail(SUBMCONV_E_INVALID_ARG, "strides is NULL");
+    SC_CHECK(heads_check("grad", n, heads, dim, strides[0], strides[1], false));
+    SC_CHECK(heads_check("x", n, heads, dim, strides[2], strides[3], false));
+    SC_CHECK(heads_check("dx", n, heads, dim, strides[4], strides[5], true));
+    if (n && (!grad || !x || !rstd || !dx || (pairs && (!positions || !freqs)))) return fail(SUBMCONV_E_INVALID_ARG, "NULL tensor pointer");
+    const size_t es = elem_size(dtype), ps = elem_size(param_dtype), wb = (size_t)weight_rows * dim * ps;
+    if (!aligned_to(grad, es) || !aligned_to(x, es) || !aligned_to(dx, es) || !aligned_to(weight, ps) || !aligned_to(dweight, ps) ||
+        !aligned_to(positions, 4) || !aligned_to(freqs, 4) || !aligned_to(rstd, 4) || !aligned16(workspace))
+        return fail(SUBMCONV_E_INVALID_ARG, "misaligned pointer");
+    const size_t need = dweight ? head_norm_bwd_workspace(n, heads, dim, dtype, weight_rows, q_heads) : 0;
+    if (need && (!workspace || workspace_bytes < need))
+        return fail(SUBMCONV_E_INVALID_ARG, "workspace of %zu bytes, %zu needed", workspace ? workspace_bytes : 0, need);
+    const bool same = grad == dx && (n <= 1 || strides[0] == strides[4]) && (heads == 1 || strides[1] == strides[5]);  // in place
+    const Range r[] = {range3("grad", same ? nullptr : grad, n, heads, dim, strides[0], strides[1], es, false),
+                       range3("x", x, n, heads, dim, strides[2], strides[3], es, false),
+                       range3("dx", dx, n, heads, dim, strides[4], strides[5], es, true),
+                       range2("positions", pairs ? positions : nullptr, n, axes, pos_row, 4, false),
+                       range1("freqs", freqs, (size_t)pairs * 4, false), range1("weight", weight, wb, false),
+                       range1("rstd", rstd, (size_t)n * heads * 4, false), range1("dweight", dweight, wb, true),
+                       range1("workspace", workspace, need, true)};
+    SC_CHECK(ranges_check(r, 9));
+    HeadNormArgs A = head_norm_args(n, heads, dim, weight, weight_rows, q_heads, param_dtype, positions, pos_row, freqs, sections, axes);
+    A.g = grad;
+    A.g_row = strides[0];
+    A.g_head = strides[1];
+    A.x = x;
+    A.x_row = strides[2];
+    A.x_head = strides[3];
+    A.out = dx;
+    A.out_row = strides[4];
+    A.out_head = strides[5];
+    A.rstd = const_cast<float *>(rstd);
+    A.partial = (float *)workspace;
+    return head_norm_backward(A, dtype, split, dweight, (hipStream_t)stream);
+}
+
+static int route_check(int64_t n, int32_t experts, int32_t k, int32_t dtype, int32_t normalize, int64_t row)
+{
+    if (!known_dtype(dtype)) return fail(SUBMCONV_E_UNSUPPORTED, "dtype %d", dtype);
+    if (experts < 1 || experts > SUBMCONV_ROUTE_MAX_EXPERTS)
+        return fail(SUBMCONV_E_UNSUPPORTED, "experts = %d outside 1..%d", experts, SUBMCONV_ROUTE_MAX_EXPERTS);
+    if (k < 1 || k > SUBMCONV_ROUTE_MAX_K || k > experts)
+        return fail(SUBMCONV_E_UNSUPPORTED, "k = %d outside 1..%d, or more than %d experts", k, SUBMCONV_ROUTE_MAX_K, experts);
+    if (n < 0 || n >= MAX_ROWS / k) return fail(SUBMCONV_E_INVALID_ARG, "n = %lld: n k must stay in [0, 2^31)", (long long)n);
+    if (normalize & ~1) return fail(SUBMCONV_E_INVALID_ARG, "normalize must be 0 or 1");
+    return row_check("logits", row, 0);
+}
+
+size_t submconv_route_workspace(int64_t n, int32_t experts, int32_t k)
+{
+    return route_check(n, experts, k, SUBMCONV_F32, 0, 0) == SUBMCONV_OK ? route_workspace(n, experts, k) : 0;
+}
+
+int submconv_route(const void *logits, int64_t row, int64_t n, int32_t experts, int32_t k, int32_t dtype,
+                   int32_t normalize, int32_t *chosen, float *gates, int32_t *offsets, int32_t *rows, int32_t *slots,
+                   void *workspace, size_t workspace_bytes, void *stream)
+{
+    SC_CHECK(route_check(n, experts, k, dtype, normalize, row));
+    if (!offsets || (n && (!logits || !chosen || !gates || !rows || !slots))) return fail(SUBMCONV_E_INVALID_ARG, "NULL tensor pointer");
+    const size_t es = elem_size(dtype), need = route_workspace(n, experts, k), pb = (size_t)n * k * 4;
+    if (!aligned_to(logits, es) || !aligned_to(chosen, 4) || !aligned_to(gates, 4) || !aligned_to(offsets, 4) || !aligned_to(rows, 4) ||
+        !aligned_to(slots, 4) || !aligned16(workspace))
+        return fail(SUBMCONV_E_INVALID_ARG, "misaligned pointer");
+    if (need && (!workspace || workspace_bytes < need))
+        return fail(SUBMCONV_E_INVALID_ARG, "workspace of %zu bytes, %zu needed", workspace ? workspace_bytes : 0, need);
+    const Range r[] = {range2("logits", logits, n, experts, row, es, false), range1("chosen", chosen, pb, true),
+                       range1("gates", gates, pb, true), range1("offsets", offsets, ((size_t)experts + 1) * 4, true),
+                       range1("rows", rows, pb, true), range1("slots", slots, pb, true), range1("workspace", workspace, need, true)};
+    SC_CHECK(ranges_check(r, 7));
+    if (n == 0) return route_none(offsets, experts, (hipStream_t)stream);
+    return route(logits, row, n, experts, k, dtype, normalize, chosen, gates, offsets, rows, slots, workspace, (hipStream_t)stream);
+}
+
+int submconv_route_backward(const float *grad, const void *logits, int64_t row, int64_t n, int32_t experts, int32_t k,
+                            int32_t dtype, int32_t normalize, const int32_t *chosen, const float *gates, void *dlogits,
+                            int64_t out_row, void *stream)
+{
+    SC_CHECK(route_check(n, experts, k, dtype, normalize, row));
+    SC_CHECK(row_check("dlogits", out_row, experts));
+    if (n == 0) return SUBMCONV_OK;
+    if (!grad || !chosen || !gates || !dlogits || (!normalize && !logits)) return fail(SUBMCONV_E_INVALID_ARG, "NULL tensor pointer");
+    const size_t es = elem_size(dtype), pb = (size_t)n * k * 4;
+    if (!aligned_to(logits, es) || !aligned_to(dlogits, es) || !aligned_to(chosen, 4) || !aligned_to(gates, 4) || !aligned_to(grad, 4))
+        return fail(SUBMCONV_E_INVALID_ARG, "misaligned pointer");
+    const Range r[] = {range2("logits", logits, n, experts, row, es, false), range2("dlogits", dlogits, n, experts, out_row, es, true),
+                       range1("grad", grad, pb, false), range1("chosen", chosen, pb, false), range1("gates", gates, pb, false)};
+    SC_CHECK(ranges_check(r, 5));
+    return route_backward(grad, logits, row, n, experts, k, dtype, normalize, chosen, gates, dlogits, out_row, (hipStream_t)stream);
+}
+
+constexpr int64_t MAX_POSITIONS = MAX_ROWS - (1 << 16);  // a tile's row numbers stay below 2^31
+constexpr int MAX_WIDTH = 1 << 16, MAX_GROUPS = 1 << 16;
+
+static int linear_check(int32_t groups, int64_t n, int64_t nx, int32_t cin, int32_t cout, int32_t dtype, bool forward, bool dx, bool dw)
+{
+    if (!known_dtype(dtype)) return fail(SUBMCONV_E_UNSUPPORTED, "dtype %d", dtype);
+    if (n < 0 || n >= MAX_POSITIONS || nx < 0 || nx >= MAX_POSITIONS)
+        return fail(SUBMCONV_E_INVALID_ARG, "n = %lld or nx = %lld outside [0, 2^31 - 2^16)", (long long)n, (long long)nx);
+    if (cin < 1 || cin > MAX_WIDTH || cout < 1 || cout > MAX_WIDTH)
+        return fail(SUBMCONV_E_UNSUPPORTED, "cin = %d, cout = %d outside 1..%d", cin, cout, MAX_WIDTH);
+    if (groups < 1 || groups > MAX_GROUPS) return fail(SUBMCONV_E_INVALID_ARG, "groups = %d outside 1..%d", groups, MAX_GROUPS);
+    if ((int64_t)groups * cin * cout >= int64_t(1) << 40) return fail(SUBMCONV_E_UNSUPPORTED, "groups cin cout reaches 2^40");
+    for (int kind = LINEAR_Y; kind <= LINEAR_DW; ++kind)
+        if ((kind == LINEAR_Y ? forward : (kind == LINEAR_DX ? dx : dw)) && linear_blocks(n, groups, cin, cout, kind) >= 1 << 24)
+            return fail(SUBMCONV_E_UNSUPPORTED, "%lld tiles are more than one launch holds", (long long)linear_blocks(n, groups, cin, cout, kind));
+    return SUBMCONV_OK;
+}
+
+int submconv_grouped_linear(const void *x, int64_t x_row, int64_t nx, const int32_t *rows, const void *weight,
+                            const float *bias, const int32_t *offsets, int32_t groups, int64_t n, int32_t cin,
+                            int32_t cout, int32_t dtype, void *out, int64_t out_row, void *stream)
+{
+    SC_CHECK(linear_check(groups, n, nx, cin, cout, dtype, true, false, false));
+    SC_CHECK(row_check("x", x_row, 0));
+    SC_CHECK(row_check("out", out_row, cout));
+    if (n == 0) return SUBMCONV_OK;
+    if (!rows && nx != n) return fail(SUBMCONV_E_INVALID_ARG, "nx = %lld and n = %lld differ, rows is NULL", (long long)nx, (long long)n);
+    if ((nx && !x) || !weight || !offsets || !out) return fail(SUBMCONV_E_INVALID_ARG, "NULL tensor pointer");
+    const size_t es = elem_size(dtype), gc = (size_t)groups * cout;
+    if (!aligned_to(x, es) || !aligned_to(weight, es) || !aligned_to(out, es) || !aligned_to(rows, 4) || !aligned_to(bias, 4) || !aligned_to(offsets, 4))
+        return fail(SUBMCONV_E_INVALID_ARG, "misaligned pointer");
+    const Range r[] = {range2("x", x, nx, cin, x_row, es, false), range2("out", out, n, cout, out_row, es, true),
+                       range1("rows", rows, (size_t)n * 4, false), range1("weight", weight, gc * cin * es, false),
+                       range1("bias", bias, gc * 4, false), range1("offsets", offsets, ((size_t)groups + 1) * 4, false)};
+    SC_CHECK(ranges_check(r, 6));
+    LinearArgs A = {};
+    A.x = x;
+    A.x_row = x_row;
+    A.nx = (int32_t)nx;
+    A.rows = rows;
+    A.w = weight;
+    A.bias = bias;
+    A.off = offsets;
+    A.groups = groups;
+    A.n = (int32_t)n;
+    A.cin = cin;
+    A.cout = cout;
+    A.out = out;
+    A.out_row = out_row;
+    return grouped_linear(A, dtype, LINEAR_Y, (hipStream_t)stream);
+}
+
+size_t submconv_grouped_linear_backward_workspace(int32_t groups, int64_t n, int32_t cin, int32_t cout, int32_t dtype)
+{
+    return 0;
+}
+
+int submconv_grouped_linear_backward(const void *grad, int64_t grad_row, const void *x, int64_t x_row, int64_t nx,
+                                     const int32_t *rows, const void *weight, const int32_t *offsets, int32_t groups,
+                                     int64_t n, int32_t cin, int32_t cout, int32_t dtype, void *dx, int64_t dx_row,
+                                     void *dweight, float *dbias, void *workspace, size_t workspace_bytes,
+                                     void *stream)
+{
+    SC_CHECK(linear_check(groups, n, nx, cin, cout, dtype, false, dx != nullptr, dweight != nullptr));
+    SC_CHECK(row_check("grad", grad_row, 0));
+    SC_CHECK(row_check("x", x_row, 0));
+    SC_CHECK(row_check("dx", dx_row, cin));
+    if (!rows && dweight && n && nx != n) return fail(SUBMCONV_E_INVALID_ARG, "nx = %lld and n = %lld differ, rows is NULL", (long long)nx, (long long)n);
+    if (dbias && !dweight) return fail(SUBMCONV_E_INVALID_ARG, "dbias without dweight");
+    if (!dx && !dweight) return SUBMCONV_OK;
+    if ((n && !grad) || !offsets || (dx && !weight) || (dweight && n && nx && !x)) return fail(SUBMCONV_E_INVALID_ARG, "NULL tensor pointer");
+    const size_t es = elem_size(dtype), gc = (size_t)groups * cout;
+    if (!aligned_to(grad, es) || !aligned_to(x, es) || !aligned_to(weight, es) || !aligned_to(dx, es) || !aligned_to(dweight, es) ||
+        !aligned_to(dbias, 4) || !aligned_to(rows, 4) || !aligned_to(offsets, 4) || !aligned16(workspace))
+        return fail(SUBMCONV_E_INVALID_ARG, "misaligned pointer");
+    const size_t need = submconv_grouped_linear_backward_workspace(groups, n, cin, cout, dtype);
+    if (need && (!workspace || workspace_bytes < need))
+        return fail(SUBMCONV_E_INVALID_ARG, "workspace of %zu bytes, %zu needed", workspace ? workspace_bytes : 0, need);
+    const Range r[] = {range2("grad", grad, n, cout, grad_row, es, false), range2("x", dweight ? x : nullptr, nx, cin, x_row, es, false),
+                       range2("dx", dx, n, cin, dx_row, es, true), range1("rows", dweight ? rows : nullptr, (size_t)n * 4, false),
+                       range1("weight", dx ? weight : nullptr, gc * cin * es, false), range1("offsets", offsets, ((size_t)groups + 1) * 4, false),
+                       range1("dweight", dweight, gc * cin * es, true), range1("dbias", dbias, gc * 4, true),
+                       range1("workspace", workspace, need, true)};
+    SC_CHECK(ranges_check(r, 9));
+    LinearArgs A = {};
+    A.g = grad;
+    A.g_row = grad_row;
+    A.x = x;
+    A.x_row = x_row;
+    A.nx = (int32_t)nx;
+    A.rows = rows;
+    A.w = weight;
+    A.off = offsets;
+    A.groups = groups;
+    A.n = (int32_t)n;
+    A.cin = cin;
+    A.cout = cout;
+    if (dx && n) {
+        A.out = dx;
+        A.out_row = dx_row;
+        SC_CHECK(grouped_linear(A, dtype, LINEAR_DX, (hipStream_t)stream));
+    }
+    if (dweight) {
+        A.out = dweight;
+        A.db = dbias;
+        SC_CHECK(grouped_linear(A, dtype, LINEAR_DW, (hipStream_t)stream));
+    }
+    return SUBMCONV_OK;
+}
+
+static int combine_check(int64_t np, int64_t n, int32_t k, int32_t c, int32_t dtype)
+{
+    if (!known_dtype(dtype)) return fail(SUBMCONV_E_UNSUPPORTED, "dtype %d", dtype);
+    if (k < 1 || k > SUBMCONV_ROUTE_MAX_K) return fail(SUBMCONV_E_UNSUPPORTED, "k = %d outside 1..%d", k, SUBMCONV_ROUTE_MAX_K);
+    if (c < 1 || c > MAX_WIDTH) return fail(SUBMCONV_E_UNSUPPORTED, "c = %d outside 1..%d", c, MAX_WIDTH);
+    if (n < 0 || n >= MAX_ROWS || np < 0 || np >= MAX_ROWS)
+        return fail(SUBMCONV_E_INVALID_ARG, "n = %lld or np = %lld outside [0, 2^31)", (long long)n, (long long)np);
+    return SUBMCONV_OK;
+}
+
+int submconv_combine(const void *y, int64_t y_row, int64_t np, const int32_t *slots, const float *gates, int64_t n,
+                     int32_t k, int32_t c, int32_t dtype, void *out, int64_t out_row, void *stream)
+{
+    SC_CHECK(combine_check(np, n, k, c, dtype));
+    SC_CHECK(row_check("y", y_row, 0));
+    SC_CHECK(row_check("out", out_row, c));
+    if (n == 0) return SUBMCONV_OK;
+    if ((np && !y) || !slots || !out) return fail(SUBMCONV_E_INVALID_ARG, "NULL tensor pointer");
+    const size_t es = elem_size(dtype), pb = (size_t)n * k * 4;
+    if (!aligned_to(y, es) || !aligned_to(out, es) || !aligned_to(slots, 4) || !aligned_to(gates, 4))
+        return fail(SUBMCONV_E_INVALID_ARG, "misaligned pointer");
+    const Range r[] = {range2("y", y, np, c, y_row, es, false), range2("out", out, n, c, out_row, es, true),
+                       range1("slots", slots, pb, false), range1("gates", gates, pb, false)};
+    SC_CHECK(ranges_check(r, 4));
+    return combine(y, y_row, np, slots, gates, n, k, c, dtype, out, out_row, (hipStream_t)stream);
+}
+
+int submconv_combine_backward(const void *grad, int64_t grad_row, const void *y, int64_t y_row, int64_t np,
+                              const int32_t *slots, const int32_t *rows, const float *gates, int64_t n, int32_t k,
+                              int32_t c, int32_t dtype, void *dy, int64_t dy_row, float *dgates, void *stream)
+{
+    SC_CHECK(combine_check(np, n, k, c, dtype));
+    SC_CHECK(row_check("grad", grad_row, 0));
+    SC_CHECK(row_check("y", y_row, 0));
+    SC_CHECK(row_check("dy", dy_row, c));
+    if ((!dy || np == 0) && (!dgates || n == 0)) return SUBMCONV_OK;
+    if ((n && (!grad || !slots)) || (dy && np && !rows) || (dgates && np && !y)) return fail(SUBMCONV_E_INVALID_ARG, "NULL tensor pointer");
+    const size_t es = elem_size(dtype), pb = (size_t)n * k * 4;
+    if (!aligned_to(grad, es) || !aligned_to(y, es) || !aligned_to(dy, es) || !aligned_to(slots, 4) || !aligned_to(rows, 4) ||
+        !aligned_to(gates, 4) || !aligned_to(dgates, 4))
+        return fail(SUBMCONV_E_INVALID_ARG, "misaligned pointer");
+    const Range r[] = {range2("grad", grad, n, c, grad_row, es, false), range2("y", dgates ? y : nullptr, np, c, y_row, es, false),
+                       range2("dy", dy, np, c, dy_row, es, true), range1("slots", slots, pb, false),
+                       range1("rows", dy ? rows : nullptr, (size_t)np * 4, false), range1("gates", gates, pb, false),
+                       range1("dgates", dgates, pb, true)};
+    SC_CHECK(ranges_check(r, 7));
+    return combine_backward(grad, grad_row, y, y_row, np, slots, rows, gates, n, k, c, dtype, dy, dy_row, dgates, (hipStream_t)stream);
 }
 
 int submconv_release_cache(int32_t device)

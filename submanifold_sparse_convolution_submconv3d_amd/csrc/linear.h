@@ -1,0 +1,108 @@
+// Shared by the grouped matrix products (linear.hip): arguments, and which rows a block's tile is of.
+#pragma once
+
+#include "attention.h"
+
+namespace sc {
+
+struct LinearArgs {
+    const void *x, *w, *g;  // rows [nx, cin] at x_row, weights [groups, cout, cin], gradient [n, cout] at g_row
+    void *out;              // y [n, cout], dx [n, cin] (at out_row), or dw
+    const float *bias;      // [groups, cout], or null
+    float *db;              // [groups, cout], or null
+    const int32_t *off;     // [groups + 1]
+    const int32_t *rows;    // row of x of each position, or null for the position itself
+    int64_t x_row, g_row, out_row;
+    int32_t n, nx;
+    int groups, cin, cout;
+};
+
+// Positions [beg, end) of a part: part 0 lies before the first offset, part p of 1..groups is group
+// p - 1, part groups + 1 lies behind the last.  Each bound is the largest offset so far, clamped to
+// [0, n]: offsets that do not ascend leave groups empty, no position is in two parts and none in
+// no part.
+struct Part {
+    int index, beg, end;
+    uint32_t tile;  // of the part
+};
+
+__device__ __forceinline__ int lanes_prefix_max(int v)
+{
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+        const int y = __shfl_up(v, o, 64);
+        if ((int)lane_id() >= o && y > v) v = y;
+    }
+    return v;
+}
+
+// Bound of part index + lane among 64 parts: the end of each; `before`: the end of part index - 1.
+__device__ __forceinline__ int part_ends(const LinearArgs &A, int index, int before)
+{
+    const int p = index + (int)lane_id();
+    int o = p <= A.groups ? A.off[p] : (p == A.groups + 1 ? A.n : 0);
+    o = o < 0 ? 0 : (o > A.n ? A.n : o);
+    if (lane_id() == 0 && before > o) o = before;
+    return lanes_prefix_max(o);
+}
+
+// The part that tile number t is of, tiles of `size` positions counted part after part without
+// gaps.  False past the last.  The same in all lanes; a wave looks at 64 parts at a time.
+__device__ __forceinline__ bool find_tile(const LinearArgs &A, int size, uint32_t t, Part *part)
+{
+    int before = 0;
+    uint32_t tiles = 0;
+    for (int index = 0; index < A.groups + 2; index += 64) {
+        const int end = part_ends(A, index, before);
+        int beg = __shfl_up(end, 1, 64);
+        if (lane_id() == 0) beg = before;
+        const uint32_t own = ((uint32_t)(end - beg) + size - 1) / size;
+        uint32_t sum = own;
+#pragma unroll
+        for (int o = 1; o < 64; o <<= 1) {
+            const uint32_t y = __shfl_up(sum, o, 64);
+            if ((int)lane_id() >= o) sum += y;
+        }
+        const uint64_t past = __ballot(tiles + sum > t);
+        if (past) {
+            const int at = __builtin_ctzll(past);
+            part->index = index + at;
+            part->beg = __builtin_amdgcn_readlane(beg, at);
+            part->end = __builtin_amdgcn_readlane(end, at);
+            part->tile = t - (tiles + (uint32_t)__builtin_amdgcn_readlane((int)(sum - own), at));
+            return true;
+        }
+        tiles += (uint32_t)__builtin_amdgcn_readlane((int)sum, 63);
+        before = __builtin_amdgcn_readlane(end, 63);
+    }
+    return false;
+}
+
+// Positions of group `group`.
+__device__ __forceinline__ void group_bounds(const LinearArgs &A, int group, Part *part)
+{
+    int before = 0;
+    for (int index = 0;; index += 64) {
+        const int end = part_ends(A, index, before);
+        const int at = group + 1 - index;  // the part's lane
+        if (at < 64) {
+            part->index = group + 1;
+            part->end = __builtin_amdgcn_readlane(end, at);
+            part->beg = at ? __builtin_amdgcn_readlane(end, at - 1) : before;
+            part->tile = 0;
+            return;
+        }
+        before = __builtin_amdgcn_readlane(end, 63);
+    }
+}
+
+// Tiles of `size` positions in all parts, at most.
+static inline int64_t most_tiles(int64_t n, int groups, int size) { return n / size + groups + 2; }
+
+enum { LINEAR_Y, LINEAR_DX, LINEAR_DW };
+
+// Blocks of a call's largest launch; a launch holds 2^24 of them.
+int64_t linear_blocks(int64_t n, int groups, int cin, int cout, int kind);
+int grouped_linear(const LinearArgs &A, int dtype, int kind, hipStream_t st);
+
+}  // namespace sc

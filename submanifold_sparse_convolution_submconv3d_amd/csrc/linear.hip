@@ -1,0 +1,237 @@
+// Matrix products of ragged groups of rows, each with the weight of its group, and their gradients.
+// For position i of group g, r = rows[i]:
+//
+//   y[i] = W_g x[r] + b_g,   dx[i] = W_g^T grad[i],   dW_g = sum over i in g of grad[i] x[r]^T,   db_g = sum grad[i]
+//
+// All three are products D[m, n] = sum over k of A[m, k] B[n, k]:
+//
+//        m            n      k          A                      B
+//   y    positions    cout   cin        x, k next to each other    W_g, k next to each other
+//   dx   positions    cin    cout       grad, k next to each other W_g, k a row apart
+//   dW   cout         cin    positions  grad, k a row apart        x, k a row apart
+//
+// Sums are fp32; one rounding to the tensors' type at the end.  Every result element is summed by
+// one lane in a fixed order, so the same call gives the same bits.
+#include "linear.h"
+
+namespace sc {
+
+constexpr int LT = 128;            // rows of either side in a tile
+constexpr int LBYTES = 64 * LT;    // bytes of one side's tile for a step of 64 / sizeof(T) along k
+
+// One side's tile in LDS.  Along k (KS false): rows of 64 bytes, their 16-byte pieces permuted so
+// that 8 rows read at one piece fall on different banks.  Across k (KS true): 64 / sizeof(T)
+// rows of LT elements; bf16 pieces are permuted for the transposing read, as in attention's tiles.
+template <typename T, bool KS>
+__device__ __forceinline__ uint32_t tile_at(uint32_t row, uint32_t piece)
+{
+    if constexpr (!KS) return row * 64 + ((piece ^ ((row >> 1) & 3)) << 4);
+    else if constexpr (sizeof(T) == 2) return piece_at<256>(row, piece);
+    else return row * 512 + piece * 16;
+}
+
+// A lane's operand of a product of 32 rows from `block` on: its share of k step j (half of the tile's k).
+template <typename T, bool KS>
+__device__ __forceinline__ Raw16 tile_operand(uint32_t lds, int block, int j)
+{
+    const uint32_t l = lane_id(), a = l >> 5;
+    if constexpr (!KS) {
+        return lds_read16(lds + tile_at<T, KS>(block + (l & 31), 2 * j + a));
+    } else if constexpr (sizeof(T) == 2) {
+        // rows 16 j + 8 a + 4 h .. + 3 of k, transposed: lane t of 16 gets element t
+        const uint32_t g = (l >> 4) & 1, t = l & 15, k = 16 * j + 8 * a + t / 4, piece = block / 8 + g * 2 + (t & 3) / 2;
+        const u32x2 lo = lds_read_tr(lds + tile_at<T, KS>(k, piece) + (t & 1) * 8);
+        const u32x2 hi = lds_read_tr(lds + tile_at<T, KS>(k + 4, piece) + (t & 1) * 8);
+        return Raw16{lo[0], lo[1], hi[0], hi[1]};
+    } else {
+        Raw16 r;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            r[i] = *(const SC_LDS uint32_t *)(uintptr_t)(lds + (4 * (2 * j + a) + i) * 512 + (block + (l & 31)) * 4);
+        return r;
+    }
+}
+
+// Any widths, row distances and alignment: pieces of 16 bytes are loaded into registers with what
+// is missing at the ends of rows as zeros, written to LDS, and the next step's loads are in flight
+// meanwhile.  Four waves, each 64 x 64 of the tile.
+template <typename T, int KIND>
+__global__ __launch_bounds__(256) void k_linear(LinearArgs A)
+{
+    constexpr int V = VEC<T>, KT = 64 / (int)sizeof(T);
+    constexpr bool AKS = KIND == LINEAR_DW, BKS = KIND != LINEAR_Y;
+    __shared__ __attribute__((aligned(16))) char smem[4 * LBYTES];
+    const uint32_t lds = (uint32_t)(uintptr_t)(SC_LDS char *)smem;
+    const int wave = threadIdx.x >> 6;
+    Part part;
+    const int n_end = KIND == LINEAR_Y ? A.cout : A.cin;
+    const uint32_t n_tiles = (n_end + LT - 1) / LT, other = blockIdx.x / n_tiles;
+    int m0, m_end, n0 = (blockIdx.x - other * n_tiles) * LT, k_end;
+    if constexpr (KIND == LINEAR_DW) {
+        const uint32_t m_tiles = (A.cout + LT - 1) / LT, group = other / m_tiles;
+        group_bounds(A, group, &part);
+        m0 = (other - group * m_tiles) * LT;
+        m_end = A.cout;
+        k_end = part.end - part.beg;
+    } else {
+        if (!find_tile(A, LT, other, &part)) return;
+        m0 = part.beg + (int)part.tile * LT;
+        m_end = part.end;
+        k_end = KIND == LINEAR_Y ? A.cin : A.cout;
+    }
+    const bool real = part.index >= 1 && part.index <= A.groups;
+    const int group = real ? part.index - 1 : 0;
+    if (!real) k_end = 0;  // rows of no group become zeros
+    const T *w = (const T *)A.w + (int64_t)group * A.cout * A.cin;
+
+    // A thread's two pieces of each side's tile.
+    const T *a_row[2], *b_row[2];
+    int r_[2][2], c_[2][2];  // row and first element of a piece in the tile
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int at = i * 256 + threadIdx.x;
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            const bool ks = s ? BKS : AKS;
+            r_[s][i] = ks ? at / (LT / V) : at / 4;
+            c_[s][i] = (ks ? at % (LT / V) : at % 4) * V;
+        }
+        if constexpr (!AKS) {
+            const int p = m0 + r_[0][i];
+            a_row[i] = nullptr;
+            if (p < m_end) {
+                if constexpr (KIND == LINEAR_DX) {
+                    a_row[i] = (const T *)A.g + (int64_t)p * A.g_row;
+                } else {
+                    const int r = A.rows ? A.rows[p] : p;
+                    if (r >= 0 && r < A.nx) a_row[i] = (const T *)A.x + (int64_t)r * A.x_row;
+                }
+            }
+        }
+        if constexpr (!BKS) b_row[i] = n0 + r_[1][i] < n_end ? w + (int64_t)(n0 + r_[1][i]) * A.cin : nullptr;
+    }
+    const auto left = [](int have) { return have < 0 ? 0 : (have < V ? have : V); };
+    Raw16 av[2], bv[2];
+    const auto load = [&](int k0) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            av[i] = bv[i] = Raw16{0, 0, 0, 0};
+            if constexpr (!AKS) {
+                const int nv = left(k_end - k0 - c_[0][i]);
+                if (a_row[i] && nv) av[i] = load_raw(a_row[i] + k0 + c_[0][i], nv);
+            } else {
+                const int nv = left(m_end - m0 - c_[0][i]), k = k0 + r_[0][i];
+                if (k < k_end && nv) av[i] = load_raw((const T *)A.g + (int64_t)(part.beg + k) * A.g_row + m0 + c_[0][i], nv);
+            }
+            if constexpr (!BKS) {
+                const int nv = left(k_end - k0 - c_[1][i]);
+                if (b_row[i] && nv) bv[i] = load_raw(b_row[i] + k0 + c_[1][i], nv);
+            } else {
+                const int nv = left(n_end - n0 - c_[1][i]), k = k0 + r_[1][i];
+                if (k < k_end && nv) {
+                    if constexpr (KIND == LINEAR_DX) {
+                        bv[i] = load_raw(w + (int64_t)k * A.cin + n0 + c_[1][i], nv);
+                    } else {
+                        const int r = A.rows ? A.rows[part.beg + k] : part.beg + k;
+                        if (r >= 0 && r < A.nx) bv[i] = load_raw((const T *)A.x + (int64_t)r * A.x_row + n0 + c_[1][i], nv);
+                    }
+                }
+            }
+        }
+    };
+    f32x16 acc[2][2], sums[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) acc[i][0][e] = acc[i][1][e] = sums[i][e] = 0.0f;
+    const int wm = (wave & 1) * 64, wn = (wave >> 1) * 64;
+    const bool summing = KIND == LINEAR_DW && A.db && n0 == 0 && wn == 0;  // this wave sums its rows of grad too
+    load(0);
+    for (int k0 = 0, buf = 0; k0 < k_end; k0 += KT, buf ^= 2 * LBYTES) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            lds_write16(lds + buf + tile_at<T, AKS>(r_[0][i], c_[0][i] / V), av[i]);
+            lds_write16(lds + buf + LBYTES + tile_at<T, BKS>(r_[1][i], c_[1][i] / V), bv[i]);
+        }
+        __syncthreads();
+        if (k0 + KT < k_end) load(k0 + KT);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            Raw16 a[2], b[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                a[i] = tile_operand<T, AKS>(lds + buf, wm + 32 * i, j);
+                b[i] = tile_operand<T, BKS>(lds + buf + LBYTES, wn + 32 * i, j);
+            }
+#pragma unroll
+            for (int m = 0; m < 2; ++m)
+#pragma unroll
+                for (int n = 0; n < 2; ++n) acc[m][n] = mma_pieces<T>(b[n], a[m], acc[m][n]);
+            if (summing) {
+                const uint32_t one = sizeof(T) == 2 ? 0x3f803f80u : 0x3f800000u;
+                const Raw16 ones = {one, one, one, one};
+#pragma unroll
+                for (int m = 0; m < 2; ++m) sums[m] = mma_pieces<T>(ones, a[m], sums[m]);
+            }
+        }
+    }
+    // a lane has row l % 32 of each block, its elements in the registers
+    const int l = lane_id() & 31;
+    const int64_t ld = KIND == LINEAR_DW ? A.cin : A.out_row;
+    T *out = (T *)A.out + (KIND == LINEAR_DW ? (int64_t)group * A.cout * A.cin : 0);
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+        const int row = m0 + wm + 32 * m + l;
+        const bool valid = row < m_end;
+        if (summing && valid && lane_id() < 32) A.db[(int64_t)group * A.cout + row] = sums[m][0];
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {  // registers 8h .. 8h + 3 and 8h + 4 .. 8h + 7: 8 elements in a row after the halves' exchange
+                float v[8];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(acc[m][n][8 * h + i]), __float_as_uint(acc[m][n][8 * h + 4 + i]), false, false);
+                    v[i] = __uint_as_float(r[0]);
+                    v[4 + i] = __uint_as_float(r[1]);
+                }
+                const int e = n0 + wn + 32 * n + 16 * h + 8 * (int)(lane_id() >> 5);
+                if (!valid || e >= n_end) continue;
+                if (KIND == LINEAR_Y && A.bias && real) {
+                    const float *b = A.bias + (int64_t)group * A.cout + e;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        if (e + i < n_end) v[i] += b[i];
+                }
+                T *to = out + (int64_t)row * ld + e;
+                if constexpr (sizeof(T) == 2) {
+                    store_raw(to, repack(v, to), n_end - e < 8 ? n_end - e : 8);
+                } else {
+                    const float lo[4] = {v[0], v[1], v[2], v[3]}, hi[4] = {v[4], v[5], v[6], v[7]};
+                    store_raw(to, repack(lo, to), n_end - e < 4 ? n_end - e : 4);
+                    if (n_end - e > 4) store_raw(to + 4, repack(hi, to), n_end - e < 8 ? n_end - e - 4 : 4);
+                }
+            }
+    }
+}
+
+int64_t linear_blocks(int64_t n, int groups, int cin, int cout, int kind)
+{
+    const int64_t in = (cin + LT - 1) / LT, out = (cout + LT - 1) / LT;
+    return kind == LINEAR_DW ? in * out * groups : most_tiles(n, groups, LT) * (kind == LINEAR_Y ? out : in);
+}
+
+int grouped_linear(const LinearArgs &A, int dtype, int kind, hipStream_t st)
+{
+    const int64_t blocks = linear_blocks(A.n, A.groups, A.cin, A.cout, kind);
+    const dim3 grid((unsigned)blocks);
+#define GO(T, KIND) hipLaunchKernelGGL((k_linear<T, KIND>), grid, dim3(256), 0, st, A)
+#define BY_KIND(T) if (kind == LINEAR_Y) GO(T, LINEAR_Y); else if (kind == LINEAR_DX) GO(T, LINEAR_DX); else GO(T, LINEAR_DW)
+    if (dtype == SUBMCONV_F32) { BY_KIND(float); } else { BY_KIND(uint16_t); }
+#undef BY_KIND
+#undef GO
+    SC_LAUNCHED("grouped_linear");
+    return SUBMCONV_OK;
+}
+
+}  // namespace sc

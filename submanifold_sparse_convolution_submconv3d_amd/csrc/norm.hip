@@ -11,21 +11,6 @@
 
 namespace sc {
 
-// A parameter vector's element (fp32 or bf16) as fp32.
-__device__ __forceinline__ float param(const void *p, int dtype, int i)
-{
-    return dtype == SUBMCONV_F32 ? ((const float *)p)[i] : bf16_to_f32(((const uint16_t *)p)[i]);
-}
-
-__device__ __forceinline__ void set_param(void *p, int dtype, int i, float v)
-{
-    if (!p) return;
-    if (dtype == SUBMCONV_F32)
-        ((float *)p)[i] = v;
-    else
-        ((uint16_t *)p)[i] = f32_to_bf16(v);
-}
-
 // Sum of v over the TPR threads of a row.  TPR = 256: the whole block, through LDS;
 // `slot` alternates between the two halves of `part`, so one barrier a sum is enough.
 template <int TPR>

@@ -13,22 +13,9 @@
 // sines and cosines of its pairs once and applies them to several heads of the row, four
 // heads' loads in flight at a time.  400,311 x 24 x 128 bf16: 860 us, 5.7 TB/s (a plain
 // device copy reaches 4.8 to 4.9); 20,384 x 24 x 128 inside a packed projection: 46 us, 5.5 TB/s.
-#include "rowvec.h"
+#include "rotary.h"
 
 namespace sc {
-
-struct RotaryAxes {
-    int end[SUBMCONV_ROTARY_MAX_AXES];  // first pair past each axis' section
-};
-
-// cos and sin of position * freq.  The product and its reduction to one turn are in fp64
-// (a position of 2^31 still leaves 1e-7 of a turn), the rest in fp32.
-__device__ __forceinline__ void turn(int32_t position, float freq, bool inverse, float *c, float *s)
-{
-    const double rev = (double)position * (double)freq * 0.15915494309189533577;
-    sincospif((float)(2.0 * (rev - rint(rev))), s, c);
-    if (inverse) *s = -*s;
-}
 
 constexpr int64_t ROTARY_BLOCKS = 1 << 22;  // along x (a launch's axis holds 2^32 threads); the rest along y
 constexpr int ROTARY_HEADS = 4;  // heads a thread works on at a time, their loads issued together
@@ -59,10 +46,7 @@ __global__ __launch_bounds__(256) void k_rotary(const T *x, int64_t x_row, int64
         c[j] = 1.0f;
         s[j] = 0.0f;
         if (p < used) {
-            int a = 0;  // the sections past the last axis end where it does
-#pragma unroll
-            for (int k = 0; k < SUBMCONV_ROTARY_MAX_AXES - 1; ++k) a += p >= ax.end[k];
-            turn(pos[row * pos_row + a], freqs[p], inverse != 0, &c[j], &s[j]);
+            turn(pos[row * pos_row + rotary_axis(ax, p)], freqs[p], inverse != 0, &c[j], &s[j]);
         }
     }
     const T *xr = x + row * x_row + e;
@@ -111,8 +95,7 @@ int rotary(const void *x, int64_t x_row, int64_t x_head, const int32_t *pos, int
            const int32_t *sections, int axes, int64_t n, int heads, int dim, int dtype, int split, int inverse,
            void *out, int64_t out_row, int64_t out_head, hipStream_t st)
 {
-    RotaryAxes ax;
-    for (int a = 0, end = 0; a < SUBMCONV_ROTARY_MAX_AXES; ++a) ax.end[a] = end += a < axes ? sections[a] : 0;
+    const RotaryAxes ax = rotary_axes(sections, axes);
     const int v = dtype == SUBMCONV_F32 ? 4 : 8, span = split ? dim / 2 : dim, pieces = (span + v - 1) / v;
     // one thread to a piece and ROTARY_HEADS heads while a block holds them
     int hgroups = (heads + ROTARY_HEADS - 1) / ROTARY_HEADS;

@@ -51,6 +51,21 @@ __device__ __forceinline__ Raw16 repack(const float (&v)[8], const uint16_t *)
     return r;
 }
 
+// A parameter vector's element (fp32 or bf16) as fp32.
+__device__ __forceinline__ float param(const void *p, int dtype, int i)
+{
+    return dtype == SUBMCONV_F32 ? ((const float *)p)[i] : bf16_to_f32(((const uint16_t *)p)[i]);
+}
+
+__device__ __forceinline__ void set_param(void *p, int dtype, int i, float v)
+{
+    if (!p) return;
+    if (dtype == SUBMCONV_F32)
+        ((float *)p)[i] = v;
+    else
+        ((uint16_t *)p)[i] = f32_to_bf16(v);
+}
+
 // The first nv elements at p (nv <= VEC), the rest zero.
 __device__ __forceinline__ Raw16 load_raw(const float *p, int nv)
 {
