@@ -16,7 +16,7 @@ LIBDIR = os.path.join(HERE, "_lib")
 LIB = os.path.join(LIBDIR, "libsubmconv.so")
 INCLUDE = os.path.join(ROOT, "include")
 SOURCES = ["api.hip", "sort_scan.hip", "mapbuild.hip", "conv.hip", "conv_win.hip", "conv_big.hip", "helpers.hip", "weights.hip",
-           "norm.hip", "rotary.hip", "attention.hip", "attention_bwd.hip", "headnorm.hip", "route.hip", "linear.hip", "combine.hip"]
+           "norm.hip", "rotary.hip", "attention.hip", "attention_bwd.hip", "headnorm.hip", "route.hip", "linear.hip", "linear_big.hip", "combine.hip"]
 ARCH = "gfx950"
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

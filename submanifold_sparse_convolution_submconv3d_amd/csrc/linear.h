@@ -104,5 +104,6 @@ enum { LINEAR_Y, LINEAR_DX, LINEAR_DW };
 // Blocks of a call's largest launch; a launch holds 2^24 of them.
 int64_t linear_blocks(int64_t n, int groups, int cin, int cout, int kind);
 int grouped_linear(const LinearArgs &A, int dtype, int kind, hipStream_t st);
+int grouped_linear_big(const LinearArgs &A, int kind, hipStream_t st);
 
 }  // namespace sc

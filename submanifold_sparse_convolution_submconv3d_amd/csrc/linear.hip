@@ -221,8 +221,22 @@ int64_t linear_blocks(int64_t n, int groups, int cin, int cout, int kind)
     return kind == LINEAR_DW ? in * out * groups : most_tiles(n, groups, LT) * (kind == LINEAR_Y ? out : in);
 }
 
+// Whether the large tiles take a call: bf16, whole pieces of 16 bytes everywhere, and both sides long
+// enough.
+static bool takes_big(const LinearArgs &A, int dtype, int kind)
+{
+    if (dtype != SUBMCONV_BF16 || A.cin % 8 || A.cout % 8) return false;
+    const auto pieces = [](const void *p, int64_t row) { return ((uintptr_t)p & 15) == 0 && row % 8 == 0; };
+    if (kind != LINEAR_DX && !pieces(A.x, A.x_row)) return false;
+    if (kind != LINEAR_Y && !pieces(A.g, A.g_row)) return false;
+    if (kind != LINEAR_DW && !pieces(A.w, 0)) return false;
+    const int cols = kind == LINEAR_Y ? A.cout : A.cin;
+    return cols >= 192 && (kind == LINEAR_DW ? A.cout >= 192 : A.n / A.groups >= 128);
+}
+
 int grouped_linear(const LinearArgs &A, int dtype, int kind, hipStream_t st)
 {
+    if (takes_big(A, dtype, kind)) return grouped_linear_big(A, kind, st);
     const int64_t blocks = linear_blocks(A.n, A.groups, A.cin, A.cout, kind);
     const dim3 grid((unsigned)blocks);
 #define GO(T, KIND) hipLaunchKernelGGL((k_linear<T, KIND>), grid, dim3(256), 0, st, A)

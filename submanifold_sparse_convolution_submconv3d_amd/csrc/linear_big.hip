@@ -1,0 +1,461 @@
+// Grouped matrix products of bf16 rows in large tiles (see linear.hip for the products).
+//
+// Blocks stay on the card and walk tiles of BM x BN.  Both sides' tiles are copied straight into a
+// ring of four places in LDS, 32 of k a step and three steps ahead, and on into the next tile, so that a
+// tile's end costs the stores alone.  In a step, each wave multiplies 32x32 blocks on the matrix cores in
+// two halves of 16 of k; the operands of the next half are read from LDS meanwhile, those of the next
+// step's first half too (its copies have landed by this step's barrier), so one barrier a step
+// is enough and no product waits for it.
+#include "linear.h"
+
+namespace sc {
+
+__device__ __attribute__((aligned(16))) const uint32_t zero_piece[4] = {0, 0, 0, 0};
+
+// A tile of the result: rows m0 .. m_end of part, from column n0 on; k_end terms a sum.
+struct BigTile {
+    int m0, m_end, n0, k_end, group, beg;  // beg: first position of the group (LINEAR_DW)
+    bool real, any;
+};
+
+// The tiles of a call.  Up to 62 groups a lane keeps its part's end and tile numbers.
+template <int KIND, int BM, int BN>
+struct BigTiles {
+    const LinearArgs &A;
+    uint32_t m_total, n_tiles, total;
+    int end, beg;         // of the lane's part
+    uint32_t tiles_end;   // tiles of the parts up to the lane's
+    bool kept;
+
+    __device__ __forceinline__ explicit BigTiles(const LinearArgs &args) : A(args)
+    {
+        n_tiles = ((KIND == LINEAR_Y ? A.cout : A.cin) + BN - 1) / BN;
+        kept = A.groups + 2 <= 64;
+        if constexpr (KIND == LINEAR_DW) {
+            m_total = (uint32_t)A.groups * ((A.cout + BM - 1) / BM);
+            if (kept) part_of(0, 0);
+        } else {
+            m_total = 0;
+            int before = 0;
+            for (int index = 0; index < A.groups + 2; index += 64) {
+                part_of(index, before);
+                m_total += (uint32_t)__builtin_amdgcn_readlane((int)tiles_end, 63);
+                before = __builtin_amdgcn_readlane(end, 63);
+            }
+        }
+        total = m_total * n_tiles;
+    }
+    // The lane's part among 64 from `index` on.
+    __device__ __forceinline__ void part_of(int index, int before)
+    {
+        end = part_ends(A, index, before);
+        beg = __shfl_up(end, 1, 64);
+        if (lane_id() == 0) beg = before;
+        tiles_end = ((uint32_t)(end - beg) + BM - 1) / BM;
+#pragma unroll
+        for (int o = 1; o < 64; o <<= 1) {
+            const uint32_t y = __shfl_up(tiles_end, o, 64);
+            if ((int)lane_id() >= o) tiles_end += y;
+        }
+    }
+    // Tile number t.  Tiles of GROUP rows of tiles follow each other column by column: the blocks
+    // of an XCD, which work on neighbouring numbers, share few rows of either side.
+    static constexpr uint32_t GROUP = 8;
+    __device__ __forceinline__ BigTile at(uint32_t t)
+    {
+        BigTile b;
+        b.any = t < total;
+        b.m0 = b.m_end = b.n0 = b.k_end = b.group = b.beg = 0;
+        b.real = false;
+        if (!b.any) return b;
+        const uint32_t g = t / (GROUP * n_tiles), r = t - g * GROUP * n_tiles, rows = m_total - g * GROUP < GROUP ? m_total - g * GROUP : GROUP;
+        const uint32_t n = r / rows, m = g * GROUP + (r - n * rows);
+        b.n0 = n * BN;
+        if constexpr (KIND == LINEAR_DW) {
+            const uint32_t m_tiles = (A.cout + BM - 1) / BM, group = m / m_tiles;
+            b.m0 = (m - group * m_tiles) * BM;
+            b.m_end = A.cout;
+            b.group = group;
+            b.real = true;
+            if (kept) {
+                b.beg = __builtin_amdgcn_readlane(end, group);  // the end of the part before it
+                b.k_end = __builtin_amdgcn_readlane(end, group + 1) - b.beg;
+            } else {
+                Part p;
+                group_bounds(A, group, &p);
+                b.beg = p.beg;
+                b.k_end = p.end - p.beg;
+            }
+        } else {
+            int index = 0, before = 0;
+            uint32_t tiles = 0;
+            if (!kept)
+                for (;; index += 64) {
+                    part_of(index, before);
+                    const uint32_t last = (uint32_t)__builtin_amdgcn_readlane((int)tiles_end, 63);
+                    if (tiles + last > m) break;
+                    tiles += last;
+                    before = __builtin_amdgcn_readlane(end, 63);
+                }
+            const int at = __builtin_ctzll(__ballot(tiles + tiles_end > m));
+            const int pb = __builtin_amdgcn_readlane(beg, at), pe = __builtin_amdgcn_readlane(end, at);
+            const uint32_t first = at ? (uint32_t)__builtin_amdgcn_readlane((int)tiles_end, at ? at - 1 : 0) : 0;
+            const int part = index + at;
+            b.m0 = pb + (int)(m - tiles - first) * BM;
+            b.m_end = pe;
+            b.real = part >= 1 && part <= A.groups;
+            b.group = b.real ? part - 1 : 0;
+            b.k_end = b.real ? (KIND == LINEAR_Y ? A.cin : A.cout) : 0;  // rows of no group become zeros
+        }
+        return b;
+    }
+};
+
+constexpr int BIG_K = 32, BIG_RING = 4;
+constexpr int big_steps(int k) { return k > 0 ? (k + BIG_K - 1) / BIG_K : 1; }
+
+// WM x WN waves of MB x NB blocks of 32 x 32.
+// SUMS (LINEAR_DW): db too.
+template <int KIND, int WM, int WN, int MB, int NB, bool SUMS>
+__global__ __launch_bounds__(64 * WM * WN, 2) void k_linear_big(LinearArgs A)
+{
+    constexpr bool AKS = KIND == LINEAR_DW, BKS = KIND != LINEAR_Y;
+    constexpr int BM = 32 * MB * WM, BN = 32 * NB * WN, WAVES = WM * WN;
+    constexpr int ABYTES = BM * 64, BBYTES = BN * 64, STAGE = ABYTES + BBYTES;
+    constexpr int CA = ABYTES / 1024 / WAVES, CB = BBYTES / 1024 / WAVES;  // copies of a wave a step
+    static_assert(CA * 1024 * WAVES == ABYTES && CB * 1024 * WAVES == BBYTES, "whole copies");
+    __shared__ __attribute__((aligned(1024))) char smem[BIG_RING * STAGE];
+    const uint32_t lds = (uint32_t)(uintptr_t)(SC_LDS char *)smem;
+    const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = lane_id();
+
+    BigTiles<KIND, BM, BN> tiles(A);
+    // the 8 XCDs, to which blocks are dealt in turn, each take an eighth of the tiles
+    const uint32_t share = (tiles.total + 7) / 8, xcd = blockIdx.x % 8, stride = gridDim.x / 8;
+    const uint32_t last = share * (xcd + 1) < tiles.total ? share * (xcd + 1) : tiles.total;
+    uint32_t number = share * xcd + blockIdx.x / 8;
+    const auto tile_at = [&](uint32_t t) { return tiles.at(t < last ? t : tiles.total); };
+
+    // ---- copies: a lane's piece of each copy, and where it reads next ----
+    const char *pa[CA], *pb[CB];
+    uint32_t sa[CA], sb[CB];     // bytes to the next step (0: the piece is zeros throughout)
+    int row_a[CA], row_b[CB];    // the copy's row in the tile
+    int piece_a[CA], piece_b[CB];
+#pragma unroll
+    for (int i = 0; i < CA; ++i) {
+        constexpr uint32_t RB = AKS ? BM * 2 : 64;
+        const uint32_t in = (wave * CA + i) * 1024 + lane * 16;
+        row_a[i] = in / RB;
+        piece_a[i] = (in % RB / 16) ^ swizzle<RB>(row_a[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < CB; ++i) {
+        constexpr uint32_t RB = BKS ? BN * 2 : 64;
+        const uint32_t in = (wave * CB + i) * 1024 + lane * 16;
+        row_b[i] = in / RB;
+        piece_b[i] = (in % RB / 16) ^ swizzle<RB>(row_b[i]);
+    }
+    // Rows of x: of the next tile (LINEAR_Y), or of the next step and the one after (LINEAR_DW), so that
+    // a number is loaded long before the copies that need it.
+    int source[KIND == LINEAR_DX ? 1 : (KIND == LINEAR_Y ? CA : CB)], source2[KIND == LINEAR_DW ? CB : 1];
+    const auto x_rows_of_tile = [&](const BigTile &t) {
+        if constexpr (KIND == LINEAR_Y) {
+#pragma unroll
+            for (int i = 0; i < CA; ++i) {
+                const int p = t.m0 + row_a[i];
+                source[i] = p < t.m_end ? (A.rows ? A.rows[p] : p) : -1;
+            }
+        }
+    };
+    const auto x_rows_of_step = [&](const BigTile &t, int k0) {  // moves on by a step
+        if constexpr (KIND == LINEAR_DW) {
+#pragma unroll
+            for (int i = 0; i < CB; ++i) {
+                const int k = k0 + row_b[i];
+                source[i] = source2[i];
+                source2[i] = k < t.k_end ? (A.rows ? A.rows[t.beg + k] : t.beg + k) : -1;
+            }
+        }
+    };
+    const char *zeros = (const char *)zero_piece;
+    const auto column = [](int at, int width) { return at + 8 <= width ? at : width - 8; };  // columns past the end: any that exist
+    const auto aim = [&](const BigTile &t) {
+        const char *w = (const char *)A.w + (int64_t)t.group * A.cout * A.cin * 2;
+#pragma unroll
+        for (int i = 0; i < CA; ++i) {
+            if constexpr (KIND == LINEAR_Y) {
+                const bool there = source[i] >= 0 && source[i] < A.nx;
+                pa[i] = there ? (const char *)A.x + ((int64_t)source[i] * A.x_row + piece_a[i] * 8) * 2 : zeros;
+                sa[i] = there ? 64 : 0;
+            } else if constexpr (KIND == LINEAR_DX) {
+                const int p = t.m0 + row_a[i] < t.m_end ? t.m0 + row_a[i] : t.m_end - 1;
+                pa[i] = (const char *)A.g + ((int64_t)p * A.g_row + piece_a[i] * 8) * 2;
+                sa[i] = 64;
+            } else {
+                pa[i] = (const char *)A.g + ((int64_t)(t.beg + row_a[i]) * A.g_row + column(t.m0 + piece_a[i] * 8, A.cout)) * 2;
+                sa[i] = (uint32_t)(BIG_K * 2) * (uint32_t)A.g_row;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < CB; ++i) {
+            if constexpr (KIND == LINEAR_Y) {
+                const int n = t.n0 + row_b[i] < A.cout ? t.n0 + row_b[i] : A.cout - 1;
+                pb[i] = w + ((int64_t)n * A.cin + piece_b[i] * 8) * 2;
+                sb[i] = 64;
+            } else if constexpr (KIND == LINEAR_DX) {
+                pb[i] = w + ((int64_t)row_b[i] * A.cin + column(t.n0 + piece_b[i] * 8, A.cin)) * 2;
+                sb[i] = (uint32_t)(BIG_K * 2) * (uint32_t)A.cin;
+            } else {
+                pb[i] = (const char *)A.x + column(t.n0 + piece_b[i] * 8, A.cin) * 2;
+                sb[i] = 0;  // the row is added step by step
+            }
+        }
+    };
+
+    BigTile now = tile_at(number);
+    if (!now.any) return;
+    uint32_t now_number = number;
+    BigTile ahead = now, after;  // what is copied, and the tile after that
+    int k_copy = 0, k_rows = 0;
+    x_rows_of_tile(ahead);
+    aim(ahead);
+    number += stride;
+    after = tile_at(number);
+    x_rows_of_tile(after);
+    // LINEAR_DW: the steps whose rows are looked up run two ahead of the copies, into the next tile too
+    BigTile looked = ahead;
+    uint32_t looked_number = now_number;
+    const auto look_ahead = [&]() {
+        if constexpr (KIND == LINEAR_DW) {
+            x_rows_of_step(looked, k_rows);
+            k_rows += BIG_K;
+            if (k_rows >= looked.k_end) {
+                looked_number += stride;
+                const BigTile t = tile_at(looked_number);
+                if (t.any) {
+                    looked = t;
+                    k_rows = 0;
+                }
+            }
+        }
+    };
+    look_ahead();
+    look_ahead();
+
+    uint32_t fill = 0;  // offset of the ring's place that is filled next
+    const auto copy_step = [&]() {
+        const bool whole = k_copy + BIG_K <= ahead.k_end;
+        const uint32_t to = __builtin_amdgcn_readfirstlane(lds + fill + wave * (CA * 1024));
+        const uint32_t tb = __builtin_amdgcn_readfirstlane(lds + fill + ABYTES + wave * (CB * 1024));
+#pragma unroll
+        for (int i = 0; i < CA; ++i) {
+            const char *from = pa[i];
+            if (!whole && k_copy + (AKS ? row_a[i] : piece_a[i] * 8) >= ahead.k_end) from = zeros;
+            __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)from, (SC_LDS void *)(uintptr_t)(to + i * 1024), 16, 0, 0);
+            pa[i] += sa[i];
+        }
+#pragma unroll
+        for (int i = 0; i < CB; ++i) {
+            const char *from = pb[i];
+            if constexpr (KIND == LINEAR_DW) {
+                from = source[i] >= 0 && source[i] < A.nx ? pb[i] + (int64_t)source[i] * A.x_row * 2 : zeros;
+            } else {
+                if (!whole && k_copy + (BKS ? row_b[i] : piece_b[i] * 8) >= ahead.k_end) from = zeros;
+            }
+            __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)from, (SC_LDS void *)(uintptr_t)(tb + i * 1024), 16, 0, 0);
+            pb[i] += sb[i];
+        }
+        fill = fill == (BIG_RING - 1) * STAGE ? 0 : fill + STAGE;
+        k_copy += BIG_K;
+        look_ahead();
+        if (k_copy >= ahead.k_end && after.any) {  // on to the next tile (past the last one zeros are copied)
+            ahead = after;
+            k_copy = 0;
+            aim(ahead);
+            number += stride;
+            after = tile_at(number);
+            x_rows_of_tile(after);
+        }
+    };
+
+    // ---- operands ----
+    const uint32_t wm = (wave % WM) * (32 * MB), wn = (wave / WM) * (32 * NB);
+    struct Operand {  // k next to each other: two addresses; a row apart: two for each block
+        uint32_t at[8];
+    } oa, ob;
+    const auto make = [&](Operand &o, bool ks, uint32_t rb, uint32_t base, uint32_t first, int blocks) {
+        const uint32_t a = lane >> 5, g = (lane >> 4) & 1, t = lane & 15;
+        if (!ks) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j) o.at[j] = base + piece_at<64>(first + (lane & 31), 2 * j + a);
+        } else {
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    if (i >= blocks) continue;
+                    const uint32_t k = 8 * a + 4 * h + t / 4, piece = first / 8 + 4 * i + g * 2 + (t & 3) / 2;
+                    o.at[4 * h + i] = base + (rb == 512 ? piece_at<512>(k, piece) : piece_at<256>(k, piece)) + (t & 1) * 8;
+                }
+        }
+    };
+    make(oa, AKS, BM * 2, lds, wm, MB);
+    make(ob, BKS, BN * 2, lds + ABYTES, wn, NB);
+    uint32_t place = 0;  // offset of the ring's place that is worked on
+    const auto read_a = [&](uint32_t from, int j, int i) {
+        if constexpr (!AKS) return lds_read16(oa.at[j] + from + i * 2048);
+        const u32x2 lo = lds_read_tr(oa.at[i] + from + j * (16 * BM * 2)), hi = lds_read_tr(oa.at[4 + i] + from + j * (16 * BM * 2));
+        return Raw16{lo[0], lo[1], hi[0], hi[1]};
+    };
+    const auto read_b = [&](uint32_t from, int j, int i) {
+        if constexpr (!BKS) return lds_read16(ob.at[j] + from + i * 2048);
+        const u32x2 lo = lds_read_tr(ob.at[i] + from + j * (16 * BN * 2)), hi = lds_read_tr(ob.at[4 + i] + from + j * (16 * BN * 2));
+        return Raw16{lo[0], lo[1], hi[0], hi[1]};
+    };
+
+    f32x16 acc[MB][NB];
+    Raw16 fa[2][MB], fb[2][NB];
+    // db: the WN waves that share rows of grad take one of their MB blocks each, read once more
+    static_assert(!SUMS || MB == WN, "a block for each wave");
+    float sum = 0.0f;
+    Operand os;
+    if constexpr (SUMS) make(os, AKS, BM * 2, lds, wm + 32 * (wave / WM), 1);
+    const auto clear = [&]() {
+#pragma unroll
+        for (int m = 0; m < MB; ++m)
+#pragma unroll
+            for (int n = 0; n < NB; ++n)
+#pragma unroll
+                for (int e = 0; e < 16; ++e) acc[m][n][e] = 0.0f;
+        sum = 0.0f;
+    };
+    const auto half = [&](int j) {  // products of half j, while the next half's operands are read
+        const uint32_t next = place == (BIG_RING - 1) * STAGE ? 0 : place + STAGE, from = j ? next : place;
+#pragma unroll
+        for (int i = 0; i < NB; ++i) fb[j ^ 1][i] = read_b(from, j ^ 1, i);
+#pragma unroll
+        for (int i = 0; i < MB; ++i) fa[j ^ 1][i] = read_a(from, j ^ 1, i);
+#pragma unroll
+        for (int m = 0; m < MB; ++m)
+#pragma unroll
+            for (int n = 0; n < NB; ++n) acc[m][n] = mma_pieces<uint16_t>(fb[j][n], fa[j][m], acc[m][n]);
+        // a product first: what it waits for was read during the last half; the reads between the next products
+        constexpr int READS = NB * (BKS ? 2 : 1) + MB * (AKS ? 2 : 1);
+#pragma unroll
+        for (int i = 0; i < 3; ++i) {
+            __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
+            __builtin_amdgcn_sched_group_barrier(0x100, (READS + 2) / 3, 0);
+        }
+        __builtin_amdgcn_sched_group_barrier(0x8, MB * NB - 3, 0);
+        if constexpr (SUMS) {
+            const u32x2 lo = lds_read_tr(os.at[0] + place + j * (16 * BM * 2)), hi = lds_read_tr(os.at[4] + place + j * (16 * BM * 2));
+            float v[8];
+            unpack(Raw16{lo[0], lo[1], hi[0], hi[1]}, v, (const uint16_t *)nullptr);
+            sum += ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
+        }
+    };
+
+    copy_step();
+    copy_step();
+    copy_step();
+    clear();
+    wait_copies_and_barrier<2 * (CA + CB)>();
+#pragma unroll
+    for (int i = 0; i < MB; ++i) fa[0][i] = read_a(0, 0, i);
+#pragma unroll
+    for (int i = 0; i < NB; ++i) fb[0][i] = read_b(0, 0, i);
+    constexpr int STORES = MB * NB * 2;
+    int stored = 0;  // steps that may still leave the last tile's stores in flight
+    for (;;) {
+        float bias = 0.0f;  // of column lane of the wave's
+        static_assert(NB <= 2, "a column a lane");
+        if (KIND == LINEAR_Y && A.bias && now.real) {
+            const int e = now.n0 + (int)wn + (int)(NB == 2 ? lane : lane % 32);
+            bias = A.bias[(int64_t)now.group * A.cout + (e < A.cout ? e : A.cout - 1)];
+        }
+        int k = 0;
+        do {
+            // The next step's copies have landed.  Loads and stores count in the order of issue: those
+            // issued later are the copies of the step after it, and at a tile's start the
+            // last one's stores (unless some were left out at an edge).
+            if (stored > 0) asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(CA + CB + STORES) : "memory");
+            else asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(CA + CB) : "memory");
+            --stored;
+            copy_step();
+            half(0);
+            half(1);
+            place = place == (BIG_RING - 1) * STAGE ? 0 : place + STAGE;
+            k += BIG_K;
+        } while (k < now.k_end);
+        // a lane has row l % 32 of each block, its elements in the registers
+        const int l = lane & 31, a = lane >> 5;
+        const int64_t ld = KIND == LINEAR_DW ? A.cin : A.out_row;
+        const int n_end = KIND == LINEAR_Y ? A.cout : A.cin;
+        uint16_t *out = (uint16_t *)A.out + (KIND == LINEAR_DW ? (int64_t)now.group * A.cout * A.cin : 0);
+        if constexpr (SUMS) {
+            sum += other_half(sum);
+            const int row = now.m0 + (int)wm + 32 * (int)(wave / WM) + l;
+            if (now.n0 == 0 && a == 0 && row < now.m_end) A.db[(int64_t)now.group * A.cout + row] = sum;
+        }
+        const bool whole = now.m0 + BM <= now.m_end && now.n0 + BN <= n_end;
+        const auto piece = [&](int m, int n, int h, float (&v)[8]) {  // 8 elements in a row after the halves' exchange
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(acc[m][n][8 * h + i]), __float_as_uint(acc[m][n][8 * h + 4 + i]), false, false);
+                v[i] = __uint_as_float(r[0]);
+                v[4 + i] = __uint_as_float(r[1]);
+            }
+        };
+#pragma unroll
+        for (int n = 0; n < NB; ++n)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                float b[8], v[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) b[i] = KIND == LINEAR_Y ? __shfl(bias, 32 * n + 16 * h + 8 * a + i, 64) : 0.0f;
+                const int e = now.n0 + (int)wn + 32 * n + 16 * h + 8 * a;
+                uint16_t *to = out + (int64_t)(now.m0 + (int)wm + l) * ld + e;
+                if (whole) {
+#pragma unroll
+                    for (int m = 0; m < MB; ++m) {
+                        piece(m, n, h, v);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) v[i] += b[i];
+                        *(Raw16Any *)(to + (int64_t)(32 * m) * ld) = repack(v, to);
+                    }
+                } else {
+#pragma unroll
+                    for (int m = 0; m < MB; ++m) {
+                        piece(m, n, h, v);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) v[i] += b[i];
+                        if (now.m0 + (int)wm + 32 * m + l < now.m_end && e < n_end)
+                            store_raw(to + (int64_t)(32 * m) * ld, repack(v, to), n_end - e < 8 ? n_end - e : 8);
+                    }
+                }
+            }
+        stored = whole ? 2 : 0;
+        now_number += stride;
+        now = tile_at(now_number);
+        if (!now.any) break;
+        clear();
+    }
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // no copy may land in LDS that the next block owns
+}
+
+// 256 x 256 in eight waves.
+int grouped_linear_big(const LinearArgs &A, int kind, hipStream_t st)
+{
+    constexpr int WM = 2, WN = 4, MB = 4, NB = 2, BM = 32 * WM * MB, BN = 32 * WN * NB;
+    const int64_t n_tiles = ((kind == LINEAR_Y ? A.cout : A.cin) + BN - 1) / BN;
+    const int64_t m_tiles = kind == LINEAR_DW ? (int64_t)A.groups * ((A.cout + BM - 1) / BM) : most_tiles(A.n, A.groups, BM);
+    const int64_t blocks = (n_tiles * m_tiles + 7) / 8 * 8;
+    const dim3 grid((unsigned)(blocks < UNITS ? blocks : UNITS)), block(64 * WM * WN);
+    if (kind == LINEAR_Y) hipLaunchKernelGGL((k_linear_big<LINEAR_Y, WM, WN, MB, NB, false>), grid, block, 0, st, A);
+    else if (kind == LINEAR_DX) hipLaunchKernelGGL((k_linear_big<LINEAR_DX, WM, WN, MB, NB, false>), grid, block, 0, st, A);
+    else if (A.db) hipLaunchKernelGGL((k_linear_big<LINEAR_DW, WM, WN, MB, NB, true>), grid, block, 0, st, A);
+    else hipLaunchKernelGGL((k_linear_big<LINEAR_DW, WM, WN, MB, NB, false>), grid, block, 0, st, A);
+    SC_LAUNCHED("grouped_linear");
+    return SUBMCONV_OK;
+}
+
+}  // namespace sc
