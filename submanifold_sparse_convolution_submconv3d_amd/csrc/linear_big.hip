@@ -1,11 +1,12 @@
 // Grouped matrix products of bf16 rows in large tiles (see linear.hip for the products).
 //
-// Blocks stay on the card and walk tiles of BM x BN.  Both sides' tiles are copied straight into a
-// ring of four places in LDS, 32 of k a step and three steps ahead, and on into the next tile, so that a
-// tile's end costs the stores alone.  In a step, each wave multiplies 32x32 blocks on the matrix cores in
-// two halves of 16 of k; the operands of the next half are read from LDS meanwhile, those of the next
-// step's first half too (its copies have landed by this step's barrier), so one barrier a step
-// is enough and no product waits for it.
+// Blocks stay on the card and walk tiles of BM x BN.  Both sides' tiles are copied straight into one of
+// two places in LDS, 64 of k a step (rows of 128 bytes: copies of 64-byte rows take 0.56 us for 32 KB
+// a compute unit, of 128-byte rows 0.34), and on into the next tile, so that a tile's end costs the stores
+// alone.  In a step, each wave multiplies 32x32 blocks on the matrix cores in four quarters of 16 of k; the
+// operands of the next quarter are read from LDS meanwhile.  Before the last quarter its operands are
+// in registers: after the step's one barrier there the next step's copies, which have landed, are read,
+// and the place that is done with is filled with the step after that.
 #include "linear.h"
 
 namespace sc {
@@ -111,8 +112,14 @@ struct BigTiles {
     }
 };
 
-constexpr int BIG_K = 32, BIG_RING = 4;
-constexpr int big_steps(int k) { return k > 0 ? (k + BIG_K - 1) / BIG_K : 1; }
+constexpr int BIG_K = 64;
+
+// A copy of 64 pieces of 16 bytes straight into LDS.  As an instruction of its own, since the compiler
+// lets every transposing read wait for all copies that it knows of; the waits are below.
+__device__ __forceinline__ void copy_pieces(const char *from, uint32_t lds)
+{
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(from), "s"(lds) : "memory", "m0");
+}
 
 // WM x WN waves of MB x NB blocks of 32 x 32.
 // SUMS (LINEAR_DW): db too.
@@ -121,10 +128,12 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_linear_big(LinearArgs A)
 {
     constexpr bool AKS = KIND == LINEAR_DW, BKS = KIND != LINEAR_Y;
     constexpr int BM = 32 * MB * WM, BN = 32 * NB * WN, WAVES = WM * WN;
-    constexpr int ABYTES = BM * 64, BBYTES = BN * 64, STAGE = ABYTES + BBYTES;
+    constexpr int ABYTES = BM * 2 * BIG_K, BBYTES = BN * 2 * BIG_K, STAGE = ABYTES + BBYTES;
+    constexpr uint32_t ARB = AKS ? BM * 2 : BIG_K * 2, BRB = BKS ? BN * 2 : BIG_K * 2;  // bytes of a row in LDS
     constexpr int CA = ABYTES / 1024 / WAVES, CB = BBYTES / 1024 / WAVES;  // copies of a wave a step
     static_assert(CA * 1024 * WAVES == ABYTES && CB * 1024 * WAVES == BBYTES, "whole copies");
-    __shared__ __attribute__((aligned(1024))) char smem[BIG_RING * STAGE];
+    static_assert((STAGE & (STAGE - 1)) == 0, "the two places' addresses differ in one bit");
+    __shared__ __attribute__((aligned(2 * STAGE))) char smem[2 * STAGE];
     const uint32_t lds = (uint32_t)(uintptr_t)(SC_LDS char *)smem;
     const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = lane_id();
 
@@ -135,48 +144,23 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_linear_big(LinearArgs A)
     uint32_t number = share * xcd + blockIdx.x / 8;
     const auto tile_at = [&](uint32_t t) { return tiles.at(t < last ? t : tiles.total); };
 
-    // ---- copies: a lane's piece of each copy, and where it reads next ----
+    // ---- copies: where a lane's piece of each copy is read next ----
     const char *pa[CA], *pb[CB];
-    uint32_t sa[CA], sb[CB];     // bytes to the next step (0: the piece is zeros throughout)
-    int row_a[CA], row_b[CB];    // the copy's row in the tile
-    int piece_a[CA], piece_b[CB];
-#pragma unroll
-    for (int i = 0; i < CA; ++i) {
-        constexpr uint32_t RB = AKS ? BM * 2 : 64;
-        const uint32_t in = (wave * CA + i) * 1024 + lane * 16;
-        row_a[i] = in / RB;
-        piece_a[i] = (in % RB / 16) ^ swizzle<RB>(row_a[i]);
-    }
-#pragma unroll
-    for (int i = 0; i < CB; ++i) {
-        constexpr uint32_t RB = BKS ? BN * 2 : 64;
-        const uint32_t in = (wave * CB + i) * 1024 + lane * 16;
-        row_b[i] = in / RB;
-        piece_b[i] = (in % RB / 16) ^ swizzle<RB>(row_b[i]);
-    }
-    // Rows of x: of the next tile (LINEAR_Y), or of the next step and the one after (LINEAR_DW), so that
-    // a number is loaded long before the copies that need it.
-    int source[KIND == LINEAR_DX ? 1 : (KIND == LINEAR_Y ? CA : CB)], source2[KIND == LINEAR_DW ? CB : 1];
-    const auto x_rows_of_tile = [&](const BigTile &t) {
+    const auto row_a = [&](int i) { return (int)(((wave * CA + i) * 1024 + lane * 16) / ARB); };  // the copy's row in the tile
+    const auto row_b = [&](int i) { return (int)(((wave * CB + i) * 1024 + lane * 16) / BRB); };
+    const auto piece_a = [&](int i) { return (int)((((wave * CA + i) * 1024 + lane * 16) % ARB / 16) ^ swizzle<ARB>(row_a(i))); };
+    const auto piece_b = [&](int i) { return (int)((((wave * CB + i) * 1024 + lane * 16) % BRB / 16) ^ swizzle<BRB>(row_b(i))); };
+    const char *zeros = (const char *)zero_piece;
+    int source[KIND == LINEAR_Y ? CA : 1];  // rows of x that the next tile takes
+    const auto x_rows = [&](const BigTile &t) {
         if constexpr (KIND == LINEAR_Y) {
 #pragma unroll
             for (int i = 0; i < CA; ++i) {
-                const int p = t.m0 + row_a[i];
+                const int p = t.m0 + row_a(i);
                 source[i] = p < t.m_end ? (A.rows ? A.rows[p] : p) : -1;
             }
         }
     };
-    const auto x_rows_of_step = [&](const BigTile &t, int k0) {  // moves on by a step
-        if constexpr (KIND == LINEAR_DW) {
-#pragma unroll
-            for (int i = 0; i < CB; ++i) {
-                const int k = k0 + row_b[i];
-                source[i] = source2[i];
-                source2[i] = k < t.k_end ? (A.rows ? A.rows[t.beg + k] : t.beg + k) : -1;
-            }
-        }
-    };
-    const char *zeros = (const char *)zero_piece;
     const auto column = [](int at, int width) { return at + 8 <= width ? at : width - 8; };  // columns past the end: any that exist
     const auto aim = [&](const BigTile &t) {
         const char *w = (const char *)A.w + (int64_t)t.group * A.cout * A.cin * 2;
@@ -184,29 +168,23 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_linear_big(LinearArgs A)
         for (int i = 0; i < CA; ++i) {
             if constexpr (KIND == LINEAR_Y) {
                 const bool there = source[i] >= 0 && source[i] < A.nx;
-                pa[i] = there ? (const char *)A.x + ((int64_t)source[i] * A.x_row + piece_a[i] * 8) * 2 : zeros;
-                sa[i] = there ? 64 : 0;
+                pa[i] = there ? (const char *)A.x + ((int64_t)source[i] * A.x_row + piece_a(i) * 8) * 2 : nullptr;
             } else if constexpr (KIND == LINEAR_DX) {
-                const int p = t.m0 + row_a[i] < t.m_end ? t.m0 + row_a[i] : t.m_end - 1;
-                pa[i] = (const char *)A.g + ((int64_t)p * A.g_row + piece_a[i] * 8) * 2;
-                sa[i] = 64;
+                const int p = t.m0 + row_a(i) < t.m_end ? t.m0 + row_a(i) : t.m_end - 1;
+                pa[i] = (const char *)A.g + ((int64_t)p * A.g_row + piece_a(i) * 8) * 2;
             } else {
-                pa[i] = (const char *)A.g + ((int64_t)(t.beg + row_a[i]) * A.g_row + column(t.m0 + piece_a[i] * 8, A.cout)) * 2;
-                sa[i] = (uint32_t)(BIG_K * 2) * (uint32_t)A.g_row;
+                pa[i] = (const char *)A.g + ((int64_t)(t.beg + row_a(i)) * A.g_row + column(t.m0 + piece_a(i) * 8, A.cout)) * 2;
             }
         }
 #pragma unroll
         for (int i = 0; i < CB; ++i) {
             if constexpr (KIND == LINEAR_Y) {
-                const int n = t.n0 + row_b[i] < A.cout ? t.n0 + row_b[i] : A.cout - 1;
-                pb[i] = w + ((int64_t)n * A.cin + piece_b[i] * 8) * 2;
-                sb[i] = 64;
+                const int n = t.n0 + row_b(i) < A.cout ? t.n0 + row_b(i) : A.cout - 1;
+                pb[i] = w + ((int64_t)n * A.cin + piece_b(i) * 8) * 2;
             } else if constexpr (KIND == LINEAR_DX) {
-                pb[i] = w + ((int64_t)row_b[i] * A.cin + column(t.n0 + piece_b[i] * 8, A.cin)) * 2;
-                sb[i] = (uint32_t)(BIG_K * 2) * (uint32_t)A.cin;
+                pb[i] = w + ((int64_t)row_b(i) * A.cin + column(t.n0 + piece_b(i) * 8, A.cin)) * 2;
             } else {
-                pb[i] = (const char *)A.x + column(t.n0 + piece_b[i] * 8, A.cin) * 2;
-                sb[i] = 0;  // the row is added step by step
+                pb[i] = (const char *)A.x + column(t.n0 + piece_b(i) * 8, A.cin) * 2;  // and the row, step by step
             }
         }
     };
@@ -215,78 +193,80 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_linear_big(LinearArgs A)
     if (!now.any) return;
     uint32_t now_number = number;
     BigTile ahead = now, after;  // what is copied, and the tile after that
-    int k_copy = 0, k_rows = 0;
-    x_rows_of_tile(ahead);
+    int k_copy = 0;
+    x_rows(ahead);
     aim(ahead);
     number += stride;
     after = tile_at(number);
-    x_rows_of_tile(after);
-    // LINEAR_DW: the steps whose rows are looked up run two ahead of the copies, into the next tile too
-    BigTile looked = ahead;
-    uint32_t looked_number = now_number;
-    const auto look_ahead = [&]() {
+    x_rows(after);
+
+    // LINEAR_DW: the rows of x of the step that is copied next.  A wave's copies take consecutive
+    // positions, so their rows' numbers are loaded once a wave, a step ahead.
+    constexpr int ROWS = KIND == LINEAR_DW ? (int)(CB * 1024 / BRB) : 1;
+    int step_rows[ROWS];
+    const auto look_up = [&]() {
         if constexpr (KIND == LINEAR_DW) {
-            x_rows_of_step(looked, k_rows);
-            k_rows += BIG_K;
-            if (k_rows >= looked.k_end) {
-                looked_number += stride;
-                const BigTile t = tile_at(looked_number);
-                if (t.any) {
-                    looked = t;
-                    k_rows = 0;
-                }
+#pragma unroll
+            for (int r = 0; r < ROWS; ++r) {
+                const int k = k_copy + (int)wave * ROWS + r, p = ahead.beg + k < A.n ? ahead.beg + k : A.n - 1;
+                step_rows[r] = k < ahead.k_end ? (A.rows ? ((const __attribute__((address_space(4))) int32_t *)(uintptr_t)A.rows)[p] : p) : -1;
             }
         }
     };
-    look_ahead();
-    look_ahead();
+    look_up();
 
-    uint32_t fill = 0;  // offset of the ring's place that is filled next
-    const auto copy_step = [&]() {
-        const bool whole = k_copy + BIG_K <= ahead.k_end;
-        const uint32_t to = __builtin_amdgcn_readfirstlane(lds + fill + wave * (CA * 1024));
-        const uint32_t tb = __builtin_amdgcn_readfirstlane(lds + fill + ABYTES + wave * (CB * 1024));
+    uint32_t fill = lds;  // the place that is filled next
+    const auto copy_a = [&](int i) {
+        const char *from = k_copy + (AKS ? row_a(i) : piece_a(i) * 8) < ahead.k_end ? pa[i] : zeros;
+        if constexpr (KIND == LINEAR_Y) from = pa[i] ? from : zeros;
+        copy_pieces(from, __builtin_amdgcn_readfirstlane(fill + (wave * CA + i) * 1024));
+    };
+    const auto copy_b = [&](int i) {
+        const char *from = k_copy + (BKS ? row_b(i) : piece_b(i) * 8) < ahead.k_end ? pb[i] : zeros;
+        if constexpr (KIND == LINEAR_DW) {
+            constexpr int PER = ROWS / CB;  // rows of a copy
+            int r = step_rows[i * PER];
+#pragma unroll
+            for (int q = 1; q < PER; ++q) r = (int)(lane * 16 / BRB) == q ? step_rows[i * PER + q] : r;
+            from = r >= 0 && r < A.nx ? pb[i] + (int64_t)r * A.x_row * 2 : zeros;
+        }
+        copy_pieces(from, __builtin_amdgcn_readfirstlane(fill + ABYTES + (wave * CB + i) * 1024));
+    };
+    const auto copied = [&]() {  // moves on by a step
+        const int64_t da = AKS ? (int64_t)BIG_K * A.g_row * 2 : BIG_K * 2, db = BKS ? (int64_t)BIG_K * A.cin * 2 : BIG_K * 2;
 #pragma unroll
         for (int i = 0; i < CA; ++i) {
-            const char *from = pa[i];
-            if (!whole && k_copy + (AKS ? row_a[i] : piece_a[i] * 8) >= ahead.k_end) from = zeros;
-            __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)from, (SC_LDS void *)(uintptr_t)(to + i * 1024), 16, 0, 0);
-            pa[i] += sa[i];
+            if constexpr (KIND == LINEAR_Y) pa[i] = pa[i] ? pa[i] + da : nullptr;
+            else pa[i] += da;
         }
+        if constexpr (KIND != LINEAR_DW) {
 #pragma unroll
-        for (int i = 0; i < CB; ++i) {
-            const char *from = pb[i];
-            if constexpr (KIND == LINEAR_DW) {
-                from = source[i] >= 0 && source[i] < A.nx ? pb[i] + (int64_t)source[i] * A.x_row * 2 : zeros;
-            } else {
-                if (!whole && k_copy + (BKS ? row_b[i] : piece_b[i] * 8) >= ahead.k_end) from = zeros;
-            }
-            __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)from, (SC_LDS void *)(uintptr_t)(tb + i * 1024), 16, 0, 0);
-            pb[i] += sb[i];
+            for (int i = 0; i < CB; ++i) pb[i] += db;
         }
-        fill = fill == (BIG_RING - 1) * STAGE ? 0 : fill + STAGE;
+        fill ^= STAGE;
         k_copy += BIG_K;
-        look_ahead();
-        if (k_copy >= ahead.k_end && after.any) {  // on to the next tile (past the last one zeros are copied)
+    };
+    const auto next_tile = [&]() {  // of the copies; past the last one zeros are copied
+        if (k_copy >= ahead.k_end && after.any) {
             ahead = after;
             k_copy = 0;
             aim(ahead);
             number += stride;
             after = tile_at(number);
-            x_rows_of_tile(after);
+            x_rows(after);
         }
+        look_up();
     };
 
     // ---- operands ----
     const uint32_t wm = (wave % WM) * (32 * MB), wn = (wave / WM) * (32 * NB);
-    struct Operand {  // k next to each other: two addresses; a row apart: two for each block
+    struct Operand {  // k next to each other: one address; a row apart: two for each block
         uint32_t at[8];
-    } oa, ob;
+    } oa, ob, os;
     const auto make = [&](Operand &o, bool ks, uint32_t rb, uint32_t base, uint32_t first, int blocks) {
         const uint32_t a = lane >> 5, g = (lane >> 4) & 1, t = lane & 15;
         if (!ks) {
-#pragma unroll
-            for (int j = 0; j < 2; ++j) o.at[j] = base + piece_at<64>(first + (lane & 31), 2 * j + a);
+            o.at[0] = base + piece_at<BIG_K * 2>(first + (lane & 31), a);
         } else {
 #pragma unroll
             for (int h = 0; h < 2; ++h)
@@ -298,27 +278,26 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_linear_big(LinearArgs A)
                 }
         }
     };
-    make(oa, AKS, BM * 2, lds, wm, MB);
-    make(ob, BKS, BN * 2, lds + ABYTES, wn, NB);
-    uint32_t place = 0;  // offset of the ring's place that is worked on
+    make(oa, AKS, ARB, lds, wm, MB);
+    make(ob, BKS, BRB, lds + ABYTES, wn, NB);
+    // db: the WN waves that share rows of grad take one of their MB blocks each, read once more
+    static_assert(!SUMS || MB == WN, "a block for each wave");
+    float sum = 0.0f;
+    if constexpr (SUMS) make(os, AKS, ARB, lds, wm + 32 * (wave / WM), 1);
+    // 16 of k: quarter j of the place at `from` (0 or STAGE)
     const auto read_a = [&](uint32_t from, int j, int i) {
-        if constexpr (!AKS) return lds_read16(oa.at[j] + from + i * 2048);
-        const u32x2 lo = lds_read_tr(oa.at[i] + from + j * (16 * BM * 2)), hi = lds_read_tr(oa.at[4 + i] + from + j * (16 * BM * 2));
+        if constexpr (!AKS) return lds_read16((oa.at[0] ^ (32 * j) ^ from) + i * (32 * ARB));
+        const u32x2 lo = lds_read_tr((oa.at[i] ^ from) + j * (16 * ARB)), hi = lds_read_tr((oa.at[4 + i] ^ from) + j * (16 * ARB));
         return Raw16{lo[0], lo[1], hi[0], hi[1]};
     };
     const auto read_b = [&](uint32_t from, int j, int i) {
-        if constexpr (!BKS) return lds_read16(ob.at[j] + from + i * 2048);
-        const u32x2 lo = lds_read_tr(ob.at[i] + from + j * (16 * BN * 2)), hi = lds_read_tr(ob.at[4 + i] + from + j * (16 * BN * 2));
+        if constexpr (!BKS) return lds_read16((ob.at[0] ^ (32 * j) ^ from) + i * (32 * BRB));
+        const u32x2 lo = lds_read_tr((ob.at[i] ^ from) + j * (16 * BRB)), hi = lds_read_tr((ob.at[4 + i] ^ from) + j * (16 * BRB));
         return Raw16{lo[0], lo[1], hi[0], hi[1]};
     };
 
     f32x16 acc[MB][NB];
     Raw16 fa[2][MB], fb[2][NB];
-    // db: the WN waves that share rows of grad take one of their MB blocks each, read once more
-    static_assert(!SUMS || MB == WN, "a block for each wave");
-    float sum = 0.0f;
-    Operand os;
-    if constexpr (SUMS) make(os, AKS, BM * 2, lds, wm + 32 * (wave / WM), 1);
     const auto clear = [&]() {
 #pragma unroll
         for (int m = 0; m < MB; ++m)
@@ -328,17 +307,19 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_linear_big(LinearArgs A)
                 for (int e = 0; e < 16; ++e) acc[m][n][e] = 0.0f;
         sum = 0.0f;
     };
-    const auto half = [&](int j) {  // products of half j, while the next half's operands are read
-        const uint32_t next = place == (BIG_RING - 1) * STAGE ? 0 : place + STAGE, from = j ? next : place;
+    uint32_t place = 0;
+    const auto quarter = [&](int j) {  // products of quarter j, while the next quarter's operands are read
+        const uint32_t from = j == 3 ? place ^ STAGE : place;
+        const int to = (j + 1) & 1, nj = (j + 1) & 3;
 #pragma unroll
-        for (int i = 0; i < NB; ++i) fb[j ^ 1][i] = read_b(from, j ^ 1, i);
+        for (int i = 0; i < NB; ++i) fb[to][i] = read_b(from, nj, i);
 #pragma unroll
-        for (int i = 0; i < MB; ++i) fa[j ^ 1][i] = read_a(from, j ^ 1, i);
+        for (int i = 0; i < MB; ++i) fa[to][i] = read_a(from, nj, i);
 #pragma unroll
         for (int m = 0; m < MB; ++m)
 #pragma unroll
-            for (int n = 0; n < NB; ++n) acc[m][n] = mma_pieces<uint16_t>(fb[j][n], fa[j][m], acc[m][n]);
-        // a product first: what it waits for was read during the last half; the reads between the next products
+            for (int n = 0; n < NB; ++n) acc[m][n] = mma_pieces<uint16_t>(fb[to ^ 1][n], fa[to ^ 1][m], acc[m][n]);
+        // a product first: what it waits for was read during the last quarter; the reads between the next products
         constexpr int READS = NB * (BKS ? 2 : 1) + MB * (AKS ? 2 : 1);
 #pragma unroll
         for (int i = 0; i < 3; ++i) {
@@ -346,25 +327,36 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_linear_big(LinearArgs A)
             __builtin_amdgcn_sched_group_barrier(0x100, (READS + 2) / 3, 0);
         }
         __builtin_amdgcn_sched_group_barrier(0x8, MB * NB - 3, 0);
-        if constexpr (SUMS) {
-            const u32x2 lo = lds_read_tr(os.at[0] + place + j * (16 * BM * 2)), hi = lds_read_tr(os.at[4] + place + j * (16 * BM * 2));
-            float v[8];
-            unpack(Raw16{lo[0], lo[1], hi[0], hi[1]}, v, (const uint16_t *)nullptr);
-            sum += ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
+        if constexpr (SUMS) {  // (the last quarter's with the one before it, while the place is still whole)
+#pragma unroll
+            for (int q = j; q < 4 && j < 3; q += j == 2 ? 1 : 4) {
+                const u32x2 lo = lds_read_tr((os.at[0] ^ place) + q * (16 * ARB)), hi = lds_read_tr((os.at[4] ^ place) + q * (16 * ARB));
+                float v[8];
+                unpack(Raw16{lo[0], lo[1], hi[0], hi[1]}, v, (const uint16_t *)nullptr);
+                sum += ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
+            }
         }
     };
 
-    copy_step();
-    copy_step();
-    copy_step();
+#pragma unroll
+    for (int i = 0; i < CA; ++i) copy_a(i);
+#pragma unroll
+    for (int i = 0; i < CB; ++i) copy_b(i);
+    copied();
+    next_tile();
+    wait_copies_and_barrier<0>();
+#pragma unroll
+    for (int i = 0; i < CA; ++i) copy_a(i);
+#pragma unroll
+    for (int i = 0; i < CB; ++i) copy_b(i);
+    copied();
     clear();
-    wait_copies_and_barrier<2 * (CA + CB)>();
 #pragma unroll
     for (int i = 0; i < MB; ++i) fa[0][i] = read_a(0, 0, i);
 #pragma unroll
     for (int i = 0; i < NB; ++i) fb[0][i] = read_b(0, 0, i);
     constexpr int STORES = MB * NB * 2;
-    int stored = 0;  // steps that may still leave the last tile's stores in flight
+    bool stored = false;  // the last tile's stores may still be in flight
     for (;;) {
         float bias = 0.0f;  // of column lane of the wave's
         static_assert(NB <= 2, "a column a lane");
@@ -374,16 +366,23 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_linear_big(LinearArgs A)
         }
         int k = 0;
         do {
-            // The next step's copies have landed.  Loads and stores count in the order of issue: those
-            // issued later are the copies of the step after it, and at a tile's start the
+            quarter(0);
+            quarter(1);
+            quarter(2);
+            next_tile();
+            // All of this step's operands are read and the next step's copies have landed.  Loads and
+            // stores count in the order of issue: those after the copies are, at a tile's start, the
             // last one's stores (unless some were left out at an edge).
-            if (stored > 0) asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(CA + CB + STORES) : "memory");
-            else asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(CA + CB) : "memory");
-            --stored;
-            copy_step();
-            half(0);
-            half(1);
-            place = place == (BIG_RING - 1) * STAGE ? 0 : place + STAGE;
+            if (stored) asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(STORES) : "memory");
+            else asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+            stored = false;
+#pragma unroll
+            for (int i = 0; i < CA; ++i) copy_a(i);
+#pragma unroll
+            for (int i = 0; i < CB; ++i) copy_b(i);
+            copied();
+            quarter(3);
+            place ^= STAGE;
             k += BIG_K;
         } while (k < now.k_end);
         // a lane has row l % 32 of each block, its elements in the registers
@@ -433,7 +432,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_linear_big(LinearArgs A)
                     }
                 }
             }
-        stored = whole ? 2 : 0;
+        stored = whole;
         now_number += stride;
         now = tile_at(now_number);
         if (!now.any) break;
