@@ -128,12 +128,13 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_linear_big(LinearArgs A)
 {
     constexpr bool AKS = KIND == LINEAR_DW, BKS = KIND != LINEAR_Y;
     constexpr int BM = 32 * MB * WM, BN = 32 * NB * WN, WAVES = WM * WN;
-    constexpr int ABYTES = BM * 2 * BIG_K, BBYTES = BN * 2 * BIG_K, STAGE = ABYTES + BBYTES;
+    constexpr int ABYTES = BM * 2 * BIG_K, BBYTES = BN * 2 * BIG_K;
     constexpr uint32_t ARB = AKS ? BM * 2 : BIG_K * 2, BRB = BKS ? BN * 2 : BIG_K * 2;  // bytes of a row in LDS
     constexpr int CA = ABYTES / 1024 / WAVES, CB = BBYTES / 1024 / WAVES;  // copies of a wave a step
     static_assert(CA * 1024 * WAVES == ABYTES && CB * 1024 * WAVES == BBYTES, "whole copies");
-    static_assert((STAGE & (STAGE - 1)) == 0, "the two places' addresses differ in one bit");
-    __shared__ __attribute__((aligned(2 * STAGE))) char smem[2 * STAGE];
+    static_assert(ABYTES == BBYTES, "one ring for both sides");
+    constexpr int RING = 5;
+    __shared__ __attribute__((aligned(1024))) char smem[RING * ABYTES];
     const uint32_t lds = (uint32_t)(uintptr_t)(SC_LDS char *)smem;
     const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = lane_id();
 
@@ -162,8 +163,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_linear_big(LinearArgs A)
         }
     };
     const auto column = [](int at, int width) { return at + 8 <= width ? at : width - 8; };  // columns past the end: any that exist
-    const auto aim = [&](const BigTile &t) {
-        const char *w = (const char *)A.w + (int64_t)t.group * A.cout * A.cin * 2;
+    const auto aim_a = [&](const BigTile &t) {
 #pragma unroll
         for (int i = 0; i < CA; ++i) {
             if constexpr (KIND == LINEAR_Y) {
@@ -176,6 +176,9 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_linear_big(LinearArgs A)
                 pa[i] = (const char *)A.g + ((int64_t)(t.beg + row_a(i)) * A.g_row + column(t.m0 + piece_a(i) * 8, A.cout)) * 2;
             }
         }
+    };
+    const auto aim_b = [&](const BigTile &t) {
+        const char *w = (const char *)A.w + (int64_t)t.group * A.cout * A.cin * 2;
 #pragma unroll
         for (int i = 0; i < CB; ++i) {
             if constexpr (KIND == LINEAR_Y) {
@@ -191,13 +194,14 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_linear_big(LinearArgs A)
 
     BigTile now = tile_at(number);
     if (!now.any) return;
-    uint32_t now_number = number;
-    BigTile ahead = now, after;  // what is copied, and the tile after that
-    int k_copy = 0;
-    x_rows(ahead);
-    aim(ahead);
-    number += stride;
-    after = tile_at(number);
+    // What is copied of each side, and from which k on; A's copies run a step ahead of B's.
+    BigTile ta = now, tb = now, after;
+    uint32_t now_number = number, b_number = number, a_number = number + stride;  // (of `after`)
+    int ka = 0, kb = 0;
+    x_rows(ta);
+    aim_a(ta);
+    aim_b(tb);
+    after = tile_at(a_number);
     x_rows(after);
 
     // LINEAR_DW: the rows of x of the step that is copied next.  A wave's copies take consecutive
@@ -208,21 +212,22 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_linear_big(LinearArgs A)
         if constexpr (KIND == LINEAR_DW) {
 #pragma unroll
             for (int r = 0; r < ROWS; ++r) {
-                const int k = k_copy + (int)wave * ROWS + r, p = ahead.beg + k < A.n ? ahead.beg + k : A.n - 1;
-                step_rows[r] = k < ahead.k_end ? (A.rows ? ((const __attribute__((address_space(4))) int32_t *)(uintptr_t)A.rows)[p] : p) : -1;
+                const int k = kb + (int)wave * ROWS + r, p = tb.beg + k < A.n ? tb.beg + k : A.n - 1;
+                step_rows[r] = k < tb.k_end ? (A.rows ? ((const __attribute__((address_space(4))) int32_t *)(uintptr_t)A.rows)[p] : p) : -1;
             }
         }
     };
     look_up();
 
     uint32_t fill = lds;  // the place that is filled next
+    const auto filled = [&]() { fill = fill == lds + (RING - 1) * ABYTES ? lds : fill + ABYTES; };
     const auto copy_a = [&](int i) {
-        const char *from = k_copy + (AKS ? row_a(i) : piece_a(i) * 8) < ahead.k_end ? pa[i] : zeros;
+        const char *from = ka + (AKS ? row_a(i) : piece_a(i) * 8) < ta.k_end ? pa[i] : zeros;
         if constexpr (KIND == LINEAR_Y) from = pa[i] ? from : zeros;
         copy_pieces(from, __builtin_amdgcn_readfirstlane(fill + (wave * CA + i) * 1024));
     };
     const auto copy_b = [&](int i) {
-        const char *from = k_copy + (BKS ? row_b(i) : piece_b(i) * 8) < ahead.k_end ? pb[i] : zeros;
+        const char *from = kb + (BKS ? row_b(i) : piece_b(i) * 8) < tb.k_end ? pb[i] : zeros;
         if constexpr (KIND == LINEAR_DW) {
             constexpr int PER = ROWS / CB;  // rows of a copy
             int r = step_rows[i * PER];
@@ -230,30 +235,43 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_linear_big(LinearArgs A)
             for (int q = 1; q < PER; ++q) r = (int)(lane * 16 / BRB) == q ? step_rows[i * PER + q] : r;
             from = r >= 0 && r < A.nx ? pb[i] + (int64_t)r * A.x_row * 2 : zeros;
         }
-        copy_pieces(from, __builtin_amdgcn_readfirstlane(fill + ABYTES + (wave * CB + i) * 1024));
+        copy_pieces(from, __builtin_amdgcn_readfirstlane(fill + (wave * CB + i) * 1024));
     };
-    const auto copied = [&]() {  // moves on by a step
-        const int64_t da = AKS ? (int64_t)BIG_K * A.g_row * 2 : BIG_K * 2, db = BKS ? (int64_t)BIG_K * A.cin * 2 : BIG_K * 2;
+    // Each side moves on by a step, and to its next tile; past the last one zeros are copied.
+    const auto copied_a = [&]() {
+        const int64_t d = AKS ? (int64_t)BIG_K * A.g_row * 2 : BIG_K * 2;
 #pragma unroll
         for (int i = 0; i < CA; ++i) {
-            if constexpr (KIND == LINEAR_Y) pa[i] = pa[i] ? pa[i] + da : nullptr;
-            else pa[i] += da;
+            if constexpr (KIND == LINEAR_Y) pa[i] = pa[i] ? pa[i] + d : nullptr;
+            else pa[i] += d;
         }
-        if constexpr (KIND != LINEAR_DW) {
-#pragma unroll
-            for (int i = 0; i < CB; ++i) pb[i] += db;
-        }
-        fill ^= STAGE;
-        k_copy += BIG_K;
-    };
-    const auto next_tile = [&]() {  // of the copies; past the last one zeros are copied
-        if (k_copy >= ahead.k_end && after.any) {
-            ahead = after;
-            k_copy = 0;
-            aim(ahead);
-            number += stride;
-            after = tile_at(number);
+        filled();
+        ka += BIG_K;
+        if (ka >= ta.k_end && after.any) {
+            ta = after;
+            ka = 0;
+            aim_a(ta);
+            a_number += stride;
+            after = tile_at(a_number);
             x_rows(after);
+        }
+    };
+    const auto copied_b = [&]() {
+        if constexpr (KIND != LINEAR_DW) {
+            const int64_t d = BKS ? (int64_t)BIG_K * A.cin * 2 : BIG_K * 2;
+#pragma unroll
+            for (int i = 0; i < CB; ++i) pb[i] += d;
+        }
+        filled();
+        kb += BIG_K;
+        if (kb >= tb.k_end) {
+            const BigTile t = tile_at(b_number + stride);
+            if (t.any) {
+                tb = t;
+                kb = 0;
+                b_number += stride;
+                aim_b(tb);
+            }
         }
         look_up();
     };
@@ -279,20 +297,20 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_linear_big(LinearArgs A)
         }
     };
     make(oa, AKS, ARB, lds, wm, MB);
-    make(ob, BKS, BRB, lds + ABYTES, wn, NB);
+    make(ob, BKS, BRB, lds, wn, NB);
     // db: the WN waves that share rows of grad take one of their MB blocks each, read once more
     static_assert(!SUMS || MB == WN, "a block for each wave");
     float sum = 0.0f;
     if constexpr (SUMS) make(os, AKS, ARB, lds, wm + 32 * (wave / WM), 1);
-    // 16 of k: quarter j of the place at `from` (0 or STAGE)
+    // 16 of k: quarter j of the place at offset `from`
     const auto read_a = [&](uint32_t from, int j, int i) {
-        if constexpr (!AKS) return lds_read16((oa.at[0] ^ (32 * j) ^ from) + i * (32 * ARB));
-        const u32x2 lo = lds_read_tr((oa.at[i] ^ from) + j * (16 * ARB)), hi = lds_read_tr((oa.at[4 + i] ^ from) + j * (16 * ARB));
+        if constexpr (!AKS) return lds_read16((oa.at[0] ^ (32 * j)) + from + i * (32 * ARB));
+        const u32x2 lo = lds_read_tr(oa.at[i] + from + j * (16 * ARB)), hi = lds_read_tr(oa.at[4 + i] + from + j * (16 * ARB));
         return Raw16{lo[0], lo[1], hi[0], hi[1]};
     };
     const auto read_b = [&](uint32_t from, int j, int i) {
-        if constexpr (!BKS) return lds_read16((ob.at[0] ^ (32 * j) ^ from) + i * (32 * BRB));
-        const u32x2 lo = lds_read_tr((ob.at[i] ^ from) + j * (16 * BRB)), hi = lds_read_tr((ob.at[4 + i] ^ from) + j * (16 * BRB));
+        if constexpr (!BKS) return lds_read16((ob.at[0] ^ (32 * j)) + from + i * (32 * BRB));
+        const u32x2 lo = lds_read_tr(ob.at[i] + from + j * (16 * BRB)), hi = lds_read_tr(ob.at[4 + i] + from + j * (16 * BRB));
         return Raw16{lo[0], lo[1], hi[0], hi[1]};
     };
 
@@ -307,30 +325,30 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_linear_big(LinearArgs A)
                 for (int e = 0; e < 16; ++e) acc[m][n][e] = 0.0f;
         sum = 0.0f;
     };
-    uint32_t place = 0;
-    const auto quarter = [&](int j) {  // products of quarter j, while the next quarter's operands are read
-        const uint32_t from = j == 3 ? place ^ STAGE : place;
+    uint32_t place_a = 0, place_b = ABYTES;  // offsets of this step's places
+    const auto on = [](uint32_t place, int places) { return place + places * ABYTES >= RING * ABYTES ? place + (places - RING) * ABYTES : place + places * ABYTES; };
+    // Products of quarter j, with the next quarter's operands read, and copies made, between them.  The
+    // order is fixed: each product is followed by its share of the rest.
+    const auto quarter = [&](int j, auto copy, int copies) {
+        const uint32_t from_a = j == 3 ? on(place_a, 2) : place_a, from_b = j == 3 ? on(place_b, 2) : place_b;
         const int to = (j + 1) & 1, nj = (j + 1) & 3;
+        constexpr int READ_STEPS = MB * NB < 4 ? MB * NB : MB * NB / 2, READS = (MB + NB + READ_STEPS - 1) / READ_STEPS;
 #pragma unroll
-        for (int i = 0; i < NB; ++i) fb[to][i] = read_b(from, nj, i);
+        for (int q = 0; q < MB * NB; ++q) {
+            const int m = q / NB, n = q % NB;
+            acc[m][n] = mma_pieces<uint16_t>(fb[to ^ 1][n], fa[to ^ 1][m], acc[m][n]);
 #pragma unroll
-        for (int i = 0; i < MB; ++i) fa[to][i] = read_a(from, nj, i);
-#pragma unroll
-        for (int m = 0; m < MB; ++m)
-#pragma unroll
-            for (int n = 0; n < NB; ++n) acc[m][n] = mma_pieces<uint16_t>(fb[to ^ 1][n], fa[to ^ 1][m], acc[m][n]);
-        // a product first: what it waits for was read during the last quarter; the reads between the next products
-        constexpr int READS = NB * (BKS ? 2 : 1) + MB * (AKS ? 2 : 1);
-#pragma unroll
-        for (int i = 0; i < 3; ++i) {
-            __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
-            __builtin_amdgcn_sched_group_barrier(0x100, (READS + 2) / 3, 0);
+            for (int r = q * READS; r < (q + 1) * READS && r < MB + NB; ++r) {
+                if (r < NB) fb[to][r] = read_b(from_b, nj, r);
+                else fa[to][r - NB] = read_a(from_a, nj, r - NB);
+            }
+            if (q % 2 && q / 2 < copies) copy(q / 2);
+            __builtin_amdgcn_sched_barrier(0x6);  // only arithmetic may cross
         }
-        __builtin_amdgcn_sched_group_barrier(0x8, MB * NB - 3, 0);
         if constexpr (SUMS) {  // (the last quarter's with the one before it, while the place is still whole)
 #pragma unroll
             for (int q = j; q < 4 && j < 3; q += j == 2 ? 1 : 4) {
-                const u32x2 lo = lds_read_tr((os.at[0] ^ place) + q * (16 * ARB)), hi = lds_read_tr((os.at[4] ^ place) + q * (16 * ARB));
+                const u32x2 lo = lds_read_tr(os.at[0] + place_a + q * (16 * ARB)), hi = lds_read_tr(os.at[4] + place_a + q * (16 * ARB));
                 float v[8];
                 unpack(Raw16{lo[0], lo[1], hi[0], hi[1]}, v, (const uint16_t *)nullptr);
                 sum += ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
@@ -338,24 +356,29 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_linear_big(LinearArgs A)
         }
     };
 
+    const auto all_a = [&]() {
 #pragma unroll
-    for (int i = 0; i < CA; ++i) copy_a(i);
+        for (int i = 0; i < CA; ++i) copy_a(i);
+        copied_a();
+    };
+    const auto all_b = [&]() {
 #pragma unroll
-    for (int i = 0; i < CB; ++i) copy_b(i);
-    copied();
-    next_tile();
-    wait_copies_and_barrier<0>();
-#pragma unroll
-    for (int i = 0; i < CA; ++i) copy_a(i);
-#pragma unroll
-    for (int i = 0; i < CB; ++i) copy_b(i);
-    copied();
+        for (int i = 0; i < CB; ++i) copy_b(i);
+        copied_b();
+    };
+    // the ring's five places: A and B of step 0, A and B of step 1, and A of step 2 in the loop
+    all_a();
+    all_b();
+    all_a();
     clear();
+    wait_copies_and_barrier<CA>();
+    all_b();
 #pragma unroll
-    for (int i = 0; i < MB; ++i) fa[0][i] = read_a(0, 0, i);
+    for (int i = 0; i < MB; ++i) fa[0][i] = read_a(place_a, 0, i);
 #pragma unroll
-    for (int i = 0; i < NB; ++i) fb[0][i] = read_b(0, 0, i);
-    constexpr int STORES = MB * NB * 2;
+    for (int i = 0; i < NB; ++i) fb[0][i] = read_b(place_b, 0, i);
+    constexpr int STORES = MB * NB * 2, C0 = CA / 2;
+    static_assert(CA <= MB * NB && CB <= MB * NB / 2, "a copy after every other product");
     bool stored = false;  // the last tile's stores may still be in flight
     for (;;) {
         float bias = 0.0f;  // of column lane of the wave's
@@ -366,23 +389,21 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_linear_big(LinearArgs A)
         }
         int k = 0;
         do {
-            quarter(0);
-            quarter(1);
-            quarter(2);
-            next_tile();
-            // All of this step's operands are read and the next step's copies have landed.  Loads and
-            // stores count in the order of issue: those after the copies are, at a tile's start, the
-            // last one's stores (unless some were left out at an edge).
-            if (stored) asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(STORES) : "memory");
-            else asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+            const auto none = [](int) {};
+            quarter(0, copy_a, C0);
+            quarter(1, [&](int i) { copy_a(C0 + i); }, CA - C0);
+            copied_a();
+            quarter(2, none, 0);
+            // All of this step's operands are read and both sides' copies for the next have landed.  Loads
+            // and stores count in the order of issue: those after B's copies are A's for the step after
+            // it, and before these, at a tile's start, the last one's stores (unless some were left out at an edge).
+            if (stored) asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(CA + STORES) : "memory");
+            else asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(CA) : "memory");
             stored = false;
-#pragma unroll
-            for (int i = 0; i < CA; ++i) copy_a(i);
-#pragma unroll
-            for (int i = 0; i < CB; ++i) copy_b(i);
-            copied();
-            quarter(3);
-            place ^= STAGE;
+            quarter(3, copy_b, CB);
+            copied_b();
+            place_a = on(place_a, 2);
+            place_b = on(place_b, 2);
             k += BIG_K;
         } while (k < now.k_end);
         // a lane has row l % 32 of each block, its elements in the registers
