@@ -1249,12 +1249,13 @@ int submconv_grouped_linear(const void *x, int64_t x_row, int64_t nx, const int3
     A.cout = cout;
     A.out = out;
     A.out_row = out_row;
-    return grouped_linear(A, dtype, LINEAR_Y, (hipStream_t)stream);
+    return grouped_linear(A, dtype, LINEAR_Y, nullptr, (hipStream_t)stream);
 }
 
 size_t submconv_grouped_linear_backward_workspace(int32_t groups, int64_t n, int32_t cin, int32_t cout, int32_t dtype)
 {
-    return 0;
+    if (linear_check(groups, n, n, cin, cout, dtype, false, false, true) != SUBMCONV_OK) return 0;
+    return linear_dw_workspace(n, groups, cin, cout, dtype);
 }
 
 int submconv_grouped_linear_backward(const void *grad, int64_t grad_row, const void *x, int64_t x_row, int64_t nx,
@@ -1275,7 +1276,7 @@ int submconv_grouped_linear_backward(const void *grad, int64_t grad_row, const v
     if (!aligned_to(grad, es) || !aligned_to(x, es) || !aligned_to(weight, es) || !aligned_to(dx, es) || !aligned_to(dweight, es) ||
         !aligned_to(dbias, 4) || !aligned_to(rows, 4) || !aligned_to(offsets, 4) || !aligned16(workspace))
         return fail(SUBMCONV_E_INVALID_ARG, "misaligned pointer");
-    const size_t need = submconv_grouped_linear_backward_workspace(groups, n, cin, cout, dtype);
+    const size_t need = dweight ? linear_dw_workspace(n, groups, cin, cout, dtype) : 0;
     if (need && (!workspace || workspace_bytes < need))
         return fail(SUBMCONV_E_INVALID_ARG, "workspace of %zu bytes, %zu needed", workspace ? workspace_bytes : 0, need);
     const Range r[] = {range2("grad", grad, n, cout, grad_row, es, false), range2("x", dweight ? x : nullptr, nx, cin, x_row, es, false),
@@ -1300,12 +1301,12 @@ int submconv_grouped_linear_backward(const void *grad, int64_t grad_row, const v
     if (dx && n) {
         A.out = dx;
         A.out_row = dx_row;
-        SC_CHECK(grouped_linear(A, dtype, LINEAR_DX, (hipStream_t)stream));
+        SC_CHECK(grouped_linear(A, dtype, LINEAR_DX, nullptr, (hipStream_t)stream));
     }
     if (dweight) {
         A.out = dweight;
         A.db = dbias;
-        SC_CHECK(grouped_linear(A, dtype, LINEAR_DW, (hipStream_t)stream));
+        SC_CHECK(grouped_linear(A, dtype, LINEAR_DW, workspace, (hipStream_t)stream));
     }
     return SUBMCONV_OK;
 }

@@ -15,6 +15,10 @@ struct LinearArgs {
     int64_t x_row, g_row, out_row;
     int32_t n, nx;
     int groups, cin, cout;
+    // LINEAR_DW in pieces of `chunk` positions of a group (0: whole groups): the sums of piece p, as tiles of
+    // `chunk` positions of all parts are counted, stand in part [p][cout][cin] and db_part [p][cout].
+    int chunk;
+    float *part, *db_part;
 };
 
 // Positions [beg, end) of a part: part 0 lies before the first offset, part p of 1..groups is group
@@ -78,6 +82,33 @@ __device__ __forceinline__ bool find_tile(const LinearArgs &A, int size, uint32_
     return false;
 }
 
+// The pieces of group `group`: the number of its first tile of `size` positions, and how many it has.
+__device__ __forceinline__ void group_tiles(const LinearArgs &A, int size, int group, uint32_t *first, uint32_t *count)
+{
+    int before = 0;
+    uint32_t tiles = 0;
+    for (int index = 0;; index += 64) {
+        const int end = part_ends(A, index, before);
+        int beg = __shfl_up(end, 1, 64);
+        if (lane_id() == 0) beg = before;
+        const uint32_t own = ((uint32_t)(end - beg) + size - 1) / size;
+        uint32_t sum = own;
+#pragma unroll
+        for (int o = 1; o < 64; o <<= 1) {
+            const uint32_t y = __shfl_up(sum, o, 64);
+            if ((int)lane_id() >= o) sum += y;
+        }
+        const int at = group + 1 - index;  // the part's lane
+        if (at < 64) {
+            *count = (uint32_t)__builtin_amdgcn_readlane((int)own, at);
+            *first = tiles + (uint32_t)__builtin_amdgcn_readlane((int)sum, at) - *count;
+            return;
+        }
+        tiles += (uint32_t)__builtin_amdgcn_readlane((int)sum, 63);
+        before = __builtin_amdgcn_readlane(end, 63);
+    }
+}
+
 // Positions of group `group`.
 __device__ __forceinline__ void group_bounds(const LinearArgs &A, int group, Part *part)
 {
@@ -101,9 +132,23 @@ static inline int64_t most_tiles(int64_t n, int groups, int size) { return n / s
 
 enum { LINEAR_Y, LINEAR_DX, LINEAR_DW };
 
+// Tiles of a call in tiles of BIG_TILE squared, at most (LINEAR_DW with a chunk: of all pieces).
+constexpr int BIG_TILE = 256;
+static inline int64_t linear_tiles(int64_t n, int groups, int cin, int cout, int kind, int chunk, int size)
+{
+    const int64_t in = (cin + size - 1) / size, out = (cout + size - 1) / size;
+    if (kind == LINEAR_DW) return in * out * (chunk ? most_tiles(n, groups, chunk) : groups);
+    return most_tiles(n, groups, size) * (kind == LINEAR_Y ? out : in);
+}
+static inline int64_t linear_big_tiles(int64_t n, int groups, int cin, int cout, int kind, int chunk)
+{
+    return linear_tiles(n, groups, cin, cout, kind, chunk, BIG_TILE);
+}
+
 // Blocks of a call's largest launch; a launch holds 2^24 of them.
 int64_t linear_blocks(int64_t n, int groups, int cin, int cout, int kind);
-int grouped_linear(const LinearArgs &A, int dtype, int kind, hipStream_t st);
+int grouped_linear(LinearArgs A, int dtype, int kind, void *workspace, hipStream_t st);
 int grouped_linear_big(const LinearArgs &A, int kind, hipStream_t st);
+size_t linear_dw_workspace(int64_t n, int groups, int cin, int cout, int dtype);
 
 }  // namespace sc

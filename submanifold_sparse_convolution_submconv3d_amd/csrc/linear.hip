@@ -12,6 +12,8 @@
 //
 // Sums are fp32; one rounding to the tensors' type at the end.  Every result element is summed by
 // one lane in a fixed order, so the same call gives the same bits.
+#include <type_traits>
+
 #include "linear.h"
 
 namespace sc {
@@ -55,7 +57,8 @@ __device__ __forceinline__ Raw16 tile_operand(uint32_t lds, int block, int j)
 // Any widths, row distances and alignment: pieces of 16 bytes are loaded into registers with what
 // is missing at the ends of rows as zeros, written to LDS, and the next step's loads are in flight
 // meanwhile.  Four waves, each 64 x 64 of the tile.
-template <typename T, int KIND>
+// PART (LINEAR_DW): pieces of groups, whose sums are kept in fp32 for k_linear_join.
+template <typename T, int KIND, bool PART>
 __global__ __launch_bounds__(256) void k_linear(LinearArgs A)
 {
     constexpr int V = VEC<T>, KT = 64 / (int)sizeof(T);
@@ -68,9 +71,15 @@ __global__ __launch_bounds__(256) void k_linear(LinearArgs A)
     const uint32_t n_tiles = (n_end + LT - 1) / LT, other = blockIdx.x / n_tiles;
     int m0, m_end, n0 = (blockIdx.x - other * n_tiles) * LT, k_end;
     if constexpr (KIND == LINEAR_DW) {
-        const uint32_t m_tiles = (A.cout + LT - 1) / LT, group = other / m_tiles;
-        group_bounds(A, group, &part);
-        m0 = (other - group * m_tiles) * LT;
+        const uint32_t m_tiles = (A.cout + LT - 1) / LT, which = other / m_tiles;
+        if constexpr (PART) {
+            if (!find_tile(A, A.chunk, which, &part) || part.index < 1 || part.index > A.groups) return;
+            part.beg += (int)part.tile * A.chunk;
+            if (part.end - part.beg > A.chunk) part.end = part.beg + A.chunk;
+        } else {
+            group_bounds(A, which, &part);
+        }
+        m0 = (other - which * m_tiles) * LT;
         m_end = A.cout;
         k_end = part.end - part.beg;
     } else {
@@ -139,13 +148,14 @@ __global__ __launch_bounds__(256) void k_linear(LinearArgs A)
             }
         }
     };
-    f32x16 acc[2][2], sums[2];
+    f32x16 acc[2][2];
 #pragma unroll
     for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int e = 0; e < 16; ++e) acc[i][0][e] = acc[i][1][e] = sums[i][e] = 0.0f;
+        for (int e = 0; e < 16; ++e) acc[i][0][e] = acc[i][1][e] = 0.0f;
     const int wm = (wave & 1) * 64, wn = (wave >> 1) * 64;
-    const bool summing = KIND == LINEAR_DW && A.db && n0 == 0 && wn == 0;  // this wave sums its rows of grad too
+    float sums[2] = {0.0f, 0.0f};  // db: of a lane's share of its rows of grad
+    const bool summing = KIND == LINEAR_DW && A.db && n0 == 0 && wn == 0;
     load(0);
     for (int k0 = 0, buf = 0; k0 < k_end; k0 += KT, buf ^= 2 * LBYTES) {
 #pragma unroll
@@ -168,22 +178,32 @@ __global__ __launch_bounds__(256) void k_linear(LinearArgs A)
 #pragma unroll
                 for (int n = 0; n < 2; ++n) acc[m][n] = mma_pieces<T>(b[n], a[m], acc[m][n]);
             if (summing) {
-                const uint32_t one = sizeof(T) == 2 ? 0x3f803f80u : 0x3f800000u;
-                const Raw16 ones = {one, one, one, one};
 #pragma unroll
-                for (int m = 0; m < 2; ++m) sums[m] = mma_pieces<T>(ones, a[m], sums[m]);
+                for (int m = 0; m < 2; ++m) {
+                    float v[V], t = 0.0f;
+                    unpack(a[m], v, (const T *)nullptr);
+#pragma unroll
+                    for (int i = 0; i < V; i += 2) t += v[i] + v[i + 1];
+                    sums[m] += t;
+                }
             }
         }
     }
     // a lane has row l % 32 of each block, its elements in the registers
     const int l = lane_id() & 31;
     const int64_t ld = KIND == LINEAR_DW ? A.cin : A.out_row;
-    T *out = (T *)A.out + (KIND == LINEAR_DW ? (int64_t)group * A.cout * A.cin : 0);
+    typedef typename std::conditional<PART, float, T>::type Out;
+    Out *out = PART ? (Out *)A.part : (Out *)A.out;
+    const int64_t block = PART ? other / ((A.cout + LT - 1) / LT) : group;  // of dw
+    if constexpr (KIND == LINEAR_DW) out += block * A.cout * A.cin;
 #pragma unroll
     for (int m = 0; m < 2; ++m) {
         const int row = m0 + wm + 32 * m + l;
         const bool valid = row < m_end;
-        if (summing && valid && lane_id() < 32) A.db[(int64_t)group * A.cout + row] = sums[m][0];
+        if (summing) {
+            const float sum = sums[m] + other_half(sums[m]);
+            if (valid && lane_id() < 32) (PART ? A.db_part : A.db)[block * A.cout + row] = sum;
+        }
 #pragma unroll
         for (int n = 0; n < 2; ++n)
 #pragma unroll
@@ -203,8 +223,8 @@ __global__ __launch_bounds__(256) void k_linear(LinearArgs A)
                     for (int i = 0; i < 8; ++i)
                         if (e + i < n_end) v[i] += b[i];
                 }
-                T *to = out + (int64_t)row * ld + e;
-                if constexpr (sizeof(T) == 2) {
+                Out *to = out + (int64_t)row * ld + e;
+                if constexpr (sizeof(Out) == 2) {
                     store_raw(to, repack(v, to), n_end - e < 8 ? n_end - e : 8);
                 } else {
                     const float lo[4] = {v[0], v[1], v[2], v[3]}, hi[4] = {v[4], v[5], v[6], v[7]};
@@ -215,36 +235,105 @@ __global__ __launch_bounds__(256) void k_linear(LinearArgs A)
     }
 }
 
+// Sums of the pieces of each group, in order, rounded once; a block is 256 elements of a group's dw (and db).
+template <typename T>
+__global__ __launch_bounds__(256) void k_linear_join(LinearArgs A)
+{
+    const int64_t size = (int64_t)A.cout * A.cin, all = size + (A.db ? A.cout : 0), blocks = (all + 255) / 256;
+    const int group = (int)(blockIdx.x / blocks);
+    uint32_t first, count;
+    group_tiles(A, A.chunk, group, &first, &count);
+    const int64_t i = (blockIdx.x - group * blocks) * 256 + threadIdx.x;
+    if (i >= all) return;
+    const bool bias = i >= size;
+    const float *from = bias ? A.db_part + (int64_t)first * A.cout + (i - size) : A.part + (int64_t)first * size + i;
+    const int64_t step = bias ? A.cout : size;
+    float sum = 0.0f;
+#pragma unroll 8
+    for (uint32_t p = 0; p < count; ++p) sum += from[p * step];
+    if (bias) A.db[(int64_t)group * A.cout + (i - size)] = sum;
+    else ((T *)A.out)[group * size + i] = Elem<T>::from_f32(sum);
+}
+
+// Positions of a piece of dw: whole groups (0) where these are blocks enough, else so many
+// that the blocks of all pieces fill the card some times over.  A piece's sums are written and read again in
+// fp32, so pieces are not shorter than 256 positions.
+static int dw_chunk(int64_t n, int groups, int cin, int cout, bool big)
+{
+    const int size = big ? BIG_TILE : LT;
+    const int64_t tiles = (int64_t)((cin + size - 1) / size) * ((cout + size - 1) / size), want = big ? UNITS : 4 * UNITS;
+    if (groups * tiles >= want / 2 || n < 512) return 0;
+    const int64_t pieces = (want + tiles - 1) / tiles;
+    int64_t chunk = (n + pieces - 1) / pieces;
+    chunk = (chunk + 63) / 64 * 64;
+    return (int)(chunk < 256 ? 256 : chunk);
+}
+
+// Whether the large tiles may take a call of these widths.
+static bool wide_enough(int cin, int cout, int dtype, int kind)
+{
+    return dtype == SUBMCONV_BF16 && cin % 8 == 0 && cout % 8 == 0 && (kind == LINEAR_Y ? cout : cin) >= 192 && (kind != LINEAR_DW || cout >= 192);
+}
+
+size_t linear_dw_workspace(int64_t n, int groups, int cin, int cout, int dtype)
+{
+    int64_t pieces = 0;
+    for (int big = 0; big < 2; ++big) {
+        if (big && !wide_enough(cin, cout, dtype, LINEAR_DW)) continue;
+        const int chunk = dw_chunk(n, groups, cin, cout, big);
+        const int64_t p = chunk ? most_tiles(n, groups, chunk) : 0;
+        pieces = p > pieces ? p : pieces;
+    }
+    return (size_t)pieces * cout * ((size_t)cin + 1) * sizeof(float);
+}
+
 int64_t linear_blocks(int64_t n, int groups, int cin, int cout, int kind)
 {
-    const int64_t in = (cin + LT - 1) / LT, out = (cout + LT - 1) / LT;
-    return kind == LINEAR_DW ? in * out * groups : most_tiles(n, groups, LT) * (kind == LINEAR_Y ? out : in);
+    return linear_tiles(n, groups, cin, cout, kind, kind == LINEAR_DW ? dw_chunk(n, groups, cin, cout, false) : 0, LT);
 }
 
 // Whether the large tiles take a call: bf16, whole pieces of 16 bytes everywhere, and both sides long
 // enough.
 static bool takes_big(const LinearArgs &A, int dtype, int kind)
 {
-    if (dtype != SUBMCONV_BF16 || A.cin % 8 || A.cout % 8) return false;
+    if (!wide_enough(A.cin, A.cout, dtype, kind)) return false;
     const auto pieces = [](const void *p, int64_t row) { return ((uintptr_t)p & 15) == 0 && row % 8 == 0; };
     if (kind != LINEAR_DX && !pieces(A.x, A.x_row)) return false;
     if (kind != LINEAR_Y && !pieces(A.g, A.g_row)) return false;
     if (kind != LINEAR_DW && !pieces(A.w, 0)) return false;
-    const int cols = kind == LINEAR_Y ? A.cout : A.cin;
-    return cols >= 192 && (kind == LINEAR_DW ? A.cout >= 192 : A.n / A.groups >= 128);
+    return kind == LINEAR_DW || A.n / A.groups >= 128;
 }
 
-int grouped_linear(const LinearArgs &A, int dtype, int kind, hipStream_t st)
+int grouped_linear(LinearArgs A, int dtype, int kind, void *workspace, hipStream_t st)
 {
-    if (takes_big(A, dtype, kind)) return grouped_linear_big(A, kind, st);
-    const int64_t blocks = linear_blocks(A.n, A.groups, A.cin, A.cout, kind);
-    const dim3 grid((unsigned)blocks);
-#define GO(T, KIND) hipLaunchKernelGGL((k_linear<T, KIND>), grid, dim3(256), 0, st, A)
-#define BY_KIND(T) if (kind == LINEAR_Y) GO(T, LINEAR_Y); else if (kind == LINEAR_DX) GO(T, LINEAR_DX); else GO(T, LINEAR_DW)
-    if (dtype == SUBMCONV_F32) { BY_KIND(float); } else { BY_KIND(uint16_t); }
+    const bool big = takes_big(A, dtype, kind);
+    if (kind == LINEAR_DW) {
+        A.chunk = dw_chunk(A.n, A.groups, A.cin, A.cout, big);
+        A.part = (float *)workspace;
+        A.db_part = A.part + (A.chunk ? most_tiles(A.n, A.groups, A.chunk) * A.cout * A.cin : 0);
+    }
+    if (big) {
+        SC_CHECK(grouped_linear_big(A, kind, st));
+    } else {
+        const dim3 grid((unsigned)linear_tiles(A.n, A.groups, A.cin, A.cout, kind, A.chunk, LT));
+#define GO(T, KIND, PART) hipLaunchKernelGGL((k_linear<T, KIND, PART>), grid, dim3(256), 0, st, A)
+#define BY_KIND(T)                                 \
+    if (kind == LINEAR_Y) GO(T, LINEAR_Y, false);  \
+    else if (kind == LINEAR_DX) GO(T, LINEAR_DX, false); \
+    else if (A.chunk) GO(T, LINEAR_DW, true);      \
+    else GO(T, LINEAR_DW, false)
+        if (dtype == SUBMCONV_F32) { BY_KIND(float); } else { BY_KIND(uint16_t); }
 #undef BY_KIND
 #undef GO
-    SC_LAUNCHED("grouped_linear");
+        SC_LAUNCHED("grouped_linear");
+    }
+    if (kind == LINEAR_DW && A.chunk) {
+        const int64_t all = (int64_t)A.cout * A.cin + (A.db ? A.cout : 0);
+        const dim3 grid((unsigned)((all + 255) / 256 * A.groups));
+        if (dtype == SUBMCONV_F32) hipLaunchKernelGGL(k_linear_join<float>, grid, dim3(256), 0, st, A);
+        else hipLaunchKernelGGL(k_linear_join<uint16_t>, grid, dim3(256), 0, st, A);
+        SC_LAUNCHED("grouped_linear sums");
+    }
     return SUBMCONV_OK;
 }
 

@@ -7,6 +7,8 @@
 // operands of the next quarter are read from LDS meanwhile.  Before the last quarter its operands are
 // in registers: after the step's one barrier there the next step's copies, which have landed, are read,
 // and the place that is done with is filled with the step after that.
+#include <type_traits>
+
 #include "linear.h"
 
 namespace sc {
@@ -15,7 +17,8 @@ __device__ __attribute__((aligned(16))) const uint32_t zero_piece[4] = {0, 0, 0,
 
 // A tile of the result: rows m0 .. m_end of part, from column n0 on; k_end terms a sum.
 struct BigTile {
-    int m0, m_end, n0, k_end, group, beg;  // beg: first position of the group (LINEAR_DW)
+    int m0, m_end, n0, k_end, group;
+    int beg, piece;  // LINEAR_DW: first position of the group or of its piece, and the piece's number
     bool real, any;
 };
 
@@ -26,15 +29,27 @@ struct BigTiles {
     uint32_t m_total, n_tiles, total;
     int end, beg;         // of the lane's part
     uint32_t tiles_end;   // tiles of the parts up to the lane's
+    int rank;             // LINEAR_DW: of the lane's group among all, the longest first
     bool kept;
+    static constexpr bool DW = KIND == LINEAR_DW;
 
     __device__ __forceinline__ explicit BigTiles(const LinearArgs &args) : A(args)
     {
         n_tiles = ((KIND == LINEAR_Y ? A.cout : A.cin) + BN - 1) / BN;
         kept = A.groups + 2 <= 64;
-        if constexpr (KIND == LINEAR_DW) {
-            m_total = (uint32_t)A.groups * ((A.cout + BM - 1) / BM);
-            if (kept) part_of(0, 0);
+        rank = 0;
+        const uint32_t m_tiles = DW ? (A.cout + BM - 1) / BM : 1;
+        if (DW && !A.chunk) {
+            m_total = (uint32_t)A.groups * m_tiles;
+            if (kept) {
+                part_of(0, 0);
+                const int group = (int)lane_id() - 1, len = end - beg;
+                for (int g = 0; g < A.groups; ++g) {
+                    const int other = __builtin_amdgcn_readlane(len, g + 1);
+                    rank += other > len || (other == len && g < group);
+                }
+                if (group < 0 || group >= A.groups) rank = -1;
+            }
         } else {
             m_total = 0;
             int before = 0;
@@ -43,6 +58,7 @@ struct BigTiles {
                 m_total += (uint32_t)__builtin_amdgcn_readlane((int)tiles_end, 63);
                 before = __builtin_amdgcn_readlane(end, 63);
             }
+            m_total *= m_tiles;
         }
         total = m_total * n_tiles;
     }
@@ -52,7 +68,8 @@ struct BigTiles {
         end = part_ends(A, index, before);
         beg = __shfl_up(end, 1, 64);
         if (lane_id() == 0) beg = before;
-        tiles_end = ((uint32_t)(end - beg) + BM - 1) / BM;
+        const uint32_t size = DW ? (A.chunk ? A.chunk : 1) : BM;
+        tiles_end = ((uint32_t)(end - beg) + size - 1) / size;
 #pragma unroll
         for (int o = 1; o < 64; o <<= 1) {
             const uint32_t y = __shfl_up(tiles_end, o, 64);
@@ -66,24 +83,26 @@ struct BigTiles {
     {
         BigTile b;
         b.any = t < total;
-        b.m0 = b.m_end = b.n0 = b.k_end = b.group = b.beg = 0;
+        b.m0 = b.m_end = b.n0 = b.k_end = b.group = b.beg = b.piece = 0;
         b.real = false;
         if (!b.any) return b;
         const uint32_t g = t / (GROUP * n_tiles), r = t - g * GROUP * n_tiles, rows = m_total - g * GROUP < GROUP ? m_total - g * GROUP : GROUP;
         const uint32_t n = r / rows, m = g * GROUP + (r - n * rows);
         b.n0 = n * BN;
-        if constexpr (KIND == LINEAR_DW) {
-            const uint32_t m_tiles = (A.cout + BM - 1) / BM, group = m / m_tiles;
-            b.m0 = (m - group * m_tiles) * BM;
+        const uint32_t m_tiles = DW ? (A.cout + BM - 1) / BM : 1, which = m / m_tiles;  // DW: of the groups by length, or of the pieces
+        if (DW && !A.chunk) {
+            b.m0 = (m - which * m_tiles) * BM;
             b.m_end = A.cout;
-            b.group = group;
             b.real = true;
             if (kept) {
-                b.beg = __builtin_amdgcn_readlane(end, group);  // the end of the part before it
-                b.k_end = __builtin_amdgcn_readlane(end, group + 1) - b.beg;
+                const int at = __builtin_ctzll(__ballot(rank == (int)which));
+                b.group = at - 1;
+                b.beg = __builtin_amdgcn_readlane(beg, at);
+                b.k_end = __builtin_amdgcn_readlane(end, at) - b.beg;
             } else {
                 Part p;
-                group_bounds(A, group, &p);
+                group_bounds(A, which, &p);
+                b.group = which;
                 b.beg = p.beg;
                 b.k_end = p.end - p.beg;
             }
@@ -94,19 +113,27 @@ struct BigTiles {
                 for (;; index += 64) {
                     part_of(index, before);
                     const uint32_t last = (uint32_t)__builtin_amdgcn_readlane((int)tiles_end, 63);
-                    if (tiles + last > m) break;
+                    if (tiles + last > which) break;
                     tiles += last;
                     before = __builtin_amdgcn_readlane(end, 63);
                 }
-            const int at = __builtin_ctzll(__ballot(tiles + tiles_end > m));
+            const int at = __builtin_ctzll(__ballot(tiles + tiles_end > which));
             const int pb = __builtin_amdgcn_readlane(beg, at), pe = __builtin_amdgcn_readlane(end, at);
             const uint32_t first = at ? (uint32_t)__builtin_amdgcn_readlane((int)tiles_end, at ? at - 1 : 0) : 0;
             const int part = index + at;
-            b.m0 = pb + (int)(m - tiles - first) * BM;
-            b.m_end = pe;
             b.real = part >= 1 && part <= A.groups;
             b.group = b.real ? part - 1 : 0;
-            b.k_end = b.real ? (KIND == LINEAR_Y ? A.cin : A.cout) : 0;  // rows of no group become zeros
+            if constexpr (DW) {
+                b.m0 = (m - which * m_tiles) * BM;
+                b.m_end = A.cout;
+                b.beg = pb + (int)(which - tiles - first) * A.chunk;
+                b.k_end = !b.real ? 0 : (pe - b.beg < A.chunk ? pe - b.beg : A.chunk);
+                b.piece = which;
+            } else {
+                b.m0 = pb + (int)(which - tiles - first) * BM;
+                b.m_end = pe;
+                b.k_end = b.real ? (KIND == LINEAR_Y ? A.cin : A.cout) : 0;  // rows of no group become zeros
+            }
         }
         return b;
     }
@@ -122,8 +149,8 @@ __device__ __forceinline__ void copy_pieces(const char *from, uint32_t lds)
 }
 
 // WM x WN waves of MB x NB blocks of 32 x 32.
-// SUMS (LINEAR_DW): db too.
-template <int KIND, int WM, int WN, int MB, int NB, bool SUMS>
+// LINEAR_DW: SUMS: db too.  PART: pieces of groups, whose sums are kept in fp32 for k_linear_join.
+template <int KIND, int WM, int WN, int MB, int NB, bool SUMS, bool PART>
 __global__ __launch_bounds__(64 * WM * WN, 2) void k_linear_big(LinearArgs A)
 {
     constexpr bool AKS = KIND == LINEAR_DW, BKS = KIND != LINEAR_Y;
@@ -139,11 +166,24 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_linear_big(LinearArgs A)
     const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = lane_id();
 
     BigTiles<KIND, BM, BN> tiles(A);
-    // the 8 XCDs, to which blocks are dealt in turn, each take an eighth of the tiles
-    const uint32_t share = (tiles.total + 7) / 8, xcd = blockIdx.x % 8, stride = gridDim.x / 8;
-    const uint32_t last = share * (xcd + 1) < tiles.total ? share * (xcd + 1) : tiles.total;
-    uint32_t number = share * xcd + blockIdx.x / 8;
-    const auto tile_at = [&](uint32_t t) { return tiles.at(t < last ? t : tiles.total); };
+    // Blocks are dealt to the 8 XCDs in turn; those of one take neighbouring tiles, that share an L2:
+    // each an eighth of all tiles, or, where tiles are of unequal length (whole groups), of each round.  Every
+    // other round of these runs backwards, so that a block with a longer tile gets a shorter one next.
+    const uint32_t xcd = blockIdx.x % 8, per = gridDim.x / 8, slot = blockIdx.x / 8, share = (tiles.total + 7) / 8;
+    const auto tile_at = [&](uint32_t round) {
+        uint32_t t;
+        bool there;
+        if (KIND == LINEAR_DW && !A.chunk) {
+            const uint32_t q = xcd * per + slot;
+            t = round * gridDim.x + (round % 2 ? gridDim.x - 1 - q : q);
+            there = t < tiles.total;
+        } else {
+            const uint32_t in = slot + round * per;
+            t = share * xcd + in;
+            there = in < share && t < tiles.total;
+        }
+        return tiles.at(there ? t : tiles.total);
+    };
 
     // ---- copies: where a lane's piece of each copy is read next ----
     const char *pa[CA], *pb[CB];
@@ -192,16 +232,16 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_linear_big(LinearArgs A)
         }
     };
 
-    BigTile now = tile_at(number);
+    BigTile now = tile_at(0);
     if (!now.any) return;
     // What is copied of each side, and from which k on; A's copies run a step ahead of B's.
     BigTile ta = now, tb = now, after;
-    uint32_t now_number = number, b_number = number, a_number = number + stride;  // (of `after`)
+    uint32_t now_round = 0, b_round = 0, a_round = 1;  // (of `after`)
     int ka = 0, kb = 0;
     x_rows(ta);
     aim_a(ta);
     aim_b(tb);
-    after = tile_at(a_number);
+    after = tile_at(a_round);
     x_rows(after);
 
     // LINEAR_DW: the rows of x of the step that is copied next.  A wave's copies take consecutive
@@ -251,8 +291,8 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_linear_big(LinearArgs A)
             ta = after;
             ka = 0;
             aim_a(ta);
-            a_number += stride;
-            after = tile_at(a_number);
+            ++a_round;
+            after = tile_at(a_round);
             x_rows(after);
         }
     };
@@ -265,11 +305,11 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_linear_big(LinearArgs A)
         filled();
         kb += BIG_K;
         if (kb >= tb.k_end) {
-            const BigTile t = tile_at(b_number + stride);
+            const BigTile t = tile_at(b_round + 1);
             if (t.any) {
                 tb = t;
                 kb = 0;
-                b_number += stride;
+                ++b_round;
                 aim_b(tb);
             }
         }
@@ -377,7 +417,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_linear_big(LinearArgs A)
     for (int i = 0; i < MB; ++i) fa[0][i] = read_a(place_a, 0, i);
 #pragma unroll
     for (int i = 0; i < NB; ++i) fb[0][i] = read_b(place_b, 0, i);
-    constexpr int STORES = MB * NB * 2, C0 = CA / 2;
+    constexpr int STORES = MB * NB * (PART ? 4 : 2), C0 = CA / 2;
     static_assert(CA <= MB * NB && CB <= MB * NB / 2, "a copy after every other product");
     bool stored = false;  // the last tile's stores may still be in flight
     for (;;) {
@@ -410,11 +450,13 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_linear_big(LinearArgs A)
         const int l = lane & 31, a = lane >> 5;
         const int64_t ld = KIND == LINEAR_DW ? A.cin : A.out_row;
         const int n_end = KIND == LINEAR_Y ? A.cout : A.cin;
-        uint16_t *out = (uint16_t *)A.out + (KIND == LINEAR_DW ? (int64_t)now.group * A.cout * A.cin : 0);
+        typedef typename std::conditional<PART, float, uint16_t>::type Out;
+        Out *out = PART ? (Out *)A.part : (Out *)A.out;
+        if constexpr (KIND == LINEAR_DW) out += (int64_t)(PART ? now.piece : now.group) * A.cout * A.cin;
         if constexpr (SUMS) {
             sum += other_half(sum);
             const int row = now.m0 + (int)wm + 32 * (int)(wave / WM) + l;
-            if (now.n0 == 0 && a == 0 && row < now.m_end) A.db[(int64_t)now.group * A.cout + row] = sum;
+            if (now.n0 == 0 && a == 0 && row < now.m_end) (PART ? A.db_part : A.db)[(int64_t)(PART ? now.piece : now.group) * A.cout + row] = sum;
         }
         const bool whole = now.m0 + BM <= now.m_end && now.n0 + BN <= n_end;
         const auto piece = [&](int m, int n, int h, float (&v)[8]) {  // 8 elements in a row after the halves' exchange
@@ -433,14 +475,23 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_linear_big(LinearArgs A)
 #pragma unroll
                 for (int i = 0; i < 8; ++i) b[i] = KIND == LINEAR_Y ? __shfl(bias, 32 * n + 16 * h + 8 * a + i, 64) : 0.0f;
                 const int e = now.n0 + (int)wn + 32 * n + 16 * h + 8 * a;
-                uint16_t *to = out + (int64_t)(now.m0 + (int)wm + l) * ld + e;
+                Out *to = out + (int64_t)(now.m0 + (int)wm + l) * ld + e;
+                const auto put = [&](Out *at, int have) {
+                    if constexpr (PART) {
+                        const float lo[4] = {v[0], v[1], v[2], v[3]}, hi[4] = {v[4], v[5], v[6], v[7]};
+                        store_raw(at, repack(lo, at), have < 4 ? have : 4);
+                        if (have > 4) store_raw(at + 4, repack(hi, at), have - 4);
+                    } else {
+                        store_raw(at, repack(v, at), have);
+                    }
+                };
                 if (whole) {
 #pragma unroll
                     for (int m = 0; m < MB; ++m) {
                         piece(m, n, h, v);
 #pragma unroll
                         for (int i = 0; i < 8; ++i) v[i] += b[i];
-                        *(Raw16Any *)(to + (int64_t)(32 * m) * ld) = repack(v, to);
+                        put(to + (int64_t)(32 * m) * ld, 8);
                     }
                 } else {
 #pragma unroll
@@ -448,32 +499,31 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_linear_big(LinearArgs A)
                         piece(m, n, h, v);
 #pragma unroll
                         for (int i = 0; i < 8; ++i) v[i] += b[i];
-                        if (now.m0 + (int)wm + 32 * m + l < now.m_end && e < n_end)
-                            store_raw(to + (int64_t)(32 * m) * ld, repack(v, to), n_end - e < 8 ? n_end - e : 8);
+                        if (now.m0 + (int)wm + 32 * m + l < now.m_end && e < n_end) put(to + (int64_t)(32 * m) * ld, n_end - e < 8 ? n_end - e : 8);
                     }
                 }
             }
         stored = whole;
-        now_number += stride;
-        now = tile_at(now_number);
+        now = tile_at(++now_round);
         if (!now.any) break;
         clear();
     }
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // no copy may land in LDS that the next block owns
 }
 
-// 256 x 256 in eight waves.
+// Tiles of 256 x 256 in eight waves.
 int grouped_linear_big(const LinearArgs &A, int kind, hipStream_t st)
 {
-    constexpr int WM = 2, WN = 4, MB = 4, NB = 2, BM = 32 * WM * MB, BN = 32 * WN * NB;
-    const int64_t n_tiles = ((kind == LINEAR_Y ? A.cout : A.cin) + BN - 1) / BN;
-    const int64_t m_tiles = kind == LINEAR_DW ? (int64_t)A.groups * ((A.cout + BM - 1) / BM) : most_tiles(A.n, A.groups, BM);
-    const int64_t blocks = (n_tiles * m_tiles + 7) / 8 * 8;
+    constexpr int WM = 2, WN = 4, MB = 4, NB = 2;
+    static_assert(32 * WM * MB == BIG_TILE && 32 * WN * NB == BIG_TILE, "the tile");
+    const int64_t blocks = (linear_big_tiles(A.n, A.groups, A.cin, A.cout, kind, A.chunk) + 7) / 8 * 8;
     const dim3 grid((unsigned)(blocks < UNITS ? blocks : UNITS)), block(64 * WM * WN);
-    if (kind == LINEAR_Y) hipLaunchKernelGGL((k_linear_big<LINEAR_Y, WM, WN, MB, NB, false>), grid, block, 0, st, A);
-    else if (kind == LINEAR_DX) hipLaunchKernelGGL((k_linear_big<LINEAR_DX, WM, WN, MB, NB, false>), grid, block, 0, st, A);
-    else if (A.db) hipLaunchKernelGGL((k_linear_big<LINEAR_DW, WM, WN, MB, NB, true>), grid, block, 0, st, A);
-    else hipLaunchKernelGGL((k_linear_big<LINEAR_DW, WM, WN, MB, NB, false>), grid, block, 0, st, A);
+#define GO(KIND, SUMS, PART) hipLaunchKernelGGL((k_linear_big<KIND, WM, WN, MB, NB, SUMS, PART>), grid, block, 0, st, A)
+    if (kind == LINEAR_Y) GO(LINEAR_Y, false, false);
+    else if (kind == LINEAR_DX) GO(LINEAR_DX, false, false);
+    else if (A.chunk) { if (A.db) GO(LINEAR_DW, true, true); else GO(LINEAR_DW, false, true); }
+    else { if (A.db) GO(LINEAR_DW, true, false); else GO(LINEAR_DW, false, false); }
+#undef GO
     SC_LAUNCHED("grouped_linear");
     return SUBMCONV_OK;
 }
