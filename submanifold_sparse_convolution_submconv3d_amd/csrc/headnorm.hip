@@ -21,18 +21,47 @@ __device__ __forceinline__ int weight_row(const HeadNormArgs &A, int h)
     return A.q_heads ? h >= A.q_heads : (A.weight_rows > 1 ? h : 0);
 }
 
-// cos and sin of the pairs of RB rows from row0 on, into tab [rb][used].
-__device__ __forceinline__ void form_angles(const HeadNormArgs &A, int64_t row0, float2 *tab)
-{
-    const int used = A.ax.end[SUBMCONV_ROTARY_MAX_AXES - 1];
-    for (int i = threadIdx.x; i < A.rb * used; i += 256) {
-        const int r = i / used, p = i - r * used;
-        const int64_t row = row0 + r < A.n ? row0 + r : A.n - 1;
-        float c, s;
-        turn(A.pos[row * A.pos_row + rotary_axis(A.ax, p)], A.freqs[p], false, &c, &s);
-        tab[i] = make_float2(c, s);
+// The angles of a block's rows in LDS, [rows][used], two sets in turn.  A thread forms its share of the next
+// rows' angles while the present rows are worked on; the position of its first one is loaded a turn earlier
+// still, so that no wave waits for it.
+struct Angles {
+    float2 *tab;
+    int used, many;     // pairs that turn, angles of a set
+    int r, p, axis;     // the thread's first angle: row and pair
+    float freq;
+    int32_t position;
+
+    __device__ __forceinline__ Angles(const HeadNormArgs &A, float2 *lds, int rows) : tab(lds)
+    {
+        used = A.ax.end[SUBMCONV_ROTARY_MAX_AXES - 1];
+        many = rows * used;
+        r = used ? threadIdx.x / used : 0;
+        p = threadIdx.x - r * used;
+        axis = rotary_axis(A.ax, p);
+        freq = (int)threadIdx.x < many ? A.freqs[p] : 0.0f;
+        position = 0;
     }
-}
+    // The first position of the rows from row0 on.
+    __device__ __forceinline__ void load(const HeadNormArgs &A, int64_t row0)
+    {
+        if ((int)threadIdx.x < many) position = A.pos[(row0 + r < A.n ? row0 + r : A.n - 1) * A.pos_row + axis];
+    }
+    // The angles of the rows from row0 on, into set k.
+    __device__ __forceinline__ void form(const HeadNormArgs &A, int64_t row0, int k)
+    {
+        if ((int)threadIdx.x < many) {
+            float c, s;
+            turn(position, freq, false, &c, &s);
+            tab[k * many + threadIdx.x] = make_float2(c, s);
+        }
+        for (int i = threadIdx.x + 256; i < many; i += 256) {
+            const int row = i / used, q = i - row * used;
+            float c, s;
+            turn(A.pos[(row0 + row < A.n ? row0 + row : A.n - 1) * A.pos_row + rotary_axis(A.ax, q)], A.freqs[q], false, &c, &s);
+            tab[k * many + i] = make_float2(c, s);
+        }
+    }
+};
 
 // A lane's elements of a head: P pieces of V.  SPLIT: the same piece of both halves (a pair is
 // elements j of both), otherwise pieces L apart (a pair is two neighbours).
@@ -80,60 +109,79 @@ struct HeadPieces {
     }
 };
 
-constexpr int HEAD_TAB = 2048;  // angles of a block's rows that fit in LDS, twice
+constexpr int HEAD_ROWS = 2;  // rows of a lane at a time, their loads issued together
 
 // out may be x (so neither is restrict).
 template <typename T, int L, int P, bool SPLIT>
 __global__ __launch_bounds__(256) void k_head_norm(HeadNormArgs A)
 {
-    constexpr int V = VEC<T>;
-    __shared__ float2 tab[2][HEAD_TAB];
+    constexpr int V = VEC<T>, U = HEAD_ROWS;
+    extern __shared__ __attribute__((aligned(16))) float2 tab[];
     const HeadPieces<T, L, P, SPLIT> at(A.dim);
-    const int used = A.ax.end[SUBMCONV_ROTARY_MAX_AXES - 1];
     const int group = threadIdx.x / L, r = group / A.hb, h = blockIdx.y * A.hb + group - r * A.hb;
     const bool here = r < A.rb && h < A.heads;
     const int hh = here ? h : 0;
+    Angles angles(A, tab, U * A.rb);
+    const int used = angles.used;
+    const T *x = (const T *)A.x + hh * A.x_head;
+    T *out = (T *)A.out + hh * A.out_head;
+    const int64_t step = (int64_t)gridDim.x * A.rb * U;
+    int64_t row0 = (int64_t)blockIdx.x * A.rb * U;
+    const auto row_at = [&](int64_t first, int u) { const int64_t row = first + u * A.rb + r; return row < A.n ? row : A.n - 1; };
+    Raw16 next[U][P];
+    const auto load = [&](int64_t first) {
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int i = 0; i < P; ++i) next[u][i] = load_raw(x + row_at(first, u) * A.x_row + at.e[i], at.nv[i]);
+    };
+    angles.load(A, row0);
+    load(row0);
     float w[P][V];
 #pragma unroll
     for (int i = 0; i < P; ++i)
 #pragma unroll
         for (int j = 0; j < V; ++j) w[i][j] = A.w && j < at.nv[i] ? param(A.w, A.pdtype, weight_row(A, hh) * A.dim + at.e[i] + j) : 1.0f;
-    const T *x = (const T *)A.x + hh * A.x_head;
-    T *out = (T *)A.out + hh * A.out_head;
-    const int64_t step = (int64_t)gridDim.x * A.rb;
-    int64_t row0 = (int64_t)blockIdx.x * A.rb;
-    const auto row_at = [&](int64_t first) { return first + r < A.n ? first + r : A.n - 1; };
-    Raw16 next[P];
-#pragma unroll
-    for (int i = 0; i < P; ++i) next[i] = load_raw(x + row_at(row0) * A.x_row + at.e[i], at.nv[i]);
-    if (used) form_angles(A, row0, tab[0]);
+    if (used) {
+        angles.form(A, row0, 0);
+        angles.load(A, row0 + step);
+    }
     const float dim = (float)A.dim;
     for (int k = 0; row0 < A.n; row0 += step, k ^= 1) {
-        float v[P][V], s = 0.0f;
+        float v[U][P][V], s[U];
 #pragma unroll
-        for (int i = 0; i < P; ++i) {
-            unpack(next[i], v[i], x);
+        for (int u = 0; u < U; ++u) {
+            s[u] = 0.0f;
 #pragma unroll
-            for (int j = 0; j < V; ++j) s += v[i][j] * v[i][j];  // zero past the head's end
+            for (int i = 0; i < P; ++i) {
+                unpack(next[u][i], v[u][i], x);
+#pragma unroll
+                for (int j = 0; j < V; ++j) s[u] += v[u][i][j] * v[u][i][j];  // zero past the head's end
+            }
         }
-        if (used) __syncthreads();  // tab[k] is written; tab[k ^ 1] is read no more
+        if (used) __syncthreads();  // set k is written; the other is read no more
         if (row0 + step < A.n) {
-#pragma unroll
-            for (int i = 0; i < P; ++i) next[i] = load_raw(x + row_at(row0 + step) * A.x_row + at.e[i], at.nv[i]);
-            if (used) form_angles(A, row0 + step, tab[k ^ 1]);
+            load(row0 + step);
+            if (used) {
+                angles.form(A, row0 + step, k ^ 1);
+                angles.load(A, row0 + 2 * step);
+            }
         }
-        const float rs = rsqrtf(lanes_sum<L>(s) / dim + A.eps);
 #pragma unroll
-        for (int i = 0; i < P; ++i)
-#pragma unroll
-            for (int j = 0; j < V; ++j) v[i][j] = v[i][j] * rs * w[i][j];
-        at.turn_pairs(v, tab[k] + (r < A.rb ? r : 0) * used, used, 1.0f);
-        const int64_t row = row0 + r;
-        if (here && row < A.n) {
+        for (int u = 0; u < U; ++u) {
+            const float rs = rsqrtf(lanes_sum<L>(s[u]) / dim + A.eps);
 #pragma unroll
             for (int i = 0; i < P; ++i)
-                if (at.nv[i]) store_raw(out + row * A.out_row + at.e[i], repack(v[i], x), at.nv[i]);
-            if (A.rstd && at.lane == 0) A.rstd[row * A.heads + h] = rs;
+#pragma unroll
+                for (int j = 0; j < V; ++j) v[u][i][j] = v[u][i][j] * rs * w[i][j];
+            at.turn_pairs(v[u], tab + k * angles.many + (u * A.rb + (r < A.rb ? r : 0)) * used, used, 1.0f);
+            const int64_t row = row0 + u * A.rb + r;
+            if (here && row < A.n) {
+#pragma unroll
+                for (int i = 0; i < P; ++i)
+                    if (at.nv[i]) store_raw(out + row * A.out_row + at.e[i], repack(v[u][i], x), at.nv[i]);
+                if (A.rstd && at.lane == 0) A.rstd[row * A.heads + h] = rs;
+            }
         }
     }
 }
@@ -144,13 +192,35 @@ __global__ __launch_bounds__(256) void k_head_norm(HeadNormArgs A)
 template <typename T, int L, int P, bool SPLIT>
 __global__ __launch_bounds__(256) void k_head_norm_bwd(HeadNormArgs A)
 {
-    constexpr int V = VEC<T>;
-    __shared__ float2 tab[2][HEAD_TAB];
+    constexpr int V = VEC<T>, U = HEAD_ROWS;
+    extern __shared__ __attribute__((aligned(16))) float2 tab[];
     const HeadPieces<T, L, P, SPLIT> at(A.dim);
-    const int used = A.ax.end[SUBMCONV_ROTARY_MAX_AXES - 1];
     const int group = threadIdx.x / L, r = group / A.hb, h = blockIdx.y * A.hb + group - r * A.hb;
     const bool here = r < A.rb && h < A.heads;
     const int hh = here ? h : 0;
+    Angles angles(A, tab, U * A.rb);
+    const int used = angles.used;
+    const T *x = (const T *)A.x + hh * A.x_head, *g = (const T *)A.g + hh * A.g_head;
+    T *out = (T *)A.out + hh * A.out_head;
+    const int64_t step = (int64_t)gridDim.x * A.rb * U;
+    int64_t row0 = (int64_t)blockIdx.x * A.rb * U;
+    const auto row_at = [&](int64_t first, int u) { const int64_t row = first + u * A.rb + r; return row < A.n ? row : A.n - 1; };
+    Raw16 nx[U][P], ng[U][P];
+    float nr[U];
+    const auto load = [&](int64_t first) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int64_t row = row_at(first, u);
+            nr[u] = A.rstd[row * A.heads + hh];
+#pragma unroll
+            for (int i = 0; i < P; ++i) {
+                nx[u][i] = load_raw(x + row * A.x_row + at.e[i], at.nv[i]);
+                ng[u][i] = load_raw(g + row * A.g_row + at.e[i], at.nv[i]);
+            }
+        }
+    };
+    angles.load(A, row0);
+    load(row0);
     float w[P][V], dw[P][V];
 #pragma unroll
     for (int i = 0; i < P; ++i)
@@ -159,65 +229,59 @@ __global__ __launch_bounds__(256) void k_head_norm_bwd(HeadNormArgs A)
             w[i][j] = A.w && j < at.nv[i] ? param(A.w, A.pdtype, weight_row(A, hh) * A.dim + at.e[i] + j) : 1.0f;
             dw[i][j] = 0.0f;
         }
-    const T *x = (const T *)A.x + hh * A.x_head, *g = (const T *)A.g + hh * A.g_head;
-    T *out = (T *)A.out + hh * A.out_head;
-    const int64_t step = (int64_t)gridDim.x * A.rb;
-    int64_t row0 = (int64_t)blockIdx.x * A.rb;
-    const auto row_at = [&](int64_t first) { return first + r < A.n ? first + r : A.n - 1; };
-    Raw16 nx[P], ng[P];
-    float nr = A.rstd[row_at(row0) * A.heads + hh];
-#pragma unroll
-    for (int i = 0; i < P; ++i) {
-        nx[i] = load_raw(x + row_at(row0) * A.x_row + at.e[i], at.nv[i]);
-        ng[i] = load_raw(g + row_at(row0) * A.g_row + at.e[i], at.nv[i]);
+    if (used) {
+        angles.form(A, row0, 0);
+        angles.load(A, row0 + step);
     }
-    if (used) form_angles(A, row0, tab[0]);
     const float dim = (float)A.dim;
     for (int k = 0; row0 < A.n; row0 += step, k ^= 1) {
-        const int64_t row = row0 + r;
-        const bool on = here && row < A.n;
-        float hat[P][V], u[P][V];
-        const float rs = nr;
+        float hat[U][P][V], g_[U][P][V], rs[U];
 #pragma unroll
-        for (int i = 0; i < P; ++i) {
-            unpack(nx[i], hat[i], x);
-            unpack(ng[i], u[i], x);
+        for (int u = 0; u < U; ++u) {
+            rs[u] = nr[u];
+#pragma unroll
+            for (int i = 0; i < P; ++i) {
+                unpack(nx[u][i], hat[u][i], x);
+                unpack(ng[u][i], g_[u][i], x);
+            }
         }
-        if (used) __syncthreads();  // tab[k] is written; tab[k ^ 1] is read no more
+        if (used) __syncthreads();  // set k is written; the other is read no more
         if (row0 + step < A.n) {
-            nr = A.rstd[row_at(row0 + step) * A.heads + hh];
-#pragma unroll
-            for (int i = 0; i < P; ++i) {
-                nx[i] = load_raw(x + row_at(row0 + step) * A.x_row + at.e[i], at.nv[i]);
-                ng[i] = load_raw(g + row_at(row0 + step) * A.g_row + at.e[i], at.nv[i]);
+            load(row0 + step);
+            if (used) {
+                angles.form(A, row0 + step, k ^ 1);
+                angles.load(A, row0 + 2 * step);
             }
-            if (used) form_angles(A, row0 + step, tab[k ^ 1]);
         }
-        at.turn_pairs(u, tab[k] + (r < A.rb ? r : 0) * used, used, -1.0f);
-        float s = 0.0f;
 #pragma unroll
-        for (int i = 0; i < P; ++i)
+        for (int u = 0; u < U; ++u) {
+            const int64_t row = row0 + u * A.rb + r;
+            const bool on = here && row < A.n;
+            at.turn_pairs(g_[u], tab + k * angles.many + (u * A.rb + (r < A.rb ? r : 0)) * used, used, -1.0f);
+            float s = 0.0f;
 #pragma unroll
-            for (int j = 0; j < V; ++j) {
-                hat[i][j] *= rs;
-                if (on) dw[i][j] += u[i][j] * hat[i][j];
-                u[i][j] *= w[i][j];
-                s += u[i][j] * hat[i][j];
-            }
-        s = lanes_sum<L>(s) / dim;
-        if (on) {
+            for (int i = 0; i < P; ++i)
 #pragma unroll
-            for (int i = 0; i < P; ++i) {
+                for (int j = 0; j < V; ++j) {
+                    hat[u][i][j] *= rs[u];
+                    if (on) dw[i][j] += g_[u][i][j] * hat[u][i][j];
+                    g_[u][i][j] *= w[i][j];
+                    s += g_[u][i][j] * hat[u][i][j];
+                }
+            s = lanes_sum<L>(s) / dim;
+            if (on) {
 #pragma unroll
-                for (int j = 0; j < V; ++j) u[i][j] = rs * (u[i][j] - hat[i][j] * s);
-                if (at.nv[i]) store_raw(out + row * A.out_row + at.e[i], repack(u[i], x), at.nv[i]);
+                for (int i = 0; i < P; ++i) {
+#pragma unroll
+                    for (int j = 0; j < V; ++j) g_[u][i][j] = rs[u] * (g_[u][i][j] - hat[u][i][j] * s);
+                    if (at.nv[i]) store_raw(out + row * A.out_row + at.e[i], repack(g_[u][i], x), at.nv[i]);
+                }
             }
         }
     }
     if (!A.partial) return;
     // [group][dim] in LDS, in the angles' place
-    constexpr int GROUPS = 256 / L, PAD = L * P * V;
-    static_assert(GROUPS * PAD <= 2 * HEAD_TAB * 2, "the lanes' sums fit");
+    constexpr int PAD = L * P * V;
     float *red = (float *)tab;
     __syncthreads();
 #pragma unroll
@@ -278,7 +342,7 @@ __global__ __launch_bounds__(256) void k_head_wgrad(const float *__restrict__ pa
 struct HeadShape {
     int lanes, pieces, hb, rb, chunks;
 };
-static HeadShape head_shape(int heads, int dim, int dtype, int split, int used)
+static HeadShape head_shape(int heads, int dim, int dtype, int split)
 {
     const int v = dtype == SUBMCONV_F32 ? 4 : 8, span = split ? dim / 2 : dim;
     HeadShape s;
@@ -290,14 +354,13 @@ static HeadShape head_shape(int heads, int dim, int dtype, int split, int used)
     s.chunks = (heads + groups - 1) / groups;
     s.hb = (heads + s.chunks - 1) / s.chunks;
     s.rb = groups / s.hb;
-    if (used && s.rb * used > HEAD_TAB) s.rb = HEAD_TAB / used;  // (used <= 256: eight rows at least)
     return s;
 }
 
 constexpr int64_t HEAD_FWD_BLOCKS = 2048, HEAD_BWD_BLOCKS = 1024;
 static int64_t head_blocks(int64_t n, const HeadShape &s, int64_t most)
 {
-    const int64_t b = (n + s.rb - 1) / s.rb, m = most / s.chunks > 0 ? most / s.chunks : 1;
+    const int64_t rows = s.rb * HEAD_ROWS, b = (n + rows - 1) / rows, m = most / s.chunks > 0 ? most / s.chunks : 1;
     return b < m ? b : m;
 }
 
@@ -309,29 +372,30 @@ static int64_t head_partials(int64_t n, const HeadShape &s, int heads, int weigh
 
 size_t head_norm_bwd_workspace(int64_t n, int heads, int dim, int dtype, int weight_rows, int q_heads)
 {
-    // (the larger of both orders of pairs and any sections)
-    int64_t most = 0;
-    for (int split = 0; split < 2; ++split)
-        for (int used = 0; used <= dim / 2; used += dim / 2) {
-            const int64_t p = head_partials(n, head_shape(heads, dim, dtype, split, used), heads, weight_rows, q_heads);
-            most = p > most ? p : most;
-        }
+    int64_t most = 0;  // of both orders of pairs
+    for (int split = 0; split < 2; ++split) {
+        const int64_t p = head_partials(n, head_shape(heads, dim, dtype, split), heads, weight_rows, q_heads);
+        most = p > most ? p : most;
+    }
     return (size_t)most * weight_rows * dim * sizeof(float);
 }
 
+// Bytes of LDS: two sets of angles (at most 32 KB a row of a lane's: a block has 256 / L rows of at most L V pairs).
+static size_t head_lds(const HeadNormArgs &A, const HeadShape &s) { return (size_t)2 * HEAD_ROWS * s.rb * A.ax.end[SUBMCONV_ROTARY_MAX_AXES - 1] * sizeof(float2); }
+
 #define HEAD_LANES(K, T, P, SPLIT)                                                                  \
     switch (s.lanes) {                                                                              \
-    case 2: hipLaunchKernelGGL((K<T, 2, P, SPLIT>), grid, dim3(256), 0, st, A); break;              \
-    case 4: hipLaunchKernelGGL((K<T, 4, P, SPLIT>), grid, dim3(256), 0, st, A); break;              \
-    case 8: hipLaunchKernelGGL((K<T, 8, P, SPLIT>), grid, dim3(256), 0, st, A); break;              \
-    case 16: hipLaunchKernelGGL((K<T, 16, P, SPLIT>), grid, dim3(256), 0, st, A); break;            \
-    case 32: hipLaunchKernelGGL((K<T, 32, P, SPLIT>), grid, dim3(256), 0, st, A); break;            \
-    default: hipLaunchKernelGGL((K<T, 64, P, SPLIT>), grid, dim3(256), 0, st, A);                   \
+    case 2: hipLaunchKernelGGL((K<T, 2, P, SPLIT>), grid, dim3(256), lds, st, A); break;              \
+    case 4: hipLaunchKernelGGL((K<T, 4, P, SPLIT>), grid, dim3(256), lds, st, A); break;              \
+    case 8: hipLaunchKernelGGL((K<T, 8, P, SPLIT>), grid, dim3(256), lds, st, A); break;              \
+    case 16: hipLaunchKernelGGL((K<T, 16, P, SPLIT>), grid, dim3(256), lds, st, A); break;            \
+    case 32: hipLaunchKernelGGL((K<T, 32, P, SPLIT>), grid, dim3(256), lds, st, A); break;            \
+    default: hipLaunchKernelGGL((K<T, 64, P, SPLIT>), grid, dim3(256), lds, st, A);                   \
     }
 #define HEAD_KERNELS(K)                                                                             \
     if (dtype == SUBMCONV_F32) {                                                                    \
         if (split) { HEAD_LANES(K, float, 2, true) }                                                \
-        else if (s.pieces == 2) hipLaunchKernelGGL((K<float, 64, 2, false>), grid, dim3(256), 0, st, A); \
+        else if (s.pieces == 2) hipLaunchKernelGGL((K<float, 64, 2, false>), grid, dim3(256), lds, st, A); \
         else { HEAD_LANES(K, float, 1, false) }                                                     \
     } else {                                                                                        \
         if (split) { HEAD_LANES(K, uint16_t, 2, true) }                                             \
@@ -340,10 +404,11 @@ size_t head_norm_bwd_workspace(int64_t n, int heads, int dim, int dtype, int wei
 
 int head_norm(HeadNormArgs A, int dtype, int split, hipStream_t st)
 {
-    const HeadShape s = head_shape(A.heads, A.dim, dtype, split, A.ax.end[SUBMCONV_ROTARY_MAX_AXES - 1]);
+    const HeadShape s = head_shape(A.heads, A.dim, dtype, split);
     A.hb = s.hb;
     A.rb = s.rb;
     const dim3 grid((unsigned)head_blocks(A.n, s, HEAD_FWD_BLOCKS), (unsigned)s.chunks);
+    const size_t lds = head_lds(A, s);
     HEAD_KERNELS(k_head_norm)
     SC_LAUNCHED("head_norm_rotary");
     return SUBMCONV_OK;
@@ -351,12 +416,14 @@ int head_norm(HeadNormArgs A, int dtype, int split, hipStream_t st)
 
 int head_norm_backward(HeadNormArgs A, int dtype, int split, void *dw, hipStream_t st)
 {
-    const HeadShape s = head_shape(A.heads, A.dim, dtype, split, A.ax.end[SUBMCONV_ROTARY_MAX_AXES - 1]);
+    const HeadShape s = head_shape(A.heads, A.dim, dtype, split);
     A.hb = s.hb;
     A.rb = s.rb;
     if (!dw) A.partial = nullptr;
     if (A.n > 0) {
         const dim3 grid((unsigned)head_blocks(A.n, s, HEAD_BWD_BLOCKS), (unsigned)s.chunks);
+        const size_t sums = dw ? (size_t)256 * s.pieces * (dtype == SUBMCONV_F32 ? 4 : 8) * sizeof(float) : 0, angles = head_lds(A, s);
+        const size_t lds = sums > angles ? sums : angles;
         HEAD_KERNELS(k_head_norm_bwd)
         SC_LAUNCHED("head_norm_rotary_backward");
     }
