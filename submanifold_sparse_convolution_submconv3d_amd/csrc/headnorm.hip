@@ -357,7 +357,7 @@ static HeadShape head_shape(int heads, int dim, int dtype, int split)
     return s;
 }
 
-constexpr int64_t HEAD_FWD_BLOCKS = 2048, HEAD_BWD_BLOCKS = 1024;
+constexpr int64_t HEAD_FWD_BLOCKS = 1024, HEAD_BWD_BLOCKS = 512;
 static int64_t head_blocks(int64_t n, const HeadShape &s, int64_t most)
 {
     const int64_t rows = s.rb * HEAD_ROWS, b = (n + rows - 1) / rows, m = most / s.chunks > 0 ? most / s.chunks : 1;
