@@ -10,6 +10,7 @@
 //   k_route_top    a block's rows: experts and gates, and how many pairs each expert gets
 //   k_route_scan   for each expert, where each block's pairs begin among the expert's
 //   k_route_place  a block's pairs to their places, in order
+// (few pairs: the first kernel alone; up to 64 blocks: without the second)
 // All counts are whole numbers, so the plan does not depend on the order of atomics.  Each kernel
 // is bound by memory where rows are many (the scores are read once), and by its launch where few.
 #include "rowvec.h"
@@ -32,57 +33,156 @@ __device__ __forceinline__ float key_value(uint32_t k)
     return __uint_as_float(k == 0xffffffffu ? 0x7fc00000u : (k >> 31 ? k ^ 0x80000000u : ~k));
 }
 
-// Of two (key, number) pairs the better one: larger key, then smaller number.
-struct Best {
-    uint32_t key, number;
-};
-__device__ __forceinline__ Best better(Best a, Best b)
+// Larger of the group's keys, in every lane of aligned groups of L lanes (a power of two).
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp_max(uint32_t v)
 {
-    return a.key > b.key || (a.key == b.key && a.number < b.number) ? a : b;
+    const uint32_t o = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xf, 0xf, true);
+    return v > o ? v : o;
 }
 template <int L>
-__device__ __forceinline__ Best lanes_best(Best b)
+__device__ __forceinline__ uint32_t lanes_max(uint32_t v)
 {
-#pragma unroll
-    for (int o = 1; o < L; o <<= 1) b = better(b, Best{(uint32_t)__shfl_xor((int)b.key, o, 64), (uint32_t)__shfl_xor((int)b.number, o, 64)});
-    return b;
+    if constexpr (L >= 2) v = dpp_max<0xb1>(v);    // the steps of lanes_sum
+    if constexpr (L >= 4) v = dpp_max<0x4e>(v);
+    if constexpr (L >= 8) v = dpp_max<0x141>(v);
+    if constexpr (L >= 16) v = dpp_max<0x140>(v);
+    if constexpr (L >= 32) {
+        auto r = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+        v = r[0] > r[1] ? r[0] : r[1];
+    }
+    if constexpr (L >= 64) {
+        auto r = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+        v = r[0] > r[1] ? r[0] : r[1];
+    }
+    return v;
 }
 
-// L lanes hold a row's scores, CH pieces of 16 bytes each.
-template <typename T, int L, int CH>
+// Where a block's pairs go.  A wave takes a run of `WAVE_PAIRS` of them, 64 at a time: they find their
+// order among those of the same expert by comparing digits across the wave, and a count of the
+// wave's pairs of each expert so far.  The counts of the block's waves then give each wave its first
+// places.  at [4][experts + 1] and lds [4] are LDS.  BASE(bin) is where the block's pairs of a bin begin
+// among all of the bin's, TOTAL(bin) how many the bin has.
+constexpr int WAVE_CHUNKS = ROUTE_PAIRS / 4 / 64;
+template <class Base, class Total>
+__device__ __forceinline__ void place_pairs(const int32_t *chosen, int64_t first, int64_t end, int k, int experts, int bits,
+                                            uint32_t (*at)[SUBMCONV_ROUTE_MAX_EXPERTS + 1], uint32_t *lds, Base base, Total total,
+                                            int32_t *offsets, int32_t *rows, int32_t *slots)
+{
+    const int bins = experts + 1, wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    for (int i = threadIdx.x; i < bins; i += 256)
+#pragma unroll
+        for (int w = 0; w < 4; ++w) at[w][i] = 0;
+    const int64_t w0 = first + (int64_t)wave * (WAVE_CHUNKS * 64);
+    int32_t e[WAVE_CHUNKS];
+    uint32_t in_wave[WAVE_CHUNKS];
+#pragma unroll
+    for (int c = 0; c < WAVE_CHUNKS; ++c) {
+        const int64_t p = w0 + c * 64 + lane;
+        const int32_t v = p < end ? chosen[p] : 0;
+        e[c] = v < 0 ? experts : v;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int c = 0; c < WAVE_CHUNKS; ++c) {
+        const bool on = w0 + c * 64 + lane < end;
+        const uint64_t same = match_digit((uint32_t)e[c], on, bits);
+        in_wave[c] = 0;
+        if (on) in_wave[c] = at[wave][e[c]] + __popcll(same & lanemask_lt());
+        // all lanes have read before the last of each expert moves its count on
+        __builtin_amdgcn_wave_barrier();
+        if (on && (same >> lane) == 1) at[wave][e[c]] = in_wave[c] + 1;
+        __builtin_amdgcn_wave_barrier();
+    }
+    __syncthreads();
+    uint32_t before = 0;
+    for (int i0 = 0; i0 < bins; i0 += 256) {
+        const int i = i0 + threadIdx.x;
+        const uint32_t v = i < bins ? total(i) : 0;
+        uint32_t sum;
+        const uint32_t start = before + block_incl_scan256(v, lds, &sum) - v;
+        before += sum;
+        if (i < bins) {
+            if (first == 0) offsets[i] = (int32_t)start;  // offsets[experts]: where the pairs without an expert begin
+            uint32_t place = start + base(i);
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+                const uint32_t c = at[w][i];
+                at[w][i] = place;
+                place += c;
+            }
+        }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int c = 0; c < WAVE_CHUNKS; ++c) {
+        const int64_t p = w0 + c * 64 + lane;
+        if (p >= end) continue;
+        const uint32_t place = at[wave][e[c]] + in_wave[c];
+        slots[p] = (int32_t)place;
+        rows[place] = (int32_t)(p / k);
+    }
+}
+
+// L lanes hold a row's scores, CH pieces of 16 bytes each, in order: the first piece of all lanes, then the
+// second.  Each round takes the largest key left; of equal ones the first in that order, which is the smallest
+// number: the first piece, then the first lane (a ballot), then the first element.
+// ALONE: one block has all rows, and places the pairs too.
+template <typename T, int L, int CH, bool ALONE>
 __global__ __launch_bounds__(256) void k_route_top(const T *__restrict__ logits, int64_t ld, int64_t n, int experts, int k,
-                                                   int normalize, int rows_per_block, int32_t *__restrict__ chosen,
-                                                   float *__restrict__ gates, uint32_t *__restrict__ counts)
+                                                   int normalize, int rows_per_block, int bits, int32_t *chosen,
+                                                   float *gates, uint32_t *counts, int32_t *offsets, int32_t *rows, int32_t *slots)
 {
     constexpr int V = VEC<T>, RPB = 256 / L;
     __shared__ uint32_t hist[SUBMCONV_ROUTE_MAX_EXPERTS + 1];
+    __shared__ uint32_t at[ALONE ? 4 : 1][SUBMCONV_ROUTE_MAX_EXPERTS + 1];
+    __shared__ uint32_t lds[4];
+    constexpr int MOST = RPB * (8 * L < SUBMCONV_ROUTE_MAX_K ? 8 * L : SUBMCONV_ROUTE_MAX_K);  // k <= experts <= 8 L
+    __shared__ int32_t numbers[MOST];
+    __shared__ float values[MOST];
     for (int i = threadIdx.x; i <= experts; i += 256) hist[i] = 0;
     __syncthreads();
     const int lane = threadIdx.x % L, g = threadIdx.x / L;
+    const uint64_t group = (L == 64 ? ~0ull : (1ull << L) - 1) << (lane_id() / L * L);  // of the wave's lanes
     const int64_t first = (int64_t)blockIdx.x * rows_per_block;
     const int64_t end = first + rows_per_block < n ? first + rows_per_block : n;
-    for (int64_t row0 = first; row0 < end; row0 += RPB) {
+    int nv[CH], e0[CH];
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+        const int e = (i * L + lane) * V;
+        nv[i] = experts - e < 0 ? 0 : (experts - e < V ? experts - e : V);
+        e0[i] = nv[i] ? e : 0;
+    }
+    Raw16 next[CH];
+    const auto load = [&](int64_t row0) {
         const int64_t row = row0 + g < end ? row0 + g : end - 1;
-        const bool on = row0 + g < end;
+#pragma unroll
+        for (int i = 0; i < CH; ++i) next[i] = load_raw(logits + row * ld + e0[i], nv[i]);
+    };
+    load(first);
+    for (int64_t row0 = first; row0 < end; row0 += RPB) {
         uint32_t key[CH][V];
 #pragma unroll
         for (int i = 0; i < CH; ++i) {
-            const int e = (i * L + lane) * V, nv = experts - e < 0 ? 0 : (experts - e < V ? experts - e : V);
             float v[V];
-            unpack(load_raw(logits + row * ld + (nv ? e : 0), nv), v, logits);
+            unpack(next[i], v, logits);
 #pragma unroll
-            for (int j = 0; j < V; ++j) key[i][j] = j < nv ? order_key(v[j]) : 0;
+            for (int j = 0; j < V; ++j) key[i][j] = j < nv[i] ? order_key(v[j]) : 0;
         }
+        if (row0 + RPB < end) load(row0 + RPB);
         float top = 0.0f, total = 0.0f;
         for (int j = 0; j < k; ++j) {
-            Best b = {0, 0xffffffffu};
+            uint32_t own[CH], best = 0;
 #pragma unroll
-            for (int i = 0; i < CH; ++i)
+            for (int i = 0; i < CH; ++i) {
+                own[i] = 0;
 #pragma unroll
-                for (int q = 0; q < V; ++q) b = better(b, Best{key[i][q], (uint32_t)((i * L + lane) * V + q)});
-            b = lanes_best<L>(b);
-            const bool there = b.key > KEY_CLOSED;
-            const float value = key_value(b.key);
+                for (int q = 0; q < V; ++q) own[i] = own[i] > key[i][q] ? own[i] : key[i][q];
+                best = best > own[i] ? best : own[i];
+            }
+            best = lanes_max<L>(best);
+            const bool there = best > KEY_CLOSED;
+            const float value = key_value(best);
             if (j == 0) {
                 top = there ? value : 0.0f;
                 if (!normalize) {
@@ -96,23 +196,52 @@ __global__ __launch_bounds__(256) void k_route_top(const T *__restrict__ logits,
             }
             const float e = there ? expf(value - top) : 0.0f;
             if (normalize) total += e;
+            if (!there) {  // the rest is closed
+                if (lane == 0) {
+                    numbers[g * k + j] = -1;
+                    values[g * k + j] = 0.0f;
+                }
+                continue;
+            }
+            bool taken = false;
 #pragma unroll
-            for (int i = 0; i < CH; ++i)
+            for (int i = 0; i < CH; ++i) {
+                const uint64_t with = __ballot(own[i] == best) & group;
+                if (!taken && with && lane_id() == (unsigned)__builtin_ctzll(with)) {
+                    bool open = true;
 #pragma unroll
-                for (int q = 0; q < V; ++q)
-                    if (b.number == (uint32_t)((i * L + lane) * V + q)) key[i][q] = 0;
-            if (on && lane == 0) {
-                const int32_t expert = there ? (int32_t)b.number : -1;
-                chosen[row * k + j] = expert;
-                gates[row * k + j] = e;  // divided below
-                atomicAdd(&hist[there ? expert : experts], 1u);
+                    for (int q = 0; q < V; ++q)
+                        if (open && key[i][q] == best) {
+                            open = false;
+                            key[i][q] = 0;
+                            numbers[g * k + j] = (i * L + lane) * V + q;
+                            values[g * k + j] = e;
+                        }
+                }
+                taken = taken || with != 0;
             }
         }
-        if (on && lane == 0)
-            for (int j = 0; j < k; ++j) gates[row * k + j] = total == 0.0f ? 0.0f : gates[row * k + j] / total;
+        // The pairs of a wave's rows lie next to each other; no other wave sees its part of the LDS.
+        __builtin_amdgcn_wave_barrier();
+        const int64_t w0 = row0 + (int64_t)(threadIdx.x >> 6) * (64 / L);
+        const int64_t here = end - w0 < 64 / L ? end - w0 : 64 / L;
+        for (int j = lane; j < k; j += L) values[g * k + j] = total == 0.0f ? 0.0f : values[g * k + j] / total;
+        __builtin_amdgcn_wave_barrier();
+        const int base = (int)(threadIdx.x >> 6) * (64 / L) * k;
+        for (int i = (int)lane_id(); i < (int)here * k; i += 64) {
+            const int32_t number = numbers[base + i];
+            chosen[w0 * k + i] = number;
+            gates[w0 * k + i] = values[base + i];
+            atomicAdd(&hist[number < 0 ? experts : number], 1u);
+        }
+        __builtin_amdgcn_wave_barrier();
     }
     __syncthreads();
-    for (int i = threadIdx.x; i <= experts; i += 256) counts[(int64_t)i * gridDim.x + blockIdx.x] = hist[i];
+    if constexpr (ALONE) {
+        place_pairs(chosen, 0, n * k, k, experts, bits, at, lds, [](int) { return 0u; }, [&](int i) { return hist[i]; }, offsets, rows, slots);
+    } else {
+        for (int i = threadIdx.x; i <= experts; i += 256) counts[(int64_t)i * gridDim.x + blockIdx.x] = hist[i];
+    }
 }
 
 // counts [bins][blocks] become, for each bin, exclusive sums over the blocks; totals [bins].
@@ -132,9 +261,9 @@ __global__ __launch_bounds__(256) void k_route_scan(uint32_t *__restrict__ count
     if (threadIdx.x == 0) totals[blockIdx.x] = before;
 }
 
-// The places of a block's pairs.  A wave takes a run of the block's pairs: it counts them by
-// expert, the counts of the block's waves give each wave its first places, and 64 pairs at a
-// time find their order among those of the same expert by comparing digits across the wave.
+// The places of each block's pairs.  SCANNED: counts are sums over the blocks already; else each block
+// adds up the few that there are.
+template <bool SCANNED>
 __global__ __launch_bounds__(256) void k_route_place(const int32_t *__restrict__ chosen, int64_t pairs, int k, int experts, int bits,
                                                      int pairs_per_block, const uint32_t *__restrict__ counts,
                                                      const uint32_t *__restrict__ totals, int32_t *__restrict__ offsets,
@@ -142,91 +271,71 @@ __global__ __launch_bounds__(256) void k_route_place(const int32_t *__restrict__
 {
     __shared__ uint32_t at[4][SUBMCONV_ROUTE_MAX_EXPERTS + 1];
     __shared__ uint32_t lds[4];
-    const int bins = experts + 1, wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-    for (int i = threadIdx.x; i < 4 * (SUBMCONV_ROUTE_MAX_EXPERTS + 1); i += 256) (&at[0][0])[i] = 0;
-    __syncthreads();
     const int64_t first = (int64_t)blockIdx.x * pairs_per_block;
     const int64_t end = first + pairs_per_block < pairs ? first + pairs_per_block : pairs;
-    const int run = (pairs_per_block / 4 + 63) / 64 * 64;  // pairs of a wave
-    const int64_t w0 = first + (int64_t)wave * run, w1 = w0 + run < end ? w0 + run : end;
-    for (int64_t p = w0 + lane; p < w1; p += 64) {
-        const int32_t e = chosen[p];
-        atomicAdd(&at[wave][e < 0 ? experts : e], 1u);
-    }
-    __syncthreads();
-    // bins in turns of 256: the place of each bin's first pair, then of each wave's
-    uint32_t before = 0;
-    for (int i0 = 0; i0 < bins; i0 += 256) {
-        const int i = i0 + threadIdx.x;
-        const uint32_t v = i < bins ? totals[i] : 0;
-        uint32_t sum;
-        const uint32_t start = before + block_incl_scan256(v, lds, &sum) - v;
-        before += sum;
-        if (i < bins) {
-            if (blockIdx.x == 0) offsets[i] = (int32_t)start;  // offsets[experts]: where the pairs without an expert begin
-            uint32_t place = start + counts[(int64_t)i * gridDim.x + blockIdx.x];
-#pragma unroll
-            for (int w = 0; w < 4; ++w) {
-                const uint32_t c = at[w][i];
-                at[w][i] = place;
-                place += c;
-            }
-        }
-    }
-    __syncthreads();
-    for (int64_t p0 = w0; p0 < w1; p0 += 64) {
-        const int64_t p = p0 + lane;
-        const bool on = p < w1;
-        const int32_t c = on ? chosen[p] : 0;
-        const uint32_t e = c < 0 ? experts : c;
-        const uint64_t same = match_digit(e, on, bits);
-        uint32_t place = 0;
-        if (on) place = at[wave][e] + __popcll(same & lanemask_lt());
-        // all lanes have read before the last of each expert moves its place on
-        __builtin_amdgcn_wave_barrier();
-        if (on && (same >> lane) == 1) at[wave][e] = place + 1;
-        __builtin_amdgcn_wave_barrier();
-        if (on) {
-            slots[p] = (int32_t)place;
-            rows[place] = (int32_t)(p / k);
-        }
-    }
+    const auto sum = [&](int bin, int blocks) {
+        uint32_t s = 0;
+#pragma unroll 8
+        for (int b = 0; b < blocks; ++b) s += counts[(int64_t)bin * gridDim.x + b];
+        return s;
+    };
+    place_pairs(chosen, first, end, k, experts, bits, at, lds,
+                [&](int bin) { return SCANNED ? counts[(int64_t)bin * gridDim.x + blockIdx.x] : sum(bin, blockIdx.x); },
+                [&](int bin) { return SCANNED ? totals[bin] : sum(bin, gridDim.x); }, offsets, rows, slots);
 }
 
 // dL/dscore of expert e: with d_j = dgate_j gate_j,  [e = expert j] d_j - p_e sum(d)  where p is the
-// softmax over the chosen experts or over all.
-template <typename T, int L, int CH>
+// softmax over the chosen experts or over all.  K: most experts of a row; their numbers, gates and
+// gradients are all loaded at once.
+template <typename T, int L, int CH, int K>
 __global__ __launch_bounds__(256) void k_route_bwd(const float *__restrict__ grad, const T *__restrict__ logits, int64_t ld, int64_t n,
                                                    int experts, int k, int normalize, const int32_t *__restrict__ chosen,
                                                    const float *__restrict__ gates, T *__restrict__ out, int64_t out_ld)
 {
     constexpr int V = VEC<T>, RPB = 256 / L;
     const int lane = threadIdx.x % L, g = threadIdx.x / L;
+    int nv[CH], e0[CH];
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+        const int e = (i * L + lane) * V;
+        nv[i] = experts - e < 0 ? 0 : (experts - e < V ? experts - e : V);
+        e0[i] = nv[i] ? e : 0;
+    }
     for (int64_t row0 = (int64_t)blockIdx.x * RPB; row0 < n; row0 += (int64_t)gridDim.x * RPB) {
         const int64_t row = row0 + g < n ? row0 + g : n - 1;
         const bool on = row0 + g < n;
-        float v[CH][V];
-        int nv[CH];
+        float v[CH][V], d[K], gate[K];
+        int32_t number[K];
+        Raw16 raw[CH];
 #pragma unroll
-        for (int i = 0; i < CH; ++i) {
-            const int e = (i * L + lane) * V;
-            nv[i] = experts - e < 0 ? 0 : (experts - e < V ? experts - e : V);
+        for (int i = 0; i < CH; ++i) raw[i] = normalize ? Raw16{0, 0, 0, 0} : load_raw(logits + row * ld + e0[i], nv[i]);
 #pragma unroll
-            for (int q = 0; q < V; ++q) v[i][q] = 0.0f;
-            if (!normalize) unpack(load_raw(logits + row * ld + (nv[i] ? e : 0), nv[i]), v[i], out);
+        for (int j = 0; j < K; ++j) {
+            const bool there = j < k;
+            const int64_t at = row * k + (there ? j : 0);
+            number[j] = there ? chosen[at] : -1;
+            gate[j] = gates[at];
+            d[j] = grad[at];
         }
         float sum = 0.0f;
-        for (int j = 0; j < k; ++j) sum += grad[row * k + j] * gates[row * k + j];
+#pragma unroll
+        for (int j = 0; j < K; ++j)
+            if (j < k) sum += d[j] * gate[j];
+#pragma unroll
+        for (int i = 0; i < CH; ++i) unpack(raw[i], v[i], out);
         if (!normalize) {
-            float top = -INFINITY, total = 0.0f;
+            float total = 0.0f;
+            uint32_t best = 0;
 #pragma unroll
             for (int i = 0; i < CH; ++i)
 #pragma unroll
-                for (int q = 0; q < V; ++q)
-                    if (q < nv[i]) top = fmaxf(top, v[i][q]);
-#pragma unroll
-            for (int o = 1; o < L; o <<= 1) top = fmaxf(top, __shfl_xor(top, o, 64));
-            const float from = top == -INFINITY ? 0.0f : top;
+                for (int q = 0; q < V; ++q) {
+                    const uint32_t key = q < nv[i] ? order_key(v[i][q]) : 0;
+                    best = best > key ? best : key;
+                }
+            best = lanes_max<L>(best);
+            const bool open = best > KEY_CLOSED;
+            const float from = open ? key_value(best) : 0.0f;
 #pragma unroll
             for (int i = 0; i < CH; ++i)
 #pragma unroll
@@ -235,78 +344,84 @@ __global__ __launch_bounds__(256) void k_route_bwd(const float *__restrict__ gra
                     total += v[i][q];
                 }
             total = lanes_sum<L>(total);
-            const float f = top == -INFINITY ? 0.0f : -sum / total;  // a row that is closed altogether has no gradient
+            const float f = open ? -sum / total : 0.0f;  // a row that is closed altogether has no gradient
 #pragma unroll
             for (int i = 0; i < CH; ++i)
 #pragma unroll
                 for (int q = 0; q < V; ++q) v[i][q] *= f;
         }
-        for (int j = 0; j < k; ++j) {
-            const int32_t e = chosen[row * k + j];
-            const float gate = gates[row * k + j];
-            const float d = gate * (normalize ? grad[row * k + j] - sum : grad[row * k + j]);
+#pragma unroll
+        for (int j = 0; j < K; ++j) {
+            if (j >= k) break;
+            const float t = gate[j] * (normalize ? d[j] - sum : d[j]);
+            const int at = number[j] - lane * V;  // in the lane's first piece
 #pragma unroll
             for (int i = 0; i < CH; ++i)
 #pragma unroll
                 for (int q = 0; q < V; ++q)
-                    if (e == (i * L + lane) * V + q) v[i][q] += d;
+                    if (at == i * L * V + q) v[i][q] += t;
         }
         if (on) {
 #pragma unroll
             for (int i = 0; i < CH; ++i)
-                if (nv[i]) store_raw(out + row * out_ld + (i * L + lane) * V, repack(v[i], out), nv[i]);
+                if (nv[i]) store_raw(out + row * out_ld + e0[i], repack(v[i], out), nv[i]);
         }
     }
 }
 
-// Lanes a row takes: a power of two with one or two pieces a lane.
-#define ROUTE_LANES(K, T, ...)                                                                  \
-    switch (lanes * 4 + ch) {                                                                   \
-    case 1 * 4 + 1: hipLaunchKernelGGL((K<T, 1, 1>), grid, dim3(256), 0, st, __VA_ARGS__); break; \
-    case 2 * 4 + 1: hipLaunchKernelGGL((K<T, 2, 1>), grid, dim3(256), 0, st, __VA_ARGS__); break; \
-    case 4 * 4 + 1: hipLaunchKernelGGL((K<T, 4, 1>), grid, dim3(256), 0, st, __VA_ARGS__); break; \
-    case 8 * 4 + 1: hipLaunchKernelGGL((K<T, 8, 1>), grid, dim3(256), 0, st, __VA_ARGS__); break; \
-    case 16 * 4 + 1: hipLaunchKernelGGL((K<T, 16, 1>), grid, dim3(256), 0, st, __VA_ARGS__); break; \
-    case 32 * 4 + 1: hipLaunchKernelGGL((K<T, 32, 1>), grid, dim3(256), 0, st, __VA_ARGS__); break; \
-    case 64 * 4 + 1: hipLaunchKernelGGL((K<T, 64, 1>), grid, dim3(256), 0, st, __VA_ARGS__); break; \
-    default:                                                                                    \
-        if constexpr (sizeof(T) == 4) hipLaunchKernelGGL((K<T, 64, 2>), grid, dim3(256), 0, st, __VA_ARGS__); \
-    }
-
-static void route_shape(int experts, int dtype, int *lanes, int *ch)
+// Lanes a row takes, a power of two: eight scores a lane (two pieces in fp32), which takes fewer steps across
+// lanes and as many in all as four (1.19M rows of 64 in fp32: see below).
+template <typename T> constexpr int ROUTE_CH = sizeof(T) == 4 ? 2 : 1;
+static int route_lanes(int experts)
 {
-    const int v = dtype == SUBMCONV_F32 ? 4 : 8, pieces = (experts + v - 1) / v;
-    *lanes = 1;
-    while (*lanes < pieces && *lanes < 64) *lanes *= 2;
-    *ch = pieces > 64 ? 2 : 1;
+    int lanes = 1;
+    while (lanes * 8 < experts) lanes *= 2;
+    return lanes;
 }
+#define ROUTE_LANES(GO, T)          \
+    switch (lanes) {                \
+    case 1: GO(T, 1); break;        \
+    case 2: GO(T, 2); break;        \
+    case 4: GO(T, 4); break;        \
+    case 8: GO(T, 8); break;        \
+    case 16: GO(T, 16); break;      \
+    case 32: GO(T, 32); break;      \
+    default: GO(T, 64);             \
+    }
+#define ROUTE_TYPES(GO) if (dtype == SUBMCONV_F32) { ROUTE_LANES(GO, float) } else { ROUTE_LANES(GO, uint16_t) }
 
 static int route_rows(int k) { return ROUTE_PAIRS / k; }
 static int64_t route_blocks(int64_t n, int k) { return (n + route_rows(k) - 1) / route_rows(k); }
 
 size_t route_workspace(int64_t n, int experts, int k)
 {
-    return n ? (size_t)(route_blocks(n, k) + 1) * (experts + 1) * sizeof(uint32_t) : 0;
+    const int64_t blocks = route_blocks(n, k);
+    return blocks > 1 ? (size_t)(blocks + 1) * (experts + 1) * sizeof(uint32_t) : 0;
 }
 
 int route(const void *logits, int64_t ld, int64_t n, int experts, int k, int dtype, int normalize, int32_t *chosen, float *gates,
           int32_t *offsets, int32_t *rows, int32_t *slots, void *workspace, hipStream_t st)
 {
-    int lanes, ch;
-    route_shape(experts, dtype, &lanes, &ch);
+    const int lanes = route_lanes(experts), bits = bits_for(experts + 1), per_block = route_rows(k);
     const int64_t blocks = route_blocks(n, k);
     uint32_t *counts = (uint32_t *)workspace, *totals = counts + blocks * (experts + 1);
-    const dim3 grid((unsigned)blocks);
-    if (dtype == SUBMCONV_F32) {
-        ROUTE_LANES(k_route_top, float, (const float *)logits, ld, n, experts, k, normalize, route_rows(k), chosen, gates, counts)
-    } else {
-        ROUTE_LANES(k_route_top, uint16_t, (const uint16_t *)logits, ld, n, experts, k, normalize, route_rows(k), chosen, gates, counts)
-    }
+#define TOP(T, L, ALONE)                                                                                                   \
+    hipLaunchKernelGGL((k_route_top<T, L, ROUTE_CH<T>, ALONE>), dim3((unsigned)blocks), dim3(256), 0, st, (const T *)logits, ld, n, experts, k, \
+                       normalize, per_block, bits, chosen, gates, counts, offsets, rows, slots)
+#define GO(T, L) if (blocks == 1) TOP(T, L, true); else TOP(T, L, false)
+    ROUTE_TYPES(GO)
+#undef GO
+#undef TOP
     SC_LAUNCHED("route");
-    hipLaunchKernelGGL(k_route_scan, dim3(experts + 1), dim3(256), 0, st, counts, (int)blocks, totals);
-    SC_LAUNCHED("route sums");
-    hipLaunchKernelGGL(k_route_place, grid, dim3(256), 0, st, chosen, n * k, k, experts, bits_for(experts + 1), route_rows(k) * k, counts,
-                       totals, offsets, rows, slots);
+    if (blocks == 1) return SUBMCONV_OK;
+    const bool scan = blocks > 64;
+    if (scan) {
+        hipLaunchKernelGGL(k_route_scan, dim3(experts + 1), dim3(256), 0, st, counts, (int)blocks, totals);
+        SC_LAUNCHED("route sums");
+    }
+    const dim3 grid((unsigned)blocks);
+    if (scan) hipLaunchKernelGGL(k_route_place<true>, grid, dim3(256), 0, st, chosen, n * k, k, experts, bits, per_block * k, counts, totals, offsets, rows, slots);
+    else hipLaunchKernelGGL(k_route_place<false>, grid, dim3(256), 0, st, chosen, n * k, k, experts, bits, per_block * k, counts, totals, offsets, rows, slots);
     SC_LAUNCHED("route places");
     return SUBMCONV_OK;
 }
@@ -326,15 +441,16 @@ int route_none(int32_t *offsets, int experts, hipStream_t st)
 int route_backward(const float *grad, const void *logits, int64_t ld, int64_t n, int experts, int k, int dtype, int normalize,
                    const int32_t *chosen, const float *gates, void *out, int64_t out_ld, hipStream_t st)
 {
-    int lanes, ch;
-    route_shape(experts, dtype, &lanes, &ch);
+    const int lanes = route_lanes(experts);
     const int64_t rpb = 256 / lanes, blocks = (n + rpb - 1) / rpb;
     const dim3 grid((unsigned)(blocks < 4096 ? blocks : 4096));
-    if (dtype == SUBMCONV_F32) {
-        ROUTE_LANES(k_route_bwd, float, grad, (const float *)logits, ld, n, experts, k, normalize, chosen, gates, (float *)out, out_ld)
-    } else {
-        ROUTE_LANES(k_route_bwd, uint16_t, grad, (const uint16_t *)logits, ld, n, experts, k, normalize, chosen, gates, (uint16_t *)out, out_ld)
-    }
+#define BACK(T, L, K)                                                                                                          \
+    hipLaunchKernelGGL((k_route_bwd<T, L, ROUTE_CH<T>, K>), grid, dim3(256), 0, st, grad, (const T *)logits, ld, n, experts, k, normalize, chosen, \
+                       gates, (T *)out, out_ld)
+#define GO(T, L) if (k <= 2) BACK(T, L, 2); else if (k <= 4) BACK(T, L, 4); else if (k <= 8) BACK(T, L, 8); else BACK(T, L, 16)
+    ROUTE_TYPES(GO)
+#undef GO
+#undef BACK
     SC_LAUNCHED("route_backward");
     return SUBMCONV_OK;
 }

@@ -66,14 +66,14 @@ def test_head_norm_backward_refusals(lib):
                  dict(dx=P(5))))
 
 
-def route(lib, logits=P(1), row=8, n=100, experts=8, k=2, dtype=0, normalize=1, chosen=P(2), gates=P(3), offsets=P(4), rows=P(5), slots=P(6),
+def route(lib, logits=P(1), row=8, n=5000, experts=8, k=2, dtype=0, normalize=1, chosen=P(2), gates=P(3), offsets=P(4), rows=P(5), slots=P(6),
           ws=P(7), nbytes=1 << 30):
     return lib.submconv_route(logits, row, n, experts, k, dtype, normalize, chosen, gates, offsets, rows, slots, ws, nbytes, None)
 
 
 def test_route_refusals(lib):
-    need = lib.submconv_route_workspace(100, 8, 2)
-    assert need > 0 and lib.submconv_route_workspace(0, 8, 2) == 0 and lib.submconv_route_workspace(10, 8, 9) == 0
+    need = lib.submconv_route_workspace(5000, 8, 2)
+    assert need > 0 and lib.submconv_route_workspace(0, 8, 2) == 0 and lib.submconv_route_workspace(100, 8, 2) == 0 and lib.submconv_route_workspace(10, 8, 9) == 0
     check(lambda **k: route(lib, **k),
           invalid=(dict(n=-1), dict(n=1 << 30), dict(logits=None), dict(chosen=None), dict(gates=None), dict(offsets=None), dict(rows=None),
                    dict(slots=None), dict(ws=None), dict(nbytes=need - 1), dict(normalize=2), dict(row=-1), dict(row=(1 << 24) + 1),
