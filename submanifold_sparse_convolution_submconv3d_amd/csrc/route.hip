@@ -33,6 +33,10 @@ __device__ __forceinline__ float key_value(uint32_t k)
     return __uint_as_float(k == 0xffffffffu ? 0x7fc00000u : (k >> 31 ? k ^ 0x80000000u : ~k));
 }
 
+// exp(d) for d <= 0, to a few roundings of d and of the result (the argument in units of log 2 is one
+// rounding of d, the instruction one of the result); below the smallest normal number it is 0.
+__device__ __forceinline__ float exp_of(float d) { return __builtin_amdgcn_exp2f(d * 1.4426950408889634f); }
+
 // Larger of the group's keys, in every lane of aligned groups of L lanes (a power of two).
 template <int CTRL>
 __device__ __forceinline__ uint32_t dpp_max(uint32_t v)
@@ -56,6 +60,13 @@ __device__ __forceinline__ uint32_t lanes_max(uint32_t v)
         v = r[0] > r[1] ? r[0] : r[1];
     }
     return v;
+}
+
+// What the wave's lanes wrote to LDS is read by the others from here on.
+__device__ __forceinline__ void wave_sync()
+{
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
 }
 
 // Where a block's pairs go.  A wave takes a run of `WAVE_PAIRS` of them, 64 at a time: they find their
@@ -90,9 +101,9 @@ __device__ __forceinline__ void place_pairs(const int32_t *chosen, int64_t first
         in_wave[c] = 0;
         if (on) in_wave[c] = at[wave][e[c]] + __popcll(same & lanemask_lt());
         // all lanes have read before the last of each expert moves its count on
-        __builtin_amdgcn_wave_barrier();
+        wave_sync();
         if (on && (same >> lane) == 1) at[wave][e[c]] = in_wave[c] + 1;
-        __builtin_amdgcn_wave_barrier();
+        wave_sync();
     }
     __syncthreads();
     uint32_t before = 0;
@@ -124,117 +135,136 @@ __device__ __forceinline__ void place_pairs(const int32_t *chosen, int64_t first
     }
 }
 
-// L lanes hold a row's scores, CH pieces of 16 bytes each, in order: the first piece of all lanes, then the
-// second.  Each round takes the largest key left; of equal ones the first in that order, which is the smallest
-// number: the first piece, then the first lane (a ballot), then the first element.
+// L lanes hold a row's scores, 16 neighbouring ones each.  A lane first sorts the K (>= k) best of its own,
+// one score after the other: with t_0 >= t_1 >= .. a score v makes t_j the median of t_{j-1}, t_j and v; only
+// a larger v goes before, so equal scores stay in order.  Then each round takes the largest of the lanes'
+// first ones, of equal ones the first lane's, and that lane moves its list up.  (All rounds over all scores
+// took twice the instructions, which are what bounds the kernel: 1,187,403 x 4 of 64 in fp32 175 us.)
 // ALONE: one block has all rows, and places the pairs too.
-template <typename T, int L, int CH, bool ALONE>
+template <typename T, int L, int K, bool ALONE>
 __global__ __launch_bounds__(256) void k_route_top(const T *__restrict__ logits, int64_t ld, int64_t n, int experts, int k,
                                                    int normalize, int rows_per_block, int bits, int32_t *chosen,
                                                    float *gates, uint32_t *counts, int32_t *offsets, int32_t *rows, int32_t *slots)
 {
-    constexpr int V = VEC<T>, RPB = 256 / L;
+    constexpr int V = VEC<T>, RPB = 256 / L, CH = 16 / V, MOST = K < 16 ? K : 16;
     __shared__ uint32_t hist[SUBMCONV_ROUTE_MAX_EXPERTS + 1];
     __shared__ uint32_t at[ALONE ? 4 : 1][SUBMCONV_ROUTE_MAX_EXPERTS + 1];
     __shared__ uint32_t lds[4];
-    constexpr int MOST = RPB * (8 * L < SUBMCONV_ROUTE_MAX_K ? 8 * L : SUBMCONV_ROUTE_MAX_K);  // k <= experts <= 8 L
-    __shared__ int32_t numbers[MOST];
-    __shared__ float values[MOST];
+    __shared__ int32_t numbers[RPB * K];
+    __shared__ uint32_t keys[RPB * K];
     for (int i = threadIdx.x; i <= experts; i += 256) hist[i] = 0;
     __syncthreads();
     const int lane = threadIdx.x % L, g = threadIdx.x / L;
     const uint64_t group = (L == 64 ? ~0ull : (1ull << L) - 1) << (lane_id() / L * L);  // of the wave's lanes
     const int64_t first = (int64_t)blockIdx.x * rows_per_block;
     const int64_t end = first + rows_per_block < n ? first + rows_per_block : n;
-    int nv[CH], e0[CH];
+    int nv[CH];
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
-        const int e = (i * L + lane) * V;
+        const int e = lane * 16 + i * V;
         nv[i] = experts - e < 0 ? 0 : (experts - e < V ? experts - e : V);
-        e0[i] = nv[i] ? e : 0;
     }
     Raw16 next[CH];
     const auto load = [&](int64_t row0) {
-        const int64_t row = row0 + g < end ? row0 + g : end - 1;
+        const T *from = logits + (row0 + g < end ? row0 + g : end - 1) * ld + lane * 16;
 #pragma unroll
-        for (int i = 0; i < CH; ++i) next[i] = load_raw(logits + row * ld + e0[i], nv[i]);
+        for (int i = 0; i < CH; ++i) next[i] = nv[i] ? load_raw(from + i * V, nv[i]) : Raw16{0, 0, 0, 0};
     };
     load(first);
     for (int64_t row0 = first; row0 < end; row0 += RPB) {
-        uint32_t key[CH][V];
+        uint32_t key[16], t[MOST];
+        int32_t at_[MOST];
 #pragma unroll
         for (int i = 0; i < CH; ++i) {
             float v[V];
             unpack(next[i], v, logits);
 #pragma unroll
-            for (int j = 0; j < V; ++j) key[i][j] = j < nv[i] ? order_key(v[j]) : 0;
+            for (int j = 0; j < V; ++j) key[i * V + j] = j < nv[i] ? order_key(v[j]) : 0;
         }
         if (row0 + RPB < end) load(row0 + RPB);
-        float top = 0.0f, total = 0.0f;
+#pragma unroll
+        for (int j = 0; j < MOST; ++j) {
+            t[j] = 0;
+            at_[j] = 0;
+        }
+#pragma unroll
+        for (int i = 0; i < CH; ++i) {
+            if (i * V >= experts) break;
+#pragma unroll
+            for (int e = i * V; e < (i + 1) * V; ++e) {
+                bool before[MOST];
+#pragma unroll
+                for (int j = 0; j < MOST; ++j) before[j] = key[e] > t[j];
+#pragma unroll
+                for (int j = MOST - 1; j >= 0; --j) {
+                    if (j > e) continue;  // so many are not sorted yet
+                    at_[j] = j > 0 && before[j > 0 ? j - 1 : 0] ? at_[j > 0 ? j - 1 : 0] : (before[j] ? lane * 16 + e : at_[j]);
+                    const uint32_t high = j > 0 ? t[j > 0 ? j - 1 : 0] : 0xffffffffu, low = t[j] > key[e] ? t[j] : key[e];
+                    t[j] = low < high ? low : high;  // (t_j <= t_{j-1})
+                }
+            }
+        }
+        float total = 0.0f;
+        if (!normalize) {
+            const uint32_t best = lanes_max<L>(t[0]);
+            const float top = best > KEY_CLOSED ? key_value(best) : 0.0f;
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                if (key[i] > KEY_CLOSED) total += exp_of(key_value(key[i]) - top);
+            total = lanes_sum<L>(total);
+        }
         for (int j = 0; j < k; ++j) {
-            uint32_t own[CH], best = 0;
-#pragma unroll
-            for (int i = 0; i < CH; ++i) {
-                own[i] = 0;
-#pragma unroll
-                for (int q = 0; q < V; ++q) own[i] = own[i] > key[i][q] ? own[i] : key[i][q];
-                best = best > own[i] ? best : own[i];
+            const uint32_t best = lanes_max<L>(t[0]);
+            bool mine = L == 1;
+            if constexpr (L > 1) {
+                const uint64_t with = __ballot(t[0] == best) & group;
+                mine = lane_id() == (unsigned)__builtin_ctzll(with);
             }
-            best = lanes_max<L>(best);
-            const bool there = best > KEY_CLOSED;
-            const float value = key_value(best);
-            if (j == 0) {
-                top = there ? value : 0.0f;
-                if (!normalize) {
+            if (mine) {
+                numbers[g * k + j] = best > KEY_CLOSED ? at_[0] : -1;
+                keys[g * k + j] = best;
 #pragma unroll
-                    for (int i = 0; i < CH; ++i)
-#pragma unroll
-                        for (int q = 0; q < V; ++q)
-                            if (key[i][q] > KEY_CLOSED) total += expf(key_value(key[i][q]) - top);
-                    total = lanes_sum<L>(total);
+                for (int i = 0; i + 1 < MOST; ++i) {
+                    t[i] = t[i + 1];
+                    at_[i] = at_[i + 1];
                 }
-            }
-            const float e = there ? expf(value - top) : 0.0f;
-            if (normalize) total += e;
-            if (!there) {  // the rest is closed
-                if (lane == 0) {
-                    numbers[g * k + j] = -1;
-                    values[g * k + j] = 0.0f;
-                }
-                continue;
-            }
-            bool taken = false;
-#pragma unroll
-            for (int i = 0; i < CH; ++i) {
-                const uint64_t with = __ballot(own[i] == best) & group;
-                if (!taken && with && lane_id() == (unsigned)__builtin_ctzll(with)) {
-                    bool open = true;
-#pragma unroll
-                    for (int q = 0; q < V; ++q)
-                        if (open && key[i][q] == best) {
-                            open = false;
-                            key[i][q] = 0;
-                            numbers[g * k + j] = (i * L + lane) * V + q;
-                            values[g * k + j] = e;
-                        }
-                }
-                taken = taken || with != 0;
+                t[MOST - 1] = 0;
             }
         }
         // The pairs of a wave's rows lie next to each other; no other wave sees its part of the LDS.
-        __builtin_amdgcn_wave_barrier();
+        wave_sync();
+        if (normalize) {
+            const uint32_t best = keys[g * k];
+            const float top = best > KEY_CLOSED ? key_value(best) : 0.0f;
+            for (int j = lane; j < k; j += L)
+                if (keys[g * k + j] > KEY_CLOSED) total += exp_of(key_value(keys[g * k + j]) - top);
+            total = lanes_sum<L>(total);
+        }
+        float gate[(K + L - 1) / L];
+#pragma unroll
+        for (int i = 0; i < (K + L - 1) / L; ++i) {
+            const int j = i * L + lane;
+            gate[i] = 0.0f;
+            if (j < k) {
+                const uint32_t own = keys[g * k + j], best = keys[g * k];
+                if (own > KEY_CLOSED) gate[i] = exp_of(key_value(own) - key_value(best)) / total;
+            }
+        }
+        wave_sync();
+#pragma unroll
+        for (int i = 0; i < (K + L - 1) / L; ++i)
+            if (i * L + lane < k) keys[g * k + i * L + lane] = __float_as_uint(gate[i]);
+        wave_sync();
         const int64_t w0 = row0 + (int64_t)(threadIdx.x >> 6) * (64 / L);
         const int64_t here = end - w0 < 64 / L ? end - w0 : 64 / L;
-        for (int j = lane; j < k; j += L) values[g * k + j] = total == 0.0f ? 0.0f : values[g * k + j] / total;
-        __builtin_amdgcn_wave_barrier();
         const int base = (int)(threadIdx.x >> 6) * (64 / L) * k;
         for (int i = (int)lane_id(); i < (int)here * k; i += 64) {
             const int32_t number = numbers[base + i];
             chosen[w0 * k + i] = number;
-            gates[w0 * k + i] = values[base + i];
+            gates[w0 * k + i] = __uint_as_float(keys[base + i]);
             atomicAdd(&hist[number < 0 ? experts : number], 1u);
         }
-        __builtin_amdgcn_wave_barrier();
+        wave_sync();
     }
     __syncthreads();
     if constexpr (ALONE) {
@@ -369,8 +399,7 @@ __global__ __launch_bounds__(256) void k_route_bwd(const float *__restrict__ gra
     }
 }
 
-// Lanes a row takes, a power of two: eight scores a lane (two pieces in fp32), which takes fewer steps across
-// lanes and as many in all as four (1.19M rows of 64 in fp32: see below).
+// Lanes a row takes in the backward pass, a power of two: eight scores a lane (two pieces in fp32).
 template <typename T> constexpr int ROUTE_CH = sizeof(T) == 4 ? 2 : 1;
 static int route_lanes(int experts)
 {
@@ -402,15 +431,26 @@ size_t route_workspace(int64_t n, int experts, int k)
 int route(const void *logits, int64_t ld, int64_t n, int experts, int k, int dtype, int normalize, int32_t *chosen, float *gates,
           int32_t *offsets, int32_t *rows, int32_t *slots, void *workspace, hipStream_t st)
 {
-    const int lanes = route_lanes(experts), bits = bits_for(experts + 1), per_block = route_rows(k);
+    const int bits = bits_for(experts + 1), per_block = route_rows(k);
+    int top_lanes = 1;
+    while (top_lanes * 16 < experts) top_lanes *= 2;
     const int64_t blocks = route_blocks(n, k);
     uint32_t *counts = (uint32_t *)workspace, *totals = counts + blocks * (experts + 1);
-#define TOP(T, L, ALONE)                                                                                                   \
-    hipLaunchKernelGGL((k_route_top<T, L, ROUTE_CH<T>, ALONE>), dim3((unsigned)blocks), dim3(256), 0, st, (const T *)logits, ld, n, experts, k, \
+#define TOP(T, L, K, ALONE)                                                                                                \
+    hipLaunchKernelGGL((k_route_top<T, L, K, ALONE>), dim3((unsigned)blocks), dim3(256), 0, st, (const T *)logits, ld, n, experts, k, \
                        normalize, per_block, bits, chosen, gates, counts, offsets, rows, slots)
-#define GO(T, L) if (blocks == 1) TOP(T, L, true); else TOP(T, L, false)
-    ROUTE_TYPES(GO)
+#define ALL(T, L, K) if (blocks == 1) TOP(T, L, K, true); else TOP(T, L, K, false)
+#define GO(T, L) if (k <= 2) { ALL(T, L, 2); } else if (k <= 4) { ALL(T, L, 4); } else if (k <= 8) { ALL(T, L, 8); } else { ALL(T, L, 16); }
+    switch (top_lanes) {
+    case 1: if (dtype == SUBMCONV_F32) { GO(float, 1) } else { GO(uint16_t, 1) } break;
+    case 2: if (dtype == SUBMCONV_F32) { GO(float, 2) } else { GO(uint16_t, 2) } break;
+    case 4: if (dtype == SUBMCONV_F32) { GO(float, 4) } else { GO(uint16_t, 4) } break;
+    case 8: if (dtype == SUBMCONV_F32) { GO(float, 8) } else { GO(uint16_t, 8) } break;
+    case 16: if (dtype == SUBMCONV_F32) { GO(float, 16) } else { GO(uint16_t, 16) } break;
+    default: if (dtype == SUBMCONV_F32) { GO(float, 32) } else { GO(uint16_t, 32) }
+    }
 #undef GO
+#undef ALL
 #undef TOP
     SC_LAUNCHED("route");
     if (blocks == 1) return SUBMCONV_OK;
