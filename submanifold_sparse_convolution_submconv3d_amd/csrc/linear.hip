@@ -235,6 +235,75 @@ __global__ __launch_bounds__(256) void k_linear(LinearArgs A)
     }
 }
 
+// y for few rows a group (single tokens): bound by reading each weight once.  A block takes 16 positions and
+// 16 NB columns; its four waves take a quarter of each run of k, with all their loads in flight, straight
+// into the matrix instruction's operands (16 x 16, columns of y in the rows), and their sums are added in LDS.
+template <typename T, int NB>
+__global__ __launch_bounds__(256) void k_linear_few(LinearArgs A, int steps)
+{
+    constexpr int V = VEC<T>, KS = 4 * V, STEPS = 8;  // k of a step; most steps of a wave at a time
+    __shared__ f32x4 part_sum[4][NB][64];
+    const uint32_t cols = (A.cout + 16 * NB - 1) / (16 * NB), tile = blockIdx.x / cols;
+    const int n0 = (int)(blockIdx.x - tile * cols) * 16 * NB, wave = threadIdx.x >> 6, l = (int)lane_id() & 15, q = (int)lane_id() >> 4;
+    Part part;
+    if (!find_tile(A, 16, tile, &part)) return;
+    const bool real = part.index >= 1 && part.index <= A.groups;
+    const int group = real ? part.index - 1 : 0, k_end = real ? A.cin : 0;
+    const int p = part.beg + (int)part.tile * 16 + l;
+    const T *w = (const T *)A.w + (int64_t)group * A.cout * A.cin, *wr[NB];
+#pragma unroll
+    for (int b = 0; b < NB; ++b) wr[b] = w + (int64_t)(n0 + 16 * b + l < A.cout ? n0 + 16 * b + l : A.cout - 1) * A.cin;
+    int row = -1;
+    if (p < part.end) row = A.rows ? A.rows[p] : p;
+    const T *x = row >= 0 && row < A.nx ? (const T *)A.x + (int64_t)row * A.x_row : nullptr;
+    f32x4 acc[NB];
+#pragma unroll
+    for (int b = 0; b < NB; ++b) acc[b] = f32x4{0, 0, 0, 0};
+    for (int k0 = wave * steps * KS; k0 < k_end; k0 += 4 * steps * KS) {
+        Raw16 wv[STEPS][NB], xv[STEPS];
+#pragma unroll
+        for (int s = 0; s < STEPS; ++s) {
+            if (s >= steps) break;
+            const int k = k0 + s * KS + q * V, nv = k_end - k < 0 ? 0 : (k_end - k < V ? k_end - k : V);
+#pragma unroll
+            for (int b = 0; b < NB; ++b) wv[s][b] = load_raw(wr[b] + (nv ? k : 0), nv);
+            xv[s] = x ? load_raw(x + (nv ? k : 0), nv) : Raw16{0, 0, 0, 0};
+        }
+#pragma unroll
+        for (int s = 0; s < STEPS; ++s) {
+            if (s >= steps) break;
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+                if constexpr (sizeof(T) == 2) {
+                    acc[b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, wv[s][b]), __builtin_bit_cast(bf16x8, xv[s]), acc[b], 0, 0, 0);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        acc[b] = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(wv[s][b][i]), __uint_as_float(xv[s][i]), acc[b], 0, 0, 0);
+                }
+            }
+        }
+    }
+#pragma unroll
+    for (int b = 0; b < NB; ++b) part_sum[wave][b][lane_id()] = acc[b];
+    __syncthreads();
+    // a lane has position l % 16 and columns 4 (l / 16) .. + 3 of a block
+    if (wave >= NB || p >= part.end) return;
+    const f32x4 sum = (part_sum[0][wave][lane_id()] + part_sum[1][wave][lane_id()]) + (part_sum[2][wave][lane_id()] + part_sum[3][wave][lane_id()]);
+    const int e = n0 + 16 * wave + 4 * q, have = A.cout - e;
+    if (have <= 0) return;
+    float v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = sum[i] + (A.bias && real && i < have ? A.bias[(int64_t)group * A.cout + e + i] : 0.0f);
+    T *to = (T *)A.out + (int64_t)p * A.out_row + e;
+    if constexpr (sizeof(T) == 4) {
+        store_raw(to, repack(v, to), have < 4 ? have : 4);
+    } else {
+        const float eight[8] = {v[0], v[1], v[2], v[3], 0, 0, 0, 0};
+        store_raw(to, repack(eight, to), have < 4 ? have : 4);
+    }
+}
+
 // Sums of the pieces of each group, in order, rounded once; a block is 256 elements of a group's dw (and db).
 template <typename T>
 __global__ __launch_bounds__(256) void k_linear_join(LinearArgs A)
@@ -304,6 +373,14 @@ static bool takes_big(const LinearArgs &A, int dtype, int kind)
     return kind == LINEAR_DW || A.n / A.groups >= 128;
 }
 
+constexpr int64_t FEW_BLOCKS = 2048;
+// Whether the kernel for few rows takes a call.
+static bool takes_few(const LinearArgs &A)
+{
+    const int64_t blocks = most_tiles(A.n, A.groups, 16) * ((A.cout + 31) / 32);
+    return blocks < 1 << 23 && (A.n <= 16 * (int64_t)A.groups || blocks <= FEW_BLOCKS);
+}
+
 int grouped_linear(LinearArgs A, int dtype, int kind, void *workspace, hipStream_t st)
 {
     const bool big = takes_big(A, dtype, kind);
@@ -312,7 +389,14 @@ int grouped_linear(LinearArgs A, int dtype, int kind, void *workspace, hipStream
         A.part = (float *)workspace;
         A.db_part = A.part + (A.chunk ? most_tiles(A.n, A.groups, A.chunk) * A.cout * A.cin : 0);
     }
-    if (big) {
+    if (kind == LINEAR_Y && takes_few(A)) {
+        constexpr int NB = 2;
+        const int ks = dtype == SUBMCONV_F32 ? 16 : 32, quarter = (A.cin + 4 * ks - 1) / (4 * ks), steps = quarter < 8 ? quarter : 8;
+        const dim3 grid((unsigned)(most_tiles(A.n, A.groups, 16) * ((A.cout + 16 * NB - 1) / (16 * NB))));
+        if (dtype == SUBMCONV_F32) hipLaunchKernelGGL((k_linear_few<float, NB>), grid, dim3(256), 0, st, A, steps);
+        else hipLaunchKernelGGL((k_linear_few<uint16_t, NB>), grid, dim3(256), 0, st, A, steps);
+        SC_LAUNCHED("grouped_linear");
+    } else if (big) {
         SC_CHECK(grouped_linear_big(A, kind, st));
     } else {
         const dim3 grid((unsigned)linear_tiles(A.n, A.groups, A.cin, A.cout, kind, A.chunk, LT));
