@@ -1213,8 +1213,8 @@ static int linear_check(int32_t groups, int64_t n, int64_t nx, int32_t cin, int3
     if (groups < 1 || groups > MAX_GROUPS) return fail(SUBMCONV_E_INVALID_ARG, "groups = %d outside 1..%d", groups, MAX_GROUPS);
     if ((int64_t)groups * cin * cout >= int64_t(1) << 40) return fail(SUBMCONV_E_UNSUPPORTED, "groups cin cout reaches 2^40");
     for (int kind = LINEAR_Y; kind <= LINEAR_DW; ++kind)
-        if ((kind == LINEAR_Y ? forward : (kind == LINEAR_DX ? dx : dw)) && linear_blocks(n, groups, cin, cout, kind) >= 1 << 24)
-            return fail(SUBMCONV_E_UNSUPPORTED, "%lld tiles are more than one launch holds", (long long)linear_blocks(n, groups, cin, cout, kind));
+        if ((kind == LINEAR_Y ? forward : (kind == LINEAR_DX ? dx : dw)) && linear_blocks(n, groups, cin, cout, dtype, kind) >= 1 << 24)
+            return fail(SUBMCONV_E_UNSUPPORTED, "%lld tiles are more than one launch holds", (long long)linear_blocks(n, groups, cin, cout, dtype, kind));
     return SUBMCONV_OK;
 }
 

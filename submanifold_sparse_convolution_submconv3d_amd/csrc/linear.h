@@ -146,7 +146,7 @@ static inline int64_t linear_big_tiles(int64_t n, int groups, int cin, int cout,
 }
 
 // Blocks of a call's largest launch; a launch holds 2^24 of them.
-int64_t linear_blocks(int64_t n, int groups, int cin, int cout, int kind);
+int64_t linear_blocks(int64_t n, int groups, int cin, int cout, int dtype, int kind);
 int grouped_linear(LinearArgs A, int dtype, int kind, void *workspace, hipStream_t st);
 int grouped_linear_big(const LinearArgs &A, int kind, hipStream_t st);
 size_t linear_dw_workspace(int64_t n, int groups, int cin, int cout, int dtype);

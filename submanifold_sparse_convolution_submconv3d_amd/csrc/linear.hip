@@ -18,52 +18,57 @@
 
 namespace sc {
 
-constexpr int LT = 128;            // rows of either side in a tile
-constexpr int LBYTES = 64 * LT;    // bytes of one side's tile for a step of 64 / sizeof(T) along k
+// Tiles of 64 B rows of either side, in steps of KB bytes along k: 64 x 64 in steps of 128 bytes, 128 x 128 in
+// steps of 64.  A thread has two pieces of 16 bytes of each side's tile.
+template <typename T, int B>
+struct TileShape {
+    static constexpr int LT = 64 * B, KB = 128 / B, KT = KB / (int)sizeof(T), BYTES = LT * KB;
+};
 
-// One side's tile in LDS.  Along k (KS false): rows of 64 bytes, their 16-byte pieces permuted so
-// that 8 rows read at one piece fall on different banks.  Across k (KS true): 64 / sizeof(T)
-// rows of LT elements; bf16 pieces are permuted for the transposing read, as in attention's tiles.
-template <typename T, bool KS>
+// One side's tile in LDS.  Along k (KS false): rows of KB bytes.  Across k (KS true): KT rows of LT
+// elements.  Pieces are permuted as in attention's tiles, but for fp32 across k, which is read by elements.
+template <typename T, int B, bool KS>
 __device__ __forceinline__ uint32_t tile_at(uint32_t row, uint32_t piece)
 {
-    if constexpr (!KS) return row * 64 + ((piece ^ ((row >> 1) & 3)) << 4);
-    else if constexpr (sizeof(T) == 2) return piece_at<256>(row, piece);
-    else return row * 512 + piece * 16;
+    using S = TileShape<T, B>;
+    if constexpr (!KS) return piece_at<S::KB>(row, piece);
+    else if constexpr (sizeof(T) == 2) return piece_at<S::LT * 2>(row, piece);
+    else return row * (S::LT * 4) + piece * 16;
 }
 
-// A lane's operand of a product of 32 rows from `block` on: its share of k step j (half of the tile's k).
-template <typename T, bool KS>
+// A lane's operand of a product of 32 rows from `block` on: its share of 32 bytes of k, number j of the step.
+template <typename T, int B, bool KS>
 __device__ __forceinline__ Raw16 tile_operand(uint32_t lds, int block, int j)
 {
     const uint32_t l = lane_id(), a = l >> 5;
     if constexpr (!KS) {
-        return lds_read16(lds + tile_at<T, KS>(block + (l & 31), 2 * j + a));
+        return lds_read16(lds + tile_at<T, B, KS>(block + (l & 31), 2 * j + a));
     } else if constexpr (sizeof(T) == 2) {
         // rows 16 j + 8 a + 4 h .. + 3 of k, transposed: lane t of 16 gets element t
         const uint32_t g = (l >> 4) & 1, t = l & 15, k = 16 * j + 8 * a + t / 4, piece = block / 8 + g * 2 + (t & 3) / 2;
-        const u32x2 lo = lds_read_tr(lds + tile_at<T, KS>(k, piece) + (t & 1) * 8);
-        const u32x2 hi = lds_read_tr(lds + tile_at<T, KS>(k + 4, piece) + (t & 1) * 8);
+        const u32x2 lo = lds_read_tr(lds + tile_at<T, B, KS>(k, piece) + (t & 1) * 8);
+        const u32x2 hi = lds_read_tr(lds + tile_at<T, B, KS>(k + 4, piece) + (t & 1) * 8);
         return Raw16{lo[0], lo[1], hi[0], hi[1]};
     } else {
         Raw16 r;
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            r[i] = *(const SC_LDS uint32_t *)(uintptr_t)(lds + (4 * (2 * j + a) + i) * 512 + (block + (l & 31)) * 4);
+            r[i] = *(const SC_LDS uint32_t *)(uintptr_t)(lds + (4 * (2 * j + a) + i) * (TileShape<T, B>::LT * 4) + (block + (l & 31)) * 4);
         return r;
     }
 }
 
-// Any widths, row distances and alignment: pieces of 16 bytes are loaded into registers with what
-// is missing at the ends of rows as zeros, written to LDS, and the next step's loads are in flight
-// meanwhile.  Four waves, each 64 x 64 of the tile.
+// Any widths, row distances and alignment: pieces of 16 bytes are loaded into registers, with what
+// is missing at the ends of rows as zeros, a step or two ahead, and written to LDS.  Four waves, each a quarter
+// of the tile.
 // PART (LINEAR_DW): pieces of groups, whose sums are kept in fp32 for k_linear_join.
-template <typename T, int KIND, bool PART>
+template <typename T, int KIND, bool PART, int B>
 __global__ __launch_bounds__(256) void k_linear(LinearArgs A)
 {
-    constexpr int V = VEC<T>, KT = 64 / (int)sizeof(T);
+    using S = TileShape<T, B>;
+    constexpr int V = VEC<T>, KT = S::KT, LT = S::LT, BYTES = S::BYTES;
     constexpr bool AKS = KIND == LINEAR_DW, BKS = KIND != LINEAR_Y;
-    __shared__ __attribute__((aligned(16))) char smem[4 * LBYTES];
+    __shared__ __attribute__((aligned(16))) char smem[4 * BYTES];
     const uint32_t lds = (uint32_t)(uintptr_t)(SC_LDS char *)smem;
     const int wave = threadIdx.x >> 6;
     Part part;
@@ -102,8 +107,8 @@ __global__ __launch_bounds__(256) void k_linear(LinearArgs A)
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
             const bool ks = s ? BKS : AKS;
-            r_[s][i] = ks ? at / (LT / V) : at / 4;
-            c_[s][i] = (ks ? at % (LT / V) : at % 4) * V;
+            r_[s][i] = ks ? at / (LT / V) : at / (S::KB / 16);
+            c_[s][i] = (ks ? at % (LT / V) : at % (S::KB / 16)) * V;
         }
         if constexpr (!AKS) {
             const int p = m0 + r_[0][i];
@@ -120,8 +125,9 @@ __global__ __launch_bounds__(256) void k_linear(LinearArgs A)
         if constexpr (!BKS) b_row[i] = n0 + r_[1][i] < n_end ? w + (int64_t)(n0 + r_[1][i]) * A.cin : nullptr;
     }
     const auto left = [](int have) { return have < 0 ? 0 : (have < V ? have : V); };
-    Raw16 av[2], bv[2];
-    const auto load = [&](int k0) {
+    constexpr int AHEAD = B == 1 ? 2 : 1;  // steps that loads run ahead (more registers cost the large tiles a block a compute unit)
+    Raw16 av_[AHEAD][2], bv_[AHEAD][2];
+    const auto load = [&](int k0, Raw16 (&av)[2], Raw16 (&bv)[2]) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             av[i] = bv[i] = Raw16{0, 0, 0, 0};
@@ -148,38 +154,41 @@ __global__ __launch_bounds__(256) void k_linear(LinearArgs A)
             }
         }
     };
-    f32x16 acc[2][2];
+    f32x16 acc[B][B];
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int i = 0; i < B; ++i)
 #pragma unroll
-        for (int e = 0; e < 16; ++e) acc[i][0][e] = acc[i][1][e] = 0.0f;
-    const int wm = (wave & 1) * 64, wn = (wave >> 1) * 64;
-    float sums[2] = {0.0f, 0.0f};  // db: of a lane's share of its rows of grad
+        for (int n = 0; n < B; ++n)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) acc[i][n][e] = 0.0f;
+    const int wm = (wave & 1) * (32 * B), wn = (wave >> 1) * (32 * B);
+    float sums[B];  // db: of a lane's share of its rows of grad
+#pragma unroll
+    for (int i = 0; i < B; ++i) sums[i] = 0.0f;
     const bool summing = KIND == LINEAR_DW && A.db && n0 == 0 && wn == 0;
-    load(0);
-    for (int k0 = 0, buf = 0; k0 < k_end; k0 += KT, buf ^= 2 * LBYTES) {
+    const auto step = [&](int k0, int buf, Raw16 (&av)[2], Raw16 (&bv)[2]) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            lds_write16(lds + buf + tile_at<T, AKS>(r_[0][i], c_[0][i] / V), av[i]);
-            lds_write16(lds + buf + LBYTES + tile_at<T, BKS>(r_[1][i], c_[1][i] / V), bv[i]);
+            lds_write16(lds + buf + tile_at<T, B, AKS>(r_[0][i], c_[0][i] / V), av[i]);
+            lds_write16(lds + buf + BYTES + tile_at<T, B, BKS>(r_[1][i], c_[1][i] / V), bv[i]);
         }
         __syncthreads();
-        if (k0 + KT < k_end) load(k0 + KT);
+        if (k0 + AHEAD * KT < k_end) load(k0 + AHEAD * KT, av, bv);
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            Raw16 a[2], b[2];
+        for (int j = 0; j < S::KB / 32; ++j) {
+            Raw16 a[B], b[B];
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                a[i] = tile_operand<T, AKS>(lds + buf, wm + 32 * i, j);
-                b[i] = tile_operand<T, BKS>(lds + buf + LBYTES, wn + 32 * i, j);
+            for (int i = 0; i < B; ++i) {
+                a[i] = tile_operand<T, B, AKS>(lds + buf, wm + 32 * i, j);
+                b[i] = tile_operand<T, B, BKS>(lds + buf + BYTES, wn + 32 * i, j);
             }
 #pragma unroll
-            for (int m = 0; m < 2; ++m)
+            for (int m = 0; m < B; ++m)
 #pragma unroll
-                for (int n = 0; n < 2; ++n) acc[m][n] = mma_pieces<T>(b[n], a[m], acc[m][n]);
+                for (int n = 0; n < B; ++n) acc[m][n] = mma_pieces<T>(b[n], a[m], acc[m][n]);
             if (summing) {
 #pragma unroll
-                for (int m = 0; m < 2; ++m) {
+                for (int m = 0; m < B; ++m) {
                     float v[V], t = 0.0f;
                     unpack(a[m], v, (const T *)nullptr);
 #pragma unroll
@@ -188,6 +197,16 @@ __global__ __launch_bounds__(256) void k_linear(LinearArgs A)
                 }
             }
         }
+    };
+    load(0, av_[0], bv_[0]);
+    if constexpr (AHEAD == 2) {
+        load(KT, av_[1], bv_[1]);
+        for (int k0 = 0; k0 < k_end; k0 += 2 * KT) {
+            step(k0, 0, av_[0], bv_[0]);
+            if (k0 + KT < k_end) step(k0 + KT, 2 * BYTES, av_[1], bv_[1]);
+        }
+    } else {
+        for (int k0 = 0, buf = 0; k0 < k_end; k0 += KT, buf ^= 2 * BYTES) step(k0, buf, av_[0], bv_[0]);
     }
     // a lane has row l % 32 of each block, its elements in the registers
     const int l = lane_id() & 31;
@@ -197,7 +216,7 @@ __global__ __launch_bounds__(256) void k_linear(LinearArgs A)
     const int64_t block = PART ? other / ((A.cout + LT - 1) / LT) : group;  // of dw
     if constexpr (KIND == LINEAR_DW) out += block * A.cout * A.cin;
 #pragma unroll
-    for (int m = 0; m < 2; ++m) {
+    for (int m = 0; m < B; ++m) {
         const int row = m0 + wm + 32 * m + l;
         const bool valid = row < m_end;
         if (summing) {
@@ -205,7 +224,7 @@ __global__ __launch_bounds__(256) void k_linear(LinearArgs A)
             if (valid && lane_id() < 32) (PART ? A.db_part : A.db)[block * A.cout + row] = sum;
         }
 #pragma unroll
-        for (int n = 0; n < 2; ++n)
+        for (int n = 0; n < B; ++n)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {  // registers 8h .. 8h + 3 and 8h + 4 .. 8h + 7: 8 elements in a row after the halves' exchange
                 float v[8];
@@ -324,13 +343,26 @@ __global__ __launch_bounds__(256) void k_linear_join(LinearArgs A)
     else ((T *)A.out)[group * size + i] = Elem<T>::from_f32(sum);
 }
 
+// The rules below were measured over 1 to 8 groups of 1 to 8192 rows, widths of 64 to 4096, in us:
+//   few rows (16 a tile) against tiles of 64, 8 groups 1024 -> 1024 bf16: 32 rows each 11.8 and 16.9, 64 16.5 and
+//   20.1, 128 27 and 18.4; fp32 64 rows 33 and 45, 128 63 and 47.
+//   Tiles of 64 against 256, bf16: 8 x 512 x 1024 -> 1024 25 and 30, 8 x 2048 88 and 41; 8192 x 1024 -> 1024 48 and 33.
+//   Tiles of 64 against 128, fp32: 8 x 512 x 1024 -> 1024 95 and 117, 8 x 2048 349 and 303.
+//   dw, tiles of 64, 128 and 256, bf16: 8 x 128 x 1024 x 1024 15, 13 and 16, 8 x 256 23, 21 and 20; 8 x 2048 x 256 x 1024 52, 56 and 43.
+constexpr int64_t FEW_ROWS = 16, FEW_BLOCKS = 1024, SMALL_TILES = 768, BIG_OUT = 1 << 23;
+constexpr double BIG_DW = 2e9, LARGE_DW = 4e9;
+
+// Which kernel takes a call.
+enum { BY_FEW, BY_SMALL, BY_LARGE, BY_BIG };
+constexpr int TILE_OF[] = {16, 64, 128, BIG_TILE};
+
 // Positions of a piece of dw: whole groups (0) where these are blocks enough, else so many
 // that the blocks of all pieces fill the card some times over.  A piece's sums are written and read again in
 // fp32, so pieces are not shorter than 256 positions.
-static int dw_chunk(int64_t n, int groups, int cin, int cout, bool big)
+static int dw_chunk(int64_t n, int groups, int cin, int cout, int by)
 {
-    const int size = big ? BIG_TILE : LT;
-    const int64_t tiles = (int64_t)((cin + size - 1) / size) * ((cout + size - 1) / size), want = big ? UNITS : 4 * UNITS;
+    const int size = TILE_OF[by];
+    const int64_t tiles = (int64_t)((cin + size - 1) / size) * ((cout + size - 1) / size), want = UNITS * (by == BY_BIG ? 1 : (by == BY_LARGE ? 4 : 16));
     if (groups * tiles >= want / 2 || n < 512) return 0;
     const int64_t pieces = (want + tiles - 1) / tiles;
     int64_t chunk = (n + pieces - 1) / pieces;
@@ -338,75 +370,79 @@ static int dw_chunk(int64_t n, int groups, int cin, int cout, bool big)
     return (int)(chunk < 256 ? 256 : chunk);
 }
 
-// Whether the large tiles may take a call of these widths.
-static bool wide_enough(int cin, int cout, int dtype, int kind)
+// Whether the large tiles may take a call of these widths, if pointers and distances are aligned.
+static bool may_be_big(int cin, int cout, int dtype) { return dtype == SUBMCONV_BF16 && cin % 8 == 0 && cout % 8 == 0; }
+
+// The kernel by sizes alone; `aligned`: whole pieces of 16 bytes everywhere.
+static int choose(int64_t n, int groups, int cin, int cout, int dtype, int kind, bool aligned)
 {
-    return dtype == SUBMCONV_BF16 && cin % 8 == 0 && cout % 8 == 0 && (kind == LINEAR_Y ? cout : cin) >= 192 && (kind != LINEAR_DW || cout >= 192);
+    const int cols = kind == LINEAR_Y ? cout : cin;
+    if (kind == LINEAR_Y) {
+        const int64_t few = most_tiles(n, groups, 16) * ((cout + 31) / 32);
+        if (n <= FEW_ROWS * (int64_t)groups || few <= (dtype == SUBMCONV_F32 ? 2 : 1) * FEW_BLOCKS) return BY_FEW;
+    }
+    if (aligned && may_be_big(cin, cout, dtype) && cols >= 192) {
+        if (kind == LINEAR_DW ? cout >= 192 && (double)n * cin * cout >= BIG_DW : n * cols >= BIG_OUT) return BY_BIG;
+    }
+    if (kind == LINEAR_DW) return (double)n * cin * cout >= LARGE_DW || linear_tiles(n, groups, cin, cout, kind, 0, 128) >= SMALL_TILES ? BY_LARGE : BY_SMALL;
+    return linear_tiles(n, groups, cin, cout, kind, 0, 128) >= SMALL_TILES ? BY_LARGE : BY_SMALL;
 }
 
 size_t linear_dw_workspace(int64_t n, int groups, int cin, int cout, int dtype)
 {
     int64_t pieces = 0;
-    for (int big = 0; big < 2; ++big) {
-        if (big && !wide_enough(cin, cout, dtype, LINEAR_DW)) continue;
-        const int chunk = dw_chunk(n, groups, cin, cout, big);
+    for (int aligned = 0; aligned < 2; ++aligned) {
+        const int chunk = dw_chunk(n, groups, cin, cout, choose(n, groups, cin, cout, dtype, LINEAR_DW, aligned));
         const int64_t p = chunk ? most_tiles(n, groups, chunk) : 0;
         pieces = p > pieces ? p : pieces;
     }
     return (size_t)pieces * cout * ((size_t)cin + 1) * sizeof(float);
 }
 
-int64_t linear_blocks(int64_t n, int groups, int cin, int cout, int kind)
+// Blocks of a call whose tensors are not aligned (aligned ones take as many or fewer).
+int64_t linear_blocks(int64_t n, int groups, int cin, int cout, int dtype, int kind)
 {
-    return linear_tiles(n, groups, cin, cout, kind, kind == LINEAR_DW ? dw_chunk(n, groups, cin, cout, false) : 0, LT);
+    const int by = choose(n, groups, cin, cout, dtype, kind, false);
+    if (by == BY_FEW) return most_tiles(n, groups, 16) * ((cout + 31) / 32);
+    return linear_tiles(n, groups, cin, cout, kind, kind == LINEAR_DW ? dw_chunk(n, groups, cin, cout, by) : 0, TILE_OF[by]);
 }
 
-// Whether the large tiles take a call: bf16, whole pieces of 16 bytes everywhere, and both sides long
-// enough.
-static bool takes_big(const LinearArgs &A, int dtype, int kind)
+static bool is_aligned(const LinearArgs &A, int kind)
 {
-    if (!wide_enough(A.cin, A.cout, dtype, kind)) return false;
     const auto pieces = [](const void *p, int64_t row) { return ((uintptr_t)p & 15) == 0 && row % 8 == 0; };
     if (kind != LINEAR_DX && !pieces(A.x, A.x_row)) return false;
     if (kind != LINEAR_Y && !pieces(A.g, A.g_row)) return false;
-    if (kind != LINEAR_DW && !pieces(A.w, 0)) return false;
-    return kind == LINEAR_DW || A.n / A.groups >= 128;
-}
-
-constexpr int64_t FEW_BLOCKS = 2048;
-// Whether the kernel for few rows takes a call.
-static bool takes_few(const LinearArgs &A)
-{
-    const int64_t blocks = most_tiles(A.n, A.groups, 16) * ((A.cout + 31) / 32);
-    return blocks < 1 << 23 && (A.n <= 16 * (int64_t)A.groups || blocks <= FEW_BLOCKS);
+    return kind == LINEAR_DW || pieces(A.w, 0);
 }
 
 int grouped_linear(LinearArgs A, int dtype, int kind, void *workspace, hipStream_t st)
 {
-    const bool big = takes_big(A, dtype, kind);
+    const int by = choose(A.n, A.groups, A.cin, A.cout, dtype, kind, is_aligned(A, kind));
     if (kind == LINEAR_DW) {
-        A.chunk = dw_chunk(A.n, A.groups, A.cin, A.cout, big);
+        A.chunk = dw_chunk(A.n, A.groups, A.cin, A.cout, by);
         A.part = (float *)workspace;
         A.db_part = A.part + (A.chunk ? most_tiles(A.n, A.groups, A.chunk) * A.cout * A.cin : 0);
     }
-    if (kind == LINEAR_Y && takes_few(A)) {
+    if (by == BY_FEW) {
         constexpr int NB = 2;
         const int ks = dtype == SUBMCONV_F32 ? 16 : 32, quarter = (A.cin + 4 * ks - 1) / (4 * ks), steps = quarter < 8 ? quarter : 8;
         const dim3 grid((unsigned)(most_tiles(A.n, A.groups, 16) * ((A.cout + 16 * NB - 1) / (16 * NB))));
         if (dtype == SUBMCONV_F32) hipLaunchKernelGGL((k_linear_few<float, NB>), grid, dim3(256), 0, st, A, steps);
         else hipLaunchKernelGGL((k_linear_few<uint16_t, NB>), grid, dim3(256), 0, st, A, steps);
         SC_LAUNCHED("grouped_linear");
-    } else if (big) {
+    } else if (by == BY_BIG) {
         SC_CHECK(grouped_linear_big(A, kind, st));
     } else {
-        const dim3 grid((unsigned)linear_tiles(A.n, A.groups, A.cin, A.cout, kind, A.chunk, LT));
-#define GO(T, KIND, PART) hipLaunchKernelGGL((k_linear<T, KIND, PART>), grid, dim3(256), 0, st, A)
-#define BY_KIND(T)                                 \
-    if (kind == LINEAR_Y) GO(T, LINEAR_Y, false);  \
-    else if (kind == LINEAR_DX) GO(T, LINEAR_DX, false); \
-    else if (A.chunk) GO(T, LINEAR_DW, true);      \
-    else GO(T, LINEAR_DW, false)
-        if (dtype == SUBMCONV_F32) { BY_KIND(float); } else { BY_KIND(uint16_t); }
+        const dim3 grid((unsigned)linear_tiles(A.n, A.groups, A.cin, A.cout, kind, A.chunk, TILE_OF[by]));
+#define GO(T, KIND, PART)                                                                             \
+    if (by == BY_SMALL) hipLaunchKernelGGL((k_linear<T, KIND, PART, 1>), grid, dim3(256), 0, st, A);  \
+    else hipLaunchKernelGGL((k_linear<T, KIND, PART, 2>), grid, dim3(256), 0, st, A)
+#define BY_KIND(T)                                              \
+    if (kind == LINEAR_Y) { GO(T, LINEAR_Y, false); }           \
+    else if (kind == LINEAR_DX) { GO(T, LINEAR_DX, false); }    \
+    else if (A.chunk) { GO(T, LINEAR_DW, true); }               \
+    else { GO(T, LINEAR_DW, false); }
+        if (dtype == SUBMCONV_F32) { BY_KIND(float) } else { BY_KIND(uint16_t) }
 #undef BY_KIND
 #undef GO
         SC_LAUNCHED("grouped_linear");
