@@ -132,23 +132,17 @@ static inline int64_t most_tiles(int64_t n, int groups, int size) { return n / s
 
 enum { LINEAR_Y, LINEAR_DX, LINEAR_DW };
 
-// Tiles of a call in tiles of BIG_TILE squared, at most (LINEAR_DW with a chunk: of all pieces).
-constexpr int BIG_TILE = 256;
+// Tiles of a call in tiles of `size` squared, at most (LINEAR_DW with a chunk: of all pieces).
 static inline int64_t linear_tiles(int64_t n, int groups, int cin, int cout, int kind, int chunk, int size)
 {
     const int64_t in = (cin + size - 1) / size, out = (cout + size - 1) / size;
     if (kind == LINEAR_DW) return in * out * (chunk ? most_tiles(n, groups, chunk) : groups);
     return most_tiles(n, groups, size) * (kind == LINEAR_Y ? out : in);
 }
-static inline int64_t linear_big_tiles(int64_t n, int groups, int cin, int cout, int kind, int chunk)
-{
-    return linear_tiles(n, groups, cin, cout, kind, chunk, BIG_TILE);
-}
-
 // Blocks of a call's largest launch; a launch holds 2^24 of them.
 int64_t linear_blocks(int64_t n, int groups, int cin, int cout, int dtype, int kind);
 int grouped_linear(LinearArgs A, int dtype, int kind, void *workspace, hipStream_t st);
-int grouped_linear_big(const LinearArgs &A, int kind, hipStream_t st);
+int grouped_linear_big(const LinearArgs &A, int dtype, int kind, int size, hipStream_t st);
 size_t linear_dw_workspace(int64_t n, int groups, int cin, int cout, int dtype);
 
 }  // namespace sc

@@ -344,17 +344,19 @@ __global__ __launch_bounds__(256) void k_linear_join(LinearArgs A)
 }
 
 // The rules below were measured over 1 to 8 groups of 1 to 8192 rows, widths of 64 to 4096, in us:
-//   few rows (16 a tile) against tiles of 64, 8 groups 1024 -> 1024 bf16: 32 rows each 11.8 and 16.9, 64 16.5 and
-//   20.1, 128 27 and 18.4; fp32 64 rows 33 and 45, 128 63 and 47.
-//   Tiles of 64 against 256, bf16: 8 x 512 x 1024 -> 1024 25 and 30, 8 x 2048 88 and 41; 8192 x 1024 -> 1024 48 and 33.
-//   Tiles of 64 against 128, fp32: 8 x 512 x 1024 -> 1024 95 and 117, 8 x 2048 349 and 303.
-//   dw, tiles of 64, 128 and 256, bf16: 8 x 128 x 1024 x 1024 15, 13 and 16, 8 x 256 23, 21 and 20; 8 x 2048 x 256 x 1024 52, 56 and 43.
-constexpr int64_t FEW_ROWS = 16, FEW_BLOCKS = 1024, SMALL_TILES = 768, BIG_OUT = 1 << 23;
-constexpr double BIG_DW = 2e9, LARGE_DW = 4e9;
+//   few rows (16 a tile) against the ring of 128, bf16, 8 groups 1024 -> 1024: 32 rows each 12.7 and 15.5, 64 16.2 and 15.3;
+//   against tiles of 64, fp32: 64 rows 34 and 46, 128 64 and 47.
+//   The rings of 128 and 256, bf16: 8 x 512 x 1024 -> 1024 18 and 30, 8 x 2048 44 and 40, 8 x 8192 166 and 145.
+//   Tiles of 64 and the ring of 128, fp32: 8 x 256 x 1024 -> 1024 60 and 77, 8 x 512 97 and 80, 8 x 8192 1368 and 1070.
+//   Tiles of 64 and 128 (unaligned), fp32: 8 x 512 x 1024 -> 1024 97 and 119, 8 x 2048 352 and 339, 8 x 8192 1368 and 1258.
+//   dw, tiles of 64, 128 and the ring of 256, bf16: 8 x 128 x 1024 x 1024 15, 13 and 16, 8 x 256 23, 21 and 20, 8 x 2048 106, 110 and 65;
+//   tiles of 64, 128 and the ring of 128, fp32: 8 x 128 39, 38 and 33, 8 x 256 62, 63 and 51; 8 x 8192 x 64 x 256 43, 63 and 56.
+constexpr int64_t FEW_ROWS = 16, FEW_BLOCKS = 1024, SMALL_TILES = 768, BIG_OUT = 1 << 24, RING_OUT = 1 << 22;
+constexpr double RING_DW = 2e9, LARGE_DW = 4e9;
 
 // Which kernel takes a call.
-enum { BY_FEW, BY_SMALL, BY_LARGE, BY_BIG };
-constexpr int TILE_OF[] = {16, 64, 128, BIG_TILE};
+enum { BY_FEW, BY_SMALL, BY_LARGE, BY_RING, BY_BIG };  // (the last two: linear_big.hip)
+constexpr int TILE_OF[] = {16, 64, 128, 128, 256};
 
 // Positions of a piece of dw: whole groups (0) where these are blocks enough, else so many
 // that the blocks of all pieces fill the card some times over.  A piece's sums are written and read again in
@@ -362,7 +364,7 @@ constexpr int TILE_OF[] = {16, 64, 128, BIG_TILE};
 static int dw_chunk(int64_t n, int groups, int cin, int cout, int by)
 {
     const int size = TILE_OF[by];
-    const int64_t tiles = (int64_t)((cin + size - 1) / size) * ((cout + size - 1) / size), want = UNITS * (by == BY_BIG ? 1 : (by == BY_LARGE ? 4 : 16));
+    const int64_t tiles = (int64_t)((cin + size - 1) / size) * ((cout + size - 1) / size), want = UNITS * (by == BY_BIG ? 1 : (by == BY_RING ? 2 : (by == BY_LARGE ? 4 : 16)));
     if (groups * tiles >= want / 2 || n < 512) return 0;
     const int64_t pieces = (want + tiles - 1) / tiles;
     int64_t chunk = (n + pieces - 1) / pieces;
@@ -370,8 +372,12 @@ static int dw_chunk(int64_t n, int groups, int cin, int cout, int by)
     return (int)(chunk < 256 ? 256 : chunk);
 }
 
-// Whether the large tiles may take a call of these widths, if pointers and distances are aligned.
-static bool may_be_big(int cin, int cout, int dtype) { return dtype == SUBMCONV_BF16 && cin % 8 == 0 && cout % 8 == 0; }
+// Whether the ring kernels may take a call of these widths, if pointers and distances are aligned.
+static bool may_be_big(int cin, int cout, int dtype)
+{
+    const int v = dtype == SUBMCONV_F32 ? 4 : 8;
+    return cin % v == 0 && cout % v == 0;
+}
 
 // The kernel by sizes alone; `aligned`: whole pieces of 16 bytes everywhere.
 static int choose(int64_t n, int groups, int cin, int cout, int dtype, int kind, bool aligned)
@@ -381,10 +387,14 @@ static int choose(int64_t n, int groups, int cin, int cout, int dtype, int kind,
         const int64_t few = most_tiles(n, groups, 16) * ((cout + 31) / 32);
         if (n <= FEW_ROWS * (int64_t)groups || few <= (dtype == SUBMCONV_F32 ? 2 : 1) * FEW_BLOCKS) return BY_FEW;
     }
-    if (aligned && may_be_big(cin, cout, dtype) && cols >= 192) {
-        if (kind == LINEAR_DW ? cout >= 192 && (double)n * cin * cout >= BIG_DW : n * cols >= BIG_OUT) return BY_BIG;
+    const bool f32 = dtype == SUBMCONV_F32, ring = aligned && may_be_big(cin, cout, dtype);
+    const double work = (double)n * cin * cout;
+    if (kind == LINEAR_DW) {
+        if (ring && work >= RING_DW && cin >= 96 && cout >= 96 && (f32 || (cin >= 192 && cout >= 192))) return f32 ? BY_RING : BY_BIG;
+        return work >= LARGE_DW || linear_tiles(n, groups, cin, cout, kind, 0, 128) >= SMALL_TILES ? BY_LARGE : BY_SMALL;
     }
-    if (kind == LINEAR_DW) return (double)n * cin * cout >= LARGE_DW || linear_tiles(n, groups, cin, cout, kind, 0, 128) >= SMALL_TILES ? BY_LARGE : BY_SMALL;
+    if (ring && !f32) return n * cols >= BIG_OUT && cols >= 192 ? BY_BIG : BY_RING;
+    if (ring && n * cols >= RING_OUT) return BY_RING;
     return linear_tiles(n, groups, cin, cout, kind, 0, 128) >= SMALL_TILES ? BY_LARGE : BY_SMALL;
 }
 
@@ -407,9 +417,10 @@ int64_t linear_blocks(int64_t n, int groups, int cin, int cout, int dtype, int k
     return linear_tiles(n, groups, cin, cout, kind, kind == LINEAR_DW ? dw_chunk(n, groups, cin, cout, by) : 0, TILE_OF[by]);
 }
 
-static bool is_aligned(const LinearArgs &A, int kind)
+static bool is_aligned(const LinearArgs &A, int dtype, int kind)
 {
-    const auto pieces = [](const void *p, int64_t row) { return ((uintptr_t)p & 15) == 0 && row % 8 == 0; };
+    const int v = dtype == SUBMCONV_F32 ? 4 : 8;
+    const auto pieces = [&](const void *p, int64_t row) { return ((uintptr_t)p & 15) == 0 && row % v == 0; };
     if (kind != LINEAR_DX && !pieces(A.x, A.x_row)) return false;
     if (kind != LINEAR_Y && !pieces(A.g, A.g_row)) return false;
     return kind == LINEAR_DW || pieces(A.w, 0);
@@ -417,7 +428,7 @@ static bool is_aligned(const LinearArgs &A, int kind)
 
 int grouped_linear(LinearArgs A, int dtype, int kind, void *workspace, hipStream_t st)
 {
-    const int by = choose(A.n, A.groups, A.cin, A.cout, dtype, kind, is_aligned(A, kind));
+    const int by = choose(A.n, A.groups, A.cin, A.cout, dtype, kind, is_aligned(A, dtype, kind));
     if (kind == LINEAR_DW) {
         A.chunk = dw_chunk(A.n, A.groups, A.cin, A.cout, by);
         A.part = (float *)workspace;
@@ -430,8 +441,8 @@ int grouped_linear(LinearArgs A, int dtype, int kind, void *workspace, hipStream
         if (dtype == SUBMCONV_F32) hipLaunchKernelGGL((k_linear_few<float, NB>), grid, dim3(256), 0, st, A, steps);
         else hipLaunchKernelGGL((k_linear_few<uint16_t, NB>), grid, dim3(256), 0, st, A, steps);
         SC_LAUNCHED("grouped_linear");
-    } else if (by == BY_BIG) {
-        SC_CHECK(grouped_linear_big(A, kind, st));
+    } else if (by >= BY_RING) {
+        SC_CHECK(grouped_linear_big(A, dtype, kind, TILE_OF[by], st));
     } else {
         const dim3 grid((unsigned)linear_tiles(A.n, A.groups, A.cin, A.cout, kind, A.chunk, TILE_OF[by]));
 #define GO(T, KIND, PART)                                                                             \

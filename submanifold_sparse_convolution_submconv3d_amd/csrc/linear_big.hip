@@ -1,4 +1,4 @@
-// Grouped matrix products of bf16 rows in large tiles (see linear.hip for the products).
+// Grouped matrix products of aligned rows in large tiles (see linear.hip for the products).
 //
 // Blocks stay on the card and walk tiles of BM x BN.  Both sides' tiles are copied straight into one of
 // two places in LDS, 64 of k a step (rows of 128 bytes: copies of 64-byte rows take 0.56 us for 32 KB
@@ -139,7 +139,7 @@ struct BigTiles {
     }
 };
 
-constexpr int BIG_K = 64;
+template <typename T> constexpr int BIG_K = 128 / (int)sizeof(T);  // of k a step
 
 // A copy of 64 pieces of 16 bytes straight into LDS.  As an instruction of its own, since the compiler
 // lets every transposing read wait for all copies that it knows of; the waits are below.
@@ -150,13 +150,13 @@ __device__ __forceinline__ void copy_pieces(const char *from, uint32_t lds)
 
 // WM x WN waves of MB x NB blocks of 32 x 32.
 // LINEAR_DW: SUMS: db too.  PART: pieces of groups, whose sums are kept in fp32 for k_linear_join.
-template <int KIND, int WM, int WN, int MB, int NB, bool SUMS, bool PART>
+template <typename T, int KIND, int WM, int WN, int MB, int NB, bool SUMS, bool PART>
 __global__ __launch_bounds__(64 * WM * WN, 2) void k_linear_big(LinearArgs A)
 {
     constexpr bool AKS = KIND == LINEAR_DW, BKS = KIND != LINEAR_Y;
-    constexpr int BM = 32 * MB * WM, BN = 32 * NB * WN, WAVES = WM * WN;
-    constexpr int ABYTES = BM * 2 * BIG_K, BBYTES = BN * 2 * BIG_K;
-    constexpr uint32_t ARB = AKS ? BM * 2 : BIG_K * 2, BRB = BKS ? BN * 2 : BIG_K * 2;  // bytes of a row in LDS
+    constexpr int BM = 32 * MB * WM, BN = 32 * NB * WN, WAVES = WM * WN, ES = (int)sizeof(T), V = VEC<T>, BK = BIG_K<T>;
+    constexpr int ABYTES = BM * 128, BBYTES = BN * 128;
+    constexpr uint32_t ARB = AKS ? BM * ES : 128, BRB = BKS ? BN * ES : 128;  // bytes of a row in LDS
     constexpr int CA = ABYTES / 1024 / WAVES, CB = BBYTES / 1024 / WAVES;  // copies of a wave a step
     static_assert(CA * 1024 * WAVES == ABYTES && CB * 1024 * WAVES == BBYTES, "whole copies");
     static_assert(ABYTES == BBYTES, "one ring for both sides");
@@ -189,8 +189,8 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_linear_big(LinearArgs A)
     const char *pa[CA], *pb[CB];
     const auto row_a = [&](int i) { return (int)(((wave * CA + i) * 1024 + lane * 16) / ARB); };  // the copy's row in the tile
     const auto row_b = [&](int i) { return (int)(((wave * CB + i) * 1024 + lane * 16) / BRB); };
-    const auto piece_a = [&](int i) { return (int)((((wave * CA + i) * 1024 + lane * 16) % ARB / 16) ^ swizzle<ARB>(row_a(i))); };
-    const auto piece_b = [&](int i) { return (int)((((wave * CB + i) * 1024 + lane * 16) % BRB / 16) ^ swizzle<BRB>(row_b(i))); };
+    const auto piece_a = [&](int i) { return (int)((((wave * CA + i) * 1024 + lane * 16) % ARB / 16) ^ (AKS && ES == 4 ? 0 : swizzle<ARB>(row_a(i)))); };
+    const auto piece_b = [&](int i) { return (int)((((wave * CB + i) * 1024 + lane * 16) % BRB / 16) ^ (BKS && ES == 4 ? 0 : swizzle<BRB>(row_b(i)))); };
     const char *zeros = (const char *)zero_piece;
     int source[KIND == LINEAR_Y ? CA : 1];  // rows of x that the next tile takes
     const auto x_rows = [&](const BigTile &t) {
@@ -202,32 +202,32 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_linear_big(LinearArgs A)
             }
         }
     };
-    const auto column = [](int at, int width) { return at + 8 <= width ? at : width - 8; };  // columns past the end: any that exist
+    const auto column = [](int at, int width) { return at + V <= width ? at : width - V; };  // columns past the end: any that exist
     const auto aim_a = [&](const BigTile &t) {
 #pragma unroll
         for (int i = 0; i < CA; ++i) {
             if constexpr (KIND == LINEAR_Y) {
                 const bool there = source[i] >= 0 && source[i] < A.nx;
-                pa[i] = there ? (const char *)A.x + ((int64_t)source[i] * A.x_row + piece_a(i) * 8) * 2 : nullptr;
+                pa[i] = there ? (const char *)A.x + ((int64_t)source[i] * A.x_row + piece_a(i) * V) * ES : nullptr;
             } else if constexpr (KIND == LINEAR_DX) {
                 const int p = t.m0 + row_a(i) < t.m_end ? t.m0 + row_a(i) : t.m_end - 1;
-                pa[i] = (const char *)A.g + ((int64_t)p * A.g_row + piece_a(i) * 8) * 2;
+                pa[i] = (const char *)A.g + ((int64_t)p * A.g_row + piece_a(i) * V) * ES;
             } else {
-                pa[i] = (const char *)A.g + ((int64_t)(t.beg + row_a(i)) * A.g_row + column(t.m0 + piece_a(i) * 8, A.cout)) * 2;
+                pa[i] = (const char *)A.g + ((int64_t)(t.beg + row_a(i)) * A.g_row + column(t.m0 + piece_a(i) * V, A.cout)) * ES;
             }
         }
     };
     const auto aim_b = [&](const BigTile &t) {
-        const char *w = (const char *)A.w + (int64_t)t.group * A.cout * A.cin * 2;
+        const char *w = (const char *)A.w + (int64_t)t.group * A.cout * A.cin * ES;
 #pragma unroll
         for (int i = 0; i < CB; ++i) {
             if constexpr (KIND == LINEAR_Y) {
                 const int n = t.n0 + row_b(i) < A.cout ? t.n0 + row_b(i) : A.cout - 1;
-                pb[i] = w + ((int64_t)n * A.cin + piece_b(i) * 8) * 2;
+                pb[i] = w + ((int64_t)n * A.cin + piece_b(i) * V) * ES;
             } else if constexpr (KIND == LINEAR_DX) {
-                pb[i] = w + ((int64_t)row_b(i) * A.cin + column(t.n0 + piece_b(i) * 8, A.cin)) * 2;
+                pb[i] = w + ((int64_t)row_b(i) * A.cin + column(t.n0 + piece_b(i) * V, A.cin)) * ES;
             } else {
-                pb[i] = (const char *)A.x + column(t.n0 + piece_b(i) * 8, A.cin) * 2;  // and the row, step by step
+                pb[i] = (const char *)A.x + column(t.n0 + piece_b(i) * V, A.cin) * ES;  // and the row, step by step
             }
         }
     };
@@ -262,31 +262,31 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_linear_big(LinearArgs A)
     uint32_t fill = lds;  // the place that is filled next
     const auto filled = [&]() { fill = fill == lds + (RING - 1) * ABYTES ? lds : fill + ABYTES; };
     const auto copy_a = [&](int i) {
-        const char *from = ka + (AKS ? row_a(i) : piece_a(i) * 8) < ta.k_end ? pa[i] : zeros;
+        const char *from = ka + (AKS ? row_a(i) : piece_a(i) * V) < ta.k_end ? pa[i] : zeros;
         if constexpr (KIND == LINEAR_Y) from = pa[i] ? from : zeros;
         copy_pieces(from, __builtin_amdgcn_readfirstlane(fill + (wave * CA + i) * 1024));
     };
     const auto copy_b = [&](int i) {
-        const char *from = kb + (BKS ? row_b(i) : piece_b(i) * 8) < tb.k_end ? pb[i] : zeros;
+        const char *from = kb + (BKS ? row_b(i) : piece_b(i) * V) < tb.k_end ? pb[i] : zeros;
         if constexpr (KIND == LINEAR_DW) {
             constexpr int PER = ROWS / CB;  // rows of a copy
             int r = step_rows[i * PER];
 #pragma unroll
             for (int q = 1; q < PER; ++q) r = (int)(lane * 16 / BRB) == q ? step_rows[i * PER + q] : r;
-            from = r >= 0 && r < A.nx ? pb[i] + (int64_t)r * A.x_row * 2 : zeros;
+            from = r >= 0 && r < A.nx ? pb[i] + (int64_t)r * A.x_row * ES : zeros;
         }
         copy_pieces(from, __builtin_amdgcn_readfirstlane(fill + (wave * CB + i) * 1024));
     };
     // Each side moves on by a step, and to its next tile; past the last one zeros are copied.
     const auto copied_a = [&]() {
-        const int64_t d = AKS ? (int64_t)BIG_K * A.g_row * 2 : BIG_K * 2;
+        const int64_t d = AKS ? (int64_t)BK * A.g_row * ES : 128;
 #pragma unroll
         for (int i = 0; i < CA; ++i) {
             if constexpr (KIND == LINEAR_Y) pa[i] = pa[i] ? pa[i] + d : nullptr;
             else pa[i] += d;
         }
         filled();
-        ka += BIG_K;
+        ka += BK;
         if (ka >= ta.k_end && after.any) {
             ta = after;
             ka = 0;
@@ -298,12 +298,12 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_linear_big(LinearArgs A)
     };
     const auto copied_b = [&]() {
         if constexpr (KIND != LINEAR_DW) {
-            const int64_t d = BKS ? (int64_t)BIG_K * A.cin * 2 : BIG_K * 2;
+            const int64_t d = BKS ? (int64_t)BK * A.cin * ES : 128;
 #pragma unroll
             for (int i = 0; i < CB; ++i) pb[i] += d;
         }
         filled();
-        kb += BIG_K;
+        kb += BK;
         if (kb >= tb.k_end) {
             const BigTile t = tile_at(b_round + 1);
             if (t.any) {
@@ -318,13 +318,15 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_linear_big(LinearArgs A)
 
     // ---- operands ----
     const uint32_t wm = (wave % WM) * (32 * MB), wn = (wave / WM) * (32 * NB);
-    struct Operand {  // k next to each other: one address; a row apart: two for each block
+    struct Operand {  // k next to each other, or fp32: one address; bf16 a row apart: two for each block
         uint32_t at[8];
     } oa, ob, os;
     const auto make = [&](Operand &o, bool ks, uint32_t rb, uint32_t base, uint32_t first, int blocks) {
         const uint32_t a = lane >> 5, g = (lane >> 4) & 1, t = lane & 15;
         if (!ks) {
-            o.at[0] = base + piece_at<BIG_K * 2>(first + (lane & 31), a);
+            o.at[0] = base + piece_at<128>(first + (lane & 31), a);
+        } else if (ES == 4) {
+            o.at[0] = base + 4 * a * rb + (first + (lane & 31)) * 4;
         } else {
 #pragma unroll
             for (int h = 0; h < 2; ++h)
@@ -342,17 +344,20 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_linear_big(LinearArgs A)
     static_assert(!SUMS || MB == WN, "a block for each wave");
     float sum = 0.0f;
     if constexpr (SUMS) make(os, AKS, ARB, lds, wm + 32 * (wave / WM), 1);
-    // 16 of k: quarter j of the place at offset `from`
-    const auto read_a = [&](uint32_t from, int j, int i) {
-        if constexpr (!AKS) return lds_read16((oa.at[0] ^ (32 * j)) + from + i * (32 * ARB));
-        const u32x2 lo = lds_read_tr(oa.at[i] + from + j * (16 * ARB)), hi = lds_read_tr(oa.at[4 + i] + from + j * (16 * ARB));
+    // 32 bytes of k: quarter j of the place at offset `from`, block i
+    const auto read = [&](const Operand &o, bool ks, uint32_t rb, uint32_t from, int j, int i) {
+        if (!ks) return lds_read16((o.at[0] ^ (32 * j)) + from + i * (32 * 128));
+        if (ES == 4) {
+            Raw16 r;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) r[e] = *(const SC_LDS uint32_t *)(uintptr_t)(o.at[0] + from + (8 * j + e) * rb + i * 128);
+            return r;
+        }
+        const u32x2 lo = lds_read_tr(o.at[i] + from + j * (16 * rb)), hi = lds_read_tr(o.at[4 + i] + from + j * (16 * rb));
         return Raw16{lo[0], lo[1], hi[0], hi[1]};
     };
-    const auto read_b = [&](uint32_t from, int j, int i) {
-        if constexpr (!BKS) return lds_read16((ob.at[0] ^ (32 * j)) + from + i * (32 * BRB));
-        const u32x2 lo = lds_read_tr(ob.at[i] + from + j * (16 * BRB)), hi = lds_read_tr(ob.at[4 + i] + from + j * (16 * BRB));
-        return Raw16{lo[0], lo[1], hi[0], hi[1]};
-    };
+    const auto read_a = [&](uint32_t from, int j, int i) { return read(oa, AKS, ARB, from, j, i); };
+    const auto read_b = [&](uint32_t from, int j, int i) { return read(ob, BKS, BRB, from, j, i); };
 
     f32x16 acc[MB][NB];
     Raw16 fa[2][MB], fb[2][NB];
@@ -376,22 +381,24 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_linear_big(LinearArgs A)
 #pragma unroll
         for (int q = 0; q < MB * NB; ++q) {
             const int m = q / NB, n = q % NB;
-            acc[m][n] = mma_pieces<uint16_t>(fb[to ^ 1][n], fa[to ^ 1][m], acc[m][n]);
+            acc[m][n] = mma_pieces<T>(fb[to ^ 1][n], fa[to ^ 1][m], acc[m][n]);
 #pragma unroll
             for (int r = q * READS; r < (q + 1) * READS && r < MB + NB; ++r) {
                 if (r < NB) fb[to][r] = read_b(from_b, nj, r);
                 else fa[to][r - NB] = read_a(from_a, nj, r - NB);
             }
-            if (q % 2 && q / 2 < copies) copy(q / 2);
+            constexpr int GAP = MB * NB < 8 ? 1 : 2;  // a copy after every product, or every other
+            if (q % GAP == GAP - 1 && q / GAP < copies) copy(q / GAP);
             __builtin_amdgcn_sched_barrier(0x6);  // only arithmetic may cross
         }
         if constexpr (SUMS) {  // (the last quarter's with the one before it, while the place is still whole)
 #pragma unroll
             for (int q = j; q < 4 && j < 3; q += j == 2 ? 1 : 4) {
-                const u32x2 lo = lds_read_tr(os.at[0] + place_a + q * (16 * ARB)), hi = lds_read_tr(os.at[4] + place_a + q * (16 * ARB));
-                float v[8];
-                unpack(Raw16{lo[0], lo[1], hi[0], hi[1]}, v, (const uint16_t *)nullptr);
-                sum += ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
+                float v[V], t = 0.0f;
+                unpack(read(os, AKS, ARB, place_a, q, 0), v, (const T *)nullptr);
+#pragma unroll
+                for (int i = 0; i < V; i += 2) t += v[i] + v[i + 1];
+                sum += t;
             }
         }
     };
@@ -417,8 +424,9 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_linear_big(LinearArgs A)
     for (int i = 0; i < MB; ++i) fa[0][i] = read_a(place_a, 0, i);
 #pragma unroll
     for (int i = 0; i < NB; ++i) fb[0][i] = read_b(place_b, 0, i);
-    constexpr int STORES = MB * NB * (PART ? 4 : 2), C0 = CA / 2;
-    static_assert(CA <= MB * NB && CB <= MB * NB / 2, "a copy after every other product");
+    constexpr bool OUT_F32 = PART || ES == 4;
+    constexpr int STORES = MB * NB * (OUT_F32 ? 4 : 2), C0 = CA / 2;
+    static_assert(CA <= MB * NB && CB <= MB * NB, "room for the copies between the products");
     bool stored = false;  // the last tile's stores may still be in flight
     for (;;) {
         float bias = 0.0f;  // of column lane of the wave's
@@ -444,13 +452,13 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_linear_big(LinearArgs A)
             copied_b();
             place_a = on(place_a, 2);
             place_b = on(place_b, 2);
-            k += BIG_K;
+            k += BK;
         } while (k < now.k_end);
         // a lane has row l % 32 of each block, its elements in the registers
         const int l = lane & 31, a = lane >> 5;
         const int64_t ld = KIND == LINEAR_DW ? A.cin : A.out_row;
         const int n_end = KIND == LINEAR_Y ? A.cout : A.cin;
-        typedef typename std::conditional<PART, float, uint16_t>::type Out;
+        typedef typename std::conditional<PART, float, T>::type Out;
         Out *out = PART ? (Out *)A.part : (Out *)A.out;
         if constexpr (KIND == LINEAR_DW) out += (int64_t)(PART ? now.piece : now.group) * A.cout * A.cin;
         if constexpr (SUMS) {
@@ -477,7 +485,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_linear_big(LinearArgs A)
                 const int e = now.n0 + (int)wn + 32 * n + 16 * h + 8 * a;
                 Out *to = out + (int64_t)(now.m0 + (int)wm + l) * ld + e;
                 const auto put = [&](Out *at, int have) {
-                    if constexpr (PART) {
+                    if constexpr (OUT_F32) {
                         const float lo[4] = {v[0], v[1], v[2], v[3]}, hi[4] = {v[4], v[5], v[6], v[7]};
                         store_raw(at, repack(lo, at), have < 4 ? have : 4);
                         if (have > 4) store_raw(at + 4, repack(hi, at), have - 4);
@@ -511,19 +519,32 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_linear_big(LinearArgs A)
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // no copy may land in LDS that the next block owns
 }
 
-// Tiles of 256 x 256 in eight waves.
-int grouped_linear_big(const LinearArgs &A, int kind, hipStream_t st)
+// Tiles of 256 x 256 in eight waves, a block a compute unit, or of 128 x 128 in four, two blocks.
+int grouped_linear_big(const LinearArgs &A, int dtype, int kind, int size, hipStream_t st)
 {
-    constexpr int WM = 2, WN = 4, MB = 4, NB = 2;
-    static_assert(32 * WM * MB == BIG_TILE && 32 * WN * NB == BIG_TILE, "the tile");
-    const int64_t blocks = (linear_big_tiles(A.n, A.groups, A.cin, A.cout, kind, A.chunk) + 7) / 8 * 8;
-    const dim3 grid((unsigned)(blocks < UNITS ? blocks : UNITS)), block(64 * WM * WN);
-#define GO(KIND, SUMS, PART) hipLaunchKernelGGL((k_linear_big<KIND, WM, WN, MB, NB, SUMS, PART>), grid, block, 0, st, A)
-    if (kind == LINEAR_Y) GO(LINEAR_Y, false, false);
-    else if (kind == LINEAR_DX) GO(LINEAR_DX, false, false);
-    else if (A.chunk) { if (A.db) GO(LINEAR_DW, true, true); else GO(LINEAR_DW, false, true); }
-    else { if (A.db) GO(LINEAR_DW, true, false); else GO(LINEAR_DW, false, false); }
-#undef GO
+    const int64_t tiles = (linear_tiles(A.n, A.groups, A.cin, A.cout, kind, A.chunk, size) + 7) / 8 * 8, most = UNITS * (size == 256 ? 1 : 2);
+    const dim3 grid((unsigned)(tiles < most ? tiles : most));
+#define LARGE(T, KIND, SUMS, PART) hipLaunchKernelGGL((k_linear_big<T, KIND, 2, 4, 4, 2, SUMS, PART>), grid, dim3(512), 0, st, A)
+#define SMALL(T, KIND, SUMS, PART) hipLaunchKernelGGL((k_linear_big<T, KIND, 2, 2, 2, 2, SUMS, PART>), grid, dim3(256), 0, st, A)
+#define DW(GO, T)                                                                                              \
+    if (A.chunk) { if (A.db) GO(T, LINEAR_DW, true, true); else GO(T, LINEAR_DW, false, true); }               \
+    else { if (A.db) GO(T, LINEAR_DW, true, false); else GO(T, LINEAR_DW, false, false); }
+    if (dtype == SUBMCONV_F32) {  // 128 throughout: a tile of 256 takes 226 us for 1024 of k
+        if (kind == LINEAR_Y) SMALL(float, LINEAR_Y, false, false);
+        else if (kind == LINEAR_DX) SMALL(float, LINEAR_DX, false, false);
+        else { DW(SMALL, float) }
+    } else if (kind == LINEAR_DW) {
+        DW(LARGE, uint16_t)
+    } else if (size == 256) {
+        if (kind == LINEAR_Y) LARGE(uint16_t, LINEAR_Y, false, false);
+        else LARGE(uint16_t, LINEAR_DX, false, false);
+    } else {
+        if (kind == LINEAR_Y) SMALL(uint16_t, LINEAR_Y, false, false);
+        else SMALL(uint16_t, LINEAR_DX, false, false);
+    }
+#undef DW
+#undef SMALL
+#undef LARGE
     SC_LAUNCHED("grouped_linear");
     return SUBMCONV_OK;
 }
