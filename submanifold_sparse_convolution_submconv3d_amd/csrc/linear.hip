@@ -351,7 +351,7 @@ __global__ __launch_bounds__(256) void k_linear_join(LinearArgs A)
 //   Tiles of 64 and 128 (unaligned), fp32: 8 x 512 x 1024 -> 1024 97 and 119, 8 x 2048 352 and 339, 8 x 8192 1368 and 1258.
 //   dw, tiles of 64, 128 and the ring of 256, bf16: 8 x 128 x 1024 x 1024 15, 13 and 16, 8 x 256 23, 21 and 20, 8 x 2048 106, 110 and 65;
 //   tiles of 64, 128 and the ring of 128, fp32: 8 x 128 39, 38 and 33, 8 x 256 62, 63 and 51; 8 x 8192 x 64 x 256 43, 63 and 56.
-constexpr int64_t FEW_ROWS = 16, FEW_BLOCKS = 1024, SMALL_TILES = 768, BIG_OUT = 1 << 24, RING_OUT = 1 << 22;
+constexpr int64_t FEW_ROWS = 16, FEW_BLOCKS = 1024, SMALL_TILES = 640, BIG_OUT = 1 << 24, RING_OUT = 1 << 22;
 constexpr double RING_DW = 2e9, LARGE_DW = 4e9;
 
 // Which kernel takes a call.

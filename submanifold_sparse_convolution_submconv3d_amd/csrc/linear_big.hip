@@ -142,10 +142,11 @@ struct BigTiles {
 template <typename T> constexpr int BIG_K = 128 / (int)sizeof(T);  // of k a step
 
 // A copy of 64 pieces of 16 bytes straight into LDS.  As an instruction of its own, since the compiler
-// lets every transposing read wait for all copies that it knows of; the waits are below.
+// lets every transposing read wait for all copies that it knows of; the waits are below.  (Nothing else in
+// these kernels uses m0.)
 __device__ __forceinline__ void copy_pieces(const char *from, uint32_t lds)
 {
-    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(from), "s"(lds) : "memory", "m0");
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(from), "s"(lds) : "memory");
 }
 
 // WM x WN waves of MB x NB blocks of 32 x 32.
