@@ -1,12 +1,18 @@
 // Grouped matrix products of aligned rows in large tiles (see linear.hip for the products).
 //
-// Blocks stay on the card and walk tiles of BM x BN.  Both sides' tiles are copied straight into one of
-// two places in LDS, 64 of k a step (rows of 128 bytes: copies of 64-byte rows take 0.56 us for 32 KB
-// a compute unit, of 128-byte rows 0.34), and on into the next tile, so that a tile's end costs the stores
-// alone.  In a step, each wave multiplies 32x32 blocks on the matrix cores in four quarters of 16 of k; the
-// operands of the next quarter are read from LDS meanwhile.  Before the last quarter its operands are
-// in registers: after the step's one barrier there the next step's copies, which have landed, are read,
-// and the place that is done with is filled with the step after that.
+// Blocks stay on the card and walk tiles of BM x BN: of 256 x 256 (bf16; eight waves, one block a compute unit) or of
+// 128 x 128 (both types; four waves, two blocks).  Both sides' tiles are copied straight into a ring of five places in
+// LDS, 64 of k in bf16 and 32 in fp32 a step (rows of 128 bytes: copies of 64-byte rows take 0.56 us for 32 KB a compute
+// unit, of 128-byte rows 0.34), and on into the next tile, so that a tile's end costs the stores alone.  (Five places of
+// one side's step each, 32 KB, let copies run a side further ahead than two of a whole step, in the same LDS.)  In a step,
+// each wave multiplies 32x32 blocks on the matrix cores in four quarters of 16 of k; the operands of the next quarter are
+// read from LDS meanwhile.  Before the last quarter its operands are in registers: after the step's one barrier there the
+// next step's copies, which have landed, are read, and the places that are done with are filled again.
+//
+// Measured, 8 groups over 40,768 rows of 1024 -> 4096 in bf16 (342 GFLOP a product): forward 347-400 us, dx 330-370,
+// dW with db 400-465 (the lower when alone; together with the others the card's power holds the clock near 1.8 GHz):
+// 0.73-0.99 PFLOP/s.  What bounds them then is the matrix cores: 67% busy in dx, 52% in the forward, 43% in dW, whose
+// operands come through transposing reads of LDS, 2 a product; and dx's 2.56 rounds of tiles, which take three.
 #include <type_traits>
 
 #include "linear.h"
@@ -149,6 +155,27 @@ __device__ __forceinline__ void copy_pieces(const char *from, uint32_t lds)
     asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(from), "s"(lds) : "memory");
 }
 
+// v[q] of the lanes l, l ^ 8, l ^ 16, l ^ 24, seen as a matrix of lanes (bits 3 and 4 of the lane's number) and q, is
+// transposed.
+__device__ __forceinline__ void trade_lanes(Raw16 (&v)[4])
+{
+#pragma unroll
+    for (int d = 0; d < 4; ++d) {
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            auto r = __builtin_amdgcn_permlane16_swap(v[q][d], v[q + 2][d], false, false);
+            v[q][d] = r[0];
+            v[q + 2][d] = r[1];
+        }
+#pragma unroll
+        for (int q = 0; q < 4; q += 2) {  // row_ror:8, into the lanes of one half of 16 each
+            const int x = (int)v[q][d], y = (int)v[q + 1][d];
+            v[q][d] = (uint32_t)__builtin_amdgcn_update_dpp(x, y, 0x128, 0xf, 0xc, false);
+            v[q + 1][d] = (uint32_t)__builtin_amdgcn_update_dpp(y, x, 0x128, 0xf, 0x3, false);
+        }
+    }
+}
+
 // WM x WN waves of MB x NB blocks of 32 x 32.
 // LINEAR_DW: SUMS: db too.  PART: pieces of groups, whose sums are kept in fp32 for k_linear_join.
 template <typename T, int KIND, int WM, int WN, int MB, int NB, bool SUMS, bool PART>
@@ -245,8 +272,9 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_linear_big(LinearArgs A)
     after = tile_at(a_round);
     x_rows(after);
 
-    // LINEAR_DW: the rows of x of the step that is copied next.  A wave's copies take consecutive
-    // positions, so their rows' numbers are loaded once a wave, a step ahead.
+    // LINEAR_DW: the rows of x of the step that is copied next.  A wave's copies take consecutive positions, so
+    // their rows' numbers are loaded once a wave, during the quarter before the copies: until then no wait for LDS
+    // reads, which counts these loads too, comes between.
     constexpr int ROWS = KIND == LINEAR_DW ? (int)(CB * 1024 / BRB) : 1;
     int step_rows[ROWS];
     const auto look_up = [&]() {
@@ -258,7 +286,6 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_linear_big(LinearArgs A)
             }
         }
     };
-    look_up();
 
     uint32_t fill = lds;  // the place that is filled next
     const auto filled = [&]() { fill = fill == lds + (RING - 1) * ABYTES ? lds : fill + ABYTES; };
@@ -314,7 +341,6 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_linear_big(LinearArgs A)
                 aim_b(tb);
             }
         }
-        look_up();
     };
 
     // ---- operands ----
@@ -362,13 +388,22 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_linear_big(LinearArgs A)
 
     f32x16 acc[MB][NB];
     Raw16 fa[2][MB], fb[2][NB];
-    const auto clear = [&]() {
+    // The bias of the wave's columns of a tile, one a lane; sums begin with it.
+    static_assert(NB == 2, "a column a lane");
+    const auto bias_of = [&](const BigTile &t) {
+        if (KIND != LINEAR_Y || !A.bias || !t.real) return 0.0f;
+        const int e = t.n0 + (int)wn + (int)lane;
+        return A.bias[(int64_t)t.group * A.cout + (e < A.cout ? e : A.cout - 1)];
+    };
+    const auto begin = [&](float bias) {
 #pragma unroll
-        for (int m = 0; m < MB; ++m)
+        for (int n = 0; n < NB; ++n)
 #pragma unroll
-            for (int n = 0; n < NB; ++n)
+            for (int e = 0; e < 16; ++e) {
+                const float b = KIND == LINEAR_Y ? __shfl(bias, 32 * n + 8 * (e / 4) + 4 * (int)(lane >> 5) + e % 4, 64) : 0.0f;
 #pragma unroll
-                for (int e = 0; e < 16; ++e) acc[m][n][e] = 0.0f;
+                for (int m = 0; m < MB; ++m) acc[m][n][e] = b;
+            }
         sum = 0.0f;
     };
     uint32_t place_a = 0, place_b = ABYTES;  // offsets of this step's places
@@ -410,6 +445,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_linear_big(LinearArgs A)
         copied_a();
     };
     const auto all_b = [&]() {
+        look_up();
 #pragma unroll
         for (int i = 0; i < CB; ++i) copy_b(i);
         copied_b();
@@ -418,7 +454,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_linear_big(LinearArgs A)
     all_a();
     all_b();
     all_a();
-    clear();
+    begin(bias_of(now));
     wait_copies_and_barrier<CA>();
     all_b();
 #pragma unroll
@@ -430,19 +466,14 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_linear_big(LinearArgs A)
     static_assert(CA <= MB * NB && CB <= MB * NB, "room for the copies between the products");
     bool stored = false;  // the last tile's stores may still be in flight
     for (;;) {
-        float bias = 0.0f;  // of column lane of the wave's
-        static_assert(NB <= 2, "a column a lane");
-        if (KIND == LINEAR_Y && A.bias && now.real) {
-            const int e = now.n0 + (int)wn + (int)(NB == 2 ? lane : lane % 32);
-            bias = A.bias[(int64_t)now.group * A.cout + (e < A.cout ? e : A.cout - 1)];
-        }
+        const BigTile next = tile_at(now_round + 1);
+        const float next_bias = bias_of(next);  // loaded long before it is needed
         int k = 0;
         do {
-            const auto none = [](int) {};
             quarter(0, copy_a, C0);
             quarter(1, [&](int i) { copy_a(C0 + i); }, CA - C0);
             copied_a();
-            quarter(2, none, 0);
+            quarter(2, [&](int) { look_up(); }, KIND == LINEAR_DW ? 1 : 0);
             // All of this step's operands are read and both sides' copies for the next have landed.  Loads
             // and stores count in the order of issue: those after B's copies are A's for the step after
             // it, and before these, at a tile's start, the last one's stores (unless some were left out at an edge).
@@ -467,55 +498,54 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_linear_big(LinearArgs A)
             const int row = now.m0 + (int)wm + 32 * (int)(wave / WM) + l;
             if (now.n0 == 0 && a == 0 && row < now.m_end) (PART ? A.db_part : A.db)[(int64_t)(PART ? now.piece : now.group) * A.cout + row] = sum;
         }
+        // Stores of whole lines: the 16-byte pieces of a row that its two lanes hold are traded among the lanes
+        // 8 apart, so that eight lanes have 128 bytes of a row, and a store writes eight rows.
         const bool whole = now.m0 + BM <= now.m_end && now.n0 + BN <= n_end;
-        const auto piece = [&](int m, int n, int h, float (&v)[8]) {  // 8 elements in a row after the halves' exchange
+        const int j = l / 8;
+        const auto put = [&](Raw16 (&v)[4], int m, int first) {  // pieces 2q + a of the 8 from column `first` on
+            trade_lanes(v);
+            const int e = first + (2 * j + a) * (16 / (int)sizeof(Out)), row = now.m0 + (int)wm + 32 * m + l % 8;
+            Out *to = out + (int64_t)row * ld + e;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(acc[m][n][8 * h + i]), __float_as_uint(acc[m][n][8 * h + 4 + i]), false, false);
-                v[i] = __uint_as_float(r[0]);
-                v[4 + i] = __uint_as_float(r[1]);
+            for (int q = 0; q < 4; ++q) {
+                if (whole) *(Raw16Any *)(to + (int64_t)(8 * q) * ld) = v[q];
+                else if (row + 8 * q < now.m_end && e < n_end)
+                    store_raw(to + (int64_t)(8 * q) * ld, v[q], n_end - e < 16 / (int)sizeof(Out) ? n_end - e : 16 / (int)sizeof(Out));
             }
         };
 #pragma unroll
-        for (int n = 0; n < NB; ++n)
+        for (int m = 0; m < MB; ++m) {
+            Raw16 v[4];
+            if constexpr (OUT_F32) {
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                float b[8], v[8];
+                for (int n = 0; n < NB; ++n) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) b[i] = KIND == LINEAR_Y ? __shfl(bias, 32 * n + 16 * h + 8 * a + i, 64) : 0.0f;
-                const int e = now.n0 + (int)wn + 32 * n + 16 * h + 8 * a;
-                Out *to = out + (int64_t)(now.m0 + (int)wm + l) * ld + e;
-                const auto put = [&](Out *at, int have) {
-                    if constexpr (OUT_F32) {
-                        const float lo[4] = {v[0], v[1], v[2], v[3]}, hi[4] = {v[4], v[5], v[6], v[7]};
-                        store_raw(at, repack(lo, at), have < 4 ? have : 4);
-                        if (have > 4) store_raw(at + 4, repack(hi, at), have - 4);
-                    } else {
-                        store_raw(at, repack(v, at), have);
-                    }
-                };
-                if (whole) {
-#pragma unroll
-                    for (int m = 0; m < MB; ++m) {
-                        piece(m, n, h, v);
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) v[i] += b[i];
-                        put(to + (int64_t)(32 * m) * ld, 8);
-                    }
-                } else {
-#pragma unroll
-                    for (int m = 0; m < MB; ++m) {
-                        piece(m, n, h, v);
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) v[i] += b[i];
-                        if (now.m0 + (int)wm + 32 * m + l < now.m_end && e < n_end) put(to + (int64_t)(32 * m) * ld, n_end - e < 8 ? n_end - e : 8);
-                    }
+                    for (int q = 0; q < 4; ++q)
+                        v[q] = Raw16{__float_as_uint(acc[m][n][4 * q]), __float_as_uint(acc[m][n][4 * q + 1]), __float_as_uint(acc[m][n][4 * q + 2]),
+                                     __float_as_uint(acc[m][n][4 * q + 3])};
+                    put(v, m, now.n0 + (int)wn + 32 * n);
                 }
+            } else {
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {  // registers 8h .. + 3 and 8h + 4 .. + 7: 8 elements in a row after the halves' exchange
+                    const int n = q / 2, h = q % 2;
+                    float t[8];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(acc[m][n][8 * h + i]), __float_as_uint(acc[m][n][8 * h + 4 + i]), false, false);
+                        t[i] = __uint_as_float(r[0]);
+                        t[4 + i] = __uint_as_float(r[1]);
+                    }
+                    v[q] = repack(t, (const uint16_t *)nullptr);
+                }
+                put(v, m, now.n0 + (int)wn);
             }
+        }
         stored = whole;
-        now = tile_at(++now_round);
+        ++now_round;
+        now = next;
         if (!now.any) break;
-        clear();
+        begin(next_bias);
     }
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // no copy may land in LDS that the next block owns
 }
