@@ -145,4 +145,26 @@ int grouped_linear(LinearArgs A, int dtype, int kind, void *workspace, hipStream
 int grouped_linear_big(const LinearArgs &A, int dtype, int kind, int size, hipStream_t st);
 size_t linear_dw_workspace(int64_t n, int groups, int cin, int cout, int dtype);
 
+static __device__ __attribute__((aligned(16))) const uint32_t zero_piece[4] = {0, 0, 0, 0};
+
+// A piece of 16 bytes of a row is loaded without a branch, so that loads stay in flight: where the row ends inside it,
+// from s elements earlier, which are dropped later.  (Rows have a whole piece or more.)
+__device__ __forceinline__ Raw16 drop(Raw16 v, int s, const float *)  // s < 4
+{
+    if (s & 1) v = Raw16{v[1], v[2], v[3], 0};
+    if (s & 2) v = Raw16{v[2], v[3], 0, 0};
+    return v;
+}
+__device__ __forceinline__ Raw16 drop(Raw16 v, int s, const uint16_t *)  // s < 8
+{
+    if (s & 1) v = Raw16{v[0] >> 16 | v[1] << 16, v[1] >> 16 | v[2] << 16, v[2] >> 16 | v[3] << 16, v[3] >> 16};
+    if (s & 2) v = Raw16{v[1], v[2], v[3], 0};
+    if (s & 4) v = Raw16{v[2], v[3], 0, 0};
+    return v;
+}
+__device__ __forceinline__ Raw16 load_global(const void *p) { return *(const __attribute__((address_space(1))) Raw16Any *)(uintptr_t)p; }
+// Elements of the piece at `at` past the row's `end`, if it has any before it.
+template <int V>
+__device__ __forceinline__ int past(int at, int end) { return at < end && at + V > end ? at + V - end : 0; }
+
 }  // namespace sc

@@ -58,11 +58,11 @@ __device__ __forceinline__ Raw16 tile_operand(uint32_t lds, int block, int j)
     }
 }
 
-// Any widths, row distances and alignment: pieces of 16 bytes are loaded into registers, with what
-// is missing at the ends of rows as zeros, a step or two ahead, and written to LDS.  Four waves, each a quarter
-// of the tile.
+// Any widths, row distances and alignment: pieces of 16 bytes are loaded into registers a step or two ahead and
+// written to LDS, with what is missing at the ends of rows as zeros.  Four waves, each a quarter of the tile.
 // PART (LINEAR_DW): pieces of groups, whose sums are kept in fp32 for k_linear_join.
-template <typename T, int KIND, bool PART, int B>
+// SHORT: rows may be shorter than a piece, and are loaded by elements.
+template <typename T, int KIND, bool PART, int B, bool SHORT>
 __global__ __launch_bounds__(256) void k_linear(LinearArgs A)
 {
     using S = TileShape<T, B>;
@@ -124,64 +124,83 @@ __global__ __launch_bounds__(256) void k_linear(LinearArgs A)
         }
         if constexpr (!BKS) b_row[i] = n0 + r_[1][i] < n_end ? w + (int64_t)(n0 + r_[1][i]) * A.cin : nullptr;
     }
-    const auto left = [](int have) { return have < 0 ? 0 : (have < V ? have : V); };
     constexpr int AHEAD = B == 1 ? 2 : 1;  // steps that loads run ahead (more registers cost the large tiles a block a compute unit)
     Raw16 av_[AHEAD][2], bv_[AHEAD][2];
-    const auto load = [&](int k0, Raw16 (&av)[2], Raw16 (&bv)[2]) {
+    // elements from `at` on of a row of `end`
+    const auto load_piece = [&](const T *row, int at, int end) {
+        if constexpr (SHORT) {
+            return row && at < end ? load_raw(row + at, end - at < V ? end - at : V) : Raw16{0, 0, 0, 0};
+        } else {
+            const T *p = row + (at < end - V ? at : end - V);
+            return load_global(row && at < end ? p : (const T *)zero_piece);
+        }
+    };
+    int x_rows[2] = {0, 0};  // LINEAR_DW: of the next step, loaded a step ahead
+    const auto look_up = [&](int k0) {
+        if constexpr (KIND == LINEAR_DW) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            av[i] = bv[i] = Raw16{0, 0, 0, 0};
-            if constexpr (!AKS) {
-                const int nv = left(k_end - k0 - c_[0][i]);
-                if (a_row[i] && nv) av[i] = load_raw(a_row[i] + k0 + c_[0][i], nv);
-            } else {
-                const int nv = left(m_end - m0 - c_[0][i]), k = k0 + r_[0][i];
-                if (k < k_end && nv) av[i] = load_raw((const T *)A.g + (int64_t)(part.beg + k) * A.g_row + m0 + c_[0][i], nv);
+            for (int i = 0; i < 2; ++i) {
+                const int p = part.beg + k0 + r_[1][i];
+                x_rows[i] = p < A.n ? p : A.n - 1;
             }
-            if constexpr (!BKS) {
-                const int nv = left(k_end - k0 - c_[1][i]);
-                if (b_row[i] && nv) bv[i] = load_raw(b_row[i] + k0 + c_[1][i], nv);
-            } else {
-                const int nv = left(n_end - n0 - c_[1][i]), k = k0 + r_[1][i];
-                if (k < k_end && nv) {
-                    if constexpr (KIND == LINEAR_DX) {
-                        bv[i] = load_raw(w + (int64_t)k * A.cin + n0 + c_[1][i], nv);
-                    } else {
-                        const int r = A.rows ? A.rows[part.beg + k] : part.beg + k;
-                        if (r >= 0 && r < A.nx) bv[i] = load_raw((const T *)A.x + (int64_t)r * A.x_row + n0 + c_[1][i], nv);
-                    }
-                }
+            if (A.rows) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i) x_rows[i] = A.rows[x_rows[i]];
             }
         }
     };
-    f32x16 acc[B][B];
+    const auto load = [&](int k0, Raw16 (&av)[2], Raw16 (&bv)[2]) {
+        const int r_now[2] = {x_rows[0], x_rows[1]};
+        look_up(k0 + KT);  // (first: a wait for these is a wait for what was loaded before them too)
 #pragma unroll
-    for (int i = 0; i < B; ++i)
+        for (int i = 0; i < 2; ++i) {
+            const int ka = k0 + r_[0][i], kb = k0 + r_[1][i];
+            if constexpr (!AKS) av[i] = load_piece(a_row[i], k0 + c_[0][i], k_end);
+            else av[i] = load_piece(ka < k_end ? (const T *)A.g + (int64_t)(part.beg + ka) * A.g_row : nullptr, m0 + c_[0][i], m_end);
+            if constexpr (!BKS) bv[i] = load_piece(b_row[i], k0 + c_[1][i], k_end);
+            else if constexpr (KIND == LINEAR_DX) bv[i] = load_piece(kb < k_end ? w + (int64_t)kb * A.cin : nullptr, n0 + c_[1][i], n_end);
+            else bv[i] = load_piece(kb < k_end && r_now[i] >= 0 && r_now[i] < A.nx ? (const T *)A.x + (int64_t)r_now[i] * A.x_row : nullptr, n0 + c_[1][i], n_end);
+        }
+    };
+    // What was loaded of before the rows' ends is dropped, in the tiles and steps that have some.
+    const auto drop_ends = [&](int k0, Raw16 (&av)[2], Raw16 (&bv)[2]) {
+        if constexpr (SHORT) return;
+        if (AKS ? m0 + LT > m_end : k0 + KT > k_end)
 #pragma unroll
-        for (int n = 0; n < B; ++n)
+            for (int i = 0; i < 2; ++i) av[i] = drop(av[i], AKS ? past<V>(m0 + c_[0][i], m_end) : past<V>(k0 + c_[0][i], k_end), (const T *)nullptr);
+        if (BKS ? n0 + LT > n_end : k0 + KT > k_end)
 #pragma unroll
-            for (int e = 0; e < 16; ++e) acc[i][n][e] = 0.0f;
-    const int wm = (wave & 1) * (32 * B), wn = (wave >> 1) * (32 * B);
+            for (int i = 0; i < 2; ++i) bv[i] = drop(bv[i], BKS ? past<V>(n0 + c_[1][i], n_end) : past<V>(k0 + c_[1][i], k_end), (const T *)nullptr);
+    };
+    const int wm = (wave & 1) * (32 * B), wn = (wave >> 1) * (32 * B), half = (int)lane_id() >> 5;
+    f32x16 acc[B][B];  // a lane has row l % 32 of each block, its elements in the registers
     float sums[B];  // db: of a lane's share of its rows of grad
 #pragma unroll
     for (int i = 0; i < B; ++i) sums[i] = 0.0f;
     const bool summing = KIND == LINEAR_DW && A.db && n0 == 0 && wn == 0;
     const auto step = [&](int k0, int buf, Raw16 (&av)[2], Raw16 (&bv)[2]) {
+        drop_ends(k0, av, bv);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             lds_write16(lds + buf + tile_at<T, B, AKS>(r_[0][i], c_[0][i] / V), av[i]);
             lds_write16(lds + buf + BYTES + tile_at<T, B, BKS>(r_[1][i], c_[1][i] / V), bv[i]);
         }
         __syncthreads();
-        if (k0 + AHEAD * KT < k_end) load(k0 + AHEAD * KT, av, bv);
-#pragma unroll
-        for (int j = 0; j < S::KB / 32; ++j) {
-            Raw16 a[B], b[B];
+        load(k0 + AHEAD * KT, av, bv);  // zeros past the end: a load that may not be there costs a wait for all
+        Raw16 a_[2][B], b_[2][B];
+        const auto read = [&](int j) {
 #pragma unroll
             for (int i = 0; i < B; ++i) {
-                a[i] = tile_operand<T, B, AKS>(lds + buf, wm + 32 * i, j);
-                b[i] = tile_operand<T, B, BKS>(lds + buf + BYTES, wn + 32 * i, j);
+                a_[j % 2][i] = tile_operand<T, B, AKS>(lds + buf, wm + 32 * i, j);
+                b_[j % 2][i] = tile_operand<T, B, BKS>(lds + buf + BYTES, wn + 32 * i, j);
             }
+        };
+        read(0);
+#pragma unroll
+        for (int j = 0; j < S::KB / 32; ++j) {
+            Raw16 (&a)[B] = a_[j % 2], (&b)[B] = b_[j % 2];
+            if (j + 1 < S::KB / 32) read(j + 1);
+            __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
             for (int m = 0; m < B; ++m)
 #pragma unroll
@@ -198,9 +217,29 @@ __global__ __launch_bounds__(256) void k_linear(LinearArgs A)
             }
         }
     };
+    look_up(0);
     load(0, av_[0], bv_[0]);
+    if constexpr (AHEAD == 2) load(KT, av_[1], bv_[1]);
+    // sums begin with the bias
+#pragma unroll
+    for (int i = 0; i < B; ++i)
+#pragma unroll
+        for (int n = 0; n < B; ++n)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) acc[i][n][e] = 0.0f;
+    if (KIND == LINEAR_Y && A.bias && real) {
+        const float *bias = A.bias + (int64_t)group * A.cout;
+#pragma unroll
+        for (int n = 0; n < B; ++n)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const int e = n0 + wn + 32 * n + 8 * (i / 4) + 4 * half + i % 4;
+                const float v = bias[e < n_end ? e : n_end - 1];
+#pragma unroll
+                for (int m = 0; m < B; ++m) acc[m][n][i] = v;
+            }
+    }
     if constexpr (AHEAD == 2) {
-        load(KT, av_[1], bv_[1]);
         for (int k0 = 0; k0 < k_end; k0 += 2 * KT) {
             step(k0, 0, av_[0], bv_[0]);
             if (k0 + KT < k_end) step(k0 + KT, 2 * BYTES, av_[1], bv_[1]);
@@ -208,7 +247,6 @@ __global__ __launch_bounds__(256) void k_linear(LinearArgs A)
     } else {
         for (int k0 = 0, buf = 0; k0 < k_end; k0 += KT, buf ^= 2 * BYTES) step(k0, buf, av_[0], bv_[0]);
     }
-    // a lane has row l % 32 of each block, its elements in the registers
     const int l = lane_id() & 31;
     const int64_t ld = KIND == LINEAR_DW ? A.cin : A.out_row;
     typedef typename std::conditional<PART, float, T>::type Out;
@@ -234,14 +272,8 @@ __global__ __launch_bounds__(256) void k_linear(LinearArgs A)
                     v[i] = __uint_as_float(r[0]);
                     v[4 + i] = __uint_as_float(r[1]);
                 }
-                const int e = n0 + wn + 32 * n + 16 * h + 8 * (int)(lane_id() >> 5);
+                const int e = n0 + wn + 32 * n + 16 * h + 8 * half;
                 if (!valid || e >= n_end) continue;
-                if (KIND == LINEAR_Y && A.bias && real) {
-                    const float *b = A.bias + (int64_t)group * A.cout + e;
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        if (e + i < n_end) v[i] += b[i];
-                }
                 Out *to = out + (int64_t)row * ld + e;
                 if constexpr (sizeof(Out) == 2) {
                     store_raw(to, repack(v, to), n_end - e < 8 ? n_end - e : 8);
@@ -257,7 +289,7 @@ __global__ __launch_bounds__(256) void k_linear(LinearArgs A)
 // y for few rows a group (single tokens): bound by reading each weight once.  A block takes 16 positions and
 // 16 NB columns; its four waves take a quarter of each run of k, with all their loads in flight, straight
 // into the matrix instruction's operands (16 x 16, columns of y in the rows), and their sums are added in LDS.
-template <typename T, int NB>
+template <typename T, int NB, bool SHORT>
 __global__ __launch_bounds__(256) void k_linear_few(LinearArgs A, int steps)
 {
     constexpr int V = VEC<T>, KS = 4 * V, STEPS = 8;  // k of a step; most steps of a wave at a time
@@ -283,10 +315,28 @@ __global__ __launch_bounds__(256) void k_linear_few(LinearArgs A, int steps)
 #pragma unroll
         for (int s = 0; s < STEPS; ++s) {
             if (s >= steps) break;
-            const int k = k0 + s * KS + q * V, nv = k_end - k < 0 ? 0 : (k_end - k < V ? k_end - k : V);
+            const int k = k0 + s * KS + q * V;
+            const auto load_piece = [&](const T *row) {
+                if constexpr (SHORT) {
+                    return row && k < k_end ? load_raw(row + k, k_end - k < V ? k_end - k : V) : Raw16{0, 0, 0, 0};
+                } else {
+                    const T *p = row + (k < k_end - V ? k : k_end - V);
+                    return load_global(row && k < k_end ? p : (const T *)zero_piece);
+                }
+            };
 #pragma unroll
-            for (int b = 0; b < NB; ++b) wv[s][b] = load_raw(wr[b] + (nv ? k : 0), nv);
-            xv[s] = x ? load_raw(x + (nv ? k : 0), nv) : Raw16{0, 0, 0, 0};
+            for (int b = 0; b < NB; ++b) wv[s][b] = load_piece(wr[b]);
+            xv[s] = load_piece(x);
+        }
+        if (!SHORT && k0 + steps * KS > k_end) {
+#pragma unroll
+            for (int s = 0; s < STEPS; ++s) {
+                if (s >= steps) break;
+                const int over = past<V>(k0 + s * KS + q * V, k_end);
+#pragma unroll
+                for (int b = 0; b < NB; ++b) wv[s][b] = drop(wv[s][b], over, (const T *)nullptr);
+                xv[s] = drop(xv[s], over, (const T *)nullptr);
+            }
         }
 #pragma unroll
         for (int s = 0; s < STEPS; ++s) {
@@ -379,6 +429,13 @@ static bool may_be_big(int cin, int cout, int dtype)
     return cin % v == 0 && cout % v == 0;
 }
 
+// Whether rows may have less than a piece of 16 bytes.
+static bool is_short(int cin, int cout, int dtype)
+{
+    const int v = dtype == SUBMCONV_F32 ? 4 : 8;
+    return cin < v || cout < v;
+}
+
 // The kernel by sizes alone; `aligned`: whole pieces of 16 bytes everywhere.
 static int choose(int64_t n, int groups, int cin, int cout, int dtype, int kind, bool aligned)
 {
@@ -387,6 +444,7 @@ static int choose(int64_t n, int groups, int cin, int cout, int dtype, int kind,
         const int64_t few = most_tiles(n, groups, 16) * ((cout + 31) / 32);
         if (n <= FEW_ROWS * (int64_t)groups || few <= (dtype == SUBMCONV_F32 ? 2 : 1) * FEW_BLOCKS) return BY_FEW;
     }
+    if (is_short(cin, cout, dtype)) return BY_SMALL;
     const bool f32 = dtype == SUBMCONV_F32, ring = aligned && may_be_big(cin, cout, dtype);
     const double work = (double)n * cin * cout;
     if (kind == LINEAR_DW) {
@@ -438,16 +496,21 @@ int grouped_linear(LinearArgs A, int dtype, int kind, void *workspace, hipStream
         constexpr int NB = 2;
         const int ks = dtype == SUBMCONV_F32 ? 16 : 32, quarter = (A.cin + 4 * ks - 1) / (4 * ks), steps = quarter < 8 ? quarter : 8;
         const dim3 grid((unsigned)(most_tiles(A.n, A.groups, 16) * ((A.cout + 16 * NB - 1) / (16 * NB))));
-        if (dtype == SUBMCONV_F32) hipLaunchKernelGGL((k_linear_few<float, NB>), grid, dim3(256), 0, st, A, steps);
-        else hipLaunchKernelGGL((k_linear_few<uint16_t, NB>), grid, dim3(256), 0, st, A, steps);
+#define GO(T)                                                                                                   \
+    if (A.cin < VEC<T>) hipLaunchKernelGGL((k_linear_few<T, NB, true>), grid, dim3(256), 0, st, A, steps);      \
+    else hipLaunchKernelGGL((k_linear_few<T, NB, false>), grid, dim3(256), 0, st, A, steps)
+        if (dtype == SUBMCONV_F32) { GO(float); } else { GO(uint16_t); }
+#undef GO
         SC_LAUNCHED("grouped_linear");
     } else if (by >= BY_RING) {
         SC_CHECK(grouped_linear_big(A, dtype, kind, TILE_OF[by], st));
     } else {
         const dim3 grid((unsigned)linear_tiles(A.n, A.groups, A.cin, A.cout, kind, A.chunk, TILE_OF[by]));
-#define GO(T, KIND, PART)                                                                             \
-    if (by == BY_SMALL) hipLaunchKernelGGL((k_linear<T, KIND, PART, 1>), grid, dim3(256), 0, st, A);  \
-    else hipLaunchKernelGGL((k_linear<T, KIND, PART, 2>), grid, dim3(256), 0, st, A)
+        const bool by_elements = is_short(A.cin, A.cout, dtype);  // (never in tiles of 128)
+#define GO(T, KIND, PART)                                                                                                  \
+    if (by_elements) hipLaunchKernelGGL((k_linear<T, KIND, PART, 1, true>), grid, dim3(256), 0, st, A);     \
+    else if (by == BY_SMALL) hipLaunchKernelGGL((k_linear<T, KIND, PART, 1, false>), grid, dim3(256), 0, st, A);           \
+    else hipLaunchKernelGGL((k_linear<T, KIND, PART, 2, false>), grid, dim3(256), 0, st, A)
 #define BY_KIND(T)                                              \
     if (kind == LINEAR_Y) { GO(T, LINEAR_Y, false); }           \
     else if (kind == LINEAR_DX) { GO(T, LINEAR_DX, false); }    \

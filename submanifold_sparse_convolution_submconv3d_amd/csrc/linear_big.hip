@@ -19,8 +19,6 @@
 
 namespace sc {
 
-__device__ __attribute__((aligned(16))) const uint32_t zero_piece[4] = {0, 0, 0, 0};
-
 // A tile of the result: rows m0 .. m_end of part, from column n0 on; k_end terms a sum.
 struct BigTile {
     int m0, m_end, n0, k_end, group;
