@@ -393,16 +393,28 @@ __global__ __launch_bounds__(256) void k_linear_join(LinearArgs A)
     else ((T *)A.out)[group * size + i] = Elem<T>::from_f32(sum);
 }
 
-// The rules below were measured over 1 to 8 groups of 1 to 8192 rows, widths of 64 to 4096, in us:
-//   few rows (16 a tile) against the ring of 128, bf16, 8 groups 1024 -> 1024: 32 rows each 12.7 and 15.5, 64 16.2 and 15.3;
-//   against tiles of 64, fp32: 64 rows 34 and 46, 128 64 and 47.
-//   The rings of 128 and 256, bf16: 8 x 512 x 1024 -> 1024 18 and 30, 8 x 2048 44 and 40, 8 x 8192 166 and 145.
-//   Tiles of 64 and the ring of 128, fp32: 8 x 256 x 1024 -> 1024 60 and 77, 8 x 512 97 and 80, 8 x 8192 1368 and 1070.
-//   Tiles of 64 and 128 (unaligned), fp32: 8 x 512 x 1024 -> 1024 97 and 119, 8 x 2048 352 and 339, 8 x 8192 1368 and 1258.
-//   dw, tiles of 64, 128 and the ring of 256, bf16: 8 x 128 x 1024 x 1024 15, 13 and 16, 8 x 256 23, 21 and 20, 8 x 2048 106, 110 and 65;
-//   tiles of 64, 128 and the ring of 128, fp32: 8 x 128 39, 38 and 33, 8 x 256 62, 63 and 51; 8 x 8192 x 64 x 256 43, 63 and 56.
-constexpr int64_t FEW_ROWS = 16, FEW_BLOCKS = 1024, SMALL_TILES = 640, BIG_OUT = 1 << 24, RING_OUT = 1 << 22;
-constexpr double RING_DW = 2e9, LARGE_DW = 4e9;
+// The rules below were measured over 1 to 8 groups of 1 to 8192 rows, widths of 61 to 4096, in us; what they compare
+// is the blocks or tiles of a call, n cols, and n cin cout.
+//   y, few rows (16 a tile) and tiles of 64, bf16: 8 groups of 1024 -> 4096, 1 row each, 16.2 and 14.0 (660 tiles of 64);
+//     3 x 64 x 1001 -> 999 18.0 and 11.2 (544 blocks of few); fp32: 1 x 256 x 1024 -> 1024 18.7 and 26.5 (576),
+//     8 x 32 x 1024 -> 1024 19.3 and 26.7 (832), 64 rows 33.2 and 27.4 (1344), 5 x 512 x 501 -> 123 14.8 and 15.9 (668).
+//   y, tiles of 64 and the ring of 128, bf16: 8 x 64 x 1024 -> 1024 11.8 and 15.6, 256 rows 14.0 and 16.6, 512 21.0 and 18.1;
+//     dx, 8 x 64 x 1024 -> 4096 32.5 and 39.8; fp32: 8 x 256 x 1024 -> 1024 46 and 77, 512 rows 82 and 77;
+//     dx, 8 x 8192 x 64 -> 256 37.5 and 46.0 (half of a tile of 128 is empty).
+//   y and dx, the rings of 128 and 256, bf16: 8 x 512 x 1024 -> 1024 18 and 30, 8 x 2048 44 and 40, 8 x 8192 166 and 145.
+//   y and dx, tiles of 64 and 128 (unaligned), bf16: 3 x 1024 x 1001 -> 999 24.2 and 32.3 (192 tiles of 128), 8 x 512 x 255 ->
+//     1023 15.3 and 14.8 (256), dx 3 x 2048 x 1001 -> 999 42.6 and 35.0 (384); fp32: dx 8 x 4096 x 255 -> 1023 175 and 158 (512).
+//   dw, tiles of 64 and 128, bf16: 5 x 4096 x 123 x 501 31.5 and 26.2 (1.3e9 products), fp32: 5 x 8192 x 123 x 501 89 and 83
+//     (2.5e9), 8 x 32 x 1024 x 1024 19.0 and 16.7 (512 tiles);
+//     tiles of 128 and the ring of 256, bf16: 8 x 256 x 1024 x 1024 15.1 and 19.1, 8 x 512 21.7 and 26.0, 8 x 8192 x 256 x 256 49.6
+//     and 39.4, 8 x 2048 x 1024 x 1024 106 and 62;
+//     tiles of 128 and the ring of 128, fp32: 8 x 128 x 1024 x 1024 32.8 and 35, 8 x 256 63 and 51; 8 x 8192 x 64 x 256 63 and 56.
+constexpr int64_t FEW_ROWS = 16, BIG_OUT = 1 << 24, RING_OUT = 1 << 22;
+constexpr int64_t few_blocks(bool f32) { return f32 ? 1024 : 512; }  // at most, for few rows
+constexpr int64_t few_tiles(bool f32) { return f32 ? INT64_MAX : 512; }  // of 64, up to FEW_ROWS a group
+constexpr int64_t large_tiles(bool f32) { return f32 ? 512 : 288; }  // of 128 from here on, ends of groups not counted
+constexpr double ring_dw(bool f32) { return f32 ? 2e9 : 4e9; }
+constexpr double large_dw(bool f32) { return f32 ? 2e9 : 1.2e9; }
 
 // Which kernel takes a call.
 enum { BY_FEW, BY_SMALL, BY_LARGE, BY_RING, BY_BIG };  // (the last two: linear_big.hip)
@@ -440,20 +452,20 @@ static bool is_short(int cin, int cout, int dtype)
 static int choose(int64_t n, int groups, int cin, int cout, int dtype, int kind, bool aligned)
 {
     const int cols = kind == LINEAR_Y ? cout : cin;
+    const bool f32 = dtype == SUBMCONV_F32, ring = aligned && may_be_big(cin, cout, dtype);
     if (kind == LINEAR_Y) {
-        const int64_t few = most_tiles(n, groups, 16) * ((cout + 31) / 32);
-        if (n <= FEW_ROWS * (int64_t)groups || few <= (dtype == SUBMCONV_F32 ? 2 : 1) * FEW_BLOCKS) return BY_FEW;
+        const int64_t blocks = most_tiles(n, groups, 16) * ((cout + 31) / 32);
+        if (blocks <= few_blocks(f32) || (n <= FEW_ROWS * (int64_t)groups && linear_tiles(n, groups, cin, cout, kind, 0, 64) <= few_tiles(f32))) return BY_FEW;
     }
     if (is_short(cin, cout, dtype)) return BY_SMALL;
-    const bool f32 = dtype == SUBMCONV_F32, ring = aligned && may_be_big(cin, cout, dtype);
     const double work = (double)n * cin * cout;
     if (kind == LINEAR_DW) {
-        if (ring && work >= RING_DW && cin >= 96 && cout >= 96 && (f32 || (cin >= 192 && cout >= 192))) return f32 ? BY_RING : BY_BIG;
-        return work >= LARGE_DW || linear_tiles(n, groups, cin, cout, kind, 0, 128) >= SMALL_TILES ? BY_LARGE : BY_SMALL;
+        if (ring && work >= ring_dw(f32) && cin >= 96 && cout >= 96 && (f32 || (cin >= 192 && cout >= 192))) return f32 ? BY_RING : BY_BIG;
+        return work >= large_dw(f32) || linear_tiles(n, groups, cin, cout, kind, 0, 128) >= 512 ? BY_LARGE : BY_SMALL;
     }
-    if (ring && !f32) return n * cols >= BIG_OUT && cols >= 192 ? BY_BIG : BY_RING;
-    if (ring && n * cols >= RING_OUT) return BY_RING;
-    return linear_tiles(n, groups, cin, cout, kind, 0, 128) >= SMALL_TILES ? BY_LARGE : BY_SMALL;
+    if (ring && !f32 && n * cols >= BIG_OUT && cols >= 192) return BY_BIG;
+    if (ring && n * cols >= RING_OUT && cols >= 96) return BY_RING;
+    return n / 128 * ((cols + 127) / 128) >= large_tiles(f32) ? BY_LARGE : BY_SMALL;
 }
 
 size_t linear_dw_workspace(int64_t n, int groups, int cin, int cout, int dtype)
