@@ -10,7 +10,12 @@
 // heads of RB rows; a lane keeps its head and walks rows, so that the weight and the sums of dw
 // stay in registers.  The heads of a row turn by the same angles: the block forms the sines and
 // cosines of its RB rows once, in LDS, while the rows before them are worked on (an angle costs
-// some 60 instructions, about what a piece may take at the memory's rate).
+// some 60 instructions, about what a piece may take at the memory's rate).  Two rows a lane at a time keep enough loads
+// in flight; the launch is as many blocks as the card holds at once, so that none waits for a place.
+//
+// Measured in bf16: forward 20,384 x 16 heads of 128, packed, 34 us (4.9 TB/s, the rate of a copy); 400,311 x 12 of
+// 64 forward 251 us (4.9 TB/s), backward 429 (4.3; one row a lane 462, twice the blocks 445 to 460), dw's sums 5.
+// 450 x 4 of 64 in fp32: 4 us, a launch and three memory latencies.
 #include "headnorm.h"
 
 namespace sc {
@@ -380,7 +385,7 @@ size_t head_norm_bwd_workspace(int64_t n, int heads, int dim, int dtype, int wei
     return (size_t)most * weight_rows * dim * sizeof(float);
 }
 
-// Bytes of LDS: two sets of angles (at most 32 KB a row of a lane's: a block has 256 / L rows of at most L V pairs).
+// Bytes of LDS: two sets of angles, at most 64 KB (256 / L rows a block of at most L V pairs each, HEAD_ROWS of them a lane).
 static size_t head_lds(const HeadNormArgs &A, const HeadShape &s) { return (size_t)2 * HEAD_ROWS * s.rb * A.ax.end[SUBMCONV_ROTARY_MAX_AXES - 1] * sizeof(float2); }
 
 #define HEAD_LANES(K, T, P, SPLIT)                                                                  \

@@ -11,7 +11,10 @@
 //   dW   cout         cin    positions  grad, k a row apart        x, k a row apart
 //
 // Sums are fp32; one rounding to the tensors' type at the end.  Every result element is summed by
-// one lane in a fixed order, so the same call gives the same bits.
+// one lane in a fixed order (or by a few whose sums are added in a fixed order), so the same call gives the same bits.
+//
+// Here: tiles of 64 and 128 for any alignment and for calls of middling size, and a kernel for few rows; linear_big.hip
+// has the large tiles.  Offsets are read on the device; a block finds its tile from them.
 #include <type_traits>
 
 #include "linear.h"
@@ -60,6 +63,11 @@ __device__ __forceinline__ Raw16 tile_operand(uint32_t lds, int block, int j)
 
 // Any widths, row distances and alignment: pieces of 16 bytes are loaded into registers a step or two ahead and
 // written to LDS, with what is missing at the ends of rows as zeros.  Four waves, each a quarter of the tile.
+// Loads without branches are what counts: with one at each row's end the compiler waited for every load before the next
+// (3 x 3000 rows of 1001 -> 999 in fp32, y, dx, dw with db: 211, 253, 318 us; now 172, 188, 222, 105 to 80 TFLOP/s).
+// 20,384 rows of 123 -> 501 in fp32: 44, 42, 47 us and 8 for the pieces' sums, where 17 is the matrix cores' time: one
+// or two rounds of short blocks, whose first loads and last stores nothing covers, and unaligned 16-byte accesses.
+// Weights that few rows share are read at the memory's rate: 8 x 1 rows of 1024 -> 4096 in bf16 11.6 us for 67 MB.
 // PART (LINEAR_DW): pieces of groups, whose sums are kept in fp32 for k_linear_join.
 // SHORT: rows may be shorter than a piece, and are loaded by elements.
 template <typename T, int KIND, bool PART, int B, bool SHORT>
@@ -143,7 +151,7 @@ __global__ __launch_bounds__(256) void k_linear(LinearArgs A)
                 const int p = part.beg + k0 + r_[1][i];
                 x_rows[i] = p < A.n ? p : A.n - 1;
             }
-            if (A.rows) {
+            if (A.rows && A.n) {
 #pragma unroll
                 for (int i = 0; i < 2; ++i) x_rows[i] = A.rows[x_rows[i]];
             }
@@ -286,7 +294,8 @@ __global__ __launch_bounds__(256) void k_linear(LinearArgs A)
     }
 }
 
-// y for few rows a group (single tokens): bound by reading each weight once.  A block takes 16 positions and
+// y for few rows a group (single tokens): bound by reading each weight once, or by the launch (450 x 2 rows of 64 -> 256
+// in fp32: 5.6 us; tiles of 64 take as long there, but 25 instead of 8 where 1024 of k are walked by few blocks).  A block takes 16 positions and
 // 16 NB columns; its four waves take a quarter of each run of k, with all their loads in flight, straight
 // into the matrix instruction's operands (16 x 16, columns of y in the rows), and their sums are added in LDS.
 template <typename T, int NB, bool SHORT>

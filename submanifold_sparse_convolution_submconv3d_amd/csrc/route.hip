@@ -12,7 +12,10 @@
 //   k_route_place  a block's pairs to their places, in order
 // (few pairs: the first kernel alone; up to 64 blocks: without the second)
 // All counts are whole numbers, so the plan does not depend on the order of atomics.  Each kernel
-// is bound by memory where rows are many (the scores are read once), and by its launch where few.
+// is bound by its launches where rows are few (450 x 8 fp32, k = 2: one kernel, 9 us), by memory and instructions where
+// many.  1,187,403 x 64 fp32, k = 4: top 108 us, scan 8, place 32, backward 122, where reading the scores once takes 62
+// and reading them and writing their gradient 123 at the rate of a copy: the backward pass is at it, the top k is bound by
+// the instructions of its sorting, and the scan by the latency of one block's walk for each expert.
 #include "rowvec.h"
 
 namespace sc {

@@ -194,6 +194,21 @@ def test_grouped_linear_parts_of_the_gradient():
         sc.submconv_grouped_linear_backward(g, x, w, off, need_weight=False, need_bias=True)
 
 
+@pytest.mark.parametrize("cin", [3, 64, 77])
+def test_grouped_linear_rows_of_no_positions(cin):
+    """The library's function with rows, but no positions: the weight's gradients are zeros and no row number is read."""
+    import ctypes
+    from submanifold_sparse_convolution_submconv3d_amd import load_library
+    x, rows, off = torch.ones((4, cin), device=DEV), ints([0, 1]), ints([0, 0, 0])
+    dw, db = torch.full((2, 5, cin), 7.0, device=DEV), torch.full((2, 5), 7.0, device=DEV)
+    ws = torch.empty(1 << 20, dtype=torch.uint8, device=DEV)
+    note("linear rows of no positions %d" % cin)
+    code = load_library().submconv_grouped_linear_backward(
+        None, 5, x.data_ptr(), cin, 4, rows.data_ptr(), None, off.data_ptr(), 2, 0, cin, 5, sc.F32, None, cin, dw.data_ptr(),
+        ctypes.cast(db.data_ptr(), ctypes.c_void_p), ws.data_ptr(), ws.numel(), torch.cuda.current_stream().cuda_stream)
+    assert code == 0 and not dw.any() and not db.any()
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_grouped_linear_offsets_past_32_bits(dtype):
     """Rows that lie more than 2^32 elements into their tensors."""

@@ -33,7 +33,8 @@ CASES = [("bf16", 200, 2056, 3, 9001), ("bf16", 2056, 200, 3, 9001), ("bf16", 72
          ("f32", 264, 516, 3, 9000), ("f32", 516, 264, 3, 9000), ("f32", 300, 520, 2, 14000), ("f32", 512, 512, 20, 9000),
          ("f32", 132, 1028, 70, 8000), ("bf16", 257, 1023, 3, 11000), ("bf16", 515, 1023, 3, 9000), ("f32", 257, 1023, 3, 11000),
          ("f32", 515, 1023, 3, 9000), ("bf16", 200, 2056, 3, 20001), ("bf16", 2056, 200, 3, 20001), ("bf16", 264, 520, 2, 60000),
-         ("bf16", 512, 512, 70, 31000), ("bf16", 1024, 1024, 16, 8000), ("bf16", 136, 520, 70, 9000), ("bf16", 520, 136, 5, 40000)]
+         ("bf16", 512, 512, 70, 31000), ("bf16", 1024, 1024, 16, 8000), ("bf16", 136, 520, 70, 9000), ("bf16", 520, 136, 5, 40000),
+         ("f32", 3, 517, 3, 90000), ("bf16", 515, 5, 3, 90000)]
 
 
 @pytest.mark.parametrize("dtype,cin,cout,groups,n", CASES)
