@@ -9,10 +9,12 @@
 // read from LDS meanwhile.  Before the last quarter its operands are in registers: after the step's one barrier there the
 // next step's copies, which have landed, are read, and the places that are done with are filled again.
 //
-// Measured, 8 groups over 40,768 rows of 1024 -> 4096 in bf16 (342 GFLOP a product): forward 347-400 us, dx 330-370,
-// dW with db 400-465 (the lower when alone; together with the others the card's power holds the clock near 1.8 GHz):
-// 0.73-0.99 PFLOP/s.  What bounds them then is the matrix cores: 67% busy in dx, 52% in the forward, 43% in dW, whose
-// operands come through transposing reads of LDS, 2 a product; and dx's 2.56 rounds of tiles, which take three.
+// Measured, 8 groups over 40,768 rows of 1024 -> 4096 in bf16 (342 GFLOP a product): forward 347-410 us, dx 330-375,
+// dW with db 400-470 (the lower when cool; in a row the card's power holds the clock near 1.8 GHz): 0.73-1.03 PFLOP/s.
+// What bounds them then is the matrix cores' waiting for operands: they are busy 67% of the time in dx, 52% in the forward,
+// 43% in dW, whose operands come through transposing reads of LDS, two a piece; and dx's 2.56 rounds of tiles take three.
+// Tiles of 128 in fp32, 8 x 8192 rows of 1024 -> 1024: 1064, 1041 and 1102 us, 125-132 TFLOP/s of the 152 that a library's
+// product of 8192^3 reaches.
 #include <type_traits>
 
 #include "linear.h"
