@@ -510,7 +510,8 @@ int submconv_route(const void *logits, int64_t row, int64_t n, int32_t experts, 
  * Gradient of the gates of submconv_route: with d_j = grad[i,j] gates[i,j],
  *     dlogits[i,e] = (sum of d_j with chosen[i,j] = e) - p_e sum_j d_j
  * where p is the softmax over the chosen experts (normalize = 1) or over all (0; a row with no open
- * expert gives zeros).  Numbers outside [0, experts) in chosen stand for no expert.
+ * expert gives zeros).  Numbers outside [0, experts) in chosen stand for no expert; with a gate of 0, as submconv_route
+ * leaves it beside a -1, such a pair adds nothing, whatever its grad is (NaN and infinities too).
  *   grad, gates : device fp32 [n, k];  chosen : device int32 [n, k];  logits : as in submconv_route
  *   (not read, may be NULL, with normalize = 1);  dlogits : device [n, experts] of dtype, out_row >= experts.
  * fp32, one rounding at the end.  Asynchronous, one launch.

@@ -915,7 +915,7 @@ def submconv_route(logits: torch.Tensor, k: int, normalize: bool = True) -> Rout
 def submconv_route_backward(grad: torch.Tensor, logits: torch.Tensor, experts: torch.Tensor, gates: torch.Tensor,
                             normalize: bool = True) -> torch.Tensor:
     """Gradient of the scores [N,E] from the gradient of submconv_route's gates, fp32 [N,k] -> dlogits, of
-    logits' type.  experts and gates are the Route's, normalize as in its call."""
+    logits' type.  experts and gates are the Route's, normalize as in its call.  What grad holds beside a -1 is not used."""
     dev = _strided(logits, "logits", 2).device
     n, e = logits.shape
     k = gates.shape[1] if gates.dim() == 2 else 0

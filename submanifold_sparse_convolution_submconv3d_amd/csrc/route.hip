@@ -319,7 +319,8 @@ __global__ __launch_bounds__(256) void k_route_place(const int32_t *__restrict__
 
 // dL/dscore of expert e: with d_j = dgate_j gate_j,  [e = expert j] d_j - p_e sum(d)  where p is the
 // softmax over the chosen experts or over all.  K: most experts of a row; their numbers, gates and
-// gradients are all loaded at once.
+// gradients are all loaded at once.  A pair of no expert has a gate of 0, and its gradient may be anything (that of a
+// logarithm of the gate is infinite): its d is 0, not 0 times that.
 template <typename T, int L, int CH, int K>
 __global__ __launch_bounds__(256) void k_route_bwd(const float *__restrict__ grad, const T *__restrict__ logits, int64_t ld, int64_t n,
                                                    int experts, int k, int normalize, const int32_t *__restrict__ chosen,
@@ -350,6 +351,9 @@ __global__ __launch_bounds__(256) void k_route_bwd(const float *__restrict__ gra
             gate[j] = gates[at];
             d[j] = grad[at];
         }
+#pragma unroll
+        for (int j = 0; j < K; ++j)
+            if ((uint32_t)number[j] >= (uint32_t)experts && gate[j] == 0.0f) d[j] = 0.0f;
         float sum = 0.0f;
 #pragma unroll
         for (int j = 0; j < K; ++j)
