@@ -69,6 +69,7 @@ _LIB_PATH = os.path.join(_HERE, "_lib", "libsubmconv.so")
 
 F32, BF16 = 0, 1
 OUT_F32 = 256  # added to the type code of an attention call whose out is fp32 (SUBMCONV_OUT_F32)
+ROUTE_MAX_K = 16  # SUBMCONV_ROUTE_MAX_K
 KERNEL_AUTO, KERNEL_GENERIC, KERNEL_LOWC, KERNEL_MFMA, KERNEL_WINDOW, KERNEL_PERSISTENT = 0, 1, 2, 3, 4, 5
 
 _lib = None
@@ -894,8 +895,8 @@ def submconv_route(logits: torch.Tensor, k: int, normalize: bool = True) -> Rout
     (offsets, rows) and submconv_combine (slots, gates); it is exact and formed on the device."""
     dev = _strided(logits, "logits", 2).device
     n, e = logits.shape
-    k = int(k)
-    m = max(k, 0)
+    k = max(-1, min(int(k), 2 ** 31 - 1))       # what the library refuses, it refuses whole,
+    m = k if 0 < k <= ROUTE_MAX_K else 0        # and nothing is allocated for
     experts = torch.empty((n, m), dtype=torch.int32, device=dev)
     slots = torch.empty((n, m), dtype=torch.int32, device=dev)
     rows = torch.empty(n * m, dtype=torch.int32, device=dev)
