@@ -447,7 +447,7 @@ int submconv_attention_backward(const void *grad, const void *q, const void *k, 
  *   dim    : even, 2..512.   heads : 1..1024.   eps >= 0.
  *   rstd   : device fp32 [n, heads] for the backward pass, or NULL.
  * The norm and the rotation are fp32, with one rounding to dtype at the end (the two calls
- * submconv_rotary and a norm round twice).  Asynchronous, one launch.
+ * submconv_rotary and a norm round twice).  Squares may leave fp32's range; rstd has to be in it.  Asynchronous, one launch.
  */
 int submconv_head_norm_rotary(const void *x, int64_t x_row, int64_t x_head, const void *weight, int32_t weight_rows,
                               int32_t q_heads, int32_t param_dtype, float eps, const int32_t *positions,

@@ -114,6 +114,27 @@ struct HeadPieces {
     }
 };
 
+// Squares leave fp32 above 2^64 and lose bits below 2^-63, though 1 / sqrt of their mean is an ordinary number there.  A mean
+// of 2^-100 to 2^120 is right (512 squares at most, and those below 2^-126 do not count).
+__device__ __forceinline__ bool head_mean_fits(float mean) { return mean >= 0x1p-100f && mean <= 0x1p+120f; }
+
+// 1 / sqrt(mean + eps) of a head whose mean is not: of the squares of c times the head, c a power of two.  2^-70 takes the
+// largest values to 2^58, whose squares' sum stays below 2^126; 2^90 takes those of a mean below 2^-100 to 2^45 at most.
+template <int L, int P, int V>
+__device__ __forceinline__ float head_rstd_far(const float (&v)[P][V], float mean, float dim, float eps)
+{
+    const float c = mean > 1.0f ? 0x1p-70f : 0x1p+90f;
+    float s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < P; ++i)
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const float t = v[i][j] * c;
+            s += t * t;
+        }
+    return rsqrtf(lanes_sum<L>(s) / dim + eps * c * c) * c;
+}
+
 constexpr int HEAD_ROWS = 2;  // rows of a lane at a time, their loads issued together
 
 // out may be x (so neither is restrict).
@@ -174,7 +195,13 @@ __global__ __launch_bounds__(256) void k_head_norm(HeadNormArgs A)
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const float rs = rsqrtf(lanes_sum<L>(s[u]) / dim + A.eps);
+            const float mean = lanes_sum<L>(s[u]) / dim + A.eps;
+            float rs = rsqrtf(mean);
+            // (a wave's branch, for few instructions: 20,384 x 16 heads of 128, packed, 31.2 -> 31.5 us; always both ways 33.8)
+            if (__builtin_expect(__ballot(!head_mean_fits(mean)) != 0, 0)) {
+                const float far = head_rstd_far<L>(v[u], mean, dim, A.eps);
+                rs = head_mean_fits(mean) ? rs : far;
+            }
 #pragma unroll
             for (int i = 0; i < P; ++i)
 #pragma unroll
