@@ -11,10 +11,12 @@
 // stay in registers.  The heads of a row turn by the same angles: the block forms the sines and
 // cosines of its RB rows once, in LDS, while the rows before them are worked on (an angle costs
 // some 60 instructions, about what a piece may take at the memory's rate).  Two rows a lane at a time keep enough loads
-// in flight; the launch is as many blocks as the card holds at once, so that none waits for a place.
+// in flight; the launch is as many blocks as the card holds at once of the bf16 kernels for paired halves, which have the
+// most registers, so that none waits for a place (of the others it would hold up to twice as many; not tried).
 //
-// Measured in bf16: forward 20,384 x 16 heads of 128, packed, 34 us (4.9 TB/s, the rate of a copy); 400,311 x 12 of
-// 64 forward 251 us (4.9 TB/s), backward 429 (4.3; one row a lane 462, twice the blocks 445 to 460), dw's sums 5.
+// Measured: forward 20,384 x 16 heads of 128 in bf16, packed, 34 us (4.9 TB/s, the rate of a copy); 400,311 x 12 of 64,
+// paired halves, bf16: forward 248 us (5.0 TB/s), backward 419 (4.4; one row a lane 462, twice the blocks 445 to 460), dw's
+// sums 5; fp32 447 (5.5) and 689 (5.4); neighbours as pairs, bf16 295 (4.2) and 481 (3.8), fp32 494 (5.0) and 854 (4.3).
 // 450 x 4 of 64 in fp32: 4 us, a launch and three memory latencies.
 #include "headnorm.h"
 

@@ -64,10 +64,11 @@ __device__ __forceinline__ Raw16 tile_operand(uint32_t lds, int block, int j)
 // Any widths, row distances and alignment: pieces of 16 bytes are loaded into registers a step or two ahead and
 // written to LDS, with what is missing at the ends of rows as zeros.  Four waves, each a quarter of the tile.
 // Loads without branches are what counts: with one at each row's end the compiler waited for every load before the next
-// (3 x 3000 rows of 1001 -> 999 in fp32, y, dx, dw with db: 211, 253, 318 us; now 172, 188, 222, 105 to 80 TFLOP/s).
+// (3 x 3000 rows of 1001 -> 999 in fp32, y, dx, dw with db: 211, 253, 318 us; without, in tiles of 64, 64 and 128, 175, 191, 226, 103
+// to 80 TFLOP/s.  The rules below take tiles of 128 there: 212, 226, 226; bf16 61, 50, 75).
 // 20,384 rows of 123 -> 501 in fp32: 44, 42, 47 us and 8 for the pieces' sums, where 17 is the matrix cores' time: one
 // or two rounds of short blocks, whose first loads and last stores nothing covers, and unaligned 16-byte accesses.
-// Weights that few rows share are read at the memory's rate: 8 x 1 rows of 1024 -> 4096 in bf16 11.6 us for 67 MB.
+// Weights that few rows share are read at the memory's rate: 8 x 1 rows of 1024 -> 4096 in bf16 13.0 us for 67 MB.
 // PART (LINEAR_DW): pieces of groups, whose sums are kept in fp32 for k_linear_join.
 // SHORT: rows may be shorter than a piece, and are loaded by elements.
 template <typename T, int KIND, bool PART, int B, bool SHORT>
@@ -295,7 +296,7 @@ __global__ __launch_bounds__(256) void k_linear(LinearArgs A)
 }
 
 // y for few rows a group (single tokens): bound by reading each weight once, or by the launch (450 x 2 rows of 64 -> 256
-// in fp32: 5.6 us; tiles of 64 take as long there, but 25 instead of 8 where 1024 of k are walked by few blocks).  A block takes 16 positions and
+// in fp32: 5.2 us; tiles of 64 take as long there, but 25 instead of 8 where 1024 of k are walked by few blocks).  A block takes 16 positions and
 // 16 NB columns; its four waves take a quarter of each run of k, with all their loads in flight, straight
 // into the matrix instruction's operands (16 x 16, columns of y in the rows), and their sums are added in LDS.
 template <typename T, int NB, bool SHORT>
@@ -402,22 +403,26 @@ __global__ __launch_bounds__(256) void k_linear_join(LinearArgs A)
     else ((T *)A.out)[group * size + i] = Elem<T>::from_f32(sum);
 }
 
-// The rules below were measured over 1 to 8 groups of 1 to 8192 rows, widths of 61 to 4096, in us; what they compare
-// is the blocks or tiles of a call, n cols, and n cin cout.
-//   y, few rows (16 a tile) and tiles of 64, bf16: 8 groups of 1024 -> 4096, 1 row each, 16.2 and 14.0 (660 tiles of 64);
-//     3 x 64 x 1001 -> 999 18.0 and 11.2 (544 blocks of few); fp32: 1 x 256 x 1024 -> 1024 18.7 and 26.5 (576),
-//     8 x 32 x 1024 -> 1024 19.3 and 26.7 (832), 64 rows 33.2 and 27.4 (1344), 5 x 512 x 501 -> 123 14.8 and 15.9 (668).
-//   y, tiles of 64 and the ring of 128, bf16: 8 x 64 x 1024 -> 1024 11.8 and 15.6, 256 rows 14.0 and 16.6, 512 21.0 and 18.1;
-//     dx, 8 x 64 x 1024 -> 4096 32.5 and 39.8; fp32: 8 x 256 x 1024 -> 1024 46 and 77, 512 rows 82 and 77;
-//     dx, 8 x 8192 x 64 -> 256 37.5 and 46.0 (half of a tile of 128 is empty).
-//   y and dx, the rings of 128 and 256, bf16: 8 x 512 x 1024 -> 1024 18 and 30, 8 x 2048 44 and 40, 8 x 8192 166 and 145.
-//   y and dx, tiles of 64 and 128 (unaligned), bf16: 3 x 1024 x 1001 -> 999 24.2 and 32.3 (192 tiles of 128), 8 x 512 x 255 ->
-//     1023 15.3 and 14.8 (256), dx 3 x 2048 x 1001 -> 999 42.6 and 35.0 (384); fp32: dx 8 x 4096 x 255 -> 1023 175 and 158 (512).
-//   dw, tiles of 64 and 128, bf16: 5 x 4096 x 123 x 501 31.5 and 26.2 (1.3e9 products), fp32: 5 x 8192 x 123 x 501 89 and 83
-//     (2.5e9), 8 x 32 x 1024 x 1024 19.0 and 16.7 (512 tiles);
-//     tiles of 128 and the ring of 256, bf16: 8 x 256 x 1024 x 1024 15.1 and 19.1, 8 x 512 21.7 and 26.0, 8 x 8192 x 256 x 256 49.6
-//     and 39.4, 8 x 2048 x 1024 x 1024 106 and 62;
-//     tiles of 128 and the ring of 128, fp32: 8 x 128 x 1024 x 1024 32.8 and 35, 8 x 256 63 and 51; 8 x 8192 x 64 x 256 63 and 56.
+// The rules below were measured over 1 to 8 groups of 1 to 8192 rows, widths of 61 to 4096, in us a call; what they compare
+// is the blocks or tiles of a call, n cols, and n cin cout.  (Rows a group are not looked at.)
+//   y, few rows (16 a tile) and tiles of 64, bf16: 8 groups of 1024 -> 4096, 1 row each, 16.6 and 13.0 (640 tiles of 64);
+//     3 x 64 x 1001 -> 999 17.0 and 10.4 (544 blocks of few); fp32: 1 x 256 x 1024 -> 1024 17.7 and 25.5 (608),
+//     8 x 32 x 1024 -> 1024 18.2 and 25.7 (832), 64 rows 31.7 and 26.1 (1344), 5 x 512 x 501 -> 123 13.8 and 15.0 (668).
+//   y, tiles of 64 and the ring of 128, bf16: 8 x 64 x 1024 -> 1024 10.4 and 14.9, 256 rows 12.8 and 15.3, 512 19.6 and 17.0;
+//     dx, 8 x 64 x 1024 -> 4096 31.7 and 40.1; fp32: 8 x 256 x 1024 -> 1024 44 and 76, 512 rows 79 and 78;
+//     dx, 8 x 8192 x 64 -> 256 32.2 and 41.8 (half of a tile of 128 is empty; the rule for widths below 96 has tiles of 128
+//     through registers there, 43).
+//   y and dx, the rings of 128 and 256, bf16: 8 x 512 x 1024 -> 1024 17 and 29, 8 x 2048 43 and 37, 8 x 8192 167 and 135.
+//   y and dx, tiles of 64 and 128 (unaligned), bf16: 3 x 1024 x 1001 -> 999 23.9 and 31.4 (192 tiles of 128), 8 x 512 x 255 ->
+//     1023 14.6 and 13.4 (256), dx 3 x 2048 x 1001 -> 999 41.9 and 33.8 (384); fp32: 8 x 4096 x 255 -> 1023 184 and 174 (2048),
+//     dx 176 and 157 (512), but 3 x 3000 x 1001 -> 999 175 and 212 (560).
+//   dw, tiles of 64 and 128, bf16: 5 x 4096 x 123 x 501 31.0 and 25.5 (1.3e9 products), 8 x 32 x 1024 x 1024 13.4 and 13.4 (512
+//     tiles); fp32: 5 x 8192 x 123 x 501 87 and 79 (2.5e9), 8 x 32 x 1024 x 1024 17.4 and 15.0 (512 tiles);
+//     tiles of 128 and the ring of 256, bf16: 8 x 256 x 1024 x 1024 14.0 and 19.2 (2.1e9); 8 x 8192 x 256 x 256 47.4 and 38.8, 4 x 4096
+//     x 512 x 512 43.6 and 37.2, 64 x 256 x 512 x 512 26.2 and 20.3 (4.3e9 each), 8 x 2048 x 1024 x 4096 216 and 146 (6.9e10).  Where
+//     whole groups leave half of the card idle tiles of 128 are faster, which products alone do not show: 8 x 512 x 1024 x 1024
+//     21.2 and 27.5, 2048 rows 64 and 68, 4096 rows 122 and 124;
+//     tiles of 128 and the ring of 128, fp32: 8 x 128 x 1024 x 1024 29.1 and 28.8 (1.1e9), 8 x 256 48.3 and 46.2.
 constexpr int64_t FEW_ROWS = 16, BIG_OUT = 1 << 24, RING_OUT = 1 << 22;
 constexpr int64_t few_blocks(bool f32) { return f32 ? 1024 : 512; }  // at most, for few rows
 constexpr int64_t few_tiles(bool f32) { return f32 ? INT64_MAX : 512; }  // of 64, up to FEW_ROWS a group

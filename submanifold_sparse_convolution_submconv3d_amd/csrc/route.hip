@@ -37,7 +37,8 @@ __device__ __forceinline__ float key_value(uint32_t k)
 }
 
 // exp(d) for d <= 0, to a few roundings of d and of the result (the argument in units of log 2 is one
-// rounding of d, the instruction one of the result); below the smallest normal number it is 0.
+// rounding of d, the instruction one of the result); below the smallest normal number it is 0.  For the forward pass, which
+// instructions bound; the backward pass, which memory bounds, has expf, and its p may differ from a gate in the last bits.
 __device__ __forceinline__ float exp_of(float d) { return __builtin_amdgcn_exp2f(d * 1.4426950408889634f); }
 
 // Larger of the group's keys, in every lane of aligned groups of L lanes (a power of two).
